@@ -10,6 +10,7 @@ the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -30,6 +31,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _LL = ctypes.c_longlong
+_F = ctypes.c_float
+_D = ctypes.c_double
 
 EXPORTS = {
     "tern_status_str": (ctypes.c_char_p, [_I]),
@@ -63,6 +66,13 @@ EXPORTS = {
     "tern_f3_packed_bytes": (_SZ, [_I, _I]),
     "tern_f3_pack": (_I, [_P, _I, _I, _P, _P, _P]),
     "tern_f3_gemv": (_I, [_P, _P, _P, _P, _I, _I, _I, _P]),
+    "tern_rope_frequencies_host": (_I, [_I, _D, _I, _D, _I, _D, _D, _P, _P]),
+    "tern_rope_append": (_I, [_P, _P, _P, _I, _LL, _LL, _LL, _P, _P, _P, _F, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "tern_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "tern_paged_attention": (_I, [_P, _LL, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _I, _P, _P, _P, _SZ, _P]),
+    "tern_attention_mass": (_I, [_P, _LL, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _I, _P, _F, _P, _P, _P]),
+    "tern_cache_evict_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "tern_cache_evict": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -399,6 +409,7 @@ def device_error() -> int:
 
 SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER = 0, 1
 DEVERR_GEMM_MMA_WAIT, DEVERR_GEMV_RANGE_FLAG_WAIT, DEVERR_GEMV_ACTIVATION_RANGE = 0x103, 0x202, 0x203
+DEVERR_CACHE_PAGE, DEVERR_CACHE_SEQUENCE, DEVERR_CACHE_SLOT = 0x301, 0x302, 0x303
 
 
 def wait_selftest(which: int, limit_us: int, stream=None) -> None:
@@ -471,3 +482,195 @@ def affine_gemm(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias
         _dev(biases, torch.float16, "biases"), _dev(y, y.dtype, "y"), 1 if y.dtype == torch.bfloat16 else 0,
         M, N, K, _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
     return y
+
+
+# ---------------------------------------------------------------------------
+# the paged key/value cache
+# ---------------------------------------------------------------------------
+
+class CacheLayout(ctypes.Structure):
+    """tern_cache_layout: strides in elements."""
+    _fields_ = [("pages", _I), ("page_size", _I), ("kv_heads", _I), ("head_dim", _I),
+                ("page_stride", _LL), ("head_stride", _LL), ("slot_stride", _LL)]
+
+
+@functools.lru_cache(maxsize=256)
+def _layout(shape, stride) -> CacheLayout:
+    return CacheLayout(shape[0], shape[2], shape[1], shape[3], stride[0], stride[1], stride[2])
+
+
+def _cache(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> CacheLayout:
+    """The layout of one cache array, bf16 [pages, kv_heads, page_size, head_dim]
+    with any strides over contiguous heads (a permuted [pages, page_size,
+    kv_heads, head_dim] array is one)."""
+    if t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be [pages, kv_heads, page_size, head_dim] with contiguous heads")
+    if like is not None and (t.shape != like.shape or t.stride() != like.stride()):
+        raise ValueError(f"{name} must have the shape and strides of its K array")
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    return _layout(tuple(t.shape), t.stride())
+
+
+def _tokens(t: torch.Tensor, dtypes, name: str, heads_dim=None) -> int:
+    """The token stride of [T, heads, head_dim] with contiguous heads."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with each token's heads contiguous")
+    if heads_dim is not None and tuple(t.shape[1:]) != heads_dim:
+        raise ValueError(f"{name} must hold {heads_dim[0]} heads of {heads_dim[1]}, got {tuple(t.shape[1:])}")
+    if not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA tensor of type {' or '.join(map(str, dtypes))}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 0, turns_fast: float = 32.0, turns_slow: float = 1.0):
+    """(inv_freq, attn_factor) of a rotation over rot_dim values: fp32 numpy
+    [rot_dim / 2] and a float.  scaling: "none", "linear" (positions divided by
+    factor), "ntk" (a larger base) or "yarn" (by parts, with original_len)."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
+    out = np.empty(max(rot_dim // 2, 1), dtype=np.float32)
+    af = ctypes.c_float(1.0)
+    _check("tern_rope_frequencies_host", lib().tern_rope_frequencies_host(
+        rot_dim, base, _ROPE_SCALING[scaling], factor, original_len, turns_fast, turns_slow, out.ctypes.data,
+        ctypes.byref(af)))
+    return out, float(af.value)
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                inv_freq: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                q_out: torch.Tensor | None = None, interleaved: bool = False, attn_factor: float = 1.0,
+                stream=None) -> torch.Tensor:
+    """Turns q and k by their positions and appends k and v to the paged cache.
+
+    q [T, q_heads, D], k and v [T, kv_heads, D]: all fp32 or all bf16, views of
+    one product output included; positions int32 [T]; slots int64 [T] (page *
+    page_size + slot, negative: not stored); inv_freq fp32 [rot_dim / 2], its
+    length setting how much of a head turns; the caches bf16 [pages, kv_heads,
+    page_size, D].  Returns the turned q, bf16 [T, q_heads, D]."""
+    lay = _cache(k_cache, "k_cache")
+    _cache(v_cache, "v_cache", k_cache)
+    T, Hq, D = q.shape
+    kinds = (q.dtype,) if q.dtype in (torch.float32, torch.bfloat16) else (torch.float32, torch.bfloat16)
+    qs, kv = _tokens(q, kinds, "q", (Hq, lay.head_dim)), (lay.kv_heads, lay.head_dim)
+    ks, vs = _tokens(k, kinds, "k", kv), _tokens(v, kinds, "v", kv)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must hold the same number of tokens")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    _covers(positions=(positions, T), slots=(slots, T), q_out=(q_out, T * Hq * D))
+    _check("tern_rope_append", lib().tern_rope_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), 1 if q.dtype == torch.float32 else 0, qs, ks, vs,
+        _dev(positions, torch.int32, "positions"), _dev(slots, torch.int64, "slots"),
+        _dev(inv_freq, torch.float32, "inv_freq"), attn_factor, 2 * inv_freq.numel(), 1 if interleaved else 0, T, Hq,
+        _dev(q_out, torch.bfloat16, "q_out"), k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay),
+        _stream(stream)))
+    return q_out
+
+
+def paged_attention_workspace_bytes(B: int, T: int, max_new: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().tern_paged_attention_workspace_bytes(B, T, max_new, q_heads, kv_heads, head_dim))
+
+
+def _sequences(q, lay, table, lens, q_start, max_new):
+    """(token stride, T, q_heads, B, table width, q_start pointer, max_new)."""
+    qs = _tokens(q, (torch.bfloat16,), "q", (q.shape[1], lay.head_dim) if q.dim() == 3 else None)
+    T, Hq = q.shape[:2]
+    if table.dim() != 2:
+        raise ValueError("table must be [B, pages per sequence]")
+    B, W = table.shape
+    _covers(lens=(lens, B), q_start=(q_start, B + 1))
+    if q_start is None:
+        return qs, T, Hq, B, W, None, 0
+    return qs, T, Hq, B, W, _dev(q_start, torch.int32, "q_start"), T if max_new is None else max_new
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                    lens: torch.Tensor, q_start: torch.Tensor | None = None, max_new: int | None = None,
+                    scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of new tokens (one, a few or a chunk for each sequence) over a
+    paged cache that already holds their keys.
+
+    q bf16 [T, q_heads, D] (any token stride); table int32 [B, W]; lens int32
+    [B], the new tokens included; q_start int32 [B + 1] (None: T / B tokens
+    each) with max_new, the most tokens of one sequence (T if not given);
+    scale 1/sqrt(D) if not given; window 0 or the number of last keys a query
+    sees.  Returns out bf16 [T, q_heads, D]; lse fp32 [T, q_heads] if given."""
+    lay = _cache(k_cache, "k_cache")
+    _cache(v_cache, "v_cache", k_cache)
+    qs, T, Hq, B, W, start, max_new = _sequences(q, lay, table, lens, q_start, max_new)
+    D = lay.head_dim
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    _covers(out=(out, T * Hq * D), lse=(lse, T * Hq))
+    if ws is None:
+        ws = workspace(paged_attention_workspace_bytes(B, T, max_new if start else T // B, Hq, lay.kv_heads, D),
+                       q.device)
+    _check("tern_paged_attention", lib().tern_paged_attention(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay),
+        _dev(table, torch.int32, "table"), W, _dev(lens, torch.int32, "lens"), start, B, T, max_new, Hq,
+        D ** -0.5 if scale is None else scale, window, _dev(out, torch.bfloat16, "out"),
+        None if lse is None else _dev(lse, torch.float32, "lse"), _dev(ws, torch.uint8, "ws"), ws.numel(),
+        _stream(stream)))
+    return out
+
+
+def attention_mass(q: torch.Tensor, k_cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                   lse: torch.Tensor, mass: torch.Tensor, out: torch.Tensor | None = None,
+                   q_start: torch.Tensor | None = None, max_new: int | None = None, scale: float | None = None,
+                   window: int = 0, decay: float = 1.0, stream=None) -> torch.Tensor:
+    """Adds the attention weight each cached key received from the new tokens
+    to its running mass: out = decay * mass + sum exp(s - lse), fp32 [pages,
+    kv_heads, page_size]; out defaults to mass itself.  The other arguments as
+    paged_attention's, lse its output."""
+    lay = _cache(k_cache, "k_cache")
+    qs, T, Hq, B, W, start, max_new = _sequences(q, lay, table, lens, q_start, max_new)
+    if out is None:
+        out = mass
+    need = lay.pages * lay.kv_heads * lay.page_size
+    _covers(lse=(lse, T * Hq), mass=(mass, need), out=(out, need))
+    _check("tern_attention_mass", lib().tern_attention_mass(
+        q.data_ptr(), qs, k_cache.data_ptr(), ctypes.addressof(lay), _dev(table, torch.int32, "table"), W,
+        _dev(lens, torch.int32, "lens"), start, B, T, max_new, Hq, lay.head_dim ** -0.5 if scale is None else scale,
+        window, _dev(lse, torch.float32, "lse"), decay, _dev(mass, torch.float32, "mass"),
+        _dev(out, torch.float32, "out"), _stream(stream)))
+    return out
+
+
+def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor, table: torch.Tensor,
+                lens: torch.Tensor, budget: int, recent: int, dst_k: torch.Tensor, dst_v: torch.Tensor,
+                dst_mass: torch.Tensor, dst_table: torch.Tensor, keep: torch.Tensor | None = None,
+                dst_lens: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Keeps `budget` keys of each sequence and head, the `recent` last and the
+    heaviest before them, and moves them (K, V and mass) to the pages
+    dst_table of the destination arrays.  Returns (keep int32 [B, kv_heads,
+    budget], the kept keys' old indices with -1 past the last, and the new
+    lengths int32 [B])."""
+    lay = _cache(k_cache, "k_cache")
+    _cache(v_cache, "v_cache", k_cache)
+    dlay = _cache(dst_k, "dst_k")
+    _cache(dst_v, "dst_v", dst_k)
+    if table.dim() != 2 or dst_table.dim() != 2 or dst_table.shape[0] != table.shape[0]:
+        raise ValueError("table and dst_table must be [B, pages per sequence]")
+    B, H = table.shape[0], lay.kv_heads
+    if keep is None:
+        keep = torch.empty((B, H, budget), dtype=torch.int32, device=mass.device)
+    if dst_lens is None:
+        dst_lens = torch.empty(B, dtype=torch.int32, device=mass.device)
+    _covers(mass=(mass, lay.pages * H * lay.page_size), lens=(lens, B), keep=(keep, B * H * budget),
+            dst_mass=(dst_mass, dlay.pages * dlay.kv_heads * dlay.page_size), dst_lens=(dst_lens, B))
+    if ws is None:
+        ws = workspace(int(lib().tern_cache_evict_workspace_bytes(B, H, table.shape[1] * lay.page_size)), mass.device)
+    _check("tern_cache_evict", lib().tern_cache_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay), _dev(mass, torch.float32, "mass"),
+        _dev(table, torch.int32, "table"), table.shape[1], _dev(lens, torch.int32, "lens"), B, budget, recent,
+        dst_k.data_ptr(), dst_v.data_ptr(), ctypes.addressof(dlay), _dev(dst_mass, torch.float32, "dst_mass"),
+        _dev(dst_table, torch.int32, "dst_table"), dst_table.shape[1], _dev(keep, torch.int32, "keep"),
+        _dev(dst_lens, torch.int32, "dst_lens"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    return keep, dst_lens

@@ -85,11 +85,14 @@ tern_status tern_device_error(int* code) {
     if (!code) return TERN_ERR_NULL;
     *code = 0;
     if (cudaDeviceSynchronize() != cudaSuccess) return TERN_ERR_CUDA;
-    int a = 0, b = 0, c = 0;
-    if (read_gemm_device_error(&a) != cudaSuccess) return TERN_ERR_CUDA;
-    if (read_gemv_device_error(&b) != cudaSuccess) return TERN_ERR_CUDA;
-    if (read_f3_device_error(&c) != cudaSuccess) return TERN_ERR_CUDA;
-    *code = a ? a : (b ? b : c);
+    // every word is read (and cleared); the first that is set is returned
+    cudaError_t (*const readers[])(int*) = {read_gemm_device_error, read_gemv_device_error, read_f3_device_error,
+                                            read_rope_device_error, read_attn_device_error, read_evict_device_error};
+    for (auto* read : readers) {
+        int c = 0;
+        if (read(&c) != cudaSuccess) return TERN_ERR_CUDA;
+        if (!*code) *code = c;
+    }
     return TERN_OK;
 }
 

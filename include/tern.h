@@ -368,6 +368,128 @@ tern_status tern_affine_gemm(const void *x, const uint32_t *codes, const void *s
                              size_t workspace_bytes, tern_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
+/* The paged key/value cache: rotary append, attention, attention mass,    */
+/* eviction.  What a step needs between its qkv product and its output     */
+/* product; the pages the packed formats come from describe none of it.    */
+/*                                                                         */
+/* The cache is `pages` pages of `page_size` slots; a slot holds one       */
+/* token's kv_heads x head_dim bf16 values (K and V in two arrays of the   */
+/* same layout).  Key j of sequence b is slot j % page_size of page        */
+/* table[b][j / page_size] (int32 [B][table_width]; entries past a         */
+/* sequence's last page are not read).  A running mass (fp32) may stand    */
+/* beside it, contiguous [pages][kv_heads][page_size].                     */
+/*                                                                         */
+/* Sequence b holds lens[b] keys (int32 [B]), its new tokens' included, and */
+/* brings the query rows q_start[b] .. q_start[b+1] - 1 of T (int32         */
+/* [B + 1], nondecreasing, at most max_new each; NULL: T / B each and       */
+/* max_new is not read).  Query i of its n sits at position                 */
+/* p = lens[b] - n + i and sees key j when 0 <= j <= p and, with window > 0, */
+/* j > p - window.  A query that sees no key (p < 0) gets zeros and an lse   */
+/* of -inf.  Query head h reads key head h / (q_heads / kv_heads).          */
+/*                                                                         */
+/* table, lens, q_start, positions, slots and the fp32 arrays need only the */
+/* alignment of their type.  Device-side values that do not fit the arrays  */
+/* are reported through tern_device_error (TERN_DEVERR_CACHE_*), never      */
+/* followed out of bounds; the call's output is then undefined.             */
+/* ---------------------------------------------------------------------- */
+
+/* Strides in elements, multiples of 8, at least head_dim each; distinct
+ * (page, head, slot) must not overlap.  page_size a multiple of 16 (at most
+ * 65536), head_dim a multiple of 8 (at most 1024; the attention calls: 64, 128
+ * or 256).  TERN_ERR_SHAPE otherwise. */
+typedef struct {
+    int pages, page_size, kv_heads, head_dim;
+    long long page_stride, head_stride, slot_stride;
+} tern_cache_layout;
+
+/* Rotary frequencies for a rotation of rot_dim values: inv_freq[i] =
+ * base^(-2 i / rot_dim), i < rot_dim / 2, changed by `scaling` for a context
+ * `factor` (>= 1) times the original:
+ *   TERN_ROPE_LINEAR  every frequency divided by factor;
+ *   TERN_ROPE_BASE    base multiplied by factor^(rot_dim / (rot_dim - 2));
+ *   TERN_ROPE_PARTS   pairs that make more than turns_fast turns in
+ *                     original_len positions are kept, those that make fewer
+ *                     than turns_slow are divided by factor, with a linear
+ *                     ramp over the pair index between, and *attn_factor is
+ *                     0.1 ln(factor) + 1 (1 otherwise).
+ * Host memory, computed in 64 bits and rounded to fp32. */
+#define TERN_ROPE_PLAIN 0
+#define TERN_ROPE_LINEAR 1
+#define TERN_ROPE_BASE 2
+#define TERN_ROPE_PARTS 3
+tern_status tern_rope_frequencies_host(int rot_dim, double base, int scaling, double factor, int original_len,
+                                       double turns_fast, double turns_slow, float *inv_freq, float *attn_factor);
+
+/* Rotary positions and the append to the cache, in one pass: for each of T
+ * tokens, q (q_heads heads) and k (kv_heads) are turned and rounded once to
+ * bf16 (nearest even); q goes to q_out, bf16 [T][q_heads][head_dim], k and v go
+ * to slot slots[t] of the cache (int64, page * page_size + slot; a negative
+ * slot stores nothing, a slot twice in one call keeps one of the two).
+ *   - q, k, v: fp32 (in_is_f32) or bf16, the token stride of each in elements
+ *     (a multiple of 8), heads contiguous in a token: pointers into one
+ *     [T][q | k | v] product output work.  16-byte aligned, no overlap with
+ *     the outputs.  q_heads = 0 leaves q out.
+ *   - The first rot_dim values of a head turn (even, <= head_dim; 0: none),
+ *     by positions[t] * inv_freq[i] (int32, fp32 [rot_dim / 2]): pair i is
+ *     values 2i and 2i + 1 (interleaved) or i and i + rot_dim / 2; cos and sin
+ *     are multiplied by attn_factor.  The angle is reduced in 64 bits, so
+ *     its error does not grow with the position.
+ * One kernel launch (none for T = 0). */
+tern_status tern_rope_append(const void *q, const void *k, const void *v, int in_is_f32, long long q_stride,
+                             long long k_stride, long long v_stride, const int *positions, const long long *slots,
+                             const float *inv_freq, float attn_factor, int rot_dim, int interleaved, int T,
+                             int q_heads, void *q_out, void *k_cache, void *v_cache, const tern_cache_layout *layout,
+                             tern_stream_t stream);
+
+/* Attention over the cache: out (bf16 [T][q_heads][head_dim]) = sum_j
+ * exp(s_ij - lse_i) v_j, s_ij = scale q_i . k_j over the keys the query sees;
+ * lse (fp32 [T][q_heads], nullable) = log sum_j exp(s_ij).  q bf16, token
+ * stride q_stride elements (a multiple of 8, >= q_heads * head_dim), heads
+ * contiguous.  Scores, sums and the output are held in fp32 and rounded once
+ * to bf16; the probabilities of the second product are rounded to bf16.  Slots
+ * at or past lens[b] may hold anything, NaN included.  q_heads a multiple of
+ * kv_heads, at most 64 query heads a key head.
+ * The workspace is zero-filled once before its first use and left ready for
+ * the next call; its size never exceeds 128 MiB.  Calls that share it must be
+ * ordered; after a device error zero-fill it again. */
+size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new, int q_heads, int kv_heads, int head_dim);
+tern_status tern_paged_attention(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
+                                 const tern_cache_layout *layout, const int *table, int table_width, const int *lens,
+                                 const int *q_start, int B, int T, int max_new, int q_heads, float scale, int window,
+                                 void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 tern_stream_t stream);
+
+/* The attention weight each key received from the new tokens, added to its
+ * running mass: for every key j < lens[b] of every sequence and key head,
+ *   mass_out = decay * mass + sum over the queries i that see j and the heads
+ *   of its group of exp(s_ij - lse_i),
+ * with the lse that tern_paged_attention gave for the same q, scale and window
+ * (a row with lse = -inf gives nothing).  mass and mass_out as described
+ * above; they may be the same array.  Slots that hold no key are left alone.
+ * No atomics: a key's sum has a fixed order. */
+tern_status tern_attention_mass(const void *q, long long q_stride, const void *k_cache,
+                                const tern_cache_layout *layout, const int *table, int table_width, const int *lens,
+                                const int *q_start, int B, int T, int max_new, int q_heads, float scale, int window,
+                                const float *lse, float decay, const float *mass, float *mass_out,
+                                tern_stream_t stream);
+
+/* Eviction: of the lens[b] keys of each sequence and key head keep
+ * min(lens[b], budget): the `recent` last (0 <= recent <= budget) and, of
+ * those before them, the ones of largest mass, equal masses to the lowest
+ * index (-0 equals 0; NaN is below every number).  The kept keys' K, V and
+ * mass move in order to slots 0, 1, ... of the pages dst_table[b] (int32
+ * [B][dst_table_width]) of the destination cache, which may be the same arrays
+ * as long as no destination page is one that the call reads; keep (int32
+ * [B][kv_heads][budget]) gets their old indices, ascending, -1 past the last,
+ * and dst_lens (int32 [B]) the new lengths.  Two kernel launches. */
+size_t tern_cache_evict_workspace_bytes(int B, int kv_heads, int max_keys);
+tern_status tern_cache_evict(const void *k_cache, const void *v_cache, const tern_cache_layout *layout,
+                             const float *mass, const int *table, int table_width, const int *lens, int B, int budget,
+                             int recent, void *dst_k, void *dst_v, const tern_cache_layout *dst_layout,
+                             float *dst_mass, const int *dst_table, int dst_table_width, int *keep, int *dst_lens,
+                             void *workspace, size_t workspace_bytes, tern_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */
 /* ---------------------------------------------------------------------- */
 
@@ -382,7 +504,10 @@ enum {
     TERN_DEVERR_GEMM_EPILOGUE_WAIT = 0x104,  /* prefill: epilogue waited for an accumulator */
     TERN_DEVERR_GEMM_TEARDOWN_WAIT = 0x105,  /* prefill: teardown waited for work in flight */
     TERN_DEVERR_GEMV_RANGE_FLAG_WAIT = 0x202, /* decode: a K-slice waited for y's clearing */
-    TERN_DEVERR_GEMV_ACTIVATION_RANGE = 0x203 /* decode: a group's largest |x| was >= 2^100 or not finite */
+    TERN_DEVERR_GEMV_ACTIVATION_RANGE = 0x203, /* decode: a group's largest |x| was >= 2^100 or not finite */
+    TERN_DEVERR_CACHE_PAGE = 0x301,          /* cache: a page id outside the pool */
+    TERN_DEVERR_CACHE_SEQUENCE = 0x302,      /* cache: a length or token range that the call's arrays do not hold */
+    TERN_DEVERR_CACHE_SLOT = 0x303           /* cache: a slot past the pool's last */
 };
 
 /* Reads and clears the sticky device-side error words of the current device
