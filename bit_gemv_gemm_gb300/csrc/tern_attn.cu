@@ -5,90 +5,12 @@
 //   o_i = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij),
 //   mass_j <- decay mass_j + sum_i exp(s_ij - lse_i)  (the queries of all the
 //   heads that share key j's head).
-#include <math.h>
-
-#include "tern_cache.cuh"
+#include "tern_attn.cuh"
 
 namespace tern {
 namespace {
 
 __device__ int g_attn_error;
-
-constexpr int kAttnWarps = 4;
-
-struct AttnArgs {
-    const __nv_bfloat16* q;
-    long long q_stride;
-    const __nv_bfloat16 *k_cache, *v_cache;
-    CacheView c;
-    SeqView s;
-    int q_heads;
-    float scale;
-    int window;
-    __nv_bfloat16* out;
-    float* lse;
-};
-
-__device__ __forceinline__ void visible(const Seq& q, int window, int i, int& j0, int& j1) {
-    const int p = q.len - q.n + i;   // may be negative: nothing is seen
-    j1 = max(p + 1, 0);
-    j0 = window > 0 ? max(p - window + 1, 0) : 0;
-}
-
-// One CTA a (sequence, token, query head); each warp takes every fourth key.
-template <int D>
-__global__ void __launch_bounds__(kAttnWarps * 32) attn_kernel(const AttnArgs a) {
-    constexpr int E = D / 32;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int b = blockIdx.z, i = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Seq q = load_seq(a.s, a.c.page_size, b, &g_attn_error);
-    if (i >= q.n) return;
-    const int hk = h / (a.q_heads / a.c.kv_heads);
-    float x[E], o[E] = {}, m = -INFINITY, l = 0.0f;
-    const __nv_bfloat16* qp = a.q + (long long)(q.q0 + i) * a.q_stride + (long long)h * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __bfloat162float(qp[e]) * a.scale;
-    int j0, j1;
-    visible(q, a.window, i, j0, j1);
-    for (int j = j0 + warp; j < j1; j += kAttnWarps) {
-        const int page = checked_page(a.s.table[(long long)b * a.s.width + j / a.c.page_size], a.c.pages, &g_attn_error);
-        const long long at = page * a.c.page_stride + hk * a.c.head_stride +
-                             (j % a.c.page_size) * a.c.slot_stride + lane * E;
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(x[e], __bfloat162float(a.k_cache[at + e]), s);
-#pragma unroll
-        for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        const float mn = fmaxf(m, s), r = m == mn ? 1.0f : expf(m - mn), p = expf(s - mn);
-        l = l * r + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * r + p * __bfloat162float(a.v_cache[at + e]);
-        m = mn;
-    }
-    __shared__ float so[kAttnWarps][D], sm[kAttnWarps], sl[kAttnWarps];
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    __syncthreads();
-    float top = -INFINITY, total = 0.0f;
-    for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sm[w]);
-    float f[kAttnWarps];
-    for (int w = 0; w < kAttnWarps; ++w) {
-        f[w] = sl[w] > 0.0f ? expf(sm[w] - top) : 0.0f;
-        total += sl[w] * f[w];
-    }
-    const long long row = (long long)(q.q0 + i) * a.q_heads + h;
-    for (int d = threadIdx.x; d < D; d += kAttnWarps * 32) {
-        float y = 0.0f;
-        for (int w = 0; w < kAttnWarps; ++w) y += so[w][d] * f[w];
-        a.out[row * D + d] = __float2bfloat16_rn(total > 0.0f ? y / total : 0.0f);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = total > 0.0f ? top + logf(total) : -INFINITY;
-}
 
 struct MassArgs {
     const __nv_bfloat16* q;
@@ -167,7 +89,7 @@ extern "C" size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new
     if (B < 1 || T < 0 || max_new < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return 256;
+    return kAttnCounterBytes + attn_rows_workspace();
 }
 
 extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, const void* k_cache,
@@ -189,21 +111,23 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
                                                                              a.c.head_dim))
         return TERN_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return TERN_ERR_ALIGN;
-    st = check_device(nullptr);
+    int sms = 0;
+    st = check_device(&sms);
     if (st != TERN_OK) return st;
+    if (sms > kMaxSms) sms = kMaxSms;
     if (a.s.max_new == 0 || T == 0) return TERN_OK;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.q_stride = q_stride;
-    a.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
-    a.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
     a.q_heads = q_heads;
-    a.scale = scale;
+    a.group = q_heads / a.c.kv_heads;
+    a.scale_log2 = scale * 1.44269504088896341f;
     a.window = window;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
-    auto kernel = a.c.head_dim == 64 ? attn_kernel<64> : a.c.head_dim == 128 ? attn_kernel<128> : attn_kernel<256>;
-    if (launch_pdl(kernel, dim3(a.s.max_new, q_heads, B), dim3(kAttnWarps * 32), 0, (cudaStream_t)stream, true, a) !=
-        cudaSuccess)
+    a.counters = static_cast<unsigned*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
+    const long long rows = (long long)a.s.max_new * a.group;
+    if (launch_attn_rows(a, k_cache, v_cache, rows > 16 ? 32 : (int)rows, sms, (cudaStream_t)stream) != cudaSuccess)
         return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

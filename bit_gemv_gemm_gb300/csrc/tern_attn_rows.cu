@@ -1,0 +1,495 @@
+// tern_attn_rows.cu -- attention of few query rows a key head (decode, verify):
+// bound by reading the cache once.
+//
+// One item is the R = 16 or 32 packed rows (token, head of the group) of one
+// sequence and key head; its keys are read in strips of 16.  All strips of all
+// items are cut into one equal contiguous share a CTA (no CTA idles behind a
+// long sequence), two CTAs an SM.  In a CTA every warp takes every fourth strip of a
+// segment for itself: its lane 0 fetches the strip's K and V by TMA into the
+// warp's own ring (three strips of 8 KB at D = 128: 192 KB in flight an SM),
+// so warps never wait for one another inside a segment.  Per strip a warp
+// does S = Q K^T and O += P V with mma.sync (m16n8k16, bf16 in, fp32 out)
+// with a running maximum that only moves when a score passes it by 2^8: the
+// sums stay below 2^8 times their largest term, far inside fp32.
+// At a segment's end the four warps' (O, m, l) meet in shared memory in a
+// fixed order.  A segment that is the whole item is written out; a part goes to
+// the workspace, and the CTA that counts itself last into the item's counter
+// adds the parts in their order, so results do not depend on which CTA is last.
+#include <algorithm>
+
+#include "tern_attn.cuh"
+
+namespace tern {
+namespace {
+
+__device__ int g_attn_rows_error;
+
+constexpr int kWarps = 4, kThreads = kWarps * 32, kStrip = 16;
+constexpr int kMaxR = 32, kMaxD = 256;
+constexpr int kMinUnits = 2 * kWarps;         // strips a share holds at least (two a warp)
+
+template <int D, int MT>
+struct Cfg {
+    static constexpr int R = 16 * MT;
+    static constexpr int kStage = kStrip * D * 4;                 // K and V of one strip
+    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kRing = kStages * kStage;                // one warp's
+    static constexpr int kQ = R * D * 2;
+    static constexpr int kCtas = D == 256 ? 1 : 2;                // an SM
+    static constexpr size_t kSmemQ = (size_t)kWarps * kRing;
+    static constexpr size_t kSmemBar = kSmemQ + kQ;
+    static constexpr size_t kSmemStat = kSmemBar + kWarps * kStages * 8;
+    static constexpr size_t kSmemMisc = kSmemStat + (size_t)kWarps * R * 8;
+    static constexpr size_t kSmem = kSmemMisc + 128 + 1024;
+    static_assert(kRing >= R * D * 4, "a warp's rows are merged through its ring");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A block-wide sum over threads before this one, and over all.
+__device__ __forceinline__ long long block_scan(long long v, long long* sm, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, k);
+        if (lane >= k) x += y;
+    }
+    if (lane == 31) sm[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sm[w];
+        total += sm[w];
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, MT>::kCtas)
+attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                 const AttnArgs a) {
+    using namespace sm100;
+    using C = Cfg<D, MT>;
+    constexpr int R = C::R;
+    extern __shared__ __align__(1024) unsigned char smem_dyn[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = sbase + (uint32_t)(warp * C::kRing), qs = sbase + (uint32_t)C::kSmemQ;
+    const uint32_t bars = sbase + (uint32_t)C::kSmemBar + (uint32_t)(warp * C::kStages * 8);
+    float* sm_m = reinterpret_cast<float*>(smem + C::kSmemStat);             // [warp][R]
+    float* sm_l = sm_m + kWarps * R;
+    long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [kWarps]
+    long long* sm_at = sm_scan + kWarps;                                      // sequence, its first unit
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_at + 2);
+    int* sm_last = reinterpret_cast<int*>(sm_at + 2) + 1;
+
+    if (lane == 0) {
+        for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8u * s, 1);
+        fence_barrier_init();
+        if (warp == 0) {
+            *abort_flag = 0;
+            tma_prefetch_desc(&tmap_k);
+            tma_prefetch_desc(&tmap_v);
+        }
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // this CTA's share of the units, and the sequence it starts in
+    const int B = a.s.B, Hk = a.c.kv_heads, cta = blockIdx.x;
+    const int per = (B + kThreads - 1) / kThreads;
+    const int b_lo = min((int)threadIdx.x * per, B), b_hi = min(b_lo + per, B);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b)
+        mine += Hk * head_units<kStrip>(load_seq(a.s, a.c.page_size, b, &g_attn_rows_error), a.group, a.window, R);
+    long long total;
+    const long long before = block_scan(mine, sm_scan, total);
+    // no share below kMinUnits: a short call is cut into fewer parts
+    const int P = (int)min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
+    if (cta >= P) return;
+    const long long w0 = unit_begin(total, P, cta), w1 = unit_begin(total, P, cta + 1);
+    if (w0 >= w1) return;
+    if (w0 >= before && w0 < before + mine) {
+        long long at = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const long long u =
+                Hk * head_units<kStrip>(load_seq(a.s, a.c.page_size, b, &g_attn_rows_error), a.group, a.window, R);
+            if (w0 < at + u) {
+                sm_at[0] = b;
+                sm_at[1] = at;
+                break;
+            }
+            at += u;
+        }
+    }
+    __syncthreads();
+
+    int b = (int)sm_at[0], hk, r0 = 0;
+    long long at = sm_at[1];   // the current item's first unit
+    Seq q = load_seq(a.s, a.c.page_size, b, &g_attn_rows_error);
+    {
+        const long long hu = head_units<kStrip>(q, a.group, a.window, R);
+        hk = (int)((w0 - at) / hu);
+        at += hk * hu;
+        for (;;) {
+            const int u = item_units<kStrip>(q, a.group, a.window, r0, min(r0 + R, q.n * a.group));
+            if (w0 < at + u) break;
+            at += u;
+            r0 += R;
+        }
+    }
+
+    uint32_t it = 0;   // strips this warp has fetched and used, over all segments
+    for (long long w = w0; w < w1;) {
+        // ---- one segment: units [w, we) of the item that starts at `at` ----
+        const int rows = min(R, q.n * a.group - r0);
+        const int units = item_units<kStrip>(q, a.group, a.window, r0, r0 + rows);
+        const long long we = min(w1, at + units);
+        int j0, j1;
+        keys_of_rows(q, a.group, a.window, r0, r0 + rows, j0, j1);
+        const int first = j0 / kStrip + (int)(w - at);
+        const int strips = j1 > j0 ? (int)(we - w) : 0;
+        const int my = strips > warp ? (strips - warp + kWarps - 1) / kWarps : 0;
+        // page ids: lane i holds the one of this warp's strip i of the current 32
+        const int* trow = a.s.table + (long long)b * a.s.width;
+        int ids = 0;
+        auto fetch_ids = [&](int base) {
+            const int k = base + lane;
+            ids = 0;
+            if (k < my) ids = checked_page(trow[(first + warp + kWarps * k) * kStrip / a.c.page_size], a.c.pages, &g_attn_rows_error);
+        };
+        auto issue = [&](int k) {   // strip k of this warp, into slot (it + k) mod stages
+            const int page = __shfl_sync(0xffffffffu, ids, k & 31);
+            if (lane == 0) {
+                const uint32_t s = (it + (uint32_t)k) % C::kStages;
+                const int slot = (first + warp + kWarps * k) * kStrip % a.c.page_size;
+                mbar_arrive_expect_tx(bars + 8u * s, C::kStage);
+                tma_load_cache(ring + s * C::kStage, &tmap_k, slot, 0, hk, page, bars + 8u * s);
+                tma_load_cache(ring + s * C::kStage + C::kStage / 2, &tmap_v, slot, 0, hk, page, bars + 8u * s);
+            }
+        };
+        fetch_ids(0);
+        for (int k = 0; k < C::kStages && k < my; ++k) issue(k);
+        // the rows of Q, in the layout of the A fragments' loads
+        for (int i = threadIdx.x; i < R * (D / 8); i += kThreads) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int t = (r0 + r) / a.group, g = (r0 + r) % a.group;
+                v = *reinterpret_cast<const uint4*>(a.q + (long long)(q.q0 + t) * a.q_stride +
+                                                    (long long)(hk * a.group + g) * D + c * 8);
+            }
+            *reinterpret_cast<uint4*>(smem + C::kSmemQ + (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+        // the keys that each of this thread's rows sees: (lo, hi]
+        int hi[MT][2], lo[MT][2];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int r = (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
+            const int p = q.len - q.n + (r0 + min(r, rows - 1)) / a.group;
+            hi[i >> 1][i & 1] = r < rows ? p : -1;
+            lo[i >> 1][i & 1] = a.window > 0 ? p - a.window : -1;
+        }
+        const int p_lo = q.len - q.n + r0 / a.group, p_hi = q.len - q.n + (r0 + rows - 1) / a.group;
+        __syncthreads();
+
+        float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+        }
+        for (int k = 0; k < my; ++k) {
+            const uint32_t slot = (it + (uint32_t)k) % C::kStages, phase = ((it + (uint32_t)k) / C::kStages) & 1u;
+            const int key0 = (first + warp + kWarps * k) * kStrip;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + 8u * slot, phase, abort_flag, kAttnWaitNs))) {
+                if (!*abort_flag) {
+                    *abort_flag = 1;
+                    if (lane == 0) report_device_error(&g_attn_rows_error, TERN_DEVERR_ATTN_WAIT);
+                }
+                if (lane == 0)   // the copies in flight land before the CTA goes away
+                    for (int x = k; x < my && x < k + C::kStages; ++x)
+                        (void)mbar_wait_drain(bars + 8u * ((it + (uint32_t)x) % C::kStages),
+                                              ((it + (uint32_t)x) / C::kStages) & 1u, 100000000ull);
+                break;
+            }
+            const uint32_t ks = ring + slot * C::kStage, vs = ks + C::kStage / 2;
+            // S = Q K^T
+            float s[MT][2][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.0f;
+            const int mi = lane >> 3, l7 = lane & 7;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t kb[4];
+                const int krow = (mi >> 1) * 8 + l7, kc = (kk & 3) * 2 + (mi & 1);
+                ldsm4(kb, ks + (kk >> 2) * (kStrip * 128) + krow * 128 + ((kc ^ l7) << 4));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t qa[4];
+                    const int qrow = i * 16 + (mi & 1) * 8 + l7, qc = (kk & 3) * 2 + (mi >> 1);
+                    ldsm4(qa, qs + (kk >> 2) * (R * 128) + qrow * 128 + ((qc ^ l7) << 4));
+                    mma_bf16(s[i][0], qa, kb[0], kb[1]);
+                    mma_bf16(s[i][1], qa, kb[2], kb[3]);
+                }
+            }
+            // scores in powers of two; a strip that some row does not see whole is masked
+            const bool masked = key0 + kStrip - 1 > p_lo || (a.window > 0 && key0 <= p_hi - a.window);
+            bool grow = false;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[i][n][e] * a.scale_log2;
+                        if (masked) {
+                            const int key = key0 + n * 8 + (lane & 3) * 2 + (e & 1);
+                            if (key > hi[i][e >> 1] || key <= lo[i][e >> 1]) x = -INFINITY;
+                        }
+                        s[i][n][e] = x;
+                        grow |= x > m[i][e >> 1] + 8.0f;
+                    }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x = fmaxf(fmaxf(s[i][0][2 * h], s[i][0][2 * h + 1]), fmaxf(s[i][1][2 * h], s[i][1][2 * h + 1]));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        if (x > m[i][h]) {
+                            const float f = exp2_fast(m[i][h] - x);   // 0 from -inf
+                            m[i][h] = x;
+                            l[i][h] *= f;
+#pragma unroll
+                            for (int n = 0; n < D / 8; ++n) {
+                                o[i][n][2 * h] *= f;
+                                o[i][n][2 * h + 1] *= f;
+                            }
+                        }
+                    }
+            }
+            uint32_t pa[MT][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // a row that has seen nothing keeps m = -inf: its probabilities are 0
+                        const float mm = m[i][h] == -INFINITY ? 0.0f : m[i][h];
+                        const float x = exp2_fast(s[i][n][2 * h] - mm), y = exp2_fast(s[i][n][2 * h + 1] - mm);
+                        l[i][h] += x + y;
+                        pa[i][2 * n + h] = pack_bf16(x, y);
+                    }
+            }
+            // slots at or past the last visible key may hold anything: their V counts as 0
+            uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
+            if (key0 + kStrip > j1) {
+                const int k0 = key0 + (lane & 3) * 2;
+                z0 = (k0 < j1 ? 0xffffu : 0u) | (k0 + 1 < j1 ? 0xffff0000u : 0u);
+                z1 = (k0 + 8 < j1 ? 0xffffu : 0u) | (k0 + 9 < j1 ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                uint32_t vb[4];
+                const int vrow = (mi & 1) * 8 + l7, vc = (n & 3) * 2 + (mi >> 1);
+                ldsm4_t(vb, vs + (n >> 2) * (kStrip * 128) + vrow * 128 + ((vc ^ l7) << 4));
+                vb[0] &= z0;
+                vb[1] &= z1;
+                vb[2] &= z0;
+                vb[3] &= z1;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    mma_bf16(o[i][2 * n], pa[i], vb[0], vb[1]);
+                    mma_bf16(o[i][2 * n + 1], pa[i], vb[2], vb[3]);
+                }
+            }
+            __syncwarp();
+            if (((k + C::kStages) & 31) == 0) fetch_ids(k + C::kStages);
+            if (k + C::kStages < my) issue(k + C::kStages);
+        }
+        it += (uint32_t)my;
+
+        // ---- the four warps' rows meet ----
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x = l[i][h];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                const int r = i * 16 + h * 8 + (lane >> 2);
+                if ((lane & 3) == 0) {
+                    sm_m[warp * R + r] = m[i][h];
+                    sm_l[warp * R + r] = x;
+                }
+                // [R][D] fp32 over the warp's own ring; columns rotated by row against bank conflicts
+                float* mo = reinterpret_cast<float*>(smem + warp * C::kRing) + r * D;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2*>(mo + ((n * 8 + (lane & 3) * 2 + r * 8) & (D - 1))) =
+                        make_float2(o[i][n][2 * h], o[i][n][2 * h + 1]);
+            }
+        __syncthreads();
+        if (*abort_flag) return;
+
+        const bool whole = w == at && we == at + units;
+        float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * (kMaxR * (kMaxD + 2));
+        auto store_row = [&](int r, int c, const float (&y)[4], float mm, float ll) {
+            // columns c .. c + 3 of row r, divided by the sum
+            const int t = (r0 + r) / a.group, g = (r0 + r) % a.group;
+            const long long row = (long long)(q.q0 + t) * a.q_heads + hk * a.group + g;
+            const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+            *reinterpret_cast<uint2*>(a.out + row * D + c) =
+                make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+            if (c == 0 && a.lse) a.lse[row] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
+        };
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
+            float mm = -INFINITY, ll = 0.0f, y[4] = {};
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sm_m[x * R + r]);
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                const float f = sm_m[x * R + r] == -INFINITY ? 0.0f : exp2_fast(sm_m[x * R + r] - mm);
+                ll += sm_l[x * R + r] * f;
+                const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + x * C::kRing) +
+                                                                  r * D + ((c + r * 8) & (D - 1)));
+                y[0] += v.x * f;
+                y[1] += v.y * f;
+                y[2] += v.z * f;
+                y[3] += v.w * f;
+            }
+            if (whole) {
+                store_row(r, c, y, mm, ll);
+            } else {
+                __stcg(reinterpret_cast<float4*>(part + r * D + c), make_float4(y[0], y[1], y[2], y[3]));
+                if (c == 0) __stcg(reinterpret_cast<float2*>(part + kMaxR * kMaxD + 2 * r), make_float2(mm, ll));
+            }
+        }
+        if (!whole) {
+            // count into the item's counter (its first CTA's); the last one adds the parts
+            const int c_lo = unit_owner(total, P, at), c_hi = unit_owner(total, P, at + units - 1);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) *sm_last = atomicInc(a.counters + c_lo, (unsigned)(c_hi - c_lo)) == (unsigned)(c_hi - c_lo);
+            __syncthreads();
+            if (*sm_last) {
+                __threadfence();
+                for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+                    const int r = i / (D / 4), c = i % (D / 4) * 4;
+                    float mm = -INFINITY, ll = 0.0f, y[4] = {};
+                    for (int x = c_lo; x <= c_hi; ++x) {
+                        // an item's first CTA may have begun before it: the part is then in its second slot
+                        const float* px = a.partial + (size_t)(2 * x + (unit_begin(total, P, x) >= at ? 0 : 1)) *
+                                                          (kMaxR * (kMaxD + 2));
+                        const float2 st = __ldcg(reinterpret_cast<const float2*>(px + kMaxR * kMaxD + 2 * r));
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(px + r * D + c));
+                        const float mn = fmaxf(mm, st.x);
+                        const float f0 = mm == -INFINITY ? 0.0f : exp2_fast(mm - mn);
+                        const float f1 = st.x == -INFINITY ? 0.0f : exp2_fast(st.x - mn);
+                        mm = mn;
+                        ll = ll * f0 + st.y * f1;
+                        y[0] = y[0] * f0 + v.x * f1;
+                        y[1] = y[1] * f0 + v.y * f1;
+                        y[2] = y[2] * f0 + v.z * f1;
+                        y[3] = y[3] * f0 + v.w * f1;
+                    }
+                    store_row(r, c, y, mm, ll);
+                }
+            }
+        }
+        // the ring was written as ordinary memory: order that before the next copies into it
+        fence_proxy_async_smem();
+        __syncthreads();
+
+        // ---- next item ----
+        w = we;
+        if (w < w1) {
+            at += units;
+            r0 += R;
+            if (r0 >= q.n * a.group) {
+                r0 = 0;
+                if (++hk == Hk) {
+                    hk = 0;
+                    do q = load_seq(a.s, a.c.page_size, ++b, &g_attn_rows_error);
+                    while (q.n == 0 && b + 1 < B);
+                }
+            }
+        }
+    }
+}
+
+template <int D, int MT>
+cudaError_t launch(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
+    using C = Cfg<D, MT>;
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, k, a.c, kStrip, D / 64) || !make_cache_map(&mv, v, a.c, kStrip, D / 64))
+        return cudaErrorInvalidValue;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    // no more CTAs than the call can have shares
+    const long long room = (long long)a.s.width * a.c.page_size;
+    const long long keys = a.window > 0 ? std::min((long long)a.window + a.s.max_new, room) : room;
+    const long long tiles = ((long long)a.s.max_new * a.group + C::R - 1) / C::R;
+    const long long most = (long long)a.s.B * a.c.kv_heads * tiles * ((keys + kStrip - 1) / kStrip + 1);
+    long long P = (long long)sms * C::kCtas;
+    P = std::min(P, (most + kMinUnits - 1) / kMinUnits);
+    return launch_pdl(attn_rows_kernel<D, MT>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, mv, a);
+}
+
+}  // namespace
+
+size_t attn_rows_workspace() { return (size_t)kMaxSms * 2 * 2 * kMaxR * (kMaxD + 2) * 4; }
+
+cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int max_rows, int sms,
+                             cudaStream_t stream) {
+    // 32 rows read the cache once for up to 32; at most 16 rows need half the products
+    switch (a.c.head_dim) {
+        case 64: return max_rows <= 16 ? launch<64, 1>(a, k, v, sms, stream) : launch<64, 2>(a, k, v, sms, stream);
+        case 128: return max_rows <= 16 ? launch<128, 1>(a, k, v, sms, stream) : launch<128, 2>(a, k, v, sms, stream);
+        default: return launch<256, 1>(a, k, v, sms, stream);
+    }
+}
+
+cudaError_t read_attn_rows_device_error(int* code) {
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_rows_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_attn_rows_error, &zero, sizeof(int));
+}
+
+}  // namespace tern

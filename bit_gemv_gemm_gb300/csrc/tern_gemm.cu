@@ -47,10 +47,6 @@
 // tcgen05.commit).  Every wait is bounded: after a second it raises a CTA abort
 // flag and the device error word, every role drains what it issued, tensor
 // memory is freed and the kernel returns.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "tern_sm100.cuh"
 
 namespace tern {
@@ -548,20 +544,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Host side: tensor maps through the driver entry point (no libcuda link).
 // ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
     auto enc = get_encode();

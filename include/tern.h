@@ -507,6 +507,7 @@ enum {
     TERN_DEVERR_GEMV_ACTIVATION_RANGE = 0x203, /* decode: a group's largest |x| was >= 2^100 or not finite */
     TERN_DEVERR_CACHE_PAGE = 0x301,          /* cache: a page id outside the pool */
     TERN_DEVERR_CACHE_SEQUENCE = 0x302,      /* cache: a length or token range that the call's arrays do not hold */
+    TERN_DEVERR_ATTN_WAIT = 0x311,           /* attention: a wait for a copy or a product gave up */
     TERN_DEVERR_CACHE_SLOT = 0x303           /* cache: a slot past the pool's last */
 };
 
