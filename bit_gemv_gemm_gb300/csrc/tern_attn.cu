@@ -5,6 +5,8 @@
 //   o_i = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij),
 //   mass_j <- decay mass_j + sum_i exp(s_ij - lse_i)  (the queries of all the
 //   heads that share key j's head).
+#include <algorithm>
+
 #include "tern_attn.cuh"
 
 namespace tern {
@@ -89,7 +91,7 @@ extern "C" size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new
     if (B < 1 || T < 0 || max_new < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return kAttnCounterBytes + attn_rows_workspace();
+    return kAttnCounterBytes + std::max(attn_rows_workspace(), attn_tiles_workspace());
 }
 
 extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, const void* k_cache,
@@ -120,15 +122,20 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.q_stride = q_stride;
     a.q_heads = q_heads;
     a.group = q_heads / a.c.kv_heads;
-    a.scale_log2 = scale * 1.44269504088896341f;
+    // (0 becomes a number that scores cannot notice: -inf times it is still -inf)
+    a.scale_log2 = scale == 0.0f ? 1e-30f : scale * 1.44269504088896341f;
     a.window = window;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
     a.counters = static_cast<unsigned*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
     const long long rows = (long long)a.s.max_new * a.group;
-    if (launch_attn_rows(a, k_cache, v_cache, rows > 16 ? 32 : (int)rows, sms, (cudaStream_t)stream) != cudaSuccess)
-        return TERN_ERR_CUDA;
+    // few rows: bound by reading the cache, which the rows kernel does once for
+    // 32 rows (16 at D = 256); more rows: the tensor cores
+    const bool few = rows <= (a.c.head_dim == 256 ? 16 : 32);
+    const cudaError_t e = few ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
+                              : launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream);
+    if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;
 }

@@ -11,7 +11,7 @@
 namespace tern {
 
 constexpr int kMaxSms = 160;                      // the workspace is sized for this many
-constexpr size_t kAttnCounterBytes = 4096;
+constexpr size_t kAttnCounterBytes = 8192;       // 8 counters a CTA
 constexpr uint64_t kAttnWaitNs = 1000000000ull;   // 1 s: far beyond any real wait
 
 struct AttnArgs {
@@ -20,6 +20,7 @@ struct AttnArgs {
     CacheView c;
     SeqView s;
     int q_heads, group;
+    int tiles;               // row tiles of the longest sequence
     float scale_log2;        // scale * log2(e): scores are kept in powers of two
     int window;
     __nv_bfloat16* out;
@@ -36,22 +37,26 @@ __device__ __forceinline__ void keys_of_rows(const Seq& q, int group, int window
     j0 = window > 0 ? max(first - window + 1, 0) : 0;
 }
 
-// Keys are handed out in units of kUnit, row tile by row tile: the units of
-// all (sequence, key head, row tile) items, in that order, are cut into one
-// equal contiguous share per CTA, whatever the sequences' lengths.  An item
-// that no key reaches counts one unit (its rows are written as zeros).
+// Keys are handed out in units of UNIT: the units of all items, in the order
+// (sequence, row tile, key head), are cut into one equal contiguous share per
+// CTA, whatever the sequences' lengths.  An item that no key reaches counts one
+// unit (its rows are written as zeros).
+struct Item {
+    int b, rt, hk;
+    Seq q;
+    int rows, j0, j1, units;   // its rows and the keys they see together
+    long long at;              // its first unit
+};
 template <int UNIT>
-__device__ __forceinline__ int item_units(const Seq& q, int group, int window, int r0, int r1) {
-    int j0, j1;
-    keys_of_rows(q, group, window, r0, r1, j0, j1);
-    return j1 > j0 ? (j1 - 1) / UNIT - j0 / UNIT + 1 : 1;
-}
-template <int UNIT>
-__device__ __forceinline__ long long head_units(const Seq& q, int group, int window, int rows) {
-    const int all = q.n * group;
-    long long sum = 0;
-    for (int r = 0; r < all; r += rows) sum += item_units<UNIT>(q, group, window, r, min(r + rows, all));
-    return sum;
+__device__ __forceinline__ void item_extent(const AttnArgs& a, int R, Item& t) {
+    const int r0 = t.rt * R, all = t.q.n * a.group;
+    t.rows = min(R, all - r0);
+    if (t.rows <= 0) {
+        t.rows = t.units = 0;
+        return;
+    }
+    keys_of_rows(t.q, a.group, a.window, r0, r0 + t.rows, t.j0, t.j1);
+    t.units = t.j1 > t.j0 ? (t.j1 - 1) / UNIT - t.j0 / UNIT + 1 : 1;
 }
 __host__ __device__ inline long long unit_begin(long long total, int P, int c) { return total * c / P; }
 __device__ inline int unit_owner(long long total, int P, long long u) {
@@ -59,6 +64,86 @@ __device__ inline int unit_owner(long long total, int P, long long u) {
     while (c + 1 < P && unit_begin(total, P, c + 1) <= u) ++c;
     while (c > 0 && unit_begin(total, P, c) > u) --c;
     return c;
+}
+
+// The next item, past row tiles that a sequence does not have; `tiles` row
+// tiles are counted for every sequence.
+template <int UNIT>
+__device__ __forceinline__ void next_item(const AttnArgs& a, int R, int tiles, Item& t, int* err) {
+    t.at += t.units;
+    if (++t.hk < a.c.kv_heads) return;
+    t.hk = 0;
+    do {
+        if (++t.rt >= tiles) {
+            t.rt = 0;
+            if (++t.b >= a.s.B) return;
+            t.q = load_seq(a.s, a.c.page_size, t.b, err);
+        }
+        item_extent<UNIT>(a, R, t);
+    } while (t.units == 0);
+}
+
+// This CTA's share [w0, w1) of all units, and the item that holds w0; P shares
+// of at least min_units each.  Called by all THREADS threads; false: no share.
+// `sm`: 8 + THREADS / 32 words of shared memory.
+template <int UNIT, int THREADS>
+__device__ bool find_share(const AttnArgs& a, int R, int tiles, int min_units, long long* sm, int* err,
+                           long long& total, int& P, long long& w0, long long& w1, Item& t) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = a.c.kv_heads;
+    const long long all = (long long)a.s.B * tiles;
+    const long long per = (all + THREADS - 1) / THREADS;
+    const long long f0 = min((long long)threadIdx.x * per, all), f1 = min(f0 + per, all);
+    auto units_of = [&](long long f) {
+        t.b = (int)(f / tiles);
+        t.rt = (int)(f - (long long)t.b * tiles);
+        t.q = load_seq(a.s, a.c.page_size, t.b, err);
+        item_extent<UNIT>(a, R, t);
+        return (long long)t.units * Hk;
+    };
+    long long mine = 0;
+    for (long long f = f0; f < f1; ++f) mine += units_of(f);
+    long long x = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, k);
+        if (lane >= k) x += y;
+    }
+    if (lane == 31) sm[8 + warp] = x;
+    __syncthreads();
+    long long before = x - mine;
+    total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sm[8 + w];
+        total += sm[8 + w];
+    }
+    P = (int)min((long long)gridDim.x, (total + min_units - 1) / min_units);
+    if ((int)blockIdx.x >= P) return false;
+    w0 = unit_begin(total, P, blockIdx.x);
+    w1 = unit_begin(total, P, blockIdx.x + 1);
+    if (w0 >= before && w0 < before + mine) {
+        long long at = before;
+        for (long long f = f0; f < f1; ++f) {
+            const long long u = units_of(f);
+            if (w0 < at + u) {
+                sm[0] = f;
+                sm[1] = at;
+                break;
+            }
+            at += u;
+        }
+    }
+    __syncthreads();
+    (void)units_of(sm[0]);
+    t.hk = (int)((w0 - sm[1]) / t.units);
+    t.at = sm[1] + (long long)t.hk * t.units;
+    return true;
+}
+
+// No call has more units than this (host: the lengths are on the device).
+inline long long most_units(const AttnArgs& a, int unit) {
+    const long long room = (long long)a.s.width * a.c.page_size;
+    const long long keys = a.window > 0 && a.window + (long long)a.s.max_new < room ? a.window + (long long)a.s.max_new : room;
+    return (long long)a.s.B * a.c.kv_heads * a.tiles * ((keys + unit - 1) / unit + 1);
 }
 
 // A cache array as the TMA sees it: [page][head][d / 64][slot][64 values], a
@@ -99,7 +184,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // Launchers of the kernels (each checks nothing: the entry point has).
-cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int max_rows, int sms, cudaStream_t stream);
+cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
+cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 size_t attn_rows_workspace();
+size_t attn_tiles_workspace();
 
 }  // namespace tern

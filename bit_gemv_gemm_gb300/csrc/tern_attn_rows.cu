@@ -40,7 +40,7 @@ struct Cfg {
     static constexpr size_t kSmemBar = kSmemQ + kQ;
     static constexpr size_t kSmemStat = kSmemBar + kWarps * kStages * 8;
     static constexpr size_t kSmemMisc = kSmemStat + (size_t)kWarps * R * 8;
-    static constexpr size_t kSmem = kSmemMisc + 128 + 1024;
+    static constexpr size_t kSmem = kSmemMisc + 128 + 1024;       // + alignment slack
     static_assert(kRing >= R * D * 4, "a warp's rows are merged through its ring");
 };
 
@@ -59,28 +59,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A block-wide sum over threads before this one, and over all.
-__device__ __forceinline__ long long block_scan(long long v, long long* sm, long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = v;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, k);
-        if (lane >= k) x += y;
-    }
-    if (lane == 31) sm[warp] = x;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sm[w];
-        total += sm[w];
-    }
-    __syncthreads();
-    return before + x - v;
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::kCtas)
 attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -97,10 +75,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const uint32_t bars = sbase + (uint32_t)C::kSmemBar + (uint32_t)(warp * C::kStages * 8);
     float* sm_m = reinterpret_cast<float*>(smem + C::kSmemStat);             // [warp][R]
     float* sm_l = sm_m + kWarps * R;
-    long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [kWarps]
-    long long* sm_at = sm_scan + kWarps;                                      // sequence, its first unit
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_at + 2);
-    int* sm_last = reinterpret_cast<int*>(sm_at + 2) + 1;
+    long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + kWarps]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_scan + 8 + kWarps);
+    int* sm_last = reinterpret_cast<int*>(sm_scan + 8 + kWarps) + 1;
 
     if (lane == 0) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8u * s, 1);
@@ -115,58 +92,18 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     pdl_launch_dependents();
     pdl_wait();
 
-    // this CTA's share of the units, and the sequence it starts in
-    const int B = a.s.B, Hk = a.c.kv_heads, cta = blockIdx.x;
-    const int per = (B + kThreads - 1) / kThreads;
-    const int b_lo = min((int)threadIdx.x * per, B), b_hi = min(b_lo + per, B);
-    long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b)
-        mine += Hk * head_units<kStrip>(load_seq(a.s, a.c.page_size, b, &g_attn_rows_error), a.group, a.window, R);
-    long long total;
-    const long long before = block_scan(mine, sm_scan, total);
-    // no share below kMinUnits: a short call is cut into fewer parts
-    const int P = (int)min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
-    if (cta >= P) return;
-    const long long w0 = unit_begin(total, P, cta), w1 = unit_begin(total, P, cta + 1);
-    if (w0 >= w1) return;
-    if (w0 >= before && w0 < before + mine) {
-        long long at = before;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const long long u =
-                Hk * head_units<kStrip>(load_seq(a.s, a.c.page_size, b, &g_attn_rows_error), a.group, a.window, R);
-            if (w0 < at + u) {
-                sm_at[0] = b;
-                sm_at[1] = at;
-                break;
-            }
-            at += u;
-        }
-    }
-    __syncthreads();
-
-    int b = (int)sm_at[0], hk, r0 = 0;
-    long long at = sm_at[1];   // the current item's first unit
-    Seq q = load_seq(a.s, a.c.page_size, b, &g_attn_rows_error);
-    {
-        const long long hu = head_units<kStrip>(q, a.group, a.window, R);
-        hk = (int)((w0 - at) / hu);
-        at += hk * hu;
-        for (;;) {
-            const int u = item_units<kStrip>(q, a.group, a.window, r0, min(r0 + R, q.n * a.group));
-            if (w0 < at + u) break;
-            at += u;
-            r0 += R;
-        }
-    }
+    const int cta = blockIdx.x;
+    int P;
+    long long total, w0, w1;
+    Item t;
+    if (!find_share<kStrip, kThreads>(a, R, a.tiles, kMinUnits, sm_scan, &g_attn_rows_error, total, P, w0, w1, t)) return;
 
     uint32_t it = 0;   // strips this warp has fetched and used, over all segments
     for (long long w = w0; w < w1;) {
-        // ---- one segment: units [w, we) of the item that starts at `at` ----
-        const int rows = min(R, q.n * a.group - r0);
-        const int units = item_units<kStrip>(q, a.group, a.window, r0, r0 + rows);
-        const long long we = min(w1, at + units);
-        int j0, j1;
-        keys_of_rows(q, a.group, a.window, r0, r0 + rows, j0, j1);
+        // ---- one segment: units [w, we) of the item ----
+        const Seq q = t.q;
+        const int rows = t.rows, units = t.units, j0 = t.j0, j1 = t.j1, r0 = t.rt * R, hk = t.hk, b = t.b;
+        const long long at = t.at, we = min(w1, at + units);
         const int first = j0 / kStrip + (int)(w - at);
         const int strips = j1 > j0 ? (int)(we - w) : 0;
         const int my = strips > warp ? (strips - warp + kWarps - 1) / kWarps : 0;
@@ -195,8 +132,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             const int r = i / (D / 8), c = i % (D / 8);
             uint4 v = make_uint4(0, 0, 0, 0);
             if (r < rows) {
-                const int t = (r0 + r) / a.group, g = (r0 + r) % a.group;
-                v = *reinterpret_cast<const uint4*>(a.q + (long long)(q.q0 + t) * a.q_stride +
+                const int tok = (r0 + r) / a.group, g = (r0 + r) % a.group;
+                v = *reinterpret_cast<const uint4*>(a.q + (long long)(q.q0 + tok) * a.q_stride +
                                                     (long long)(hk * a.group + g) * D + c * 8);
             }
             *reinterpret_cast<uint4*>(smem + C::kSmemQ + (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
@@ -363,8 +300,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * (kMaxR * (kMaxD + 2));
         auto store_row = [&](int r, int c, const float (&y)[4], float mm, float ll) {
             // columns c .. c + 3 of row r, divided by the sum
-            const int t = (r0 + r) / a.group, g = (r0 + r) % a.group;
-            const long long row = (long long)(q.q0 + t) * a.q_heads + hk * a.group + g;
+            const int tok = (r0 + r) / a.group, g = (r0 + r) % a.group;
+            const long long row = (long long)(q.q0 + tok) * a.q_heads + hk * a.group + g;
             const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
             *reinterpret_cast<uint2*>(a.out + row * D + c) =
                 make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
@@ -429,25 +366,13 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         fence_proxy_async_smem();
         __syncthreads();
 
-        // ---- next item ----
         w = we;
-        if (w < w1) {
-            at += units;
-            r0 += R;
-            if (r0 >= q.n * a.group) {
-                r0 = 0;
-                if (++hk == Hk) {
-                    hk = 0;
-                    do q = load_seq(a.s, a.c.page_size, ++b, &g_attn_rows_error);
-                    while (q.n == 0 && b + 1 < B);
-                }
-            }
-        }
+        if (w < w1) next_item<kStrip>(a, R, a.tiles, t, &g_attn_rows_error);
     }
 }
 
 template <int D, int MT>
-cudaError_t launch(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
+cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream_t stream) {
     using C = Cfg<D, MT>;
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, k, a.c, kStrip, D / 64) || !make_cache_map(&mv, v, a.c, kStrip, D / 64))
@@ -461,13 +386,8 @@ cudaError_t launch(const AttnArgs& a, const void* k, const void* v, int sms, cud
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    // no more CTAs than the call can have shares
-    const long long room = (long long)a.s.width * a.c.page_size;
-    const long long keys = a.window > 0 ? std::min((long long)a.window + a.s.max_new, room) : room;
-    const long long tiles = ((long long)a.s.max_new * a.group + C::R - 1) / C::R;
-    const long long most = (long long)a.s.B * a.c.kv_heads * tiles * ((keys + kStrip - 1) / kStrip + 1);
-    long long P = (long long)sms * C::kCtas;
-    P = std::min(P, (most + kMinUnits - 1) / kMinUnits);
+    a.tiles = (int)(((long long)a.s.max_new * a.group + C::R - 1) / C::R);
+    const long long P = std::min<long long>((long long)sms * C::kCtas, (most_units(a, kStrip) + kMinUnits - 1) / kMinUnits);
     return launch_pdl(attn_rows_kernel<D, MT>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, mv, a);
 }
 
@@ -475,8 +395,9 @@ cudaError_t launch(const AttnArgs& a, const void* k, const void* v, int sms, cud
 
 size_t attn_rows_workspace() { return (size_t)kMaxSms * 2 * 2 * kMaxR * (kMaxD + 2) * 4; }
 
-cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int max_rows, int sms,
+cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms,
                              cudaStream_t stream) {
+    const long long max_rows = (long long)a.s.max_new * a.group;
     // 32 rows read the cache once for up to 32; at most 16 rows need half the products
     switch (a.c.head_dim) {
         case 64: return max_rows <= 16 ? launch<64, 1>(a, k, v, sms, stream) : launch<64, 2>(a, k, v, sms, stream);

@@ -1,0 +1,625 @@
+// tern_attn_tiles.cu -- attention of many query rows a key head (prompt chunks)
+// on the tcgen05 tensor cores.
+//
+// A row tile is 128 packed rows (128 / group tokens, every head of the group),
+// so one K and V tile serves all the heads that share it.  A CTA keeps NS row
+// tiles at once (two; one at D = 256, where the accumulator takes half of
+// tensor memory) against the same stream of 128-key tiles:
+//   * a TMA warp brings Q once and then K and V, in 16 KB pieces of 64 head
+//     values x 128 keys (128-byte swizzled rows), through one ring of eight; a
+//     page gives boxes of up to 128 slots, one lane a box;
+//   * one thread issues S = Q K^T (both operands in shared memory, K-major) and
+//     O += P V (P in tensor memory, V MN-major) with M = 128;
+//   * a warpgroup per row tile, one thread a row, reads S, takes the running
+//     maximum, writes P = exp2(S - m) as bf16 over S's own columns and keeps
+//     the sum in fp32.  O is only rescaled when a score passes the maximum in
+//     use by 2^8, so P and the sums stay below 2^8 of their largest term.
+// While one tile's softmax runs the tensor cores work for the other (at D =
+// 256: for the next keys, into a second S).  The MMA thread issues PV(j) and
+// then QK(j + 1) of a row tile, so S (and P over it) needs one buffer a tile:
+// products complete in issue order.
+// Slots past a sequence's last key may hold anything: scores are masked before
+// the exponential and V's rows are zeroed in shared memory by the TMA warp
+// before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
+// Work is shared out as in the rows kernel: equal contiguous shares of all
+// (sequence, row tiles, key head) items' 128-key tiles; parts meet in the
+// workspace, and the warp that counts last for its 32 rows adds them in order.
+#include <algorithm>
+
+#include "tern_attn.cuh"
+
+namespace tern {
+namespace {
+
+using namespace sm100;
+
+__device__ int g_attn_tiles_error;
+
+constexpr int kKeys = 128, kRows = 128;
+constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
+constexpr int kSlots = 8;
+constexpr int kMinTiles = 4;                // key tiles a share holds at least
+
+template <int D>
+struct Cfg {
+    static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
+    static constexpr int NS = D == 256 ? 1 : 2;             // row tiles a CTA
+    static constexpr int kSoftWarps = 4 * NS;
+    static constexpr int kThreads = 32 * (kSoftWarps + 2);
+    static constexpr uint32_t kS = 0, kO = 256;             // tensor memory: S (and P) at 128 b, O at kO + D s
+    static constexpr size_t kSmemQ = 0;
+    static constexpr size_t kSmemRing = (size_t)NS * NC * kChunk;
+    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * kChunk;
+    // barriers: full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], tail, drain
+    static constexpr int kBars = 2 * kSlots + 14;
+    static constexpr size_t kSmemMisc = kSmemBar + kBars * 8;
+    static constexpr size_t kSmem = kSmemMisc + 256 + 1024;
+    static constexpr size_t kPart = (size_t)NS * kRows * (D + 2);   // floats of one part
+};
+constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys);
+
+// floats are exchanged four columns at a time, [column / 4][row][4]
+__device__ __forceinline__ size_t part_at(int D, int s, int row, int c4) {
+    return (size_t)s * kRows * (D + 2) + ((size_t)c4 * kRows + row) * 4;
+}
+__device__ __forceinline__ size_t part_stat(int D, int s, int row) {
+    return (size_t)s * kRows * (D + 2) + (size_t)D * kRows + 2 * row;
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, const AttnArgs a, const int box_rows) {
+    using C = Cfg<D>;
+    constexpr int NC = C::NC, NS = C::NS;
+    constexpr bool kWide = D == 256;   // one row tile, two S buffers
+    extern __shared__ __align__(1024) unsigned char smem_dyn[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem), bar0 = sbase + (uint32_t)C::kSmemBar;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    auto full_bar = [&](uint32_t i) { return bar((int)(i % kSlots)); };
+    auto empty_bar = [&](uint32_t i) { return bar(kSlots + (int)(i % kSlots)); };
+    auto slot_phase = [&](uint32_t i) { return (i / kSlots) & 1u; };
+    auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)kChunk; };
+    enum { Q_FULL = 2 * kSlots, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FULL = P_FULL + 2,
+           O_EMPTY = O_FULL + 2, TAIL = O_EMPTY + 2, DRAIN = TAIL + 1 };
+    long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm_scan + 8 + C::kThreads / 32);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kBars; ++i) {
+            const bool by_warps = (i >= P_FULL && i < P_FULL + 2) || (i >= O_EMPTY && i < O_EMPTY + 2);
+            mbar_init(bar(i), by_warps ? 4 : 1);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+    }
+    if (warp == C::kSoftWarps + 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int tile_rows = kRows / a.group * a.group;   // whole tokens
+    const int R = NS * tile_rows;
+    int P;
+    long long total, w0, w1;
+    Item t;
+    const bool busy = find_share<kKeys, C::kThreads>(a, R, a.tiles, kMinTiles, sm_scan, &g_attn_tiles_error, total, P,
+                                                     w0, w1, t);
+    auto fail = [&] {
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            report_device_error(&g_attn_tiles_error, TERN_DEVERR_ATTN_WAIT);
+        }
+    };
+    auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, abort_flag, kAttnWaitNs); };
+
+    if (!busy) {
+        // no share: straight to the end
+    } else if (warp == C::kSoftWarps) {
+        // ------------------------------ TMA ------------------------------
+        uint32_t it = 0, seg = 0, used[2] = {0, 0}, tails = 0;
+        bool ok = true;
+        const int boxes = kKeys / box_rows;
+        for (long long w = w0; w < w1 && ok; ++seg) {
+            const long long we = min(w1, t.at + t.units);
+            const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
+            const int key0 = (t.j0 / kKeys + (int)(w - t.at)) * kKeys;
+            for (int s = 0; s < NS && ok && nt > 0; ++s) {
+                if (s * tile_rows >= t.rows) continue;
+                if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY + s), (used[s] & 1u) ^ 1u))) { ok = false; break; }
+                ++used[s];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(Q_FULL + s), (uint32_t)(NC * tile_rows * 128));
+                    const int tok = t.q.q0 + (t.rt * R + s * tile_rows) / a.group;
+                    for (int c = 0; c < NC; ++c)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+                            "{%2, %3, %4, %5}], [%6];" ::"r"(sbase + (uint32_t)((s * NC + c) * kChunk)),
+                            "l"(reinterpret_cast<uint64_t>(&tmap_q)), "r"(0), "r"(t.hk * a.group), "r"(tok), "r"(c),
+                            "r"(bar(Q_FULL + s))
+                            : "memory");
+                }
+            }
+            const int* trow = a.s.table + (long long)t.b * a.s.width;
+            const int c = lane / boxes, box = lane - c * boxes;   // this lane's piece of a tile
+            auto page_of = [&](int j) {
+                const int k = key0 + j * kKeys + box * box_rows;
+                const bool use = c < NC && k < t.q.len && k + box_rows > t.j0;
+                return use ? checked_page(trow[k / a.c.page_size], a.c.pages, &g_attn_tiles_error) : -1;
+            };
+            auto load = [&](int j, int page, bool is_v) {
+                const int k0 = key0 + j * kKeys;
+                // boxes that hold no key of these rows are not read; V's rows there count as 0
+                const bool part = is_v && (k0 + kKeys > t.q.len || k0 + box_rows <= t.j0);
+                for (int x = 0; x < NC; ++x)
+                    if (!__all_sync(0xffffffffu, wait(empty_bar(it + x), slot_phase(it + x) ^ 1u))) {
+                        ok = false;
+                        return;
+                    }
+                const uint32_t mine = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t bytes = (uint32_t)__popc(mine & ((1u << boxes) - 1u)) * box_rows * 128u;
+                if (lane == 0) {
+                    if (part)
+                        mbar_arrive_expect_tx(bar(TAIL), bytes * NC);
+                    else
+                        for (int x = 0; x < NC; ++x) mbar_arrive_expect_tx(full_bar(it + x), bytes);
+                }
+                __syncwarp();
+                if (page >= 0)
+                    tma_load_cache(slot_addr(it + c) + (uint32_t)(box * box_rows * 128), is_v ? &tmap_v : &tmap_k,
+                                   (k0 + box * box_rows) % a.c.page_size, c, t.hk, page,
+                                   part ? bar(TAIL) : full_bar(it + c));
+                if (part) {
+                    if (!__all_sync(0xffffffffu, wait(bar(TAIL), tails & 1u))) {
+                        ok = false;
+                        return;
+                    }
+                    ++tails;
+                    for (int i = lane; i < kKeys * NC * 8; i += 32) {
+                        const int x = i / (kKeys * 8), r = i / 8 % kKeys, k = k0 + r;
+                        if (k >= t.q.len || (k / box_rows + 1) * box_rows <= t.j0)
+                            *reinterpret_cast<uint4*>(smem + C::kSmemRing + ((it + x) % kSlots) * kChunk + r * 128 +
+                                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int x = 0; x < NC; ++x) mbar_arrive(full_bar(it + x));
+                }
+                it += NC;
+            };
+            // in the order of their use: K0, then V(j), K(j + 1) (D = 256: K(j + 1), V(j))
+            int page = nt > 0 ? page_of(0) : -1;
+            if (nt > 0) load(0, page, false);
+            for (int j = 0; j < nt && ok; ++j) {
+                const int next = j + 1 < nt ? page_of(j + 1) : -1;
+                if (!kWide) load(j, page, true);
+                if (ok && j + 1 < nt) load(j + 1, next, false);
+                if (kWide && ok) load(j, page, true);
+                page = next;
+            }
+            w = we;
+            if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
+        }
+        if (!ok && lane == 0) {
+            fail();
+            // copies in flight land before the CTA goes away
+            for (uint32_t i = it < (uint32_t)kSlots ? 0 : it - kSlots; i < it + NC; ++i)
+                (void)mbar_wait_drain(full_bar(i), slot_phase(i), 20000000ull);
+            for (int s = 0; s < NS; ++s)
+                if (used[s]) (void)mbar_wait_drain(bar(Q_FULL + s), (used[s] - 1u) & 1u, 20000000ull);
+            (void)mbar_wait_drain(bar(TAIL), tails & 1u, 20000000ull);
+        }
+        __syncwarp();
+    } else if (warp == C::kSoftWarps + 1) {
+        // ------------------------------ MMA ------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, D) | kIdescBMnMajor;
+            uint32_t it = 0, used[2] = {0, 0}, pc[2] = {0, 0}, jobs = 0;
+            bool ok = true, issued = false;
+            auto need = [&](uint32_t b, uint32_t parity) {
+                if (ok && !wait(b, parity)) ok = false;
+                return ok;
+            };
+            auto qk = [&](int s, uint32_t buf, uint32_t slot) {   // S(buf) = Q(s) K^T, K's chunks from `slot`
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)((s * NC + c) * kChunk));
+                    const uint64_t kd = smem_desc_k_sw128(slot_addr(slot + c));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16_ss(tmem + C::kS + 128u * buf, qd + 2 * kk, kd + 2 * kk, kIdescQK, (c | kk) ? 1u : 0u);
+                }
+                mma_commit(bar(S_FULL + (int)buf));
+                issued = true;
+            };
+            auto pv = [&](int s, uint32_t buf, uint32_t slot, bool acc) {   // O(s) += P(buf) V
+                const uint64_t vd = smem_desc_mn_sw128(slot_addr(slot), kChunk);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_f16_ts(tmem + C::kO + (uint32_t)(D * s), tmem + C::kS + 128u * buf + 8u * kk,
+                               vd + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (acc || kk) ? 1u : 0u);
+            };
+            auto arrived = [&](uint32_t slot) {   // the tile's chunks are in shared memory
+                for (int c = 0; c < NC; ++c)
+                    if (!need(full_bar(slot + c), slot_phase(slot + c))) return false;
+                return true;
+            };
+            auto release = [&](uint32_t slot) {
+                for (int c = 0; c < NC; ++c) mma_commit(empty_bar(slot + c));
+            };
+            for (long long w = w0; w < w1 && ok;) {
+                const long long we = min(w1, t.at + t.units);
+                const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
+                const int ns = t.rows > tile_rows ? NS : 1;
+                if (nt > 0) {
+                    if (!kWide) {
+                        const uint32_t k0 = it;
+                        it += NC;
+                        for (int s = 0; s < ns && ok; ++s) {
+                            if (need(bar(Q_FULL + s), used[s] & 1u) && (s > 0 || arrived(k0))) {
+                                tc_fence_after();
+                                qk(s, s, k0);
+                            }
+                        }
+                        if (ok) release(k0);
+                        for (int j = 0; j < nt && ok; ++j) {
+                            const uint32_t v = it, k = it + NC;
+                            const bool more = j + 1 < nt;
+                            it += more ? 2 * NC : NC;
+                            for (int s = 0; s < ns && ok; ++s) {
+                                if (s == 0 && !arrived(v)) break;
+                                if (!need(bar(P_FULL + s), pc[s]++ & 1u)) break;
+                                // the previous item's output has been read
+                                if (j == 0 && !need(bar(O_EMPTY + s), (used[s] & 1u) ^ 1u)) break;
+                                tc_fence_after();
+                                pv(s, s, v, j > 0);
+                                if (s == ns - 1) release(v);
+                                if (more) {
+                                    if (s == 0 && !arrived(k)) break;
+                                    tc_fence_after();
+                                    qk(s, s, k);
+                                    if (s == ns - 1) release(k);
+                                } else {
+                                    mma_commit(bar(O_FULL + s));
+                                    mma_commit(bar(Q_EMPTY + s));
+                                    ++used[s];
+                                }
+                            }
+                        }
+                    } else {
+                        uint32_t k = it;
+                        it += NC;
+                        if (need(bar(Q_FULL), used[0] & 1u) && arrived(k)) {
+                            tc_fence_after();
+                            qk(0, jobs & 1u, k);
+                            release(k);
+                        }
+                        for (int j = 0; j < nt && ok; ++j) {
+                            if (j + 1 < nt) {
+                                k = it;
+                                it += NC;
+                                if (!arrived(k)) break;
+                                tc_fence_after();
+                                qk(0, (jobs + 1) & 1u, k);   // its P, two tiles back, has been used
+                                release(k);
+                            }
+                            const uint32_t v = it;
+                            it += NC;
+                            if (!arrived(v)) break;
+                            if (!need(bar(P_FULL + (int)(jobs & 1u)), (jobs >> 1) & 1u)) break;
+                            if (j == 0 && !need(bar(O_EMPTY), (used[0] & 1u) ^ 1u)) break;
+                            tc_fence_after();
+                            pv(0, jobs & 1u, v, j > 0);
+                            release(v);
+                            mma_commit(bar(O_FULL));
+                            ++jobs;
+                        }
+                        if (ok) {
+                            mma_commit(bar(Q_EMPTY));
+                            ++used[0];
+                        }
+                    }
+                }
+                w = we;
+                if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
+            }
+            if (!ok) {
+                fail();
+                if (issued) {
+                    mma_commit(bar(DRAIN));
+                    (void)mbar_wait_drain(bar(DRAIN), 0u, 100000000ull);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ softmax, output ------------------------------
+        const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t to = tmem + lanes + C::kO + (uint32_t)(D * s);
+        uint32_t sc = 0, oc = 0;   // S and O tiles seen
+        const bool flip = a.scale_log2 < 0.0f;
+        const float scale = fabsf(a.scale_log2);
+        bool ok = true;
+        for (long long w = w0; w < w1 && ok;) {
+            const long long we = min(w1, t.at + t.units);
+            const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
+            const int rows = min(tile_rows, t.rows - s * tile_rows);   // of this row tile
+            if (rows > 0) {
+                const int r = t.rt * R + s * tile_rows + row;          // packed row of the sequence
+                const bool live = row < rows;
+                const int p = t.q.len - t.q.n + r / a.group;
+                const int hi = live ? p : -1, lo = a.window > 0 ? p - a.window : -1;
+                const int p_lo = t.q.len - t.q.n + (t.rt * R + s * tile_rows) / a.group;
+                const int p_hi = t.q.len - t.q.n + (t.rt * R + s * tile_rows + rows - 1) / a.group;
+                const int key0 = (t.j0 / kKeys + (int)(w - t.at)) * kKeys;
+                float m = -INFINITY, l = 0.0f;
+                for (int j = 0; j < nt && ok; ++j, ++sc) {
+                    const uint32_t buf = kWide ? sc & 1u : (uint32_t)s;
+                    const uint32_t ph = kWide ? (sc >> 1) & 1u : sc & 1u;
+                    if (!__all_sync(0xffffffffu, wait(bar(S_FULL + (int)buf), ph))) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t ts = tmem + lanes + C::kS + 128u * buf;
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld_x32(ts + 32u * i, x[i]);
+                    tmem_ld_wait();
+                    if (flip)
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) x[i >> 5][i & 31] ^= 0x80000000u;
+                    const int k0 = key0 + j * kKeys;
+                    if (k0 + kKeys - 1 > p_lo || (a.window > 0 && k0 <= p_hi - a.window)) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (k0 + i > hi || k0 + i <= lo) x[i >> 5][i & 31] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mx[i] = __uint_as_float(x[i][0]);
+#pragma unroll
+                        for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(x[i][e]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (__any_sync(0xffffffffu, (top - m) * scale > 8.0f)) {
+                        const float mn = fmaxf(m, top);
+                        const float f = m == -INFINITY ? 0.0f : exp2_fast((m - mn) * scale);
+                        m = mn;
+                        l *= f;
+                        if (j > 0) {
+                            if (kWide) {
+                                // the product before this one is still adding into O
+                                if (!__all_sync(0xffffffffu, wait(bar(O_FULL), (oc + (uint32_t)j - 1u) & 1u))) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld_x32(to + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st_x32(to + c, o);
+                            }
+                        }
+                    }
+                    const float mb = m == -INFINITY ? 0.0f : m * scale;
+                    float sum[4] = {};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float u = exp2_fast(fmaf(__uint_as_float(x[2 * h + (e >> 4)][2 * (e & 15)]), scale, -mb));
+                            const float v = exp2_fast(fmaf(__uint_as_float(x[2 * h + (e >> 4)][2 * (e & 15) + 1]), scale, -mb));
+                            sum[2 * (e & 1)] += u;
+                            sum[2 * (e & 1) + 1] += v;
+                            pk[e] = pack_bf16(u, v);
+                        }
+                        tmem_st_x32(ts + 32u * h, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(P_FULL + (int)buf));
+                }
+                if (!ok) break;
+                const bool whole = w == t.at && we == t.at + t.units;
+                const int tok = t.q.q0 + r / a.group, head = t.hk * a.group + r % a.group;
+                const long long orow = (long long)tok * a.q_heads + head;
+                if (nt > 0) {
+                    oc += kWide ? (uint32_t)nt : 1u;
+                    // (with two S buffers the product before the last may be running too)
+                    bool done = !kWide || nt < 2 || wait(bar(O_FULL + s), (oc - 2u) & 1u);
+                    done = done && wait(bar(O_FULL + s), (oc - 1u) & 1u);
+                    if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
+                    tc_fence_after();
+                }
+                float* part = a.partial + (size_t)(2 * blockIdx.x + (w == w0 ? 0 : 1)) * C::kPart;
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tmem_ld_x32(to + c, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    if (whole) {
+                        if (live) {
+                            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    y[i] = pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
+                                                     __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
+                                dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __stcg(reinterpret_cast<uint4*>(part + part_at(D, s, row, c / 4 + e)),
+                                   make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                    }
+                }
+                if (nt > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(O_EMPTY + s));
+                }
+                const float m2 = m * scale;   // -inf stays
+                if (whole) {
+                    if (live && a.lse) a.lse[orow] = l > 0.0f ? (m2 + log2f(l)) * 0.693147180559945309f : -INFINITY;
+                } else {
+                    __stcg(reinterpret_cast<float2*>(part + part_stat(D, s, row)), make_float2(m2, l));
+                    __threadfence();
+                    __syncwarp();
+                    const int c_lo = unit_owner(total, P, t.at), c_hi = unit_owner(total, P, t.at + t.units - 1);
+                    unsigned last = 0;
+                    if (lane == 0)
+                        last = atomicInc(a.counters + 8 * c_lo + 4 * s + quad, (unsigned)(c_hi - c_lo)) ==
+                               (unsigned)(c_hi - c_lo);
+                    if (__shfl_sync(0xffffffffu, last, 0)) {
+                        __threadfence();
+                        auto part_of = [&](int x) {   // an item's first CTA may have begun before it
+                            return a.partial + (size_t)(2 * x + (unit_begin(total, P, x) >= t.at ? 0 : 1)) * C::kPart;
+                        };
+                        float mm = -INFINITY, ll = 0.0f;
+                        for (int x = c_lo; x <= c_hi; ++x)
+                            mm = fmaxf(mm, __ldcg(part_of(x) + part_stat(D, s, row)));
+                        const float base = mm == -INFINITY ? 0.0f : mm;
+                        for (int x = c_lo; x <= c_hi; ++x) {
+                            const float2 st = __ldcg(reinterpret_cast<const float2*>(part_of(x) + part_stat(D, s, row)));
+                            ll += st.y * exp2_fast(st.x - base);
+                        }
+                        const float inv2 = ll > 0.0f ? 1.0f / ll : 0.0f;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float y[32] = {};
+                            for (int x = c_lo; x <= c_hi; ++x) {
+                                const float* px = part_of(x);
+                                const float f = exp2_fast(__ldcg(px + part_stat(D, s, row)) - base);
+                                float4 v[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    v[e] = __ldcg(reinterpret_cast<const float4*>(px + part_at(D, s, row, c / 4 + e)));
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    y[4 * e] += v[e].x * f;
+                                    y[4 * e + 1] += v[e].y * f;
+                                    y[4 * e + 2] += v[e].z * f;
+                                    y[4 * e + 3] += v[e].w * f;
+                                }
+                            }
+                            if (live) {
+                                uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    dst[e] = make_uint4(pack_bf16(y[8 * e] * inv2, y[8 * e + 1] * inv2),
+                                                        pack_bf16(y[8 * e + 2] * inv2, y[8 * e + 3] * inv2),
+                                                        pack_bf16(y[8 * e + 4] * inv2, y[8 * e + 5] * inv2),
+                                                        pack_bf16(y[8 * e + 6] * inv2, y[8 * e + 7] * inv2));
+                            }
+                        }
+                        if (live && a.lse)
+                            a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
+                    }
+                }
+            }
+            w = we;
+            if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
+        }
+        if (!ok && lane == 0) fail();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::kSoftWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// q as [token][head][d / 64][64 values], a box of one chunk of a row tile.
+bool make_q_map(CUtensorMap* m, const AttnArgs& a, int D) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t dim[4] = {64, (cuuint64_t)a.q_heads, (cuuint64_t)a.s.T, (cuuint64_t)(D / 64)};
+    const cuuint64_t stride[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.group, (cuuint32_t)(kRows / a.group), 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(a.q), dim, stride, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream_t stream) {
+    using C = Cfg<D>;
+    int box = 128;
+    while (a.c.page_size % box) box >>= 1;   // page_size is a multiple of 16
+    CUtensorMap mq, mk, mv;
+    if (!make_q_map(&mq, a, D) || !make_cache_map(&mk, k, a.c, box, 1) || !make_cache_map(&mv, v, a.c, box, 1))
+        return cudaErrorInvalidValue;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    const int R = C::NS * (kRows / a.group * a.group);
+    a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
+    const long long P = std::min<long long>(sms, (most_units(a, kKeys) + kMinTiles - 1) / kMinTiles);
+    return launch_pdl(attn_tiles_kernel<D>, dim3((unsigned)P), dim3(C::kThreads), C::kSmem, stream, true, mq, mk, mv, a,
+                      box);
+}
+
+}  // namespace
+
+size_t attn_tiles_workspace() {
+    return (size_t)kMaxSms * 2 * 4 * std::max({Cfg<64>::kPart, Cfg<128>::kPart, Cfg<256>::kPart});
+}
+
+cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
+    switch (a.c.head_dim) {
+        case 64: return launch<64>(a, k, v, sms, stream);
+        case 128: return launch<128>(a, k, v, sms, stream);
+        default: return launch<256>(a, k, v, sms, stream);
+    }
+}
+
+cudaError_t read_attn_tiles_device_error(int* code) {
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_tiles_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_attn_tiles_error, &zero, sizeof(int));
+}
+
+}  // namespace tern

@@ -38,6 +38,7 @@ cudaError_t read_f3_device_error(int* code);
 cudaError_t read_rope_device_error(int* code);
 cudaError_t read_attn_device_error(int* code);
 cudaError_t read_attn_rows_device_error(int* code);
+cudaError_t read_attn_tiles_device_error(int* code);
 cudaError_t read_evict_device_error(int* code);
 // One-CTA kernels that run a bounded wait nothing completes (tern_wait_selftest).
 cudaError_t launch_flag_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
