@@ -5,19 +5,23 @@
 // so one K and V tile serves all the heads that share it.  A CTA keeps NS row
 // tiles at once (two; one at D = 256, where the accumulator takes half of
 // tensor memory) against the same stream of 128-key tiles:
-//   * a TMA warp brings Q once and then K and V, in 16 KB pieces of 64 head
-//     values x 128 keys (128-byte swizzled rows), through one ring of eight; a
-//     page gives boxes of up to 128 slots, one lane a box;
-//   * one thread issues S = Q K^T (both operands in shared memory, K-major) and
-//     O += P V (P in tensor memory, V MN-major) with M = 128;
+//   * a TMA warp brings Q once and then K and V, in chunks of 64 head values x
+//     128 keys (16 KB of 128-byte swizzled rows), through one ring; a page
+//     gives boxes of up to 128 slots, one lane a box;
+//   * one thread a row tile issues S = Q K^T (both operands in shared memory,
+//     K-major) and O += P V (P in tensor memory, V MN-major) with M = 128.
+//     Issuing is nearly synchronous (a wait or a commit between products costs
+//     the thread about 150 and 57 clocks that its tensor work does not cover:
+//     110 clocks a 64-clock product from one thread), so two threads issue, each
+//     covering the other's waits; at D = 256 one issues QK, the other PV;
 //   * a warpgroup per row tile, one thread a row, reads S, takes the running
 //     maximum, writes P = exp2(S - m) as bf16 over S's own columns and keeps
 //     the sum in fp32.  O is only rescaled when a score passes the maximum in
 //     use by 2^8, so P and the sums stay below 2^8 of their largest term.
 // While one tile's softmax runs the tensor cores work for the other (at D =
-// 256: for the next keys, into a second S).  The MMA thread issues PV(j) and
-// then QK(j + 1) of a row tile, so S (and P over it) needs one buffer a tile:
-// products complete in issue order.
+// 256: for the next keys, into a second S).  A row tile's thread issues PV(j)
+// and then QK(j + 1), so S (and P over it) needs one buffer a tile: one
+// thread's products complete in issue order.
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
@@ -37,26 +41,57 @@ __device__ int g_attn_tiles_error;
 
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
-constexpr int kSlots = 8;
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 
 template <int D>
 struct Cfg {
     static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
     static constexpr int NS = D == 256 ? 1 : 2;             // row tiles a CTA
+    static constexpr int CG = D == 128 ? 2 : 1;             // chunks of a ring slot
+    static constexpr int NG = NC / CG;                      // slots of a K or V tile
+    static constexpr int kSlots = D == 64 ? 10 : D == 128 ? 5 : 8;
     static constexpr int kSoftWarps = 4 * NS;
-    static constexpr int kThreads = 32 * (kSoftWarps + 2);
+    // two row tiles: a third warpgroup (TMA, two MMA warps, an idle one) gives registers
+    // to the softmax warps, which hold a row of S each: 256 x 208 + 128 x 88 =
+    // 384 x 168, what the CTA was launched with
+    static constexpr int kThreads = NS == 2 ? 384 : 224;
     static constexpr uint32_t kS = 0, kO = 256;             // tensor memory: S (and P) at 128 b, O at kO + D s
     static constexpr size_t kSmemQ = 0;
     static constexpr size_t kSmemRing = (size_t)NS * NC * kChunk;
-    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * kChunk;
-    // barriers: full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], tail, drain
-    static constexpr int kBars = 2 * kSlots + 14;
+    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
+    // barriers: full[slots], empty[slots], then pairs: q_full, q_empty, s_full,
+    // s_empty, p_full, o_full, o_empty, drain; tail
+    static constexpr int kBars = 2 * kSlots + 17;
     static constexpr size_t kSmemMisc = kSmemBar + kBars * 8;
     static constexpr size_t kSmem = kSmemMisc + 256 + 1024;
     static constexpr size_t kPart = (size_t)NS * kRows * (D + 2);   // floats of one part
 };
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys);
+
+// two fp32 values in a register pair
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // floats are exchanged four columns at a time, [column / 4][row][4]
 __device__ __forceinline__ size_t part_at(int D, int s, int row, int c4) {
@@ -71,7 +106,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const AttnArgs a, const int box_rows) {
     using C = Cfg<D>;
-    constexpr int NC = C::NC, NS = C::NS;
+    constexpr int NC = C::NC, NS = C::NS, CG = C::CG, NG = C::NG, kSlots = C::kSlots;
     constexpr bool kWide = D == 256;   // one row tile, two S buffers
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -81,9 +116,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     auto full_bar = [&](uint32_t i) { return bar((int)(i % kSlots)); };
     auto empty_bar = [&](uint32_t i) { return bar(kSlots + (int)(i % kSlots)); };
     auto slot_phase = [&](uint32_t i) { return (i / kSlots) & 1u; };
-    auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)kChunk; };
-    enum { Q_FULL = 2 * kSlots, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FULL = P_FULL + 2,
-           O_EMPTY = O_FULL + 2, TAIL = O_EMPTY + 2, DRAIN = TAIL + 1 };
+    auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)(CG * kChunk); };
+    enum { Q_FULL = 2 * kSlots, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, S_EMPTY = S_FULL + 2, P_FULL = S_EMPTY + 2,
+           O_FULL = P_FULL + 2, O_EMPTY = O_FULL + 2, DRAIN = O_EMPTY + 2, TAIL = DRAIN + 2 };
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm_scan + 8 + C::kThreads / 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -92,7 +127,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kBars; ++i) {
             const bool by_warps = (i >= P_FULL && i < P_FULL + 2) || (i >= O_EMPTY && i < O_EMPTY + 2);
-            mbar_init(bar(i), by_warps ? 4 : 1);
+            const bool by_tiles = NS == 2 && i >= kSlots && i < 2 * kSlots;   // both MMA threads release a slot
+            mbar_init(bar(i), by_warps ? 4 : by_tiles ? 2 : 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -128,7 +164,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 
     if (!busy) {
         // no share: straight to the end
-    } else if (warp == C::kSoftWarps) {
+    } else if (warp >= C::kSoftWarps) {
+      if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp == C::kSoftWarps) {
         // ------------------------------ TMA ------------------------------
         uint32_t it = 0, seg = 0, used[2] = {0, 0}, tails = 0;
         bool ok = true;
@@ -164,24 +202,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const int k0 = key0 + j * kKeys;
                 // boxes that hold no key of these rows are not read; V's rows there count as 0
                 const bool part = is_v && (k0 + kKeys > t.q.len || k0 + box_rows <= t.j0);
-                for (int x = 0; x < NC; ++x)
-                    if (!__all_sync(0xffffffffu, wait(empty_bar(it + x), slot_phase(it + x) ^ 1u))) {
+                const uint32_t mine = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t bytes = (uint32_t)__popc(mine & ((1u << boxes) - 1u)) * box_rows * 128u;   // a chunk's
+                if (part && lane == 0) mbar_arrive_expect_tx(bar(TAIL), bytes * NC);
+                for (int g = 0; g < NG; ++g) {
+                    if (!__all_sync(0xffffffffu, wait(empty_bar(it + g), slot_phase(it + g) ^ 1u))) {
                         ok = false;
                         return;
                     }
-                const uint32_t mine = __ballot_sync(0xffffffffu, page >= 0);
-                const uint32_t bytes = (uint32_t)__popc(mine & ((1u << boxes) - 1u)) * box_rows * 128u;
-                if (lane == 0) {
-                    if (part)
-                        mbar_arrive_expect_tx(bar(TAIL), bytes * NC);
-                    else
-                        for (int x = 0; x < NC; ++x) mbar_arrive_expect_tx(full_bar(it + x), bytes);
+                    if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it + g), bytes * CG);
+                    __syncwarp();
+                    if (page >= 0 && c / CG == g)
+                        tma_load_cache(slot_addr(it + g) + (uint32_t)((c % CG) * kChunk + box * box_rows * 128),
+                                       is_v ? &tmap_v : &tmap_k, (k0 + box * box_rows) % a.c.page_size, c, t.hk, page,
+                                       part ? bar(TAIL) : full_bar(it + g));
                 }
-                __syncwarp();
-                if (page >= 0)
-                    tma_load_cache(slot_addr(it + c) + (uint32_t)(box * box_rows * 128), is_v ? &tmap_v : &tmap_k,
-                                   (k0 + box * box_rows) % a.c.page_size, c, t.hk, page,
-                                   part ? bar(TAIL) : full_bar(it + c));
                 if (part) {
                     if (!__all_sync(0xffffffffu, wait(bar(TAIL), tails & 1u))) {
                         ok = false;
@@ -191,24 +226,23 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     for (int i = lane; i < kKeys * NC * 8; i += 32) {
                         const int x = i / (kKeys * 8), r = i / 8 % kKeys, k = k0 + r;
                         if (k >= t.q.len || (k / box_rows + 1) * box_rows <= t.j0)
-                            *reinterpret_cast<uint4*>(smem + C::kSmemRing + ((it + x) % kSlots) * kChunk + r * 128 +
+                            *reinterpret_cast<uint4*>(smem + C::kSmemRing +
+                                                      (((it + x / CG) % kSlots) * CG + x % CG) * kChunk + r * 128 +
                                                       (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        for (int x = 0; x < NC; ++x) mbar_arrive(full_bar(it + x));
+                        for (int g = 0; g < NG; ++g) mbar_arrive(full_bar(it + g));
                 }
-                it += NC;
+                it += NG;
             };
-            // in the order of their use: K0, then V(j), K(j + 1) (D = 256: K(j + 1), V(j))
+            // in the order of their use: K(0), V(0), K(1), ...
             int page = nt > 0 ? page_of(0) : -1;
-            if (nt > 0) load(0, page, false);
             for (int j = 0; j < nt && ok; ++j) {
                 const int next = j + 1 < nt ? page_of(j + 1) : -1;
-                if (!kWide) load(j, page, true);
-                if (ok && j + 1 < nt) load(j + 1, next, false);
-                if (kWide && ok) load(j, page, true);
+                load(j, page, false);
+                if (ok) load(j, page, true);
                 page = next;
             }
             w = we;
@@ -217,122 +251,110 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         if (!ok && lane == 0) {
             fail();
             // copies in flight land before the CTA goes away
-            for (uint32_t i = it < (uint32_t)kSlots ? 0 : it - kSlots; i < it + NC; ++i)
+            for (uint32_t i = it < (uint32_t)kSlots ? 0 : it - kSlots; i < it + NG; ++i)
                 (void)mbar_wait_drain(full_bar(i), slot_phase(i), 20000000ull);
             for (int s = 0; s < NS; ++s)
                 if (used[s]) (void)mbar_wait_drain(bar(Q_FULL + s), (used[s] - 1u) & 1u, 20000000ull);
             (void)mbar_wait_drain(bar(TAIL), tails & 1u, 20000000ull);
         }
         __syncwarp();
-    } else if (warp == C::kSoftWarps + 1) {
+      } else if (warp <= C::kSoftWarps + 2) {
         // ------------------------------ MMA ------------------------------
         if (lane == 0) {
             constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, D) | kIdescBMnMajor;
-            uint32_t it = 0, used[2] = {0, 0}, pc[2] = {0, 0}, jobs = 0;
+            const int me = warp - C::kSoftWarps - 1;
+            uint32_t it = 0, used = 0, jobs = 0;
             bool ok = true, issued = false;
             auto need = [&](uint32_t b, uint32_t parity) {
                 if (ok && !wait(b, parity)) ok = false;
                 return ok;
             };
-            auto qk = [&](int s, uint32_t buf, uint32_t slot) {   // S(buf) = Q(s) K^T, K's chunks from `slot`
+            auto qk = [&](int s, uint32_t buf, int c, uint32_t addr) {   // S(buf) (+)= chunk c of Q(s) K^T
+                const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)((s * NC + c) * kChunk));
+                const uint64_t kd = smem_desc_k_sw128(addr);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)((s * NC + c) * kChunk));
-                    const uint64_t kd = smem_desc_k_sw128(slot_addr(slot + c));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_ss(tmem + C::kS + 128u * buf, qd + 2 * kk, kd + 2 * kk, kIdescQK, (c | kk) ? 1u : 0u);
-                }
-                mma_commit(bar(S_FULL + (int)buf));
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16_ss(tmem + C::kS + 128u * buf, qd + 2 * kk, kd + 2 * kk, kIdescQK, (c | kk) ? 1u : 0u);
                 issued = true;
             };
-            auto pv = [&](int s, uint32_t buf, uint32_t slot, bool acc) {   // O(s) += P(buf) V
-                const uint64_t vd = smem_desc_mn_sw128(slot_addr(slot), kChunk);
+            auto pv = [&](int s, uint32_t buf, uint32_t addr, bool acc) {   // O(s) (+)= P(buf) V
+                const uint64_t vd = smem_desc_mn_sw128(addr, kChunk);
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)
                     mma_f16_ts(tmem + C::kO + (uint32_t)(D * s), tmem + C::kS + 128u * buf + 8u * kk,
                                vd + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (acc || kk) ? 1u : 0u);
-            };
-            auto arrived = [&](uint32_t slot) {   // the tile's chunks are in shared memory
-                for (int c = 0; c < NC; ++c)
-                    if (!need(full_bar(slot + c), slot_phase(slot + c))) return false;
-                return true;
-            };
-            auto release = [&](uint32_t slot) {
-                for (int c = 0; c < NC; ++c) mma_commit(empty_bar(slot + c));
+                issued = true;
             };
             for (long long w = w0; w < w1 && ok;) {
                 const long long we = min(w1, t.at + t.units);
                 const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
-                const int ns = t.rows > tile_rows ? NS : 1;
-                if (nt > 0) {
-                    if (!kWide) {
-                        const uint32_t k0 = it;
-                        it += NC;
-                        for (int s = 0; s < ns && ok; ++s) {
-                            if (need(bar(Q_FULL + s), used[s] & 1u) && (s > 0 || arrived(k0))) {
-                                tc_fence_after();
-                                qk(s, s, k0);
-                            }
-                        }
-                        if (ok) release(k0);
-                        for (int j = 0; j < nt && ok; ++j) {
-                            const uint32_t v = it, k = it + NC;
-                            const bool more = j + 1 < nt;
-                            it += more ? 2 * NC : NC;
-                            for (int s = 0; s < ns && ok; ++s) {
-                                if (s == 0 && !arrived(v)) break;
-                                if (!need(bar(P_FULL + s), pc[s]++ & 1u)) break;
-                                // the previous item's output has been read
-                                if (j == 0 && !need(bar(O_EMPTY + s), (used[s] & 1u) ^ 1u)) break;
-                                tc_fence_after();
-                                pv(s, s, v, j > 0);
-                                if (s == ns - 1) release(v);
-                                if (more) {
-                                    if (s == 0 && !arrived(k)) break;
-                                    tc_fence_after();
-                                    qk(s, s, k);
-                                    if (s == ns - 1) release(k);
-                                } else {
-                                    mma_commit(bar(O_FULL + s));
-                                    mma_commit(bar(Q_EMPTY + s));
-                                    ++used[s];
-                                }
-                            }
-                        }
-                    } else {
-                        uint32_t k = it;
-                        it += NC;
-                        if (need(bar(Q_FULL), used[0] & 1u) && arrived(k)) {
+                if constexpr (NS == 2) {
+                    // PV(j), QK(j + 1) of row tile `me`; a tile that the item does not have only releases slots
+                    const bool active = t.rows > me * tile_rows;
+                    if (active && nt > 0) need(bar(Q_FULL + me), used & 1u);
+                    for (int j = 0; j < nt && ok; ++j) {
+                        if (!need(full_bar(it), slot_phase(it))) break;
+                        if (active) {
                             tc_fence_after();
-                            qk(0, jobs & 1u, k);
-                            release(k);
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) qk(me, me, c, slot_addr(it) + (uint32_t)(c * kChunk));
+                            mma_commit(bar(S_FULL + me));
+                            mma_commit(empty_bar(it));
+                        } else {
+                            mbar_arrive(empty_bar(it));
                         }
-                        for (int j = 0; j < nt && ok; ++j) {
-                            if (j + 1 < nt) {
-                                k = it;
-                                it += NC;
-                                if (!arrived(k)) break;
-                                tc_fence_after();
-                                qk(0, (jobs + 1) & 1u, k);   // its P, two tiles back, has been used
-                                release(k);
-                            }
-                            const uint32_t v = it;
-                            it += NC;
-                            if (!arrived(v)) break;
-                            if (!need(bar(P_FULL + (int)(jobs & 1u)), (jobs >> 1) & 1u)) break;
-                            if (j == 0 && !need(bar(O_EMPTY), (used[0] & 1u) ^ 1u)) break;
+                        ++it;
+                        if (!need(full_bar(it), slot_phase(it))) break;
+                        if (active) {
+                            if (!need(bar(P_FULL + me), jobs++ & 1u)) break;
+                            // the previous item's output has been read
+                            if (j == 0 && !need(bar(O_EMPTY + me), (used & 1u) ^ 1u)) break;
                             tc_fence_after();
-                            pv(0, jobs & 1u, v, j > 0);
-                            release(v);
-                            mma_commit(bar(O_FULL));
-                            ++jobs;
+                            pv(me, me, slot_addr(it), j > 0);
+                            mma_commit(empty_bar(it));
+                        } else {
+                            mbar_arrive(empty_bar(it));
                         }
-                        if (ok) {
-                            mma_commit(bar(Q_EMPTY));
-                            ++used[0];
-                        }
+                        ++it;
                     }
+                    if (active && nt > 0 && ok) {
+                        mma_commit(bar(O_FULL + me));
+                        mma_commit(bar(Q_EMPTY + me));
+                        ++used;
+                    }
+                } else if (me == 0) {
+                    if (nt > 0) need(bar(Q_FULL), used & 1u);
+                    for (int j = 0; j < nt && ok; ++j, ++jobs) {
+                        // the P that was over this S, two tiles back, has been used
+                        if (!need(bar(S_EMPTY + (int)(jobs & 1u)), ((jobs >> 1) & 1u) ^ 1u)) break;
+                        for (int c = 0; c < NC; ++c) {
+                            if (!need(full_bar(it + c), slot_phase(it + c))) break;
+                            tc_fence_after();
+                            qk(0, jobs & 1u, c, slot_addr(it + c));
+                            mma_commit(empty_bar(it + c));
+                        }
+                        mma_commit(bar(S_FULL + (int)(jobs & 1u)));
+                        it += 2 * NC;
+                    }
+                    if (nt > 0 && ok) {
+                        mma_commit(bar(Q_EMPTY));
+                        ++used;
+                    }
+                } else {
+                    for (int j = 0; j < nt && ok; ++j, ++jobs) {
+                        it += NC;
+                        for (int c = 0; c < NC; ++c) need(full_bar(it + c), slot_phase(it + c));
+                        need(bar(P_FULL + (int)(jobs & 1u)), (jobs >> 1) & 1u);
+                        if (j == 0) need(bar(O_EMPTY), (used & 1u) ^ 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(0, jobs & 1u, slot_addr(it), j > 0);
+                        mma_commit(bar(O_FULL));
+                        mma_commit(bar(S_EMPTY + (int)(jobs & 1u)));
+                        for (int c = 0; c < NC; ++c) mma_commit(empty_bar(it + c));
+                        it += NC;
+                    }
+                    if (nt > 0) ++used;
                 }
                 w = we;
                 if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
@@ -340,14 +362,16 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             if (!ok) {
                 fail();
                 if (issued) {
-                    mma_commit(bar(DRAIN));
-                    (void)mbar_wait_drain(bar(DRAIN), 0u, 100000000ull);
+                    mma_commit(bar(DRAIN + me));
+                    (void)mbar_wait_drain(bar(DRAIN + me), 0u, 100000000ull);
                 }
             }
         }
         __syncwarp();
+      }
     } else {
         // ------------------------------ softmax, output ------------------------------
+        if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t to = tmem + lanes + C::kO + (uint32_t)(D * s);
@@ -392,9 +416,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     for (int i = 0; i < 4; ++i) {
                         mx[i] = __uint_as_float(x[i][0]);
 #pragma unroll
-                        for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(x[i][e]));
+                        for (int e = 1; e < 31; e += 2)
+                            mx[i] = max3(mx[i], __uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1]));
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float top = max3(fmaxf(mx[0], __uint_as_float(x[0][31])), fmaxf(mx[1], __uint_as_float(x[1][31])),
+                                           max3(mx[2], __uint_as_float(x[2][31]), fmaxf(mx[3], __uint_as_float(x[3][31]))));
                     if (__any_sync(0xffffffffu, (top - m) * scale > 8.0f)) {
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.0f : exp2_fast((m - mn) * scale);
@@ -410,32 +436,36 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                                 tc_fence_after();
                             }
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld_x32(to + c, o);
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld_x16(to + c, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st_x32(to + c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st_x16(to + c, o);
                             }
                         }
                     }
                     const float mb = m == -INFINITY ? 0.0f : m * scale;
-                    float sum[4] = {};
+                    const uint64_t sc2 = pack2(scale, scale), mb2 = pack2(-mb, -mb);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[32];
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float u = exp2_fast(fmaf(__uint_as_float(x[2 * h + (e >> 4)][2 * (e & 15)]), scale, -mb));
-                            const float v = exp2_fast(fmaf(__uint_as_float(x[2 * h + (e >> 4)][2 * (e & 15) + 1]), scale, -mb));
-                            sum[2 * (e & 1)] += u;
-                            sum[2 * (e & 1) + 1] += v;
+                        for (int e = 0; e < 16; ++e) {
+                            float u, v;
+                            unpack2(fma2(pack2(__uint_as_float(x[i][2 * e]), __uint_as_float(x[i][2 * e + 1])), sc2, mb2), u, v);
+                            u = exp2_fast(u);
+                            v = exp2_fast(v);
+                            sum[e & 1] = add2(sum[e & 1], pack2(u, v));
                             pk[e] = pack_bf16(u, v);
                         }
-                        tmem_st_x32(ts + 32u * h, pk);
+                        tmem_st_x16(ts + 16u * i, pk);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float su, sv;
+                    unpack2(add2(sum[0], sum[1]), su, sv);
+                    l += su + sv;
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
