@@ -12,59 +12,8 @@
 namespace tern {
 namespace {
 
-__device__ int g_attn_error;
-
-struct MassArgs {
-    const __nv_bfloat16* q;
-    long long q_stride;
-    const __nv_bfloat16* k_cache;
-    CacheView c;
-    SeqView s;
-    int q_heads;
-    float scale;
-    int window;
-    const float* lse;
-    float decay;
-    const float* mass;
-    float* out;
-};
-
-// One warp a (sequence, key head, key): it runs over the queries that see it.
-template <int D>
-__global__ void __launch_bounds__(256) mass_kernel(const MassArgs a) {
-    constexpr int E = D / 32;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int b = blockIdx.z, hk = blockIdx.y, lane = threadIdx.x & 31, group = a.q_heads / a.c.kv_heads;
-    const Seq q = load_seq(a.s, a.c.page_size, b, &g_attn_error);
-    for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < q.len; j += gridDim.x * 8) {
-        const int page = checked_page(a.s.table[(long long)b * a.s.width + j / a.c.page_size], a.c.pages, &g_attn_error);
-        const int slot = j % a.c.page_size;
-        const long long at = page * a.c.page_stride + hk * a.c.head_stride + slot * a.c.slot_stride + lane * E;
-        float k[E], sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) k[e] = __bfloat162float(a.k_cache[at + e]);
-        // key j is seen by positions j .. j + window - 1
-        const int i0 = max(j - (q.len - q.n), 0);
-        const int i1 = a.window > 0 ? (int)min((long long)q.n, (long long)j - (q.len - q.n) + a.window) : q.n;
-        for (int i = i0; i < i1; ++i)
-            for (int g = 0; g < group; ++g) {
-                const int h = hk * group + g;
-                const __nv_bfloat16* qp = a.q + (long long)(q.q0 + i) * a.q_stride + (long long)h * D + lane * E;
-                float s = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) s = fmaf(__bfloat162float(qp[e]), k[e], s);
-#pragma unroll
-                for (int r = 16; r; r >>= 1) s += __shfl_xor_sync(0xffffffffu, s, r);
-                const float lse = a.lse[(long long)(q.q0 + i) * a.q_heads + h];
-                if (lse > -INFINITY) sum += expf(s * a.scale - lse);
-            }
-        if (lane == 0) {
-            const long long m = ((long long)page * a.c.kv_heads + hk) * a.c.page_size + slot;
-            a.out[m] = a.decay * a.mass[m] + sum;
-        }
-    }
-}
+// The rows kernel of the mass holds this many query rows of a sequence and head.
+constexpr int kMassRows = 64;
 
 tern_status check_heads(const CacheView& c, int q_heads, long long q_stride) {
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return TERN_ERR_SHAPE;
@@ -74,13 +23,6 @@ tern_status check_heads(const CacheView& c, int q_heads, long long q_stride) {
 }
 
 }  // namespace
-
-cudaError_t read_attn_device_error(int* code) {
-    int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_error, sizeof(int));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(int));
-}
 
 }  // namespace tern
 
@@ -161,19 +103,20 @@ extern "C" tern_status tern_attention_mass(const void* q, long long q_stride, co
     if (st != TERN_OK) return st;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.q_stride = q_stride;
-    a.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
+    if (sms > kMaxSms) sms = kMaxSms;
     a.q_heads = q_heads;
-    a.scale = scale;
+    a.group = q_heads / a.c.kv_heads;
+    a.tiles = 0;
+    a.scale_log2 = scale * 1.44269504088896341f;
     a.window = window;
     a.lse = lse;
     a.decay = decay;
     a.mass = mass;
     a.out = mass_out;
-    const long long keys = (long long)table_width * a.c.page_size;
-    const int grid = (int)((keys + 7) / 8 < 4096 ? (keys + 7) / 8 : 4096);
-    auto kernel = a.c.head_dim == 64 ? mass_kernel<64> : a.c.head_dim == 128 ? mass_kernel<128> : mass_kernel<256>;
-    if (launch_pdl(kernel, dim3(grid, a.c.kv_heads, B), dim3(256), 0, (cudaStream_t)stream, true, a) != cudaSuccess)
-        return TERN_ERR_CUDA;
+    const bool few = (long long)a.s.max_new * a.group <= kMassRows;
+    const cudaError_t e = few ? launch_mass_rows(a, k_cache, sms, (cudaStream_t)stream)
+                              : launch_mass_tiles(a, k_cache, sms, (cudaStream_t)stream);
+    if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;
 }

@@ -47,17 +47,22 @@ struct Item {
     int rows, j0, j1, units;   // its rows and the keys they see together
     long long at;              // its first unit
 };
+// The extent of an item by its (b, rt, q): a row tile of R rows over the keys
+// it sees.  units = 0: the sequence has no such item.
 template <int UNIT>
-__device__ __forceinline__ void item_extent(const AttnArgs& a, int R, Item& t) {
-    const int r0 = t.rt * R, all = t.q.n * a.group;
-    t.rows = min(R, all - r0);
-    if (t.rows <= 0) {
-        t.rows = t.units = 0;
-        return;
+struct RowTileExtent {
+    int R, group, window;
+    __device__ __forceinline__ void operator()(Item& t) const {
+        const int r0 = t.rt * R, all = t.q.n * group;
+        t.rows = min(R, all - r0);
+        if (t.rows <= 0) {
+            t.rows = t.units = 0;
+            return;
+        }
+        keys_of_rows(t.q, group, window, r0, r0 + t.rows, t.j0, t.j1);
+        t.units = t.j1 > t.j0 ? (t.j1 - 1) / UNIT - t.j0 / UNIT + 1 : 1;
     }
-    keys_of_rows(t.q, a.group, a.window, r0, r0 + t.rows, t.j0, t.j1);
-    t.units = t.j1 > t.j0 ? (t.j1 - 1) / UNIT - t.j0 / UNIT + 1 : 1;
-}
+};
 __host__ __device__ inline long long unit_begin(long long total, int P, int c) { return total * c / P; }
 __device__ inline int unit_owner(long long total, int P, long long u) {
     int c = (int)((u * P) / total);
@@ -68,36 +73,37 @@ __device__ inline int unit_owner(long long total, int P, long long u) {
 
 // The next item, past row tiles that a sequence does not have; `tiles` row
 // tiles are counted for every sequence.
-template <int UNIT>
-__device__ __forceinline__ void next_item(const AttnArgs& a, int R, int tiles, Item& t, int* err) {
+template <typename Extent>
+__device__ __forceinline__ void next_item(const SeqView& sv, const CacheView& cv, const Extent& extent, int tiles,
+                                          Item& t, int* err) {
     t.at += t.units;
-    if (++t.hk < a.c.kv_heads) return;
+    if (++t.hk < cv.kv_heads) return;
     t.hk = 0;
     do {
         if (++t.rt >= tiles) {
             t.rt = 0;
-            if (++t.b >= a.s.B) return;
-            t.q = load_seq(a.s, a.c.page_size, t.b, err);
+            if (++t.b >= sv.B) return;
+            t.q = load_seq(sv, cv.page_size, t.b, err);
         }
-        item_extent<UNIT>(a, R, t);
+        extent(t);
     } while (t.units == 0);
 }
 
 // This CTA's share [w0, w1) of all units, and the item that holds w0; P shares
 // of at least min_units each.  Called by all THREADS threads; false: no share.
 // `sm`: 8 + THREADS / 32 words of shared memory.
-template <int UNIT, int THREADS>
-__device__ bool find_share(const AttnArgs& a, int R, int tiles, int min_units, long long* sm, int* err,
-                           long long& total, int& P, long long& w0, long long& w1, Item& t) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = a.c.kv_heads;
-    const long long all = (long long)a.s.B * tiles;
+template <int THREADS, typename Extent>
+__device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent& extent, int tiles, int min_units,
+                           long long* sm, int* err, long long& total, int& P, long long& w0, long long& w1, Item& t) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = cv.kv_heads;
+    const long long all = (long long)sv.B * tiles;
     const long long per = (all + THREADS - 1) / THREADS;
     const long long f0 = min((long long)threadIdx.x * per, all), f1 = min(f0 + per, all);
     auto units_of = [&](long long f) {
         t.b = (int)(f / tiles);
         t.rt = (int)(f - (long long)t.b * tiles);
-        t.q = load_seq(a.s, a.c.page_size, t.b, err);
-        item_extent<UNIT>(a, R, t);
+        t.q = load_seq(sv, cv.page_size, t.b, err);
+        extent(t);
         return (long long)t.units * Hk;
     };
     long long mine = 0;
@@ -183,7 +189,81 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two fp32 values in a register pair
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The heads of one token group as the TMA sees them: q as
+// [d / 64][token][head][64 values], a box of one chunk of `tokens` tokens.
+inline bool make_q_map(CUtensorMap* m, const __nv_bfloat16* q, long long q_stride, int q_heads, int T, int D, int group,
+                       int tokens) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t dim[4] = {64, (cuuint64_t)q_heads, (cuuint64_t)T, (cuuint64_t)(D / 64)};
+    const cuuint64_t stride[3] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)tokens, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(q), dim, stride, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+__device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* m, int head, int token, int chunk,
+                                           uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(head), "r"(token), "r"(chunk), "r"(bar)
+        : "memory");
+}
+
 // Launchers of the kernels (each checks nothing: the entry point has).
+struct MassArgs {
+    const __nv_bfloat16* q;
+    long long q_stride;
+    CacheView c;
+    SeqView s;
+    int q_heads, group;
+    int tiles;               // the tiles kernel: key tile pairs of the longest sequence
+    float scale_log2;
+    int window;
+    const float* lse;
+    float decay;
+    const float* mass;
+    float* out;
+};
+
+cudaError_t launch_mass_rows(const MassArgs& a, const void* k, int sms, cudaStream_t stream);
+cudaError_t launch_mass_tiles(const MassArgs& a, const void* k, int sms, cudaStream_t stream);
 cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 size_t attn_rows_workspace();

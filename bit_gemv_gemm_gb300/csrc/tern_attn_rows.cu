@@ -44,21 +44,10 @@ struct Cfg {
     static_assert(kRing >= R * D * 4, "a warp's rows are merged through its ring");
 };
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::kCtas)
 attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -96,7 +85,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     int P;
     long long total, w0, w1;
     Item t;
-    if (!find_share<kStrip, kThreads>(a, R, a.tiles, kMinUnits, sm_scan, &g_attn_rows_error, total, P, w0, w1, t)) return;
+    const RowTileExtent<kStrip> extent{R, a.group, a.window};
+    if (!find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinUnits, sm_scan, &g_attn_rows_error, total, P, w0, w1, t))
+        return;
 
     uint32_t it = 0;   // strips this warp has fetched and used, over all segments
     for (long long w = w0; w < w1;) {
@@ -367,7 +358,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         __syncthreads();
 
         w = we;
-        if (w < w1) next_item<kStrip>(a, R, a.tiles, t, &g_attn_rows_error);
+        if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_rows_error);
     }
 }
 

@@ -68,31 +68,6 @@ struct Cfg {
 };
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys);
 
-// two fp32 values in a register pair
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // floats are exchanged four columns at a time, [column / 4][row][4]
 __device__ __forceinline__ size_t part_at(int D, int s, int row, int c4) {
     return (size_t)s * kRows * (D + 2) + ((size_t)c4 * kRows + row) * 4;
@@ -152,8 +127,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     int P;
     long long total, w0, w1;
     Item t;
-    const bool busy = find_share<kKeys, C::kThreads>(a, R, a.tiles, kMinTiles, sm_scan, &g_attn_tiles_error, total, P,
-                                                     w0, w1, t);
+    const RowTileExtent<kKeys> extent{R, a.group, a.window};
+    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, sm_scan, &g_attn_tiles_error, total,
+                                              P, w0, w1, t);
     auto fail = [&] {
         if (!*abort_flag) {
             *abort_flag = 1;
@@ -183,12 +159,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     mbar_arrive_expect_tx(bar(Q_FULL + s), (uint32_t)(NC * tile_rows * 128));
                     const int tok = t.q.q0 + (t.rt * R + s * tile_rows) / a.group;
                     for (int c = 0; c < NC; ++c)
-                        asm volatile(
-                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-                            "{%2, %3, %4, %5}], [%6];" ::"r"(sbase + (uint32_t)((s * NC + c) * kChunk)),
-                            "l"(reinterpret_cast<uint64_t>(&tmap_q)), "r"(0), "r"(t.hk * a.group), "r"(tok), "r"(c),
-                            "r"(bar(Q_FULL + s))
-                            : "memory");
+                        tma_load_q(sbase + (uint32_t)((s * NC + c) * kChunk), &tmap_q, t.hk * a.group, tok, c,
+                                   bar(Q_FULL + s));
                 }
             }
             const int* trow = a.s.table + (long long)t.b * a.s.width;
@@ -246,7 +218,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 page = next;
             }
             w = we;
-            if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
+            if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_tiles_error);
         }
         if (!ok && lane == 0) {
             fail();
@@ -357,7 +329,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (nt > 0) ++used;
                 }
                 w = we;
-                if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
+                if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_tiles_error);
             }
             if (!ok) {
                 fail();
@@ -580,7 +552,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 }
             }
             w = we;
-            if (w < w1) next_item<kKeys>(a, R, a.tiles, t, &g_attn_tiles_error);
+            if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_tiles_error);
         }
         if (!ok && lane == 0) fail();
         __syncwarp();
@@ -594,26 +566,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     }
 }
 
-// q as [token][head][d / 64][64 values], a box of one chunk of a row tile.
-bool make_q_map(CUtensorMap* m, const AttnArgs& a, int D) {
-    auto enc = get_encode();
-    if (!enc) return false;
-    const cuuint64_t dim[4] = {64, (cuuint64_t)a.q_heads, (cuuint64_t)a.s.T, (cuuint64_t)(D / 64)};
-    const cuuint64_t stride[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2, 128};
-    const cuuint32_t box[4] = {64, (cuuint32_t)a.group, (cuuint32_t)(kRows / a.group), 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(a.q), dim, stride, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream_t stream) {
     using C = Cfg<D>;
     int box = 128;
     while (a.c.page_size % box) box >>= 1;   // page_size is a multiple of 16
     CUtensorMap mq, mk, mv;
-    if (!make_q_map(&mq, a, D) || !make_cache_map(&mk, k, a.c, box, 1) || !make_cache_map(&mv, v, a.c, box, 1))
+    if (!make_q_map(&mq, a.q, a.q_stride, a.q_heads, a.s.T, D, a.group, kRows / a.group) || !make_cache_map(&mk, k, a.c, box, 1) || !make_cache_map(&mv, v, a.c, box, 1))
         return cudaErrorInvalidValue;
     static bool attr_set[64] = {};
     int dev = 0;

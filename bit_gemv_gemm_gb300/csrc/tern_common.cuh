@@ -36,7 +36,8 @@ cudaError_t read_gemm_device_error(int* code);
 cudaError_t read_gemv_device_error(int* code);
 cudaError_t read_f3_device_error(int* code);
 cudaError_t read_rope_device_error(int* code);
-cudaError_t read_attn_device_error(int* code);
+cudaError_t read_mass_rows_device_error(int* code);
+cudaError_t read_mass_tiles_device_error(int* code);
 cudaError_t read_attn_rows_device_error(int* code);
 cudaError_t read_attn_tiles_device_error(int* code);
 cudaError_t read_evict_device_error(int* code);
