@@ -15,6 +15,13 @@ namespace {
 // The rows kernel of the mass holds this many query rows of a sequence and head.
 constexpr int kMassRows = 64;
 
+// The scale of scores in powers of two.  One too small to matter becomes 1e-30,
+// so that masked scores (-inf) stay -inf under it.
+float to_log2(float scale) {
+    const float s = scale * 1.44269504088896341f;
+    return fabsf(s) < 1e-30f ? copysignf(1e-30f, s) : s;
+}
+
 tern_status check_heads(const CacheView& c, int q_heads, long long q_stride) {
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return TERN_ERR_SHAPE;
     if (q_heads < 1 || q_heads % c.kv_heads != 0 || q_heads / c.kv_heads > 64) return TERN_ERR_SHAPE;
@@ -64,8 +71,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.q_stride = q_stride;
     a.q_heads = q_heads;
     a.group = q_heads / a.c.kv_heads;
-    // (0 becomes a number that scores cannot notice: -inf times it is still -inf)
-    a.scale_log2 = scale == 0.0f ? 1e-30f : scale * 1.44269504088896341f;
+    a.scale_log2 = to_log2(scale);
     a.window = window;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
@@ -107,7 +113,7 @@ extern "C" tern_status tern_attention_mass(const void* q, long long q_stride, co
     a.q_heads = q_heads;
     a.group = q_heads / a.c.kv_heads;
     a.tiles = 0;
-    a.scale_log2 = scale * 1.44269504088896341f;
+    a.scale_log2 = to_log2(scale);
     a.window = window;
     a.lse = lse;
     a.decay = decay;

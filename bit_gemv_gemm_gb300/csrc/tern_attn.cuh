@@ -63,9 +63,13 @@ struct RowTileExtent {
         t.units = t.j1 > t.j0 ? (t.j1 - 1) / UNIT - t.j0 / UNIT + 1 : 1;
     }
 };
-__host__ __device__ inline long long unit_begin(long long total, int P, int c) { return total * c / P; }
+__host__ __device__ inline long long unit_begin(long long total, int P, int c) {
+    const long long x = total * c;
+    return x <= 0x7fffffff ? (long long)((unsigned)x / (unsigned)P) : x / P;
+}
 __device__ inline int unit_owner(long long total, int P, long long u) {
-    int c = (int)((u * P) / total);
+    const long long x = u * P;
+    int c = x <= 0x7fffffff ? (int)((unsigned)x / (unsigned)total) : (int)(x / total);
     while (c + 1 < P && unit_begin(total, P, c + 1) <= u) ++c;
     while (c > 0 && unit_begin(total, P, c) > u) --c;
     return c;
@@ -92,15 +96,20 @@ __device__ __forceinline__ void next_item(const SeqView& sv, const CacheView& cv
 // This CTA's share [w0, w1) of all units, and the item that holds w0; P shares
 // of at least min_units each.  Called by all THREADS threads; false: no share.
 // `sm`: 8 + THREADS / 32 words of shared memory.
+//
+// A call begins with this, so its latency counts (one token over 500 keys: a
+// third of the kernel): the thread that finds the item hands it on through
+// shared memory instead of every thread reading the lengths again, and the
+// divisions are 32-bit ones where the numbers allow (a 64-bit one is a loop).
 template <int THREADS, typename Extent>
 __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent& extent, int tiles, int min_units,
                            long long* sm, int* err, long long& total, int& P, long long& w0, long long& w1, Item& t) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = cv.kv_heads;
     const long long all = (long long)sv.B * tiles;
-    const long long per = (all + THREADS - 1) / THREADS;
+    const long long per = all <= THREADS ? 1 : (all + THREADS - 1) / THREADS;
     const long long f0 = min((long long)threadIdx.x * per, all), f1 = min(f0 + per, all);
     auto units_of = [&](long long f) {
-        t.b = (int)(f / tiles);
+        t.b = f <= 0x7fffffff ? (int)((unsigned)f / (unsigned)tiles) : (int)(f / tiles);
         t.rt = (int)(f - (long long)t.b * tiles);
         t.q = load_seq(sv, cv.page_size, t.b, err);
         extent(t);
@@ -118,30 +127,44 @@ __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent&
     __syncthreads();
     long long before = x - mine;
     total = 0;
+#pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += sm[8 + w];
-        total += sm[8 + w];
+        const long long v = sm[8 + w];
+        if (w < warp) before += v;
+        total += v;
     }
-    P = (int)min((long long)gridDim.x, (total + min_units - 1) / min_units);
+    const long long most = total <= 0x7fffffff ? ((unsigned)total + min_units - 1) / (unsigned)min_units
+                                               : (total + min_units - 1) / min_units;
+    P = (int)min((long long)gridDim.x, most);
     if ((int)blockIdx.x >= P) return false;
     w0 = unit_begin(total, P, blockIdx.x);
     w1 = unit_begin(total, P, blockIdx.x + 1);
     if (w0 >= before && w0 < before + mine) {
         long long at = before;
         for (long long f = f0; f < f1; ++f) {
-            const long long u = units_of(f);
-            if (w0 < at + u) {
-                sm[0] = f;
-                sm[1] = at;
-                break;
-            }
+            const long long u = per == 1 ? mine : units_of(f);
+            if (w0 < at + u) break;
             at += u;
         }
+        t.hk = (int)((unsigned)(w0 - at) / (unsigned)t.units);   // below kv_heads * units
+        t.at = at + (long long)t.hk * t.units;
+        int* o = reinterpret_cast<int*>(sm);
+        o[0] = t.b;
+        o[1] = t.rt;
+        o[2] = t.hk;
+        o[3] = t.q.q0;
+        o[4] = t.q.n;
+        o[5] = t.q.len;
+        sm[3] = t.at;
     }
     __syncthreads();
-    (void)units_of(sm[0]);
-    t.hk = (int)((w0 - sm[1]) / t.units);
-    t.at = sm[1] + (long long)t.hk * t.units;
+    const int* o = reinterpret_cast<const int*>(sm);
+    t.b = o[0];
+    t.rt = o[1];
+    t.hk = o[2];
+    t.q = Seq{o[3], o[4], o[5]};
+    t.at = sm[3];
+    extent(t);
     return true;
 }
 
@@ -213,6 +236,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -255,6 +283,7 @@ struct MassArgs {
     int q_heads, group;
     int tiles;               // the tiles kernel: key tile pairs of the longest sequence
     float scale_log2;
+    float lse_scale, nothing;   // the tiles kernel: -log2(e) / scale_log2; what a row that weighs nothing gets
     int window;
     const float* lse;
     float decay;

@@ -5,17 +5,26 @@
 // The scores are computed transposed, S^T = K Q^T: a key is a row of the
 // product, so a thread owns a key and its sum over the query rows is a sum of
 // its own registers (no exchange, no atomics, a fixed order).  With the lse known
-// a weight is exp2(S - lse) at once.
+// a weight is exp2(S - lse) at once, and the lse, a constant of a column, is
+// subtracted by the product itself: one more K = 16 step multiplies three ones
+// on K's side with -lse / scale on Q's, as the sum of three bf16 values (24
+// bits).  Reading it from shared memory instead, broadcast to every thread, cost
+// four wavefronts a 16-byte load beside products that already take the whole
+// bandwidth of shared memory (99 us for 512 tokens over 16k keys, 32 heads).
 // An item is NS key tiles of 128 keys (two; one at D = 256) of one sequence and
 // key head.  K's tiles are brought once and stay; the query rows that see them
 // stream past in tiles of 128 packed rows (128 / group tokens, every head of
 // the group), each used by both key tiles:
 //   * a TMA warp fills K (double-buffered where it fits) and the ring of Q tiles;
-//   * one thread a key tile issues S^T = K Q^T into two tensor-memory buffers
-//     of its own;
-//   * a warpgroup a key tile reads S^T (32 columns at a time), subtracts the
-//     columns' lse (in shared memory, copied by the warpgroup one tile ahead),
-//     exponentiates and adds.
+//     another writes the lse step beside each;
+//   * two threads issue S^T = K Q^T, for all key tiles, one for the even row tiles
+//     and one for the odd, each into its own tensor-memory buffers: issuing is
+//     nearly synchronous, and one thread's products cover the other's waits and
+//     commits (a thread a key tile, with twice the commits: 1800 clocks a pair of
+//     tiles against the products' 1152);
+//   * a warpgroup a key tile reads S^T whole, frees the buffer, exponentiates and
+//     adds.  (Two warpgroups a tile, one for each parity, have too few registers
+//     to read a tile whole and hold their buffer: 105 us for 512 tokens over 16k.)
 // Items are whole and dealt out in equal contiguous shares of their row tiles.
 #include <algorithm>
 
@@ -39,12 +48,13 @@ struct Cfg {
     static constexpr int KB = D == 256 ? 1 : 2;                 // buffers of K's tiles
     static constexpr int kSlots = D == 64 ? 6 : 2;              // Q tiles in flight
     static constexpr int kSoftWarps = 4 * NS;
-    static constexpr int kThreads = 32 * (kSoftWarps + 1 + NS);
+    static constexpr int kThreads = 32 * (kSoftWarps + 4);
     static constexpr size_t kSmemRing = (size_t)KB * NS * kTile;
-    static constexpr size_t kSmemLse = kSmemRing + (size_t)kSlots * kTile;        // [NS][2][128]
-    static constexpr size_t kSmemBar = kSmemLse + (size_t)NS * 2 * kRows * 4;
-    // barriers: q_full[slots], q_empty[slots], k_full[KB], k_empty[KB], s_full[4], s_empty[4], drain[2]
-    static constexpr int kBars = 2 * kSlots + 2 * KB + 10;
+    static constexpr size_t kSmemLse = kSmemRing + (size_t)kSlots * kTile;        // [slot][128 rows][16] bf16
+    static constexpr size_t kSmemOne = kSmemLse + (size_t)kSlots * kRows * 32;    // [128 keys][16]: 1, 1, 1, 0, ...
+    static constexpr size_t kSmemBar = kSmemOne + (size_t)kKeys * 32;
+    // barriers: q_full[slots], q_empty[slots], k_full[KB], k_empty[KB], s_full[2], s_empty[2], drain[2]
+    static constexpr int kBars = 2 * kSlots + 2 * KB + 6;
     static constexpr size_t kSmemMisc = kSmemBar + kBars * 8;
     static constexpr size_t kSmem = kSmemMisc + 256 + 1024;
 };
@@ -74,6 +84,13 @@ struct KeyTileExtent {
     }
 };
 
+// Row r of a K = 16 step: x, y, z and thirteen zeros.
+__device__ __forceinline__ void write_step(unsigned char* base, int r, float x, float y, float z) {
+    const int flip = (r >> 2) & 1;
+    *reinterpret_cast<uint4*>(base + r * 32 + 16 * flip) = make_uint4(pack_bf16(x, y), pack_bf16(z, 0.0f), 0, 0);
+    *reinterpret_cast<uint4*>(base + r * 32 + 16 * (1 - flip)) = make_uint4(0, 0, 0, 0);
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -86,7 +103,7 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     const uint32_t sbase = smem_u32(smem), bar0 = sbase + (uint32_t)C::kSmemBar;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     enum { Q_FULL = 0, Q_EMPTY = kSlots, K_FULL = 2 * kSlots, K_EMPTY = K_FULL + KB, S_FULL = K_EMPTY + KB,
-           S_EMPTY = S_FULL + 4, DRAIN = S_EMPTY + 4 };
+           S_EMPTY = S_FULL + 2, DRAIN = S_EMPTY + 2 };
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm_scan + 8 + C::kThreads / 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -95,8 +112,9 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kBars; ++i) {
             int count = 1;
-            if ((i >= Q_EMPTY && i < Q_EMPTY + kSlots) || (i >= K_EMPTY && i < K_EMPTY + KB)) count = NS;
-            if (i >= S_EMPTY && i < S_EMPTY + 4) count = 4;
+            if (i >= K_EMPTY && i < K_EMPTY + KB) count = 2;
+            if (i >= S_EMPTY && i < S_EMPTY + 2) count = 4 * NS;
+            if (i < kSlots) count = 2;   // the copy, and the lse step
             mbar_init(bar(i), count);
         }
         *abort_flag = 0;
@@ -104,6 +122,9 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         tma_prefetch_desc(&tmap_q);
         tma_prefetch_desc(&tmap_k);
     }
+    for (int r = threadIdx.x; r < kKeys; r += C::kThreads)
+        write_step(smem + C::kSmemOne, r, 1.0f, 1.0f, 1.0f);
+    fence_proxy_async_smem();
     if (warp == C::kSoftWarps) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -178,10 +199,54 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 (void)mbar_wait_drain(bar(K_FULL + (int)(i % KB)), (i / KB) & 1u, 20000000ull);
         }
         __syncwarp();
+    } else if (warp == C::kSoftWarps + 1) {
+        // ------------------------------ the lse steps ------------------------------
+        uint32_t it = 0;
+        bool ok = true;
+        while (t.at < w1 && ok) {
+            int lo, hi;
+            extent.row_tiles(t, lo, hi);
+            // the lse of this lane's four rows of a row tile, fetched a tile ahead
+            const float* lse[4];
+            float z[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int row = lane + 32 * x;
+                lse[x] = a.lse + (long long)(t.q.q0 + row / a.group) * a.q_heads + t.hk * a.group + row % a.group;
+            }
+            auto fetch = [&](int r) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = lane + 32 * x;
+                    z[x] = row < tile_rows && r * tile_rows + row < t.rows ? lse[x][(long long)r * tokens * a.q_heads] : -INFINITY;
+                }
+            };
+            if (hi > lo) fetch(lo);
+            for (int r = lo; r < hi; ++r, ++it) {
+                const uint32_t s = it % kSlots;
+                if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY + (int)s), ((it / kSlots) & 1u) ^ 1u))) { ok = false; break; }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    // a row that weighs nothing gets a finite value that leaves exp2 at 0: 0 * inf would be NaN
+                    const float v = z[x] == -INFINITY ? a.nothing : z[x] * a.lse_scale;
+                    const float top = __bfloat162float(__float2bfloat16_rn(v));
+                    const float mid = __bfloat162float(__float2bfloat16_rn(v - top));
+                    write_step(smem + C::kSmemLse + s * (kRows * 32), lane + 32 * x, top, mid, v - top - mid);
+                }
+                if (r + 1 < hi) fetch(r + 1);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Q_FULL + (int)s));
+            }
+            next_item(a.s, a.c, extent, a.tiles, t, &g_mass_tiles_error);
+            if (t.b >= a.s.B) break;
+        }
+        if (!ok && lane == 0) fail();
+        __syncwarp();
     } else if (warp > C::kSoftWarps) {
-        // ------------------------------ MMA, one thread a key tile ------------------------------
+        // ------------------------------ MMA, one thread a parity of row tiles ------------------------------
         if (lane == 0) {
-            const int me = warp - C::kSoftWarps - 1;
+            const uint32_t me = (uint32_t)(warp - C::kSoftWarps - 2);
             uint32_t it = 0, kt = 0;
             bool ok = true, issued = false;
             while (t.at < w1 && ok) {
@@ -189,38 +254,33 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 extent.row_tiles(t, lo, hi);
                 if (hi > lo) {
                     const uint32_t kb = kt % KB;
-                    // a pair's second tile may hold no key: its products are not needed
-                    const bool active = t.j0 + me * kKeys < t.j1;
                     ok = wait(bar(K_FULL + (int)kb), (kt / KB) & 1u);
                     for (int r = lo; r < hi && ok; ++r, ++it) {
-                        const uint32_t s = it % kSlots, buf = (uint32_t)(2 * me) + (it & 1u);
-                        ok = wait(bar(S_EMPTY + (int)buf), ((it >> 1) & 1u) ^ 1u);
-                        ok = ok && wait(bar(Q_FULL + (int)s), (it / kSlots) & 1u);
+                        if ((it & 1u) != me) continue;
+                        const uint32_t s = it % kSlots;
+                        ok = wait(bar(Q_FULL + (int)s), (it / kSlots) & 1u);
+                        ok = ok && wait(bar(S_EMPTY + (int)me), ((it >> 1) & 1u) ^ 1u);
                         if (!ok) break;
-                        if (active) {
-                            tc_fence_after();
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 0; x < NS; ++x) {   // (a pair's second tile may hold no key: its sums are not stored)
 #pragma unroll
                             for (int c = 0; c < NC; ++c) {
-                                const uint64_t kd = smem_desc_k_sw128(sbase + (uint32_t)(((kb * NS + me) * NC + c) * kChunk));
+                                const uint64_t kd = smem_desc_k_sw128(sbase + (uint32_t)(((kb * NS + x) * NC + c) * kChunk));
                                 const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)(C::kSmemRing + s * C::kTile + c * kChunk));
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    mma_f16_ss(tmem + 128u * buf, kd + 2 * kk, qd + 2 * kk, kIdesc, (c | kk) ? 1u : 0u);
+                                    mma_f16_ss(tmem + 256u * x + 128u * me, kd + 2 * kk, qd + 2 * kk, kIdesc, (c | kk) ? 1u : 0u);
                             }
-                            issued = true;
-                            mma_commit(bar(S_FULL + (int)buf));
-                            mma_commit(bar(Q_EMPTY + (int)s));
-                        } else {
-                            // keep the buffers' phases in step
-                            mbar_arrive(bar(S_FULL + (int)buf));
-                            mbar_arrive(bar(Q_EMPTY + (int)s));
+                            mma_f16_ss(tmem + 256u * x + 128u * me, smem_desc_k_sw32(sbase + (uint32_t)C::kSmemOne),
+                                       smem_desc_k_sw32(sbase + (uint32_t)(C::kSmemLse + s * (kRows * 32))), kIdesc, 1u);
                         }
+                        issued = true;
+                        mma_commit(bar(S_FULL + (int)me));
+                        mma_commit(bar(Q_EMPTY + (int)s));
                     }
                     if (!ok) break;
-                    if (active)
-                        mma_commit(bar(K_EMPTY + (int)kb));
-                    else
-                        mbar_arrive(bar(K_EMPTY + (int)kb));
+                    mma_commit(bar(K_EMPTY + (int)kb));   // (at once where this thread had no product)
                     ++kt;
                 }
                 next_item(a.s, a.c, extent, a.tiles, t, &g_mass_tiles_error);
@@ -229,8 +289,8 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             if (!ok) {
                 fail();
                 if (issued) {
-                    mma_commit(bar(DRAIN + me));
-                    (void)mbar_wait_drain(bar(DRAIN + me), 0u, 100000000ull);
+                    mma_commit(bar(DRAIN + (int)me));
+                    (void)mbar_wait_drain(bar(DRAIN + (int)me), 0u, 100000000ull);
                 }
             }
         }
@@ -238,10 +298,10 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     } else {
         // ------------------------------ weights and sums ------------------------------
         const int me = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        float* sm_lse = reinterpret_cast<float*>(smem + C::kSmemLse) + me * 2 * kRows;
         uint32_t it = 0;
         bool ok = true;
         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+        const uint32_t skip = a.scale_log2 < 0.0f ? 0x7f800000u : 0xff800000u;   // times the scale: -inf
         while (t.at < w1 && ok) {
             int lo, hi;
             extent.row_tiles(t, lo, hi);
@@ -254,63 +314,51 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 at = ((long long)page * a.c.kv_heads + t.hk) * a.c.page_size + key % a.c.page_size;
                 old = __ldg(a.mass + at);
             }
-            // minus the lse of this thread's column of row tile r, in powers of two: -inf where the row weighs nothing
-            auto column = [&](int r) {
-                const int x = r * tile_rows + row;
-                if (row >= tile_rows || x >= t.rows) return -INFINITY;
-                const float z = a.lse[(long long)(t.q.q0 + x / a.group) * a.q_heads + t.hk * a.group + x % a.group];
-                return z == -INFINITY ? -INFINITY : -z * 1.44269504088896341f;
-            };
-            float next = hi > lo ? column(lo) : 0.0f;
             // tokens [first, end) see this key
             const int first = key - (t.q.len - t.q.n);
             const int end = a.window > 0 ? (int)min((long long)t.q.n, (long long)first + a.window) : t.q.n;
             const int k_lo = t.j0 + me * kKeys - (t.q.len - t.q.n);   // of the tile's first key; its last is 127 above
-            uint64_t sum[2] = {0, 0};
+            uint64_t sum[4] = {0, 0, 0, 0};
             for (int r = lo; r < hi; ++r, ++it) {
-                float* z = sm_lse + (it & 1u) * kRows;
-                z[row] = next;
-                next = r + 1 < hi ? column(r + 1) : 0.0f;
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + me) : "memory");
-                const uint32_t buf = (uint32_t)(2 * me) + (it & 1u);
-                if (!__all_sync(0xffffffffu, wait(bar(S_FULL + (int)buf), (it >> 1) & 1u))) { ok = false; break; }
+                const int odd = (int)(it & 1u);
+                if (!__all_sync(0xffffffffu, wait(bar(S_FULL + odd), (it >> 1) & 1u))) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + 128u * buf;
+                const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(256 * me + 128 * odd);
                 const int tok0 = r * tokens;
                 // some column of the tile may not see some key of it (or is no row at all)
                 const bool masked = tok0 < k_lo + kKeys - 1 || tile_rows < kRows || (r + 1) * tile_rows > t.rows ||
                                     (a.window > 0 && tok0 + tokens - 1 >= k_lo + a.window);
                 const int c0 = max(first - tok0, 0) * a.group, c1 = min(max(end - tok0, 0) * a.group, tile_rows);
+                uint32_t x[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld_x32(ts + 32u * i, x[i]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S_EMPTY + odd));
+                if (masked) {   // (the lse step alone covers rows that weigh nothing, not scores that are not finite)
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        if (e < c0 || e >= c1) x[e >> 5][e & 31] = skip;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t x[32];
-                    tmem_ld_x32(ts + 32u * i, x);
-                    tmem_ld_wait();
-                    if (i == 3) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(S_EMPTY + (int)buf));
-                    }
+                    float u[32];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 zz = *reinterpret_cast<const float4*>(z + 32 * i + e);
-                        float u[4];
-                        unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, pack2(zz.x, zz.y)), u[0], u[1]);
-                        unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), scale2, pack2(zz.z, zz.w)), u[2], u[3]);
+                    for (int e = 0; e < 32; e += 2)
+                        unpack2(mul2(pack2(__uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1])), scale2), u[e], u[e + 1]);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            u[y] = exp2_fast(u[y]);
-                            if (masked && (32 * i + e + y < c0 || 32 * i + e + y >= c1)) u[y] = 0.0f;
-                        }
-                        sum[0] = add2(sum[0], pack2(u[0], u[1]));
-                        sum[1] = add2(sum[1], pack2(u[2], u[3]));
-                    }
+                    for (int e = 0; e < 32; ++e) u[e] = exp2_fast(u[e]);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) sum[y] = add2(sum[y], pack2(u[e + 2 * y], u[e + 2 * y + 1]));
                 }
             }
             if (!ok) break;
             if (live) {
                 float x, y;
-                unpack2(add2(sum[0], sum[1]), x, y);
+                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
                 a.out[at] = fmaf(a.decay, old, x + y);
             }
             next_item(a.s, a.c, extent, a.tiles, t, &g_mass_tiles_error);
@@ -346,6 +394,8 @@ cudaError_t launch(MassArgs a, const void* k, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
+    a.lse_scale = -1.44269504088896341f / a.scale_log2;
+    a.nothing = a.scale_log2 < 0.0f ? 1e38f : -1e38f;   // times any scale a call may have: below every exponent
     a.tiles = (int)(((long long)a.s.width * a.c.page_size + C::NS * kKeys - 1) / (C::NS * kKeys));
     const long long items = (long long)a.s.B * a.c.kv_heads * a.tiles;
     return launch_pdl(mass_tiles_kernel<D>, dim3((unsigned)std::min<long long>(sms, items)), dim3(C::kThreads), C::kSmem,

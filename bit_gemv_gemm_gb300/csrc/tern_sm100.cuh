@@ -215,6 +215,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
+// A K-major operand of one K = 16 step alone: rows of 32 B in the canonical
+// 32-byte-swizzled layout (the two 16-byte halves of rows 4-7 of every 8
+// change places), 8-row groups 256 B apart.
+__device__ __forceinline__ uint64_t smem_desc_k_sw32(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;
+    d |= (uint64_t)(256u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)6u << 61;                           // layout: 32-byte swizzle
+    return d;
+}
+
 // Instruction descriptor, kind::f16: D f32, A and B bf16, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4)                        // D format: f32

@@ -196,13 +196,15 @@ def test_uniform_tokens_without_q_start(tern, B):
 @pytest.mark.parametrize("new", [1, 140])
 def test_sharp_and_flat_scores(tern, new):
     """Scores of a standard deviation of about 12 (one key takes the row), all
-    equal scores, and a negative scale."""
+    equal scores, a negative scale and none."""
     p = Problem(1, [new + 500], [new], 8, 2, 128, spread=12.0)
     check_both(tern, p)
     p = Problem(2, [new + 500], [new], 8, 2, 128, spread=0.0)
     check_both(tern, p)
     p = Problem(3, [new + 500], [new], 8, 2, 128)
     p.scale = -p.scale
+    check_both(tern, p)
+    p.scale = 0.0
     check_both(tern, p)
 
 
