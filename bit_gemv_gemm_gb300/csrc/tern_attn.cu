@@ -80,7 +80,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     const long long rows = (long long)a.s.max_new * a.group;
     // few rows: bound by reading the cache, which the rows kernel does once for
     // 32 rows (16 at D = 256); more rows: the tensor cores
-    const bool few = rows <= (a.c.head_dim == 256 ? 16 : 32);
+    const bool few = rows <= 16;
     const cudaError_t e = few ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
                               : launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;

@@ -104,13 +104,13 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         auto fetch_ids = [&](int base) {
             const int k = base + lane;
             ids = 0;
-            if (k < my) ids = checked_page(trow[(first + warp + kWarps * k) * kStrip / a.c.page_size], a.c.pages, &g_attn_rows_error);
+            if (k < my) ids = checked_page(trow[(unsigned)((first + warp + kWarps * k) * kStrip) / (unsigned)a.c.page_size], a.c.pages, &g_attn_rows_error);
         };
         auto issue = [&](int k) {   // strip k of this warp, into slot (it + k) mod stages
             const int page = __shfl_sync(0xffffffffu, ids, k & 31);
             if (lane == 0) {
                 const uint32_t s = (it + (uint32_t)k) % C::kStages;
-                const int slot = (first + warp + kWarps * k) * kStrip % a.c.page_size;
+                const int slot = (unsigned)((first + warp + kWarps * k) * kStrip) % (unsigned)a.c.page_size;
                 mbar_arrive_expect_tx(bars + 8u * s, C::kStage);
                 tma_load_cache(ring + s * C::kStage, &tmap_k, slot, 0, hk, page, bars + 8u * s);
                 tma_load_cache(ring + s * C::kStage + C::kStage / 2, &tmap_v, slot, 0, hk, page, bars + 8u * s);

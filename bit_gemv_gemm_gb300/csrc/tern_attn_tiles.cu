@@ -22,6 +22,10 @@
 // 256: for the next keys, into a second S).  A row tile's thread issues PV(j)
 // and then QK(j + 1), so S (and P over it) needs one buffer a tile: one
 // thread's products complete in issue order.
+// Where an item has one row tile only (verify steps, short chunks), the two
+// streams take its even and its odd key tiles, with an accumulator each; the
+// first one's warpgroup then adds both (tensor memory is open to it).  Warps without a live row do no arithmetic.  Such calls are
+// bound by reading the cache.
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
@@ -60,10 +64,11 @@ struct Cfg {
     static constexpr size_t kSmemRing = (size_t)NS * NC * kChunk;
     static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
     // barriers: full[slots], empty[slots], then pairs: q_full, q_empty, s_full,
-    // s_empty, p_full, o_full, o_empty, drain; tail
-    static constexpr int kBars = 2 * kSlots + 17;
+    // s_empty, p_full, o_full, o_empty, drain; tail, merge
+    static constexpr int kBars = 2 * kSlots + 18;
     static constexpr size_t kSmemMisc = kSmemBar + kBars * 8;
-    static constexpr size_t kSmem = kSmemMisc + 256 + 1024;
+    static constexpr size_t kSmemStat = kSmemMisc + 256;              // the second stream's (m, l), a split item
+    static constexpr size_t kSmem = kSmemStat + (NS == 2 ? kRows * 8 : 0) + 1024;
     static constexpr size_t kPart = (size_t)NS * kRows * (D + 2);   // floats of one part
 };
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys);
@@ -93,7 +98,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     auto slot_phase = [&](uint32_t i) { return (i / kSlots) & 1u; };
     auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)(CG * kChunk); };
     enum { Q_FULL = 2 * kSlots, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, S_EMPTY = S_FULL + 2, P_FULL = S_EMPTY + 2,
-           O_FULL = P_FULL + 2, O_EMPTY = O_FULL + 2, DRAIN = O_EMPTY + 2, TAIL = DRAIN + 2 };
+           O_FULL = P_FULL + 2, O_EMPTY = O_FULL + 2, DRAIN = O_EMPTY + 2, TAIL = DRAIN + 2, MERGE = TAIL + 1 };
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm_scan + 8 + C::kThreads / 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -101,7 +106,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kBars; ++i) {
-            const bool by_warps = (i >= P_FULL && i < P_FULL + 2) || (i >= O_EMPTY && i < O_EMPTY + 2);
+            const bool by_warps = (i >= P_FULL && i < P_FULL + 2) || (i >= O_EMPTY && i < O_EMPTY + 2) || i == MERGE;
             const bool by_tiles = NS == 2 && i >= kSlots && i < 2 * kSlots;   // both MMA threads release a slot
             mbar_init(bar(i), by_warps ? 4 : by_tiles ? 2 : 1);
         }
@@ -152,12 +157,12 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
             const int key0 = (t.j0 / kKeys + (int)(w - t.at)) * kKeys;
             for (int s = 0; s < NS && ok && nt > 0; ++s) {
-                if (s * tile_rows >= t.rows) continue;
+                const bool split = t.rows <= tile_rows;   // both streams take the one row tile
                 if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY + s), (used[s] & 1u) ^ 1u))) { ok = false; break; }
                 ++used[s];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(Q_FULL + s), (uint32_t)(NC * tile_rows * 128));
-                    const int tok = t.q.q0 + (t.rt * R + s * tile_rows) / a.group;
+                    const int tok = t.q.q0 + (t.rt * R + (split ? 0 : s * tile_rows)) / a.group;
                     for (int c = 0; c < NC; ++c)
                         tma_load_q(sbase + (uint32_t)((s * NC + c) * kChunk), &tmap_q, t.hk * a.group, tok, c,
                                    bar(Q_FULL + s));
@@ -261,10 +266,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const long long we = min(w1, t.at + t.units);
                 const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
                 if constexpr (NS == 2) {
-                    // PV(j), QK(j + 1) of row tile `me`; a tile that the item does not have only releases slots
-                    const bool active = t.rows > me * tile_rows;
-                    if (active && nt > 0) need(bar(Q_FULL + me), used & 1u);
+                    // QK(j), PV(j) of row tile `me`, or of every second key tile; of the others only the slots are released
+                    const bool split = t.rows <= tile_rows;
+                    if (nt > 0) need(bar(Q_FULL + me), used & 1u);
                     for (int j = 0; j < nt && ok; ++j) {
+                        const bool active = !split || (j & 1) == me;
                         if (!need(full_bar(it), slot_phase(it))) break;
                         if (active) {
                             tc_fence_after();
@@ -280,16 +286,17 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         if (active) {
                             if (!need(bar(P_FULL + me), jobs++ & 1u)) break;
                             // the previous item's output has been read
-                            if (j == 0 && !need(bar(O_EMPTY + me), (used & 1u) ^ 1u)) break;
+                            const bool first = j == (split ? me : 0);
+                            if (first && !need(bar(O_EMPTY + me), (used & 1u) ^ 1u)) break;
                             tc_fence_after();
-                            pv(me, me, slot_addr(it), j > 0);
+                            pv(me, me, slot_addr(it), !first);
                             mma_commit(empty_bar(it));
                         } else {
                             mbar_arrive(empty_bar(it));
                         }
                         ++it;
                     }
-                    if (active && nt > 0 && ok) {
+                    if (nt > 0 && ok) {   // (one key tile, the second stream: nothing to wait for)
                         mma_commit(bar(O_FULL + me));
                         mma_commit(bar(Q_EMPTY + me));
                         ++used;
@@ -347,27 +354,34 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t to = tmem + lanes + C::kO + (uint32_t)(D * s);
-        uint32_t sc = 0, oc = 0;   // S and O tiles seen
+        uint32_t sc = 0, oc = 0, merges = 0;   // S and O tiles and split items seen
         const bool flip = a.scale_log2 < 0.0f;
         const float scale = fabsf(a.scale_log2);
         bool ok = true;
         for (long long w = w0; w < w1 && ok;) {
             const long long we = min(w1, t.at + t.units);
             const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
-            const int rows = min(tile_rows, t.rows - s * tile_rows);   // of this row tile
-            if (rows > 0) {
-                const int r = t.rt * R + s * tile_rows + row;          // packed row of the sequence
-                const bool live = row < rows;
+            const bool split = NS == 2 && t.rows <= tile_rows;   // every second key tile of the one row tile
+            const int sr = split ? 0 : s;
+            const int rows = min(tile_rows, t.rows - sr * tile_rows);   // of this row tile
+            {
+                const int r = t.rt * R + sr * tile_rows + row;         // packed row of the sequence
+                const bool live = row < rows, idle = quad * 32 >= rows;
                 const int p = t.q.len - t.q.n + r / a.group;
                 const int hi = live ? p : -1, lo = a.window > 0 ? p - a.window : -1;
-                const int p_lo = t.q.len - t.q.n + (t.rt * R + s * tile_rows) / a.group;
-                const int p_hi = t.q.len - t.q.n + (t.rt * R + s * tile_rows + rows - 1) / a.group;
+                const int p_lo = t.q.len - t.q.n + (t.rt * R + sr * tile_rows) / a.group;
+                const int p_hi = t.q.len - t.q.n + (t.rt * R + sr * tile_rows + rows - 1) / a.group;
                 const int key0 = (t.j0 / kKeys + (int)(w - t.at)) * kKeys;
                 float m = -INFINITY, l = 0.0f;
-                for (int j = 0; j < nt && ok; ++j, ++sc) {
+                const int j_first = split ? s : 0, j_step = split ? 2 : 1;
+                for (int j = j_first; j < nt && ok; j += j_step, ++sc) {
                     const uint32_t buf = kWide ? sc & 1u : (uint32_t)s;
                     const uint32_t ph = kWide ? (sc >> 1) & 1u : sc & 1u;
                     if (!__all_sync(0xffffffffu, wait(bar(S_FULL + (int)buf), ph))) { ok = false; break; }
+                    if (idle) {
+                        if (lane == 0) mbar_arrive(bar(P_FULL + (int)buf));
+                        continue;
+                    }
                     tc_fence_after();
                     const uint32_t ts = tmem + lanes + C::kS + 128u * buf;
                     uint32_t x[4][32];
@@ -398,7 +412,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         const float f = m == -INFINITY ? 0.0f : exp2_fast((m - mn) * scale);
                         m = mn;
                         l *= f;
-                        if (j > 0) {
+                        if (j > j_first) {
                             if (kWide) {
                                 // the product before this one is still adding into O
                                 if (!__all_sync(0xffffffffu, wait(bar(O_FULL), (oc + (uint32_t)j - 1u) & 1u))) {
@@ -455,13 +469,45 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
                     tc_fence_after();
                 }
+                float m2 = m * scale;   // -inf stays
+                float f0 = 1.0f, f1 = 0.0f;
+                if (split && nt > 0) {
+                    float2* stat = reinterpret_cast<float2*>(smem + C::kSmemStat);
+                    if (s == 1) {
+                        // the first stream has read what the last split item left here
+                        if (oc > 1 && !__all_sync(0xffffffffu, wait(bar(O_EMPTY + 1), oc & 1u))) { ok = false; break; }
+                        stat[row] = make_float2(m2, l);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(MERGE));
+                    } else {
+                        if (!__all_sync(0xffffffffu, wait(bar(MERGE), merges++ & 1u))) { ok = false; break; }
+                        tc_fence_after();   // (the second stream waited for its last product)
+                        const float2 o = stat[row];
+                        const float mm = fmaxf(m2, o.x), base = mm == -INFINITY ? 0.0f : mm;
+                        f0 = exp2_fast(m2 - base);
+                        f1 = exp2_fast(o.x - base);
+                        l = l * f0 + o.y * f1;
+                        m2 = mm;
+                    }
+                }
+                if (!split || s == 0) {   // (not indented: the output of a row tile)
                 float* part = a.partial + (size_t)(2 * blockIdx.x + (w == w0 ? 0 : 1)) * C::kPart;
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < D && !idle; c += 32) {
                     uint32_t o[32];
                     if (nt > 0) {
                         tmem_ld_x32(to + c, o);
+                        if (split) {
+                            uint32_t o1[32];   // (an accumulator that no product reached holds anything)
+                            tmem_ld_x32(to + (uint32_t)D + c, o1);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float x = f0 > 0.0f ? __uint_as_float(o[e]) * f0 : 0.0f;
+                                o[e] = __float_as_uint(f1 > 0.0f ? fmaf(__uint_as_float(o1[e]), f1, x) : x);
+                            }
+                        }
                         tmem_ld_wait();
                     } else {
 #pragma unroll
@@ -480,29 +526,32 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                                 dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
                             }
                         }
-                    } else {
+                    } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            __stcg(reinterpret_cast<uint4*>(part + part_at(D, s, row, c / 4 + e)),
+                            __stcg(reinterpret_cast<uint4*>(part + part_at(D, sr, row, c / 4 + e)),
                                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
                     }
                 }
                 if (nt > 0) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(O_EMPTY + s));
+                    if (lane == 0) {
+                        mbar_arrive(bar(O_EMPTY + s));
+                        if (split) mbar_arrive(bar(O_EMPTY + 1));
+                    }
                 }
-                const float m2 = m * scale;   // -inf stays
-                if (whole) {
+                if (idle) {
+                } else if (whole) {
                     if (live && a.lse) a.lse[orow] = l > 0.0f ? (m2 + log2f(l)) * 0.693147180559945309f : -INFINITY;
                 } else {
-                    __stcg(reinterpret_cast<float2*>(part + part_stat(D, s, row)), make_float2(m2, l));
+                    __stcg(reinterpret_cast<float2*>(part + part_stat(D, sr, row)), make_float2(m2, l));
                     __threadfence();
                     __syncwarp();
                     const int c_lo = unit_owner(total, P, t.at), c_hi = unit_owner(total, P, t.at + t.units - 1);
                     unsigned last = 0;
                     if (lane == 0)
-                        last = atomicInc(a.counters + 8 * c_lo + 4 * s + quad, (unsigned)(c_hi - c_lo)) ==
+                        last = atomicInc(a.counters + 8 * c_lo + 4 * sr + quad, (unsigned)(c_hi - c_lo)) ==
                                (unsigned)(c_hi - c_lo);
                     if (__shfl_sync(0xffffffffu, last, 0)) {
                         __threadfence();
@@ -511,10 +560,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         };
                         float mm = -INFINITY, ll = 0.0f;
                         for (int x = c_lo; x <= c_hi; ++x)
-                            mm = fmaxf(mm, __ldcg(part_of(x) + part_stat(D, s, row)));
+                            mm = fmaxf(mm, __ldcg(part_of(x) + part_stat(D, sr, row)));
                         const float base = mm == -INFINITY ? 0.0f : mm;
                         for (int x = c_lo; x <= c_hi; ++x) {
-                            const float2 st = __ldcg(reinterpret_cast<const float2*>(part_of(x) + part_stat(D, s, row)));
+                            const float2 st = __ldcg(reinterpret_cast<const float2*>(part_of(x) + part_stat(D, sr, row)));
                             ll += st.y * exp2_fast(st.x - base);
                         }
                         const float inv2 = ll > 0.0f ? 1.0f / ll : 0.0f;
@@ -523,11 +572,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             float y[32] = {};
                             for (int x = c_lo; x <= c_hi; ++x) {
                                 const float* px = part_of(x);
-                                const float f = exp2_fast(__ldcg(px + part_stat(D, s, row)) - base);
+                                const float f = exp2_fast(__ldcg(px + part_stat(D, sr, row)) - base);
                                 float4 v[8];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    v[e] = __ldcg(reinterpret_cast<const float4*>(px + part_at(D, s, row, c / 4 + e)));
+                                    v[e] = __ldcg(reinterpret_cast<const float4*>(px + part_at(D, sr, row, c / 4 + e)));
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
                                     y[4 * e] += v[e].x * f;
@@ -549,6 +598,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         if (live && a.lse)
                             a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
                     }
+                }
                 }
             }
             w = we;

@@ -17,14 +17,17 @@ namespace {
 
 __device__ int g_mass_rows_error;
 
-constexpr int kWarps = 8, kThreads = kWarps * 32, kStrip = 16;
-constexpr int kRows = 64;
-constexpr int kMinUnits = 2 * kWarps;
+constexpr int kStrip = 16, kRows = 64;
 
+// A strip is little work in a long chain (wait, loads, products, exponentials,
+// shuffles: about 2000 clocks), so an SM needs many warps to keep its copies
+// coming: 16, with three strips each in flight.
 template <int D>
 struct Cfg {
+    static constexpr int kWarps = D == 256 ? 8 : 16, kThreads = kWarps * 32;
+    static constexpr int kMinUnits = kWarps;           // strips a share holds at least
     static constexpr int kStage = kStrip * D * 2;      // K of one strip
-    static constexpr int kStages = 8 * 64 / D;         // 8 at D = 64, 4, 2: 16 KB a warp
+    static constexpr int kStages = D == 64 ? 6 : 3;
     static constexpr size_t kSmemQ = (size_t)kWarps * kStages * kStage;
     static constexpr size_t kSmemBar = kSmemQ + (size_t)kRows * D * 2;
     static constexpr size_t kSmemLse = kSmemBar + kWarps * kStages * 8;
@@ -44,9 +47,11 @@ struct AllKeysExtent {   // every key of the sequence, against all its rows
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
     using namespace sm100;
     using C = Cfg<D>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_consta
     long long total, w0, w1;
     Item t;
     const AllKeysExtent<kStrip> extent{a.group};
-    if (!find_share<kThreads>(a.s, a.c, extent, 1, kMinUnits, sm_scan, &g_mass_rows_error, total, P, w0, w1, t)) return;
+    if (!find_share<kThreads>(a.s, a.c, extent, 1, C::kMinUnits, sm_scan, &g_mass_rows_error, total, P, w0, w1, t)) return;
 
     uint32_t it = 0;
     for (long long w = w0; w < w1;) {
@@ -89,23 +94,26 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_consta
             const int k = base + lane;
             ids = 0;
             if (k < my)
-                ids = checked_page(trow[(first + warp + kWarps * k) * kStrip / a.c.page_size], a.c.pages, &g_mass_rows_error);
+                ids = checked_page(trow[(unsigned)((first + warp + kWarps * k) * kStrip) / (unsigned)a.c.page_size], a.c.pages, &g_mass_rows_error);
         };
         auto issue = [&](int k) {
             const int page = __shfl_sync(0xffffffffu, ids, k & 31);
             if (lane == 0) {
                 const uint32_t s = (it + (uint32_t)k) % C::kStages;
-                const int slot = (first + warp + kWarps * k) * kStrip % a.c.page_size;
+                const int slot = (unsigned)((first + warp + kWarps * k) * kStrip) % (unsigned)a.c.page_size;
                 mbar_arrive_expect_tx(bars + 8u * s, C::kStage);
                 tma_load_cache(ring + s * C::kStage, &tmap_k, slot, 0, hk, page, bars + 8u * s);
             }
         };
-        // the page ids are looked up again, one strip ahead, for the mass: the ring runs further ahead
-        auto mass_at = [&](int k) -> long long {   // of this lane's key (lane & 15) of strip k; -1: none
-            const int key = (first + warp + kWarps * k) * kStrip + (lane & 15);
+        // the mass of strip k, lane (lane & 15)'s key; -1: none.  Its page id is still in the lanes: in the block of
+        // 32 that the ring is being filled from, or in the one before
+        int before = 0;
+        auto mass_at = [&](int k, int filled) -> long long {
+            const int now = __shfl_sync(0xffffffffu, ids, k & 31), old = __shfl_sync(0xffffffffu, before, k & 31);
+            const int strip = first + warp + kWarps * k, key = strip * kStrip + (lane & 15);
             if (k >= my || key >= q.len || lane >= 16) return -1;
-            const int page = checked_page(trow[key / a.c.page_size], a.c.pages, &g_mass_rows_error);
-            return ((long long)page * a.c.kv_heads + hk) * a.c.page_size + key % a.c.page_size;
+            const int page = (k >> 5) == (filled >> 5) ? now : old;
+            return ((long long)page * a.c.kv_heads + hk) * a.c.page_size + (unsigned)key % (unsigned)a.c.page_size;
         };
         fetch_ids(0);
         for (int k = 0; k < C::kStages && k < my; ++k) issue(k);
@@ -129,12 +137,13 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_consta
         const int p_lo = q.len - q.n, p_hi = q.len - 1;
         __syncthreads();
 
-        long long at = mass_at(0);
+        long long at = mass_at(0, 0);
         float old = at >= 0 ? __ldg(a.mass + at) : 0.0f;
         for (int k = 0; k < my; ++k) {
             const uint32_t slot = (it + (uint32_t)k) % C::kStages, phase = ((it + (uint32_t)k) / C::kStages) & 1u;
             const int key0 = (first + warp + kWarps * k) * kStrip;
-            const long long next_at = mass_at(k + 1);
+            // (the block of strip k + stages is in ids from the end of step k on, that of strip k + stages - 1 now)
+            const long long next_at = mass_at(k + 1, k + C::kStages - 1);
             const float next_old = next_at >= 0 ? __ldg(a.mass + next_at) : 0.0f;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + 8u * slot, phase, abort_flag, kAttnWaitNs))) {
                 if (!*abort_flag) {
@@ -152,17 +161,29 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_consta
             float sum[2][2] = {};   // keys key0 + 8 n + 2 (lane & 3) + e
             const bool masked = key0 + kStrip - 1 > p_lo || (a.window > 0 && key0 <= p_hi - a.window);
             for (int i = 0; i < tiles; ++i) {
-                float s[2][4] = {};
+                // two accumulators a column tile, fragments loaded four steps ahead: the products are a short chain
+                float s2[2][2][4] = {};
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t kb[4], qa[4];
-                    const int krow = (mi >> 1) * 8 + l7, kc = (kk & 3) * 2 + (mi & 1);
-                    ldsm4(kb, ks + (kk >> 2) * (kStrip * 128) + krow * 128 + ((kc ^ l7) << 4));
-                    const int qrow = i * 16 + (mi & 1) * 8 + l7, qc = (kk & 3) * 2 + (mi >> 1);
-                    ldsm4(qa, qs + (kk >> 2) * (kRows * 128) + qrow * 128 + ((qc ^ l7) << 4));
-                    mma_bf16(s[0], qa, kb[0], kb[1]);
-                    mma_bf16(s[1], qa, kb[2], kb[3]);
+                for (int k4 = 0; k4 < D / 64; ++k4) {
+                    uint32_t kb[4][4], qa[4][4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int krow = (mi >> 1) * 8 + l7, kc = x * 2 + (mi & 1);
+                        ldsm4(kb[x], ks + k4 * (kStrip * 128) + krow * 128 + ((kc ^ l7) << 4));
+                        const int qrow = i * 16 + (mi & 1) * 8 + l7, qc = x * 2 + (mi >> 1);
+                        ldsm4(qa[x], qs + k4 * (kRows * 128) + qrow * 128 + ((qc ^ l7) << 4));
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        mma_bf16(s2[x & 1][0], qa[x], kb[x][0], kb[x][1]);
+                        mma_bf16(s2[x & 1][1], qa[x], kb[x][2], kb[x][3]);
+                    }
                 }
+                float s[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] = s2[0][n][e] + s2[1][n][e];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = i * 16 + h * 8 + (lane >> 2);
@@ -182,7 +203,10 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_consta
                 }
             }
             __syncwarp();
-            if (((k + C::kStages) & 31) == 0) fetch_ids(k + C::kStages);
+            if (((k + C::kStages) & 31) == 0) {
+                before = ids;
+                fetch_ids(k + C::kStages);
+            }
             if (k + C::kStages < my) issue(k + C::kStages);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -224,8 +248,8 @@ cudaError_t launch(const MassArgs& a, const void* k, int sms, cudaStream_t strea
         attr_set[dev] = true;
     }
     const long long strips = (long long)a.s.B * a.c.kv_heads * ((long long)a.s.width * a.c.page_size / kStrip);
-    const long long P = std::min<long long>(sms, (strips + kMinUnits - 1) / kMinUnits);
-    return launch_pdl(mass_rows_kernel<D>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, a);
+    const long long P = std::min<long long>(sms, (strips + C::kMinUnits - 1) / C::kMinUnits);
+    return launch_pdl(mass_rows_kernel<D>, dim3((unsigned)P), dim3(C::kThreads), C::kSmem, stream, true, mk, a);
 }
 
 }  // namespace
