@@ -39,18 +39,19 @@ __device__ __forceinline__ void keys_of_rows(const Seq& q, int group, int window
 
 // Keys are handed out in units of UNIT: the units of all items, in the order
 // (sequence, row tile, key head), are cut into one equal contiguous share per
-// CTA, whatever the sequences' lengths.  An item that no key reaches counts one
-// unit (its rows are written as zeros).
+// CTA, whatever the sequences' lengths.  An item counts `cost` units more than
+// its keys have, for what it costs to begin and end one.
 struct Item {
     int b, rt, hk;
     Seq q;
-    int rows, j0, j1, units;   // its rows and the keys they see together
+    int rows, j0, j1, units;   // its rows, the keys they see together, and its units
     long long at;              // its first unit
 };
 // The extent of an item by its (b, rt, q): a row tile of R rows over the keys
 // it sees.  units = 0: the sequence has no such item.
-template <int UNIT>
+template <int UNIT, int COST>
 struct RowTileExtent {
+    static constexpr int kUnit = UNIT, kCost = COST;
     int R, group, window;
     __device__ __forceinline__ void operator()(Item& t) const {
         const int r0 = t.rt * R, all = t.q.n * group;
@@ -60,7 +61,7 @@ struct RowTileExtent {
             return;
         }
         keys_of_rows(t.q, group, window, r0, r0 + t.rows, t.j0, t.j1);
-        t.units = t.j1 > t.j0 ? (t.j1 - 1) / UNIT - t.j0 / UNIT + 1 : 1;
+        t.units = COST + (t.j1 > t.j0 ? (t.j1 - 1) / UNIT - t.j0 / UNIT + 1 : 0);
     }
 };
 __host__ __device__ inline long long unit_begin(long long total, int P, int c) {
@@ -73,6 +74,27 @@ __device__ inline int unit_owner(long long total, int P, long long u) {
     while (c + 1 < P && unit_begin(total, P, c + 1) <= u) ++c;
     while (c > 0 && unit_begin(total, P, c) > u) --c;
     return c;
+}
+
+// What units [w, we) of an item are in key units: `n` from `first` on.  A
+// segment of an item that has keys, but none of them, is `skip`ped; an item
+// without keys (zeros are written) goes to the share that holds its first unit.
+struct Segment {
+    long long we;
+    int first, n;
+    bool whole, skip;
+};
+template <typename Extent>
+__device__ __forceinline__ Segment segment_of(const Extent&, const Item& t, long long w, long long w1) {
+    Segment s;
+    s.we = min(w1, t.at + t.units);
+    const int lo = max((int)(w - t.at) - Extent::kCost, 0), hi = max((int)(s.we - t.at) - Extent::kCost, 0);
+    const int all = t.units - Extent::kCost;
+    s.n = hi - lo;
+    s.first = (t.j1 > t.j0 ? t.j0 / Extent::kUnit : 0) + lo;
+    s.whole = s.n == all;
+    s.skip = all > 0 ? s.n == 0 : w != t.at;
+    return s;
 }
 
 // The next item, past row tiles that a sequence does not have; `tiles` row
@@ -169,10 +191,10 @@ __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent&
 }
 
 // No call has more units than this (host: the lengths are on the device).
-inline long long most_units(const AttnArgs& a, int unit) {
+inline long long most_units(const AttnArgs& a, int unit, int cost) {
     const long long room = (long long)a.s.width * a.c.page_size;
     const long long keys = a.window > 0 && a.window + (long long)a.s.max_new < room ? a.window + (long long)a.s.max_new : room;
-    return (long long)a.s.B * a.c.kv_heads * a.tiles * ((keys + unit - 1) / unit + 1);
+    return (long long)a.s.B * a.c.kv_heads * a.tiles * ((keys + unit - 1) / unit + 1 + cost);
 }
 
 // A cache array as the TMA sees it: [page][head][d / 64][slot][64 values], a

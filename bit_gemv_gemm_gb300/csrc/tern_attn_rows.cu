@@ -26,6 +26,7 @@ __device__ int g_attn_rows_error;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStrip = 16;
 constexpr int kMaxR = 32, kMaxD = 256;
+constexpr int kItemCost = 4;                   // strips' time that an item costs besides its own
 constexpr int kMinUnits = 2 * kWarps;         // strips a share holds at least (two a warp)
 
 template <int D, int MT>
@@ -85,18 +86,19 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     int P;
     long long total, w0, w1;
     Item t;
-    const RowTileExtent<kStrip> extent{R, a.group, a.window};
+    const RowTileExtent<kStrip, kItemCost> extent{R, a.group, a.window};
     if (!find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinUnits, sm_scan, &g_attn_rows_error, total, P, w0, w1, t))
         return;
 
     uint32_t it = 0;   // strips this warp has fetched and used, over all segments
     for (long long w = w0; w < w1;) {
-        // ---- one segment: units [w, we) of the item ----
+        // ---- one segment of the item ----
         const Seq q = t.q;
-        const int rows = t.rows, units = t.units, j0 = t.j0, j1 = t.j1, r0 = t.rt * R, hk = t.hk, b = t.b;
-        const long long at = t.at, we = min(w1, at + units);
-        const int first = j0 / kStrip + (int)(w - at);
-        const int strips = j1 > j0 ? (int)(we - w) : 0;
+        const int rows = t.rows, units = t.units, j1 = t.j1, r0 = t.rt * R, hk = t.hk, b = t.b;
+        const Segment seg = segment_of(extent, t, w, w1);
+        const long long at = t.at, we = seg.we;
+        const int first = seg.first, strips = seg.n;
+        if (!seg.skip) {
         const int my = strips > warp ? (strips - warp + kWarps - 1) / kWarps : 0;
         // page ids: lane i holds the one of this warp's strip i of the current 32
         const int* trow = a.s.table + (long long)b * a.s.width;
@@ -287,7 +289,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         __syncthreads();
         if (*abort_flag) return;
 
-        const bool whole = w == at && we == at + units;
+        const bool whole = seg.whole;
         float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * (kMaxR * (kMaxD + 2));
         auto store_row = [&](int r, int c, const float (&y)[4], float mm, float ll) {
             // columns c .. c + 3 of row r, divided by the sum
@@ -323,20 +325,21 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         if (!whole) {
             // count into the item's counter (its first CTA's); the last one adds the parts
-            const int c_lo = unit_owner(total, P, at), c_hi = unit_owner(total, P, at + units - 1);
+            const int c_lo = unit_owner(total, P, at + kItemCost), c_hi = unit_owner(total, P, at + units - 1);
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) *sm_last = atomicInc(a.counters + c_lo, (unsigned)(c_hi - c_lo)) == (unsigned)(c_hi - c_lo);
             __syncthreads();
             if (*sm_last) {
                 __threadfence();
+                // an item's first CTA may have begun before it: the part is then in its second slot
+                const int late = unit_begin(total, P, c_lo) >= at ? 0 : 1;
                 for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
                     const int r = i / (D / 4), c = i % (D / 4) * 4;
                     float mm = -INFINITY, ll = 0.0f, y[4] = {};
+#pragma unroll 4
                     for (int x = c_lo; x <= c_hi; ++x) {
-                        // an item's first CTA may have begun before it: the part is then in its second slot
-                        const float* px = a.partial + (size_t)(2 * x + (unit_begin(total, P, x) >= at ? 0 : 1)) *
-                                                          (kMaxR * (kMaxD + 2));
+                        const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * (kMaxR * (kMaxD + 2));
                         const float2 st = __ldcg(reinterpret_cast<const float2*>(px + kMaxR * kMaxD + 2 * r));
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(px + r * D + c));
                         const float mn = fmaxf(mm, st.x);
@@ -356,6 +359,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         // the ring was written as ordinary memory: order that before the next copies into it
         fence_proxy_async_smem();
         __syncthreads();
+        }
 
         w = we;
         if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_rows_error);
@@ -378,7 +382,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
         attr_set[dev] = true;
     }
     a.tiles = (int)(((long long)a.s.max_new * a.group + C::R - 1) / C::R);
-    const long long P = std::min<long long>((long long)sms * C::kCtas, (most_units(a, kStrip) + kMinUnits - 1) / kMinUnits);
+    const long long P = std::min<long long>((long long)sms * C::kCtas, (most_units(a, kStrip, kItemCost) + kMinUnits - 1) / kMinUnits);
     return launch_pdl(attn_rows_kernel<D, MT>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, mv, a);
 }
 

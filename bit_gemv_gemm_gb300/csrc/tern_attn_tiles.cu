@@ -5,9 +5,12 @@
 // so one K and V tile serves all the heads that share it.  A CTA keeps NS row
 // tiles at once (two; one at D = 256, where the accumulator takes half of
 // tensor memory) against the same stream of 128-key tiles:
-//   * a TMA warp brings Q once and then K and V, in chunks of 64 head values x
-//     128 keys (16 KB of 128-byte swizzled rows), through one ring; a page
-//     gives boxes of up to 128 slots, one lane a box;
+//   * a TMA warp brings Q once and then K, another V, in chunks of 64 head
+//     values x 128 keys (16 KB of 128-byte swizzled rows), through one ring; a
+//     page gives boxes of up to 128 slots, one lane a box.  A copy takes a warp
+//     about 110 clocks to issue, and a page id some 700 to look up (one warp
+//     for both, without looking ahead, took 2000 to 3000 a tile and bound every
+//     call), hence two warps, and ids fetched 32 boxes ahead;
 //   * one thread a row tile issues S = Q K^T (both operands in shared memory,
 //     K-major) and O += P V (P in tensor memory, V MN-major) with M = 128.
 //     Issuing is nearly synchronous (a wait or a commit between products costs
@@ -45,6 +48,7 @@ __device__ int g_attn_tiles_error;
 
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
+constexpr int kItemCost = 3;                // key tiles' time that an item costs besides its own (about 3.5 us)
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 
 template <int D>
@@ -55,10 +59,10 @@ struct Cfg {
     static constexpr int NG = NC / CG;                      // slots of a K or V tile
     static constexpr int kSlots = D == 64 ? 10 : D == 128 ? 5 : 8;
     static constexpr int kSoftWarps = 4 * NS;
-    // two row tiles: a third warpgroup (TMA, two MMA warps, an idle one) gives registers
+    // two row tiles: a third warpgroup (two TMA and two MMA warps) gives registers
     // to the softmax warps, which hold a row of S each: 256 x 208 + 128 x 88 =
     // 384 x 168, what the CTA was launched with
-    static constexpr int kThreads = NS == 2 ? 384 : 224;
+    static constexpr int kThreads = NS == 2 ? 384 : 256;
     static constexpr uint32_t kS = 0, kO = 256;             // tensor memory: S (and P) at 128 b, O at kO + D s
     static constexpr size_t kSmemQ = 0;
     static constexpr size_t kSmemRing = (size_t)NS * NC * kChunk;
@@ -132,7 +136,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     int P;
     long long total, w0, w1;
     Item t;
-    const RowTileExtent<kKeys> extent{R, a.group, a.window};
+    const RowTileExtent<kKeys, kItemCost> extent{R, a.group, a.window};
     const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, sm_scan, &g_attn_tiles_error, total,
                                               P, w0, w1, t);
     auto fail = [&] {
@@ -147,62 +151,70 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         // no share: straight to the end
     } else if (warp >= C::kSoftWarps) {
       if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-      if (warp == C::kSoftWarps) {
-        // ------------------------------ TMA ------------------------------
-        uint32_t it = 0, seg = 0, used[2] = {0, 0}, tails = 0;
+      if (warp == C::kSoftWarps || warp == C::kSoftWarps + 3) {
+        // ------------------------------ TMA: Q and K, or V ------------------------------
+        const bool is_v = warp != C::kSoftWarps;
+        const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+        uint32_t it = is_v ? NG : 0, used[2] = {0, 0}, tails = 0;   // slots: K(0), V(0), K(1), ...
         bool ok = true;
-        const int boxes = kKeys / box_rows;
-        for (long long w = w0; w < w1 && ok; ++seg) {
-            const long long we = min(w1, t.at + t.units);
-            const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
-            const int key0 = (t.j0 / kKeys + (int)(w - t.at)) * kKeys;
-            for (int s = 0; s < NS && ok && nt > 0; ++s) {
+        const int boxes = kKeys / box_rows, c = lane / boxes, box = lane - c * boxes;   // this lane's piece of a tile
+        for (long long w = w0; w < w1 && ok;) {
+            const Segment seg = segment_of(extent, t, w, w1);
+            const int nt = seg.n, key0 = seg.first * kKeys;
+            const int* trow = a.s.table + (long long)t.b * a.s.width;
+            // lane i: the page of box i of the current 32 boxes of this segment, and of the next 32
+            auto raw_id = [&](int x) {
+                const int k = key0 + x * box_rows;
+                return x < nt * boxes && k < t.q.len && k + box_rows > t.j0 ? trow[(unsigned)k / (unsigned)a.c.page_size] : 0;
+            };
+            int ids = 0, ahead = raw_id(lane);
+            for (int s = 0; s < NS && ok && nt > 0 && !is_v; ++s) {
                 const bool split = t.rows <= tile_rows;   // both streams take the one row tile
                 if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY + s), (used[s] & 1u) ^ 1u))) { ok = false; break; }
                 ++used[s];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(Q_FULL + s), (uint32_t)(NC * tile_rows * 128));
                     const int tok = t.q.q0 + (t.rt * R + (split ? 0 : s * tile_rows)) / a.group;
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_q(sbase + (uint32_t)((s * NC + c) * kChunk), &tmap_q, t.hk * a.group, tok, c,
+                    for (int x = 0; x < NC; ++x)
+                        tma_load_q(sbase + (uint32_t)((s * NC + x) * kChunk), &tmap_q, t.hk * a.group, tok, x,
                                    bar(Q_FULL + s));
                 }
             }
-            const int* trow = a.s.table + (long long)t.b * a.s.width;
-            const int c = lane / boxes, box = lane - c * boxes;   // this lane's piece of a tile
-            auto page_of = [&](int j) {
-                const int k = key0 + j * kKeys + box * box_rows;
-                const bool use = c < NC && k < t.q.len && k + box_rows > t.j0;
-                return use ? checked_page(trow[k / a.c.page_size], a.c.pages, &g_attn_tiles_error) : -1;
-            };
-            auto load = [&](int j, int page, bool is_v) {
-                const int k0 = key0 + j * kKeys;
+            for (int j = 0; j < nt && ok; ++j) {
+                if (((j * boxes) & 31) == 0) {
+                    ids = checked_page(ahead, a.c.pages, &g_attn_tiles_error);
+                    ahead = raw_id(j * boxes + 32 + lane);
+                }
+                const int page = __shfl_sync(0xffffffffu, ids, (j * boxes + box) & 31);
+                const int k0 = key0 + j * kKeys, k = k0 + box * box_rows;
                 // boxes that hold no key of these rows are not read; V's rows there count as 0
+                const bool use = c < NC && k < t.q.len && k + box_rows > t.j0;
                 const bool part = is_v && (k0 + kKeys > t.q.len || k0 + box_rows <= t.j0);
-                const uint32_t mine = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t mine = __ballot_sync(0xffffffffu, use);
                 const uint32_t bytes = (uint32_t)__popc(mine & ((1u << boxes) - 1u)) * box_rows * 128u;   // a chunk's
+                const int slot = (unsigned)k % (unsigned)a.c.page_size;
                 if (part && lane == 0) mbar_arrive_expect_tx(bar(TAIL), bytes * NC);
                 for (int g = 0; g < NG; ++g) {
                     if (!__all_sync(0xffffffffu, wait(empty_bar(it + g), slot_phase(it + g) ^ 1u))) {
                         ok = false;
-                        return;
+                        break;
                     }
                     if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it + g), bytes * CG);
                     __syncwarp();
-                    if (page >= 0 && c / CG == g)
-                        tma_load_cache(slot_addr(it + g) + (uint32_t)((c % CG) * kChunk + box * box_rows * 128),
-                                       is_v ? &tmap_v : &tmap_k, (k0 + box * box_rows) % a.c.page_size, c, t.hk, page,
-                                       part ? bar(TAIL) : full_bar(it + g));
+                    if (use && c / CG == g)
+                        tma_load_cache(slot_addr(it + g) + (uint32_t)((c % CG) * kChunk + box * box_rows * 128), map,
+                                       slot, c, t.hk, page, part ? bar(TAIL) : full_bar(it + g));
                 }
+                if (!ok) break;
                 if (part) {
                     if (!__all_sync(0xffffffffu, wait(bar(TAIL), tails & 1u))) {
                         ok = false;
-                        return;
+                        break;
                     }
                     ++tails;
                     for (int i = lane; i < kKeys * NC * 8; i += 32) {
-                        const int x = i / (kKeys * 8), r = i / 8 % kKeys, k = k0 + r;
-                        if (k >= t.q.len || (k / box_rows + 1) * box_rows <= t.j0)
+                        const int x = i / (kKeys * 8), r = i / 8 % kKeys, key = k0 + r;
+                        if (key >= t.q.len || (key / box_rows + 1) * box_rows <= t.j0)
                             *reinterpret_cast<uint4*>(smem + C::kSmemRing +
                                                       (((it + x / CG) % kSlots) * CG + x % CG) * kChunk + r * 128 +
                                                       (i & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -212,27 +224,19 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (lane == 0)
                         for (int g = 0; g < NG; ++g) mbar_arrive(full_bar(it + g));
                 }
-                it += NG;
-            };
-            // in the order of their use: K(0), V(0), K(1), ...
-            int page = nt > 0 ? page_of(0) : -1;
-            for (int j = 0; j < nt && ok; ++j) {
-                const int next = j + 1 < nt ? page_of(j + 1) : -1;
-                load(j, page, false);
-                if (ok) load(j, page, true);
-                page = next;
+                it += 2 * NG;
             }
-            w = we;
+            w = seg.we;
             if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_tiles_error);
         }
         if (!ok && lane == 0) {
             fail();
             // copies in flight land before the CTA goes away
-            for (uint32_t i = it < (uint32_t)kSlots ? 0 : it - kSlots; i < it + NG; ++i)
-                (void)mbar_wait_drain(full_bar(i), slot_phase(i), 20000000ull);
+            for (uint32_t i = it < 2 * kSlots ? (is_v ? NG : 0) : it - 2 * kSlots; i <= it; i += 2 * NG)
+                for (int g = 0; g < NG; ++g) (void)mbar_wait_drain(full_bar(i + g), slot_phase(i + g), 20000000ull);
             for (int s = 0; s < NS; ++s)
                 if (used[s]) (void)mbar_wait_drain(bar(Q_FULL + s), (used[s] - 1u) & 1u, 20000000ull);
-            (void)mbar_wait_drain(bar(TAIL), tails & 1u, 20000000ull);
+            if (is_v) (void)mbar_wait_drain(bar(TAIL), tails & 1u, 20000000ull);
         }
         __syncwarp();
       } else if (warp <= C::kSoftWarps + 2) {
@@ -263,8 +267,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 issued = true;
             };
             for (long long w = w0; w < w1 && ok;) {
-                const long long we = min(w1, t.at + t.units);
-                const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
+                const Segment seg = segment_of(extent, t, w, w1);
+                const int nt = seg.n;
                 if constexpr (NS == 2) {
                     // QK(j), PV(j) of row tile `me`, or of every second key tile; of the others only the slots are released
                     const bool split = t.rows <= tile_rows;
@@ -278,6 +282,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             for (int c = 0; c < NC; ++c) qk(me, me, c, slot_addr(it) + (uint32_t)(c * kChunk));
                             mma_commit(bar(S_FULL + me));
                             mma_commit(empty_bar(it));
+                            if (j + (split ? 2 : 1) >= nt) mma_commit(bar(Q_EMPTY + me));   // its last use: the next may come
                         } else {
                             mbar_arrive(empty_bar(it));
                         }
@@ -298,7 +303,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     if (nt > 0 && ok) {   // (one key tile, the second stream: nothing to wait for)
                         mma_commit(bar(O_FULL + me));
-                        mma_commit(bar(Q_EMPTY + me));
+                        if (split && me >= nt) mbar_arrive(bar(Q_EMPTY + me));
                         ++used;
                     }
                 } else if (me == 0) {
@@ -335,7 +340,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     if (nt > 0) ++used;
                 }
-                w = we;
+                w = seg.we;
                 if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_tiles_error);
             }
             if (!ok) {
@@ -359,19 +364,19 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         const float scale = fabsf(a.scale_log2);
         bool ok = true;
         for (long long w = w0; w < w1 && ok;) {
-            const long long we = min(w1, t.at + t.units);
-            const int nt = t.j1 > t.j0 ? (int)(we - w) : 0;
+            const Segment seg = segment_of(extent, t, w, w1);
+            const int nt = seg.n;
             const bool split = NS == 2 && t.rows <= tile_rows;   // every second key tile of the one row tile
             const int sr = split ? 0 : s;
             const int rows = min(tile_rows, t.rows - sr * tile_rows);   // of this row tile
-            {
+            if (!seg.skip) {
                 const int r = t.rt * R + sr * tile_rows + row;         // packed row of the sequence
                 const bool live = row < rows, idle = quad * 32 >= rows;
                 const int p = t.q.len - t.q.n + r / a.group;
                 const int hi = live ? p : -1, lo = a.window > 0 ? p - a.window : -1;
                 const int p_lo = t.q.len - t.q.n + (t.rt * R + sr * tile_rows) / a.group;
                 const int p_hi = t.q.len - t.q.n + (t.rt * R + sr * tile_rows + rows - 1) / a.group;
-                const int key0 = (t.j0 / kKeys + (int)(w - t.at)) * kKeys;
+                const int key0 = seg.first * kKeys;
                 float m = -INFINITY, l = 0.0f;
                 const int j_first = split ? s : 0, j_step = split ? 2 : 1;
                 for (int j = j_first; j < nt && ok; j += j_step, ++sc) {
@@ -458,7 +463,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (lane == 0) mbar_arrive(bar(P_FULL + (int)buf));
                 }
                 if (!ok) break;
-                const bool whole = w == t.at && we == t.at + t.units;
+                const bool whole = seg.whole;
                 const int tok = t.q.q0 + r / a.group, head = t.hk * a.group + r % a.group;
                 const long long orow = (long long)tok * a.q_heads + head;
                 if (nt > 0) {
@@ -548,20 +553,23 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     __stcg(reinterpret_cast<float2*>(part + part_stat(D, sr, row)), make_float2(m2, l));
                     __threadfence();
                     __syncwarp();
-                    const int c_lo = unit_owner(total, P, t.at), c_hi = unit_owner(total, P, t.at + t.units - 1);
+                    const int c_lo = unit_owner(total, P, t.at + kItemCost), c_hi = unit_owner(total, P, t.at + t.units - 1);
                     unsigned last = 0;
                     if (lane == 0)
                         last = atomicInc(a.counters + 8 * c_lo + 4 * sr + quad, (unsigned)(c_hi - c_lo)) ==
                                (unsigned)(c_hi - c_lo);
                     if (__shfl_sync(0xffffffffu, last, 0)) {
                         __threadfence();
-                        auto part_of = [&](int x) {   // an item's first CTA may have begun before it
-                            return a.partial + (size_t)(2 * x + (unit_begin(total, P, x) >= t.at ? 0 : 1)) * C::kPart;
-                        };
+                        // (an item's first CTA may have begun before it: its part is then in its second slot)
+                        const int late = unit_begin(total, P, c_lo) >= t.at ? 0 : 1;
+                        auto part_of = [&](int x) { return a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * C::kPart; };
+                        // no branch in these loops: all the loads of a few parts are in flight together
                         float mm = -INFINITY, ll = 0.0f;
+#pragma unroll 4
                         for (int x = c_lo; x <= c_hi; ++x)
                             mm = fmaxf(mm, __ldcg(part_of(x) + part_stat(D, sr, row)));
                         const float base = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll 4
                         for (int x = c_lo; x <= c_hi; ++x) {
                             const float2 st = __ldcg(reinterpret_cast<const float2*>(part_of(x) + part_stat(D, sr, row)));
                             ll += st.y * exp2_fast(st.x - base);
@@ -570,6 +578,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float y[32] = {};
+#pragma unroll 3
                             for (int x = c_lo; x <= c_hi; ++x) {
                                 const float* px = part_of(x);
                                 const float f = exp2_fast(__ldcg(px + part_stat(D, sr, row)) - base);
@@ -579,10 +588,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                                     v[e] = __ldcg(reinterpret_cast<const float4*>(px + part_at(D, sr, row, c / 4 + e)));
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
-                                    y[4 * e] += v[e].x * f;
-                                    y[4 * e + 1] += v[e].y * f;
-                                    y[4 * e + 2] += v[e].z * f;
-                                    y[4 * e + 3] += v[e].w * f;
+                                    y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
+                                    y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
+                                    y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
+                                    y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
                                 }
                             }
                             if (live) {
@@ -601,7 +610,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 }
                 }
             }
-            w = we;
+            w = seg.we;
             if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_tiles_error);
         }
         if (!ok && lane == 0) fail();
@@ -635,7 +644,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
     }
     const int R = C::NS * (kRows / a.group * a.group);
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
-    const long long P = std::min<long long>(sms, (most_units(a, kKeys) + kMinTiles - 1) / kMinTiles);
+    const long long P = std::min<long long>(sms, (most_units(a, kKeys, kItemCost) + kMinTiles - 1) / kMinTiles);
     return launch_pdl(attn_tiles_kernel<D>, dim3((unsigned)P), dim3(C::kThreads), C::kSmem, stream, true, mq, mk, mv, a,
                       box);
 }
