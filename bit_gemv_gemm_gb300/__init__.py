@@ -85,6 +85,8 @@ class TernError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libtern.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -78,8 +78,9 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.counters = static_cast<unsigned*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
     const long long rows = (long long)a.s.max_new * a.group;
-    // few rows: bound by reading the cache, which the rows kernel does once for
-    // 32 rows (16 at D = 256); more rows: the tensor cores
+    // few rows: bound by reading the cache and by latency, which suits mma.sync
+    // and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
+    // 32k keys, 4 sequences: 106 us, against 115 from the rows kernel with 32 rows an item)
     const bool few = rows <= 16;
     const cudaError_t e = few ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
                               : launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream);

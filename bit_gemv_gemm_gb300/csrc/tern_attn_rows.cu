@@ -1,8 +1,8 @@
 // tern_attn_rows.cu -- attention of few query rows a key head (decode, verify):
 // bound by reading the cache once.
 //
-// One item is the R = 16 or 32 packed rows (token, head of the group) of one
-// sequence and key head; its keys are read in strips of 16.  All strips of all
+// One item is up to 16 packed rows (token, head of the group) of one sequence
+// and key head; its keys are read in strips of 16.  All strips of all
 // items are cut into one equal contiguous share a CTA (no CTA idles behind a
 // long sequence), two CTAs an SM.  In a CTA every warp takes every fourth strip of a
 // segment for itself: its lane 0 fetches the strip's K and V by TMA into the
@@ -25,13 +25,12 @@ namespace {
 __device__ int g_attn_rows_error;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStrip = 16;
-constexpr int kMaxR = 32, kMaxD = 256;
+constexpr int R = 16, kMaxD = 256;            // query rows of an item
 constexpr int kItemCost = 4;                   // strips' time that an item costs besides its own
 constexpr int kMinUnits = 2 * kWarps;         // strips a share holds at least (two a warp)
 
-template <int D, int MT>
+template <int D>
 struct Cfg {
-    static constexpr int R = 16 * MT;
     static constexpr int kStage = kStrip * D * 4;                 // K and V of one strip
     static constexpr int kStages = D == 64 ? 6 : 3;
     static constexpr int kRing = kStages * kStage;                // one warp's
@@ -49,13 +48,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, MT>::kCtas)
+template <int D>
+__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
 attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const AttnArgs a) {
     using namespace sm100;
-    using C = Cfg<D, MT>;
-    constexpr int R = C::R;
+    using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -132,25 +130,18 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             *reinterpret_cast<uint4*>(smem + C::kSmemQ + (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
         }
         // the keys that each of this thread's rows sees: (lo, hi]
-        int hi[MT][2], lo[MT][2];
+        int hi[2], lo[2];
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            const int r = (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 8 + (lane >> 2);
             const int p = q.len - q.n + (r0 + min(r, rows - 1)) / a.group;
-            hi[i >> 1][i & 1] = r < rows ? p : -1;
-            lo[i >> 1][i & 1] = a.window > 0 ? p - a.window : -1;
+            hi[i] = r < rows ? p : -1;
+            lo[i] = a.window > 0 ? p - a.window : -1;
         }
         const int p_lo = q.len - q.n + r0 / a.group, p_hi = q.len - q.n + (r0 + rows - 1) / a.group;
         __syncthreads();
 
-        float o[MT][D / 8][4], m[MT][2], l[MT][2];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            m[i][0] = m[i][1] = -INFINITY;
-            l[i][0] = l[i][1] = 0.0f;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
-        }
+        float o[D / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
         for (int k = 0; k < my; ++k) {
             const uint32_t slot = (it + (uint32_t)k) % C::kStages, phase = ((it + (uint32_t)k) / C::kStages) & 1u;
             const int key0 = (first + warp + kWarps * k) * kStrip;
@@ -167,77 +158,62 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             }
             const uint32_t ks = ring + slot * C::kStage, vs = ks + C::kStage / 2;
             // S = Q K^T
-            float s[MT][2][4];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.0f;
+            float s[2][4] = {};
             const int mi = lane >> 3, l7 = lane & 7;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t kb[4];
+                uint32_t kb[4], qa[4];
                 const int krow = (mi >> 1) * 8 + l7, kc = (kk & 3) * 2 + (mi & 1);
                 ldsm4(kb, ks + (kk >> 2) * (kStrip * 128) + krow * 128 + ((kc ^ l7) << 4));
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    uint32_t qa[4];
-                    const int qrow = i * 16 + (mi & 1) * 8 + l7, qc = (kk & 3) * 2 + (mi >> 1);
-                    ldsm4(qa, qs + (kk >> 2) * (R * 128) + qrow * 128 + ((qc ^ l7) << 4));
-                    mma_bf16(s[i][0], qa, kb[0], kb[1]);
-                    mma_bf16(s[i][1], qa, kb[2], kb[3]);
-                }
+                const int qrow = (mi & 1) * 8 + l7, qc = (kk & 3) * 2 + (mi >> 1);
+                ldsm4(qa, qs + (kk >> 2) * (R * 128) + qrow * 128 + ((qc ^ l7) << 4));
+                mma_bf16(s[0], qa, kb[0], kb[1]);
+                mma_bf16(s[1], qa, kb[2], kb[3]);
             }
             // scores in powers of two; a strip that some row does not see whole is masked
             const bool masked = key0 + kStrip - 1 > p_lo || (a.window > 0 && key0 <= p_hi - a.window);
             bool grow = false;
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = s[i][n][e] * a.scale_log2;
-                        if (masked) {
-                            const int key = key0 + n * 8 + (lane & 3) * 2 + (e & 1);
-                            if (key > hi[i][e >> 1] || key <= lo[i][e >> 1]) x = -INFINITY;
-                        }
-                        s[i][n][e] = x;
-                        grow |= x > m[i][e >> 1] + 8.0f;
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[n][e] * a.scale_log2;
+                    if (masked) {
+                        const int key = key0 + n * 8 + (lane & 3) * 2 + (e & 1);
+                        if (key > hi[e >> 1] || key <= lo[e >> 1]) x = -INFINITY;
                     }
+                    s[n][e] = x;
+                    grow |= x > m[e >> 1] + 8.0f;
+                }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+                for (int h = 0; h < 2; ++h) {
+                    float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    if (x > m[h]) {
+                        const float f = exp2_fast(m[h] - x);   // 0 from -inf
+                        m[h] = x;
+                        l[h] *= f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float x = fmaxf(fmaxf(s[i][0][2 * h], s[i][0][2 * h + 1]), fmaxf(s[i][1][2 * h], s[i][1][2 * h + 1]));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        if (x > m[i][h]) {
-                            const float f = exp2_fast(m[i][h] - x);   // 0 from -inf
-                            m[i][h] = x;
-                            l[i][h] *= f;
-#pragma unroll
-                            for (int n = 0; n < D / 8; ++n) {
-                                o[i][n][2 * h] *= f;
-                                o[i][n][2 * h + 1] *= f;
-                            }
+                        for (int n = 0; n < D / 8; ++n) {
+                            o[n][2 * h] *= f;
+                            o[n][2 * h + 1] *= f;
                         }
                     }
+                }
             }
-            uint32_t pa[MT][4];
+            uint32_t pa[4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // a row that has seen nothing keeps m = -inf: its probabilities are 0
-                        const float mm = m[i][h] == -INFINITY ? 0.0f : m[i][h];
-                        const float x = exp2_fast(s[i][n][2 * h] - mm), y = exp2_fast(s[i][n][2 * h + 1] - mm);
-                        l[i][h] += x + y;
-                        pa[i][2 * n + h] = pack_bf16(x, y);
-                    }
-            }
+                for (int h = 0; h < 2; ++h) {
+                    // a row that has seen nothing keeps m = -inf: its probabilities are 0
+                    const float mm = m[h] == -INFINITY ? 0.0f : m[h];
+                    const float x = exp2_fast(s[n][2 * h] - mm), y = exp2_fast(s[n][2 * h + 1] - mm);
+                    l[h] += x + y;
+                    pa[2 * n + h] = pack_bf16(x, y);
+                }
             // slots at or past the last visible key may hold anything: their V counts as 0
             uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
             if (key0 + kStrip > j1) {
@@ -254,11 +230,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 vb[1] &= z1;
                 vb[2] &= z0;
                 vb[3] &= z1;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    mma_bf16(o[i][2 * n], pa[i], vb[0], vb[1]);
-                    mma_bf16(o[i][2 * n + 1], pa[i], vb[2], vb[3]);
-                }
+                mma_bf16(o[2 * n], pa, vb[0], vb[1]);
+                mma_bf16(o[2 * n + 1], pa, vb[2], vb[3]);
             }
             __syncwarp();
             if (((k + C::kStages) & 31) == 0) fetch_ids(k + C::kStages);
@@ -268,29 +241,27 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
         // ---- the four warps' rows meet ----
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x = l[i][h];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                const int r = i * 16 + h * 8 + (lane >> 2);
-                if ((lane & 3) == 0) {
-                    sm_m[warp * R + r] = m[i][h];
-                    sm_l[warp * R + r] = x;
-                }
-                // [R][D] fp32 over the warp's own ring; columns rotated by row against bank conflicts
-                float* mo = reinterpret_cast<float*>(smem + warp * C::kRing) + r * D;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-                    *reinterpret_cast<float2*>(mo + ((n * 8 + (lane & 3) * 2 + r * 8) & (D - 1))) =
-                        make_float2(o[i][n][2 * h], o[i][n][2 * h + 1]);
+        for (int h = 0; h < 2; ++h) {
+            float x = l[h];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            const int r = h * 8 + (lane >> 2);
+            if ((lane & 3) == 0) {
+                sm_m[warp * R + r] = m[h];
+                sm_l[warp * R + r] = x;
             }
+            // [R][D] fp32 over the warp's own ring; columns rotated by row against bank conflicts
+            float* mo = reinterpret_cast<float*>(smem + warp * C::kRing) + r * D;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+                *reinterpret_cast<float2*>(mo + ((n * 8 + (lane & 3) * 2 + r * 8) & (D - 1))) =
+                    make_float2(o[n][2 * h], o[n][2 * h + 1]);
+        }
         __syncthreads();
         if (*abort_flag) return;
 
         const bool whole = seg.whole;
-        float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * (kMaxR * (kMaxD + 2));
+        float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * (R * (kMaxD + 2));
         auto store_row = [&](int r, int c, const float (&y)[4], float mm, float ll) {
             // columns c .. c + 3 of row r, divided by the sum
             const int tok = (r0 + r) / a.group, g = (r0 + r) % a.group;
@@ -320,7 +291,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 store_row(r, c, y, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(part + r * D + c), make_float4(y[0], y[1], y[2], y[3]));
-                if (c == 0) __stcg(reinterpret_cast<float2*>(part + kMaxR * kMaxD + 2 * r), make_float2(mm, ll));
+                if (c == 0) __stcg(reinterpret_cast<float2*>(part + R * kMaxD + 2 * r), make_float2(mm, ll));
             }
         }
         if (!whole) {
@@ -339,8 +310,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     float mm = -INFINITY, ll = 0.0f, y[4] = {};
 #pragma unroll 4
                     for (int x = c_lo; x <= c_hi; ++x) {
-                        const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * (kMaxR * (kMaxD + 2));
-                        const float2 st = __ldcg(reinterpret_cast<const float2*>(px + kMaxR * kMaxD + 2 * r));
+                        const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * (R * (kMaxD + 2));
+                        const float2 st = __ldcg(reinterpret_cast<const float2*>(px + R * kMaxD + 2 * r));
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(px + r * D + c));
                         const float mn = fmaxf(mm, st.x);
                         const float f0 = mm == -INFINITY ? 0.0f : exp2_fast(mm - mn);
@@ -366,9 +337,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     }
 }
 
-template <int D, int MT>
+template <int D>
 cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream_t stream) {
-    using C = Cfg<D, MT>;
+    using C = Cfg<D>;
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, k, a.c, kStrip, D / 64) || !make_cache_map(&mv, v, a.c, kStrip, D / 64))
         return cudaErrorInvalidValue;
@@ -376,28 +347,26 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)C::kSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    a.tiles = (int)(((long long)a.s.max_new * a.group + C::R - 1) / C::R);
+    a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
     const long long P = std::min<long long>((long long)sms * C::kCtas, (most_units(a, kStrip, kItemCost) + kMinUnits - 1) / kMinUnits);
-    return launch_pdl(attn_rows_kernel<D, MT>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, mv, a);
+    return launch_pdl(attn_rows_kernel<D>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, mv, a);
 }
 
 }  // namespace
 
-size_t attn_rows_workspace() { return (size_t)kMaxSms * 2 * 2 * kMaxR * (kMaxD + 2) * 4; }
+size_t attn_rows_workspace() { return (size_t)kMaxSms * 2 * 2 * R * (kMaxD + 2) * 4; }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms,
                              cudaStream_t stream) {
-    const long long max_rows = (long long)a.s.max_new * a.group;
-    // 32 rows read the cache once for up to 32; at most 16 rows need half the products
     switch (a.c.head_dim) {
-        case 64: return max_rows <= 16 ? launch<64, 1>(a, k, v, sms, stream) : launch<64, 2>(a, k, v, sms, stream);
-        case 128: return max_rows <= 16 ? launch<128, 1>(a, k, v, sms, stream) : launch<128, 2>(a, k, v, sms, stream);
-        default: return launch<256, 1>(a, k, v, sms, stream);
+        case 64: return launch<64>(a, k, v, sms, stream);
+        case 128: return launch<128>(a, k, v, sms, stream);
+        default: return launch<256>(a, k, v, sms, stream);
     }
 }
 
