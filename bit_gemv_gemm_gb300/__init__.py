@@ -71,8 +71,7 @@ EXPORTS = {
     "tern_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "tern_paged_attention": (_I, [_P, _LL, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _I, _P, _P, _P, _SZ, _P]),
     "tern_attention_mass": (_I, [_P, _LL, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _I, _P, _F, _P, _P, _P]),
-    "tern_cache_evict_workspace_bytes": (_SZ, [_I, _I, _I]),
-    "tern_cache_evict": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "tern_cache_evict": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P]),
 }
 
 
@@ -108,7 +107,8 @@ def _check(fn: str, st: int) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: building a Stream object takes longer than a small call's launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -122,6 +122,8 @@ def _covers(**need) -> None:
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -496,33 +498,50 @@ class CacheLayout(ctypes.Structure):
                 ("page_stride", _LL), ("head_stride", _LL), ("slot_stride", _LL)]
 
 
-@functools.lru_cache(maxsize=256)
-def _layout(shape, stride) -> CacheLayout:
+# What the calls below learn from shapes and strides alone is kept by shape: a
+# decode step makes the same small calls over and over, and the checks would take
+# longer than the launch.
+
+@functools.lru_cache(maxsize=1024)
+def _layout(name: str, shape, stride, like=None) -> CacheLayout:
+    """The layout of one cache array, bf16 [pages, kv_heads, page_size, head_dim]
+    with any strides over contiguous heads (a permuted [pages, page_size,
+    kv_heads, head_dim] array is one); `like`: the shape and strides of its K array."""
+    if len(shape) != 4 or stride[3] != 1:
+        raise ValueError(f"{name} must be [pages, kv_heads, page_size, head_dim] with contiguous heads")
+    if like is not None and (shape, stride) != like:
+        raise ValueError(f"{name} must have the shape and strides of its K array")
     return CacheLayout(shape[0], shape[2], shape[1], shape[3], stride[0], stride[1], stride[2])
 
 
-def _cache(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> CacheLayout:
-    """The layout of one cache array, bf16 [pages, kv_heads, page_size, head_dim]
-    with any strides over contiguous heads (a permuted [pages, page_size,
-    kv_heads, head_dim] array is one)."""
-    if t.dim() != 4 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be [pages, kv_heads, page_size, head_dim] with contiguous heads")
-    if like is not None and (t.shape != like.shape or t.stride() != like.stride()):
-        raise ValueError(f"{name} must have the shape and strides of its K array")
-    if not t.is_cuda or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
-    return _layout(tuple(t.shape), t.stride())
+def _caches(k: torch.Tensor, v: torch.Tensor | None, kn: str, vn: str) -> CacheLayout:
+    ks, kt = k.shape, k.stride()
+    lay = _layout(kn, ks, kt)
+    if v is not None:
+        _layout(vn, v.shape, v.stride(), (ks, kt))
+    if not k.is_cuda or k.dtype != torch.bfloat16:
+        raise TypeError(f"{kn} must be a bfloat16 CUDA tensor")
+    if v is not None:
+        if not v.is_cuda or v.dtype != torch.bfloat16:
+            raise TypeError(f"{vn} must be a bfloat16 CUDA tensor")
+    return lay
 
 
-def _tokens(t: torch.Tensor, dtypes, name: str, heads_dim=None) -> int:
-    """The token stride of [T, heads, head_dim] with contiguous heads."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+@functools.lru_cache(maxsize=4096)
+def _token_stride(name: str, shape, stride, heads, dim: int) -> int:
+    """The token stride of [T, heads, dim] with each token's heads contiguous."""
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with each token's heads contiguous")
-    if heads_dim is not None and tuple(t.shape[1:]) != heads_dim:
-        raise ValueError(f"{name} must hold {heads_dim[0]} heads of {heads_dim[1]}, got {tuple(t.shape[1:])}")
-    if not t.is_cuda or t.dtype not in dtypes:
-        raise TypeError(f"{name} must be a CUDA tensor of type {' or '.join(map(str, dtypes))}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must hold {'' if heads is None else heads} heads of {dim}, got {tuple(shape[1:])}")
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _tokens(t: torch.Tensor, dtype, name: str, heads, dim: int) -> int:
+    stride = _token_stride(name, t.shape, t.stride(), heads, dim)
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of type {dtype}")
+    return stride
 
 
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -554,19 +573,19 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     page_size + slot, negative: not stored); inv_freq fp32 [rot_dim / 2], its
     length setting how much of a head turns; the caches bf16 [pages, kv_heads,
     page_size, D].  Returns the turned q, bf16 [T, q_heads, D]."""
-    lay = _cache(k_cache, "k_cache")
-    _cache(v_cache, "v_cache", k_cache)
-    T, Hq, D = q.shape
-    kinds = (q.dtype,) if q.dtype in (torch.float32, torch.bfloat16) else (torch.float32, torch.bfloat16)
-    qs, kv = _tokens(q, kinds, "q", (Hq, lay.head_dim)), (lay.kv_heads, lay.head_dim)
-    ks, vs = _tokens(k, kinds, "k", kv), _tokens(v, kinds, "v", kv)
+    lay = _caches(k_cache, v_cache, "k_cache", "v_cache")
+    D, Hk, kind = lay.head_dim, lay.kv_heads, q.dtype
+    if kind not in (torch.float32, torch.bfloat16):
+        raise TypeError("q must be float32 or bfloat16")
+    qs, ks, vs = _tokens(q, kind, "q", None, D), _tokens(k, kind, "k", Hk, D), _tokens(v, kind, "v", Hk, D)
+    T, Hq = q.shape[:2]
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("q, k and v must hold the same number of tokens")
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     _covers(positions=(positions, T), slots=(slots, T), q_out=(q_out, T * Hq * D))
     _check("tern_rope_append", lib().tern_rope_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), 1 if q.dtype == torch.float32 else 0, qs, ks, vs,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), 1 if kind == torch.float32 else 0, qs, ks, vs,
         _dev(positions, torch.int32, "positions"), _dev(slots, torch.int64, "slots"),
         _dev(inv_freq, torch.float32, "inv_freq"), attn_factor, 2 * inv_freq.numel(), 1 if interleaved else 0, T, Hq,
         _dev(q_out, torch.bfloat16, "q_out"), k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay),
@@ -580,7 +599,7 @@ def paged_attention_workspace_bytes(B: int, T: int, max_new: int, q_heads: int, 
 
 def _sequences(q, lay, table, lens, q_start, max_new):
     """(token stride, T, q_heads, B, table width, q_start pointer, max_new)."""
-    qs = _tokens(q, (torch.bfloat16,), "q", (q.shape[1], lay.head_dim) if q.dim() == 3 else None)
+    qs = _tokens(q, torch.bfloat16, "q", None, lay.head_dim)
     T, Hq = q.shape[:2]
     if table.dim() != 2:
         raise ValueError("table must be [B, pages per sequence]")
@@ -603,8 +622,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     each) with max_new, the most tokens of one sequence (T if not given);
     scale 1/sqrt(D) if not given; window 0 or the number of last keys a query
     sees.  Returns out bf16 [T, q_heads, D]; lse fp32 [T, q_heads] if given."""
-    lay = _cache(k_cache, "k_cache")
-    _cache(v_cache, "v_cache", k_cache)
+    lay = _caches(k_cache, v_cache, "k_cache", "v_cache")
     qs, T, Hq, B, W, start, max_new = _sequences(q, lay, table, lens, q_start, max_new)
     D = lay.head_dim
     if out is None:
@@ -630,7 +648,7 @@ def attention_mass(q: torch.Tensor, k_cache: torch.Tensor, table: torch.Tensor, 
     to its running mass: out = decay * mass + sum exp(s - lse), fp32 [pages,
     kv_heads, page_size]; out defaults to mass itself.  The other arguments as
     paged_attention's, lse its output."""
-    lay = _cache(k_cache, "k_cache")
+    lay = _caches(k_cache, None, "k_cache", "")
     qs, T, Hq, B, W, start, max_new = _sequences(q, lay, table, lens, q_start, max_new)
     if out is None:
         out = mass
@@ -653,11 +671,10 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor
     heaviest before them, and moves them (K, V and mass) to the pages
     dst_table of the destination arrays.  Returns (keep int32 [B, kv_heads,
     budget], the kept keys' old indices with -1 past the last, and the new
-    lengths int32 [B])."""
-    lay = _cache(k_cache, "k_cache")
-    _cache(v_cache, "v_cache", k_cache)
-    dlay = _cache(dst_k, "dst_k")
-    _cache(dst_v, "dst_v", dst_k)
+    lengths int32 [B]).  The call needs no workspace; `ws` is accepted as by the
+    other calls and left alone."""
+    lay = _caches(k_cache, v_cache, "k_cache", "v_cache")
+    dlay = _caches(dst_k, dst_v, "dst_k", "dst_v")
     if table.dim() != 2 or dst_table.dim() != 2 or dst_table.shape[0] != table.shape[0]:
         raise ValueError("table and dst_table must be [B, pages per sequence]")
     B, H = table.shape[0], lay.kv_heads
@@ -667,12 +684,10 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor
         dst_lens = torch.empty(B, dtype=torch.int32, device=mass.device)
     _covers(mass=(mass, lay.pages * H * lay.page_size), lens=(lens, B), keep=(keep, B * H * budget),
             dst_mass=(dst_mass, dlay.pages * dlay.kv_heads * dlay.page_size), dst_lens=(dst_lens, B))
-    if ws is None:
-        ws = workspace(int(lib().tern_cache_evict_workspace_bytes(B, H, table.shape[1] * lay.page_size)), mass.device)
     _check("tern_cache_evict", lib().tern_cache_evict(
         k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay), _dev(mass, torch.float32, "mass"),
         _dev(table, torch.int32, "table"), table.shape[1], _dev(lens, torch.int32, "lens"), B, budget, recent,
         dst_k.data_ptr(), dst_v.data_ptr(), ctypes.addressof(dlay), _dev(dst_mass, torch.float32, "dst_mass"),
         _dev(dst_table, torch.int32, "dst_table"), dst_table.shape[1], _dev(keep, torch.int32, "keep"),
-        _dev(dst_lens, torch.int32, "dst_lens"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _dev(dst_lens, torch.int32, "dst_lens"), _stream(stream)))
     return keep, dst_lens

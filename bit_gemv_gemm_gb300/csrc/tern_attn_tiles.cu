@@ -64,7 +64,6 @@ struct Cfg {
     // 384 x 168, what the CTA was launched with
     static constexpr int kThreads = NS == 2 ? 384 : 256;
     static constexpr uint32_t kS = 0, kO = 256;             // tensor memory: S (and P) at 128 b, O at kO + D s
-    static constexpr size_t kSmemQ = 0;
     static constexpr size_t kSmemRing = (size_t)NS * NC * kChunk;
     static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
     // barriers: full[slots], empty[slots], then pairs: q_full, q_empty, s_full,

@@ -3,25 +3,46 @@
 // of those before them, the ones with the largest mass, `budget` in all; the
 // kept keys move, in order, to pages of their own.
 //
-// Selection (one CTA a sequence and head) finds the smallest kept mass by
-// radix selection over the masses as ordered 32-bit integers, a byte a pass
-// from the highest, and then writes the kept indices with a running count, so
-// equal masses go to the lowest index.  The move is a copy, 16 bytes a thread.
+// One cluster of up to eight CTAs a sequence and head; a CTA takes an equal
+// part of the keys and keeps their masses in shared memory, as integers of the
+// same order, so the cache's masses are read once.
+//   * The smallest kept mass is found by radix selection from the top, a byte a
+//     pass: each CTA counts its keys by digit, every CTA adds the cluster's histograms
+//     through distributed shared memory, a thread a digit, and finds the one that
+//     the selection ends in.  (11 bits a pass, three passes, moved eight times
+//     the words between the SMs, at 10 us a pass.)
+//   * From the CTAs' and warps' counts every warp knows where its kept keys begin
+//     in the result (equal masses go to the lowest index) and lists them there.
+//   * The list is then copied, each CTA an equal part of it: K, V and mass, 16
+//     bytes a thread, the rows of two keys in flight a thread and the places of
+//     the next two looked up meanwhile.
+// Bound by the copy: each kept key's rows are read and written once.  A CTA is a
+// chain of waits (lengths, masses, six cluster barriers, table, rows), so four
+// share an SM, and the clusters are as large as lets all CTAs run at once:
+// sixteen sequences of 20000 keys cut to 4096, eight heads, take 365 us with one
+// CTA an SM, 181 with four in clusters of eight (two waves).
+#include <cooperative_groups.h>
+
 #include "tern_cache.cuh"
 
 namespace tern {
 namespace {
 
+namespace cg = cooperative_groups;
+
 __device__ int g_evict_error;
 
-constexpr int kSelThreads = 1024;
+constexpr int kMaxCluster = 8, kThreads = 256, kWarps = kThreads / 32, kCtas = 4;   // an SM
+constexpr int kBits = 8, kBins = 1 << kBits;
+constexpr int kMaxHeld = 40 * 1024;          // masses a CTA holds; longer shares are read again each pass
+constexpr int kSmallHeld = 10 * 1024;        // so many leave room for kCtas CTAs
 
 struct EvictArgs {
     const __nv_bfloat16 *k, *v;
     CacheView c;
     const float* mass;
     const int *table, *lens;
-    int width, B, budget, recent;
+    int width, B, budget, recent, held;      // held: masses that shared memory has room for
     __nv_bfloat16 *dk, *dv;
     CacheView dc;
     float* dmass;
@@ -38,108 +59,206 @@ __device__ __forceinline__ uint32_t order_of(float m) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int evict_len(const EvictArgs& a, int b) {
-    const int len = a.lens[b];
-    const long long room = (long long)a.width * a.c.page_size;
-    const int cut = (int)min((long long)max(len, 0), room);
-    if (cut != len) report_device_error(&g_evict_error, TERN_DEVERR_CACHE_SEQUENCE);
-    return cut;
-}
-__device__ __forceinline__ float mass_at(const EvictArgs& a, int b, int hk, int j) {
-    const int page = checked_page(a.table[(long long)b * a.width + j / a.c.page_size], a.c.pages, &g_evict_error);
-    return a.mass[((long long)page * a.c.kv_heads + hk) * a.c.page_size + j % a.c.page_size];
-}
+struct Way {   // where a key's rows and mass lie, and where they go
+    long long from, to, mass, dmass;
+};
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int pick[2];
-    __shared__ int warp_gt[32], warp_eq[32];
+struct Shared {
+    int hist[2][kBins];          // by pass parity: a CTA may be counting while another still reads
+    int counts[2];               // of this CTA's keys: above the smallest kept mass, equal to it
+    int warp_a[kWarps], warp_b[kWarps];   // the same by warp
+    int digit, above;
+};
+
+__global__ void __launch_bounds__(kThreads, kCtas)
+evict_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t held[];       // ordered masses of this CTA's keys
+    __shared__ Shared sm;
+    cg::cluster_group cluster = cg::this_cluster();
     pdl_launch_dependents();
     pdl_wait();
-    const int b = blockIdx.y, hk = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int len = evict_len(a, b), kept = min(len, a.budget), recent = min(a.recent, kept);
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int item = blockIdx.x / ctas, b = item / a.c.kv_heads, hk = item % a.c.kv_heads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int len = a.lens[b];
+    {
+        const long long room = (long long)a.width * a.c.page_size;
+        const int cut = (int)min((long long)max(len, 0), room);
+        if (cut != len && tid == 0) report_device_error(&g_evict_error, TERN_DEVERR_CACHE_SEQUENCE);
+        len = cut;
+    }
+    const int kept = min(len, a.budget), recent = min(a.recent, kept);
     const int cand = len - recent, want = kept - recent;   // the first `cand` keys give `want`
+    const int per = (len + ctas - 1) / ctas;
+    const int j_lo = min(rank * per, len), j_hi = min(j_lo + per, len), n = max(min(j_hi, cand) - j_lo, 0);
+    const int* trow = a.table + (long long)b * a.width;
+    auto page_of = [&](int j) {
+        return checked_page(trow[(unsigned)j / (unsigned)a.c.page_size], a.c.pages, &g_evict_error);
+    };
+    auto mass_index = [&](int page, int j) {
+        return ((long long)page * a.c.kv_heads + hk) * a.c.page_size + (unsigned)j % (unsigned)a.c.page_size;
+    };
+    auto ordered = [&](int x) {   // candidate x of this CTA
+        return x < a.held ? held[x] : order_of(a.mass[mass_index(page_of(j_lo + x), j_lo + x)]);
+    };
     int* keep = a.keep + ((long long)b * a.c.kv_heads + hk) * a.budget;
-    if (hk == 0 && tid == 0) a.dlens[b] = kept;
-    for (int i = want + tid; i < a.budget; i += kSelThreads) keep[i] = i < kept ? cand + i - want : -1;
+    if (rank == 0) {
+        if (hk == 0 && tid == 0) a.dlens[b] = kept;
+        for (int i = kept + tid; i < a.budget; i += kThreads) keep[i] = -1;
+    }
+
     uint32_t prefix = 0;
     int left = want;   // to be taken among the keys that share the prefix
-    if (want > 0 && want < cand) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    const bool choose = want > 0 && want < cand;
+    if (choose) {
+#pragma unroll 4
+        for (int x = tid; x < min(n, a.held); x += kThreads)
+            held[x] = order_of(a.mass[mass_index(page_of(j_lo + x), j_lo + x)]);
+#pragma unroll 1
+        for (int shift = 32 - kBits, pass = 0; shift >= 0; shift -= kBits, ++pass) {
+            const uint32_t known = pass == 0 ? 0u : 0xffffffffu << (shift + kBits);
+            int* hist = sm.hist[pass & 1];
+            for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
             __syncthreads();
-            for (int j = tid; j < cand; j += kSelThreads) {
-                const uint32_t u = order_of(mass_at(a, b, hk, j));
-                if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(u >> shift) & 255], 1);
+#pragma unroll 4
+            for (int x = tid; x < n; x += kThreads) {
+                const uint32_t u = ordered(x);
+                if ((u & known) == (prefix & known)) atomicAdd(&hist[(u >> shift) & (uint32_t)(kBins - 1)], 1);
+            }
+            cluster.sync();
+            // digits from the top, one a thread; the running sum says which of them the selection ends in
+            int own = 0;
+            if (tid < kBins)
+#pragma unroll kMaxCluster
+                for (int r = 0; r < ctas; ++r) own += cluster.map_shared_rank(hist, r)[kBins - 1 - tid];
+            int x = own;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, k);
+                if (lane >= k) x += y;
+            }
+            if (lane == 31) sm.warp_a[warp] = x;
+            __syncthreads();
+            int before = x - own;
+            for (int w = 0; w < warp; ++w) before += sm.warp_a[w];
+            if (tid < kBins && before < left && before + own >= left) {
+                sm.digit = kBins - 1 - tid;
+                sm.above = before;
             }
             __syncthreads();
-            if (tid == 0) {
-                int above = 0, d = 255;
-                while (d > 0 && above + hist[d] < left) above += hist[d--];
-                pick[0] = d;
-                pick[1] = above;
-            }
-            __syncthreads();
-            prefix |= (uint32_t)pick[0] << shift;
-            left -= pick[1];
-            __syncthreads();
+            prefix |= (uint32_t)sm.digit << shift;
+            left -= sm.above;
         }
     } else {
-        left = cand;   // all of them, or none
+        left = want > 0 ? cand : 0;   // all of them, or none
     }
-    if (want == 0) return;
-    const bool all = want >= cand;
-    int gt0 = 0, eq0 = 0;
-    for (int base = 0; base < cand; base += kSelThreads) {
-        const int j = base + tid;
-        bool gt = false, eq = false;
-        if (j < cand) {
-            const uint32_t u = all ? 0u : order_of(mass_at(a, b, hk, j));
-            gt = !all && u > prefix;
-            eq = all || u == prefix;
-        }
-        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            warp_gt[warp] = __popc(mg);
-            warp_eq[warp] = __popc(me);
-        }
-        __syncthreads();
-        int g = gt0, e = eq0;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) {
-                g += warp_gt[w];
-                e += warp_eq[w];
-            }
-            gt0 += warp_gt[w];
-            eq0 += warp_eq[w];
-        }
-        g += __popc(mg & ((1u << lane) - 1u));
-        e += __popc(me & ((1u << lane) - 1u));
-        if (gt || (eq && e < left)) keep[g + min(e, left)] = j;
-        __syncthreads();
-    }
-}
 
-// One warp a kept key of one head.
-__global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int b = blockIdx.z, hk = blockIdx.y, lane = threadIdx.x & 31, D = a.c.head_dim;
-    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < a.budget; i += gridDim.x * 8) {
-        const int j = a.keep[((long long)b * a.c.kv_heads + hk) * a.budget + i];
-        if (j < 0) return;
-        const int page = checked_page(a.table[(long long)b * a.width + j / a.c.page_size], a.c.pages, &g_evict_error);
-        const int dpage = checked_page(a.dtable[(long long)b * a.dwidth + i / a.dc.page_size], a.dc.pages, &g_evict_error);
-        const int slot = j % a.c.page_size, dslot = i % a.dc.page_size;
+    // how many of this warp's candidates (a run of its own) are above the smallest kept mass, and equal to it
+    const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, x_lo = min(warp * run, n), x_hi = min(x_lo + run, n);
+    int gt = 0, eq = 0;
+    if (choose) {
+#pragma unroll 4
+        for (int x = x_lo + lane; x < x_hi; x += 32) {
+            const uint32_t u = ordered(x);
+            gt += u > prefix;
+            eq += u == prefix;
+        }
+#pragma unroll
+        for (int k = 16; k; k >>= 1) {
+            gt += __shfl_xor_sync(0xffffffffu, gt, k);
+            eq += __shfl_xor_sync(0xffffffffu, eq, k);
+        }
+    } else {
+        eq = x_hi - x_lo;
+    }
+    __syncthreads();   // warp_a has been read
+    if (lane == 0) {
+        sm.warp_a[warp] = gt;
+        sm.warp_b[warp] = eq;
+    }
+    __syncthreads();
+    int gt_before = 0, eq_before = 0;
+    {
+        int g = 0, e = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) {
+                gt_before = g;
+                eq_before = e;
+            }
+            g += sm.warp_a[w];
+            e += sm.warp_b[w];
+        }
+        if (tid == 0) {
+            sm.counts[0] = g;
+            sm.counts[1] = e;
+        }
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+        const int* c = cluster.map_shared_rank(sm.counts, r);
+        gt_before += c[0];
+        eq_before += c[1];
+    }
+    // the list: this warp's kept candidates, then the recent keys of this CTA's part
+    if (want > 0)
+        for (int x0 = x_lo; x0 < x_hi; x0 += 32) {
+            const int x = x0 + lane;
+            const uint32_t u = choose && x < x_hi ? ordered(x) : 0u;
+            const bool is_gt = choose && x < x_hi && u > prefix, is_eq = x < x_hi && (!choose || u == prefix);
+            const unsigned mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
+            const unsigned under = (1u << lane) - 1u;
+            const int g = gt_before + __popc(mg & under), e = eq_before + __popc(me & under);
+            if (is_gt || (is_eq && e < left)) keep[g + min(e, left)] = j_lo + x;
+            gt_before += __popc(mg);
+            eq_before += __popc(me);
+        }
+    for (int j = max(j_lo, cand) + tid; j < j_hi; j += kThreads) keep[want + j - cand] = j;
+    __threadfence();
+    cluster.sync();   // the whole list is written (and this CTA's counts have been read)
+
+    auto way = [&](int j, int i) {
+        const int page = page_of(j), dpage = checked_page(a.dtable[(long long)b * a.dwidth + (unsigned)i / (unsigned)a.dc.page_size],
+                                                           a.dc.pages, &g_evict_error);
+        const int slot = (unsigned)j % (unsigned)a.c.page_size, dslot = (unsigned)i % (unsigned)a.dc.page_size;
         const long long from = page * a.c.page_stride + hk * a.c.head_stride + slot * a.c.slot_stride;
         const long long to = dpage * a.dc.page_stride + hk * a.dc.head_stride + dslot * a.dc.slot_stride;
-        for (int d = lane * 8; d < D; d += 256) {
-            *reinterpret_cast<uint4*>(a.dk + to + d) = *reinterpret_cast<const uint4*>(a.k + from + d);
-            *reinterpret_cast<uint4*>(a.dv + to + d) = *reinterpret_cast<const uint4*>(a.v + from + d);
+        return Way{from, to, mass_index(page, j), ((long long)dpage * a.dc.kv_heads + hk) * a.dc.page_size + dslot};
+    };
+    // keys i_lo .. i_hi - 1 of the list; threads in groups of `lanes` (D / 8, at most 32) a row
+    const int part = (kept + ctas - 1) / ctas, i_lo = min(rank * part, kept), i_hi = min(i_lo + part, kept);
+    const int D = a.c.head_dim, lanes = D >= 256 ? 32 : D > 64 ? 16 : 8, groups = kThreads / lanes;
+    const int l0 = tid % lanes * 8;
+    int i = i_lo + tid / lanes;
+    if (i >= i_hi) return;
+    auto place = [&](int x) { return way(__ldcg(keep + min(x, i_hi - 1)), min(x, i_hi - 1)); };
+    Way p = place(i), q = place(i + groups);
+    for (; i < i_hi; i += 2 * groups) {
+        const bool two = i + groups < i_hi, more = i + 2 * groups < i_hi;
+        const Way p0 = p, q0 = q;
+        for (int d = l0; d < D; d += lanes * 8) {
+            const uint4 k0 = __ldcs(reinterpret_cast<const uint4*>(a.k + p0.from + d));
+            const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(a.v + p0.from + d));
+            const uint4 k1 = __ldcs(reinterpret_cast<const uint4*>(a.k + q0.from + d));
+            const uint4 v1 = __ldcs(reinterpret_cast<const uint4*>(a.v + q0.from + d));
+            if (d == l0 && more) {
+                p = place(i + 2 * groups);
+                q = place(i + 3 * groups);
+            }
+            *reinterpret_cast<uint4*>(a.dk + p0.to + d) = k0;
+            *reinterpret_cast<uint4*>(a.dv + p0.to + d) = v0;
+            if (two) {
+                *reinterpret_cast<uint4*>(a.dk + q0.to + d) = k1;
+                *reinterpret_cast<uint4*>(a.dv + q0.to + d) = v1;
+            }
         }
-        if (lane == 0)
-            a.dmass[((long long)dpage * a.dc.kv_heads + hk) * a.dc.page_size + dslot] =
-                a.mass[((long long)page * a.c.kv_heads + hk) * a.c.page_size + slot];
+        if (l0 >= D && more) {   // a lane past the row's end
+            p = place(i + 2 * groups);
+            q = place(i + 3 * groups);
+        }
+        if (l0 == 0) {
+            a.dmass[p0.dmass] = a.mass[p0.mass];
+            if (two) a.dmass[q0.dmass] = a.mass[q0.mass];
+        }
     }
 }
 
@@ -156,17 +275,11 @@ cudaError_t read_evict_device_error(int* code) {
 
 using namespace tern;
 
-extern "C" size_t tern_cache_evict_workspace_bytes(int B, int kv_heads, int max_keys) {
-    if (B < 1 || kv_heads < 1 || max_keys < 0) return 0;
-    return 256;
-}
-
 extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache, const tern_cache_layout* layout,
                                         const float* mass, const int* table, int table_width, const int* lens, int B,
                                         int budget, int recent, void* dst_k, void* dst_v,
                                         const tern_cache_layout* dst_layout, float* dst_mass, const int* dst_table,
-                                        int dst_table_width, int* keep, int* dst_lens, void* workspace,
-                                        size_t workspace_bytes, tern_stream_t stream) {
+                                        int dst_table_width, int* keep, int* dst_lens, tern_stream_t stream) {
     set_launch_count(0);
     EvictArgs a;
     tern_status st = make_cache_view(layout, &a.c);
@@ -174,7 +287,8 @@ extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache
     if (st != TERN_OK) return st;
     if (a.c.kv_heads != a.dc.kv_heads || a.c.head_dim != a.dc.head_dim || B < 1 || B > 65535 || table_width < 1 ||
         dst_table_width < 1 || budget < 1 || recent < 0 || recent > budget ||
-        (long long)dst_table_width * a.dc.page_size < budget || (long long)table_width * a.c.page_size > 0x7fffffffLL)
+        (long long)dst_table_width * a.dc.page_size < budget || (long long)table_width * a.c.page_size > 0x7fffffffLL ||
+        (long long)B * a.c.kv_heads > 0x7fffffffLL / kMaxCluster)
         return TERN_ERR_SHAPE;
     if (!k_cache || !v_cache || !mass || !table || !lens || !dst_k || !dst_v || !dst_mass || !dst_table || !keep ||
         !dst_lens)
@@ -183,11 +297,8 @@ extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache
         !aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(dst_mass, 4) || !aligned_to(dst_table, 4) ||
         !aligned_to(keep, 4) || !aligned_to(dst_lens, 4))
         return TERN_ERR_ALIGN;
-    if (!workspace ||
-        workspace_bytes < tern_cache_evict_workspace_bytes(B, a.c.kv_heads, table_width * a.c.page_size))
-        return TERN_ERR_WORKSPACE;
-    if (!aligned_to(workspace, 256)) return TERN_ERR_ALIGN;
-    st = check_device(nullptr);
+    int sms = 0;
+    st = check_device(&sms);
     if (st != TERN_OK) return st;
     a.k = static_cast<const __nv_bfloat16*>(k_cache);
     a.v = static_cast<const __nv_bfloat16*>(v_cache);
@@ -205,13 +316,33 @@ extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache
     a.dwidth = dst_table_width;
     a.keep = keep;
     a.dlens = dst_lens;
-    if (launch_pdl(select_kernel, dim3(a.c.kv_heads, B), dim3(kSelThreads), 0, (cudaStream_t)stream, true, a) !=
-        cudaSuccess)
-        return TERN_ERR_CUDA;
-    const int grid = (budget + 31) / 32 < 1024 ? (budget + 31) / 32 : 1024;
-    if (launch_pdl(move_kernel, dim3(grid, a.c.kv_heads, B), dim3(256), 0, (cudaStream_t)stream, true, a) !=
-        cudaSuccess)
-        return TERN_ERR_CUDA;
-    set_launch_count(2);
+    const long long room = (long long)table_width * a.c.page_size, items = (long long)B * a.c.kv_heads;
+    int ctas = kMaxCluster;
+    while (ctas > 1 && items * ctas > (long long)kCtas * sms && room / (ctas / 2) <= kSmallHeld) ctas /= 2;
+    const long long share = (room + ctas - 1) / ctas;
+    a.held = (int)(share < kMaxHeld ? share : kMaxHeld);
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TERN_ERR_CUDA;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 4) != cudaSuccess)
+            return TERN_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)a.held * 4;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, evict_kernel, a) != cudaSuccess) return TERN_ERR_CUDA;
+    set_launch_count(1);
     return TERN_OK;
 }

@@ -481,13 +481,12 @@ tern_status tern_attention_mass(const void *q, long long q_stride, const void *k
  * [B][dst_table_width]) of the destination cache, which may be the same arrays
  * as long as no destination page is one that the call reads; keep (int32
  * [B][kv_heads][budget]) gets their old indices, ascending, -1 past the last,
- * and dst_lens (int32 [B]) the new lengths.  Two kernel launches. */
-size_t tern_cache_evict_workspace_bytes(int B, int kv_heads, int max_keys);
+ * and dst_lens (int32 [B]) the new lengths.  One kernel launch, no workspace. */
 tern_status tern_cache_evict(const void *k_cache, const void *v_cache, const tern_cache_layout *layout,
                              const float *mass, const int *table, int table_width, const int *lens, int B, int budget,
                              int recent, void *dst_k, void *dst_v, const tern_cache_layout *dst_layout,
                              float *dst_mass, const int *dst_table, int dst_table_width, int *keep, int *dst_lens,
-                             void *workspace, size_t workspace_bytes, tern_stream_t stream);
+                             tern_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */

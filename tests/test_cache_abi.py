@@ -86,19 +86,17 @@ def test_mass_refuses_arguments(tern, bad, code):
 
 def evict(tern, lay=None, dlay=None, **k):
     a = dict(k=P, v=P, mass=P, table=P, width=100, lens=P, B=2, budget=100, recent=10, dk=P, dv=P, dm=P, dt=P, dw=7,
-             keep=P, dl=P, ws=P, n=1 << 24)
+             keep=P, dl=P)
     a.update(k)
     lay, dlay = lay or layout(tern), dlay or layout(tern)
     return tern.lib().tern_cache_evict(a["k"], a["v"], ctypes.addressof(lay), a["mass"], a["table"], a["width"],
                                        a["lens"], a["B"], a["budget"], a["recent"], a["dk"], a["dv"],
-                                       ctypes.addressof(dlay), a["dm"], a["dt"], a["dw"], a["keep"], a["dl"], a["ws"],
-                                       a["n"], None)
+                                       ctypes.addressof(dlay), a["dm"], a["dt"], a["dw"], a["keep"], a["dl"], None)
 
 
 @pytest.mark.parametrize("bad,code", [(dict(budget=0), SHAPE), (dict(recent=101), SHAPE), (dict(recent=-1), SHAPE),
                                       (dict(dw=6), SHAPE), (dict(B=0), SHAPE), (dict(width=1 << 28), SHAPE),
-                                      (dict(keep=None), NULL), (dict(dm=None), NULL), (dict(dk=P + 8), ALIGN),
-                                      (dict(ws=None), WORKSPACE), (dict(n=1), WORKSPACE)])
+                                      (dict(keep=None), NULL), (dict(dm=None), NULL), (dict(dk=P + 8), ALIGN)])
 def test_evict_refuses_arguments(tern, bad, code):
     assert evict(tern, **bad) == code
 
