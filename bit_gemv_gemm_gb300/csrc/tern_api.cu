@@ -89,7 +89,8 @@ tern_status tern_device_error(int* code) {
     cudaError_t (*const readers[])(int*) = {read_gemm_device_error, read_gemv_device_error, read_f3_device_error,
                                             read_rope_device_error, read_mass_rows_device_error,
                                             read_mass_tiles_device_error, read_attn_rows_device_error,
-                                            read_attn_tiles_device_error, read_evict_device_error};
+                                            read_attn_tiles_device_error,
+                                            read_attn_pairs_device_error, read_evict_device_error};
     for (auto* read : readers) {
         int c = 0;
         if (read(&c) != cudaSuccess) return TERN_ERR_CUDA;

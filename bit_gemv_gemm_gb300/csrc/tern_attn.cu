@@ -40,7 +40,7 @@ extern "C" size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new
     if (B < 1 || T < 0 || max_new < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return kAttnCounterBytes + std::max(attn_rows_workspace(), attn_tiles_workspace());
+    return kAttnCounterBytes + std::max({attn_rows_workspace(), attn_tiles_workspace(), attn_pairs_workspace()});
 }
 
 extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, const void* k_cache,
@@ -81,9 +81,11 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     // few rows: bound by reading the cache and by latency, which suits mma.sync
     // and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
     // 32k keys, 4 sequences: 106 us, against 115 from the rows kernel with 32 rows an item)
-    const bool few = rows <= 16;
-    const cudaError_t e = few ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                              : launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream);
+    // and, past one row tile, pairs of CTAs with a row tile each
+    const cudaError_t e = rows <= 16 ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
+                          : a.s.max_new <= 128 / a.group
+                              ? launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream)
+                              : launch_attn_pairs(a, k_cache, v_cache, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

@@ -115,8 +115,9 @@ __device__ __forceinline__ void next_item(const SeqView& sv, const CacheView& cv
     } while (t.units == 0);
 }
 
-// This CTA's share [w0, w1) of all units, and the item that holds w0; P shares
-// of at least min_units each.  Called by all THREADS threads; false: no share.
+// Share `share` of at most `shares`, [w0, w1) of all units, and the item that
+// holds w0; P shares of at least min_units each.  Called by all THREADS threads
+// of a CTA; false: no share.
 // `sm`: 8 + THREADS / 32 words of shared memory.
 //
 // A call begins with this, so its latency counts (one token over 500 keys: a
@@ -125,7 +126,7 @@ __device__ __forceinline__ void next_item(const SeqView& sv, const CacheView& cv
 // divisions are 32-bit ones where the numbers allow (a 64-bit one is a loop).
 template <int THREADS, typename Extent>
 __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent& extent, int tiles, int min_units,
-                           long long* sm, int* err, long long& total, int& P, long long& w0, long long& w1, Item& t) {
+                           int share, int shares, long long* sm, int* err, long long& total, int& P, long long& w0, long long& w1, Item& t) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = cv.kv_heads;
     const long long all = (long long)sv.B * tiles;
     const long long per = all <= THREADS ? 1 : (all + THREADS - 1) / THREADS;
@@ -157,10 +158,10 @@ __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent&
     }
     const long long most = total <= 0x7fffffff ? ((unsigned)total + min_units - 1) / (unsigned)min_units
                                                : (total + min_units - 1) / min_units;
-    P = (int)min((long long)gridDim.x, most);
-    if ((int)blockIdx.x >= P) return false;
-    w0 = unit_begin(total, P, blockIdx.x);
-    w1 = unit_begin(total, P, blockIdx.x + 1);
+    P = (int)min((long long)shares, most);
+    if (share >= P) return false;
+    w0 = unit_begin(total, P, share);
+    w1 = unit_begin(total, P, share + 1);
     if (w0 >= before && w0 < before + mine) {
         long long at = before;
         for (long long f = f0; f < f1; ++f) {
@@ -218,6 +219,17 @@ __device__ __forceinline__ void tma_load_cache(uint32_t dst, const CUtensorMap* 
         "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
         "[%7];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(slot), "r"(chunk), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+// The same into both CTAs of a pair: the same place of each's shared memory, the
+// same barrier of each.
+__device__ __forceinline__ void tma_load_cache_pair(uint32_t dst, const CUtensorMap* m, int slot, int chunk, int head,
+                                                    int page, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
+        "%3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(slot), "r"(chunk), "r"(head), "r"(page), "r"(bar),
+        "h"((unsigned short)3)
         : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -297,6 +309,106 @@ __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* m, i
 }
 
 // Launchers of the kernels (each checks nothing: the entry point has).
+// A row tile's results: parts are exchanged four columns at a time, [column /
+// 4][row][4], then (m, l) by row.
+constexpr int kTileRows = 128;
+constexpr size_t part_floats(int D) { return (size_t)kTileRows * (D + 2); }
+
+// The output of one row (a thread; `load(c, o)` gives 32 columns of its
+// accumulator): to memory, divided by the sum, or into `part`.
+template <int D, typename Load>
+__device__ __forceinline__ void emit_row(const AttnArgs& a, bool whole, float* part, int row, bool live, long long orow,
+                                         float m2, float l, Load load) {
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        load(c, o);   // (a whole warp's)
+        if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
+                dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                __stcg(reinterpret_cast<uint4*>(part + ((size_t)(c / 4 + e) * kTileRows + row) * 4),
+                       make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+        }
+    }
+    if (whole && live && a.lse) a.lse[orow] = l > 0.0f ? (m2 + log2f(l)) * 0.693147180559945309f : -INFINITY;
+    if (!whole) __stcg(reinterpret_cast<float2*>(part + (size_t)D * kTileRows + 2 * row), make_float2(m2, l));
+}
+
+// A warp has stored its 32 rows' part; the one that counts last into the
+// item's counter adds the parts of all shares, in their order.  `counter` and
+// `first` are those of the row tile in share 0; a share has two parts, `stride`
+// floats apart.
+template <int D, int COST>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, unsigned* counter, const float* first,
+                                           size_t stride, int row, bool live, long long orow, long long total, int P) {
+    __threadfence();
+    __syncwarp();
+    const int c_lo = unit_owner(total, P, t.at + COST), c_hi = unit_owner(total, P, t.at + t.units - 1);
+    unsigned last = 0;
+    if ((threadIdx.x & 31) == 0)
+        last = atomicInc(counter + 8 * c_lo, (unsigned)(c_hi - c_lo)) == (unsigned)(c_hi - c_lo);
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    // (an item's first share may have begun before it: its part is then in its second slot)
+    const int late = unit_begin(total, P, c_lo) >= t.at ? 0 : 1;
+    auto part_of = [&](int x) { return first + (size_t)(2 * x + (x == c_lo ? late : 0)) * stride; };
+    auto stat_of = [&](int x) {
+        return __ldcg(reinterpret_cast<const float2*>(part_of(x) + (size_t)D * kTileRows + 2 * row));
+    };
+    // no branch in these loops: all the loads of a few parts are in flight together
+    float mm = -INFINITY, ll = 0.0f;
+#pragma unroll 4
+    for (int x = c_lo; x <= c_hi; ++x) mm = fmaxf(mm, stat_of(x).x);
+    const float base = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll 4
+    for (int x = c_lo; x <= c_hi; ++x) {
+        const float2 st = stat_of(x);
+        ll += st.y * exp2_fast(st.x - base);
+    }
+    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        float y[32] = {};
+#pragma unroll 3
+        for (int x = c_lo; x <= c_hi; ++x) {
+            const float f = exp2_fast(stat_of(x).x - base);
+            float4 v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + ((size_t)(c / 4 + e) * kTileRows + row) * 4));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
+                y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
+                y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
+                y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
+            }
+        }
+        if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dst[e] = make_uint4(pack_bf16(y[8 * e] * inv, y[8 * e + 1] * inv),
+                                    pack_bf16(y[8 * e + 2] * inv, y[8 * e + 3] * inv),
+                                    pack_bf16(y[8 * e + 4] * inv, y[8 * e + 5] * inv),
+                                    pack_bf16(y[8 * e + 6] * inv, y[8 * e + 7] * inv));
+        }
+    }
+    if (live && a.lse) a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
+}
+
 struct MassArgs {
     const __nv_bfloat16* q;
     long long q_stride;
@@ -317,7 +429,9 @@ cudaError_t launch_mass_rows(const MassArgs& a, const void* k, int sms, cudaStre
 cudaError_t launch_mass_tiles(const MassArgs& a, const void* k, int sms, cudaStream_t stream);
 cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
+cudaError_t launch_attn_pairs(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 size_t attn_rows_workspace();
 size_t attn_tiles_workspace();
+size_t attn_pairs_workspace();
 
 }  // namespace tern

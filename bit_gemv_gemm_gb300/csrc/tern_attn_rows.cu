@@ -85,7 +85,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     long long total, w0, w1;
     Item t;
     const RowTileExtent<kStrip, kItemCost> extent{R, a.group, a.window};
-    if (!find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinUnits, sm_scan, &g_attn_rows_error, total, P, w0, w1, t))
+    if (!find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinUnits, (int)blockIdx.x, (int)gridDim.x, sm_scan, &g_attn_rows_error, total, P, w0, w1, t))
         return;
 
     uint32_t it = 0;   // strips this warp has fetched and used, over all segments

@@ -136,7 +136,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     long long total, w0, w1;
     Item t;
     const RowTileExtent<kKeys, kItemCost> extent{R, a.group, a.window};
-    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, sm_scan, &g_attn_tiles_error, total,
+    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, (int)blockIdx.x, (int)gridDim.x, sm_scan, &g_attn_tiles_error, total,
                                               P, w0, w1, t);
     auto fail = [&] {
         if (!*abort_flag) {

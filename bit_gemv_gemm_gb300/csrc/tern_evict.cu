@@ -329,20 +329,9 @@ extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache
             return TERN_ERR_CUDA;
         attr_set[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)a.held * 4;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, evict_kernel, a) != cudaSuccess) return TERN_ERR_CUDA;
+    if (launch_pdl_clusters(evict_kernel, (unsigned)ctas, dim3((unsigned)(items * ctas)), dim3(kThreads),
+                            (size_t)a.held * 4, (cudaStream_t)stream, a) != cudaSuccess)
+        return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;
 }

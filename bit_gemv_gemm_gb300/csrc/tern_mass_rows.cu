@@ -79,7 +79,7 @@ mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
     long long total, w0, w1;
     Item t;
     const AllKeysExtent<kStrip> extent{a.group};
-    if (!find_share<kThreads>(a.s, a.c, extent, 1, C::kMinUnits, sm_scan, &g_mass_rows_error, total, P, w0, w1, t)) return;
+    if (!find_share<kThreads>(a.s, a.c, extent, 1, C::kMinUnits, (int)blockIdx.x, (int)gridDim.x, sm_scan, &g_mass_rows_error, total, P, w0, w1, t)) return;
 
     uint32_t it = 0;
     for (long long w = w0; w < w1;) {

@@ -141,7 +141,7 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     int P;
     long long total, w0, w1;
     Item t;
-    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, 1, sm_scan, &g_mass_tiles_error, total, P, w0,
+    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, 1, (int)blockIdx.x, (int)gridDim.x, sm_scan, &g_mass_tiles_error, total, P, w0,
                                               w1, t);
     // whole items: those that begin in this CTA's share
     if (busy && t.at < w0) next_item(a.s, a.c, extent, a.tiles, t, &g_mass_tiles_error);
