@@ -83,7 +83,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     // 32k keys, 4 sequences: 106 us, against 115 from the rows kernel with 32 rows an item)
     // and, past one row tile, pairs of CTAs with a row tile each
     const cudaError_t e = rows <= 16 ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                          : a.s.max_new <= 128 / a.group
+                          : a.s.max_new <= 128 / a.group || a.c.head_dim == 256
                               ? launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream)
                               : launch_attn_pairs(a, k_cache, v_cache, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;

@@ -15,8 +15,7 @@
 //     synchronous (a wait or a commit between products costs the thread about
 //     150 and 57 clocks that its own products do not cover: 110 clocks a 64-clock
 //     product from one thread), so each covers the other's;
-//   * S has three buffers (two at D = 256, where O takes half of tensor memory),
-//     so QK runs ahead, and two softmax warpgroups take the tiles in turn, one
+//   * S has three buffers, so QK runs ahead, and two softmax warpgroups take the tiles in turn, one
 //     thread a row: read S, exponentiate, write P as bf16 over S's own columns.
 // The two warpgroups share a row's maximum in use: each hands it on as soon as
 // it has looked at its tile's scores, well before it has exponentiated them.  It
@@ -49,6 +48,7 @@ constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys
 constexpr int kItemCost = 3;                // key tiles' time that an item costs besides its own
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
+constexpr int kBuffers = 3;                 // of S
 // a third warpgroup (two TMA and two MMA warps) gives registers to the softmax
 // warps, which hold a row of S each: 256 x 208 + 128 x 88 = 384 x 168, what the
 // CTA was launched with
@@ -57,14 +57,11 @@ constexpr int kThreads = 384;
 template <int D>
 struct Cfg {
     static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
-    static constexpr int CG = D == 128 ? 2 : 1;             // chunks of a ring slot
-    static constexpr int NG = NC / CG;                      // slots of a K or V tile
-    static constexpr int kSlots = D == 64 ? 12 : D == 128 ? 6 : 8;
-    static constexpr int NB = D == 256 ? 2 : 3;             // S buffers
-    static constexpr uint32_t kS = 0, kO = 128 * NB;        // tensor memory: S (and P) at 128 b, then O
+    static constexpr int kSlots = D == 64 ? 12 : 6;         // tiles of K and V, in turn
+    static constexpr uint32_t kS = 0, kO = 128 * kBuffers;  // tensor memory: S (and P) at 128 b, then O
     static constexpr size_t kSmemRing = (size_t)NC * kChunk;
-    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
-    static constexpr int kBars = 2 * kSlots + 2 + 3 * NB + 2 + 1 + 8 + 1 + 2 + 2;
+    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * NC * kChunk;
+    static constexpr int kBars = 2 * kSlots + 2 + 3 * kBuffers + 1 + 8 + 1 + 2 + 2;
     static constexpr size_t kSmemMisc = (kSmemBar + kBars * 8 + 15) / 16 * 16;
     static constexpr size_t kSmemM = kSmemMisc + 256;       // a row's maximum in use, and a warpgroup's sums
     static constexpr size_t kSmem = kSmemM + 2 * kRows * 4 + 1024;
@@ -77,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const AttnArgs a, const int box_rows) {
     using C = Cfg<D>;
-    constexpr int NC = C::NC, CG = C::CG, NG = C::NG, NB = C::NB, kSlots = C::kSlots;
+    constexpr int NC = C::NC, NB = kBuffers, kSlots = C::kSlots;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -86,9 +83,8 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     auto full_bar = [&](uint32_t i) { return bar((int)(i % kSlots)); };
     auto empty_bar = [&](uint32_t i) { return bar(kSlots + (int)(i % kSlots)); };
     auto slot_phase = [&](uint32_t i) { return (i / kSlots) & 1u; };
-    auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)(CG * kChunk); };
-    enum { Q_FULL = 2 * kSlots, Q_EMPTY, S_FULL, S_EMPTY = S_FULL + NB, P_FULL = S_EMPTY + NB, O_DONE = P_FULL + NB,
-           O_EMPTY = O_DONE + 2, HAND, MERGE = HAND + 8, TAIL, DRAIN = TAIL + 2 };   // DRAIN: two
+    auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)(NC * kChunk); };
+    enum { Q_FULL = 2 * kSlots, Q_EMPTY, S_FULL, S_EMPTY = S_FULL + NB, P_FULL = S_EMPTY + NB, O_EMPTY = P_FULL + NB, HAND, MERGE = HAND + 8, TAIL, DRAIN = TAIL + 2 };   // DRAIN: two
     static_assert(DRAIN + 2 == C::kBars, "barriers");
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm_scan + 8 + kThreads / 32);
@@ -148,7 +144,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             // ------------------------------ TMA: Q and K, or V ------------------------------
             const bool is_v = warp != kSoftWarps;
             const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-            uint32_t it = is_v ? NG : 0, used = 0, tails = 0;   // slots: K(0), V(0), K(1), ...
+            uint32_t n = 0, used = 0, tails = 0;   // key tiles so far; slot 2 n is K(n), 2 n + 1 V(n)
             bool ok = true;
             const int boxes = kKeys / box_rows, pieces = NC * boxes;   // of a tile; this CTA brings half of them
             const int c = lane / boxes, box = lane - c * boxes;        // this lane's piece
@@ -163,7 +159,8 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     return x < nt * boxes && k < t.q.len && k + box_rows > t.j0 ? trow[(unsigned)k / (unsigned)a.c.page_size] : 0;
                 };
                 int ids = 0, ahead = raw_id(lane);
-                if (!is_v && nt > 0 && t.rows > rank * tile_rows) {
+                const bool active = t.rows > rank * tile_rows;
+                if (!is_v && nt > 0 && active) {
                     if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY), (used & 1u) ^ 1u))) { ok = false; break; }
                     ++used;
                     if (lane == 0) {
@@ -173,7 +170,8 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             tma_load_q(sbase + (uint32_t)(x * kChunk), &tmap_q, t.hk * a.group, tok, x, bar(Q_FULL));
                     }
                 }
-                for (int j = 0; j < nt; ++j) {
+                for (int j = 0; j < nt; ++j, ++n) {
+                    const uint32_t it = 2 * n + (is_v ? 1 : 0);
                     if (((j * boxes) & 31) == 0) {
                         ids = checked_page(ahead, a.c.pages, &g_attn_pairs_error);
                         ahead = raw_id(j * boxes + 32 + lane);
@@ -189,18 +187,15 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     // (two barriers in turn: the other CTA may be one such tile ahead)
                     const uint32_t tail = bar(TAIL + (int)(tails & 1u));
                     if (part && lane == 0) mbar_arrive_expect_tx(tail, bytes * NC);
-                    for (int g = 0; g < NG; ++g) {
-                        if (!__all_sync(0xffffffffu, wait(empty_bar(it + g), slot_phase(it + g) ^ 1u))) {
-                            ok = false;
-                            break;
-                        }
-                        if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it + g), bytes * CG);
-                        __syncwarp();
-                        if (use && mine && c / CG == g)
-                            tma_load_cache_pair(slot_addr(it + g) + (uint32_t)((c % CG) * kChunk + box * box_rows * 128),
-                                                map, slot, c, t.hk, page, part ? tail : full_bar(it + g));
+                    if (!__all_sync(0xffffffffu, wait(empty_bar(it), slot_phase(it) ^ 1u))) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
+                    if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it), bytes * NC);
+                    __syncwarp();
+                    if (use && mine)
+                        tma_load_cache_pair(slot_addr(it) + (uint32_t)(c * kChunk + box * box_rows * 128), map, slot, c,
+                                            t.hk, page, part ? tail : full_bar(it));
                     if (part) {
                         if (!__all_sync(0xffffffffu, wait(tail, (tails >> 1) & 1u))) {
                             ok = false;
@@ -210,16 +205,13 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         for (int i = lane; i < kKeys * NC * 8; i += 32) {
                             const int x = i / (kKeys * 8), r = i / 8 % kKeys, key = k0 + r;
                             if (key >= t.q.len || (key / box_rows + 1) * box_rows <= t.j0)
-                                *reinterpret_cast<uint4*>(smem + C::kSmemRing +
-                                                          (((it + x / CG) % kSlots) * CG + x % CG) * kChunk + r * 128 +
-                                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(smem + C::kSmemRing + ((it % kSlots) * NC + x) * kChunk +
+                                                          r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0)
-                            for (int g = 0; g < NG; ++g) mbar_arrive(full_bar(it + g));
+                        if (lane == 0) mbar_arrive(full_bar(it));
                     }
-                    it += 2 * NG;
                 }
                 w = seg.we;
                 if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_pairs_error);
@@ -227,8 +219,8 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             if (!ok && lane == 0) {
                 fail();
                 // copies in flight land before the CTA goes away
-                for (uint32_t i = it < 2 * kSlots ? (is_v ? NG : 0) : it - 2 * kSlots; i <= it; i += 2 * NG)
-                    for (int g = 0; g < NG; ++g) (void)mbar_wait_drain(full_bar(i + g), slot_phase(i + g), 20000000ull);
+                for (uint32_t x = n < kSlots / 2 ? 0 : n - kSlots / 2; x <= n; ++x)
+                    (void)mbar_wait_drain(full_bar(2 * x + (is_v ? 1 : 0)), slot_phase(2 * x + (is_v ? 1 : 0)), 20000000ull);
                 if (used) (void)mbar_wait_drain(bar(Q_FULL), (used - 1u) & 1u, 20000000ull);
                 if (is_v) (void)mbar_wait_drain(bar(TAIL + (int)(tails & 1u)), (tails >> 1) & 1u, 20000000ull);
             }
@@ -238,7 +230,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             if (lane == 0) {
                 const bool is_pv = warp != kSoftWarps + 1;
                 constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, D) | kIdescBMnMajor;
-                uint32_t it = is_pv ? NG : 0, used = 0, n = 0;   // n: key tiles so far
+                uint32_t it = is_pv ? 1 : 0, used = 0, n = 0;   // slot of the next key tile; those taken part in so far
                 bool ok = true, issued = false;
                 auto need = [&](uint32_t b, uint32_t parity) {
                     if (ok && !wait(b, parity)) ok = false;
@@ -246,58 +238,50 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 };
                 for (long long w = w0; w < w1 && ok;) {
                     const Segment seg = segment_of(extent, t, w, w1);
-                    // a pair's second row tile may be absent: its slots are released all the same
-                    const bool active = t.rows > rank * tile_rows;
-                    if (!is_pv && active && seg.n > 0) need(bar(Q_FULL), used & 1u);
-                    for (int j = 0; j < seg.n && ok; ++j, it += 2 * NG) {
-                        if (!active) {
-                            for (int g = 0; g < NG; ++g)
-                                if (need(full_bar(it + g), slot_phase(it + g))) mma_commit_pair(empty_bar(it + g));
-                            continue;
-                        }
-                        const uint32_t buf = n % NB, ph = (n / NB) & 1u;
-                        if (!is_pv) {
-                            // the P that was over this S has been used
-                            if (!need(bar(S_EMPTY + (int)buf), ph ^ 1u)) break;
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                if (!need(full_bar(it + g), slot_phase(it + g))) break;
+                    if (t.rows <= rank * tile_rows) {   // a pair's second row tile may be absent
+                        // ... and its slots are released all the same
+                        for (int j = 0; j < seg.n && ok; ++j, it += 2)
+                            if (need(full_bar(it), slot_phase(it))) mma_commit_pair(empty_bar(it));
+                    } else if (seg.n > 0) {
+                        if (!is_pv) need(bar(Q_FULL), used & 1u);
+                        for (int j = 0; j < seg.n && ok; ++j, it += 2, ++n) {
+                            const uint32_t buf = n % NB, ph = (n / NB) & 1u, addr = slot_addr(it);
+                            if (!is_pv) {
+                                need(full_bar(it), slot_phase(it));
+                                need(bar(S_EMPTY + (int)buf), ph ^ 1u);   // the P that was over this S has been used
+                                if (!ok) break;
                                 tc_fence_after();
 #pragma unroll
-                                for (int x = 0; x < CG; ++x) {
-                                    const int c = g * CG + x;
+                                for (int c = 0; c < NC; ++c) {
                                     const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)(c * kChunk));
-                                    const uint64_t kd = smem_desc_k_sw128(slot_addr(it + g) + (uint32_t)(x * kChunk));
+                                    const uint64_t kd = smem_desc_k_sw128(addr + (uint32_t)(c * kChunk));
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
                                         mma_f16_ss(tmem + C::kS + 128u * buf, qd + 2 * kk, kd + 2 * kk, kIdescQK,
                                                    (c | kk) ? 1u : 0u);
                                 }
-                                issued = true;
-                                if (g == NG - 1) mma_commit(bar(S_FULL + (int)buf));
-                                mma_commit_pair(empty_bar(it + g));
-                            }
-                        } else {
-                            for (int g = 0; g < NG; ++g) need(full_bar(it + g), slot_phase(it + g));
-                            need(bar(P_FULL + (int)buf), ph);
-                            if (j == 0) need(bar(O_EMPTY), (used & 1u) ^ 1u);   // the previous item's output has been read
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t vd = smem_desc_mn_sw128(slot_addr(it), kChunk);
+                                mma_commit(bar(S_FULL + (int)buf));
+                                mma_commit_pair(empty_bar(it));
+                            } else {
+                                need(full_bar(it), slot_phase(it));
+                                need(bar(P_FULL + (int)buf), ph);
+                                if (j == 0) need(bar(O_EMPTY), (used & 1u) ^ 1u);   // the previous item's output has been read
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint64_t vd = smem_desc_mn_sw128(addr, kChunk);
 #pragma unroll
-                            for (int kk = 0; kk < kKeys / 16; ++kk)
-                                mma_f16_ts(tmem + C::kO, tmem + C::kS + 128u * buf + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)),
-                                           kIdescPV, (j || kk) ? 1u : 0u);
+                                for (int kk = 0; kk < kKeys / 16; ++kk)
+                                    mma_f16_ts(tmem + C::kO, tmem + C::kS + 128u * buf + 8u * kk,
+                                               vd + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (j || kk) ? 1u : 0u);
+                                mma_commit(bar(S_EMPTY + (int)buf));
+                                mma_commit_pair(empty_bar(it));
+                            }
                             issued = true;
-                            mma_commit(bar(O_DONE + (int)(n & 1u)));
-                            mma_commit(bar(S_EMPTY + (int)buf));
-                            for (int g = 0; g < NG; ++g) mma_commit_pair(empty_bar(it + g));
                         }
-                        ++n;
-                    }
-                    if (active && seg.n > 0 && ok) {
-                        if (!is_pv) mma_commit(bar(Q_EMPTY));
-                        ++used;
+                        if (ok) {
+                            if (!is_pv) mma_commit(bar(Q_EMPTY));
+                            ++used;
+                        }
                     }
                     w = seg.we;
                     if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_pairs_error);
@@ -389,8 +373,8 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     l *= m == -INFINITY ? 0.0f : exp2_fast((m - now) * scale);
                     m = now;
                     if (move && j > 0) {
-                        // the product before has been added (this barrier's one before it has, when S had room for n)
-                        if (!all_wait(O_DONE + (int)((n - 1u) & 1u), ((n - 1u) >> 1) & 1u)) break;
+                        // the product before has been added
+                        if (!all_wait(S_EMPTY + (int)((n - 1u) % NB), ((n - 1u) / NB) & 1u)) break;
                         tc_fence_after();
                         const float f = before == -INFINITY ? 0.0f : exp2_fast((before - now) * scale);
 #pragma unroll 1
@@ -449,9 +433,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 }
                 if (writer) {
                     if (nt > 0) {
-                        // (in this order: each barrier's product before has then been added)
-                        if (last > 0 && !all_wait(O_DONE + (int)((last - 1u) & 1u), ((last - 1u) >> 1) & 1u)) break;
-                        if (!all_wait(O_DONE + (int)(last & 1u), (last >> 1) & 1u)) break;
+                        if (!all_wait(S_EMPTY + (int)(last % NB), (last / NB) & 1u)) break;
                         tc_fence_after();
                     }
                     const float m2 = m * scale;   // -inf stays
@@ -523,13 +505,12 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
 
 }  // namespace
 
-size_t attn_pairs_workspace() { return (size_t)(kMaxSms / 2) * 2 * 2 * 4 * part_floats(256); }
+size_t attn_pairs_workspace() { return (size_t)(kMaxSms / 2) * 2 * 2 * 4 * part_floats(128); }
 
 cudaError_t launch_attn_pairs(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
     switch (a.c.head_dim) {
         case 64: return launch<64>(a, k, v, sms, stream);
-        case 128: return launch<128>(a, k, v, sms, stream);
-        default: return launch<256>(a, k, v, sms, stream);
+        default: return launch<128>(a, k, v, sms, stream);
     }
 }
 
