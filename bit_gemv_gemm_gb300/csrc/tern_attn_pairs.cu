@@ -45,7 +45,8 @@ __device__ int g_attn_pairs_error;
 
 constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
-constexpr int kItemCost = 3;                // key tiles' time that an item costs besides its own
+constexpr int kItemCost = 5;                // key tiles' time that an item costs besides its own (measured: 3 and 8 are
+                                            // slower for whole prompts, whose items are of unlike length)
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
 constexpr int kBuffers = 3;                 // of S

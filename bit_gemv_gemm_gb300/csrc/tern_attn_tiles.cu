@@ -1,39 +1,33 @@
-// tern_attn_tiles.cu -- attention of many query rows a key head (prompt chunks)
-// on the tcgen05 tensor cores.
+// tern_attn_tiles.cu -- attention of query rows that fill one row tile a key
+// head or less (verify steps, short chunks), and of heads of 256 values, on the
+// tcgen05 tensor cores.
 //
 // A row tile is 128 packed rows (128 / group tokens, every head of the group),
-// so one K and V tile serves all the heads that share it.  A CTA keeps NS row
-// tiles at once (two; one at D = 256, where the accumulator takes half of
-// tensor memory) against the same stream of 128-key tiles:
+// so one K and V tile serves all the heads that share it.  A CTA takes a row tile
+// through a run of 128-key tiles:
 //   * a TMA warp brings Q once and then K, another V, in chunks of 64 head
 //     values x 128 keys (16 KB of 128-byte swizzled rows), through one ring; a
 //     page gives boxes of up to 128 slots, one lane a box.  A copy takes a warp
 //     about 110 clocks to issue, and a page id some 700 to look up (one warp
 //     for both, without looking ahead, took 2000 to 3000 a tile and bound every
 //     call), hence two warps, and ids fetched 32 boxes ahead;
-//   * one thread a row tile issues S = Q K^T (both operands in shared memory,
-//     K-major) and O += P V (P in tensor memory, V MN-major) with M = 128.
-//     Issuing is nearly synchronous (a wait or a commit between products costs
-//     the thread about 150 and 57 clocks that its tensor work does not cover:
-//     110 clocks a 64-clock product from one thread), so two threads issue, each
-//     covering the other's waits; at D = 256 one issues QK, the other PV;
-//   * a warpgroup per row tile, one thread a row, reads S, takes the running
-//     maximum, writes P = exp2(S - m) as bf16 over S's own columns and keeps
-//     the sum in fp32.  O is only rescaled when a score passes the maximum in
-//     use by 2^8, so P and the sums stay below 2^8 of their largest term.
-// While one tile's softmax runs the tensor cores work for the other (at D =
-// 256: for the next keys, into a second S).  A row tile's thread issues PV(j)
-// and then QK(j + 1), so S (and P over it) needs one buffer a tile: one
-// thread's products complete in issue order.
-// Where an item has one row tile only (verify steps, short chunks), the two
-// streams take its even and its odd key tiles, with an accumulator each; the
-// first one's warpgroup then adds both (tensor memory is open to it).  Warps without a live row do no arithmetic.  Such calls are
-// bound by reading the cache.
+//   * two threads issue S = Q K^T (both operands in shared memory, K-major) and
+//     O += P V (P in tensor memory, V MN-major) with M = 128;
+//   * warpgroups, one thread a row, read S, take the running maximum, write P =
+//     exp2(S - m) as bf16 over S's own columns and keep the sum in fp32.  O is
+//     only rescaled when a score passes the maximum in use by 2^8, so P and the
+//     sums stay below 2^8 of their largest term.
+// At D <= 128 two streams, each with an MMA thread, a warpgroup, an S and an O,
+// take the even and the odd key tiles; the first one's warpgroup then adds both
+// (tensor memory is open to it).  Such calls are bound by reading the cache, and
+// warps without a live row do no arithmetic.  At D = 256, where one O takes half
+// of tensor memory, there is one stream with two S buffers: one thread issues QK,
+// ahead by a tile, the other PV.
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
 // Work is shared out as in the rows kernel: equal contiguous shares of all
-// (sequence, row tiles, key head) items' 128-key tiles; parts meet in the
+// (sequence, row tile, key head) items' 128-key tiles; parts meet in the
 // workspace, and the warp that counts last for its 32 rows adds them in order.
 #include <algorithm>
 
@@ -46,7 +40,7 @@ using namespace sm100;
 
 __device__ int g_attn_tiles_error;
 
-constexpr int kKeys = 128, kRows = 128;
+constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
 constexpr int kItemCost = 3;                // key tiles' time that an item costs besides its own (about 3.5 us)
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
@@ -54,35 +48,26 @@ constexpr int kMinTiles = 4;                // key tiles a share holds at least
 template <int D>
 struct Cfg {
     static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
-    static constexpr int NS = D == 256 ? 1 : 2;             // row tiles a CTA
+    static constexpr int NS = D == 256 ? 1 : 2;             // streams: every NS-th key tile each
     static constexpr int CG = D == 128 ? 2 : 1;             // chunks of a ring slot
     static constexpr int NG = NC / CG;                      // slots of a K or V tile
     static constexpr int kSlots = D == 64 ? 10 : D == 128 ? 5 : 8;
     static constexpr int kSoftWarps = 4 * NS;
-    // two row tiles: a third warpgroup (two TMA and two MMA warps) gives registers
+    // two streams: a third warpgroup (two TMA and two MMA warps) gives registers
     // to the softmax warps, which hold a row of S each: 256 x 208 + 128 x 88 =
     // 384 x 168, what the CTA was launched with
     static constexpr int kThreads = NS == 2 ? 384 : 256;
     static constexpr uint32_t kS = 0, kO = 256;             // tensor memory: S (and P) at 128 b, O at kO + D s
-    static constexpr size_t kSmemRing = (size_t)NS * NC * kChunk;
+    static constexpr size_t kSmemRing = (size_t)NC * kChunk;
     static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
     // barriers: full[slots], empty[slots], then pairs: q_full, q_empty, s_full,
     // s_empty, p_full, o_full, o_empty, drain; tail, merge
     static constexpr int kBars = 2 * kSlots + 18;
     static constexpr size_t kSmemMisc = kSmemBar + kBars * 8;
-    static constexpr size_t kSmemStat = kSmemMisc + 256;              // the second stream's (m, l), a split item
+    static constexpr size_t kSmemStat = kSmemMisc + 256;              // the second stream's (m, l)
     static constexpr size_t kSmem = kSmemStat + (NS == 2 ? kRows * 8 : 0) + 1024;
-    static constexpr size_t kPart = (size_t)NS * kRows * (D + 2);   // floats of one part
 };
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys);
-
-// floats are exchanged four columns at a time, [column / 4][row][4]
-__device__ __forceinline__ size_t part_at(int D, int s, int row, int c4) {
-    return (size_t)s * kRows * (D + 2) + ((size_t)c4 * kRows + row) * 4;
-}
-__device__ __forceinline__ size_t part_stat(int D, int s, int row) {
-    return (size_t)s * kRows * (D + 2) + (size_t)D * kRows + 2 * row;
-}
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
@@ -110,8 +95,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kBars; ++i) {
             const bool by_warps = (i >= P_FULL && i < P_FULL + 2) || (i >= O_EMPTY && i < O_EMPTY + 2) || i == MERGE;
-            const bool by_tiles = NS == 2 && i >= kSlots && i < 2 * kSlots;   // both MMA threads release a slot
-            mbar_init(bar(i), by_warps ? 4 : by_tiles ? 2 : 1);
+            const bool by_threads = NS == 2 && ((i >= kSlots && i < 2 * kSlots) || i == Q_EMPTY);   // both MMA threads
+            mbar_init(bar(i), by_warps ? 4 : by_threads ? 2 : 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -131,13 +116,12 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     pdl_wait();
 
     const int tile_rows = kRows / a.group * a.group;   // whole tokens
-    const int R = NS * tile_rows;
     int P;
     long long total, w0, w1;
     Item t;
-    const RowTileExtent<kKeys, kItemCost> extent{R, a.group, a.window};
-    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, (int)blockIdx.x, (int)gridDim.x, sm_scan, &g_attn_tiles_error, total,
-                                              P, w0, w1, t);
+    const RowTileExtent<kKeys, kItemCost> extent{tile_rows, a.group, a.window};
+    const bool busy = find_share<C::kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, (int)blockIdx.x, (int)gridDim.x,
+                                              sm_scan, &g_attn_tiles_error, total, P, w0, w1, t);
     auto fail = [&] {
         if (!*abort_flag) {
             *abort_flag = 1;
@@ -154,7 +138,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         // ------------------------------ TMA: Q and K, or V ------------------------------
         const bool is_v = warp != C::kSoftWarps;
         const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-        uint32_t it = is_v ? NG : 0, used[2] = {0, 0}, tails = 0;   // slots: K(0), V(0), K(1), ...
+        uint32_t it = is_v ? NG : 0, used = 0, tails = 0;   // slots: K(0), V(0), K(1), ...
         bool ok = true;
         const int boxes = kKeys / box_rows, c = lane / boxes, box = lane - c * boxes;   // this lane's piece of a tile
         for (long long w = w0; w < w1 && ok;) {
@@ -167,16 +151,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 return x < nt * boxes && k < t.q.len && k + box_rows > t.j0 ? trow[(unsigned)k / (unsigned)a.c.page_size] : 0;
             };
             int ids = 0, ahead = raw_id(lane);
-            for (int s = 0; s < NS && ok && nt > 0 && !is_v; ++s) {
-                const bool split = t.rows <= tile_rows;   // both streams take the one row tile
-                if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY + s), (used[s] & 1u) ^ 1u))) { ok = false; break; }
-                ++used[s];
+            if (!is_v && nt > 0) {
+                if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY), (used & 1u) ^ 1u))) { ok = false; break; }
+                ++used;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(Q_FULL + s), (uint32_t)(NC * tile_rows * 128));
-                    const int tok = t.q.q0 + (t.rt * R + (split ? 0 : s * tile_rows)) / a.group;
+                    mbar_arrive_expect_tx(bar(Q_FULL), (uint32_t)(NC * tile_rows * 128));
+                    const int tok = t.q.q0 + t.rt * (tile_rows / a.group);
                     for (int x = 0; x < NC; ++x)
-                        tma_load_q(sbase + (uint32_t)((s * NC + x) * kChunk), &tmap_q, t.hk * a.group, tok, x,
-                                   bar(Q_FULL + s));
+                        tma_load_q(sbase + (uint32_t)(x * kChunk), &tmap_q, t.hk * a.group, tok, x, bar(Q_FULL));
                 }
             }
             for (int j = 0; j < nt && ok; ++j) {
@@ -233,8 +215,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             // copies in flight land before the CTA goes away
             for (uint32_t i = it < 2 * kSlots ? (is_v ? NG : 0) : it - 2 * kSlots; i <= it; i += 2 * NG)
                 for (int g = 0; g < NG; ++g) (void)mbar_wait_drain(full_bar(i + g), slot_phase(i + g), 20000000ull);
-            for (int s = 0; s < NS; ++s)
-                if (used[s]) (void)mbar_wait_drain(bar(Q_FULL + s), (used[s] - 1u) & 1u, 20000000ull);
+            if (used) (void)mbar_wait_drain(bar(Q_FULL), (used - 1u) & 1u, 20000000ull);
             if (is_v) (void)mbar_wait_drain(bar(TAIL), tails & 1u, 20000000ull);
         }
         __syncwarp();
@@ -249,8 +230,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 if (ok && !wait(b, parity)) ok = false;
                 return ok;
             };
-            auto qk = [&](int s, uint32_t buf, int c, uint32_t addr) {   // S(buf) (+)= chunk c of Q(s) K^T
-                const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)((s * NC + c) * kChunk));
+            auto qk = [&](uint32_t buf, int c, uint32_t addr) {   // S(buf) (+)= chunk c of Q K^T
+                const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)(c * kChunk));
                 const uint64_t kd = smem_desc_k_sw128(addr);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -269,31 +250,29 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const Segment seg = segment_of(extent, t, w, w1);
                 const int nt = seg.n;
                 if constexpr (NS == 2) {
-                    // QK(j), PV(j) of row tile `me`, or of every second key tile; of the others only the slots are released
-                    const bool split = t.rows <= tile_rows;
-                    if (nt > 0) need(bar(Q_FULL + me), used & 1u);
+                    // QK(j), PV(j) of every second key tile; of the others only the slots are released
+                    if (nt > 0) need(bar(Q_FULL), used & 1u);
                     for (int j = 0; j < nt && ok; ++j) {
-                        const bool active = !split || (j & 1) == me;
+                        const bool mine = (j & 1) == me;
                         if (!need(full_bar(it), slot_phase(it))) break;
-                        if (active) {
+                        if (mine) {
                             tc_fence_after();
 #pragma unroll
-                            for (int c = 0; c < NC; ++c) qk(me, me, c, slot_addr(it) + (uint32_t)(c * kChunk));
+                            for (int c = 0; c < NC; ++c) qk(me, c, slot_addr(it) + (uint32_t)(c * kChunk));
                             mma_commit(bar(S_FULL + me));
                             mma_commit(empty_bar(it));
-                            if (j + (split ? 2 : 1) >= nt) mma_commit(bar(Q_EMPTY + me));   // its last use: the next may come
+                            if (j + 2 >= nt) mma_commit(bar(Q_EMPTY));   // its last use: the next may come
                         } else {
                             mbar_arrive(empty_bar(it));
                         }
                         ++it;
                         if (!need(full_bar(it), slot_phase(it))) break;
-                        if (active) {
+                        if (mine) {
                             if (!need(bar(P_FULL + me), jobs++ & 1u)) break;
                             // the previous item's output has been read
-                            const bool first = j == (split ? me : 0);
-                            if (first && !need(bar(O_EMPTY + me), (used & 1u) ^ 1u)) break;
+                            if (j == me && !need(bar(O_EMPTY + me), (used & 1u) ^ 1u)) break;
                             tc_fence_after();
-                            pv(me, me, slot_addr(it), !first);
+                            pv(me, me, slot_addr(it), j != me);
                             mma_commit(empty_bar(it));
                         } else {
                             mbar_arrive(empty_bar(it));
@@ -302,7 +281,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     if (nt > 0 && ok) {   // (one key tile, the second stream: nothing to wait for)
                         mma_commit(bar(O_FULL + me));
-                        if (split && me >= nt) mbar_arrive(bar(Q_EMPTY + me));
+                        if (me >= nt) mbar_arrive(bar(Q_EMPTY));
                         ++used;
                     }
                 } else if (me == 0) {
@@ -313,7 +292,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         for (int c = 0; c < NC; ++c) {
                             if (!need(full_bar(it + c), slot_phase(it + c))) break;
                             tc_fence_after();
-                            qk(0, jobs & 1u, c, slot_addr(it + c));
+                            qk(jobs & 1u, c, slot_addr(it + c));
                             mma_commit(empty_bar(it + c));
                         }
                         mma_commit(bar(S_FULL + (int)(jobs & 1u)));
@@ -358,27 +337,23 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t to = tmem + lanes + C::kO + (uint32_t)(D * s);
-        uint32_t sc = 0, oc = 0, merges = 0;   // S and O tiles and split items seen
+        uint32_t sc = 0, oc = 0, merges = 0;   // S and O tiles and merged items seen
         const bool flip = a.scale_log2 < 0.0f;
         const float scale = fabsf(a.scale_log2);
         bool ok = true;
         for (long long w = w0; w < w1 && ok;) {
             const Segment seg = segment_of(extent, t, w, w1);
             const int nt = seg.n;
-            const bool split = NS == 2 && t.rows <= tile_rows;   // every second key tile of the one row tile
-            const int sr = split ? 0 : s;
-            const int rows = min(tile_rows, t.rows - sr * tile_rows);   // of this row tile
             if (!seg.skip) {
-                const int r = t.rt * R + sr * tile_rows + row;         // packed row of the sequence
+                const int rows = t.rows, r = t.rt * tile_rows + row;   // packed row of the sequence
                 const bool live = row < rows, idle = quad * 32 >= rows;
                 const int p = t.q.len - t.q.n + r / a.group;
                 const int hi = live ? p : -1, lo = a.window > 0 ? p - a.window : -1;
-                const int p_lo = t.q.len - t.q.n + (t.rt * R + sr * tile_rows) / a.group;
-                const int p_hi = t.q.len - t.q.n + (t.rt * R + sr * tile_rows + rows - 1) / a.group;
+                const int p_lo = t.q.len - t.q.n + t.rt * tile_rows / a.group;
+                const int p_hi = t.q.len - t.q.n + (t.rt * tile_rows + rows - 1) / a.group;
                 const int key0 = seg.first * kKeys;
                 float m = -INFINITY, l = 0.0f;
-                const int j_first = split ? s : 0, j_step = split ? 2 : 1;
-                for (int j = j_first; j < nt && ok; j += j_step, ++sc) {
+                for (int j = s; j < nt && ok; j += NS, ++sc) {
                     const uint32_t buf = kWide ? sc & 1u : (uint32_t)s;
                     const uint32_t ph = kWide ? (sc >> 1) & 1u : sc & 1u;
                     if (!__all_sync(0xffffffffu, wait(bar(S_FULL + (int)buf), ph))) { ok = false; break; }
@@ -416,7 +391,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         const float f = m == -INFINITY ? 0.0f : exp2_fast((m - mn) * scale);
                         m = mn;
                         l *= f;
-                        if (j > j_first) {
+                        if (j > s) {
                             if (kWide) {
                                 // the product before this one is still adding into O
                                 if (!__all_sync(0xffffffffu, wait(bar(O_FULL), (oc + (uint32_t)j - 1u) & 1u))) {
@@ -462,9 +437,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (lane == 0) mbar_arrive(bar(P_FULL + (int)buf));
                 }
                 if (!ok) break;
-                const bool whole = seg.whole;
-                const int tok = t.q.q0 + r / a.group, head = t.hk * a.group + r % a.group;
-                const long long orow = (long long)tok * a.q_heads + head;
+                const long long orow = (long long)(t.q.q0 + r / a.group) * a.q_heads + t.hk * a.group + r % a.group;
                 if (nt > 0) {
                     oc += kWide ? (uint32_t)nt : 1u;
                     // (with two S buffers the product before the last may be running too)
@@ -475,10 +448,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 }
                 float m2 = m * scale;   // -inf stays
                 float f0 = 1.0f, f1 = 0.0f;
-                if (split && nt > 0) {
+                if (NS == 2 && nt > 0) {
                     float2* stat = reinterpret_cast<float2*>(smem + C::kSmemStat);
                     if (s == 1) {
-                        // the first stream has read what the last split item left here
+                        // the first stream has read what the last item left here
                         if (oc > 1 && !__all_sync(0xffffffffu, wait(bar(O_EMPTY + 1), oc & 1u))) { ok = false; break; }
                         stat[row] = make_float2(m2, l);
                         __syncwarp();
@@ -494,119 +467,39 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         m2 = mm;
                     }
                 }
-                if (!split || s == 0) {   // (not indented: the output of a row tile)
-                float* part = a.partial + (size_t)(2 * blockIdx.x + (w == w0 ? 0 : 1)) * C::kPart;
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < D && !idle; c += 32) {
-                    uint32_t o[32];
-                    if (nt > 0) {
-                        tmem_ld_x32(to + c, o);
-                        if (split) {
-                            uint32_t o1[32];   // (an accumulator that no product reached holds anything)
-                            tmem_ld_x32(to + (uint32_t)D + c, o1);
-                            tmem_ld_wait();
+                if (s == 0) {
+                    float* part = a.partial + (size_t)(2 * blockIdx.x + (w == w0 ? 0 : 1)) * part_floats(D);
+                    if (!idle)
+                        emit_row<D>(a, seg.whole, part, row, live, orow, m2, l, [&](int c, uint32_t (&o)[32]) {
+                            if (nt == 0) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float x = f0 > 0.0f ? __uint_as_float(o[e]) * f0 : 0.0f;
-                                o[e] = __float_as_uint(f1 > 0.0f ? fmaf(__uint_as_float(o1[e]), f1, x) : x);
+                                for (int e = 0; e < 32; ++e) o[e] = 0u;
+                                return;
                             }
-                        }
-                        tmem_ld_wait();
-                    } else {
+                            tmem_ld_x32(to + c, o);
+                            if constexpr (NS == 2) {
+                                uint32_t o1[32];   // (an accumulator that no product reached holds anything)
+                                tmem_ld_x32(to + (uint32_t)D + c, o1);
+                                tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    }
-                    if (whole) {
-                        if (live) {
-                            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t y[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    y[i] = pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
-                                                     __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
-                                dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
-                            }
-                        }
-                    } else if (live) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            __stcg(reinterpret_cast<uint4*>(part + part_at(D, sr, row, c / 4 + e)),
-                                   make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-                    }
-                }
-                if (nt > 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(O_EMPTY + s));
-                        if (split) mbar_arrive(bar(O_EMPTY + 1));
-                    }
-                }
-                if (idle) {
-                } else if (whole) {
-                    if (live && a.lse) a.lse[orow] = l > 0.0f ? (m2 + log2f(l)) * 0.693147180559945309f : -INFINITY;
-                } else {
-                    __stcg(reinterpret_cast<float2*>(part + part_stat(D, sr, row)), make_float2(m2, l));
-                    __threadfence();
-                    __syncwarp();
-                    const int c_lo = unit_owner(total, P, t.at + kItemCost), c_hi = unit_owner(total, P, t.at + t.units - 1);
-                    unsigned last = 0;
-                    if (lane == 0)
-                        last = atomicInc(a.counters + 8 * c_lo + 4 * sr + quad, (unsigned)(c_hi - c_lo)) ==
-                               (unsigned)(c_hi - c_lo);
-                    if (__shfl_sync(0xffffffffu, last, 0)) {
-                        __threadfence();
-                        // (an item's first CTA may have begun before it: its part is then in its second slot)
-                        const int late = unit_begin(total, P, c_lo) >= t.at ? 0 : 1;
-                        auto part_of = [&](int x) { return a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * C::kPart; };
-                        // no branch in these loops: all the loads of a few parts are in flight together
-                        float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 4
-                        for (int x = c_lo; x <= c_hi; ++x)
-                            mm = fmaxf(mm, __ldcg(part_of(x) + part_stat(D, sr, row)));
-                        const float base = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll 4
-                        for (int x = c_lo; x <= c_hi; ++x) {
-                            const float2 st = __ldcg(reinterpret_cast<const float2*>(part_of(x) + part_stat(D, sr, row)));
-                            ll += st.y * exp2_fast(st.x - base);
-                        }
-                        const float inv2 = ll > 0.0f ? 1.0f / ll : 0.0f;
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float y[32] = {};
-#pragma unroll 3
-                            for (int x = c_lo; x <= c_hi; ++x) {
-                                const float* px = part_of(x);
-                                const float f = exp2_fast(__ldcg(px + part_stat(D, sr, row)) - base);
-                                float4 v[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    v[e] = __ldcg(reinterpret_cast<const float4*>(px + part_at(D, sr, row, c / 4 + e)));
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
-                                    y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
-                                    y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
-                                    y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
+                                for (int e = 0; e < 32; ++e) {
+                                    const float x = f0 > 0.0f ? __uint_as_float(o[e]) * f0 : 0.0f;
+                                    o[e] = __float_as_uint(f1 > 0.0f ? fmaf(__uint_as_float(o1[e]), f1, x) : x);
                                 }
                             }
-                            if (live) {
-                                uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    dst[e] = make_uint4(pack_bf16(y[8 * e] * inv2, y[8 * e + 1] * inv2),
-                                                        pack_bf16(y[8 * e + 2] * inv2, y[8 * e + 3] * inv2),
-                                                        pack_bf16(y[8 * e + 4] * inv2, y[8 * e + 5] * inv2),
-                                                        pack_bf16(y[8 * e + 6] * inv2, y[8 * e + 7] * inv2));
-                            }
+                            tmem_ld_wait();
+                        });
+                    if (nt > 0) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(O_EMPTY));
+                            if (NS == 2) mbar_arrive(bar(O_EMPTY + 1));
                         }
-                        if (live && a.lse)
-                            a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
                     }
-                }
+                    if (!seg.whole && !idle)
+                        join_parts<D, kItemCost>(a, t, a.counters + quad, a.partial, part_floats(D), row, live, orow,
+                                                 total, P);
                 }
             }
             w = seg.we;
@@ -641,7 +534,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int R = C::NS * (kRows / a.group * a.group);
+    const int R = kRows / a.group * a.group;
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
     const long long P = std::min<long long>(sms, (most_units(a, kKeys, kItemCost) + kMinTiles - 1) / kMinTiles);
     return launch_pdl(attn_tiles_kernel<D>, dim3((unsigned)P), dim3(C::kThreads), C::kSmem, stream, true, mq, mk, mv, a,
@@ -651,7 +544,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
 }  // namespace
 
 size_t attn_tiles_workspace() {
-    return (size_t)kMaxSms * 2 * 4 * std::max({Cfg<64>::kPart, Cfg<128>::kPart, Cfg<256>::kPart});
+    return (size_t)kMaxSms * 2 * 4 * part_floats(256);
 }
 
 cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
