@@ -25,7 +25,8 @@ float to_log2(float scale) {
 tern_status check_heads(const CacheView& c, int q_heads, long long q_stride) {
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return TERN_ERR_SHAPE;
     if (q_heads < 1 || q_heads % c.kv_heads != 0 || q_heads / c.kv_heads > 64) return TERN_ERR_SHAPE;
-    if (q_stride < (long long)q_heads * c.head_dim || q_stride % 8 != 0) return TERN_ERR_SHAPE;
+    if (q_stride < (long long)q_heads * c.head_dim || q_stride % 8 != 0 || q_stride >= (1LL << 37))
+        return TERN_ERR_SHAPE;
     return TERN_OK;
 }
 
@@ -51,7 +52,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     set_launch_count(0);
     AttnArgs a;
     tern_status st = make_cache_view(layout, &a.c);
-    if (st == TERN_OK) st = make_seq_view(table, table_width, lens, q_start, B, T, max_new, &a.s);
+    if (st == TERN_OK) st = make_seq_view(table, table_width, a.c.page_size, lens, q_start, B, T, max_new, &a.s);
     if (st == TERN_OK) st = check_heads(a.c, q_heads, q_stride);
     if (st != TERN_OK) return st;
     if (window < 0 || !(fabsf(scale) < INFINITY)) return TERN_ERR_SHAPE;
@@ -99,7 +100,7 @@ extern "C" tern_status tern_attention_mass(const void* q, long long q_stride, co
     set_launch_count(0);
     MassArgs a;
     tern_status st = make_cache_view(layout, &a.c);
-    if (st == TERN_OK) st = make_seq_view(table, table_width, lens, q_start, B, T, max_new, &a.s);
+    if (st == TERN_OK) st = make_seq_view(table, table_width, a.c.page_size, lens, q_start, B, T, max_new, &a.s);
     if (st == TERN_OK) st = check_heads(a.c, q_heads, q_stride);
     if (st != TERN_OK) return st;
     if (window < 0 || !(fabsf(scale) < INFINITY) || !(fabsf(decay) < INFINITY)) return TERN_ERR_SHAPE;

@@ -195,7 +195,8 @@ __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent&
 inline long long most_units(const AttnArgs& a, int unit, int cost) {
     const long long room = (long long)a.s.width * a.c.page_size;
     const long long keys = a.window > 0 && a.window + (long long)a.s.max_new < room ? a.window + (long long)a.s.max_new : room;
-    return (long long)a.s.B * a.c.kv_heads * a.tiles * ((keys + unit - 1) / unit + 1 + cost);
+    const double most = (double)a.s.B * a.c.kv_heads * a.tiles * (double)((keys + unit - 1) / unit + 1 + cost);
+    return most < 1e15 ? (long long)most : (long long)1e15;
 }
 
 // A cache array as the TMA sees it: [page][head][d / 64][slot][64 values], a

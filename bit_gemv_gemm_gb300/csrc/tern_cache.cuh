@@ -93,9 +93,13 @@ inline tern_status make_cache_view(const tern_cache_layout* l, CacheView* v) {
     *v = CacheView{l->pages, l->page_size, l->kv_heads, l->head_dim, l->page_stride, l->head_stride, l->slot_stride};
     return TERN_OK;
 }
-inline tern_status make_seq_view(const int* table, int width, const int* lens, const int* q_start, int B, int T,
-                                 int max_new, SeqView* s) {
-    if (B < 1 || B > 65535 || width < 1 || T < 0 || max_new < 0) return TERN_ERR_SHAPE;
+// The most keys a table row may name: indices stay well inside 32 bits.
+constexpr long long kMaxKeys = 1LL << 30;
+
+inline tern_status make_seq_view(const int* table, int width, int page_size, const int* lens, const int* q_start, int B,
+                                 int T, int max_new, SeqView* s) {
+    if (B < 1 || B > 65535 || width < 1 || T < 0 || max_new < 0 || (long long)width * page_size > kMaxKeys)
+        return TERN_ERR_SHAPE;
     if (!q_start && T % B != 0) return TERN_ERR_SHAPE;
     if (!table || !lens) return TERN_ERR_NULL;
     if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(q_start, 4)) return TERN_ERR_ALIGN;

@@ -287,7 +287,7 @@ extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache
     if (st != TERN_OK) return st;
     if (a.c.kv_heads != a.dc.kv_heads || a.c.head_dim != a.dc.head_dim || B < 1 || B > 65535 || table_width < 1 ||
         dst_table_width < 1 || budget < 1 || recent < 0 || recent > budget ||
-        (long long)dst_table_width * a.dc.page_size < budget || (long long)table_width * a.c.page_size > 0x7fffffffLL ||
+        (long long)dst_table_width * a.dc.page_size < budget || (long long)table_width * a.c.page_size > kMaxKeys ||
         (long long)B * a.c.kv_heads > 0x7fffffffLL / kMaxCluster)
         return TERN_ERR_SHAPE;
     if (!k_cache || !v_cache || !mass || !table || !lens || !dst_k || !dst_v || !dst_mass || !dst_table || !keep ||

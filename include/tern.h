@@ -387,6 +387,10 @@ tern_status tern_affine_gemm(const void *x, const uint32_t *codes, const void *s
 /* j > p - window.  A query that sees no key (p < 0) gets zeros and an lse   */
 /* of -inf.  Query head h reads key head h / (q_heads / kv_heads).          */
 /*                                                                         */
+/* A table row names at most 2^30 keys (TERN_ERR_SHAPE beyond).             */
+/* Nothing is read before the previous kernel on the stream has finished,   */
+/* so every argument may be its output.                                     */
+/*                                                                         */
 /* table, lens, q_start, positions, slots and the fp32 arrays need only the */
 /* alignment of their type.  Device-side values that do not fit the arrays  */
 /* are reported through tern_device_error (TERN_DEVERR_CACHE_*), never      */
@@ -447,8 +451,12 @@ tern_status tern_rope_append(const void *q, const void *k, const void *v, int in
  * stride q_stride elements (a multiple of 8, >= q_heads * head_dim), heads
  * contiguous.  Scores, sums and the output are held in fp32 and rounded once
  * to bf16; the probabilities of the second product are rounded to bf16.  Slots
- * at or past lens[b] may hold anything, NaN included.  q_heads a multiple of
- * kv_heads, at most 64 query heads a key head.
+ * at or past lens[b] may hold anything, NaN included, and with a window only the
+ * pages that hold a visible key are read.  A value of V that is not finite, of a
+ * key that some query of the call sees, may reach queries that do not see it
+ * (their probability of 0 times it).  q_heads a multiple of kv_heads, at most 64
+ * query heads a key head; head_dim 64, 128 or 256.  One kernel launch; the
+ * result does not vary from run to run.
  * The workspace is zero-filled once before its first use and left ready for
  * the next call; its size never exceeds 128 MiB.  Calls that share it must be
  * ordered; after a device error zero-fill it again. */
@@ -465,8 +473,9 @@ tern_status tern_paged_attention(const void *q, long long q_stride, const void *
  *   of its group of exp(s_ij - lse_i),
  * with the lse that tern_paged_attention gave for the same q, scale and window
  * (a row with lse = -inf gives nothing).  mass and mass_out as described
- * above; they may be the same array.  Slots that hold no key are left alone.
- * No atomics: a key's sum has a fixed order. */
+ * above; they may be the same array.  Every key's page is read, a key outside
+ * every window decays.  Slots that hold no key are left alone.  One kernel
+ * launch, no atomics: a key's sum has a fixed order. */
 tern_status tern_attention_mass(const void *q, long long q_stride, const void *k_cache,
                                 const tern_cache_layout *layout, const int *table, int table_width, const int *lens,
                                 const int *q_start, int B, int T, int max_new, int q_heads, float scale, int window,

@@ -47,6 +47,7 @@ def test_attention_refuses_layouts(tern, bad):
 
 
 @pytest.mark.parametrize("bad,code", [(dict(B=0), SHAPE), (dict(width=0), SHAPE), (dict(T=-1), SHAPE),
+                                      (dict(width=1 << 27), SHAPE), (dict(q_stride=1 << 37), SHAPE),
                                       (dict(q_heads=7), SHAPE), (dict(q_heads=2 * 65, q_stride=1 << 20), SHAPE),
                                       (dict(q_stride=1000), SHAPE), (dict(q_stride=1028), SHAPE),
                                       (dict(window=-1), SHAPE), (dict(scale=float("nan")), SHAPE),

@@ -180,6 +180,38 @@ def test_window_other_heads(tern, D, window):
     check_both(tern, Problem(D, [900, 411], [300, 2], 8, 2, D, 64, "nhd"), window)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 20, 150])
+def test_window_leaves_earlier_pages_alone(tern, D, new):
+    """Pages that hold no visible key are not read: their table entries may be
+    anything, as a cache that drops them leaves it."""
+    p = Problem(new, [new + 700, new + 64], [new, new], 4, 2, D, 32)
+    gone = p.table.clone()
+    for b, L in enumerate(p.lens):
+        first = max(L - new - 100 + 1, 0) // p.page
+        gone[b, :first] = p.pages + 5
+    kept, p.table = p.table, gone
+    out, lse = run_attention(tern, p, 100)
+    p.table = kept
+    check_attention(p, out, lse, 100)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,D,new", [(64, 1, 64, 1), (64, 1, 128, 3), (48, 1, 256, 2), (126, 2, 64, 5),
+                                                    (33, 1, 128, 40), (3, 3, 64, 129), (1, 1, 128, 257)])
+def test_group_sizes(tern, q_heads, kv_heads, D, new):
+    """Up to 64 query heads a key head, and groups that do not divide 128."""
+    check_both(tern, Problem(new, [new + 333, new], [new, new], q_heads, kv_heads, D, 16))
+
+
+def test_many_sequences(tern):
+    """More sequences than threads look for their share, most of them without
+    new tokens or keys, and row tiles that few of them have."""
+    lens = [(37 * b) % 300 for b in range(900)]
+    new = [min(L, (0, 1, 0, 3)[b % 4]) for b, L in enumerate(lens)]
+    lens[450], new[450] = 500, 200
+    check_both(tern, Problem(2, lens, new, 4, 1, 64, 16))
+
+
 def test_long_context(tern):
     """Enough keys for every split of the keys over the GPU."""
     check_both(tern, Problem(3, [20011], [1], 8, 2, 128, 16))
