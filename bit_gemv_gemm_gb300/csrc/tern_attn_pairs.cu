@@ -419,11 +419,9 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const bool writer = nt > 0 ? (int)(last & 1u) == wg : wg == 0;
                 if (nt > 1) {
                     if (!writer) {
-                        if (!idle) {
-                            if (!handed(last)) break;
-                            const float end = sm_m[row];
-                            sm_l[row] = m == -INFINITY ? 0.0f : l * exp2_fast((m - end) * scale);
-                        }
+                        // (idle warps wait, too: one that ran on into the next item would count itself in for this one)
+                        if (!handed(last)) break;
+                        if (!idle) sm_l[row] = m == -INFINITY ? 0.0f : l * exp2_fast((m - sm_m[row]) * scale);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(MERGE));
                     } else {
