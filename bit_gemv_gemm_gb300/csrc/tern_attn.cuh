@@ -368,33 +368,45 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, uns
     auto stat_of = [&](int x) {
         return __ldcg(reinterpret_cast<const float2*>(part_of(x) + (size_t)D * kTileRows + 2 * row));
     };
-    // no branch in these loops: all the loads of a few parts are in flight together
+    // four parts at a time, all their loads in flight together; past the last, its own again with no weight
     float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 4
-    for (int x = c_lo; x <= c_hi; ++x) mm = fmaxf(mm, stat_of(x).x);
-    const float base = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll 4
-    for (int x = c_lo; x <= c_hi; ++x) {
-        const float2 st = stat_of(x);
-        ll += st.y * exp2_fast(st.x - base);
+    for (int x0 = c_lo; x0 <= c_hi; x0 += 4) {
+        float2 st[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[i] = stat_of(min(x0 + i, c_hi));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float mn = fmaxf(mm, st[i].x), base = mn == -INFINITY ? 0.0f : mn;
+            ll = ll * exp2_fast(mm - base) + (x0 + i <= c_hi ? st[i].y * exp2_fast(st[i].x - base) : 0.0f);
+            mm = mn;
+        }
     }
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const float base = mm == -INFINITY ? 0.0f : mm, inv = ll > 0.0f ? 1.0f / ll : 0.0f;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         float y[32] = {};
-#pragma unroll 3
-        for (int x = c_lo; x <= c_hi; ++x) {
-            const float f = exp2_fast(stat_of(x).x - base);
-            float4 v[8];
+#pragma unroll 1
+        for (int x0 = c_lo; x0 <= c_hi; x0 += 4) {
+            float4 v[4][8];
+            float f[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + ((size_t)(c / 4 + e) * kTileRows + row) * 4));
+            for (int i = 0; i < 4; ++i) {
+                const int x = min(x0 + i, c_hi);
+                f[i] = stat_of(x).x;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[4 * e] = fmaf(v[e].x, f, y[4 * e]);
-                y[4 * e + 1] = fmaf(v[e].y, f, y[4 * e + 1]);
-                y[4 * e + 2] = fmaf(v[e].z, f, y[4 * e + 2]);
-                y[4 * e + 3] = fmaf(v[e].w, f, y[4 * e + 3]);
+                for (int e = 0; e < 8; ++e)
+                    v[i][e] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + ((size_t)(c / 4 + e) * kTileRows + row) * 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] = x0 + i <= c_hi ? exp2_fast(f[i] - base) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[4 * e] = fmaf(v[i][e].x, f[i], y[4 * e]);
+                    y[4 * e + 1] = fmaf(v[i][e].y, f[i], y[4 * e + 1]);
+                    y[4 * e + 2] = fmaf(v[i][e].z, f[i], y[4 * e + 2]);
+                    y[4 * e + 3] = fmaf(v[i][e].w, f[i], y[4 * e + 3]);
+                }
             }
         }
         if (live) {

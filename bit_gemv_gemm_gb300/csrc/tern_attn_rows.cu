@@ -308,20 +308,28 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
                     const int r = i / (D / 4), c = i % (D / 4) * 4;
                     float mm = -INFINITY, ll = 0.0f, y[4] = {};
-#pragma unroll 4
-                    for (int x = c_lo; x <= c_hi; ++x) {
-                        const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * (R * (kMaxD + 2));
-                        const float2 st = __ldcg(reinterpret_cast<const float2*>(px + R * kMaxD + 2 * r));
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(px + r * D + c));
-                        const float mn = fmaxf(mm, st.x);
-                        const float f0 = mm == -INFINITY ? 0.0f : exp2_fast(mm - mn);
-                        const float f1 = st.x == -INFINITY ? 0.0f : exp2_fast(st.x - mn);
-                        mm = mn;
-                        ll = ll * f0 + st.y * f1;
-                        y[0] = y[0] * f0 + v.x * f1;
-                        y[1] = y[1] * f0 + v.y * f1;
-                        y[2] = y[2] * f0 + v.z * f1;
-                        y[3] = y[3] * f0 + v.w * f1;
+                    // eight parts' loads in flight together; past the last, its own again with no weight
+                    for (int x0 = c_lo; x0 <= c_hi; x0 += 8) {
+                        float2 st[8];
+                        float4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int x = min(x0 + k, c_hi);
+                            const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * (R * (kMaxD + 2));
+                            st[k] = __ldcg(reinterpret_cast<const float2*>(px + R * kMaxD + 2 * r));
+                            v[k] = __ldcg(reinterpret_cast<const float4*>(px + r * D + c));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float mn = fmaxf(mm, st[k].x), base = mn == -INFINITY ? 0.0f : mn;
+                            const float f0 = exp2_fast(mm - base), f1 = x0 + k <= c_hi ? exp2_fast(st[k].x - base) : 0.0f;
+                            mm = mn;
+                            ll = ll * f0 + st[k].y * f1;
+                            y[0] = y[0] * f0 + v[k].x * f1;
+                            y[1] = y[1] * f0 + v[k].y * f1;
+                            y[2] = y[2] * f0 + v[k].z * f1;
+                            y[3] = y[3] * f0 + v[k].w * f1;
+                        }
                     }
                     store_row(r, c, y, mm, ll);
                 }

@@ -22,9 +22,7 @@
 //     nearly synchronous, and one thread's products cover the other's waits and
 //     commits (a thread a key tile, with twice the commits: 1800 clocks a pair of
 //     tiles against the products' 1152);
-//   * a warpgroup a key tile reads S^T whole, frees the buffer, exponentiates and
-//     adds.  (Two warpgroups a tile, one for each parity, have too few registers
-//     to read a tile whole and hold their buffer: 105 us for 512 tokens over 16k.)
+//   * a warpgroup a key tile reads S^T, exponentiates and adds.
 // Items are whole and dealt out in equal contiguous shares of their row tiles.
 #include <algorithm>
 
@@ -39,6 +37,7 @@ __device__ int g_mass_tiles_error;
 
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kChunk = 64 * kKeys * 2;
+constexpr int kItemCost = 3;                // row tiles' time that an item costs besides its own
 
 template <int D>
 struct Cfg {
@@ -73,7 +72,7 @@ struct KeyTileExtent {
         }
         int lo, hi;
         row_tiles(t, lo, hi);
-        t.units = max(hi - lo, 1);   // keys that nobody sees still decay
+        t.units = kItemCost + hi - lo;   // keys that nobody sees still decay
     }
     // row tiles [lo, hi): token i sees key j when j - (len - n) <= i (and i < that + window)
     __device__ __forceinline__ void row_tiles(const Item& t, int& lo, int& hi) const {
@@ -124,6 +123,13 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     }
     for (int r = threadIdx.x; r < kKeys; r += C::kThreads)
         write_step(smem + C::kSmemOne, r, 1.0f, 1.0f, 1.0f);
+    const int tokens = kRows / a.group, tile_rows = tokens * a.group;
+    // the rows of a Q tile that no copy fills (a group that does not divide 128) are 0: finite scores, which the lse
+    // step takes to no weight
+    for (int i = threadIdx.x; i < kSlots * NC * (kRows - tile_rows) * 8; i += C::kThreads) {
+        const int x = i / ((kRows - tile_rows) * 8), r = tile_rows + i / 8 % (kRows - tile_rows);
+        *reinterpret_cast<uint4*>(smem + C::kSmemRing + x * kChunk + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
     fence_proxy_async_smem();
     if (warp == C::kSoftWarps) {
         tmem_alloc(smem_u32(tmem_slot), 512);
@@ -136,7 +142,6 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     pdl_launch_dependents();
     pdl_wait();
 
-    const int tokens = kRows / a.group, tile_rows = tokens * a.group;
     const KeyTileExtent extent{a.group, a.window, NS * kKeys, tokens};
     int P;
     long long total, w0, w1;
@@ -301,7 +306,7 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         uint32_t it = 0;
         bool ok = true;
         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
-        const uint32_t skip = a.scale_log2 < 0.0f ? 0x7f800000u : 0xff800000u;   // times the scale: -inf
+        const float skip = a.scale_log2 < 0.0f ? INFINITY : -INFINITY;   // times the scale: -inf
         while (t.at < w1 && ok) {
             int lo, hi;
             extent.row_tiles(t, lo, hi);
@@ -325,34 +330,39 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 tc_fence_after();
                 const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(256 * me + 128 * odd);
                 const int tok0 = r * tokens;
-                // some column of the tile may not see some key of it (or is no row at all)
-                const bool masked = tok0 < k_lo + kKeys - 1 || tile_rows < kRows || (r + 1) * tile_rows > t.rows ||
+                // some column of the tile may not see some key of it (or is no row of the sequence)
+                const bool masked = tok0 < k_lo + kKeys - 1 || (r + 1) * tile_rows > t.rows ||
                                     (a.window > 0 && tok0 + tokens - 1 >= k_lo + a.window);
                 const int c0 = max(first - tok0, 0) * a.group, c1 = min(max(end - tok0, 0) * a.group, tile_rows);
-                uint32_t x[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld_x32(ts + 32u * i, x[i]);
+                // 32 columns at a time, the next ones on their way meanwhile
+                uint32_t x[2][32];
+                tmem_ld_x32(ts, x[0]);
                 tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S_EMPTY + odd));
-                if (masked) {   // (the lse step alone covers rows that weigh nothing, not scores that are not finite)
-#pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e < c0 || e >= c1) x[e >> 5][e & 31] = skip;
-                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if (i < 3) tmem_ld_x32(ts + 32u * (i + 1), x[(i + 1) & 1]);
                     float u[32];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        unpack2(mul2(pack2(__uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1])), scale2), u[e], u[e + 1]);
+                    for (int e = 0; e < 32; ++e) u[e] = __uint_as_float(x[i & 1][e]);
+                    if (masked) {   // (the lse step alone covers rows that weigh nothing, not scores that are not finite)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * i + e < c0 || 32 * i + e >= c1) u[e] = skip;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) unpack2(mul2(pack2(u[e], u[e + 1]), scale2), u[e], u[e + 1]);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) u[e] = exp2_fast(u[e]);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
 #pragma unroll
                         for (int y = 0; y < 4; ++y) sum[y] = add2(sum[y], pack2(u[e + 2 * y], u[e + 2 * y + 1]));
+                    if (i < 3) tmem_ld_wait();
+                    if (i == 2) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S_EMPTY + odd));
+                    }
                 }
             }
             if (!ok) break;
