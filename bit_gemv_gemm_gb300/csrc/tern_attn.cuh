@@ -4,6 +4,9 @@
 
 #include <math.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "tern_cache.cuh"
 #include "tern_mma.cuh"
 #include "tern_sm100.cuh"
@@ -191,12 +194,17 @@ __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent&
     return true;
 }
 
-// No call has more units than this (host: the lengths are on the device).
-inline long long most_units(const AttnArgs& a, int unit, int cost) {
+// The most shares that a call's work fills (host: the lengths are on the device;
+// no item has more units than this).  Where there are few items, each is cut into
+// at most sqrt(units) parts: a part costs the join about what a unit costs, so
+// units / parts + parts is least there (16 rows over one key head of 32k keys, 1000
+// strips: 16, 32, 48, 304 parts 35, 28, 29, 73 us; of 130k keys 103, 62, 51 us).
+inline long long most_shares(const AttnArgs& a, int unit, int cost, int min_units, long long shares) {
     const long long room = (long long)a.s.width * a.c.page_size;
     const long long keys = a.window > 0 && a.window + (long long)a.s.max_new < room ? a.window + (long long)a.s.max_new : room;
-    const double most = (double)a.s.B * a.c.kv_heads * a.tiles * (double)((keys + unit - 1) / unit + 1 + cost);
-    return most < 1e15 ? (long long)most : (long long)1e15;
+    const long long items = (long long)a.s.B * a.c.kv_heads * a.tiles, units = (keys + unit - 1) / unit + 1 + cost;
+    const double most = std::min((double)items * std::sqrt((double)units), (double)items * units / min_units + 1.0);
+    return most < (double)shares ? std::max((long long)most, 1LL) : shares;
 }
 
 // A cache array as the TMA sees it: [page][head][d / 64][slot][64 values], a
@@ -236,6 +244,23 @@ __device__ __forceinline__ void tma_load_cache_pair(uint32_t dst, const CUtensor
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+
+// One warp: zeroes the rows [r0, r1) of a chunk of 128-byte rows.  Rows of V that
+// no key of this call's stands in count as 0: those of boxes that are not read
+// before the boxes are, those past the last key inside a box after it has come.
+// (Tested row by row this took 10 us of a tile; rows are taken by their range.)
+__device__ __forceinline__ void zero_rows(unsigned char* chunk, int r0, int r1) {
+    for (int i = r0 * 8 + (int)(threadIdx.x & 31); i < r1 * 8; i += 32)
+        *reinterpret_cast<uint4*>(chunk + i * 16) = make_uint4(0, 0, 0, 0);
+}
+struct VRows {
+    int front, back, back_box;   // [0, front) and [back_box, tile) are not read, [back, back_box) holds no key
+    __device__ __forceinline__ VRows(int k0, int tile, int box_rows, int j0, int len) {
+        front = max((j0 & ~(box_rows - 1)) - k0, 0);   // (box_rows is a power of two)
+        back = min(len - k0, tile);
+        back_box = min((back + box_rows - 1) & ~(box_rows - 1), tile);
+    }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -368,7 +393,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, uns
     auto stat_of = [&](int x) {
         return __ldcg(reinterpret_cast<const float2*>(part_of(x) + (size_t)D * kTileRows + 2 * row));
     };
-    // four parts at a time, all their loads in flight together; past the last, its own again with no weight
+    // all loads in flight together; past the last part, its own again with no weight
     float mm = -INFINITY, ll = 0.0f;
     for (int x0 = c_lo; x0 <= c_hi; x0 += 4) {
         float2 st[4];
@@ -382,41 +407,45 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, uns
         }
     }
     const float base = mm == -INFINITY ? 0.0f : mm, inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    constexpr int W = D == 256 ? 2 : 3, COLS = D == 256 ? 64 : 32;   // parts and columns in flight
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-        float y[32] = {};
-#pragma unroll 1
-        for (int x0 = c_lo; x0 <= c_hi; x0 += 4) {
-            float4 v[4][8];
-            float f[4];
+    for (int c = 0; c < D; c += COLS) {
+        float4 y[COLS / 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int e = 0; e < COLS / 4; ++e) y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int x0 = c_lo; x0 <= c_hi; x0 += W) {
+            float4 v[W][COLS / 4];
+            float f[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
                 const int x = min(x0 + i, c_hi);
+                const float* p = part_of(x) + ((size_t)(c / 4) * kTileRows + row) * 4;
                 f[i] = stat_of(x).x;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[i][e] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + ((size_t)(c / 4 + e) * kTileRows + row) * 4));
+                for (int e = 0; e < COLS / 4; ++e)
+                    v[i][e] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)e * kTileRows * 4));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < W; ++i) {
                 f[i] = x0 + i <= c_hi ? exp2_fast(f[i] - base) : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[4 * e] = fmaf(v[i][e].x, f[i], y[4 * e]);
-                    y[4 * e + 1] = fmaf(v[i][e].y, f[i], y[4 * e + 1]);
-                    y[4 * e + 2] = fmaf(v[i][e].z, f[i], y[4 * e + 2]);
-                    y[4 * e + 3] = fmaf(v[i][e].w, f[i], y[4 * e + 3]);
+                for (int e = 0; e < COLS / 4; ++e) {
+                    y[e].x = fmaf(v[i][e].x, f[i], y[e].x);
+                    y[e].y = fmaf(v[i][e].y, f[i], y[e].y);
+                    y[e].z = fmaf(v[i][e].z, f[i], y[e].z);
+                    y[e].w = fmaf(v[i][e].w, f[i], y[e].w);
                 }
             }
         }
         if (live) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                dst[e] = make_uint4(pack_bf16(y[8 * e] * inv, y[8 * e + 1] * inv),
-                                    pack_bf16(y[8 * e + 2] * inv, y[8 * e + 3] * inv),
-                                    pack_bf16(y[8 * e + 4] * inv, y[8 * e + 5] * inv),
-                                    pack_bf16(y[8 * e + 6] * inv, y[8 * e + 7] * inv));
+            for (int e = 0; e < COLS / 8; ++e)
+                dst[e] = make_uint4(pack_bf16(y[2 * e].x * inv, y[2 * e].y * inv),
+                                    pack_bf16(y[2 * e].z * inv, y[2 * e].w * inv),
+                                    pack_bf16(y[2 * e + 1].x * inv, y[2 * e + 1].y * inv),
+                                    pack_bf16(y[2 * e + 1].z * inv, y[2 * e + 1].w * inv));
         }
     }
     if (live && a.lse) a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;

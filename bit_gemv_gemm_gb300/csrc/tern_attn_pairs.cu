@@ -32,8 +32,6 @@
 // (sequence, pair of row tiles, key head) items' 128-key tiles, a share a
 // cluster; parts meet in the workspace, and the warp that counts last for its
 // 32 rows adds them in order.
-#include <algorithm>
-
 #include "tern_attn.cuh"
 
 namespace tern {
@@ -181,7 +179,9 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     const int k0 = key0 + j * kKeys, k = k0 + box * box_rows;
                     // boxes that hold no key of these rows are not read; V's rows there count as 0
                     const bool use = lane < pieces && k < t.q.len && k + box_rows > t.j0;
-                    const bool part = is_v && (k0 + kKeys > t.q.len || k0 + box_rows <= t.j0);
+                    const VRows rows(k0, kKeys, box_rows, t.j0, t.q.len);
+                    const bool part = is_v && rows.back < rows.back_box;
+                    unsigned char* chunks = smem + C::kSmemRing + (it % kSlots) * (NC * kChunk);
                     const uint32_t used_boxes = __ballot_sync(0xffffffffu, use);
                     const uint32_t bytes = (uint32_t)__popc(used_boxes & ((1u << boxes) - 1u)) * box_rows * 128u;   // a chunk's
                     const int slot = (unsigned)k % (unsigned)a.c.page_size;
@@ -191,6 +191,14 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (!__all_sync(0xffffffffu, wait(empty_bar(it), slot_phase(it) ^ 1u))) {
                         ok = false;
                         break;
+                    }
+                    if (is_v && (rows.front > 0 || rows.back_box < kKeys)) {
+                        for (int x = 0; x < NC; ++x) {
+                            zero_rows(chunks + x * kChunk, 0, rows.front);
+                            zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
                     if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it), bytes * NC);
                     __syncwarp();
@@ -203,12 +211,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             break;
                         }
                         ++tails;
-                        for (int i = lane; i < kKeys * NC * 8; i += 32) {
-                            const int x = i / (kKeys * 8), r = i / 8 % kKeys, key = k0 + r;
-                            if (key >= t.q.len || (key / box_rows + 1) * box_rows <= t.j0)
-                                *reinterpret_cast<uint4*>(smem + C::kSmemRing + ((it % kSlots) * NC + x) * kChunk +
-                                                          r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
+                        for (int x = 0; x < NC; ++x) zero_rows(chunks + x * kChunk, rows.back, rows.back_box);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(full_bar(it));
@@ -497,7 +500,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
     }
     const int R = 2 * (kRows / a.group * a.group);
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
-    const long long P = std::min<long long>(sms / 2, (most_units(a, kKeys, kItemCost) + kMinTiles - 1) / kMinTiles);
+    const long long P = most_shares(a, kKeys, kItemCost, kMinTiles, sms / 2);
     return launch_pdl_clusters(attn_pairs_kernel<D>, 2, dim3((unsigned)(2 * P)), dim3(kThreads), C::kSmem, stream, mq, mk,
                                mv, a, box);
 }

@@ -361,7 +361,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
         attr_set[dev] = true;
     }
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
-    const long long P = std::min<long long>((long long)sms * C::kCtas, (most_units(a, kStrip, kItemCost) + kMinUnits - 1) / kMinUnits);
+    const long long P = most_shares(a, kStrip, kItemCost, kMinUnits, (long long)sms * C::kCtas);
     return launch_pdl(attn_rows_kernel<D>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mk, mv, a);
 }
 

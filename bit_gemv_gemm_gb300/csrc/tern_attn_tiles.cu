@@ -29,8 +29,6 @@
 // Work is shared out as in the rows kernel: equal contiguous shares of all
 // (sequence, row tile, key head) items' 128-key tiles; parts meet in the
 // workspace, and the warp that counts last for its 32 rows adds them in order.
-#include <algorithm>
-
 #include "tern_attn.cuh"
 
 namespace tern {
@@ -170,7 +168,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const int k0 = key0 + j * kKeys, k = k0 + box * box_rows;
                 // boxes that hold no key of these rows are not read; V's rows there count as 0
                 const bool use = c < NC && k < t.q.len && k + box_rows > t.j0;
-                const bool part = is_v && (k0 + kKeys > t.q.len || k0 + box_rows <= t.j0);
+                const VRows rows(k0, kKeys, box_rows, t.j0, t.q.len);
+                const bool part = is_v && rows.back < rows.back_box, unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
                 const uint32_t mine = __ballot_sync(0xffffffffu, use);
                 const uint32_t bytes = (uint32_t)__popc(mine & ((1u << boxes) - 1u)) * box_rows * 128u;   // a chunk's
                 const int slot = (unsigned)k % (unsigned)a.c.page_size;
@@ -179,6 +178,15 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (!__all_sync(0xffffffffu, wait(empty_bar(it + g), slot_phase(it + g) ^ 1u))) {
                         ok = false;
                         break;
+                    }
+                    unsigned char* chunks = smem + C::kSmemRing + ((it + g) % kSlots) * (CG * kChunk);
+                    if (unread) {
+                        for (int x = 0; x < CG; ++x) {
+                            zero_rows(chunks + x * kChunk, 0, rows.front);
+                            zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
                     if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it + g), bytes * CG);
                     __syncwarp();
@@ -193,13 +201,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         break;
                     }
                     ++tails;
-                    for (int i = lane; i < kKeys * NC * 8; i += 32) {
-                        const int x = i / (kKeys * 8), r = i / 8 % kKeys, key = k0 + r;
-                        if (key >= t.q.len || (key / box_rows + 1) * box_rows <= t.j0)
-                            *reinterpret_cast<uint4*>(smem + C::kSmemRing +
-                                                      (((it + x / CG) % kSlots) * CG + x % CG) * kChunk + r * 128 +
-                                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                    for (int x = 0; x < NC; ++x)
+                        zero_rows(smem + C::kSmemRing + (((it + x / CG) % kSlots) * CG + x % CG) * kChunk, rows.back,
+                                  rows.back_box);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
@@ -536,7 +540,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
     }
     const int R = kRows / a.group * a.group;
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
-    const long long P = std::min<long long>(sms, (most_units(a, kKeys, kItemCost) + kMinTiles - 1) / kMinTiles);
+    const long long P = most_shares(a, kKeys, kItemCost, kMinTiles, sms);
     return launch_pdl(attn_tiles_kernel<D>, dim3((unsigned)P), dim3(C::kThreads), C::kSmem, stream, true, mq, mk, mv, a,
                       box);
 }
