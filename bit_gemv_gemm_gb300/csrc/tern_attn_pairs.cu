@@ -68,6 +68,17 @@ struct Cfg {
 };
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys);
 
+// Where one role is in a ring of N slots.
+template <int N>
+struct Ring {
+    uint32_t slot, phase = 0;
+    __device__ __forceinline__ explicit Ring(uint32_t first) : slot(first) {}
+    __device__ __forceinline__ void skip(uint32_t n) {
+        slot += n;
+        if (slot >= N) slot -= N, phase ^= 1u;
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -80,9 +91,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     const uint32_t sbase = smem_u32(smem), bar0 = sbase + (uint32_t)C::kSmemBar;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     auto full_bar = [&](uint32_t i) { return bar((int)(i % kSlots)); };
-    auto empty_bar = [&](uint32_t i) { return bar(kSlots + (int)(i % kSlots)); };
     auto slot_phase = [&](uint32_t i) { return (i / kSlots) & 1u; };
-    auto slot_addr = [&](uint32_t i) { return sbase + (uint32_t)C::kSmemRing + (i % kSlots) * (uint32_t)(NC * kChunk); };
     enum { Q_FULL = 2 * kSlots, Q_EMPTY, S_FULL, S_EMPTY = S_FULL + NB, P_FULL = S_EMPTY + NB, O_EMPTY = P_FULL + NB, HAND, MERGE = HAND + 8, TAIL, DRAIN = TAIL + 2 };   // DRAIN: two
     static_assert(DRAIN + 2 == C::kBars, "barriers");
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
@@ -148,6 +157,9 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             const int boxes = kKeys / box_rows, pieces = NC * boxes;   // of a tile; this CTA brings half of them
             const int c = lane / boxes, box = lane - c * boxes;        // this lane's piece
             const bool mine = lane < pieces && lane / (pieces / 2) == rank;
+            const uint32_t piece = (uint32_t)(c * kChunk + box * box_rows * 128);
+            const bool page_boxes = box_rows == a.c.page_size;         // a box is a whole page
+            Ring<kSlots> ring(is_v ? 1 : 0);
             for (long long w = w0; w < w1 && ok;) {
                 const Segment seg = segment_of(extent, t, w, w1);
                 const int nt = seg.n, key0 = seg.first * kKeys;
@@ -169,30 +181,33 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             tma_load_q(sbase + (uint32_t)(x * kChunk), &tmap_q, t.hk * a.group, tok, x, bar(Q_FULL));
                     }
                 }
-                for (int j = 0; j < nt; ++j, ++n) {
-                    const uint32_t it = 2 * n + (is_v ? 1 : 0);
+                for (int j = 0; j < nt; ++j, ++n, ring.skip(2)) {
                     if (((j * boxes) & 31) == 0) {
                         ids = checked_page(ahead, a.c.pages, &g_attn_pairs_error);
                         ahead = raw_id(j * boxes + 32 + lane);
                     }
                     const int page = __shfl_sync(0xffffffffu, ids, (j * boxes + box) & 31);
                     const int k0 = key0 + j * kKeys, k = k0 + box * box_rows;
-                    // boxes that hold no key of these rows are not read; V's rows there count as 0
-                    const bool use = lane < pieces && k < t.q.len && k + box_rows > t.j0;
+                    const int slot = page_boxes ? 0 : (unsigned)k % (unsigned)a.c.page_size;
+                    bool use = lane < pieces, part = false, unread = false;
+                    uint32_t bytes = kKeys * 128u;   // a chunk's
                     const VRows rows(k0, kKeys, box_rows, t.j0, t.q.len);
-                    const bool part = is_v && rows.back < rows.back_box;
-                    unsigned char* chunks = smem + C::kSmemRing + (it % kSlots) * (NC * kChunk);
-                    const uint32_t used_boxes = __ballot_sync(0xffffffffu, use);
-                    const uint32_t bytes = (uint32_t)__popc(used_boxes & ((1u << boxes) - 1u)) * box_rows * 128u;   // a chunk's
-                    const int slot = (unsigned)k % (unsigned)a.c.page_size;
+                    if (k0 < t.j0 || k0 + kKeys > t.q.len) {
+                        // boxes that hold no key of these rows are not read; V's rows there count as 0
+                        use = use && k < t.q.len && k + box_rows > t.j0;
+                        bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, use) & ((1u << boxes) - 1u)) * box_rows * 128u;
+                        part = is_v && rows.back < rows.back_box;
+                        unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
+                    }
                     // (two barriers in turn: the other CTA may be one such tile ahead)
-                    const uint32_t tail = bar(TAIL + (int)(tails & 1u));
+                    const uint32_t tail = bar(TAIL + (int)(tails & 1u)), full = bar((int)ring.slot);
+                    unsigned char* chunks = smem + C::kSmemRing + ring.slot * (uint32_t)(NC * kChunk);
                     if (part && lane == 0) mbar_arrive_expect_tx(tail, bytes * NC);
-                    if (!__all_sync(0xffffffffu, wait(empty_bar(it), slot_phase(it) ^ 1u))) {
+                    if (!__all_sync(0xffffffffu, wait(bar(kSlots + (int)ring.slot), ring.phase ^ 1u))) {
                         ok = false;
                         break;
                     }
-                    if (is_v && (rows.front > 0 || rows.back_box < kKeys)) {
+                    if (unread) {
                         for (int x = 0; x < NC; ++x) {
                             zero_rows(chunks + x * kChunk, 0, rows.front);
                             zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
@@ -200,11 +215,10 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    if (!part && lane == 0) mbar_arrive_expect_tx(full_bar(it), bytes * NC);
+                    if (!part && lane == 0) mbar_arrive_expect_tx(full, bytes * NC);
                     __syncwarp();
                     if (use && mine)
-                        tma_load_cache_pair(slot_addr(it) + (uint32_t)(c * kChunk + box * box_rows * 128), map, slot, c,
-                                            t.hk, page, part ? tail : full_bar(it));
+                        tma_load_cache_pair(smem_u32(chunks) + piece, map, slot, c, t.hk, page, part ? tail : full);
                     if (part) {
                         if (!__all_sync(0xffffffffu, wait(tail, (tails >> 1) & 1u))) {
                             ok = false;
@@ -214,7 +228,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         for (int x = 0; x < NC; ++x) zero_rows(chunks + x * kChunk, rows.back, rows.back_box);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(full_bar(it));
+                        if (lane == 0) mbar_arrive(full);
                     }
                 }
                 w = seg.we;
@@ -234,52 +248,58 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             if (lane == 0) {
                 const bool is_pv = warp != kSoftWarps + 1;
                 constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, D) | kIdescBMnMajor;
-                uint32_t it = is_pv ? 1 : 0, used = 0, n = 0;   // slot of the next key tile; those taken part in so far
+                uint32_t used = 0;
+                Ring<kSlots> ring(is_pv ? 1 : 0);   // the next key tile's slot
+                Ring<NB> sb(0);                     // ... and its S
+                // between one tile's products and the next this thread spends some 600 of a tile's 1600
+                // clocks, waits that are over and commits; slots are counted along, not divided out, and
+                // both barriers are asked at once (heads of 64, 512 tokens over 32k: 173 -> 168 us)
+                const uint64_t qd0 = smem_desc_k_sw128(sbase), kd0 = smem_desc_k_sw128(sbase + (uint32_t)C::kSmemRing);
+                const uint64_t vd0 = smem_desc_mn_sw128(sbase + (uint32_t)C::kSmemRing, kChunk);
                 bool ok = true, issued = false;
                 auto need = [&](uint32_t b, uint32_t parity) {
                     if (ok && !wait(b, parity)) ok = false;
+                    return ok;
+                };
+                auto need2 = [&](uint32_t b, uint32_t parity, uint32_t b2, uint32_t parity2) {
+                    const bool r = mbar_try_wait(b, parity), r2 = mbar_try_wait(b2, parity2);
+                    if (!r) need(b, parity);
+                    if (!r2) need(b2, parity2);
                     return ok;
                 };
                 for (long long w = w0; w < w1 && ok;) {
                     const Segment seg = segment_of(extent, t, w, w1);
                     if (t.rows <= rank * tile_rows) {   // a pair's second row tile may be absent
                         // ... and its slots are released all the same
-                        for (int j = 0; j < seg.n && ok; ++j, it += 2)
-                            if (need(full_bar(it), slot_phase(it))) mma_commit_pair(empty_bar(it));
+                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(2))
+                            if (need(bar((int)ring.slot), ring.phase)) mma_commit_pair(bar(kSlots + (int)ring.slot));
                     } else if (seg.n > 0) {
                         if (!is_pv) need(bar(Q_FULL), used & 1u);
-                        for (int j = 0; j < seg.n && ok; ++j, it += 2, ++n) {
-                            const uint32_t buf = n % NB, ph = (n / NB) & 1u, addr = slot_addr(it);
+                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(2), sb.skip(1)) {
+                            const uint32_t s_tmem = tmem + C::kS + 128u * sb.slot, o_tmem = tmem + C::kO;
+                            const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(NC * kChunk >> 4));
                             if (!is_pv) {
-                                need(full_bar(it), slot_phase(it));
-                                need(bar(S_EMPTY + (int)buf), ph ^ 1u);   // the P that was over this S has been used
-                                if (!ok) break;
+                                // the P that was over this S has been used
+                                if (!need2(bar((int)ring.slot), ring.phase, bar(S_EMPTY + (int)sb.slot), sb.phase ^ 1u)) break;
                                 tc_fence_after();
 #pragma unroll
-                                for (int c = 0; c < NC; ++c) {
-                                    const uint64_t qd = smem_desc_k_sw128(sbase + (uint32_t)(c * kChunk));
-                                    const uint64_t kd = smem_desc_k_sw128(addr + (uint32_t)(c * kChunk));
+                                for (int c = 0; c < NC; ++c)
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
-                                        mma_f16_ss(tmem + C::kS + 128u * buf, qd + 2 * kk, kd + 2 * kk, kIdescQK,
-                                                   (c | kk) ? 1u : 0u);
-                                }
-                                mma_commit(bar(S_FULL + (int)buf));
-                                mma_commit_pair(empty_bar(it));
+                                        mma_f16_ss(s_tmem, qd0 + (uint64_t)(c * (kChunk >> 4) + 2 * kk),
+                                                   kd0 + at + (uint64_t)(c * (kChunk >> 4) + 2 * kk), kIdescQK, (c | kk) ? 1u : 0u);
+                                mma_commit(bar(S_FULL + (int)sb.slot));
                             } else {
-                                need(full_bar(it), slot_phase(it));
-                                need(bar(P_FULL + (int)buf), ph);
-                                if (j == 0) need(bar(O_EMPTY), (used & 1u) ^ 1u);   // the previous item's output has been read
-                                if (!ok) break;
+                                if (!need2(bar((int)ring.slot), ring.phase, bar(P_FULL + (int)sb.slot), sb.phase)) break;
+                                if (j == 0 && !need(bar(O_EMPTY), (used & 1u) ^ 1u)) break;   // the previous item's output has been read
                                 tc_fence_after();
-                                const uint64_t vd = smem_desc_mn_sw128(addr, kChunk);
 #pragma unroll
                                 for (int kk = 0; kk < kKeys / 16; ++kk)
-                                    mma_f16_ts(tmem + C::kO, tmem + C::kS + 128u * buf + 8u * kk,
-                                               vd + (uint64_t)(kk * (2048 >> 4)), kIdescPV, (j || kk) ? 1u : 0u);
-                                mma_commit(bar(S_EMPTY + (int)buf));
-                                mma_commit_pair(empty_bar(it));
+                                    mma_f16_ts(o_tmem, s_tmem + 8u * kk, vd0 + at + (uint64_t)(kk * (2048 >> 4)), kIdescPV,
+                                               (j || kk) ? 1u : 0u);
+                                mma_commit(bar(S_EMPTY + (int)sb.slot));
                             }
+                            mma_commit_pair(bar(kSlots + (int)ring.slot));
                             issued = true;
                         }
                         if (ok) {
