@@ -47,9 +47,9 @@ template <int D>
 struct Cfg {
     static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
     static constexpr int NS = D == 256 ? 1 : 2;             // streams: every NS-th key tile each
-    static constexpr int CG = D == 128 ? 2 : 1;             // chunks of a ring slot
+    static constexpr int CG = D == 64 ? 1 : 2;             // chunks of a ring slot
     static constexpr int NG = NC / CG;                      // slots of a K or V tile
-    static constexpr int kSlots = D == 64 ? 10 : D == 128 ? 5 : 8;
+    static constexpr int kSlots = D == 64 ? 10 : D == 128 ? 5 : 4;
     static constexpr int kSoftWarps = 4 * NS;
     // two streams: a third warpgroup (two TMA and two MMA warps) gives registers
     // to the softmax warps, which hold a row of S each: 256 x 208 + 128 x 88 =
@@ -293,14 +293,16 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     for (int j = 0; j < nt && ok; ++j, ++jobs) {
                         // the P that was over this S, two tiles back, has been used
                         if (!need(bar(S_EMPTY + (int)(jobs & 1u)), ((jobs >> 1) & 1u) ^ 1u)) break;
-                        for (int c = 0; c < NC; ++c) {
-                            if (!need(full_bar(it + c), slot_phase(it + c))) break;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            if (!need(full_bar(it + g), slot_phase(it + g))) break;
                             tc_fence_after();
-                            qk(jobs & 1u, c, slot_addr(it + c));
-                            mma_commit(empty_bar(it + c));
+#pragma unroll
+                            for (int c = 0; c < CG; ++c) qk(jobs & 1u, g * CG + c, slot_addr(it + g) + (uint32_t)(c * kChunk));
+                            if (g == NG - 1) mma_commit(bar(S_FULL + (int)(jobs & 1u)));
+                            mma_commit(empty_bar(it + g));
                         }
-                        mma_commit(bar(S_FULL + (int)(jobs & 1u)));
-                        it += 2 * NC;
+                        it += 2 * NG;
                     }
                     if (nt > 0 && ok) {
                         mma_commit(bar(Q_EMPTY));
@@ -308,17 +310,19 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                 } else {
                     for (int j = 0; j < nt && ok; ++j, ++jobs) {
-                        it += NC;
-                        for (int c = 0; c < NC; ++c) need(full_bar(it + c), slot_phase(it + c));
+                        it += NG;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) need(full_bar(it + g), slot_phase(it + g));
                         need(bar(P_FULL + (int)(jobs & 1u)), (jobs >> 1) & 1u);
                         if (j == 0) need(bar(O_EMPTY), (used & 1u) ^ 1u);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(0, jobs & 1u, slot_addr(it), j > 0);
+                        pv(0, jobs & 1u, slot_addr(it), j > 0);   // (its slots lie one behind the other)
                         mma_commit(bar(O_FULL));
                         mma_commit(bar(S_EMPTY + (int)(jobs & 1u)));
-                        for (int c = 0; c < NC; ++c) mma_commit(empty_bar(it + c));
-                        it += NC;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) mma_commit(empty_bar(it + g));
+                        it += NG;
                     }
                     if (nt > 0) ++used;
                 }
