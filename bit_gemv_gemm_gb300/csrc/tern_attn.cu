@@ -79,14 +79,19 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.counters = static_cast<unsigned*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
     const long long rows = (long long)a.s.max_new * a.group;
+    const long long room = (long long)a.s.width * a.c.page_size;
+    const long long keys = window > 0 && window < room ? window : room;   // that a row sees at most
     // few rows: bound by reading the cache and by latency, which suits mma.sync
     // and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
-    // 32k keys, 4 sequences: 106 us, against 115 from the rows kernel with 32 rows an item)
-    // and, past one row tile, pairs of CTAs with a row tile each
+    // 32k keys, 4 sequences: 95 us, against 115 from the rows kernel with 32 rows an item);
+    // past one row tile, pairs of CTAs with a row tile each.  Heads of 256 only gain by
+    // pairs over long keys, where L2's rate bounds single CTAs (512 tokens over 32k keys 243 ->
+    // 216 us, 2 x 300 over 10k 118 -> 113; over 1k or a window of 4096 2 to 7 % are lost to
+    // the second tile's waits)
+    const bool one = a.s.max_new <= 128 / a.group || (a.c.head_dim == 256 && keys < 8192);
     const cudaError_t e = rows <= 16 ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                          : a.s.max_new <= 128 / a.group || a.c.head_dim == 256
-                              ? launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                              : launch_attn_pairs(a, k_cache, v_cache, sms, (cudaStream_t)stream);
+                          : one      ? launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream)
+                                     : launch_attn_pairs(a, k_cache, v_cache, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

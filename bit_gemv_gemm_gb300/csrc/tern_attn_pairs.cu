@@ -47,7 +47,6 @@ constexpr int kItemCost = 5;                // key tiles' time that an item cost
                                             // slower for whole prompts, whose items are of unlike length)
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
-constexpr int kBuffers = 3;                 // of S
 // a third warpgroup (two TMA and two MMA warps) gives registers to the softmax
 // warps, which hold a row of S each: 256 x 208 + 128 x 88 = 384 x 168, what the
 // CTA was launched with
@@ -56,11 +55,14 @@ constexpr int kThreads = 384;
 template <int D>
 struct Cfg {
     static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
-    static constexpr int kSlots = D == 64 ? 12 : 6;         // tiles of K and V, in turn
-    static constexpr uint32_t kS = 0, kO = 128 * kBuffers;  // tensor memory: S (and P) at 128 b, then O
+    static constexpr int CG = D == 64 ? 1 : 2;              // chunks of a ring slot
+    static constexpr int NG = NC / CG;                      // slots of a K or V tile
+    static constexpr int kSlots = D == 64 ? 12 : D == 128 ? 6 : 4;   // K and V tiles, in turn
+    static constexpr int NB = D == 256 ? 2 : 3;             // buffers of S
+    static constexpr uint32_t kS = 0, kO = 128 * NB;        // tensor memory: S (and P) at 128 b, then O
     static constexpr size_t kSmemRing = (size_t)NC * kChunk;
-    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * NC * kChunk;
-    static constexpr int kBars = 2 * kSlots + 2 + 3 * kBuffers + 1 + 8 + 1 + 2 + 2;
+    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
+    static constexpr int kBars = 2 * kSlots + 2 + 3 * NB + 1 + 8 + 1 + 2 + 2;
     static constexpr size_t kSmemMisc = (kSmemBar + kBars * 8 + 15) / 16 * 16;
     static constexpr size_t kSmemM = kSmemMisc + 256;       // a row's maximum in use, and a warpgroup's sums
     static constexpr size_t kSmem = kSmemM + 2 * kRows * 4 + 1024;
@@ -84,14 +86,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const AttnArgs a, const int box_rows) {
     using C = Cfg<D>;
-    constexpr int NC = C::NC, NB = kBuffers, kSlots = C::kSlots;
+    constexpr int NC = C::NC, CG = C::CG, NG = C::NG, NB = C::NB, kSlots = C::kSlots;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem), bar0 = sbase + (uint32_t)C::kSmemBar;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    auto full_bar = [&](uint32_t i) { return bar((int)(i % kSlots)); };
-    auto slot_phase = [&](uint32_t i) { return (i / kSlots) & 1u; };
     enum { Q_FULL = 2 * kSlots, Q_EMPTY, S_FULL, S_EMPTY = S_FULL + NB, P_FULL = S_EMPTY + NB, O_EMPTY = P_FULL + NB, HAND, MERGE = HAND + 8, TAIL, DRAIN = TAIL + 2 };   // DRAIN: two
     static_assert(DRAIN + 2 == C::kBars, "barriers");
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
@@ -152,14 +152,14 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             // ------------------------------ TMA: Q and K, or V ------------------------------
             const bool is_v = warp != kSoftWarps;
             const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-            uint32_t n = 0, used = 0, tails = 0;   // key tiles so far; slot 2 n is K(n), 2 n + 1 V(n)
+            uint32_t n = 0, used = 0, tails = 0;   // key tiles, items, tiles past a sequence's end so far
             bool ok = true;
             const int boxes = kKeys / box_rows, pieces = NC * boxes;   // of a tile; this CTA brings half of them
             const int c = lane / boxes, box = lane - c * boxes;        // this lane's piece
             const bool mine = lane < pieces && lane / (pieces / 2) == rank;
-            const uint32_t piece = (uint32_t)(c * kChunk + box * box_rows * 128);
+            const uint32_t piece = (uint32_t)(c % CG * kChunk + box * box_rows * 128);   // in its slot
             const bool page_boxes = box_rows == a.c.page_size;         // a box is a whole page
-            Ring<kSlots> ring(is_v ? 1 : 0);
+            Ring<kSlots> ring(is_v ? NG : 0);   // K(0), V(0), K(1), ...
             for (long long w = w0; w < w1 && ok;) {
                 const Segment seg = segment_of(extent, t, w, w1);
                 const int nt = seg.n, key0 = seg.first * kKeys;
@@ -181,7 +181,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             tma_load_q(sbase + (uint32_t)(x * kChunk), &tmap_q, t.hk * a.group, tok, x, bar(Q_FULL));
                     }
                 }
-                for (int j = 0; j < nt; ++j, ++n, ring.skip(2)) {
+                for (int j = 0; j < nt; ++j, ++n, ring.skip(NG)) {
                     if (((j * boxes) & 31) == 0) {
                         ids = checked_page(ahead, a.c.pages, &g_attn_pairs_error);
                         ahead = raw_id(j * boxes + 32 + lane);
@@ -200,35 +200,42 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
                     }
                     // (two barriers in turn: the other CTA may be one such tile ahead)
-                    const uint32_t tail = bar(TAIL + (int)(tails & 1u)), full = bar((int)ring.slot);
-                    unsigned char* chunks = smem + C::kSmemRing + ring.slot * (uint32_t)(NC * kChunk);
+                    const uint32_t tail = bar(TAIL + (int)(tails & 1u)), first = ring.slot;
                     if (part && lane == 0) mbar_arrive_expect_tx(tail, bytes * NC);
-                    if (!__all_sync(0xffffffffu, wait(bar(kSlots + (int)ring.slot), ring.phase ^ 1u))) {
-                        ok = false;
-                        break;
-                    }
-                    if (unread) {
-                        for (int x = 0; x < NC; ++x) {
-                            zero_rows(chunks + x * kChunk, 0, rows.front);
-                            zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g, ring.skip(1)) {
+                        const uint32_t full = bar((int)ring.slot);
+                        unsigned char* chunks = smem + C::kSmemRing + ring.slot * (uint32_t)(CG * kChunk);
+                        if (!__all_sync(0xffffffffu, wait(bar(kSlots + (int)ring.slot), ring.phase ^ 1u))) {
+                            ok = false;
+                            break;
                         }
-                        fence_proxy_async_smem();
+                        if (unread) {
+                            for (int x = 0; x < CG; ++x) {
+                                zero_rows(chunks + x * kChunk, 0, rows.front);
+                                zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (!part && lane == 0) mbar_arrive_expect_tx(full, bytes * CG);
                         __syncwarp();
+                        if (use && mine && c / CG == g)
+                            tma_load_cache_pair(smem_u32(chunks) + piece, map, slot, c, t.hk, page, part ? tail : full);
                     }
-                    if (!part && lane == 0) mbar_arrive_expect_tx(full, bytes * NC);
-                    __syncwarp();
-                    if (use && mine)
-                        tma_load_cache_pair(smem_u32(chunks) + piece, map, slot, c, t.hk, page, part ? tail : full);
+                    if (!ok) break;
                     if (part) {
                         if (!__all_sync(0xffffffffu, wait(tail, (tails >> 1) & 1u))) {
                             ok = false;
                             break;
                         }
                         ++tails;
-                        for (int x = 0; x < NC; ++x) zero_rows(chunks + x * kChunk, rows.back, rows.back_box);
+                        for (int x = 0; x < NC; ++x)   // (a tile's slots lie one behind the other)
+                            zero_rows(smem + C::kSmemRing + (first * CG + x) * kChunk, rows.back, rows.back_box);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(full);
+                        if (lane == 0)
+                            for (int g = 0; g < NG; ++g) mbar_arrive(bar((int)first + g));
                     }
                 }
                 w = seg.we;
@@ -237,8 +244,10 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             if (!ok && lane == 0) {
                 fail();
                 // copies in flight land before the CTA goes away
-                for (uint32_t x = n < kSlots / 2 ? 0 : n - kSlots / 2; x <= n; ++x)
-                    (void)mbar_wait_drain(full_bar(2 * x + (is_v ? 1 : 0)), slot_phase(2 * x + (is_v ? 1 : 0)), 20000000ull);
+                constexpr uint32_t kTiles = kSlots / (2 * NG);
+                for (uint32_t x = n < kTiles ? 0 : n - kTiles; x <= n; ++x)
+                    for (uint32_t r = (2 * x + (is_v ? 1 : 0)) * NG, g = 0; g < NG; ++g, ++r)
+                        (void)mbar_wait_drain(bar((int)(r % kSlots)), (r / kSlots) & 1u, 20000000ull);
                 if (used) (void)mbar_wait_drain(bar(Q_FULL), (used - 1u) & 1u, 20000000ull);
                 if (is_v) (void)mbar_wait_drain(bar(TAIL + (int)(tails & 1u)), (tails >> 1) & 1u, 20000000ull);
             }
@@ -249,7 +258,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const bool is_pv = warp != kSoftWarps + 1;
                 constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, D) | kIdescBMnMajor;
                 uint32_t used = 0;
-                Ring<kSlots> ring(is_pv ? 1 : 0);   // the next key tile's slot
+                Ring<kSlots> ring(is_pv ? NG : 0);   // the next key tile's slot
                 Ring<NB> sb(0);                     // ... and its S
                 // between one tile's products and the next this thread spends some 600 of a tile's 1600
                 // clocks, waits that are over and commits; slots are counted along, not divided out, and
@@ -271,35 +280,45 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     const Segment seg = segment_of(extent, t, w, w1);
                     if (t.rows <= rank * tile_rows) {   // a pair's second row tile may be absent
                         // ... and its slots are released all the same
-                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(2))
-                            if (need(bar((int)ring.slot), ring.phase)) mma_commit_pair(bar(kSlots + (int)ring.slot));
+                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(NG))
+                            for (int g = 0; g < NG && ok; ++g, ring.skip(1))
+                                if (need(bar((int)ring.slot), ring.phase)) mma_commit_pair(bar(kSlots + (int)ring.slot));
                     } else if (seg.n > 0) {
                         if (!is_pv) need(bar(Q_FULL), used & 1u);
-                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(2), sb.skip(1)) {
+                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(NG), sb.skip(1)) {
                             const uint32_t s_tmem = tmem + C::kS + 128u * sb.slot, o_tmem = tmem + C::kO;
-                            const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(NC * kChunk >> 4));
                             if (!is_pv) {
                                 // the P that was over this S has been used
                                 if (!need2(bar((int)ring.slot), ring.phase, bar(S_EMPTY + (int)sb.slot), sb.phase ^ 1u)) break;
-                                tc_fence_after();
 #pragma unroll
-                                for (int c = 0; c < NC; ++c)
+                                for (int g = 0; g < NG; ++g, ring.skip(1)) {
+                                    if (g > 0 && !need(bar((int)ring.slot), ring.phase)) break;
+                                    tc_fence_after();
+                                    const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(CG * kChunk >> 4));
 #pragma unroll
-                                    for (int kk = 0; kk < 4; ++kk)
-                                        mma_f16_ss(s_tmem, qd0 + (uint64_t)(c * (kChunk >> 4) + 2 * kk),
-                                                   kd0 + at + (uint64_t)(c * (kChunk >> 4) + 2 * kk), kIdescQK, (c | kk) ? 1u : 0u);
-                                mma_commit(bar(S_FULL + (int)sb.slot));
+                                    for (int c = 0; c < CG; ++c)
+#pragma unroll
+                                        for (int kk = 0; kk < 4; ++kk)
+                                            mma_f16_ss(s_tmem, qd0 + (uint64_t)((g * CG + c) * (kChunk >> 4) + 2 * kk),
+                                                       kd0 + at + (uint64_t)(c * (kChunk >> 4) + 2 * kk), kIdescQK,
+                                                       (g | c | kk) ? 1u : 0u);
+                                    if (g == NG - 1) mma_commit(bar(S_FULL + (int)sb.slot));
+                                    mma_commit_pair(bar(kSlots + (int)ring.slot));
+                                }
                             } else {
                                 if (!need2(bar((int)ring.slot), ring.phase, bar(P_FULL + (int)sb.slot), sb.phase)) break;
+                                if (NG > 1 && !need(bar((int)ring.slot + NG - 1), ring.phase)) break;
                                 if (j == 0 && !need(bar(O_EMPTY), (used & 1u) ^ 1u)) break;   // the previous item's output has been read
                                 tc_fence_after();
+                                const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(CG * kChunk >> 4));
 #pragma unroll
                                 for (int kk = 0; kk < kKeys / 16; ++kk)
                                     mma_f16_ts(o_tmem, s_tmem + 8u * kk, vd0 + at + (uint64_t)(kk * (2048 >> 4)), kIdescPV,
                                                (j || kk) ? 1u : 0u);
                                 mma_commit(bar(S_EMPTY + (int)sb.slot));
+#pragma unroll
+                                for (int g = 0; g < NG; ++g, ring.skip(1)) mma_commit_pair(bar(kSlots + (int)ring.slot));
                             }
-                            mma_commit_pair(bar(kSlots + (int)ring.slot));
                             issued = true;
                         }
                         if (ok) {
@@ -527,12 +546,13 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
 
 }  // namespace
 
-size_t attn_pairs_workspace() { return (size_t)(kMaxSms / 2) * 2 * 2 * 4 * part_floats(128); }
+size_t attn_pairs_workspace() { return (size_t)(kMaxSms / 2) * 2 * 2 * 4 * part_floats(256); }
 
 cudaError_t launch_attn_pairs(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
     switch (a.c.head_dim) {
         case 64: return launch<64>(a, k, v, sms, stream);
-        default: return launch<128>(a, k, v, sms, stream);
+        case 128: return launch<128>(a, k, v, sms, stream);
+        default: return launch<256>(a, k, v, sms, stream);
     }
 }
 
