@@ -218,6 +218,28 @@ def test_long_context(tern):
     check_both(tern, Problem(4, [9001, 17], [5, 17], 8, 1, 128, 64, "nhd"))
 
 
+@pytest.mark.parametrize("page,layout,window", [(16, "nhd", 0), (48, "hnd", 0), (64, "hnd", 8200), (256, "nhd", 0)])
+@pytest.mark.parametrize("new", [33, 150, 300])
+def test_wide_heads_over_a_long_table(tern, page, layout, window, new):
+    """Heads of 256 take another kernel where the table has room for 8192 keys;
+    the second sequence's last row tile is alone, the third has one only."""
+    p = Problem(new, [new + 777, new + 130, 9, 2 * new], [new, new - 1, 9, 2], 8, 2, 256, page, layout,
+                wide_table=8192 // page)
+    check_attention(p, *run_attention(tern, p, window), window)
+
+
+@pytest.mark.parametrize("new", [40, 150])
+def test_wide_heads_with_a_growing_maximum(tern, new):
+    """The running maximum moves with every key tile: what was added is scaled down."""
+    p = Problem(new, [new + 1500], [new], 4, 1, 256, 64, wide_table=128, spread=1.0)
+    grow = torch.linspace(0, 24, p.lens[0])
+    for i in range(p.lens[0]):
+        pg, sl = int(p.table[0, i // p.page]), i % p.page
+        p.k[pg, :, sl] *= float(grow[i])
+    p.host = (p.host[0], f64(p.k), p.host[2], p.host[3])
+    check_attention(p, *run_attention(tern, p))
+
+
 @pytest.mark.parametrize("B", [1, 3, 200])
 def test_uniform_tokens_without_q_start(tern, B):
     p = Problem(B, [30 + 7 * b for b in range(B)], [2] * B, 4, 2, 64)
