@@ -15,16 +15,20 @@
 //     synchronous (a wait or a commit between products costs the thread about
 //     150 and 57 clocks that its own products do not cover: 110 clocks a 64-clock
 //     product from one thread), so each covers the other's;
-//   * S has three buffers, so QK runs ahead, and two softmax warpgroups take the tiles in turn, one
+//   * S has three buffers (two at D = 256, whose O takes half of tensor memory),
+//     so QK runs ahead, and two softmax warpgroups take the tiles in turn, one
 //     thread a row: read S, exponentiate, write P as bf16 over S's own columns.
 // The two warpgroups share a row's maximum in use: each hands it on as soon as
 // it has looked at its tile's scores, well before it has exponentiated them.  It
 // only moves when a score passes it by 2^8 (then O is rescaled, after the product
 // before has been added), so P and the sums stay below 2^8 of their largest term.
 // Each warpgroup keeps its own sum, in fp32; they meet at the item's end.
-// One CTA with two row tiles and one S each instead (512 tokens over 32k keys, 32
-// heads of 128): a row tile's chain QK - softmax - PV - QK took 3950 clocks a
-// key tile, against 2048 of products: 245 us.
+// 512 tokens over 32k keys, 32 heads of 128: 191 us, 1.41 PFLOP/s, a key tile in 1600
+// clocks against 1024 of products.  What bounds it is the two issuing threads'
+// round, a tile's waits, products, commits and the loop: without the exponentials,
+// the maximum or the conversions the time is the same.  (One CTA with two row tiles
+// and one S each instead: a row tile's chain QK - softmax - PV - QK took 3950 clocks
+// a key tile, against 2048 of products: 245 us.)
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
@@ -43,8 +47,9 @@ __device__ int g_attn_pairs_error;
 
 constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
-constexpr int kItemCost = 5;                // key tiles' time that an item costs besides its own (measured: 3 and 8 are
-                                            // slower for whole prompts, whose items are of unlike length)
+// key tiles' time that an item costs besides its own (four prompts of up to 4000
+// tokens, whose items are of unlike length: 188, 170, 155, 149, 156, 151 us with 2 to 7)
+constexpr int kItemCost = 5;
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
 // a third warpgroup (two TMA and two MMA warps) gives registers to the softmax

@@ -1,6 +1,6 @@
 // tern_attn_tiles.cu -- attention of query rows that fill one row tile a key
-// head or less (verify steps, short chunks), and of heads of 256 values, on the
-// tcgen05 tensor cores.
+// head or less (verify steps, short chunks), and of heads of 256 values over
+// fewer than 8192 keys, on the tcgen05 tensor cores.
 //
 // A row tile is 128 packed rows (128 / group tokens, every head of the group),
 // so one K and V tile serves all the heads that share it.  A CTA takes a row tile
@@ -22,7 +22,10 @@
 // (tensor memory is open to it).  Such calls are bound by reading the cache, and
 // warps without a live row do no arithmetic.  At D = 256, where one O takes half
 // of tensor memory, there is one stream with two S buffers: one thread issues QK,
-// ahead by a tile, the other PV.
+// ahead by a tile, the other PV.  Row tiles that read the same keys are then
+// bound by L2's rate, 8.5 TB/s (2 x 300 tokens, window of 4096: 58 us), and a
+// verify step by the cache's (4 x 5 tokens over 32k keys, 8 key heads of 128: 95 us,
+// 5.5 TB/s, the last 10 us one join).
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
@@ -40,7 +43,7 @@ __device__ int g_attn_tiles_error;
 
 constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
-constexpr int kItemCost = 3;                // key tiles' time that an item costs besides its own (about 3.5 us)
+constexpr int kItemCost = 3;                // key tiles' time that an item costs besides its own (2 and 4: within 3 %)
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 
 template <int D>
