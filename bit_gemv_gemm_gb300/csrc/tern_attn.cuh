@@ -372,20 +372,28 @@ __device__ __forceinline__ void emit_row(const AttnArgs& a, bool whole, float* p
     if (!whole) __stcg(reinterpret_cast<float2*>(part + (size_t)D * kTileRows + 2 * row), make_float2(m2, l));
 }
 
-// A warp has stored its 32 rows' part; the one that counts last into the
-// item's counter adds the parts of all shares, in their order.  `counter` and
-// `first` are those of the row tile in share 0; a share has two parts, `stride`
-// floats apart.
-template <int D, int COST>
-__device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, unsigned* counter, const float* first,
-                                           size_t stride, int row, bool live, long long orow, long long total, int P) {
+// A warp has stored its 32 rows' part and counts it into the item's counter:
+// true if it was the last, which then adds the parts of all shares.  `counter`
+// is that of the rows in share 0.
+template <int COST>
+__device__ __forceinline__ bool count_part(const Item& t, unsigned* counter, long long total, int P) {
     __threadfence();
     __syncwarp();
     const int c_lo = unit_owner(total, P, t.at + COST), c_hi = unit_owner(total, P, t.at + t.units - 1);
     unsigned last = 0;
     if ((threadIdx.x & 31) == 0)
         last = atomicInc(counter + 8 * c_lo, (unsigned)(c_hi - c_lo)) == (unsigned)(c_hi - c_lo);
-    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    return __shfl_sync(0xffffffffu, last, 0) != 0;
+}
+
+// Adds the parts of all shares in their order, columns [c0, c1) of one row a
+// thread; `first` is the row tile's part in share 0, a share has two, `stride`
+// floats apart.
+constexpr int join_columns(int D) { return D == 256 ? 64 : 32; }   // at a time
+template <int D, int COST>
+__device__ __forceinline__ void add_parts(const AttnArgs& a, const Item& t, const float* first, size_t stride, int row,
+                                          bool live, long long orow, long long total, int P, int c0, int c1) {
+    const int c_lo = unit_owner(total, P, t.at + COST), c_hi = unit_owner(total, P, t.at + t.units - 1);
     __threadfence();
     // (an item's first share may have begun before it: its part is then in its second slot)
     const int late = unit_begin(total, P, c_lo) >= t.at ? 0 : 1;
@@ -407,9 +415,9 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, uns
         }
     }
     const float base = mm == -INFINITY ? 0.0f : mm, inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-    constexpr int W = D == 256 ? 2 : 3, COLS = D == 256 ? 64 : 32;   // parts and columns in flight
+    constexpr int W = D == 256 ? 2 : 3, COLS = join_columns(D);   // parts and columns in flight
 #pragma unroll 1
-    for (int c = 0; c < D; c += COLS) {
+    for (int c = c0; c < c1; c += COLS) {
         float4 y[COLS / 4];
 #pragma unroll
         for (int e = 0; e < COLS / 4; ++e) y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -448,7 +456,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const Item& t, uns
                                     pack_bf16(y[2 * e + 1].z * inv, y[2 * e + 1].w * inv));
         }
     }
-    if (live && a.lse) a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
+    if (live && a.lse && c0 == 0) a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
 }
 
 struct MassArgs {

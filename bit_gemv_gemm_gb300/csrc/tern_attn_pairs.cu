@@ -501,9 +501,10 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(O_EMPTY));
                     }
-                    if (!seg.whole && !idle)
-                        join_parts<D, kItemCost>(a, t, a.counters + 4 * rank + quad, a.partial + rank * part_floats(D),
-                                                 kPart, row, live, orow, total, P);
+                    if (!seg.whole && !idle &&
+                        count_part<kItemCost>(t, a.counters + 4 * rank + quad, total, P))
+                        add_parts<D, kItemCost>(a, t, a.partial + rank * part_floats(D), kPart, row, live, orow, total, P, 0,
+                                                D);
                 }
                 first_tile += (uint32_t)nt;
             }
