@@ -83,7 +83,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     const long long keys = window > 0 && window < room ? window : room;   // that a row sees at most
     // few rows: bound by reading the cache and by latency, which suits mma.sync
     // and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
-    // 32k keys, 4 sequences: 95 us, against 115 from the rows kernel with 32 rows an item);
+    // 32k keys, 4 sequences: 92 us, against 115 from the rows kernel with 32 rows an item);
     // past one row tile, pairs of CTAs with a row tile each.  Heads of 256 only gain by
     // pairs over long keys, where L2's rate bounds single CTAs (512 tokens over 32k keys 243 ->
     // 216 us, 2 x 300 over 10k 118 -> 113; over 1k or a window of 4096 2 to 7 % are lost to

@@ -24,8 +24,8 @@
 // of tensor memory, there is one stream with two S buffers: one thread issues QK,
 // ahead by a tile, the other PV.  Row tiles that read the same keys are then
 // bound by L2's rate, 8.5 TB/s (2 x 300 tokens, window of 4096: 58 us), and a
-// verify step by the cache's (4 x 5 tokens over 32k keys, 8 key heads of 128: 95 us,
-// 5.5 TB/s, the last 10 us one join).
+// verify step by the cache's (4 x 5 tokens over 32k keys, 8 key heads of 128: 92 us,
+// 5.7 TB/s, the last 8 us the joins).
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
