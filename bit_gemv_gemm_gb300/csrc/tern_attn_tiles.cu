@@ -387,7 +387,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (k0 + kKeys - 1 > p_lo || (a.window > 0 && k0 <= p_hi - a.window)) {
 #pragma unroll
                         for (int i = 0; i < 128; ++i)
-                            if (k0 + i > hi || k0 + i <= lo) x[i >> 5][i & 31] = 0xff800000u;
+                            if (i > hi - k0) x[i >> 5][i & 31] = 0xff800000u;
+                        if (a.window > 0)   // (apart: both in one test took whole prompts 153 us, not 142)
+#pragma unroll
+                            for (int i = 0; i < 128; ++i)
+                                if (i <= lo - k0) x[i >> 5][i & 31] = 0xff800000u;
                     }
                     float mx[4];
 #pragma unroll

@@ -333,8 +333,8 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(256 * me + 128 * odd);
                 const int tok0 = r * tokens;
                 // some column of the tile may not see some key of it (or is no row of the sequence)
-                const bool masked = tok0 < k_lo + kKeys - 1 || (r + 1) * tile_rows > t.rows ||
-                                    (a.window > 0 && tok0 + tokens - 1 >= k_lo + a.window);
+                const bool ends = (r + 1) * tile_rows > t.rows || (a.window > 0 && tok0 + tokens - 1 >= k_lo + a.window);
+                const bool masked = ends || tok0 < k_lo + kKeys - 1;
                 const int c0 = max(first - tok0, 0) * a.group, c1 = min(max(end - tok0, 0) * a.group, tile_rows);
                 // 32 columns at a time, the next ones on their way meanwhile
                 uint32_t x[2][32];
@@ -349,7 +349,11 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (masked) {   // (the lse step alone covers rows that weigh nothing, not scores that are not finite)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (32 * i + e < c0 || 32 * i + e >= c1) u[e] = skip;
+                            if (32 * i + e < c0) u[e] = skip;
+                        if (ends)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * i + e >= c1) u[e] = skip;
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) unpack2(mul2(pack2(u[e], u[e + 1]), scale2), u[e], u[e + 1]);
