@@ -23,7 +23,7 @@
 // only moves when a score passes it by 2^8 (then O is rescaled, after the product
 // before has been added), so P and the sums stay below 2^8 of their largest term.
 // Each warpgroup keeps its own sum, in fp32; they meet at the item's end.
-// 512 tokens over 32k keys, 32 heads of 128: 191 us, 1.41 PFLOP/s, a key tile in 1600
+// 512 tokens over 32k keys, 32 heads of 128: 189 us, 1.43 PFLOP/s, a key tile in 1600
 // clocks against 1024 of products.  What bounds it is the two issuing threads'
 // round, a tile's waits, products, commits and the loop: without the exponentials,
 // the maximum or the conversions the time is the same.  (One CTA with two row tiles
@@ -48,7 +48,7 @@ __device__ int g_attn_pairs_error;
 constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
 // key tiles' time that an item costs besides its own (four prompts of up to 4000
-// tokens, whose items are of unlike length: 188, 170, 155, 149, 156, 151 us with 2 to 7)
+// tokens, whose items are of unlike length: 188, 170, 155, 149, 156, 151 us with 2 to 7; now 142)
 constexpr int kItemCost = 5;
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
