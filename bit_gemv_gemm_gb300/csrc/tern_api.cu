@@ -90,7 +90,7 @@ tern_status tern_device_error(int* code) {
                                             read_rope_device_error, read_mass_rows_device_error,
                                             read_mass_tiles_device_error, read_attn_rows_device_error,
                                             read_attn_tiles_device_error,
-                                            read_attn_pairs_device_error, read_evict_device_error};
+                                            read_attn_chunk_device_error, read_evict_device_error};
     for (auto* read : readers) {
         int c = 0;
         if (read(&c) != cudaSuccess) return TERN_ERR_CUDA;

@@ -41,7 +41,7 @@ extern "C" size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new
     if (B < 1 || T < 0 || max_new < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return kAttnCounterBytes + std::max({attn_rows_workspace(), attn_tiles_workspace(), attn_pairs_workspace()});
+    return kAttnCounterBytes + std::max({attn_rows_workspace(), attn_tiles_workspace(), attn_chunk_workspace()});
 }
 
 extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, const void* k_cache,
@@ -79,19 +79,15 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.counters = static_cast<unsigned*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
     const long long rows = (long long)a.s.max_new * a.group;
-    const long long room = (long long)a.s.width * a.c.page_size;
-    const long long keys = window > 0 && window < room ? window : room;   // that a row sees at most
     // few rows: bound by reading the cache and by latency, which suits mma.sync
     // and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
     // 32k keys, 4 sequences: 92 us, against 115 from the rows kernel with 32 rows an item);
-    // past one row tile, pairs of CTAs with a row tile each.  Heads of 256 only gain by
-    // pairs over long keys, where L2's rate bounds single CTAs (512 tokens over 32k keys 243 ->
-    // 216 us, 2 x 300 over 10k 118 -> 113; over 1k or a window of 4096 2 to 7 % are lost to
-    // the second tile's waits)
-    const bool one = a.s.max_new <= 128 / a.group || (a.c.head_dim == 256 && keys < 8192);
+    // past one row tile the kernel with three S buffers, which at heads of 256 has room
+    // for two only and gains nothing (512 tokens over 32k keys: 245 us against 241)
+    const bool one = a.s.max_new <= 128 / a.group || a.c.head_dim == 256;
     const cudaError_t e = rows <= 16 ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
                           : one      ? launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                                     : launch_attn_pairs(a, k_cache, v_cache, sms, (cudaStream_t)stream);
+                                     : launch_attn_chunk(a, k_cache, v_cache, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

@@ -230,17 +230,6 @@ __device__ __forceinline__ void tma_load_cache(uint32_t dst, const CUtensorMap* 
         "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(slot), "r"(chunk), "r"(head), "r"(page), "r"(bar)
         : "memory");
 }
-// The same into both CTAs of a pair: the same place of each's shared memory, the
-// same barrier of each.
-__device__ __forceinline__ void tma_load_cache_pair(uint32_t dst, const CUtensorMap* m, int slot, int chunk, int head,
-                                                    int page, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-        "%3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(slot), "r"(chunk), "r"(head), "r"(page), "r"(bar),
-        "h"((unsigned short)3)
-        : "memory");
-}
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -479,9 +468,9 @@ cudaError_t launch_mass_rows(const MassArgs& a, const void* k, int sms, cudaStre
 cudaError_t launch_mass_tiles(const MassArgs& a, const void* k, int sms, cudaStream_t stream);
 cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
-cudaError_t launch_attn_pairs(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
+cudaError_t launch_attn_chunk(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 size_t attn_rows_workspace();
 size_t attn_tiles_workspace();
-size_t attn_pairs_workspace();
+size_t attn_chunk_workspace();
 
 }  // namespace tern

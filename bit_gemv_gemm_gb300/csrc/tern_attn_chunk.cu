@@ -1,41 +1,36 @@
-// tern_attn_pairs.cu -- attention of many query rows a key head (prompt chunks,
-// more than one row tile) on the tcgen05 tensor cores, by pairs of CTAs.
+// tern_attn_chunk.cu -- attention of many query rows a key head (prompt chunks,
+// more than one row tile, heads of 64 and 128) on the tcgen05 tensor cores.
 //
 // A row tile is 128 packed rows (128 / group tokens, every head of the group),
-// so one K and V tile serves all the heads that share it.  The two CTAs of a
-// cluster keep a row tile each, against the same stream of 128-key tiles: each
-// brings half of every K and V tile and writes it into both (TMA multicast), so
-// L2 gives each tile once for 256 rows.  In a CTA:
-//   * a TMA warp brings Q and its halves of K, another its halves of V, in
-//     chunks of 64 head values x 128 keys, through one ring.  A copy takes a warp
-//     about 110 clocks to issue and a page id some 700 to look up, hence two
-//     warps, and ids fetched 32 boxes ahead;
+// so one K and V tile serves all the heads that share it.  A CTA takes a row tile
+// through a run of 128-key tiles:
+//   * a TMA warp brings Q and K, another V, in chunks of 64 head values x 128
+//     keys, through one ring.  A copy takes a warp about 110 clocks to issue and a
+//     page id some 700 to look up, hence two warps, and ids fetched 32 boxes ahead;
 //   * one thread issues S = Q K^T (both operands in shared memory, K-major),
 //     another O += P V (P in tensor memory, V MN-major).  Issuing is nearly
 //     synchronous (a wait or a commit between products costs the thread about
 //     150 and 57 clocks that its own products do not cover: 110 clocks a 64-clock
 //     product from one thread), so each covers the other's;
-//   * S has three buffers (two at D = 256, whose O takes half of tensor memory),
-//     so QK runs ahead, and two softmax warpgroups take the tiles in turn, one
-//     thread a row: read S, exponentiate, write P as bf16 over S's own columns.
+//   * S has three buffers, so QK runs ahead, and two softmax warpgroups take the
+//     tiles in turn, one thread a row: read S, exponentiate, write P as bf16 over
+//     S's own columns.
 // The two warpgroups share a row's maximum in use: each hands it on as soon as
 // it has looked at its tile's scores, well before it has exponentiated them.  It
 // only moves when a score passes it by 2^8 (then O is rescaled, after the product
 // before has been added), so P and the sums stay below 2^8 of their largest term.
 // Each warpgroup keeps its own sum, in fp32; they meet at the item's end.
-// 512 tokens over 32k keys, 32 heads of 128: 189 us, 1.43 PFLOP/s, a key tile in 1600
-// clocks against 1024 of products.  What bounds it is the two issuing threads'
-// round, a tile's waits, products, commits and the loop: without the exponentials,
-// the maximum or the conversions the time is the same.  (One CTA with two row tiles
-// and one S each instead: a row tile's chain QK - softmax - PV - QK took 3950 clocks
-// a key tile, against 2048 of products: 245 us.)
+// 512 tokens over 32k keys, 32 heads of 128: 202 us, 1.34 PFLOP/s, 10 TB/s from L2;
+// row tiles that read the same keys each fetch them.  (TMA multicast to pairs of
+// CTAs took 191 us there and 149 us for whole prompts that now take 175; a library
+// that several GPUs load has no multicast loads.  The tiles kernel's two streams
+// take 243 and 176, and 241 us for heads of 256, where this scheme takes 245.)
 // Slots past a sequence's last key may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
 // Work is shared out as in the rows kernel: equal contiguous shares of all
-// (sequence, pair of row tiles, key head) items' 128-key tiles, a share a
-// cluster; parts meet in the workspace, and the warp that counts last for its
-// 32 rows adds them in order.
+// (sequence, row tile, key head) items' 128-key tiles; parts meet in the workspace,
+// and the warp that counts last for its 32 rows adds them in order.
 #include "tern_attn.cuh"
 
 namespace tern {
@@ -43,13 +38,14 @@ namespace {
 
 using namespace sm100;
 
-__device__ int g_attn_pairs_error;
+__device__ int g_attn_chunk_error;
 
 constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
 // key tiles' time that an item costs besides its own (four prompts of up to 4000
-// tokens, whose items are of unlike length: 188, 170, 155, 149, 156, 151 us with 2 to 7; now 142)
-constexpr int kItemCost = 5;
+// tokens, whose items are of unlike length: 219, 209, 194, 188, 181, 186 us with 2, 3, 4,
+// 5, 7, 10; four of up to 2000, heads of 128: 100, 92, 93, 93, 95, 96; the first now 175)
+constexpr int kItemCost = 7;
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
 // a third warpgroup (two TMA and two MMA warps) gives registers to the softmax
@@ -60,14 +56,15 @@ constexpr int kThreads = 384;
 template <int D>
 struct Cfg {
     static constexpr int NC = D / 64;                       // chunks of a K, V or Q tile
-    static constexpr int CG = D == 64 ? 1 : 2;              // chunks of a ring slot
-    static constexpr int NG = NC / CG;                      // slots of a K or V tile
-    static constexpr int kSlots = D == 64 ? 12 : D == 128 ? 6 : 4;   // K and V tiles, in turn
-    static constexpr int NB = D == 256 ? 2 : 3;             // buffers of S
+    static constexpr int kTile = NC * kChunk;
+    static constexpr int kSlots = D == 64 ? 12 : 6;         // K and V tiles, in turn
+    // K and V have a warp each that waits for its own slots alone: a slot has to be always the same one's
+    static_assert(kSlots % 2 == 0, "K's slots and V's");
+    static constexpr int NB = 3;                            // buffers of S
     static constexpr uint32_t kS = 0, kO = 128 * NB;        // tensor memory: S (and P) at 128 b, then O
-    static constexpr size_t kSmemRing = (size_t)NC * kChunk;
-    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * CG * kChunk;
-    static constexpr int kBars = 2 * kSlots + 2 + 3 * NB + 1 + 8 + 1 + 2 + 2;
+    static constexpr size_t kSmemRing = (size_t)kTile;
+    static constexpr size_t kSmemBar = kSmemRing + (size_t)kSlots * kTile;
+    static constexpr int kBars = 2 * kSlots + 2 + 3 * NB + 1 + 8 + 1 + 1 + 2;
     static constexpr size_t kSmemMisc = (kSmemBar + kBars * 8 + 15) / 16 * 16;
     static constexpr size_t kSmemM = kSmemMisc + 256;       // a row's maximum in use, and a warpgroup's sums
     static constexpr size_t kSmem = kSmemM + 2 * kRows * 4 + 1024;
@@ -88,16 +85,16 @@ struct Ring {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const AttnArgs a, const int box_rows) {
     using C = Cfg<D>;
-    constexpr int NC = C::NC, CG = C::CG, NG = C::NG, NB = C::NB, kSlots = C::kSlots;
+    constexpr int NC = C::NC, NB = C::NB, kSlots = C::kSlots, kTile = C::kTile;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem), bar0 = sbase + (uint32_t)C::kSmemBar;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    enum { Q_FULL = 2 * kSlots, Q_EMPTY, S_FULL, S_EMPTY = S_FULL + NB, P_FULL = S_EMPTY + NB, O_EMPTY = P_FULL + NB, HAND, MERGE = HAND + 8, TAIL, DRAIN = TAIL + 2 };   // DRAIN: two
+    enum { Q_FULL = 2 * kSlots, Q_EMPTY, S_FULL, S_EMPTY = S_FULL + NB, P_FULL = S_EMPTY + NB, O_EMPTY = P_FULL + NB, HAND, MERGE = HAND + 8, TAIL, DRAIN };   // DRAIN: two
     static_assert(DRAIN + 2 == C::kBars, "barriers");
     long long* sm_scan = reinterpret_cast<long long*>(smem + C::kSmemMisc);   // [8 + warps]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm_scan + 8 + kThreads / 32);
@@ -105,12 +102,10 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     float* sm_m = reinterpret_cast<float*>(smem + C::kSmemM);
     float* sm_l = sm_m + kRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kBars; ++i) {
             int count = 1;
-            if (i >= kSlots && i < 2 * kSlots) count = 2;   // both CTAs are done with a slot
             if ((i >= P_FULL && i < P_FULL + NB) || i == O_EMPTY || i == MERGE) count = 4;
             mbar_init(bar(i), count);
         }
@@ -126,25 +121,22 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();   // the pair's barriers are ready for each other
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
     pdl_wait();
 
     const int tile_rows = kRows / a.group * a.group;   // whole tokens
-    const int R = 2 * tile_rows;
-    const RowTileExtent<kKeys, kItemCost> extent{R, a.group, a.window};
-    const int share = (int)blockIdx.x / 2;
+    const RowTileExtent<kKeys, kItemCost> extent{tile_rows, a.group, a.window};
     int P;
     long long total, w0, w1;
     Item t;
-    const bool busy = find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, share, (int)gridDim.x / 2, sm_scan,
-                                           &g_attn_pairs_error, total, P, w0, w1, t);
+    const bool busy = find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, (int)blockIdx.x, (int)gridDim.x,
+                                           sm_scan, &g_attn_chunk_error, total, P, w0, w1, t);
     auto fail = [&] {
         if (!*abort_flag) {
             *abort_flag = 1;
-            report_device_error(&g_attn_pairs_error, TERN_DEVERR_ATTN_WAIT);
+            report_device_error(&g_attn_chunk_error, TERN_DEVERR_ATTN_WAIT);
         }
     };
     auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, abort_flag, kAttnWaitNs); };
@@ -159,12 +151,11 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
             uint32_t n = 0, used = 0, tails = 0;   // key tiles, items, tiles past a sequence's end so far
             bool ok = true;
-            const int boxes = kKeys / box_rows, pieces = NC * boxes;   // of a tile; this CTA brings half of them
-            const int c = lane / boxes, box = lane - c * boxes;        // this lane's piece
-            const bool mine = lane < pieces && lane / (pieces / 2) == rank;
-            const uint32_t piece = (uint32_t)(c % CG * kChunk + box * box_rows * 128);   // in its slot
+            const int boxes = kKeys / box_rows;                        // of a chunk
+            const int c = lane / boxes, box = lane - c * boxes;        // this lane's piece of a tile
+            const uint32_t piece = (uint32_t)(c * kChunk + box * box_rows * 128);   // in its slot
             const bool page_boxes = box_rows == a.c.page_size;         // a box is a whole page
-            Ring<kSlots> ring(is_v ? NG : 0);   // K(0), V(0), K(1), ...
+            Ring<kSlots> ring(is_v ? 1 : 0);   // K(0), V(0), K(1), ...
             for (long long w = w0; w < w1 && ok;) {
                 const Segment seg = segment_of(extent, t, w, w1);
                 const int nt = seg.n, key0 = seg.first * kKeys;
@@ -175,26 +166,25 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     return x < nt * boxes && k < t.q.len && k + box_rows > t.j0 ? trow[(unsigned)k / (unsigned)a.c.page_size] : 0;
                 };
                 int ids = 0, ahead = raw_id(lane);
-                const bool active = t.rows > rank * tile_rows;
-                if (!is_v && nt > 0 && active) {
+                if (!is_v && nt > 0) {
                     if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY), (used & 1u) ^ 1u))) { ok = false; break; }
                     ++used;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(Q_FULL), (uint32_t)(NC * tile_rows * 128));
-                        const int tok = t.q.q0 + (t.rt * R + rank * tile_rows) / a.group;
+                        const int tok = t.q.q0 + t.rt * (tile_rows / a.group);
                         for (int x = 0; x < NC; ++x)
                             tma_load_q(sbase + (uint32_t)(x * kChunk), &tmap_q, t.hk * a.group, tok, x, bar(Q_FULL));
                     }
                 }
-                for (int j = 0; j < nt; ++j, ++n, ring.skip(NG)) {
+                for (int j = 0; j < nt; ++j, ++n, ring.skip(2)) {
                     if (((j * boxes) & 31) == 0) {
-                        ids = checked_page(ahead, a.c.pages, &g_attn_pairs_error);
+                        ids = checked_page(ahead, a.c.pages, &g_attn_chunk_error);
                         ahead = raw_id(j * boxes + 32 + lane);
                     }
                     const int page = __shfl_sync(0xffffffffu, ids, (j * boxes + box) & 31);
                     const int k0 = key0 + j * kKeys, k = k0 + box * box_rows;
                     const int slot = page_boxes ? 0 : (unsigned)k % (unsigned)a.c.page_size;
-                    bool use = lane < pieces, part = false, unread = false;
+                    bool use = c < NC, part = false, unread = false;
                     uint32_t bytes = kKeys * 128u;   // a chunk's
                     const VRows rows(k0, kKeys, box_rows, t.j0, t.q.len);
                     if (k0 < t.j0 || k0 + kKeys > t.q.len) {
@@ -204,57 +194,48 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         part = is_v && rows.back < rows.back_box;
                         unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
                     }
-                    // (two barriers in turn: the other CTA may be one such tile ahead)
-                    const uint32_t tail = bar(TAIL + (int)(tails & 1u)), first = ring.slot;
-                    if (part && lane == 0) mbar_arrive_expect_tx(tail, bytes * NC);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g, ring.skip(1)) {
-                        const uint32_t full = bar((int)ring.slot);
-                        unsigned char* chunks = smem + C::kSmemRing + ring.slot * (uint32_t)(CG * kChunk);
-                        if (!__all_sync(0xffffffffu, wait(bar(kSlots + (int)ring.slot), ring.phase ^ 1u))) {
-                            ok = false;
-                            break;
-                        }
-                        if (unread) {
-                            for (int x = 0; x < CG; ++x) {
-                                zero_rows(chunks + x * kChunk, 0, rows.front);
-                                zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                        if (!part && lane == 0) mbar_arrive_expect_tx(full, bytes * CG);
-                        __syncwarp();
-                        if (use && mine && c / CG == g)
-                            tma_load_cache_pair(smem_u32(chunks) + piece, map, slot, c, t.hk, page, part ? tail : full);
+                    const uint32_t full = part ? bar(TAIL) : bar((int)ring.slot);
+                    unsigned char* chunks = smem + C::kSmemRing + ring.slot * (uint32_t)kTile;
+                    if (!__all_sync(0xffffffffu, wait(bar(kSlots + (int)ring.slot), ring.phase ^ 1u))) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
+                    if (unread) {
+                        for (int x = 0; x < NC; ++x) {
+                            zero_rows(chunks + x * kChunk, 0, rows.front);
+                            zero_rows(chunks + x * kChunk, rows.back_box, kKeys);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes * NC);
+                    __syncwarp();
+                    if (use) tma_load_cache(smem_u32(chunks) + piece, map, slot, c, t.hk, page, full);
                     if (part) {
-                        if (!__all_sync(0xffffffffu, wait(tail, (tails >> 1) & 1u))) {
+                        if (!__all_sync(0xffffffffu, wait(full, tails & 1u))) {
                             ok = false;
                             break;
                         }
                         ++tails;
-                        for (int x = 0; x < NC; ++x)   // (a tile's slots lie one behind the other)
-                            zero_rows(smem + C::kSmemRing + (first * CG + x) * kChunk, rows.back, rows.back_box);
+                        for (int x = 0; x < NC; ++x) zero_rows(chunks + x * kChunk, rows.back, rows.back_box);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0)
-                            for (int g = 0; g < NG; ++g) mbar_arrive(bar((int)first + g));
+                        if (lane == 0) mbar_arrive(bar((int)ring.slot));
                     }
                 }
                 w = seg.we;
-                if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_pairs_error);
+                if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_chunk_error);
             }
             if (!ok && lane == 0) {
                 fail();
                 // copies in flight land before the CTA goes away
-                constexpr uint32_t kTiles = kSlots / (2 * NG);
-                for (uint32_t x = n < kTiles ? 0 : n - kTiles; x <= n; ++x)
-                    for (uint32_t r = (2 * x + (is_v ? 1 : 0)) * NG, g = 0; g < NG; ++g, ++r)
-                        (void)mbar_wait_drain(bar((int)(r % kSlots)), (r / kSlots) & 1u, 20000000ull);
+                constexpr uint32_t kTiles = kSlots / 2;
+                for (uint32_t x = n < kTiles ? 0 : n - kTiles; x <= n; ++x) {
+                    const uint32_t r = 2 * x + (is_v ? 1 : 0);
+                    (void)mbar_wait_drain(bar((int)(r % kSlots)), (r / kSlots) & 1u, 20000000ull);
+                }
                 if (used) (void)mbar_wait_drain(bar(Q_FULL), (used - 1u) & 1u, 20000000ull);
-                if (is_v) (void)mbar_wait_drain(bar(TAIL + (int)(tails & 1u)), (tails >> 1) & 1u, 20000000ull);
+                if (is_v) (void)mbar_wait_drain(bar(TAIL), tails & 1u, 20000000ull);
             }
             __syncwarp();
         } else {
@@ -263,7 +244,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const bool is_pv = warp != kSoftWarps + 1;
                 constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, D) | kIdescBMnMajor;
                 uint32_t used = 0;
-                Ring<kSlots> ring(is_pv ? NG : 0);   // the next key tile's slot
+                Ring<kSlots> ring(is_pv ? 1 : 0);   // the next key tile's slot
                 Ring<NB> sb(0);                     // ... and its S
                 // between one tile's products and the next this thread spends some 600 of a tile's 1600
                 // clocks, waits that are over and commits; slots are counted along, not divided out, and
@@ -283,47 +264,34 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 };
                 for (long long w = w0; w < w1 && ok;) {
                     const Segment seg = segment_of(extent, t, w, w1);
-                    if (t.rows <= rank * tile_rows) {   // a pair's second row tile may be absent
-                        // ... and its slots are released all the same
-                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(NG))
-                            for (int g = 0; g < NG && ok; ++g, ring.skip(1))
-                                if (need(bar((int)ring.slot), ring.phase)) mma_commit_pair(bar(kSlots + (int)ring.slot));
-                    } else if (seg.n > 0) {
+                    if (seg.n > 0) {
                         if (!is_pv) need(bar(Q_FULL), used & 1u);
-                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(NG), sb.skip(1)) {
+                        for (int j = 0; j < seg.n && ok; ++j, ring.skip(2), sb.skip(1)) {
                             const uint32_t s_tmem = tmem + C::kS + 128u * sb.slot, o_tmem = tmem + C::kO;
+                            const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(kTile >> 4));
                             if (!is_pv) {
                                 // the P that was over this S has been used
                                 if (!need2(bar((int)ring.slot), ring.phase, bar(S_EMPTY + (int)sb.slot), sb.phase ^ 1u)) break;
+                                tc_fence_after();
 #pragma unroll
-                                for (int g = 0; g < NG; ++g, ring.skip(1)) {
-                                    if (g > 0 && !need(bar((int)ring.slot), ring.phase)) break;
-                                    tc_fence_after();
-                                    const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(CG * kChunk >> 4));
+                                for (int c = 0; c < NC; ++c)
 #pragma unroll
-                                    for (int c = 0; c < CG; ++c)
-#pragma unroll
-                                        for (int kk = 0; kk < 4; ++kk)
-                                            mma_f16_ss(s_tmem, qd0 + (uint64_t)((g * CG + c) * (kChunk >> 4) + 2 * kk),
-                                                       kd0 + at + (uint64_t)(c * (kChunk >> 4) + 2 * kk), kIdescQK,
-                                                       (g | c | kk) ? 1u : 0u);
-                                    if (g == NG - 1) mma_commit(bar(S_FULL + (int)sb.slot));
-                                    mma_commit_pair(bar(kSlots + (int)ring.slot));
-                                }
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        mma_f16_ss(s_tmem, qd0 + (uint64_t)(c * (kChunk >> 4) + 2 * kk),
+                                                   kd0 + at + (uint64_t)(c * (kChunk >> 4) + 2 * kk), kIdescQK,
+                                                   (c | kk) ? 1u : 0u);
+                                mma_commit(bar(S_FULL + (int)sb.slot));
                             } else {
                                 if (!need2(bar((int)ring.slot), ring.phase, bar(P_FULL + (int)sb.slot), sb.phase)) break;
-                                if (NG > 1 && !need(bar((int)ring.slot + NG - 1), ring.phase)) break;
                                 if (j == 0 && !need(bar(O_EMPTY), (used & 1u) ^ 1u)) break;   // the previous item's output has been read
                                 tc_fence_after();
-                                const uint64_t at = (uint64_t)(ring.slot * (uint32_t)(CG * kChunk >> 4));
 #pragma unroll
                                 for (int kk = 0; kk < kKeys / 16; ++kk)
                                     mma_f16_ts(o_tmem, s_tmem + 8u * kk, vd0 + at + (uint64_t)(kk * (2048 >> 4)), kIdescPV,
                                                (j || kk) ? 1u : 0u);
                                 mma_commit(bar(S_EMPTY + (int)sb.slot));
-#pragma unroll
-                                for (int g = 0; g < NG; ++g, ring.skip(1)) mma_commit_pair(bar(kSlots + (int)ring.slot));
                             }
+                            mma_commit(bar(kSlots + (int)ring.slot));
                             issued = true;
                         }
                         if (ok) {
@@ -332,7 +300,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         }
                     }
                     w = seg.we;
-                    if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_pairs_error);
+                    if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_chunk_error);
                 }
                 if (!ok) {
                     fail();
@@ -362,14 +330,14 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         auto handed = [&](uint32_t n) { return all_wait(HAND + (int)(n & 1u) * 4 + quad, (n >> 1) & 1u); };
         for (long long w = w0; w < w1 && ok;) {
             const Segment seg = segment_of(extent, t, w, w1);
-            const int nt = seg.n, rows = min(tile_rows, t.rows - rank * tile_rows);   // of this CTA's row tile
-            if (!seg.skip && rows > 0) {
-                const int r = t.rt * R + rank * tile_rows + row;   // packed row of the sequence
+            const int nt = seg.n, rows = t.rows;
+            if (!seg.skip) {
+                const int r = t.rt * tile_rows + row;   // packed row of the sequence
                 const bool live = row < rows, idle = quad * 32 >= rows;
                 const int p = t.q.len - t.q.n + r / a.group;
                 const int hi = live ? p : -1, lo = a.window > 0 ? p - a.window : -1;
-                const int p_lo = t.q.len - t.q.n + (t.rt * R + rank * tile_rows) / a.group;
-                const int p_hi = t.q.len - t.q.n + (t.rt * R + rank * tile_rows + rows - 1) / a.group;
+                const int p_lo = t.q.len - t.q.n + t.rt * tile_rows / a.group;
+                const int p_hi = t.q.len - t.q.n + (t.rt * tile_rows + rows - 1) / a.group;
                 const int key0 = seg.first * kKeys;
                 float m = -INFINITY, l = 0.0f;   // l is relative to m, the maximum in use when this warpgroup last looked
                 for (int j = 0; j < nt && ok; ++j) {
@@ -488,8 +456,7 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     const float m2 = m * scale;   // -inf stays
                     const long long orow = (long long)(t.q.q0 + r / a.group) * a.q_heads + t.hk * a.group + r % a.group;
-                    constexpr size_t kPart = 2 * part_floats(D);   // both row tiles
-                    float* part = a.partial + (size_t)(2 * share + (w == w0 ? 0 : 1)) * kPart + rank * part_floats(D);
+                    float* part = a.partial + (size_t)(2 * blockIdx.x + (w == w0 ? 0 : 1)) * part_floats(D);
                     if (!idle)
                         emit_row<D>(a, seg.whole, part, row, live, orow, m2, l, [&](int c, uint32_t (&o)[32]) {
                             if (nt > 0) {
@@ -506,14 +473,13 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         if (lane == 0) mbar_arrive(bar(O_EMPTY));
                     }
                     if (!seg.whole && !idle &&
-                        count_part<kItemCost>(t, a.counters + 4 * rank + quad, total, P))
-                        add_parts<D, kItemCost>(a, t, a.partial + rank * part_floats(D), kPart, row, live, orow, total, P, 0,
-                                                D);
+                        count_part<kItemCost>(t, a.counters + quad, total, P))
+                        add_parts<D, kItemCost>(a, t, a.partial, part_floats(D), row, live, orow, total, P, 0, D);
                 }
                 first_tile += (uint32_t)nt;
             }
             w = seg.we;
-            if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_pairs_error);
+            if (w < w1) next_item(a.s, a.c, extent, a.tiles, t, &g_attn_chunk_error);
         }
         if (!ok && lane == 0) fail();
         __syncwarp();
@@ -521,7 +487,6 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();   // nothing of the other CTA's comes here any more
     if (warp == kSoftWarps + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -531,9 +496,8 @@ attn_pairs_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 template <int D>
 cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream_t stream) {
     using C = Cfg<D>;
-    // page_size is a multiple of 16; a tile is at least two pieces, one a CTA
-    int box = D == 64 ? 64 : 128;
-    while (a.c.page_size % box) box >>= 1;
+    int box = 128;
+    while (a.c.page_size % box) box >>= 1;   // page_size is a multiple of 16
     CUtensorMap mq, mk, mv;
     if (!make_q_map(&mq, a.q, a.q_stride, a.q_heads, a.s.T, D, a.group, kRows / a.group) ||
         !make_cache_map(&mk, k, a.c, box, 1) || !make_cache_map(&mv, v, a.c, box, 1))
@@ -542,35 +506,33 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_pairs_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)C::kSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int R = 2 * (kRows / a.group * a.group);
+    const int R = kRows / a.group * a.group;
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
-    const long long P = most_shares(a, kKeys, kItemCost, kMinTiles, sms / 2);
-    return launch_pdl_clusters(attn_pairs_kernel<D>, 2, dim3((unsigned)(2 * P)), dim3(kThreads), C::kSmem, stream, mq, mk,
-                               mv, a, box);
+    const long long P = most_shares(a, kKeys, kItemCost, kMinTiles, sms);
+    return launch_pdl(attn_chunk_kernel<D>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mq, mk, mv, a, box);
 }
 
 }  // namespace
 
-size_t attn_pairs_workspace() { return (size_t)(kMaxSms / 2) * 2 * 2 * 4 * part_floats(256); }
+size_t attn_chunk_workspace() { return (size_t)kMaxSms * 2 * 4 * part_floats(128); }
 
-cudaError_t launch_attn_pairs(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
+cudaError_t launch_attn_chunk(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
     switch (a.c.head_dim) {
         case 64: return launch<64>(a, k, v, sms, stream);
-        case 128: return launch<128>(a, k, v, sms, stream);
-        default: return launch<256>(a, k, v, sms, stream);
+        default: return launch<128>(a, k, v, sms, stream);
     }
 }
 
-cudaError_t read_attn_pairs_device_error(int* code) {
+cudaError_t read_attn_chunk_device_error(int* code) {
     int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_pairs_error, sizeof(int));
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_chunk_error, sizeof(int));
     if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_attn_pairs_error, &zero, sizeof(int));
+    return cudaMemcpyToSymbol(g_attn_chunk_error, &zero, sizeof(int));
 }
 
 }  // namespace tern

@@ -1,6 +1,6 @@
 // tern_attn_tiles.cu -- attention of query rows that fill one row tile a key
-// head or less (verify steps, short chunks), and of heads of 256 values over
-// fewer than 8192 keys, on the tcgen05 tensor cores.
+// head or less (verify steps, short chunks), and of any number at heads of 256
+// values, on the tcgen05 tensor cores.
 //
 // A row tile is 128 packed rows (128 / group tokens, every head of the group),
 // so one K and V tile serves all the heads that share it.  A CTA takes a row tile

@@ -40,7 +40,7 @@ cudaError_t read_mass_rows_device_error(int* code);
 cudaError_t read_mass_tiles_device_error(int* code);
 cudaError_t read_attn_rows_device_error(int* code);
 cudaError_t read_attn_tiles_device_error(int* code);
-cudaError_t read_attn_pairs_device_error(int* code);
+cudaError_t read_attn_chunk_device_error(int* code);
 cudaError_t read_evict_device_error(int* code);
 // One-CTA kernels that run a bounded wait nothing completes (tern_wait_selftest).
 cudaError_t launch_flag_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
