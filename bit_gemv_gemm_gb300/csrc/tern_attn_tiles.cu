@@ -288,9 +288,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         }
                         ++it;
                     }
-                    if (nt > 0 && ok) {   // (one key tile, the second stream: nothing to wait for)
-                        mma_commit(bar(O_FULL + me));
-                        if (me >= nt) mbar_arrive(bar(Q_EMPTY));
+                    if (nt > 0 && ok) {
+                        // a stream without a tile of this item says nothing of its O: no P of its warpgroup
+                        // came first, so the barrier could run two phases ahead of that warpgroup
+                        if (me < nt) mma_commit(bar(O_FULL + me));
+                        else mbar_arrive(bar(Q_EMPTY));
                         ++used;
                     }
                 } else if (me == 0) {
@@ -350,7 +352,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t to = tmem + lanes + C::kO + (uint32_t)(D * s);
-        uint32_t sc = 0, oc = 0, merges = 0, joins = 0;   // S and O tiles, merged and joined items seen
+        // S tiles and finished O's of this stream, items with keys, merged and joined items
+        uint32_t sc = 0, oc = 0, items = 0, merges = 0, joins = 0;
         const bool flip = a.scale_log2 < 0.0f;
         const float scale = fabsf(a.scale_log2);
         bool ok = true;
@@ -455,7 +458,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 }
                 if (!ok) break;
                 const long long orow = (long long)(t.q.q0 + r / a.group) * a.q_heads + t.hk * a.group + r % a.group;
-                if (nt > 0) {
+                if (nt > 0) ++items;
+                if (nt > s) {
                     oc += kWide ? (uint32_t)nt : 1u;
                     // (with two S buffers the product before the last may be running too)
                     bool done = !kWide || nt < 2 || wait(bar(O_FULL + s), (oc - 2u) & 1u);
@@ -469,7 +473,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     float2* stat = reinterpret_cast<float2*>(smem + C::kSmemStat);
                     if (s == 1) {
                         // the first stream has read what the last item left here
-                        if (oc > 1 && !__all_sync(0xffffffffu, wait(bar(O_EMPTY + 1), oc & 1u))) { ok = false; break; }
+                        if (items > 1 && !__all_sync(0xffffffffu, wait(bar(O_EMPTY + 1), items & 1u))) { ok = false; break; }
                         stat[row] = make_float2(m2, l);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(MERGE));
