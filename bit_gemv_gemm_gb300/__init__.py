@@ -155,6 +155,35 @@ def workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
+# What a call allocates itself has to be ready on the stream that the call runs on,
+# which need not be the current one: memory that was freed on the current stream
+# may still be in use there, and a fill there is not ordered before the kernel.
+
+def _there(stream):
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on `stream`."""
+    if stream is None:
+        return workspace(nbytes, device)
+    with _there(stream):
+        return workspace(nbytes, device)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream`, which the current stream will use too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _there(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream()
+    if t.is_cuda and here.cuda_stream != stream.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 # ---------------------------------------------------------------------------
 # packing
 # ---------------------------------------------------------------------------
@@ -167,7 +196,7 @@ def pack(t: torch.Tensor, codes: torch.Tensor | None = None, bad_count: torch.Te
     entries outside {-1, 0, +1} is added to it."""
     N, K = t.shape
     if codes is None:
-        codes = torch.empty((N, K // 16), dtype=torch.int32, device=t.device)
+        codes = _new((N, K // 16), torch.int32, t.device, stream)
     _covers(codes=(codes, N * (K // 16)), bad_count=(bad_count, 1))
     bp = _dev(bad_count, torch.int32, "bad_count") if bad_count is not None else None
     _check("tern_pack", lib().tern_pack(_dev(t, torch.int8, "t"), N, K, _dev(codes, torch.int32, "codes"),
@@ -179,7 +208,7 @@ def scales_from_g64(s64: torch.Tensor, K: int, mismatch: torch.Tensor | None = N
     """Scales of the group-size-64 pack (fp16 [N, K/64], each g128 scale
     repeated) -> g128 scales fp16 [N, K/128]; differing halves are counted."""
     N = s64.shape[0]
-    out = torch.empty((N, K // 128), dtype=torch.float16, device=s64.device)
+    out = _new((N, K // 128), torch.float16, s64.device, stream)
     _covers(s64=(s64, N * (K // 64)), mismatch=(mismatch, 1))
     mp = _dev(mismatch, torch.int32, "mismatch") if mismatch is not None else None
     _check("tern_scales_from_g64", lib().tern_scales_from_g64(_dev(s64, torch.float16, "s64"), N, K,
@@ -203,7 +232,7 @@ def bin_pack(t: torch.Tensor, words: torch.Tensor | None = None, bad_count: torc
     words [N, K/32] (as int32 storage), bit k%32 of word k/32 set for +1."""
     N, K = t.shape
     if words is None:
-        words = torch.empty((N, K // 32), dtype=torch.int32, device=t.device)
+        words = _new((N, K // 32), torch.int32, t.device, stream)
     _covers(words=(words, N * (K // 32)), bad_count=(bad_count, 1))
     bp = _dev(bad_count, torch.int32, "bad_count") if bad_count is not None else None
     _check("tern_bin_pack", lib().tern_bin_pack(_dev(t, torch.int8, "t"), N, K, _dev(words, torch.int32, "words"),
@@ -218,7 +247,7 @@ def f3_pack(t: torch.Tensor, packed: torch.Tensor | None = None, bad_count: torc
     N, K = t.shape
     nbytes = int(lib().tern_f3_packed_bytes(N, K))
     if packed is None:
-        packed = torch.empty((N, 26 * (K // 128)), dtype=torch.uint8, device=t.device)
+        packed = _new((N, 26 * (K // 128)), torch.uint8, t.device, stream)
     _covers(packed=(packed, nbytes), bad_count=(bad_count, 1))
     bp = _dev(bad_count, torch.int32, "bad_count") if bad_count is not None else None
     _check("tern_f3_pack", lib().tern_f3_pack(_dev(t, torch.int8, "t"), N, K, _dev(packed, torch.uint8, "packed"),
@@ -233,7 +262,7 @@ def f3_gemv(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, y: torc
     M, K = x.shape
     N = packed.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new((M, N), torch.float32, x.device, stream)
     _covers(packed=(packed, N * 26 * (K // 128)), scales=(scales, N * (K // 128)), y=(y, M * N))
     _check("tern_f3_gemv", lib().tern_f3_gemv(
         _dev(x, torch.bfloat16, "x"), _dev(packed, torch.uint8, "packed"), _dev(scales, torch.float16, "scales"),
@@ -294,10 +323,10 @@ def gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: torch.Te
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new((M, N), torch.float32, x.device, stream)
     _covers(codes=(codes, N * (K // 16)), scales=(scales, N * (K // 128)), y=(y, M * N))
     if ws is None:
-        ws = workspace(gemv_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemv_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_gemv", lib().tern_gemv(
         _dev(x, torch.bfloat16, "x"), _dev(codes, torch.int32, "codes"), _dev(scales, torch.float16, "scales"),
         _dev(y, torch.float32, "y"), M, N, K, _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
@@ -311,10 +340,10 @@ def bin_gemv(x: torch.Tensor, words: torch.Tensor, scales: torch.Tensor, y: torc
     M, K = x.shape
     N = words.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new((M, N), torch.float32, x.device, stream)
     _covers(words=(words, N * (K // 32)), scales=(scales, N * (K // 128)), y=(y, M * N))
     if ws is None:
-        ws = workspace(gemv_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemv_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_bin_gemv", lib().tern_bin_gemv(
         _dev(x, torch.bfloat16, "x"), _dev(words, torch.int32, "words"), _dev(scales, torch.float16, "scales"),
         _dev(y, torch.float32, "y"), M, N, K, _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
@@ -328,13 +357,13 @@ def gemv_pair(x: torch.Tensor, codes_a: torch.Tensor, scales_a: torch.Tensor, co
     M, K = x.shape
     Na, Nb = codes_a.shape[0], codes_b.shape[0]
     if y_a is None:
-        y_a = torch.empty((M, Na), dtype=torch.float32, device=x.device)
+        y_a = _new((M, Na), torch.float32, x.device, stream)
     if y_b is None:
-        y_b = torch.empty((M, Nb), dtype=torch.float32, device=x.device)
+        y_b = _new((M, Nb), torch.float32, x.device, stream)
     _covers(codes_a=(codes_a, Na * (K // 16)), scales_a=(scales_a, Na * (K // 128)), y_a=(y_a, M * Na),
             codes_b=(codes_b, Nb * (K // 16)), scales_b=(scales_b, Nb * (K // 128)), y_b=(y_b, M * Nb))
     if ws is None:
-        ws = workspace(int(lib().tern_gemv_pair_workspace_bytes(M, Na, Nb, K)), x.device)
+        ws = _scratch(int(lib().tern_gemv_pair_workspace_bytes(M, Na, Nb, K)), x.device, stream)
     _check("tern_gemv_pair", lib().tern_gemv_pair(
         _dev(x, torch.bfloat16, "x"), _dev(codes_a, torch.int32, "codes_a"), _dev(scales_a, torch.float16, "scales_a"),
         _dev(y_a, torch.float32, "y_a"), Na, _dev(codes_b, torch.int32, "codes_b"),
@@ -349,7 +378,7 @@ def gemv_noalloc(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: 
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new((M, N), torch.float32, x.device, stream)
     _covers(codes=(codes, N * (K // 16)), scales=(scales, N * (K // 128)), y=(y, M * N))
     _check("tern_gemv_noalloc", lib().tern_gemv_noalloc(
         _dev(x, torch.bfloat16, "x"), _dev(codes, torch.int32, "codes"), _dev(scales, torch.float16, "scales"),
@@ -361,7 +390,7 @@ def fwht(x: torch.Tensor, signs: torch.Tensor, y: torch.Tensor | None = None, st
     """y (bf16 [M, K]) = H_4096 (signs * x) / 64 per 4096-block of the last dimension."""
     M, K = x.shape
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     _covers(signs=(signs, K), y=(y, M * K))
     _check("tern_fwht", lib().tern_fwht(_dev(x, torch.bfloat16, "x"), _dev(signs, torch.int8, "signs"),
                                         _dev(y, torch.bfloat16, "y"), M, K, _stream(stream)))
@@ -374,10 +403,10 @@ def fwht_gemm(x: torch.Tensor, signs: torch.Tensor, codes: torch.Tensor, scales:
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new((M, N), torch.float32, x.device, stream)
     _covers(signs=(signs, K), codes=(codes, N * (K // 16)), scales=(scales, N * (K // 128)), y=(y, M * N))
     if ws is None:
-        ws = workspace(gemv_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemv_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_fwht_gemm", lib().tern_fwht_gemm(
         _dev(x, torch.bfloat16, "x"), _dev(signs, torch.int8, "signs"), _dev(codes, torch.int32, "codes"),
         _dev(scales, torch.float16, "scales"), _dev(y, torch.float32, "y"), M, N, K,
@@ -391,12 +420,12 @@ def gemm(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, y: torch.Te
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("y must be float32 or bfloat16")
     _covers(codes=(codes, N * (K // 16)), scales=(scales, N * (K // 128)), y=(y, M * N))
     if ws is None:
-        ws = workspace(gemm_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemm_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_gemm", lib().tern_gemm(
         _dev(x, torch.bfloat16, "x"), _dev(codes, torch.int32, "codes"), _dev(scales, torch.float16, "scales"),
         _dev(y, y.dtype, "y"), 1 if y.dtype == torch.bfloat16 else 0, M, N, K,
@@ -433,12 +462,12 @@ def bin_gemm(x: torch.Tensor, words: torch.Tensor, scales: torch.Tensor, y: torc
     M, K = x.shape
     N = words.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("y must be float32 or bfloat16")
     _covers(words=(words, N * (K // 32)), scales=(scales, N * (K // 128)), y=(y, M * N))
     if ws is None:
-        ws = workspace(gemm_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemm_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_bin_gemm", lib().tern_bin_gemm(
         _dev(x, torch.bfloat16, "x"), _dev(words, torch.int32, "words"), _dev(scales, torch.float16, "scales"),
         _dev(y, y.dtype, "y"), 1 if y.dtype == torch.bfloat16 else 0, M, N, K,
@@ -454,11 +483,11 @@ def affine_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new((M, N), torch.float32, x.device, stream)
     _covers(codes=(codes, N * (K // 16)), scales=(scales, N * (K // 128)), biases=(biases, N * (K // 128)),
             y=(y, M * N))
     if ws is None:
-        ws = workspace(gemv_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemv_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_affine_gemv", lib().tern_affine_gemv(
         _dev(x, torch.bfloat16, "x"), _dev(codes, torch.int32, "codes"), _dev(scales, torch.float16, "scales"),
         _dev(biases, torch.float16, "biases"), _dev(y, torch.float32, "y"), M, N, K,
@@ -474,13 +503,13 @@ def affine_gemm(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("y must be float32 or bfloat16")
     _covers(codes=(codes, N * (K // 16)), scales=(scales, N * (K // 128)), biases=(biases, N * (K // 128)),
             y=(y, M * N))
     if ws is None:
-        ws = workspace(gemm_workspace_bytes(M, N, K), x.device)
+        ws = _scratch(gemm_workspace_bytes(M, N, K), x.device, stream)
     _check("tern_affine_gemm", lib().tern_affine_gemm(
         _dev(x, torch.bfloat16, "x"), _dev(codes, torch.int32, "codes"), _dev(scales, torch.float16, "scales"),
         _dev(biases, torch.float16, "biases"), _dev(y, y.dtype, "y"), 1 if y.dtype == torch.bfloat16 else 0,
@@ -582,7 +611,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("q, k and v must hold the same number of tokens")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        q_out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
     _covers(positions=(positions, T), slots=(slots, T), q_out=(q_out, T * Hq * D))
     _check("tern_rope_append", lib().tern_rope_append(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), 1 if kind == torch.float32 else 0, qs, ks, vs,
@@ -626,11 +655,11 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     qs, T, Hq, B, W, start, max_new = _sequences(q, lay, table, lens, q_start, max_new)
     D = lay.head_dim
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
     _covers(out=(out, T * Hq * D), lse=(lse, T * Hq))
     if ws is None:
-        ws = workspace(paged_attention_workspace_bytes(B, T, max_new if start else T // B, Hq, lay.kv_heads, D),
-                       q.device)
+        ws = _scratch(paged_attention_workspace_bytes(B, T, max_new if start else T // B, Hq, lay.kv_heads, D),
+                      q.device, stream)
     _check("tern_paged_attention", lib().tern_paged_attention(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay),
         _dev(table, torch.int32, "table"), W, _dev(lens, torch.int32, "lens"), start, B, T, max_new, Hq,
@@ -679,9 +708,9 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor
         raise ValueError("table and dst_table must be [B, pages per sequence]")
     B, H = table.shape[0], lay.kv_heads
     if keep is None:
-        keep = torch.empty((B, H, budget), dtype=torch.int32, device=mass.device)
+        keep = _new((B, H, budget), torch.int32, mass.device, stream)
     if dst_lens is None:
-        dst_lens = torch.empty(B, dtype=torch.int32, device=mass.device)
+        dst_lens = _new(B, torch.int32, mass.device, stream)
     _covers(mass=(mass, lay.pages * H * lay.page_size), lens=(lens, B), keep=(keep, B * H * budget),
             dst_mass=(dst_mass, dlay.pages * dlay.kv_heads * dlay.page_size), dst_lens=(dst_lens, B))
     _check("tern_cache_evict", lib().tern_cache_evict(

@@ -19,6 +19,56 @@ def tern():
     return t
 
 
+def leave_garbage(nbytes, stream=None):
+    """Freed blocks of device memory, full of ones, for the allocator to hand out again."""
+    with torch.cuda.stream(stream):
+        x = [torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    del x
+
+
+@pytest.mark.parametrize("new", [1, 5, 150])
+def test_attention_on_another_stream_without_a_workspace(tern, new):
+    """The call makes its workspace and output ready on the stream that it runs on."""
+    p = Problem(new, [4000 + new, 900 + new], [new, new], 8, 2, 128)
+    side = torch.cuda.Stream()
+    lse = torch.empty((p.T, 8), device="cuda")
+    leave_garbage(1 << 26)
+    leave_garbage(1 << 26, side)
+    torch.cuda._sleep(200_000_000)             # the current stream is busy meanwhile (0.1 s)
+    out = tern.paged_attention(p.q, p.k, p.v, p.table, p.lens_d, q_start=p.q_start_d, max_new=new, lse=lse, stream=side)
+    side.synchronize()
+    got, glse = out.clone(), lse.clone()
+    torch.cuda.synchronize()
+    assert tern.device_error() == 0
+    check_attention(p, got, glse)
+
+
+@pytest.mark.parametrize("call,M", [("gemv", 1), ("gemv", 5), ("gemv", 16), ("gemm", 200), ("fwht_gemm", 1)])
+def test_products_on_another_stream_without_a_workspace(tern, call, M):
+    """The same of the products: bf16 weights and fp32 sums of 4096 terms are off by less than
+    (2^-9 + 2^-12) of the sum of the magnitudes; the rotation rounds its result to bf16 once more."""
+    N, K = 512, 4096
+    g = torch.Generator("cuda").manual_seed(M)
+    t = torch.randint(-1, 2, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    s = (torch.rand((N, K // 128), device="cuda", generator=g) + 0.5).half()
+    x = torch.randn((M, K), device="cuda", generator=g).bfloat16()
+    codes, signs = tern.pack(t), torch.ones(K, dtype=torch.int8, device="cuda")
+    turned = tern.fwht(x, signs) if call == "fwht_gemm" else x
+    w = t.double() * s.double().repeat_interleave(128, dim=1)
+    want, most = turned.double() @ w.T, turned.double().abs() @ w.abs().T
+    side = torch.cuda.Stream()
+    leave_garbage(1 << 24)
+    leave_garbage(1 << 24, side)
+    torch.cuda._sleep(200_000_000)
+    y = getattr(tern, call)(*((x, signs, codes, s) if call == "fwht_gemm" else (x, codes, s)), stream=side)
+    side.synchronize()
+    got = y.clone()
+    torch.cuda.synchronize()
+    assert tern.device_error() == 0
+    assert bool(((got.double() - want).abs() <= 2.0 ** -7 * most).all())
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("group", [4, 8])
 def test_many_short_sequences_of_one_key_tile(tern, D, group):
