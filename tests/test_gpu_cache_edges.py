@@ -81,3 +81,25 @@ def test_many_short_sequences_of_one_key_tile(tern, D, group):
     for _ in range(20):
         b = run_attention(tern, p)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_tensors_of_another_gpu_are_refused(tern, monkeypatch):
+    """With another device current than the tensors', each call says so before anything is launched."""
+    p = Problem(1, [40], [1], 4, 2, 128)
+    lse, m = torch.zeros((1, 4), device="cuda"), torch.zeros((p.pages, 2, p.page), device="cuda")
+    inv = torch.from_numpy(tern.rope_frequencies(128)[0]).cuda()
+    pos, slots = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    k0, m0 = p.k.clone(), m.clone()
+    kv, dst = torch.zeros((1, 2, 128), device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    now = torch.cuda.current_device()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now + 1)
+    for call in (lambda: tern.paged_attention(p.q, p.k, p.v, p.table, p.lens_d, out=p.q.clone()),
+                 lambda: tern.attention_mass(p.q, p.k, p.table, p.lens_d, lse, m),
+                 lambda: tern.rope_append(p.q.float(), kv, kv, pos, slots, inv, p.k, p.v, q_out=p.q.clone()),
+                 lambda: tern.cache_evict(p.k, p.v, m, p.table, p.lens_d, 16, 1, p.k, p.v, m, dst)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert torch.equal(p.k.view(torch.int16), k0.view(torch.int16)) and torch.equal(m, m0)
+    _, _ = run_attention(tern, p)
