@@ -22,6 +22,13 @@ float to_log2(float scale) {
     return fabsf(s) < 1e-30f ? copysignf(1e-30f, s) : s;
 }
 
+// A window of all the keys that a sequence may have hides none.  (Without it the
+// kernels' 32-bit first - window + 1 has no room to wrap.)
+template <typename Args>
+int useful_window(const Args& a, int window) {
+    return window < (long long)a.s.width * a.c.page_size ? window : 0;
+}
+
 tern_status check_heads(const CacheView& c, int q_heads, long long q_stride) {
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return TERN_ERR_SHAPE;
     if (q_heads < 1 || q_heads % c.kv_heads != 0 || q_heads / c.kv_heads > 64) return TERN_ERR_SHAPE;
@@ -73,7 +80,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.q_heads = q_heads;
     a.group = q_heads / a.c.kv_heads;
     a.scale_log2 = to_log2(scale);
-    a.window = window;
+    a.window = useful_window(a, window);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
     a.counters = static_cast<unsigned*>(workspace);
@@ -119,7 +126,7 @@ extern "C" tern_status tern_attention_mass(const void* q, long long q_stride, co
     a.group = q_heads / a.c.kv_heads;
     a.tiles = 0;
     a.scale_log2 = to_log2(scale);
-    a.window = window;
+    a.window = useful_window(a, window);
     a.lse = lse;
     a.decay = decay;
     a.mass = mass;

@@ -4,7 +4,7 @@ not fill a row tile.  Bounds as in test_gpu_cache.py, where they are derived."""
 import pytest
 import torch
 
-from test_gpu_cache import Problem, check_attention, run_attention
+from test_gpu_cache import Problem, check_attention, check_both, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +17,14 @@ def tern():
     build.build()
     import bit_gemv_gemm_gb300 as t
     return t
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("length,new", [(3, 8), (20, 40), (100, 300)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100])
+def test_window_past_every_key(tern, D, length, new, window):
+    """The largest windows hide nothing, in sequences whose first tokens see no key either."""
+    check_both(tern, Problem(new, [length, new + 50], [new, 1], 4, 2, D), window)
 
 
 def leave_garbage(nbytes, stream=None):
