@@ -251,6 +251,14 @@ struct VRows {
     }
 };
 
+// What a row's sum l of 2^(s - m) gives.  0: it saw no key (or none of more weight
+// than 0), its output is 0 and its lse -inf; a sum that is not a number, of scores
+// that are not, makes both NaN.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float lse_of(float m2, float l) {
+    return l == 0.0f ? -INFINITY : (m2 + log2f(l)) * 0.693147180559945309f;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -334,7 +342,7 @@ constexpr size_t part_floats(int D) { return (size_t)kTileRows * (D + 2); }
 template <int D, typename Load>
 __device__ __forceinline__ void emit_row(const AttnArgs& a, bool whole, float* part, int row, bool live, long long orow,
                                          float m2, float l, Load load) {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = inverse_sum(l);
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -357,7 +365,7 @@ __device__ __forceinline__ void emit_row(const AttnArgs& a, bool whole, float* p
                        make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
         }
     }
-    if (whole && live && a.lse) a.lse[orow] = l > 0.0f ? (m2 + log2f(l)) * 0.693147180559945309f : -INFINITY;
+    if (whole && live && a.lse) a.lse[orow] = lse_of(m2, l);
     if (!whole) __stcg(reinterpret_cast<float2*>(part + (size_t)D * kTileRows + 2 * row), make_float2(m2, l));
 }
 
@@ -403,7 +411,7 @@ __device__ __forceinline__ void add_parts(const AttnArgs& a, const Item& t, cons
             mm = mn;
         }
     }
-    const float base = mm == -INFINITY ? 0.0f : mm, inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const float base = mm == -INFINITY ? 0.0f : mm, inv = inverse_sum(ll);
     constexpr int W = D == 256 ? 2 : 3, COLS = join_columns(D);   // parts and columns in flight
 #pragma unroll 1
     for (int c = c0; c < c1; c += COLS) {
@@ -445,7 +453,7 @@ __device__ __forceinline__ void add_parts(const AttnArgs& a, const Item& t, cons
                                     pack_bf16(y[2 * e + 1].z * inv, y[2 * e + 1].w * inv));
         }
     }
-    if (live && a.lse && c0 == 0) a.lse[orow] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
+    if (live && a.lse && c0 == 0) a.lse[orow] = lse_of(mm, ll);
 }
 
 struct MassArgs {

@@ -440,7 +440,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     if (!writer) {
                         // (idle warps wait, too: one that ran on into the next item would count itself in for this one)
                         if (!handed(last)) break;
-                        if (!idle) sm_l[row] = m == -INFINITY ? 0.0f : l * exp2_fast((m - sm_m[row]) * scale);
+                        // (a sum that is not a number stays one, whatever its weight)
+                        const float top = sm_m[row];
+                        if (!idle) sm_l[row] = l * (top == -INFINITY ? 1.0f : exp2_fast((m - top) * scale));
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(MERGE));
                     } else {

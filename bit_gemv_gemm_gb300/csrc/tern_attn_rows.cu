@@ -268,10 +268,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             // columns c .. c + 3 of row r, divided by the sum
             const int tok = (r0 + r) / a.group, g = (r0 + r) % a.group;
             const long long row = (long long)(q.q0 + tok) * a.q_heads + hk * a.group + g;
-            const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+            const float inv = inverse_sum(ll);
             *reinterpret_cast<uint2*>(a.out + row * D + c) =
                 make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
-            if (c == 0 && a.lse) a.lse[row] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
+            if (c == 0 && a.lse) a.lse[row] = lse_of(mm, ll);
         };
         for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;

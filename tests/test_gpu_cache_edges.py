@@ -1,10 +1,12 @@
 """The paged-cache operators where their arguments are at their ends: windows
 past every key, values that are not finite, streams of their own, groups that do
 not fill a row tile.  Bounds as in test_gpu_cache.py, where they are derived."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache import Problem, check_attention, check_both, run_attention
+from oracle import cache as ref
+from test_gpu_cache import Problem, check_attention, check_both, f64, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -25,6 +27,47 @@ def tern():
 def test_window_past_every_key(tern, D, length, new, window):
     """The largest windows hide nothing, in sequences whose first tokens see no key either."""
     check_both(tern, Problem(new, [length, new + 50], [new, 1], 4, 2, D), window)
+
+
+def rows_but(p, out, lse, hit, window=0):
+    """Every row but those of `hit` [T, q_heads] against the definition."""
+    q, k, v, table = p.host
+    q = np.where(hit[..., None], 0.0, q)
+    o, l, A, S = ref.attention(q, np.nan_to_num(k), np.nan_to_num(v), table, p.lens, p.q_start, p.scale, window)
+    err, bound = np.abs(f64(out) - o), 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -13) * A + 1e-30
+    assert (err <= bound)[~hit].all()
+    lerr, lb = np.abs(f64(lse) - l), 2.0 ** -21 * (S + np.abs(l)) + 2.0 ** -20
+    assert (lerr <= lb)[~hit].all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 20, 150])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_whose_query_is_not_finite(tern, D, new, value):
+    """Its output and lse are NaN (an lse of -inf says that a row sees no key), and no other row's."""
+    p = Problem(new, [new + 900], [new], 8, 2, D)
+    hit = np.zeros((new, 8), dtype=bool)
+    for t, h in ((0, 1), (new - 1, 6)):
+        p.q[t, h, 5] = value
+        hit[t, h] = True
+    out, lse = run_attention(tern, p)
+    assert np.isnan(f64(out)[hit]).all() and np.isnan(f64(lse)[hit]).all()
+    rows_but(p, out, lse, hit)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [5, 40, 150])
+def test_a_key_that_is_not_a_number(tern, D, new):
+    """The rows that see it are NaN, the others not."""
+    p = Problem(new, [new + 500], [new], 4, 2, D)
+    j = 500 + new // 2
+    p.k[p.table[0, j // p.page].long(), 1, j % p.page, 3] = float("nan")
+    out, lse = run_attention(tern, p)
+    hit = np.zeros((new, 4), dtype=bool)
+    hit[new // 2:, 2:] = True
+    assert np.isnan(f64(out)[hit]).all() and np.isnan(f64(lse)[hit]).all()
+    p.host = (p.host[0], np.nan_to_num(p.host[1]), p.host[2], p.host[3])
+    rows_but(p, out, lse, hit)
 
 
 def leave_garbage(nbytes, stream=None):
