@@ -237,8 +237,9 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 if (!__all_sync(0xffffffffu, wait(bar(Q_EMPTY + (int)s), ((it / kSlots) & 1u) ^ 1u))) { ok = false; break; }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    // a row that weighs nothing gets a finite value that leaves exp2 at 0: 0 * inf would be NaN
-                    const float v = z[x] == -INFINITY ? a.nothing : z[x] * a.lse_scale;
+                    // a row that weighs nothing (lse -inf: it sees no key; +inf: exp(s - inf)) gets a finite value that
+                    // leaves exp2 at 0: 0 * inf would be NaN
+                    const float v = fabsf(z[x]) == INFINITY ? a.nothing : z[x] * a.lse_scale;
                     const float top = __bfloat162float(__float2bfloat16_rn(v));
                     const float mid = __bfloat162float(__float2bfloat16_rn(v - top));
                     write_step(smem + C::kSmemLse + s * (kRows * 32), lane + 32 * x, top, mid, v - top - mid);

@@ -472,7 +472,7 @@ tern_status tern_paged_attention(const void *q, long long q_stride, const void *
  *   mass_out = decay * mass + sum over the queries i that see j and the heads
  *   of its group of exp(s_ij - lse_i),
  * with the lse that tern_paged_attention gave for the same q, scale and window
- * (a row with lse = -inf gives nothing).  mass and mass_out as described
+ * (a row with an infinite lse gives nothing).  mass and mass_out as described
  * above; they may be the same array.  Every key's page is read, a key outside
  * every window decays.  Slots that hold no key are left alone.  One kernel
  * launch, no atomics: a key's sum has a fixed order. */

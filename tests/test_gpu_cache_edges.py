@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import cache as ref
-from test_gpu_cache import Problem, check_attention, check_both, f64, run_attention
+from test_gpu_cache import Problem, check_attention, check_both, f64, run_attention, run_mass
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +68,16 @@ def test_a_key_that_is_not_a_number(tern, D, new):
     assert np.isnan(f64(out)[hit]).all() and np.isnan(f64(lse)[hit]).all()
     p.host = (p.host[0], np.nan_to_num(p.host[1]), p.host[2], p.host[3])
     rows_but(p, out, lse, hit)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [2, 140])
+def test_mass_of_a_row_with_an_infinite_lse(tern, D, new):
+    """exp(s - inf) is 0: the row weighs nothing, the others what they do."""
+    p = Problem(new, [new + 300], [new], 4, 2, D)
+    _, lse = run_attention(tern, p)
+    lse[0, 1] = lse[new - 1, 3] = float("inf")
+    run_mass(tern, p, lse)
 
 
 def leave_garbage(nbytes, stream=None):
