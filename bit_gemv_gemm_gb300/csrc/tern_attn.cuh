@@ -235,19 +235,27 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // One warp: zeroes the rows [r0, r1) of a chunk of 128-byte rows.  Rows of V that
-// no key of this call's stands in count as 0: those of boxes that are not read
-// before the boxes are, those past the last key inside a box after it has come.
+// hold no key of the sequence, or one before every window, count as 0: those of
+// boxes that are not read before the boxes are, those inside a box after it has come.
 // (Tested row by row this took 10 us of a tile; rows are taken by their range.)
 __device__ __forceinline__ void zero_rows(unsigned char* chunk, int r0, int r1) {
     for (int i = r0 * 8 + (int)(threadIdx.x & 31); i < r1 * 8; i += 32)
         *reinterpret_cast<uint4*>(chunk + i * 16) = make_uint4(0, 0, 0, 0);
 }
 struct VRows {
-    int front, back, back_box;   // [0, front) and [back_box, tile) are not read, [back, back_box) holds no key
+    // [0, front) and [back_box, tile) are not read, [front, front_key) and [back, back_box) hold nothing seen
+    int front, front_key, back, back_box;
     __device__ __forceinline__ VRows(int k0, int tile, int box_rows, int j0, int len) {
         front = max((j0 & ~(box_rows - 1)) - k0, 0);   // (box_rows is a power of two)
+        front_key = max(j0 - k0, 0);
         back = min(len - k0, tile);
         back_box = min((back + box_rows - 1) & ~(box_rows - 1), tile);
+    }
+    // some row of a box that is read counts as 0
+    __device__ __forceinline__ bool inside() const { return front < front_key || back < back_box; }
+    __device__ __forceinline__ void zero_inside(unsigned char* chunk) const {
+        zero_rows(chunk, front, front_key);
+        zero_rows(chunk, back, back_box);
     }
 };
 

@@ -25,7 +25,7 @@
 // CTAs took 191 us there and 149 us for whole prompts that now take 175; a library
 // that several GPUs load has no multicast loads.  The tiles kernel's two streams
 // take 243 and 176, and 241 us for heads of 256, where this scheme takes 245.)
-// Slots past a sequence's last key may hold anything: scores are masked before
+// Slots past a sequence's last key and before its windows may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
 // Work is shared out as in the rows kernel: equal contiguous shares of all
@@ -149,7 +149,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             // ------------------------------ TMA: Q and K, or V ------------------------------
             const bool is_v = warp != kSoftWarps;
             const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-            uint32_t n = 0, used = 0, tails = 0;   // key tiles, items, tiles past a sequence's end so far
+            uint32_t n = 0, used = 0, tails = 0;   // key tiles, items, tiles with rows to zero so far
             bool ok = true;
             const int boxes = kKeys / box_rows;                        // of a chunk
             const int c = lane / boxes, box = lane - c * boxes;        // this lane's piece of a tile
@@ -191,7 +191,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         // boxes that hold no key of these rows are not read; V's rows there count as 0
                         use = use && k < t.q.len && k + box_rows > t.j0;
                         bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, use) & ((1u << boxes) - 1u)) * box_rows * 128u;
-                        part = is_v && rows.back < rows.back_box;
+                        part = is_v && rows.inside();
                         unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
                     }
                     const uint32_t full = part ? bar(TAIL) : bar((int)ring.slot);
@@ -217,7 +217,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                             break;
                         }
                         ++tails;
-                        for (int x = 0; x < NC; ++x) zero_rows(chunks + x * kChunk, rows.back, rows.back_box);
+                        for (int x = 0; x < NC; ++x) rows.zero_inside(chunks + x * kChunk);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar((int)ring.slot));

@@ -94,7 +94,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     for (long long w = w0; w < w1;) {
         // ---- one segment of the item ----
         const Seq q = t.q;
-        const int rows = t.rows, units = t.units, j1 = t.j1, r0 = t.rt * R, hk = t.hk, b = t.b;
+        const int rows = t.rows, units = t.units, j0 = t.j0, j1 = t.j1, r0 = t.rt * R, hk = t.hk, b = t.b;
         const Segment seg = segment_of(extent, t, w, w1);
         const long long at = t.at, we = seg.we;
         const int first = seg.first, strips = seg.n;
@@ -216,12 +216,13 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     l[h] += x + y;
                     pa[2 * n + h] = pack_bf16(x, y);
                 }
-            // slots at or past the last visible key may hold anything: their V counts as 0
+            // slots before the first visible key and past the last may hold anything: their V counts as 0
             uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
-            if (key0 + kStrip > j1) {
+            if (key0 + kStrip > j1 || key0 < j0) {
                 const int k0 = key0 + (lane & 3) * 2;
-                z0 = (k0 < j1 ? 0xffffu : 0u) | (k0 + 1 < j1 ? 0xffff0000u : 0u);
-                z1 = (k0 + 8 < j1 ? 0xffffu : 0u) | (k0 + 9 < j1 ? 0xffff0000u : 0u);
+                auto seen = [&](int k) { return k >= j0 && k < j1; };
+                z0 = (seen(k0) ? 0xffffu : 0u) | (seen(k0 + 1) ? 0xffff0000u : 0u);
+                z1 = (seen(k0 + 8) ? 0xffffu : 0u) | (seen(k0 + 9) ? 0xffff0000u : 0u);
             }
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {

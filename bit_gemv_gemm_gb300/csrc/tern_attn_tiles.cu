@@ -26,7 +26,7 @@
 // bound by L2's rate, 8.5 TB/s (2 x 300 tokens, window of 4096: 58 us), and a
 // verify step by the cache's (4 x 5 tokens over 32k keys, 8 key heads of 128: 92 us,
 // 5.7 TB/s, the last 8 us the joins).
-// Slots past a sequence's last key may hold anything: scores are masked before
+// Slots past a sequence's last key and before its windows may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
 // Work is shared out as in the rows kernel: equal contiguous shares of all
@@ -174,7 +174,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 // boxes that hold no key of these rows are not read; V's rows there count as 0
                 const bool use = c < NC && k < t.q.len && k + box_rows > t.j0;
                 const VRows rows(k0, kKeys, box_rows, t.j0, t.q.len);
-                const bool part = is_v && rows.back < rows.back_box, unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
+                const bool part = is_v && rows.inside(), unread = is_v && (rows.front > 0 || rows.back_box < kKeys);
                 const uint32_t mine = __ballot_sync(0xffffffffu, use);
                 const uint32_t bytes = (uint32_t)__popc(mine & ((1u << boxes) - 1u)) * box_rows * 128u;   // a chunk's
                 const int slot = (unsigned)k % (unsigned)a.c.page_size;
@@ -207,8 +207,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     ++tails;
                     for (int x = 0; x < NC; ++x)
-                        zero_rows(smem + C::kSmemRing + (((it + x / CG) % kSlots) * CG + x % CG) * kChunk, rows.back,
-                                  rows.back_box);
+                        rows.zero_inside(smem + C::kSmemRing + (((it + x / CG) % kSlots) * CG + x % CG) * kChunk);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)

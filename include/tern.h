@@ -451,10 +451,10 @@ tern_status tern_rope_append(const void *q, const void *k, const void *v, int in
  * stride q_stride elements (a multiple of 8, >= q_heads * head_dim), heads
  * contiguous.  Scores, sums and the output are held in fp32 and rounded once
  * to bf16; the probabilities of the second product are rounded to bf16.  Slots
- * at or past lens[b] may hold anything, NaN included, and with a window only the
- * pages that hold a visible key are read.  A value of V that is not finite, of a
- * key that some query of the call sees, may reach queries that do not see it
- * (their probability of 0 times it).  q_heads a multiple of kv_heads, at most 64
+ * at or past lens[b], and with a window those of keys before every query's, may
+ * hold anything, NaN included; only the pages that hold a visible key are read.  A
+ * value of V that is not finite, of a key that some query of the call sees, may
+ * reach queries that do not see it (their probability of 0 times it).  q_heads a multiple of kv_heads, at most 64
  * query heads a key head; head_dim 64, 128 or 256.  One kernel launch; the
  * result does not vary from run to run.
  * The workspace is zero-filled once before its first use and left ready for

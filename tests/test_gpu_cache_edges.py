@@ -80,6 +80,21 @@ def test_mass_of_a_row_with_an_infinite_lse(tern, D, new):
     run_mass(tern, p, lse)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("new", [1, 20, 150])
+def test_keys_before_every_window_may_hold_anything(tern, D, page, new):
+    """Keys and values that no query sees any more, in the pages and tiles of those that some do."""
+    p = Problem(new, [new + 405, new + 1000], [new, new], 4, 2, D, page)
+    for b, L in enumerate(p.lens):
+        for j in range(L - new - 100 + 1):
+            page_id = p.table[b, j // page].long()
+            p.k[page_id, :, j % page] = float("nan")
+            p.v[page_id, :, j % page] = float("inf") if j % 2 else float("nan")
+    out, lse = run_attention(tern, p, 100)
+    check_attention(p, out, lse, 100)
+
+
 def leave_garbage(nbytes, stream=None):
     """Freed blocks of device memory, full of ones, for the allocator to hand out again."""
     with torch.cuda.stream(stream):
