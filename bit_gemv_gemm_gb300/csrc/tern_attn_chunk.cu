@@ -384,7 +384,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     // (the tile before, of the last item too: the hand-overs stay in step)
                     if (n > 0 && !handed(n - 1)) break;
                     float now = j > 0 ? sm_m[row] : -INFINITY;
-                    const bool move = __any_sync(0xffffffffu, (top - now) * scale > 8.0f);
+                    // (rows of no query of the sequence hold what the copies left: they have no vote)
+                    const bool move = __any_sync(0xffffffffu, live && (top - now) * scale > 8.0f);
                     const float before = now;
                     if (move) now = fmaxf(now, top);
                     sm_m[row] = now;

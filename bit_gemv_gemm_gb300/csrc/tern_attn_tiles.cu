@@ -405,7 +405,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     const float top = max3(fmaxf(mx[0], __uint_as_float(x[0][31])), fmaxf(mx[1], __uint_as_float(x[1][31])),
                                            max3(mx[2], __uint_as_float(x[2][31]), fmaxf(mx[3], __uint_as_float(x[3][31]))));
-                    if (__any_sync(0xffffffffu, (top - m) * scale > 8.0f)) {
+                    // (rows of no query of the sequence hold what the copies left: they have no vote)
+                    if (__any_sync(0xffffffffu, live && (top - m) * scale > 8.0f)) {
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.0f : exp2_fast((m - mn) * scale);
                         m = mn;

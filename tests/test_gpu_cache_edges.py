@@ -95,6 +95,34 @@ def test_keys_before_every_window_may_hold_anything(tern, D, page, new):
     check_attention(p, out, lse, 100)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group", [3, 5, 7, 11])
+@pytest.mark.parametrize("new", [9, 90])
+def test_results_do_not_depend_on_the_calls_before(tern, D, group, new):
+    """A group that does not divide 128 leaves rows of a row tile over: what the
+    last kernel left in them changes no bit of the others."""
+    p = Problem(new, [new + 3000] * 6, [new] * 6, 2 * group, 2, D)
+    ws, got = tern.workspace(1 << 27), []
+    for spread in (0.0, 60.0, 300.0):
+        r = Problem(1, [new + 2000] * 12, [max(new, 10)] * 12, 8, 2, D, spread=spread)
+        run_attention(tern, r, ws=ws)
+        got.append(run_attention(tern, p, ws=ws))
+    check_attention(p, *got[0])
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("new", [9, 90])
+def test_results_do_not_depend_on_the_sequences_beside(tern, new):
+    """A sequence's rows are the same bits whatever queries follow them in the call."""
+    got = []
+    for spread in (0.0, 100.0):
+        p = Problem(new, [new + 700, new + 700], [new, new], 8, 2, 128)
+        p.q[new:] = torch.randn(p.q[new:].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) * spread
+        got.append([x[:new].clone() for x in run_attention(tern, p)])
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def leave_garbage(nbytes, stream=None):
     """Freed blocks of device memory, full of ones, for the allocator to hand out again."""
     with torch.cuda.stream(stream):
