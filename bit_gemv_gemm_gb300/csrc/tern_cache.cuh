@@ -103,7 +103,8 @@ inline tern_status make_seq_view(const int* table, int width, int page_size, con
     if (!q_start && T % B != 0) return TERN_ERR_SHAPE;
     if (!table || !lens) return TERN_ERR_NULL;
     if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(q_start, 4)) return TERN_ERR_ALIGN;
-    *s = SeqView{table, lens, q_start, width, B, T, q_start ? max_new : T / B};
+    // (no sequence brings more than all T: a max_new that allows more chooses no other kernel)
+    *s = SeqView{table, lens, q_start, width, B, T, q_start ? (max_new < T ? max_new : T) : T / B};
     return TERN_OK;
 }
 

@@ -173,6 +173,25 @@ def test_products_on_another_stream_without_a_workspace(tern, call, M):
     assert bool(((got.double() - want).abs() <= 2.0 ** -7 * most).all())
 
 
+@pytest.mark.parametrize("max_new", [0, 1, 512])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_mass_of_a_step_without_tokens(tern, D, max_new):
+    """No token at all, whatever max_new allows: every key decays."""
+    p = Problem(3, [200, 31, 0], [0, 0, 0], 8, 2, D)
+    m = torch.rand((p.pages, 2, p.page), device="cuda") + 1.0
+    out = torch.full_like(m, -5.0)
+    lse = torch.empty((0, 8), device="cuda")
+    tern.attention_mass(p.q, p.k, p.table, p.lens_d, lse, m, out=out, q_start=p.q_start_d, max_new=max_new, decay=0.5)
+    torch.cuda.synchronize()
+    assert tern.device_error() == 0
+    want = np.full(m.shape, -5.0)
+    for b, L in enumerate(p.lens):
+        for j in range(L):
+            pg, sl = int(p.table[b, j // p.page]), j % p.page
+            want[pg, :, sl] = 0.5 * f64(m)[pg, :, sl]
+    assert np.array_equal(f64(out), want)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("group", [4, 8])
 def test_many_short_sequences_of_one_key_tile(tern, D, group):
