@@ -225,7 +225,7 @@ extern "C" tern_status tern_rope_frequencies_host(int rot_dim, double base, int 
             return rot_dim * log(original_len / (turns * 6.283185307179586477)) / (2.0 * log(base));
         };
         lo = fmax(0.0, floor(at(turns_fast)));
-        hi = fmin(half - 1.0, ceil(at(turns_slow)));
+        hi = fmin(rot_dim - 1.0, ceil(at(turns_slow)));   // (may lie past the last pair: the ramp then ends there, unfinished)
     }
     for (int i = 0; i < half; ++i) {
         double f = pow(base, -2.0 * i / rot_dim);

@@ -414,8 +414,10 @@ typedef struct {
  *   TERN_ROPE_PARTS   pairs that make more than turns_fast turns in
  *                     original_len positions are kept, those that make fewer
  *                     than turns_slow are divided by factor, with a linear
- *                     ramp over the pair index between, and *attn_factor is
- *                     0.1 ln(factor) + 1 (1 otherwise).
+ *                     ramp over the pair index between, from the index of
+ *                     turns_fast rounded down (0 at least) to that of turns_slow
+ *                     rounded up (rot_dim - 1 at most, which may be past the last
+ *                     pair), and *attn_factor is 0.1 ln(factor) + 1 (1 otherwise).
  * Host memory, computed in 64 bits and rounded to fp32. */
 #define TERN_ROPE_PLAIN 0
 #define TERN_ROPE_LINEAR 1

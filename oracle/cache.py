@@ -38,7 +38,7 @@ def rope_frequencies(rot_dim, base, scaling="none", factor=1.0, original_len=0, 
         def index_of(turns):   # base^(-2 i / r) * original_len = 2 pi turns
             return rot_dim / 2 * np.log(original_len / (2 * np.pi * turns)) / np.log(base)
         lo = max(np.floor(index_of(turns_fast)), 0.0)
-        hi = min(np.ceil(index_of(turns_slow)), rot_dim // 2 - 1)
+        hi = min(np.ceil(index_of(turns_slow)), rot_dim - 1)
         ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0, 1)
         return f * (1 - ramp) + f / factor * ramp, 0.1 * np.log(factor) + 1.0
     return f, 1.0
