@@ -49,12 +49,18 @@ __device__ __forceinline__ Seq load_seq(const SeqView& s, int page_size, int b, 
     if (bad || len != r.len) report_device_error(err, TERN_DEVERR_CACHE_SEQUENCE);
     return r;
 }
-// A page id from the table, checked against the pool (a bad one is reported
-// and read as page 0; the call's output is then undefined).
+// A page id from the table, checked against the pool.  A bad one is reported and
+// read as page 0 (the call's output is then undefined)...
 __device__ __forceinline__ int checked_page(int id, int pages, int* err) {
     if ((unsigned)id < (unsigned)pages) return id;
     report_device_error(err, TERN_DEVERR_CACHE_PAGE);
     return 0;
+}
+// ... but never written: page 0 is another sequence's.  -1 where the id is bad.
+__device__ __forceinline__ int checked_page_to_write(int id, int pages, int* err) {
+    if ((unsigned)id < (unsigned)pages) return id;
+    report_device_error(err, TERN_DEVERR_CACHE_PAGE);
+    return -1;
 }
 
 // launch_pdl with clusters of `cluster` CTAs.

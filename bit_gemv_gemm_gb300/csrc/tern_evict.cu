@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t order_of(float m) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct Way {   // where a key's rows and mass lie, and where they go
+struct Way {   // where a key's rows and mass lie, and where they go (to < 0: nowhere, a bad page id)
     long long from, to, mass, dmass;
 };
 
@@ -217,11 +217,11 @@ evict_kernel(const EvictArgs a) {
     cluster.sync();   // the whole list is written (and this CTA's counts have been read)
 
     auto way = [&](int j, int i) {
-        const int page = page_of(j), dpage = checked_page(a.dtable[(long long)b * a.dwidth + (unsigned)i / (unsigned)a.dc.page_size],
+        const int page = page_of(j), dpage = checked_page_to_write(a.dtable[(long long)b * a.dwidth + (unsigned)i / (unsigned)a.dc.page_size],
                                                            a.dc.pages, &g_evict_error);
         const int slot = (unsigned)j % (unsigned)a.c.page_size, dslot = (unsigned)i % (unsigned)a.dc.page_size;
         const long long from = page * a.c.page_stride + hk * a.c.head_stride + slot * a.c.slot_stride;
-        const long long to = dpage * a.dc.page_stride + hk * a.dc.head_stride + dslot * a.dc.slot_stride;
+        const long long to = dpage < 0 ? -1 : dpage * a.dc.page_stride + hk * a.dc.head_stride + dslot * a.dc.slot_stride;
         return Way{from, to, mass_index(page, j), ((long long)dpage * a.dc.kv_heads + hk) * a.dc.page_size + dslot};
     };
     // keys i_lo .. i_hi - 1 of the list; threads in groups of `lanes` (D / 8, at most 32) a row
@@ -233,8 +233,8 @@ evict_kernel(const EvictArgs a) {
     auto place = [&](int x) { return way(__ldcg(keep + min(x, i_hi - 1)), min(x, i_hi - 1)); };
     Way p = place(i), q = place(i + groups);
     for (; i < i_hi; i += 2 * groups) {
-        const bool two = i + groups < i_hi, more = i + 2 * groups < i_hi;
         const Way p0 = p, q0 = q;
+        const bool one = p0.to >= 0, two = q0.to >= 0 && i + groups < i_hi, more = i + 2 * groups < i_hi;
         for (int d = l0; d < D; d += lanes * 8) {
             const uint4 k0 = __ldcs(reinterpret_cast<const uint4*>(a.k + p0.from + d));
             const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(a.v + p0.from + d));
@@ -244,8 +244,10 @@ evict_kernel(const EvictArgs a) {
                 p = place(i + 2 * groups);
                 q = place(i + 3 * groups);
             }
-            *reinterpret_cast<uint4*>(a.dk + p0.to + d) = k0;
-            *reinterpret_cast<uint4*>(a.dv + p0.to + d) = v0;
+            if (one) {
+                *reinterpret_cast<uint4*>(a.dk + p0.to + d) = k0;
+                *reinterpret_cast<uint4*>(a.dv + p0.to + d) = v0;
+            }
             if (two) {
                 *reinterpret_cast<uint4*>(a.dk + q0.to + d) = k1;
                 *reinterpret_cast<uint4*>(a.dv + q0.to + d) = v1;
@@ -256,7 +258,7 @@ evict_kernel(const EvictArgs a) {
             q = place(i + 3 * groups);
         }
         if (l0 == 0) {
-            a.dmass[p0.dmass] = a.mass[p0.mass];
+            if (one) a.dmass[p0.dmass] = a.mass[p0.mass];
             if (two) a.dmass[q0.dmass] = a.mass[q0.mass];
         }
     }

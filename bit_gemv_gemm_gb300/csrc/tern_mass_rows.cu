@@ -96,7 +96,7 @@ mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
             const int k = base + lane;
             ids = 0;
             if (k < my)
-                ids = checked_page(trow[(unsigned)((first + warp + kWarps * k) * kStrip) / (unsigned)a.c.page_size], a.c.pages, &g_mass_rows_error);
+                ids = checked_page_to_write(trow[(unsigned)((first + warp + kWarps * k) * kStrip) / (unsigned)a.c.page_size], a.c.pages, &g_mass_rows_error);
         };
         auto issue = [&](int k) {
             const int page = __shfl_sync(0xffffffffu, ids, k & 31);
@@ -104,7 +104,7 @@ mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
                 const uint32_t s = (it + (uint32_t)k) % C::kStages;
                 const int slot = (unsigned)((first + warp + kWarps * k) * kStrip) % (unsigned)a.c.page_size;
                 mbar_arrive_expect_tx(bars + 8u * s, C::kStage);
-                tma_load_cache(ring + s * C::kStage, &tmap_k, slot, 0, hk, page, bars + 8u * s);
+                tma_load_cache(ring + s * C::kStage, &tmap_k, slot, 0, hk, max(page, 0), bars + 8u * s);
             }
         };
         // the mass of strip k, lane (lane & 15)'s key; -1: none.  Its page id is still in the lanes: in the block of
@@ -115,6 +115,7 @@ mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
             const int strip = first + warp + kWarps * k, key = strip * kStrip + (lane & 15);
             if (k >= my || key >= q.len || lane >= 16) return -1;
             const int page = (k >> 5) == (filled >> 5) ? now : old;
+            if (page < 0) return -1;   // (a bad id)
             return ((long long)page * a.c.kv_heads + hk) * a.c.page_size + (unsigned)key % (unsigned)a.c.page_size;
         };
         fetch_ids(0);

@@ -317,13 +317,14 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             int lo, hi;
             extent.row_tiles(t, lo, hi);
             const int key = t.j0 + me * kKeys + row;
-            const bool live = key < t.j1;
-            long long at = 0;
+            long long at = -1;   // where this key's mass is; -1: no key, or a bad page id
             float old = 0.0f;
-            if (live) {
-                const int page = checked_page(a.s.table[(long long)t.b * a.s.width + key / a.c.page_size], a.c.pages, &g_mass_tiles_error);
-                at = ((long long)page * a.c.kv_heads + t.hk) * a.c.page_size + key % a.c.page_size;
-                old = __ldg(a.mass + at);
+            if (key < t.j1) {
+                const int page = checked_page_to_write(a.s.table[(long long)t.b * a.s.width + key / a.c.page_size], a.c.pages, &g_mass_tiles_error);
+                if (page >= 0) {
+                    at = ((long long)page * a.c.kv_heads + t.hk) * a.c.page_size + key % a.c.page_size;
+                    old = __ldg(a.mass + at);
+                }
             }
             // tokens [first, end) see this key
             const int first = key - (t.q.len - t.q.n);
@@ -382,7 +383,7 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 else weigh(std::false_type{});
             }
             if (!ok) break;
-            if (live) {
+            if (at >= 0) {
                 float x, y;
                 unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
                 a.out[at] = fmaf(a.decay, old, x + y);

@@ -192,6 +192,36 @@ def test_mass_of_a_step_without_tokens(tern, D, max_new):
     assert np.array_equal(f64(out), want)
 
 
+@pytest.mark.parametrize("new", [1, 140])
+def test_a_bad_page_changes_no_other_page(tern, new):
+    """A page id outside the pool is reported, and nothing of its sequence is written elsewhere."""
+    p = Problem(4, [100 + new, 20 + new], [new, new], 4, 2, 128)
+    _, lse = run_attention(tern, p)
+    for bad in (-7, p.pages, 2 ** 31 - 1):
+        table = p.table.clone()
+        table[0] = bad
+        m = torch.full((p.pages, 2, p.page), 3.0, device="cuda")
+        tern.attention_mass(p.q, p.k, table, p.lens_d, lse, m, q_start=p.q_start_d, max_new=new, decay=0.5)
+        assert tern.device_error() == tern.DEVERR_CACHE_PAGE
+        own = torch.zeros(p.pages, dtype=torch.bool)
+        own[p.table[1, :-(-p.lens[1] // p.page)].long().cpu()] = True
+        assert bool((m[~own.cuda()] == 3.0).all())
+
+
+def test_a_bad_destination_page_changes_no_other_page(tern):
+    p = Problem(1, [300], [0], 2, 2, 64, 16)
+    m = torch.rand((p.pages, 2, 16), device="cuda")
+    for bad in (-3, 7, 2 ** 31 - 1):
+        dk, dv = (torch.full((7, 2, 16, 64), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        dm = torch.full((7, 2, 16), 9.0, device="cuda")
+        dst = torch.full((1, 7), bad, dtype=torch.int32, device="cuda")
+        dst[0, 3] = 5
+        tern.cache_evict(p.k, p.v, m, p.table, p.lens_d, 100, 10, dk, dv, dm, dst)
+        assert tern.device_error() == tern.DEVERR_CACHE_PAGE
+        rest = [0, 1, 2, 3, 4, 6]
+        assert all(bool((x[rest] == 9.0).all()) for x in (dk, dv, dm)) and not bool((dm[5] == 9.0).any())
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("group", [4, 8])
 def test_many_short_sequences_of_one_key_tile(tern, D, group):
