@@ -299,6 +299,9 @@ extern "C" tern_status tern_cache_evict(const void* k_cache, const void* v_cache
         !aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(dst_mass, 4) || !aligned_to(dst_table, 4) ||
         !aligned_to(keep, 4) || !aligned_to(dst_lens, 4))
         return TERN_ERR_ALIGN;
+    // one head's cluster writes a sequence's new length while another's may still read the old
+    const uintptr_t old_at = reinterpret_cast<uintptr_t>(lens), new_at = reinterpret_cast<uintptr_t>(dst_lens);
+    if (old_at < new_at + 4 * (uintptr_t)B && new_at < old_at + 4 * (uintptr_t)B) return TERN_ERR_SHAPE;
     int sms = 0;
     st = check_device(&sms);
     if (st != TERN_OK) return st;

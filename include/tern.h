@@ -492,7 +492,8 @@ tern_status tern_attention_mass(const void *q, long long q_stride, const void *k
  * [B][dst_table_width]) of the destination cache, which may be the same arrays
  * as long as no destination page is one that the call reads; keep (int32
  * [B][kv_heads][budget]) gets their old indices, ascending, -1 past the last,
- * and dst_lens (int32 [B]) the new lengths.  One kernel launch, no workspace. */
+ * and dst_lens (int32 [B], which may not overlap lens: TERN_ERR_SHAPE) the new
+ * lengths.  One kernel launch, no workspace. */
 tern_status tern_cache_evict(const void *k_cache, const void *v_cache, const tern_cache_layout *layout,
                              const float *mass, const int *table, int table_width, const int *lens, int B, int budget,
                              int recent, void *dst_k, void *dst_v, const tern_cache_layout *dst_layout,

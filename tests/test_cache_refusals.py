@@ -1,0 +1,27 @@
+"""Arguments of the paged-cache calls that are refused before any device use.
+Fake pointers: every call here is one that is refused."""
+import ctypes
+
+import pytest
+
+P = 4096
+SHAPE = 2
+
+
+@pytest.fixture(scope="module")
+def tern():
+    from bit_gemv_gemm_gb300 import build
+    build.build()
+    import bit_gemv_gemm_gb300 as t
+    return t
+
+
+def layout(tern):
+    return tern.CacheLayout(10, 16, 2, 128, 2 * 16 * 128, 16 * 128, 128)
+
+
+@pytest.mark.parametrize("shift", [0, 4, 12, -12])
+def test_evict_refuses_new_lengths_over_the_old(tern, shift):
+    lay = layout(tern)
+    at = ctypes.addressof(lay)
+    assert tern.lib().tern_cache_evict(P, P, at, P, P, 100, P, 4, 100, 10, P, P, at, P, P, 7, P, P + shift, None) == SHAPE
