@@ -476,7 +476,7 @@ struct MassArgs {
     int window;
     const float* lse;
     float decay;
-    const float* mass;
+    const float* mass;       // may be out: plain loads, none that take it for read-only
     float* out;
 };
 

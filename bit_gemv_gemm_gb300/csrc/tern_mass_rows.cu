@@ -141,13 +141,13 @@ mass_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const MassArgs a) {
         __syncthreads();
 
         long long at = mass_at(0, 0);
-        float old = at >= 0 ? __ldg(a.mass + at) : 0.0f;
+        float old = at >= 0 ? a.mass[at] : 0.0f;
         for (int k = 0; k < my; ++k) {
             const uint32_t slot = (it + (uint32_t)k) % C::kStages, phase = ((it + (uint32_t)k) / C::kStages) & 1u;
             const int key0 = (first + warp + kWarps * k) * kStrip;
             // (the block of strip k + stages is in ids from the end of step k on, that of strip k + stages - 1 now)
             const long long next_at = mass_at(k + 1, k + C::kStages - 1);
-            const float next_old = next_at >= 0 ? __ldg(a.mass + next_at) : 0.0f;
+            const float next_old = next_at >= 0 ? a.mass[next_at] : 0.0f;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + 8u * slot, phase, abort_flag, kAttnWaitNs))) {
                 if (!*abort_flag) {
                     *abort_flag = 1;

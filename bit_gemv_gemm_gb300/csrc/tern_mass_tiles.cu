@@ -323,7 +323,7 @@ mass_tiles_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 const int page = checked_page_to_write(a.s.table[(long long)t.b * a.s.width + key / a.c.page_size], a.c.pages, &g_mass_tiles_error);
                 if (page >= 0) {
                     at = ((long long)page * a.c.kv_heads + t.hk) * a.c.page_size + key % a.c.page_size;
-                    old = __ldg(a.mass + at);
+                    old = a.mass[at];
                 }
             }
             // tokens [first, end) see this key

@@ -192,6 +192,19 @@ def test_mass_of_a_step_without_tokens(tern, D, max_new):
     assert np.array_equal(f64(out), want)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 16, 140])
+def test_mass_in_place_is_the_same_bits(tern, D, new):
+    """The running mass may be its own output, as it is by default."""
+    p = Problem(new, [new + 700, new + 50], [new, new], 4, 2, D)
+    _, lse = run_attention(tern, p)
+    apart, same = run_mass(tern, p, lse), run_mass(tern, p, lse, in_place=True)
+    for b, L in enumerate(p.lens):
+        j = torch.arange(L, device="cuda")
+        pg, sl = p.table[b].long()[j // p.page], j % p.page
+        assert torch.equal(apart[pg, :, sl], same[pg, :, sl])
+
+
 @pytest.mark.parametrize("new", [1, 140])
 def test_a_bad_page_changes_no_other_page(tern, new):
     """A page id outside the pool is reported, and nothing of its sequence is written elsewhere."""
