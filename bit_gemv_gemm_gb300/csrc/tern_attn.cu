@@ -62,7 +62,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     if (st == TERN_OK) st = make_seq_view(table, table_width, a.c.page_size, lens, q_start, B, T, max_new, &a.s);
     if (st == TERN_OK) st = check_heads(a.c, q_heads, q_stride);
     if (st != TERN_OK) return st;
-    if (window < 0 || !(fabsf(scale) < INFINITY)) return TERN_ERR_SHAPE;
+    if (window < 0 || !(fabsf(to_log2(scale)) < INFINITY)) return TERN_ERR_SHAPE;
     if (!k_cache || !v_cache || (T > 0 && (!q || !out))) return TERN_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned_to(lse, 4))
         return TERN_ERR_ALIGN;
@@ -111,7 +111,7 @@ extern "C" tern_status tern_attention_mass(const void* q, long long q_stride, co
     if (st == TERN_OK) st = make_seq_view(table, table_width, a.c.page_size, lens, q_start, B, T, max_new, &a.s);
     if (st == TERN_OK) st = check_heads(a.c, q_heads, q_stride);
     if (st != TERN_OK) return st;
-    if (window < 0 || !(fabsf(scale) < INFINITY) || !(fabsf(decay) < INFINITY)) return TERN_ERR_SHAPE;
+    if (window < 0 || !(fabsf(to_log2(scale)) < INFINITY) || !(fabsf(decay) < INFINITY)) return TERN_ERR_SHAPE;
     if (!k_cache || !mass || !mass_out || (T > 0 && (!q || !lse))) return TERN_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned_to(lse, 4) || !aligned_to(mass, 4) ||
         !aligned_to(mass_out, 4))

@@ -25,3 +25,13 @@ def test_evict_refuses_new_lengths_over_the_old(tern, shift):
     lay = layout(tern)
     at = ctypes.addressof(lay)
     assert tern.lib().tern_cache_evict(P, P, at, P, P, 100, P, 4, 100, 10, P, P, at, P, P, 7, P, P + shift, None) == SHAPE
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38, float("inf"), float("nan")])
+def test_scales_without_a_finite_product_with_log2_e_are_refused(tern, scale):
+    """The kernels keep scores in powers of two: a scale that is infinite there made NaN of every 0."""
+    lay = layout(tern)
+    at = ctypes.addressof(lay)
+    assert tern.lib().tern_paged_attention(P, 1024, P, P, at, P, 4, P, P, 2, 2, 1, 8, scale, 0, P, P, P, 1 << 27,
+                                           None) == SHAPE
+    assert tern.lib().tern_attention_mass(P, 1024, P, at, P, 4, P, P, 2, 2, 1, 8, scale, 0, P, 1.0, P, P, None) == SHAPE
