@@ -164,12 +164,17 @@ def _there(stream):
                              else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace for one call on `stream`."""
-    if stream is None:
+def _scratch(nbytes: int, device, stream, counters: int | None = None) -> torch.Tensor:
+    """A workspace for one call on `stream`, of which the first `counters` bytes
+    (all if not given) have to be zero."""
+    if stream is not None:
+        with _there(stream):
+            return _scratch(nbytes, device, None, counters)
+    if counters is None:
         return workspace(nbytes, device)
-    with _there(stream):
-        return workspace(nbytes, device)
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    ws[:counters].zero_()
+    return ws
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
@@ -634,6 +639,9 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     return q_out
 
 
+ATTENTION_COUNTER_BYTES = 8192   # of the workspace, that have to be zero before its first use
+
+
 def paged_attention_workspace_bytes(B: int, T: int, max_new: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().tern_paged_attention_workspace_bytes(B, T, max_new, q_heads, kv_heads, head_dim))
 
@@ -672,7 +680,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     _here(q=q, k_cache=k_cache, v_cache=v_cache, table=table, lens=lens, q_start=q_start, out=out, lse=lse, ws=ws)
     if ws is None:
         ws = _scratch(paged_attention_workspace_bytes(B, T, max_new if start else T // B, Hq, lay.kv_heads, D),
-                      q.device, stream)
+                      q.device, stream, ATTENTION_COUNTER_BYTES)
     _check("tern_paged_attention", lib().tern_paged_attention(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay),
         _dev(table, torch.int32, "table"), W, _dev(lens, torch.int32, "lens"), start, B, T, max_new, Hq,

@@ -14,7 +14,8 @@
 namespace tern {
 
 constexpr int kMaxSms = 160;                      // the workspace is sized for this many
-constexpr size_t kAttnCounterBytes = 8192;       // 8 counters a CTA
+constexpr size_t kAttnCounterBytes = TERN_ATTENTION_COUNTER_BYTES;   // 8 counters a CTA
+static_assert(kAttnCounterBytes >= 8 * kMaxSms * sizeof(unsigned), "counters");
 constexpr uint64_t kAttnWaitNs = 1000000000ull;   // 1 s: far beyond any real wait
 
 struct AttnArgs {

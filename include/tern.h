@@ -459,9 +459,11 @@ tern_status tern_rope_append(const void *q, const void *k, const void *v, int in
  * reach queries that do not see it (their probability of 0 times it).  q_heads a multiple of kv_heads, at most 64
  * query heads a key head; head_dim 64, 128 or 256.  One kernel launch; the
  * result does not vary from run to run.
- * The workspace is zero-filled once before its first use and left ready for
- * the next call; its size never exceeds 128 MiB.  Calls that share it must be
+ * The workspace's first TERN_ATTENTION_COUNTER_BYTES are zero-filled once before
+ * its first use and left ready for the next call, the rest may hold anything; its
+ * size never exceeds 128 MiB.  Calls that share it must be
  * ordered; after a device error zero-fill it again. */
+#define TERN_ATTENTION_COUNTER_BYTES 8192
 size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new, int q_heads, int kv_heads, int head_dim);
 tern_status tern_paged_attention(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
                                  const tern_cache_layout *layout, const int *table, int table_width, const int *lens,

@@ -148,6 +148,18 @@ def test_attention_on_another_stream_without_a_workspace(tern, new):
     check_attention(p, got, glse)
 
 
+@pytest.mark.parametrize("new", [1, 5, 150])
+def test_a_workspace_is_zero_only_where_it_counts(tern, new):
+    """The call's own workspace in memory full of ones, and one that is zero in its first bytes alone."""
+    p = Problem(new, [4000 + new, 900 + new], [new, new], 8, 2, 128)
+    leave_garbage(1 << 26)
+    check_attention(p, *run_attention(tern, p))
+    ws = torch.full((tern.paged_attention_workspace_bytes(2, p.T, new, 8, 2, 128),), 255, dtype=torch.uint8, device="cuda")
+    ws[:tern.ATTENTION_COUNTER_BYTES] = 0
+    for _ in range(2):
+        check_attention(p, *run_attention(tern, p, ws=ws))
+
+
 @pytest.mark.parametrize("call,M", [("gemv", 1), ("gemv", 5), ("gemv", 16), ("gemm", 200), ("fwht_gemm", 1)])
 def test_products_on_another_stream_without_a_workspace(tern, call, M):
     """The same of the products: bf16 weights and fp32 sums of 4096 terms are off by less than
