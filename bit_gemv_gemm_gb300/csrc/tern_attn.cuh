@@ -173,7 +173,8 @@ __device__ bool find_share(const SeqView& sv, const CacheView& cv, const Extent&
             if (w0 < at + u) break;
             at += u;
         }
-        t.hk = (int)((unsigned)(w0 - at) / (unsigned)t.units);   // below kv_heads * units
+        const long long in = w0 - at;   // below kv_heads * units, which may pass 32 bits
+        t.hk = in <= 0xffffffffLL ? (int)((unsigned)in / (unsigned)t.units) : (int)(in / t.units);
         t.at = at + (long long)t.hk * t.units;
         int* o = reinterpret_cast<int*>(sm);
         o[0] = t.b;
