@@ -536,6 +536,15 @@ class CacheLayout(ctypes.Structure):
 # decode step makes the same small calls over and over, and the checks would take
 # longer than the launch.
 
+def _steps(shape, stride):
+    """The strides with those of axes of one element, which say nothing (a view may
+    hold any there), as in a contiguous array."""
+    dense = [1] * len(shape)
+    for i in range(len(shape) - 2, -1, -1):
+        dense[i] = dense[i + 1] * shape[i + 1]
+    return tuple(d if n == 1 else s for n, s, d in zip(shape, stride, dense))
+
+
 @functools.lru_cache(maxsize=1024)
 def _layout(name: str, shape, stride, like=None) -> CacheLayout:
     """The layout of one cache array, bf16 [pages, kv_heads, page_size, head_dim]
@@ -543,7 +552,8 @@ def _layout(name: str, shape, stride, like=None) -> CacheLayout:
     kv_heads, head_dim] array is one); `like`: the shape and strides of its K array."""
     if len(shape) != 4 or stride[3] != 1:
         raise ValueError(f"{name} must be [pages, kv_heads, page_size, head_dim] with contiguous heads")
-    if like is not None and (shape, stride) != like:
+    stride = _steps(shape, stride)
+    if like is not None and (shape, stride) != (like[0], _steps(*like)):
         raise ValueError(f"{name} must have the shape and strides of its K array")
     return CacheLayout(shape[0], shape[2], shape[1], shape[3], stride[0], stride[1], stride[2])
 

@@ -3,6 +3,7 @@ Fake pointers: every call here is one that is refused."""
 import ctypes
 
 import pytest
+import torch
 
 P = 4096
 SHAPE = 2
@@ -35,3 +36,18 @@ def test_scales_without_a_finite_product_with_log2_e_are_refused(tern, scale):
     assert tern.lib().tern_paged_attention(P, 1024, P, P, at, P, 4, P, P, 2, 2, 1, 8, scale, 0, P, P, P, 1 << 27,
                                            None) == SHAPE
     assert tern.lib().tern_attention_mass(P, 1024, P, at, P, 4, P, P, 2, 2, 1, 8, scale, 0, P, 1.0, P, P, None) == SHAPE
+
+
+def test_strides_of_single_axes_say_nothing(tern):
+    """A pool of one page, one head or both may come as a view with any stride there."""
+    x = torch.zeros(4 * 16 * 64, dtype=torch.bfloat16)
+    for shape, stride in (((4, 1, 16, 64), (1024, 0, 64, 1)), ((4, 1, 16, 64), (1024, 7, 64, 1)),
+                          ((1, 4, 16, 64), (3, 1024, 64, 1)), ((1, 1, 64, 64), (0, 0, 64, 1))):
+        v = x.as_strided(shape, stride)
+        lay = tern._layout("k_cache", v.shape, v.stride())
+        assert lay.page_stride >= 64 and lay.page_stride % 8 == 0 and lay.head_stride >= 64 and lay.head_stride % 8 == 0
+        assert lay.slot_stride == 64
+        dense = torch.zeros(shape, dtype=torch.bfloat16)
+        tern._layout("v_cache", dense.shape, dense.stride(), (v.shape, v.stride()))
+    with pytest.raises(ValueError, match="v_cache"):
+        tern._layout("v_cache", (4, 2, 16, 64), (2048, 1024, 64, 1), ((4, 2, 16, 64), (2048, 64, 128, 1)))
