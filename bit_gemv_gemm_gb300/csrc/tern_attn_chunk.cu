@@ -20,17 +20,24 @@
 // only moves when a score passes it by 2^8 (then O is rescaled, after the product
 // before has been added), so P and the sums stay below 2^8 of their largest term.
 // Each warpgroup keeps its own sum, in fp32; they meet at the item's end.
-// 512 tokens over 32k keys, 32 heads of 128: 202 us, 1.34 PFLOP/s, 10 TB/s from L2;
-// row tiles that read the same keys each fetch them.  (TMA multicast to pairs of
-// CTAs took 191 us there and 149 us for whole prompts that now take 175; a library
-// that several GPUs load has no multicast loads.  The tiles kernel's two streams
-// take 243 and 176, and 241 us for heads of 256, where this scheme takes 245.)
+// Two neighbouring row tiles are one item, taken by a pair of CTAs that start
+// together and go through the same key tiles at the same pace, each with its own
+// loads and waits: what one has just read is in L2 for the other.  A pair is
+// launched as a cluster, which puts it on neighbouring SMs, and shares nothing
+// else (single CTAs with a row tile each, 512 tokens over 32k keys 226 us and whole
+// prompts 188; pairs without the cluster 213 and 192; pairs 212 and 148).
+// 512 tokens over 32k keys, 32 heads of 128: 212 us, 1.28 PFLOP/s, 10 TB/s from L2
+// (195 us, 1.39 PFLOP/s, where three inputs take turns).  TMA multicast of each
+// half to both CTAs took 202 (191), but a library that programs of several GPUs
+// load has no multicast loads.  The tiles kernel's two streams take 243 there and
+// 176 for the prompts.
 // Slots past a sequence's last key and before its windows may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).
 // Work is shared out as in the rows kernel: equal contiguous shares of all
-// (sequence, row tile, key head) items' 128-key tiles; parts meet in the workspace,
-// and the warp that counts last for its 32 rows adds them in order.
+// (sequence, pair of row tiles, key head) items' 128-key tiles, a share a pair; parts
+// meet in the workspace, and the warp that counts last for its 32 rows adds them in
+// order.
 #include "tern_attn.cuh"
 
 namespace tern {
@@ -43,9 +50,9 @@ __device__ int g_attn_chunk_error;
 constexpr int kKeys = 128, kRows = kTileRows;
 constexpr int kChunk = 64 * kKeys * 2;      // 16 KB: 64 head values of 128 keys (or rows)
 // key tiles' time that an item costs besides its own (four prompts of up to 4000
-// tokens, whose items are of unlike length: 219, 209, 194, 188, 181, 186 us with 2, 3, 4,
-// 5, 7, 10; four of up to 2000, heads of 128: 100, 92, 93, 93, 95, 96; the first now 175)
-constexpr int kItemCost = 7;
+// tokens, whose items are of unlike length: 155, 148, 151 us with 4, 5, 7; four of up
+// to 2000, heads of 128: 76, 77, 80)
+constexpr int kItemCost = 5;
 constexpr int kMinTiles = 4;                // key tiles a share holds at least
 constexpr int kSoftWarps = 8;
 // a third warpgroup (two TMA and two MMA warps) gives registers to the softmax
@@ -127,11 +134,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     pdl_wait();
 
     const int tile_rows = kRows / a.group * a.group;   // whole tokens
-    const RowTileExtent<kKeys, kItemCost> extent{tile_rows, a.group, a.window};
+    const int R = 2 * tile_rows;                       // rows of an item: this CTA's row tile and its neighbour's
+    const int rank = (int)blockIdx.x & 1, share = (int)blockIdx.x / 2;
+    const RowTileExtent<kKeys, kItemCost> extent{R, a.group, a.window};
     int P;
     long long total, w0, w1;
     Item t;
-    const bool busy = find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, (int)blockIdx.x, (int)gridDim.x,
+    const bool busy = find_share<kThreads>(a.s, a.c, extent, a.tiles, kMinTiles, share, (int)gridDim.x / 2,
                                            sm_scan, &g_attn_chunk_error, total, P, w0, w1, t);
     auto fail = [&] {
         if (!*abort_flag) {
@@ -158,7 +167,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             Ring<kSlots> ring(is_v ? 1 : 0);   // K(0), V(0), K(1), ...
             for (long long w = w0; w < w1 && ok;) {
                 const Segment seg = segment_of(extent, t, w, w1);
-                const int nt = seg.n, key0 = seg.first * kKeys;
+                // (an item's second row tile may be absent)
+                const int nt = t.rows > rank * tile_rows ? seg.n : 0, key0 = seg.first * kKeys;
                 const int* trow = a.s.table + (long long)t.b * a.s.width;
                 // lane i: the page of box i of the current 32 boxes of this segment, and of the next 32
                 auto raw_id = [&](int x) {
@@ -171,7 +181,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     ++used;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(Q_FULL), (uint32_t)(NC * tile_rows * 128));
-                        const int tok = t.q.q0 + t.rt * (tile_rows / a.group);
+                        const int tok = t.q.q0 + (t.rt * R + rank * tile_rows) / a.group;
                         for (int x = 0; x < NC; ++x)
                             tma_load_q(sbase + (uint32_t)(x * kChunk), &tmap_q, t.hk * a.group, tok, x, bar(Q_FULL));
                     }
@@ -264,7 +274,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 };
                 for (long long w = w0; w < w1 && ok;) {
                     const Segment seg = segment_of(extent, t, w, w1);
-                    if (seg.n > 0) {
+                    if (seg.n > 0 && t.rows > rank * tile_rows) {
                         if (!is_pv) need(bar(Q_FULL), used & 1u);
                         for (int j = 0; j < seg.n && ok; ++j, ring.skip(2), sb.skip(1)) {
                             const uint32_t s_tmem = tmem + C::kS + 128u * sb.slot, o_tmem = tmem + C::kO;
@@ -330,14 +340,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         auto handed = [&](uint32_t n) { return all_wait(HAND + (int)(n & 1u) * 4 + quad, (n >> 1) & 1u); };
         for (long long w = w0; w < w1 && ok;) {
             const Segment seg = segment_of(extent, t, w, w1);
-            const int nt = seg.n, rows = t.rows;
-            if (!seg.skip) {
-                const int r = t.rt * tile_rows + row;   // packed row of the sequence
+            const int nt = seg.n, rows = min(tile_rows, t.rows - rank * tile_rows);   // of this CTA's row tile
+            if (!seg.skip && rows > 0) {
+                const int r = t.rt * R + rank * tile_rows + row;   // packed row of the sequence
                 const bool live = row < rows, idle = quad * 32 >= rows;
                 const int p = t.q.len - t.q.n + r / a.group;
                 const int hi = live ? p : -1, lo = a.window > 0 ? p - a.window : -1;
-                const int p_lo = t.q.len - t.q.n + t.rt * tile_rows / a.group;
-                const int p_hi = t.q.len - t.q.n + (t.rt * tile_rows + rows - 1) / a.group;
+                const int p_lo = t.q.len - t.q.n + (t.rt * R + rank * tile_rows) / a.group;
+                const int p_hi = t.q.len - t.q.n + (t.rt * R + rank * tile_rows + rows - 1) / a.group;
                 const int key0 = seg.first * kKeys;
                 float m = -INFINITY, l = 0.0f;   // l is relative to m, the maximum in use when this warpgroup last looked
                 for (int j = 0; j < nt && ok; ++j) {
@@ -459,7 +469,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     }
                     const float m2 = m * scale;   // -inf stays
                     const long long orow = (long long)(t.q.q0 + r / a.group) * a.q_heads + t.hk * a.group + r % a.group;
-                    float* part = a.partial + (size_t)(2 * blockIdx.x + (w == w0 ? 0 : 1)) * part_floats(D);
+                    constexpr size_t kPart = 2 * part_floats(D);   // both row tiles
+                    float* part = a.partial + (size_t)(2 * share + (w == w0 ? 0 : 1)) * kPart + rank * part_floats(D);
                     if (!idle)
                         emit_row<D>(a, seg.whole, part, row, live, orow, m2, l, [&](int c, uint32_t (&o)[32]) {
                             if (nt > 0) {
@@ -476,8 +487,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         if (lane == 0) mbar_arrive(bar(O_EMPTY));
                     }
                     if (!seg.whole && !idle &&
-                        count_part<kItemCost>(t, a.counters + quad, total, P))
-                        add_parts<D, kItemCost>(a, t, a.partial, part_floats(D), row, live, orow, total, P, 0, D);
+                        count_part<kItemCost>(t, a.counters + 4 * rank + quad, total, P))
+                        add_parts<D, kItemCost>(a, t, a.partial + rank * part_floats(D), kPart, row, live, orow, total, P, 0,
+                                                D);
                 }
                 first_tile += (uint32_t)nt;
             }
@@ -514,10 +526,11 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const int R = kRows / a.group * a.group;
+    const int R = 2 * (kRows / a.group * a.group);
     a.tiles = (int)(((long long)a.s.max_new * a.group + R - 1) / R);
-    const long long P = most_shares(a, kKeys, kItemCost, kMinTiles, sms);
-    return launch_pdl(attn_chunk_kernel<D>, dim3((unsigned)P), dim3(kThreads), C::kSmem, stream, true, mq, mk, mv, a, box);
+    const long long P = most_shares(a, kKeys, kItemCost, kMinTiles, sms / 2);
+    return launch_pdl_clusters(attn_chunk_kernel<D>, 2, dim3((unsigned)(2 * P)), dim3(kThreads), C::kSmem, stream, mq, mk,
+                               mv, a, box);
 }
 
 }  // namespace
