@@ -558,14 +558,14 @@ def _layout(name: str, shape, stride, like=None) -> CacheLayout:
     return CacheLayout(shape[0], shape[2], shape[1], shape[3], stride[0], stride[1], stride[2])
 
 
-def _here(**tensors) -> None:
-    """name=tensor or None: each lies on the current device, whose kernel the call
+def _here(names: str, *tensors) -> None:
+    """Each tensor (None left out) lies on the current device, whose kernel the call
     launches.  (A kernel can reach another GPU's memory where peer access is on,
     which is no way to run these.)"""
     now = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() not in (now, -1):   # (-1, a CPU tensor: _dev says so)
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{now}")
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != now and t.is_cuda:   # (a CPU tensor: _dev says so)
+            raise ValueError(f"{names.split()[i]} is on cuda:{t.get_device()}, the current device is cuda:{now}")
 
 
 def _caches(k: torch.Tensor, v: torch.Tensor | None, kn: str, vn: str) -> CacheLayout:
@@ -638,8 +638,8 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     if q_out is None:
         q_out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
     _covers(positions=(positions, T), slots=(slots, T), q_out=(q_out, T * Hq * D))
-    _here(q=q, k=k, v=v, positions=positions, slots=slots, inv_freq=inv_freq, k_cache=k_cache, v_cache=v_cache,
-          q_out=q_out)
+    _here("q k v positions slots inv_freq k_cache v_cache q_out",
+          q, k, v, positions, slots, inv_freq, k_cache, v_cache, q_out)
     _check("tern_rope_append", lib().tern_rope_append(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), 1 if kind == torch.float32 else 0, qs, ks, vs,
         _dev(positions, torch.int32, "positions"), _dev(slots, torch.int64, "slots"),
@@ -687,7 +687,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if out is None:
         out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
     _covers(out=(out, T * Hq * D), lse=(lse, T * Hq))
-    _here(q=q, k_cache=k_cache, v_cache=v_cache, table=table, lens=lens, q_start=q_start, out=out, lse=lse, ws=ws)
+    _here("q k_cache v_cache table lens q_start out lse ws", q, k_cache, v_cache, table, lens, q_start, out, lse, ws)
     if ws is None:
         ws = _scratch(paged_attention_workspace_bytes(B, T, max_new if start else T // B, Hq, lay.kv_heads, D),
                       q.device, stream, ATTENTION_COUNTER_BYTES)
@@ -714,7 +714,7 @@ def attention_mass(q: torch.Tensor, k_cache: torch.Tensor, table: torch.Tensor, 
         out = mass
     need = lay.pages * lay.kv_heads * lay.page_size
     _covers(lse=(lse, T * Hq), mass=(mass, need), out=(out, need))
-    _here(q=q, k_cache=k_cache, table=table, lens=lens, q_start=q_start, lse=lse, mass=mass, out=out)
+    _here("q k_cache table lens q_start lse mass out", q, k_cache, table, lens, q_start, lse, mass, out)
     _check("tern_attention_mass", lib().tern_attention_mass(
         q.data_ptr(), qs, k_cache.data_ptr(), ctypes.addressof(lay), _dev(table, torch.int32, "table"), W,
         _dev(lens, torch.int32, "lens"), start, B, T, max_new, Hq, lay.head_dim ** -0.5 if scale is None else scale,
@@ -745,8 +745,8 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor
         dst_lens = _new(B, torch.int32, mass.device, stream)
     _covers(mass=(mass, lay.pages * H * lay.page_size), lens=(lens, B), keep=(keep, B * H * budget),
             dst_mass=(dst_mass, dlay.pages * dlay.kv_heads * dlay.page_size), dst_lens=(dst_lens, B))
-    _here(k_cache=k_cache, v_cache=v_cache, mass=mass, table=table, lens=lens, dst_k=dst_k, dst_v=dst_v,
-          dst_mass=dst_mass, dst_table=dst_table, keep=keep, dst_lens=dst_lens)
+    _here("k_cache v_cache mass table lens dst_k dst_v dst_mass dst_table keep dst_lens",
+          k_cache, v_cache, mass, table, lens, dst_k, dst_v, dst_mass, dst_table, keep, dst_lens)
     _check("tern_cache_evict", lib().tern_cache_evict(
         k_cache.data_ptr(), v_cache.data_ptr(), ctypes.addressof(lay), _dev(mass, torch.float32, "mass"),
         _dev(table, torch.int32, "table"), table.shape[1], _dev(lens, torch.int32, "lens"), B, budget, recent,
