@@ -170,7 +170,9 @@ def _scratch(nbytes: int, device, stream, counters: int | None = None) -> torch.
     if stream is not None:
         with _there(stream):
             return _scratch(nbytes, device, None, counters)
-    if counters is None:
+    # (filling a small one takes less than the host needs for a view of its counters: a call of
+    # one token 31 us, not 35)
+    if counters is None or nbytes <= 8 << 20:
         return workspace(nbytes, device)
     ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     ws[:counters].zero_()

@@ -29,6 +29,17 @@ int useful_window(const Args& a, int window) {
     return window < (long long)a.s.width * a.c.page_size ? window : 0;
 }
 
+// few rows: bound by reading the cache and by latency, which suits mma.sync
+// and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
+// 32k keys, 4 sequences: 92 us, against 115 from the rows kernel with 32 rows an item);
+// past one row tile the kernel with three S buffers, which at heads of 256 has room
+// for two only and gains nothing (512 tokens over 32k keys: 245 us against 241)
+enum class AttnKernel { rows, tiles, chunk };
+AttnKernel attn_kernel(int max_new, int group, int head_dim) {
+    if ((long long)max_new * group <= 16) return AttnKernel::rows;
+    return max_new <= 128 / group || head_dim == 256 ? AttnKernel::tiles : AttnKernel::chunk;
+}
+
 tern_status check_heads(const CacheView& c, int q_heads, long long q_stride) {
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return TERN_ERR_SHAPE;
     if (q_heads < 1 || q_heads % c.kv_heads != 0 || q_heads / c.kv_heads > 64) return TERN_ERR_SHAPE;
@@ -48,7 +59,12 @@ extern "C" size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new
     if (B < 1 || T < 0 || max_new < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return kAttnCounterBytes + std::max({attn_rows_workspace(), attn_tiles_workspace(), attn_chunk_workspace()});
+    // the longest sequence's tokens: the average at least (a call without q_start has all equal)
+    const int most = std::max(std::min(max_new, T), T / B);
+    const AttnKernel kernel = attn_kernel(most, q_heads / kv_heads, head_dim);
+    return kAttnCounterBytes + (kernel == AttnKernel::rows    ? attn_rows_workspace(head_dim)
+                                : kernel == AttnKernel::tiles ? attn_tiles_workspace(head_dim)
+                                                              : attn_chunk_workspace(head_dim));
 }
 
 extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, const void* k_cache,
@@ -66,7 +82,7 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     if (!k_cache || !v_cache || (T > 0 && (!q || !out))) return TERN_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned_to(lse, 4))
         return TERN_ERR_ALIGN;
-    if (!workspace || workspace_bytes < tern_paged_attention_workspace_bytes(B, T, max_new, q_heads, a.c.kv_heads,
+    if (!workspace || workspace_bytes < tern_paged_attention_workspace_bytes(B, T, a.s.max_new, q_heads, a.c.kv_heads,
                                                                              a.c.head_dim))
         return TERN_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return TERN_ERR_ALIGN;
@@ -85,16 +101,9 @@ extern "C" tern_status tern_paged_attention(const void* q, long long q_stride, c
     a.lse = lse;
     a.counters = static_cast<unsigned*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
-    const long long rows = (long long)a.s.max_new * a.group;
-    // few rows: bound by reading the cache and by latency, which suits mma.sync
-    // and warps that work alone; more rows, from 17 on: tcgen05 (20 rows a head over
-    // 32k keys, 4 sequences: 92 us, against 115 from the rows kernel with 32 rows an item);
-    // past one row tile the kernel with three S buffers, which at heads of 256 has room
-    // for two only and gains nothing (512 tokens over 32k keys: 245 us against 241)
-    const bool one = a.s.max_new <= 128 / a.group || a.c.head_dim == 256;
-    const cudaError_t e = rows <= 16 ? launch_attn_rows(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                          : one      ? launch_attn_tiles(a, k_cache, v_cache, sms, (cudaStream_t)stream)
-                                     : launch_attn_chunk(a, k_cache, v_cache, sms, (cudaStream_t)stream);
+    const AttnKernel kernel = attn_kernel(a.s.max_new, a.group, a.c.head_dim);
+    auto launch = kernel == AttnKernel::rows ? launch_attn_rows : kernel == AttnKernel::tiles ? launch_attn_tiles : launch_attn_chunk;
+    const cudaError_t e = launch(a, k_cache, v_cache, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

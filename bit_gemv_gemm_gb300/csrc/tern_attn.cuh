@@ -487,8 +487,8 @@ cudaError_t launch_mass_tiles(const MassArgs& a, const void* k, int sms, cudaStr
 cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 cudaError_t launch_attn_tiles(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
 cudaError_t launch_attn_chunk(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream);
-size_t attn_rows_workspace();
-size_t attn_tiles_workspace();
-size_t attn_chunk_workspace();
+size_t attn_rows_workspace(int D);
+size_t attn_tiles_workspace(int D);
+size_t attn_chunk_workspace(int D);
 
 }  // namespace tern

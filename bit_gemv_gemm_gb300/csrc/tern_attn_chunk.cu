@@ -535,7 +535,7 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
 
 }  // namespace
 
-size_t attn_chunk_workspace() { return (size_t)kMaxSms * 2 * 4 * part_floats(128); }
+size_t attn_chunk_workspace(int D) { return (size_t)kMaxSms * 2 * 4 * part_floats(D); }
 
 cudaError_t launch_attn_chunk(const AttnArgs& a, const void* k, const void* v, int sms, cudaStream_t stream) {
     switch (a.c.head_dim) {

@@ -27,7 +27,7 @@ namespace {
 __device__ int g_attn_rows_error;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStrip = 16;
-constexpr int R = 16, kMaxD = 256;            // query rows of an item
+constexpr int R = 16;                          // query rows of an item
 constexpr int kItemCost = 4;                   // strips' time that an item costs besides its own
 constexpr int kMinUnits = 2 * kWarps;         // strips a share holds at least (two a warp)
 
@@ -38,6 +38,7 @@ struct Cfg {
     static constexpr int kRing = kStages * kStage;                // one warp's
     static constexpr int kQ = R * D * 2;
     static constexpr int kCtas = D == 256 ? 1 : 2;                // an SM
+    static constexpr int kPart = R * (D + 2);                     // floats of a part
     static constexpr size_t kSmemQ = (size_t)kWarps * kRing;
     static constexpr size_t kSmemBar = kSmemQ + kQ;
     static constexpr size_t kSmemStat = kSmemBar + kWarps * kStages * 8;
@@ -264,7 +265,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         if (*abort_flag) return;
 
         const bool whole = seg.whole;
-        float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * (R * (kMaxD + 2));
+        float* part = a.partial + (size_t)(2 * cta + (w == w0 ? 0 : 1)) * C::kPart;
         auto store_row = [&](int r, int c, const float (&y)[4], float mm, float ll) {
             // columns c .. c + 3 of row r, divided by the sum
             const int tok = (r0 + r) / a.group, g = (r0 + r) % a.group;
@@ -294,7 +295,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 store_row(r, c, y, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(part + r * D + c), make_float4(y[0], y[1], y[2], y[3]));
-                if (c == 0) __stcg(reinterpret_cast<float2*>(part + R * kMaxD + 2 * r), make_float2(mm, ll));
+                if (c == 0) __stcg(reinterpret_cast<float2*>(part + R * D + 2 * r), make_float2(mm, ll));
             }
         }
         if (!whole) {
@@ -318,8 +319,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int x = min(x0 + k, c_hi);
-                            const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * (R * (kMaxD + 2));
-                            st[k] = __ldcg(reinterpret_cast<const float2*>(px + R * kMaxD + 2 * r));
+                            const float* px = a.partial + (size_t)(2 * x + (x == c_lo ? late : 0)) * C::kPart;
+                            st[k] = __ldcg(reinterpret_cast<const float2*>(px + R * D + 2 * r));
                             v[k] = __ldcg(reinterpret_cast<const float4*>(px + r * D + c));
                         }
 #pragma unroll
@@ -370,7 +371,11 @@ cudaError_t launch(AttnArgs a, const void* k, const void* v, int sms, cudaStream
 
 }  // namespace
 
-size_t attn_rows_workspace() { return (size_t)kMaxSms * 2 * 2 * R * (kMaxD + 2) * 4; }
+template <int D>
+constexpr size_t parts_bytes() { return (size_t)kMaxSms * Cfg<D>::kCtas * 2 * Cfg<D>::kPart * 4; }
+size_t attn_rows_workspace(int D) {
+    return D == 64 ? parts_bytes<64>() : D == 128 ? parts_bytes<128>() : parts_bytes<256>();
+}
 
 cudaError_t launch_attn_rows(const AttnArgs& a, const void* k, const void* v, int sms,
                              cudaStream_t stream) {

@@ -51,3 +51,15 @@ def test_strides_of_single_axes_say_nothing(tern):
         tern._layout("v_cache", dense.shape, dense.stride(), (v.shape, v.stride()))
     with pytest.raises(ValueError, match="v_cache"):
         tern._layout("v_cache", (4, 2, 16, 64), (2048, 1024, 64, 1), ((4, 2, 16, 64), (2048, 64, 128, 1)))
+
+
+def test_attention_workspaces_follow_the_need(tern):
+    """One token takes less than a chunk, small heads less than large, and what a longer step needs is never less."""
+    size = tern.paged_attention_workspace_bytes
+    assert size(1, 1, 1, 32, 8, 128) < 8 << 20 < size(1, 512, 512, 32, 8, 128)
+    for d in (64, 128, 256):
+        steps = [size(2, 2 * n, n, 32, 8, d) for n in (0, 1, 4, 5, 32, 33, 4000)]
+        assert steps == sorted(steps) and steps[-1] <= 1 << 27
+        # max_new counts up to T, and is the average at least
+        assert size(4, 4, 100, 32, 8, d) == size(4, 4, 4, 32, 8, d) and size(4, 80, 0, 32, 8, d) == size(4, 80, 20, 32, 8, d)
+    assert size(1, 512, 512, 32, 8, 64) < size(1, 512, 512, 32, 8, 128) < size(1, 512, 512, 32, 8, 256)
