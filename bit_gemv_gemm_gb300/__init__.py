@@ -450,6 +450,7 @@ def device_error() -> int:
 SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER = 0, 1
 DEVERR_GEMM_MMA_WAIT, DEVERR_GEMV_RANGE_FLAG_WAIT, DEVERR_GEMV_ACTIVATION_RANGE = 0x103, 0x202, 0x203
 DEVERR_CACHE_PAGE, DEVERR_CACHE_SEQUENCE, DEVERR_CACHE_SLOT = 0x301, 0x302, 0x303
+DEVERR_ATTN_WAIT = 0x311
 
 
 def wait_selftest(which: int, limit_us: int, stream=None) -> None:
@@ -709,7 +710,8 @@ def attention_mass(q: torch.Tensor, k_cache: torch.Tensor, table: torch.Tensor, 
     """Adds the attention weight each cached key received from the new tokens
     to its running mass: out = decay * mass + sum exp(s - lse), fp32 [pages,
     kv_heads, page_size]; out defaults to mass itself.  The other arguments as
-    paged_attention's, lse its output."""
+    paged_attention's, lse its output.  No page may stand in two sequences'
+    tables: one's sum would overwrite the other's."""
     lay = _caches(k_cache, None, "k_cache", "")
     qs, T, Hq, B, W, start, max_new = _sequences(q, lay, table, lens, q_start, max_new)
     if out is None:

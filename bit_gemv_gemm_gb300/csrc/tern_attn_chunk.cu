@@ -25,8 +25,8 @@
 // loads and waits: what one has just read is in L2 for the other.  A pair is
 // launched as a cluster, which puts it on neighbouring SMs, and shares nothing
 // else (single CTAs with a row tile each, 512 tokens over 32k keys 226 us and whole
-// prompts 188; pairs without the cluster 213 and 192; pairs 212 and 148).
-// 512 tokens over 32k keys, 32 heads of 128: 212 us, 1.28 PFLOP/s, 10 TB/s from L2
+// prompts 188; pairs without the cluster 213 and 192; pairs 214 and 148).
+// 512 tokens over 32k keys, 32 heads of 128: 214 us, 1.27 PFLOP/s, 10 TB/s from L2
 // (195 us, 1.39 PFLOP/s, where three inputs take turns).  TMA multicast of each
 // half to both CTAs took 202 (191), but a library that programs of several GPUs
 // load has no multicast loads.  The tiles kernel's two streams take 243 there and

@@ -15,7 +15,7 @@
 // fixed order.  A segment that is the whole item is written out; a part goes to
 // the workspace, and the CTA that counts itself last into the item's counter
 // adds the parts in their order, so results do not depend on which CTA is last.
-// 32 sequences of up to 16k keys, 8 key heads of 128: 204 us, 6.4 TB/s; one token
+// 32 sequences of up to 16k keys, 8 key heads of 128: 207 us, 6.4 TB/s; one token
 // over 500 keys is a chain of dependent reads, some 8 us.
 #include <algorithm>
 

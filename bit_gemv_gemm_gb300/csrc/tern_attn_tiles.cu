@@ -23,9 +23,9 @@
 // warps without a live row do no arithmetic.  At D = 256, where one O takes half
 // of tensor memory, there is one stream with two S buffers: one thread issues QK,
 // ahead by a tile, the other PV.  Row tiles that read the same keys are then
-// bound by L2's rate, 8.5 TB/s (2 x 300 tokens, window of 4096: 58 us), and a
-// verify step by the cache's (4 x 5 tokens over 32k keys, 8 key heads of 128: 92 us,
-// 5.7 TB/s, the last 8 us the joins).
+// bound by L2's rate, 8.5 TB/s (2 x 300 tokens, window of 4096: 61 us), and a
+// verify step by the cache's (4 x 5 tokens over 32k keys, 8 key heads of 128: 94 us,
+// 5.6 TB/s, the last 8 us the joins).
 // Slots past a sequence's last key and before its windows may hold anything: scores are masked before
 // the exponential and V's rows are zeroed in shared memory by the TMA warp
 // before the tile is handed on (a row of P is 0 there, and 0 * NaN is not).

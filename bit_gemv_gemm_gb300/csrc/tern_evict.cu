@@ -17,10 +17,10 @@
 //     bytes a thread, the rows of two keys in flight a thread and the places of
 //     the next two looked up meanwhile.
 // Bound by the copy: each kept key's rows are read and written once.  A CTA is a
-// chain of waits (lengths, masses, six cluster barriers, table, rows), so four
+// chain of waits (lengths, masses, selection, table, rows), so four
 // share an SM, and the clusters are as large as lets all CTAs run at once:
 // sixteen sequences of 20000 keys cut to 4096, eight heads, take 365 us with one
-// CTA an SM, 152 with four in clusters of eight (two waves; 3.6 TB/s of the rows).
+// CTA an SM, 142 with four in clusters of four (512 CTAs, one wave; 3.9 TB/s of the rows).
 #include <cooperative_groups.h>
 
 #include "tern_cache.cuh"

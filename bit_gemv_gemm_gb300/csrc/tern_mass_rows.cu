@@ -8,7 +8,7 @@
 // the weights are exp2(S - lse) at once, and a key's sum is a sum down its
 // column of S: over a thread's rows, then over the eight lanes that hold the
 // column.  A strip belongs to one warp, so a key's sum has a fixed order.
-// 8 sequences of up to 16k keys, 8 key heads of 128: 38 us, 4.7 TB/s (some 5 us to
+// 8 sequences of up to 16k keys, 8 key heads of 128: 39 us, 4.7 TB/s (some 5 us to
 // find the shares and fill the rings).
 #include <algorithm>
 

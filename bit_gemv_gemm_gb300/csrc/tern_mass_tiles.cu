@@ -11,7 +11,7 @@
 // bits).  Reading it from shared memory instead, broadcast to every thread, cost
 // four wavefronts a 16-byte load beside products that already take the whole
 // bandwidth of shared memory (512 tokens over 16k keys, 32 heads of 128: 99 us then,
-// 65 us, 1.05 PFLOP/s, now).
+// 66 us, 1.03 PFLOP/s, now).
 // An item is NS key tiles of 128 keys (two; one at D = 256) of one sequence and
 // key head.  K's tiles are brought once and stay; the query rows that see them
 // stream past in tiles of 128 packed rows (128 / group tokens, every head of

@@ -394,7 +394,12 @@ tern_status tern_affine_gemm(const void *x, const uint32_t *codes, const void *s
 /* table, lens, q_start, positions, slots and the fp32 arrays need only the */
 /* alignment of their type.  Device-side values that do not fit the arrays  */
 /* are reported through tern_device_error (TERN_DEVERR_CACHE_*), never      */
-/* followed out of bounds; the call's output is then undefined.             */
+/* followed out of bounds; the call's output is then undefined, and nothing */
+/* is written in the place of a bad page.                                   */
+/*                                                                          */
+/* Every array is memory of the current device.  Pages may stand in several */
+/* sequences' tables (a common prefix) where a call only reads them; what a */
+/* call writes has to be one sequence's alone.                              */
 /* ---------------------------------------------------------------------- */
 
 /* Strides in elements, multiples of 8, at least head_dim each; distinct
@@ -430,7 +435,7 @@ tern_status tern_rope_frequencies_host(int rot_dim, double base, int scaling, do
  * tokens, q (q_heads heads) and k (kv_heads) are turned and rounded once to
  * bf16 (nearest even); q goes to q_out, bf16 [T][q_heads][head_dim], k and v go
  * to slot slots[t] of the cache (int64, page * page_size + slot; a negative
- * slot stores nothing, a slot twice in one call keeps one of the two).
+ * slot stores nothing; a slot twice in one call ends up with values of both).
  *   - q, k, v: fp32 (in_is_f32) or bf16, the token stride of each in elements
  *     (a multiple of 8), heads contiguous in a token: pointers into one
  *     [T][q | k | v] product output work.  16-byte aligned, no overlap with
@@ -438,8 +443,9 @@ tern_status tern_rope_frequencies_host(int rot_dim, double base, int scaling, do
  *   - The first rot_dim values of a head turn (even, <= head_dim; 0: none),
  *     by positions[t] * inv_freq[i] (int32, fp32 [rot_dim / 2]): pair i is
  *     values 2i and 2i + 1 (interleaved) or i and i + rot_dim / 2; cos and sin
- *     are multiplied by attn_factor.  The angle is reduced in 64 bits, so
- *     its error does not grow with the position.
+ *     are multiplied by attn_factor.  The angle is reduced in 64 bits: its error
+ *     is at most 2^-51 of pos * inv_freq (1e-6 rad at position 2^31, 5e-11 at 1e5)
+ *     beside the fp32 sine's and cosine's own.
  * One kernel launch (none for T = 0). */
 tern_status tern_rope_append(const void *q, const void *k, const void *v, int in_is_f32, long long q_stride,
                              long long k_stride, long long v_stride, const int *positions, const long long *slots,
@@ -456,13 +462,16 @@ tern_status tern_rope_append(const void *q, const void *k, const void *v, int in
  * at or past lens[b], and with a window those of keys before every query's, may
  * hold anything, NaN included; only the pages that hold a visible key are read.  A
  * value of V that is not finite, of a key that some query of the call sees, may
- * reach queries that do not see it (their probability of 0 times it).  q_heads a multiple of kv_heads, at most 64
- * query heads a key head; head_dim 64, 128 or 256.  One kernel launch; the
+ * reach queries that do not see it (their probability of 0 times it).  A row that
+ * sees a score of NaN or +inf gets NaN, output and lse; a score of -inf weighs
+ * nothing, and a row of such alone is one that sees no key.
+ *   q_heads a multiple of kv_heads, at most 64 query heads a key head; head_dim 64,
+ * 128 or 256; scale * log2(e) finite (TERN_ERR_SHAPE).  One kernel launch; the
  * result does not vary from run to run.
- * The workspace's first TERN_ATTENTION_COUNTER_BYTES are zero-filled once before
+ *   The workspace's first TERN_ATTENTION_COUNTER_BYTES are zero-filled once before
  * its first use and left ready for the next call, the rest may hold anything; its
- * size never exceeds 128 MiB.  Calls that share it must be
- * ordered; after a device error zero-fill it again. */
+ * size never exceeds 128 MiB.  Calls that share it must be ordered; after a device
+ * error zero-fill those bytes again. */
 #define TERN_ATTENTION_COUNTER_BYTES 8192
 size_t tern_paged_attention_workspace_bytes(int B, int T, int max_new, int q_heads, int kv_heads, int head_dim);
 tern_status tern_paged_attention(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
@@ -479,7 +488,8 @@ tern_status tern_paged_attention(const void *q, long long q_stride, const void *
  * (a row with an infinite lse gives nothing).  mass and mass_out as described
  * above; they may be the same array.  Every key's page is read, a key outside
  * every window decays.  Slots that hold no key are left alone.  One kernel
- * launch, no atomics: a key's sum has a fixed order. */
+ * launch, no atomics: a key's sum has a fixed order.  A page belongs to one
+ * sequence of the call: the sums of two that share it would overwrite each other. */
 tern_status tern_attention_mass(const void *q, long long q_stride, const void *k_cache,
                                 const tern_cache_layout *layout, const int *table, int table_width, const int *lens,
                                 const int *q_start, int B, int T, int max_new, int q_heads, float scale, int window,
