@@ -71,6 +71,11 @@ EXPORTS = {
     "tern_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "tern_paged_attention": (_I, [_P, _LL, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _I, _P, _P, _P, _SZ, _P]),
     "tern_attention_mass": (_I, [_P, _LL, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _I, _P, _F, _P, _P, _P]),
+    "tern_rms_norm": (_I, [_P, _I, _LL, _LL, _P, _I, _LL, _LL, _P, _I, _LL, _LL, _I, _P, _F, _F, _F, _I, _I, _I, _I, _P,
+                           _I, _P, _P]),
+    "tern_short_conv": (_I, [_P, _I, _LL, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "tern_gated_delta": (_I, [_P, _P, _P, _LL, _LL, _LL, _P, _LL, _P, _LL, _P, _P, _F, _I, _P, _I, _P, _P, _P, _P, _I,
+                              _I, _I, _I, _I, _I, _I, _P, _P]),
     "tern_cache_evict": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P]),
 }
 
@@ -450,7 +455,7 @@ def device_error() -> int:
 SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER = 0, 1
 DEVERR_GEMM_MMA_WAIT, DEVERR_GEMV_RANGE_FLAG_WAIT, DEVERR_GEMV_ACTIVATION_RANGE = 0x103, 0x202, 0x203
 DEVERR_CACHE_PAGE, DEVERR_CACHE_SEQUENCE, DEVERR_CACHE_SLOT = 0x301, 0x302, 0x303
-DEVERR_ATTN_WAIT = 0x311
+DEVERR_ATTN_WAIT, DEVERR_STATE_SLOT = 0x311, 0x321
 
 
 def wait_selftest(which: int, limit_us: int, stream=None) -> None:
@@ -758,3 +763,175 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor
         _dev(dst_table, torch.int32, "dst_table"), dst_table.shape[1], _dev(keep, torch.int32, "keep"),
         _dev(dst_lens, torch.int32, "dst_lens"), _stream(stream)))
     return keep, dst_lens
+
+
+# ---------------------------------------------------------------------------
+# the linear-attention layer
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=4096)
+def _row_strides(name: str, shape, stride, like=None) -> tuple[int, int]:
+    """The token and head strides of rows [T, dim] or [T, heads, dim], each row contiguous."""
+    if len(shape) not in (2, 3) or (stride[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be [tokens, dim] or [tokens, heads, dim] with contiguous rows")
+    if like is not None and shape != like:
+        raise ValueError(f"{name} must have x's shape {tuple(like)}, got {tuple(shape)}")
+    stride = _steps(shape, stride)
+    return stride[0], stride[1] if len(shape) == 3 else 0
+
+
+def _f32_or_bf16(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor")
+    return 1 if t.dtype is torch.float32 else 0
+
+
+_GATES = {"silu": 0, "sigmoid": 1}
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, scale: float = 1.0,
+             gate: torch.Tensor | None = None, gate_act: str = "silu", eps: float = 1e-6, weight_offset: float = 0.0,
+             after: bool = False, residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             out_dtype=None, stream=None) -> torch.Tensor:
+    """The norm before or after a block, with the residual stream and a gate.
+
+    before: h = residual + scale * x, residual_out = h where given (it may be the
+    residual itself), out = h / rms(h) * (weight + weight_offset) [* act(gate)];
+    after=True: out = residual + scale * (x / rms(x) * (weight + weight_offset) [* act(gate)]).
+
+    x, residual and gate [T, dim] or [T, heads, dim], fp32 or bf16 each, any token
+    and head strides; weight fp32 [dim].  Returns out, contiguous, of out_dtype:
+    bf16 if not given, the residual's type after a block."""
+    if gate_act not in _GATES:
+        raise ValueError(f"gate_act must be one of {sorted(_GATES)}")
+    shape = x.shape
+    xt, xh = _row_strides("x", shape, x.stride())
+    T, dim = shape[0], shape[-1]
+    heads = shape[1] if len(shape) == 3 else 1
+    rt = rh = gt = gh = 0
+    kinds = [_f32_or_bf16(x, "x"), 0, 0]
+    if residual is not None:
+        rt, rh = _row_strides("residual", residual.shape, residual.stride(), shape)
+        kinds[1] = _f32_or_bf16(residual, "residual")
+    if gate is not None:
+        gt, gh = _row_strides("gate", gate.shape, gate.stride(), shape)
+        kinds[2] = _f32_or_bf16(gate, "gate")
+    if residual_out is not None and residual is None:
+        raise ValueError("residual_out needs a residual")
+    if residual_out is not None and after:
+        raise ValueError("after a block the output is the new residual")
+    if out is None:
+        out = _new(shape, out_dtype or (residual.dtype if after and residual is not None else torch.bfloat16), x.device,
+                   stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    of32 = _f32_or_bf16(out, "out")
+    _covers(weight=(weight, dim), out=(out, T * heads * dim), residual_out=(residual_out, T * heads * dim))
+    _here("x weight residual gate residual_out out", x, weight, residual, gate, residual_out, out)
+    _check("tern_rms_norm", lib().tern_rms_norm(
+        x.data_ptr(), kinds[0], xt, xh, None if residual is None else residual.data_ptr(), kinds[1], rt, rh,
+        None if gate is None else gate.data_ptr(), kinds[2], gt, gh, _GATES[gate_act],
+        _dev(weight, torch.float32, "weight"), weight_offset, scale, eps, 1 if after else 0, T, heads, dim,
+        _dev(out, out.dtype, "out"), of32,
+        None if residual_out is None else _dev(residual_out, residual.dtype, "residual_out"), _stream(stream)))
+    return out
+
+
+def _states(T: int, slots, dst_slots, past, q_start, max_new):
+    """(slots, dst_slots, past, q_start pointers, B, max_new) of the sequences of a call."""
+    B = slots.numel()
+    _covers(dst_slots=(dst_slots, B), past=(past, B), q_start=(q_start, B + 1))
+    i32 = torch.int32
+    return (_dev(slots, i32, "slots"), None if dst_slots is None else _dev(dst_slots, i32, "dst_slots"),
+            None if past is None else _dev(past, i32, "past"),
+            None if q_start is None else _dev(q_start, i32, "q_start"), B, T if max_new is None else max_new)
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, slots: torch.Tensor,
+               q_start: torch.Tensor | None = None, max_new: int | None = None, bias: torch.Tensor | None = None,
+               silu: bool = True, past: torch.Tensor | None = None, dst_slots: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The causal convolution along the tokens, channel by channel, with its state.
+
+    x fp32 or bf16 [T, C] (any token stride); weight fp32 [C, W], W = 2..4, the
+    last column the token's own; bias fp32 [C]; state fp32 [pool, W - 1, C], a
+    sequence's last W - 1 inputs.  The tokens are those of B = slots.numel()
+    sequences in a row: q_start int32 [B + 1] (None: T / B each) with max_new, the
+    most tokens of one (T if not given).  slots int32 [B]: the states read
+    (negative: zeros); dst_slots: those written (None: slots, negative: none);
+    past int32 [B]: 0 where a sequence starts from zeros.  Returns bf16 [T, C]."""
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError("x must be [tokens, channels] with contiguous tokens")
+    T, C = x.shape
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be [channels, width] for {C} channels, got {tuple(weight.shape)}")
+    W = weight.shape[1]
+    if state.dim() != 3 or state.shape[1:] != (W - 1, C):
+        raise ValueError(f"state must be [pool, {W - 1}, {C}], got {tuple(state.shape)}")
+    kind = _f32_or_bf16(x, "x")
+    if out is None:
+        out = _new((T, C), torch.bfloat16, x.device, stream)
+    _covers(out=(out, T * C), bias=(bias, C))
+    _here("x weight state slots q_start bias past dst_slots out", x, weight, state, slots, q_start, bias, past,
+          dst_slots, out)
+    sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new)
+    _check("tern_short_conv", lib().tern_short_conv(
+        x.data_ptr(), kind, x.stride(0) if T > 1 else C, _dev(weight, torch.float32, "weight"), W,
+        None if bias is None else _dev(bias, torch.float32, "bias"), 1 if silu else 0,
+        _dev(state, torch.float32, "state"), state.shape[0], sl, dl, pp, qp, B, T, max_new, C,
+        _dev(out, torch.bfloat16, "out"), _stream(stream)))
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _gate_stride(name: str, shape, stride, tokens: int, heads: int) -> int:
+    if tuple(shape) != (tokens, heads) or (stride[1] != 1 and heads > 1):
+        raise ValueError(f"{name} must be [{tokens}, {heads}] with contiguous tokens, got {tuple(shape)}")
+    return stride[0] if tokens > 1 else heads
+
+
+def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                state: torch.Tensor, slots: torch.Tensor, q_start: torch.Tensor | None = None,
+                max_new: int | None = None, scale: float | None = None, qk_norm: bool = False,
+                a_log: torch.Tensor | None = None, dt_bias: torch.Tensor | None = None,
+                past: torch.Tensor | None = None, dst_slots: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gated delta rule over new tokens (one, a few or a prompt for each
+    sequence): per value head, S <- exp(g) S + u k^T with u = beta (v - exp(g) S k),
+    out = scale S q.
+
+    q, k bf16 [T, k_heads, Dk], v bf16 [T, v_heads, Dv], views of one
+    convolution's output included; g, beta fp32 [T, v_heads]; state fp32 [pool,
+    v_heads, Dv, Dk], read and written by slot; slots, q_start, max_new, past and
+    dst_slots as short_conv's.  scale 1/sqrt(Dk) if not given.  qk_norm divides
+    queries and keys by their lengths.  With a_log and dt_bias (fp32 [v_heads])
+    the gates come raw: g <- -exp(a_log) softplus(g + dt_bias), beta <-
+    sigmoid(beta).  Returns bf16 [T, v_heads, Dv]."""
+    if state.dim() != 4:
+        raise ValueError("state must be [pool, v_heads, Dv, Dk]")
+    pool, Hv, Dv, Dk = state.shape
+    bf16 = torch.bfloat16
+    qs, ks, vs = _tokens(q, bf16, "q", None, Dk), _tokens(k, bf16, "k", q.shape[1], Dk), _tokens(v, bf16, "v", Hv, Dv)
+    T, Hk = q.shape[:2]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must hold the same number of tokens")
+    gs = _gate_stride("g", g.shape, g.stride(), T, Hv)
+    bs = _gate_stride("beta", beta.shape, beta.stride(), T, Hv)
+    for name, t in (("g", g), ("beta", beta)):
+        if not t.is_cuda or t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be a float32 CUDA tensor")
+    if (a_log is None) != (dt_bias is None):
+        raise ValueError("a_log and dt_bias come together")
+    if out is None:
+        out = _new((T, Hv, Dv), bf16, q.device, stream)
+    _covers(out=(out, T * Hv * Dv), a_log=(a_log, Hv), dt_bias=(dt_bias, Hv))
+    _here("q k v g beta state slots q_start a_log dt_bias past dst_slots out", q, k, v, g, beta, state, slots, q_start,
+          a_log, dt_bias, past, dst_slots, out)
+    sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new)
+    _check("tern_gated_delta", lib().tern_gated_delta(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, g.data_ptr(), gs, beta.data_ptr(), bs,
+        None if a_log is None else _dev(a_log, torch.float32, "a_log"),
+        None if dt_bias is None else _dev(dt_bias, torch.float32, "dt_bias"), Dk ** -0.5 if scale is None else scale,
+        1 if qk_norm else 0, _dev(state, torch.float32, "state"), pool, sl, dl, pp, qp, B, T, max_new, Hk, Hv, Dk, Dv,
+        _dev(out, bf16, "out"), _stream(stream)))
+    return out

@@ -1,0 +1,215 @@
+// tern_delta.cu -- the gated delta rule, token by token.
+//
+//   a = exp(g),  u = beta (v - a S k),  S <- a S + u k^T,  o = scale S q
+//
+// per value head, S [dv][dk] in 32 bits.  A CTA owns some rows of one head's S,
+// which depend on one another's only through q and k: they stay in registers
+// from the first token to the last, so a call of a few tokens reads and writes
+// every state once and is bound by that.
+#include "tern_delta.cuh"
+
+namespace tern {
+namespace {
+
+__device__ int g_delta_error;
+
+constexpr int kStepThreads = 128, kStepBatch = 8;
+
+// 8 lanes share a row: lane l has the values 32 i + 4 l + {0..3}, so that a row's
+// loads are 128 bytes in a piece.  A warp holds 4 x ROWS rows.
+template <int DK>
+__global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArgs a) {
+    constexpr int V4 = DK / 32, ROWS = 256 / DK, PER_WARP = 4 * ROWS, PER_CTA = 4 * PER_WARP, MY = DK / 32;
+    __shared__ __align__(16) float ks[kStepBatch][DK], qs[kStepBatch][DK];
+    __shared__ float4 gates[kStepBatch];          // decay, beta, k.q, unused
+    __shared__ float vs[kStepBatch][PER_CTA];
+    __shared__ __nv_bfloat16 os[kStepBatch][PER_CTA];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % 8;
+    const int h = blockIdx.y, row0 = blockIdx.x * PER_CTA, hk = h / a.group;
+    const StateSeq s = load_state_seq(a.s, blockIdx.z, &g_delta_error);
+    const int live = min(PER_CTA, a.dv - row0);
+
+    float4 S[ROWS][V4];
+    const int mine = warp * PER_WARP + lane / 8;   // and every fourth row after it
+    const long long head = (long long)a.dv * DK;
+    {
+        const float* from = a.state + ((long long)s.src * a.v_heads + h) * head + (long long)row0 * DK;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int i = 0; i < V4; ++i)
+                S[r][i] = s.src >= 0 && mine + 4 * r < live
+                              ? *reinterpret_cast<const float4*>(from + (mine + 4 * r) * DK + 32 * i + 4 * sub)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int t0 = 0; t0 < s.n; t0 += kStepBatch) {
+        const int n = min(kStepBatch, s.n - t0);
+        // a warp a token: its query and key (divided by their lengths), its gates and values
+        for (int i = warp; i < n; i += 4) {
+            const long long t = s.t0 + t0 + i;
+            const __nv_bfloat16* kp = a.k + t * a.k_token + hk * DK + MY * lane;
+            const __nv_bfloat16* qp = a.q + t * a.q_token + hk * DK + MY * lane;
+            float k[MY], q[MY], kk = 0.0f, qq = 0.0f, kq = 0.0f;
+#pragma unroll
+            for (int e = 0; e < MY; e += 2) {
+                const float2 k2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kp + e));
+                const float2 q2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qp + e));
+                k[e] = k2.x;
+                k[e + 1] = k2.y;
+                q[e] = q2.x;
+                q[e + 1] = q2.y;
+            }
+            for (int r = lane; r < live; r += 32)
+                vs[i][r] = __bfloat162float(a.v[t * a.v_token + (long long)h * a.dv + row0 + r]);
+#pragma unroll
+            for (int e = 0; e < MY; ++e) {
+                kk = fmaf(k[e], k[e], kk);
+                qq = fmaf(q[e], q[e], qq);
+                kq = fmaf(k[e], q[e], kq);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                qq += __shfl_xor_sync(0xffffffffu, qq, o);
+                kq += __shfl_xor_sync(0xffffffffu, kq, o);
+            }
+            const float ik = a.norm ? 1.0f / sqrtf(kk + kDeltaNormEps) : 1.0f;
+            const float iq = (a.norm ? 1.0f / sqrtf(qq + kDeltaNormEps) : 1.0f) * a.scale;
+#pragma unroll
+            for (int e = 0; e < MY; ++e) {
+                ks[i][MY * lane + e] = k[e] * ik;
+                qs[i][MY * lane + e] = q[e] * iq;
+            }
+            if (lane == 0) {
+                const float2 gb = delta_gates(a, t, h);
+                gates[i] = make_float4(expf(gb.x), gb.y, kq * ik * iq, 0.0f);
+            }
+        }
+        __syncthreads();
+        for (int i = 0; i < n; ++i) {
+            float4 k[V4], q[V4];
+#pragma unroll
+            for (int c = 0; c < V4; ++c) {
+                k[c] = *reinterpret_cast<const float4*>(&ks[i][32 * c + 4 * sub]);
+                q[c] = *reinterpret_cast<const float4*>(&qs[i][32 * c + 4 * sub]);
+            }
+            const float4 gate = gates[i];
+            float sk[ROWS], sq[ROWS];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                sk[r] = sq[r] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < V4; ++c) {
+                    sk[r] = fmaf(S[r][c].x, k[c].x, fmaf(S[r][c].y, k[c].y, fmaf(S[r][c].z, k[c].z, fmaf(S[r][c].w, k[c].w, sk[r]))));
+                    sq[r] = fmaf(S[r][c].x, q[c].x, fmaf(S[r][c].y, q[c].y, fmaf(S[r][c].z, q[c].z, fmaf(S[r][c].w, q[c].w, sq[r]))));
+                }
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    sk[r] += __shfl_xor_sync(0xffffffffu, sk[r], o);
+                    sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+                }
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const float u = gate.y * (vs[i][mine + 4 * r] - gate.x * sk[r]);
+#pragma unroll
+                for (int c = 0; c < V4; ++c) {
+                    S[r][c].x = fmaf(u, k[c].x, gate.x * S[r][c].x);
+                    S[r][c].y = fmaf(u, k[c].y, gate.x * S[r][c].y);
+                    S[r][c].z = fmaf(u, k[c].z, gate.x * S[r][c].z);
+                    S[r][c].w = fmaf(u, k[c].w, gate.x * S[r][c].w);
+                }
+                if (sub == 0) os[i][mine + 4 * r] = __float2bfloat16(fmaf(u, gate.z, gate.x * sq[r]));
+            }
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < n * PER_CTA; j += kStepThreads) {
+            const int i = j / PER_CTA, r = j % PER_CTA;
+            if (r < live) a.out[((long long)(s.t0 + t0 + i) * a.v_heads + h) * a.dv + row0 + r] = os[i][r];
+        }
+        // (the next batch's staging touches neither os nor anything read above)
+    }
+    if (s.dst < 0 || (s.n == 0 && s.dst == s.src)) return;
+    float* to = a.state + ((long long)s.dst * a.v_heads + h) * head + (long long)row0 * DK;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int i = 0; i < V4; ++i)
+            if (mine + 4 * r < live) *reinterpret_cast<float4*>(to + (mine + 4 * r) * DK + 32 * i + 4 * sub) = S[r][i];
+}
+
+}  // namespace
+
+cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream) {
+    const int per = a.dk == 128 ? 32 : 64;
+    return launch_pdl(a.dk == 128 ? delta_step_kernel<128> : delta_step_kernel<64>,
+                      dim3((a.dv + per - 1) / per, a.v_heads, a.s.B), dim3(kStepThreads), 0, stream, true, a);
+}
+
+cudaError_t read_delta_device_error(int* code) {
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_delta_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_delta_error, &zero, sizeof(int));
+}
+
+}  // namespace tern
+
+using namespace tern;
+
+extern "C" tern_status tern_gated_delta(const void* q, const void* k, const void* v, long long q_token,
+                                        long long k_token, long long v_token, const float* g, long long g_token,
+                                        const float* beta, long long beta_token, const float* a_log,
+                                        const float* dt_bias, float scale, int qk_norm, float* state, int pool,
+                                        const int* slots, const int* dst_slots, const int* past, const int* q_start,
+                                        int B, int T, int max_new, int k_heads, int v_heads, int dk, int dv, void* out,
+                                        tern_stream_t stream) {
+    set_launch_count(0);
+    DeltaArgs a;
+    tern_status st = make_state_seq_view(q_start, slots, dst_slots, past, B, T, max_new, pool, &a.s);
+    if (st != TERN_OK) return st;
+    if ((dk != 64 && dk != 128) || dv < 16 || dv % 16 != 0 || dv > 256 || k_heads < 1 || v_heads < 1 || v_heads > 65535 ||
+        v_heads % k_heads != 0 || !(fabsf(scale) < INFINITY))
+        return TERN_ERR_SHAPE;
+    const long long strides[5] = {q_token, k_token, v_token, g_token, beta_token};
+    const long long least[5] = {(long long)k_heads * dk, (long long)k_heads * dk, (long long)v_heads * dv, v_heads, v_heads};
+    for (int i = 0; i < 5; ++i)
+        if (strides[i] < 0 || (T > 1 && strides[i] < least[i]) || strides[i] >= (1LL << 37) || (i < 3 && strides[i] % 8 != 0))
+            return TERN_ERR_SHAPE;
+    if (!state || (!a_log) != (!dt_bias) || (T > 0 && (!q || !k || !v || !g || !beta || !out))) return TERN_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(out) || !aligned_to(g, 4) ||
+        !aligned_to(beta, 4) || !aligned_to(a_log, 4) || !aligned_to(dt_bias, 4))
+        return TERN_ERR_ALIGN;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != TERN_OK) return st;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.q_token = q_token;
+    a.k_token = k_token;
+    a.v_token = v_token;
+    a.g = g;
+    a.beta = beta;
+    a.g_token = g_token;
+    a.beta_token = beta_token;
+    a.a_log = a_log;
+    a.dt_bias = dt_bias;
+    a.state = state;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.k_heads = k_heads;
+    a.v_heads = v_heads;
+    a.dk = dk;
+    a.dv = dv;
+    a.group = v_heads / k_heads;
+    a.norm = qk_norm;
+    a.scale = scale;
+    const cudaError_t e = launch_delta_step(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return TERN_ERR_CUDA;
+    set_launch_count(1);
+    return TERN_OK;
+}

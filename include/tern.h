@@ -513,6 +513,84 @@ tern_status tern_cache_evict(const void *k_cache, const void *v_cache, const ter
                              tern_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
+/* The linear-attention layer: norms around a block, the short causal      */
+/* convolution, the gated delta rule.  The article's models keep a state   */
+/* in place of keys in three of four layers ("24 linear + 8 full           */
+/* attention", "conv k = 4, fp32 state"); the formulas are the method's,   */
+/* the interface this library's.                                           */
+/*                                                                         */
+/* short_conv and gated_delta take the new tokens of B sequences in a row: */
+/* sequence b's are q_start[b] .. q_start[b+1] - 1 of T (int32 [B + 1],    */
+/* nondecreasing, at most max_new each; NULL: T / B each and max_new is not */
+/* read).  Its state is slot slots[b] of a pool (int32 [B]; negative:      */
+/* zeros), and its new state goes to slot dst_slots[b] (NULL: slots;       */
+/* negative: not stored).  past[b] (int32 [B], nullable) == 0: the sequence */
+/* starts from zeros, whatever its slot holds.  A sequence without tokens  */
+/* moves its state.  Several sequences may read one slot; a slot that one  */
+/* writes may not be another's, read or written, in the same call.  Output */
+/* rows of no sequence are left as they were.                              */
+/*                                                                         */
+/* q_start, slots, dst_slots and past are device arrays.  Values that do   */
+/* not fit are reported through tern_device_error (CACHE_SEQUENCE,         */
+/* STATE_SLOT), never followed out of bounds; a bad slot is neither read   */
+/* nor written.  Every array is memory of the current device; nothing is   */
+/* read before the previous kernel on the stream has finished.  One kernel */
+/* launch, no workspace, no atomics: a result does not vary from run to run. */
+/* ---------------------------------------------------------------------- */
+
+/* Norms of T x heads rows of dim values, fused with the residual stream and a gate:
+ *   before a block (after == 0):  h = residual + scale * x (x without a residual),
+ *     residual_out (nullable, residual's type, contiguous; it may be the residual
+ *     itself) = h, out = h / sqrt(mean(h^2) + eps) * (weight + weight_offset) [* act(gate)];
+ *   after a block (after != 0):  out = residual + scale * (x / sqrt(mean(x^2) + eps)
+ *     * (weight + weight_offset) [* act(gate)]) (0 without a residual).
+ * x, residual (nullable), gate (nullable): fp32 or bf16 each, strides of the token
+ * and the head in elements (multiples of 8), the values of a row contiguous; weight
+ * fp32 [dim]; out fp32 or bf16, contiguous [T][heads][dim].  act(z) is z / (1 + e^-z)
+ * (TERN_GATE_SILU) or 1 / (1 + e^-z).  All sums in fp32, h not rounded before its norm,
+ * every output rounded once.  dim a multiple of 8, at most 32768 (TERN_ERR_SHAPE);
+ * 16-byte aligned pointers.  out may be x or the residual where their types and layouts
+ * agree; no other overlap. */
+#define TERN_GATE_SILU 0
+#define TERN_GATE_SIGMOID 1
+tern_status tern_rms_norm(const void *x, int x_is_f32, long long x_token, long long x_head, const void *residual,
+                          int residual_is_f32, long long residual_token, long long residual_head, const void *gate,
+                          int gate_is_f32, long long gate_token, long long gate_head, int gate_act,
+                          const float *weight, float weight_offset, float scale, float eps, int after, int T,
+                          int heads, int dim, void *out, int out_is_f32, void *residual_out, tern_stream_t stream);
+
+/* The causal convolution of width 2..4 along the tokens, channel by channel:
+ *   out[t][c] = act(bias[c] + sum_w weight[c][w] * x[t - (width - 1) + w][c]),
+ * the inputs before a sequence's first token from its state, fp32 [pool][width - 1]
+ * [channels], the oldest first; the new state is its last width - 1 inputs.  x fp32
+ * or bf16, token stride in elements (a multiple of 8, >= channels), out bf16 [T][channels],
+ * weight fp32 [channels][width], bias fp32 [channels] or NULL, act SiLU (silu != 0) or
+ * none.  channels a multiple of 8, at most 2^20; max_new at most 2^20 (TERN_ERR_SHAPE). */
+tern_status tern_short_conv(const void *x, int x_is_f32, long long x_token, const float *weight, int width,
+                            const float *bias, int silu, float *state, int pool, const int *slots,
+                            const int *dst_slots, const int *past, const int *q_start, int B, int T, int max_new,
+                            int channels, void *out, tern_stream_t stream);
+
+/* The gated delta rule: per value head and token, with the head's state S
+ * (fp32 [dv][dk] of the pool's [pool][v_heads][dv][dk]),
+ *   a = exp(g),  u = beta * (v - a S k),  S <- a S + u k^T,  out = scale * S q.
+ * q, k bf16 [T][k_heads][dk], v bf16 [T][v_heads][dv], token strides in elements
+ * (multiples of 8), heads contiguous in a token (views of one convolution's output
+ * work); value head h reads query and key head h / (v_heads / k_heads).  g and beta
+ * fp32 [T][v_heads], any token stride; g <= 0 (the log of the decay; -inf forgets all).
+ * With a_log and dt_bias (fp32 [v_heads] both, or NULL both) the gates come raw:
+ *   g <- -exp(a_log) * softplus(g + dt_bias),  beta <- 1 / (1 + exp(-beta)).
+ * qk_norm != 0: q and k are divided by sqrt(sum of squares + 1e-6).  out bf16
+ * [T][v_heads][dv].  The state and all sums are fp32; out is rounded once.
+ * dk 64 or 128, dv a multiple of 16, at most 256; |scale| finite (TERN_ERR_SHAPE). */
+tern_status tern_gated_delta(const void *q, const void *k, const void *v, long long q_token, long long k_token,
+                             long long v_token, const float *g, long long g_token, const float *beta,
+                             long long beta_token, const float *a_log, const float *dt_bias, float scale, int qk_norm,
+                             float *state, int pool, const int *slots, const int *dst_slots, const int *past,
+                             const int *q_start, int B, int T, int max_new, int k_heads, int v_heads, int dk, int dv,
+                             void *out, tern_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */
 /* ---------------------------------------------------------------------- */
 
@@ -531,7 +609,8 @@ enum {
     TERN_DEVERR_CACHE_PAGE = 0x301,          /* cache: a page id outside the pool */
     TERN_DEVERR_CACHE_SEQUENCE = 0x302,      /* cache: a length or token range that the call's arrays do not hold */
     TERN_DEVERR_ATTN_WAIT = 0x311,           /* attention: a wait for a copy or a product gave up */
-    TERN_DEVERR_CACHE_SLOT = 0x303           /* cache: a slot past the pool's last */
+    TERN_DEVERR_CACHE_SLOT = 0x303,          /* cache: a slot past the pool's last */
+    TERN_DEVERR_STATE_SLOT = 0x321           /* short_conv, gated_delta: a state slot past the pool's last */
 };
 
 /* Reads and clears the sticky device-side error words of the current device

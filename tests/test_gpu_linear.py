@@ -1,0 +1,448 @@
+"""The linear-attention layer's operators on the GPU against their definitions in 64 bits.
+
+Bounds.  A rounding to bf16 is off by at most 2^-8 of the value (half a step), one
+to fp32 by 2^-24.  Norm: the sum of squares of D terms, its root and the three
+products add at most (D / 8 + 40) 2^-24 in relative terms (8 partial sums at
+least a row), a residual's sum 2^-24 of its parts, and a gate's exponential
+2^-16.  Convolution: 8 products and sums, 2^-20 of the sum of magnitudes; what it
+does to y passes through an activation whose slope is at most 1.1, and whose own
+relative error is 2^-16 from the exponential.  The delta rule: with R the
+largest row of S plus the largest |v|, a token adds errors of at most 2^-17 R to
+a row (two dot products of Dk <= 128 terms, an update; in the chunk form the
+same products with their operands in parts that carry 2^-24), decays shrink them and the
+correction does not grow them (|k| <= 1, beta <= 1), so a row of the final state is
+off by at most `memory` 2^-17 R, `memory` the largest sum of what the decays
+leave.  out reads that with |q| <= 1, and in the chunk form adds products of
+bf16 roundings within a chunk: at most 2^-7 of scale memory R beside its own
+rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import linear as ref
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def tern():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_gemv_gemm_gb300 import build
+    build.build()
+    import bit_gemv_gemm_gb300 as t
+    return t
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def i32(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(shape, g, kind=torch.float32):
+    return torch.randn(shape, generator=g, device="cuda").to(kind)
+
+
+def within(got, want, bound, what):
+    err = np.abs(f64(got) - want)
+    bad = ~(err <= bound)
+    if bad.any():
+        i = np.argwhere(bad)[:4].tolist()
+        raise AssertionError(f"{what}: {bad.sum()} of {bad.size} off, first {i}: got {f64(got)[bad][:4]}, "
+                             f"want {want[bad][:4]}, bound {np.broadcast_to(bound, want.shape)[bad][:4]}")
+
+
+# ---------------------------------------------------------------------------
+# rms_norm
+# ---------------------------------------------------------------------------
+
+KINDS = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def check_norm(tern, x, w, out, residual=None, scale=1.0, gate=None, act="silu", offset=0.0, after=False, res_out=None,
+               residual_was=None):
+    D = x.shape[-1]
+    r = f64(residual) if residual_was is None else residual_was
+    want, h = ref.rms_norm(f64(x), f64(w), r, scale, f64(gate), act, EPS, offset, after)
+    half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -23
+    rel = (D / 8 + 40) * 2.0 ** -24 + (2.0 ** -15 if gate is not None else 0.0)
+    parts = np.abs(scale * f64(x)) + (0 if r is None else np.abs(r))
+    own = want if not after else want - (0 if r is None else r)
+    bound = half * np.abs(want) + 2 * rel * np.abs(own) + 1e-30
+    if not after:   # h's own rounding, through the same factors
+        inv = 1 / np.sqrt(np.mean(h * h, -1, keepdims=True) + EPS)
+        z = 1.0 if gate is None else np.abs(f64(gate)) + 1.0
+        bound = bound + 2.0 ** -23 * parts * inv * (np.abs(f64(w)) + abs(offset)) * z * 2
+    within(out, want, bound, "norm")
+    if res_out is not None:
+        half = 2.0 ** -8 if res_out.dtype == torch.bfloat16 else 2.0 ** -24
+        within(res_out, h, half * np.abs(h) + 2.0 ** -23 * parts, "residual")
+
+
+@pytest.mark.parametrize("T,heads,D", [(1, 1, 8), (3, 1, 64), (7, 5, 72), (33, 3, 128), (5, 7, 176), (9, 1, 256),
+                                       (4, 2, 264), (6, 1, 512), (3, 1, 520), (2, 1, 1000), (700, 1, 1032), (5, 1, 5120),
+                                       (3, 1, 8192), (2, 2, 8200), (2, 1, 17408), (1, 1, 32768), (1000, 9, 128)])
+@pytest.mark.parametrize("kinds", ["f32", "bf16"])
+def test_norm_sizes(tern, T, heads, D, kinds):
+    g, kind = gen(T + D), KINDS[kinds]
+    x, r, z = rand((T, heads, D), g, kind), 3 * rand((T, heads, D), g, kind), rand((T, heads, D), g, kind)
+    r = r.to(kind)
+    w = 1 + 0.3 * rand(D, g)
+    out = tern.rms_norm(x, w)
+    check_norm(tern, x, w, out)
+    new = torch.empty_like(r)
+    out = tern.rms_norm(x, w, residual=r, scale=0.5, gate=z, residual_out=new)
+    check_norm(tern, x, w, out, r, 0.5, z, res_out=new)
+    out = tern.rms_norm(x, w, residual=r, scale=-0.5, gate=z, gate_act="sigmoid", weight_offset=1.0, after=True)
+    assert out.dtype == kind
+    check_norm(tern, x, w, out, r, -0.5, z, "sigmoid", 1.0, True)
+
+
+def test_norm_in_place_strided_and_mixed(tern):
+    g = gen(2)
+    T, H, D = 37, 4, 128
+    wide = rand((T, 64 + H * D + 8), g)
+    x = wide[:, 64:64 + H * D].unflatten(1, (H, D))
+    z = rand((H, T, D), g, torch.bfloat16).transpose(0, 1)
+    r, w = rand((T, H, D), g, torch.bfloat16), rand(D, g)
+    was = f64(r)
+    out = tern.rms_norm(x, w, residual=r, gate=z, residual_out=r, out_dtype=torch.float32)
+    assert out.dtype == torch.float32
+    check_norm(tern, x, w, out, r, 1.0, z, res_out=r, residual_was=was)
+    # one row of a residual read by all, and the output over the input
+    row = rand((1, 5120), g).expand(9, 5120)
+    y = rand((9, 5120), g, torch.bfloat16)
+    x = y.clone()
+    tern.rms_norm(y, torch.ones(5120, device="cuda"), residual=row, out=y)
+    check_norm(tern, x, torch.ones(5120), y, row)
+    # after a block, over the residual
+    r = rand((6, 1024), g)
+    was, x = f64(r), rand((6, 1024), g, torch.bfloat16)
+    tern.rms_norm(x, torch.ones(1024, device="cuda"), residual=r, scale=0.25, after=True, out=r)
+    check_norm(tern, x, torch.ones(1024), r, None, 0.25, after=True, residual_was=was)
+
+
+def test_norm_rows_alone(tern):
+    """A row of zeros, of huge and tiny values, of NaN: none touches another."""
+    x = torch.ones((6, 256), device="cuda")
+    x[0], x[1], x[2], x[3, 5], x[4] = 0.0, 1e18, 1e-18, float("nan"), -2.0
+    w = torch.arange(256, device="cuda").float()
+    for D in (256, 2048):
+        xx, ww = x.repeat(1, D // 256), w.repeat(D // 256)
+        out = f64(tern.rms_norm(xx, ww, out_dtype=torch.float32))
+        assert (out[0] == 0).all() and np.isnan(out[3]).all() and np.isfinite(out[[1, 2, 4, 5]]).all()
+        assert np.allclose(out[1], f64(ww), rtol=1e-6) and np.allclose(out[4], -f64(ww), rtol=1e-6)
+        assert np.abs(out[2] - 1e-15 * f64(ww)).max() < 1e-18
+
+
+def test_norm_of_no_tokens(tern):
+    assert tern.rms_norm(torch.zeros((0, 64), device="cuda"), torch.ones(64, device="cuda")).shape == (0, 64)
+
+
+# ---------------------------------------------------------------------------
+# short_conv
+# ---------------------------------------------------------------------------
+
+def sequences(lens, behind=0):
+    start = np.cumsum([0] + list(lens))
+    return start.tolist(), int(start[-1]) + behind
+
+
+def check_conv(x, w, bias, silu, before, after, out, sl, start, past=None, dst=None, out_was=None):
+    want, new, size = ref.short_conv(f64(x), f64(w), before, sl, start, None if bias is None else f64(bias), silu, past,
+                                     dst)
+    rows = ~np.isnan(want).all(-1)
+    bound = 2.0 ** -8 * np.abs(want) + (1.2 * 2.0 ** -20) * size + (2.0 ** -15 * np.abs(want) if silu else 0) + 1e-30
+    within(out[torch.from_numpy(rows).cuda()], want[rows], bound[rows], "conv")
+    if out_was is not None:
+        assert np.array_equal(f64(out)[~rows], out_was[~rows])
+    assert np.array_equal(f64(after), new)
+
+
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,C", [([1], 8), ([1] * 5, 520), ([0, 2, 3, 1, 0], 64), ([31, 32, 33, 0, 65], 1032),
+                                    ([300], 512), ([7, 100, 1], 2048)])
+def test_conv(tern, W, kind, lens, C):
+    g, B = gen(W + C), len(lens)
+    start, T = sequences(lens, behind=3)
+    x = rand((T, C + 16), g, kind)[:, 8:8 + C]
+    w, bias, pool = rand((C, W), g), rand(C, g), rand((2 * B + 2, W - 1, C), g)
+    order = torch.randperm(2 * B + 2, generator=gen(1), device="cuda").tolist()
+    sl, dst = order[:B], order[B:2 * B]
+    past = [int(b % 3 != 1) for b in range(B)]
+    for kw in (dict(), dict(dst=dst), dict(dst=dst, past=past, bias=bias, silu=False)):
+        state, before = pool.clone(), f64(pool)
+        out = torch.full((T, C), 7.0, dtype=torch.bfloat16, device="cuda")
+        tern.short_conv(x, w, state, i32(sl), q_start=i32(start), max_new=max(max(lens), 1), bias=kw.get("bias"),
+                        silu=kw.get("silu", True), past=i32(kw.get("past")), dst_slots=i32(kw.get("dst")), out=out)
+        check_conv(x, w, kw.get("bias"), kw.get("silu", True), before, state, out, sl, start, kw.get("past"),
+                   kw.get("dst"), np.full((T, C), 7.0))
+    assert tern.device_error() == 0
+
+
+def test_conv_equal_lengths_negative_slots_and_a_split(tern):
+    g = gen(5)
+    x, w, pool = rand((12, 64), g), rand((64, 4), g), rand((3, 3, 64), g)
+    state = pool.clone()
+    out = tern.short_conv(x, w, state, i32([2, -1, 0]), dst_slots=i32([-1, 1, 0]))
+    check_conv(x, w, None, True, f64(pool), state, out, [2, -1, 0], [0, 4, 8, 12], dst=[-1, 1, 0])
+    # in one piece and in three
+    x, state, whole = rand((70, 64), g, torch.bfloat16), pool.clone(), pool.clone()
+    once = tern.short_conv(x, w, whole, i32([1]))
+    parts = [tern.short_conv(x[a:b], w, state, i32([1])) for a, b in ((0, 1), (1, 3), (3, 70))]
+    assert torch.equal(torch.cat(parts), once) and torch.equal(state, whole)
+    assert tern.short_conv(x[:0], w, state, i32([1])).shape == (0, 64) and torch.equal(state, whole)
+    assert tern.device_error() == 0
+
+
+def test_conv_reports_bad_values(tern):
+    g = gen(6)
+    x, w, pool = rand((4, 64), g), rand((64, 4), g), rand((3, 3, 64), g)
+    for sl, dst, start, code in (([0, 3], [1, 2], [0, 2, 4], tern.DEVERR_STATE_SLOT),
+                                 ([0, 1], [2, 1 << 30], [0, 2, 4], tern.DEVERR_STATE_SLOT),
+                                 ([0, 1], [1, 2], [0, 2, 5], tern.DEVERR_CACHE_SEQUENCE),
+                                 ([0, 1], [1, 2], [0, 3, 4], tern.DEVERR_CACHE_SEQUENCE),
+                                 ([0, 1], [1, 2], [0, 2, -7], tern.DEVERR_CACHE_SEQUENCE)):
+        state = pool.clone()
+        tern.short_conv(x, w, state, i32(sl), q_start=i32(start), max_new=2, dst_slots=i32(dst))
+        assert tern.device_error() == code
+        if code == tern.DEVERR_STATE_SLOT:   # nothing is written in the place of a bad slot
+            bad = [s for s in range(3) if s not in dst]
+            assert torch.equal(state[bad], pool[bad])
+    assert tern.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# gated_delta
+# ---------------------------------------------------------------------------
+
+HEADS = [(2, 4, 64, 16), (1, 3, 128, 48), (2, 2, 128, 128), (1, 2, 64, 256), (1, 1, 128, 176)]
+
+
+def delta_inputs(T, Hk, Hv, Dk, Dv, g, raw=False, norm=True):
+    x = rand((T, 2 * Hk * Dk + Hv * Dv + 8), g)
+    x = x * torch.sigmoid(x)
+    if not norm:
+        qk = x[:, :2 * Hk * Dk].view(T, 2 * Hk, Dk)
+        qk *= 0.99 / (qk.norm(dim=-1, keepdim=True) + 1e-3)
+    x = x.bfloat16()
+    q, k = x[:, :Hk * Dk].view(T, Hk, Dk), x[:, Hk * Dk:2 * Hk * Dk].view(T, Hk, Dk)
+    v = x[:, 2 * Hk * Dk:2 * Hk * Dk + Hv * Dv].view(T, Hv, Dv)
+    gates = rand((T, 2 * Hv + 3), g)
+    a, b = gates[:, :Hv], gates[:, Hv + 2:2 * Hv + 2]
+    if raw:
+        return q, k, v, a, b, torch.log(1 + 3 * torch.rand(Hv, generator=g, device="cuda")), rand(Hv, g) - 2
+    a.copy_(-0.3 * torch.exp(a))
+    b.copy_(torch.sigmoid(b))
+    return q, k, v, a, b, None, None
+
+
+def check_delta(inputs, scale, norm, before, after, out, sl, start, past=None, dst=None, out_was=None):
+    q, k, v, g, b, al, dt = (f64(t) for t in inputs)
+    want, new, reach, memory = ref.gated_delta(q, k, v, g, b, before, sl, start, scale, norm, al, dt, past, dst)
+    rows = ~np.isnan(want).all((1, 2)) if len(want) else np.zeros(0, bool)
+    step = 2.0 ** -17 * memory * reach
+    longest = max(b - a for a, b in zip(start, start[1:]))
+    inside = 2.0 ** -7 * memory * reach if longest > 1 else 0 * reach
+    length = 1.0 if norm else max(1.0, np.sqrt((q * q).sum(-1)).max())
+    bound = 2.0 ** -8 * np.abs(want) + (abs(scale) * length * (step + 2.0 ** -17 * reach + inside))[None, :, None]
+    within(out[torch.from_numpy(rows).cuda()], want[rows], bound[rows], "delta")
+    if out_was is not None:
+        assert np.array_equal(f64(out)[~rows], out_was[~rows])
+    moved = (new != before).any((1, 2, 3))
+    assert np.array_equal(f64(after)[~moved], before[~moved])
+    within(after[torch.from_numpy(moved).cuda()], new[moved], step[None, :, None, None] + 2.0 ** -23 * np.abs(new[moved]),
+           "state")
+    # as a whole far nearer than the worst case: roundings to 32 bits alone (2e-7 each, a few of them)
+    err = f64(after) - new
+    assert np.linalg.norm(err[moved]) <= 4e-6 * np.linalg.norm(new[moved]) + 1e-30
+    if rows.any() and longest > 1:
+        assert np.linalg.norm((f64(out) - want)[rows]) <= 2.0 ** -8 * np.linalg.norm(want[rows])
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1], [0, 3, 1], [5, 8, 0, 9], [16, 2], [17], [33, 64, 1, 0, 31], [200, 47],
+                                  [500]])
+@pytest.mark.parametrize("raw", [False, True])
+def test_delta(tern, heads, lens, raw):
+    Hk, Hv, Dk, Dv = heads
+    g, B = gen(sum(lens) + Dv), len(lens)
+    start, T = sequences(lens, behind=2)
+    inputs = delta_inputs(T, *heads, g, raw, norm=raw)
+    pool = rand((2 * B + 2, Hv, Dv, Dk), g)
+    order = torch.randperm(2 * B + 2, generator=gen(7), device="cuda").tolist()
+    sl, dst = order[:B], order[B:2 * B]
+    past = [int(b % 3 != 2) for b in range(B)]
+    scale = Dk ** -0.5
+    for kw in (dict(), dict(dst=dst, past=past)):
+        state, before = pool.clone(), f64(pool)
+        out = torch.full((T, Hv, Dv), 7.0, dtype=torch.bfloat16, device="cuda")
+        tern.gated_delta(*inputs[:5], state, i32(sl), q_start=i32(start), max_new=max(max(lens), 1), qk_norm=raw,
+                         a_log=inputs[5], dt_bias=inputs[6], past=i32(kw.get("past")), dst_slots=i32(kw.get("dst")),
+                         out=out)
+        assert tern.device_error() == 0
+        check_delta(inputs, scale, raw, before, state, out, sl, start, kw.get("past"), kw.get("dst"),
+                    np.full(out.shape, 7.0))
+
+
+@pytest.mark.parametrize("n", [1, 6, 70])
+def test_delta_extreme_gates(tern, n):
+    """Decays of 0 (-inf, far below fp32's least), of 1, steps of 0 and 1, in one sequence."""
+    Hk, Hv, Dk, Dv = 1, 2, 128, 32
+    g = gen(n)
+    inputs = list(delta_inputs(2 * n, Hk, Hv, Dk, Dv, g))
+    inputs[3][:, 0] = torch.tensor([0.0, -float("inf"), -1e30, -150.0, -1e-7, 0.0, 0.0])[torch.arange(2 * n) % 7].cuda()
+    inputs[3][:, 1] = torch.where(torch.arange(2 * n) % 5 == 3, -90.0, -1e-3).cuda()
+    inputs[4][:, 0] = torch.tensor([0.0, 1.0, 1.0, 0.5])[torch.arange(2 * n) % 4].cuda()
+    pool = rand((2, Hv, Dv, Dk), g)
+    state = pool.clone()
+    out = tern.gated_delta(*inputs[:5], state, i32([1, 0]), qk_norm=True)
+    assert tern.device_error() == 0
+    check_delta(inputs, Dk ** -0.5, True, f64(pool), state, out, [1, 0], [0, n, 2 * n])
+
+
+def test_delta_negative_slots_shared_reads_and_no_tokens(tern):
+    Hk, Hv, Dk, Dv = 1, 2, 64, 32
+    g = gen(11)
+    for n in (1, 20):
+        inputs = delta_inputs(3 * n, Hk, Hv, Dk, Dv, g)
+        pool = rand((5, Hv, Dv, Dk), g)
+        state = pool.clone()
+        out = tern.gated_delta(*inputs[:5], state, i32([1, 1, -1]), dst_slots=i32([2, -1, 4]), qk_norm=True, scale=-2.0)
+        check_delta(inputs, -2.0, True, f64(pool), state, out, [1, 1, -1], [0, n, 2 * n, 3 * n], dst=[2, -1, 4])
+    # no tokens at all: states move
+    state = pool.clone()
+    e = [t[:0] for t in inputs[:5]]
+    assert tern.gated_delta(*e, state, i32([1, 0]), dst_slots=i32([3, 2]), past=i32([1, 0])).shape == (0, Hv, Dv)
+    assert torch.equal(state[3], pool[1]) and not state[2].any() and torch.equal(state[[0, 1, 4]], pool[[0, 1, 4]])
+    assert tern.device_error() == 0
+
+
+def test_delta_in_one_piece_and_in_several(tern):
+    """A prompt at once, in unlike parts, and token by token: the same states, within their bounds."""
+    heads = (2, 4, 128, 64)
+    g = gen(12)
+    inputs = delta_inputs(150, *heads, g)
+    pool = rand((1, 4, 64, 128), g)
+    for cuts in ([0, 150], [0, 64, 65, 100, 150], list(range(0, 151, 3))):
+        state, outs = pool.clone(), []
+        for a, b in zip(cuts, cuts[1:]):
+            outs.append(tern.gated_delta(*[t[a:b] for t in inputs[:5]], state, i32([0]), qk_norm=True))
+        check_delta(inputs, 128 ** -0.5, True, f64(pool), state, torch.cat(outs), [0], [0, 150])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_delta_reports_bad_values(tern, n):
+    Hk, Hv, Dk, Dv = 1, 2, 64, 32
+    g = gen(13)
+    inputs = delta_inputs(2 * n, Hk, Hv, Dk, Dv, g)
+    pool = rand((3, Hv, Dv, Dk), g)
+    for sl, dst, start, code in (([0, 3], [1, 2], [0, n, 2 * n], tern.DEVERR_STATE_SLOT),
+                                 ([0, 1], [2, 1 << 30], [0, n, 2 * n], tern.DEVERR_STATE_SLOT),
+                                 ([0, 1], [1, 2], [0, n, 2 * n + 1], tern.DEVERR_CACHE_SEQUENCE),
+                                 ([0, 1], [1, 2], [-1, n, 2 * n], tern.DEVERR_CACHE_SEQUENCE),
+                                 ([0, 1], [1, 2], [0, n, -9], tern.DEVERR_CACHE_SEQUENCE)):
+        state = pool.clone()
+        tern.gated_delta(*inputs[:5], state, i32(sl), q_start=i32(start), max_new=n, dst_slots=i32(dst), qk_norm=True)
+        assert tern.device_error() == code
+        if code == tern.DEVERR_STATE_SLOT:
+            bad = [s for s in range(3) if s not in dst]
+            assert torch.equal(state[bad], pool[bad])
+    assert tern.device_error() == 0
+
+
+def test_states_past_2_to_the_31(tern):
+    """Slots whose offsets do not fit 32 bits."""
+    Hk, Hv, Dk, Dv = 2, 32, 128, 128
+    slots = [4200, 4150]
+    state = torch.empty((4201, Hv, Dv, Dk), device="cuda")
+    g = gen(14)
+    for n in (1, 20):
+        inputs = delta_inputs(n, Hk, Hv, Dk, Dv, g)
+        state[slots] = 0.1 * rand((2, Hv, Dv, Dk), g)
+        before = f64(state[slots])
+        out = tern.gated_delta(*inputs[:5], state, i32(slots[:1]), dst_slots=i32(slots[1:]), qk_norm=True)
+        check_delta(inputs, Dk ** -0.5, True, before, state[slots], out, [0], [0, n], dst=[1])
+    assert tern.device_error() == 0
+
+
+def test_one_head_alone(tern):
+    """NaN in one sequence's values, state and gates: the other sequences and heads stay as they were."""
+    heads = (1, 2, 64, 32)
+    for n in (1, 45):
+        g = gen(15)
+        inputs = [t if t is None else t.clone() for t in delta_inputs(3 * n, *heads, g)]
+        pool = rand((3, 2, 32, 64), g)
+        clean, state = pool.clone(), pool.clone()
+        want = tern.gated_delta(*inputs[:5], clean, i32([0, 1, 2]), qk_norm=True)
+        inputs[2][n:2 * n, 1, 5] = float("nan")
+        inputs[4][n, 1] = float("inf")
+        state[1, 1, 3] = float("nan")
+        got = tern.gated_delta(*inputs[:5], state, i32([0, 1, 2]), qk_norm=True)
+        keep = [i for i in range(3 * n) if not n <= i < 2 * n]
+        assert torch.equal(got[keep], want[keep]) and torch.equal(got[:, 0], want[:, 0])
+        assert torch.equal(state[[0, 2]], clean[[0, 2]]) and torch.equal(state[:, 0], clean[:, 0])
+        assert torch.isnan(got[2 * n - 1, 1]).any()
+
+
+def test_another_stream_and_replays(tern):
+    """The three calls captured once and replayed on new inputs, on a stream of their own."""
+    g = gen(16)
+    B, Hk, Hv, D = 3, 1, 2, 64
+    C = (2 * Hk + Hv) * D
+    side = torch.cuda.Stream()
+    for n in (1, 21):
+        T = B * n
+        x, w = rand((T, C), g, torch.bfloat16), rand((C, 4), g)
+        gates, nw = rand((T, 2, Hv), g), 1 + 0.1 * rand(D, g)
+        conv, delta, slots = rand((B, 3, C), g), rand((B, Hv, D, D), g), i32([2, 0, 1])
+        al, dt = torch.zeros(Hv, device="cuda"), torch.zeros(Hv, device="cuda") - 2
+
+        def layer(stream=None):
+            y = tern.short_conv(x, w, conv, slots, stream=stream)
+            q, k, v = y[:, :D].view(T, 1, D), y[:, D:2 * D].view(T, 1, D), y[:, 2 * D:].view(T, Hv, D)
+            o = tern.gated_delta(q, k, v, gates[:, 0], gates[:, 1], delta, slots, qk_norm=True, a_log=al, dt_bias=dt,
+                                 stream=stream)
+            return tern.rms_norm(o, nw, gate=x.view(T, -1, D)[:, :Hv], stream=stream)
+
+        keep = [t.clone() for t in (conv, delta)]
+        first = layer().clone()
+        second_x = rand((T, C), g, torch.bfloat16)
+        then = [t.clone() for t in (conv, delta)]
+        old_x = x.clone()
+        x.copy_(second_x)
+        second = layer().clone()
+        last = [t.clone() for t in (conv, delta)]
+
+        def reset(a, b):
+            for t, s in zip((conv, delta), a):
+                t.copy_(s)
+            x.copy_(b)
+
+        reset(keep, old_x)
+        torch.cuda.synchronize()
+        got = layer(side)
+        side.synchronize()
+        assert torch.equal(got, first)
+        reset(keep, old_x)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = layer()
+        graph.replay()
+        assert torch.equal(out, first) and torch.equal(conv, then[0]) and torch.equal(delta, then[1])
+        x.copy_(second_x)
+        graph.replay()
+        assert torch.equal(out, second) and torch.equal(conv, last[0]) and torch.equal(delta, last[1])
+    assert tern.device_error() == 0
