@@ -455,7 +455,7 @@ def device_error() -> int:
 SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER = 0, 1
 DEVERR_GEMM_MMA_WAIT, DEVERR_GEMV_RANGE_FLAG_WAIT, DEVERR_GEMV_ACTIVATION_RANGE = 0x103, 0x202, 0x203
 DEVERR_CACHE_PAGE, DEVERR_CACHE_SEQUENCE, DEVERR_CACHE_SLOT = 0x301, 0x302, 0x303
-DEVERR_ATTN_WAIT, DEVERR_STATE_SLOT = 0x311, 0x321
+DEVERR_ATTN_WAIT, DEVERR_STATE_SLOT, DEVERR_DELTA_WAIT = 0x311, 0x321, 0x322
 
 
 def wait_selftest(which: int, limit_us: int, stream=None) -> None:

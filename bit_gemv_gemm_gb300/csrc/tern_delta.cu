@@ -14,6 +14,7 @@ namespace {
 __device__ int g_delta_error;
 
 constexpr int kStepThreads = 128, kStepBatch = 8;
+constexpr int kStepTokens = 16;   // the most of a sequence that go token by token
 
 // 8 lanes share a row: lane l has the values 32 i + 4 l + {0..3}, so that a row's
 // loads are 128 bytes in a piece.  A warp holds 4 x ROWS rows.
@@ -208,7 +209,8 @@ extern "C" tern_status tern_gated_delta(const void* q, const void* k, const void
     a.group = v_heads / k_heads;
     a.norm = qk_norm;
     a.scale = scale;
-    const cudaError_t e = launch_delta_step(a, (cudaStream_t)stream);
+    const cudaError_t e = a.s.max_new > kStepTokens ? launch_delta_chunk(a, (cudaStream_t)stream)
+                                                    : launch_delta_step(a, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

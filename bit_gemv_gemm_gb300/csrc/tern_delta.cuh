@@ -34,5 +34,6 @@ __device__ __forceinline__ float2 delta_gates(const DeltaArgs& a, long long toke
 }
 
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
+cudaError_t launch_delta_chunk(const DeltaArgs& a, cudaStream_t stream);
 
 }  // namespace tern

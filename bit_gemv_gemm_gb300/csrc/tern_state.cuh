@@ -5,6 +5,7 @@
 #pragma once
 
 #include "tern_cache.cuh"
+#include "tern_mma.cuh"
 
 namespace tern {
 
@@ -87,10 +88,6 @@ __device__ __forceinline__ void widen8(const Raw8& r, int is_f32, float (&x)[8])
             x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
         }
     }
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ void store_raw8(void* base, long long at, int is_f32, const float (&x)[8]) {
     if (is_f32) {
