@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
                 qs[i][MY * lane + e] = q[e] * iq;
             }
             if (lane == 0) {
-                const float2 gb = delta_gates(a, t, h);
+                const float2 gb = delta_gates(delta_head(a, h), delta_raw_gates(a, t, h));
                 gates[i] = make_float4(expf(gb.x), gb.y, kq * ik * iq, 0.0f);
             }
         }

@@ -20,14 +20,25 @@ struct DeltaArgs {
 
 constexpr float kDeltaNormEps = 1e-6f;
 
-// The gates of one token and value head: the log of the decay, and the step.  A
-// log below -200 (a decay of 0 in 32 bits all the same) becomes -200, so that
-// differences of sums of it stay numbers.
-__device__ __forceinline__ float2 delta_gates(const DeltaArgs& a, long long token, int h) {
-    float g = a.g[token * a.g_token + h], b = a.beta[token * a.beta_token + h];
-    if (a.a_log) {
-        const float x = g + a.dt_bias[h];
-        g = -expf(a.a_log[h]) * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
+// The gates of one token and value head as they lie in memory...
+__device__ __forceinline__ float2 delta_raw_gates(const DeltaArgs& a, long long token, int h) {
+    return make_float2(a.g[token * a.g_token + h], a.beta[token * a.beta_token + h]);
+}
+// ... and the log of the decay and the step that they stand for.  A log below -200 (a
+// decay of 0 in 32 bits all the same) becomes -200, so that differences of sums of it
+// stay numbers.
+struct DeltaHead {
+    bool raw;
+    float rate, bias;
+};
+__device__ __forceinline__ DeltaHead delta_head(const DeltaArgs& a, int h) {
+    return a.a_log ? DeltaHead{true, expf(a.a_log[h]), a.dt_bias[h]} : DeltaHead{false, 0.0f, 0.0f};
+}
+__device__ __forceinline__ float2 delta_gates(const DeltaHead& head, float2 raw) {
+    float g = raw.x, b = raw.y;
+    if (head.raw) {
+        const float x = g + head.bias;
+        g = -head.rate * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
         b = 1.0f / (1.0f + expf(-b));
     }
     return make_float2(g < -200.0f ? -200.0f : g, b);

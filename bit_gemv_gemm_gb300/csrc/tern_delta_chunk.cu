@@ -2,31 +2,31 @@
 // on the tcgen05 tensor cores.
 //
 // With G the running sum of the decays' logs in a chunk and S the state before it,
-//   A_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i),   T = (I + A)^-1 diag(beta),
-//   U = T (V - e^G K S^T),
+//   A_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i),   T = (I + A)^-1,
+//   X = beta (V - e^G K S^T),   U = T X,
 //   O = scale e^G Q S^T + P U,   P_ij = scale e^(G_i - G_j) q_i.k_j (j <= i),
 //   S <- e^(G_last) S + sum_j e^(G_last - G_j) u_j k_j^T.
 // A CTA takes 128 rows of one head's S through its sequence.  Everything with rows
-// of S (S itself, X = V - e^G K S^T, U, O) is kept transposed, a thread a row, so
-// those products have M = 128 and their left operand in tensor memory, and what
-// passes from one product to the next never leaves its row.
+// of S (S itself, X, U, O) is kept transposed, a tensor memory lane a row, so those
+// products have M = 128 and their left operand in tensor memory, and what passes
+// from one product to the next never leaves its lane.
 //
-// The chain from chunk to chunk, four phases of eight warps (two threads a row)
-// between three products:
-//   S = e^G_last S + D, its parts to tensor memory  ->  K S^T
-//   X = V - e^G K S^T                               ->  U = T X
+// What bounds a sequence is the chain from chunk to chunk, three phases of eight
+// warps (two threads a row) between three products:
+//   S = e^G_last S + D, its parts to tensor memory  ->  [K; Q] S^T
+//   X                                               ->  U = T X
 //   e^(G_last - G) U                                ->  D = U^T K
-// and beside it, in the gaps of the tensor pipe: Q S^T and P U, the output, and the
-// Gram matrices [K; Q] K^T of the chunk after the next, from which four warps make T
-// (forward substitution, a thread a column) and P, two warps the decays and the
-// lengths of q and k from the tiles themselves.
+// and beside it: P U; four warps for the output; the Gram matrices [K; Q] K^T of the
+// chunk after the next, from which four warps make P and T (16 x 16 blocks by
+// substitution, a column a lane, joined by mma.sync); two for decays and lengths.
 //
 // Rounding.  q, k, v are exact as bf16.  S, X, U and T are fp32 cut into two bf16
-// values, which carry 2^-17 of each (one would lose 2^-8 of the state a chunk);
-// lengths and decays are applied in fp32, to rows and columns of results.  P is one
-// bf16: it only reaches the output, which is rounded to that.
-// Exponents are differences of G, at most 0, and G is a sum in 64 bits kept as two
-// fp32: a long or strong decay before a pair of tokens does not blur theirs.
+// values, which carry 2^-17 of each (one would lose 2^-8 of the state a chunk); what
+// that leaves of X is added to U in fp32, T's diagonal being 1.  Lengths and decays
+// are applied in fp32, to rows and columns of results.  P is one bf16: it only
+// reaches the output, which is rounded to that.  Exponents are differences of G, at
+// most 0, and G is a sum in 64 bits kept as two fp32: a long or strong decay before
+// a pair of tokens does not blur theirs.
 #include "tern_delta.cuh"
 #include "tern_sm100.cuh"
 
@@ -37,63 +37,103 @@ using namespace sm100;
 
 __device__ int g_delta_chunk_error;
 
-constexpr int kDiagRow = 20;                          // floats of a row of a 16 x 16 block of A
 constexpr int kTok = 64, kRows = 128;                 // tokens of a chunk, rows of S
-constexpr int kKqStages = 3, kVStages = 3, kCoefStages = 4, kTpStages = 2;
-constexpr uint64_t kDeltaWaitNs = 1000000000ull;      // 1 s: far beyond any real wait
+constexpr int kKqStages = 3, kVStages = 2, kCoefStages = 4, kTpStages = 2, kAStages = 2;
+constexpr uint32_t kTile = kTok * 128;                // bytes of a [64][64] bf16 tile, 128-byte swizzled rows
+constexpr uint32_t kATile = kTok * 64;                // of a part of A below its diagonal blocks: a_at()
+constexpr int kDiagRow = 20, kDiagBlock = 16 * kDiagRow + 16;   // floats of a column and of a block of -A's diagonal blocks
+constexpr uint32_t kDeltaTries = 1u << 19, kDeltaNap = 2000;   // of a wait, and ns of each: a second, far beyond any real one
 
 // What one chunk's tokens are scaled by.
 struct alignas(16) Coef {
-    float beta[kTok], minus_near[kTok];   // beta; -beta e^G |k|^-1
-    float left[kTok];                     // e^(G_last - G) |k|^-1
-    float near_q[kTok];                   // scale e^G |q|^-1
-    float beta_k[kTok], scale_q[kTok], k[kTok];   // beta |k|^-1; scale |q|^-1; |k|^-1
-    float to_end[kTok];                   // |k|^-1 e^(G at its 16's last token - G)
-    float2 G[kTok];                       // G in powers of two, two parts
-    float2 end[4];                        // that of each 16's last token
-    float last, unused[3];                // e^G_last
+    float beta[kTok], near[kTok];   // beta; e^G
+    float minus_near[kTok];         // -beta e^G |k|^-1
+    float left[kTok];               // e^(G_last - G) |k|^-1
+    float near_q[kTok];             // scale e^G |q|^-1
+    float scale_q[kTok];            // scale |q|^-1
+    float to_end[kTok];             // |k|^-1 e^(G at its 16's last token - G)
+    float2 G[kTok];                 // G in powers of two, two parts
+    float2 Gk[kTok];                // G - log |k|^-1
+    float2 end[4];                  // that of each 16's last token
+    float last, unused[3];          // e^G_last
 };
 
 template <int DK>
 struct Cfg {
     static constexpr int NC = DK / 64;                          // chunks of 64 values of a K or Q row
-    static constexpr int HALF = DK / 2;                         // columns of S that a thread holds
-    static constexpr int kKqBytes = NC * 2 * kTok * 128;        // K over Q, 128-byte swizzled rows
-    static constexpr int kVBytes = 2 * kTok * 128;
-    static constexpr int kTpBytes = 3 * kTok * 128;             // T's two parts, P
+    static constexpr int COLS = DK / 2;                         // columns of S that a thread holds
+    static constexpr int kKqBytes = NC * 2 * (int)kTile;        // 64 values of K's and Q's rows, the next 64
+    static constexpr int kVBytes = 4 * kTok * 64;               // 32 rows of S a tile: [token][32]
+    static constexpr int kTpBytes = 3 * (int)kTile;             // T's two parts, P
+    static constexpr int kABytes = 2 * (int)kATile + 4 * kDiagBlock * 4;   // A's two parts, its diagonal blocks
     static constexpr size_t kKq = 0, kV = kKq + (size_t)kKqStages * kKqBytes, kTp = kV + (size_t)kVStages * kVBytes,
-                            kA = kTp + (size_t)kTpStages * kTpBytes, kDiag = kA + 2 * kTok * 128,
-                            kCoef = kDiag + kTok * kDiagRow * 4,
-                            kBar = kCoef + kCoefStages * sizeof(Coef), kMisc = kBar + 48 * 8, kSmem = kMisc + 64 + 1024;
+                            kA = kTp + (size_t)kTpStages * kTpBytes, kCoef = kA + (size_t)kAStages * kABytes, kBar = kCoef + kCoefStages * sizeof(Coef),
+                            kMisc = kBar + 48 * 8, kSmem = kMisc + 64 + 1024;
 };
-constexpr int kThreads = 512;
-
-// tensor memory columns: D over the parts of S; K S^T, then U; Q S^T; parts of X, then
-// of U; parts of the scaled U; P U; Gram matrices
-enum { T_S = 0, T_KS = 128, T_QS = 192, T_X = 256, T_UP = 320, T_O = 384, T_GRAM = 448 };
+// warps: the chain, the output, A and P, T, then one each for products and copies and two for decays
+constexpr int kOutWarp = 8, kGramWarp = 12, kInvWarp = 16, kMmaWarp = 20, kTmaWarp = 21, kCoefWarp = 22, kThreads = 24 * 32;
+// registers a thread: 256 x 144 + 128 x (48 + 56 + 48 + 40) = 768 x 80, what the CTA is launched with
+// tensor memory columns: D over the parts of S, then those of X; Q S^T of odd chunks; K S^T, then U,
+// then U's parts; Q S^T of even chunks; parts of the scaled U; P U; Gram matrices
+enum { T_S = 0, T_X = T_S, T_QS_ODD = 128, T_KS = 192, T_QS_EVEN = 256, T_UP = 320, T_O = 384, T_GRAM = 448 };
+// An odd chunk's rows of Q stand before those of K, an even one's behind: [K; Q] S^T is
+// one product either way, and its Q half does not wait for the last chunk's output.
+__host__ __device__ constexpr int k_row(int chunk) { return (chunk & 1) * kTok; }
+__host__ __device__ constexpr int q_row(int chunk) { return kTok - k_row(chunk); }
 
 enum {
     KQ_FULL = 0, KQ_EMPTY = KQ_FULL + kKqStages, V_FULL = KQ_EMPTY + kKqStages, V_EMPTY = V_FULL + kVStages,
     COEF_FULL = V_EMPTY + kVStages, COEF_EMPTY = COEF_FULL + kCoefStages, TP_FULL = COEF_EMPTY + kCoefStages,
-    TP_EMPTY = TP_FULL + kTpStages, GRAM_FULL = TP_EMPTY + kTpStages, GRAM_EMPTY, S_FULL, KS_FULL, X_FULL, U_FULL,
-    UP_FULL, U2_FULL, D_FULL, O_FULL, O_EMPTY, PREP, TAIL, DRAIN, BARS
+    TP_EMPTY = TP_FULL + kTpStages, GRAM_FULL = TP_EMPTY + kTpStages, GRAM_EMPTY, KS_FULL, U_FULL, D_FULL, O_FULL, O_EMPTY, A_FULL, A_EMPTY = A_FULL + kAStages, LENGTHS = A_EMPTY + kAStages,
+    INVERSE, TAIL, DRAIN, BARS
 };
 static_assert(BARS <= 48, "barriers");
+// From the chain's 8 warps to the one that issues products: the SM's own barriers, whose
+// last arrival wakes it sooner than an mbarrier's.  Nothing bounds a wait at one, so both
+// sides go through all their turns whatever has failed: a failed wait only ends the others.
+enum { S_READY = 1, X_READY, UP_READY, U2_READY };
+constexpr int kChainThreads = 256 + 32;
+__device__ __forceinline__ void chain_arrive(int b) { asm volatile("bar.arrive %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
+__device__ __forceinline__ void chain_wait(int b) { asm volatile("bar.sync %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
 
 __device__ __forceinline__ int bar_count(int i) {
-    if (i >= V_EMPTY && i < V_EMPTY + kVStages) return 8;
+    if (i >= V_EMPTY && i < V_EMPTY + kVStages) return 4;
     if (i >= COEF_FULL && i < COEF_EMPTY) return 2;
-    if (i >= COEF_EMPTY && i < TP_FULL) return 8;
-    if ((i >= TP_FULL && i < TP_EMPTY) || i == GRAM_EMPTY || i == PREP) return 4;
-    if (i == S_FULL || i == X_FULL || i == UP_FULL || i == U2_FULL || i == O_EMPTY) return 8;
+    if (i >= COEF_EMPTY && i < TP_FULL) return 12;
+    if ((i >= TP_FULL && i < TP_EMPTY) || i == GRAM_EMPTY || i == O_EMPTY || (i >= A_FULL && i <= INVERSE)) return 4;
     return 1;
 }
 
+// A warp's wait, which gives up after a number of tries.  (Short: some forty of them
+// stand in loops whose code has to stay in the instruction cache.  Every lane asks; one
+// for all made the others wait longer.)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    uint32_t ok = 0;
+#pragma unroll 1
+    for (uint32_t n = kDeltaTries; !ok && n > 0; --n)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kDeltaNap)
+            : "memory");
+    return __all_sync(0xffffffffu, ok);
+}
+// One lane of a warp whose lanes all come here: what it alone then does is known to be
+// done by one, and its operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e != 0;
+}
+// a - a bf16 pair
+__device__ __forceinline__ uint64_t less_bf16(uint64_t a, uint32_t b) {
+    return fma2(pack2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), pack2(-1.0f, -1.0f), a);
+}
 // Two neighbours as a bf16 pair and what it leaves of them as another.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16(a, b);
     float x, y;
-    unpack2(add2(pack2(a, b), pack2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u))), x, y);
+    unpack2(less_bf16(pack2(a, b), hi), x, y);
     lo = pack_bf16(x, y);
 }
 
@@ -124,30 +164,38 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Column `col` of the inverse of a 16 x 16 unit lower triangle, whose strict part is at A.
+// Column `col` of the inverse of a 16 x 16 unit lower triangle, whose negated strict
+// part lies at A by columns: each value found is at once taken to all below it.
 __device__ __forceinline__ void solve16(const float* A, int col, float (&t)[16]) {
     uint64_t pair[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        uint64_t s0 = 0, s1 = 0;
+    for (int i = 0; i < 8; ++i) pair[i] = pack2(2 * i == col ? 1.0f : 0.0f, 2 * i + 1 == col ? 1.0f : 0.0f);
 #pragma unroll
-        for (int k = 0; k < i; k += 4) {
-            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(A + i * kDiagRow + k);
-            s0 = fma2(a.x, pair[k / 2], s0);
-            if (k + 2 < i) s1 = fma2(a.y, pair[k / 2 + 1], s1);
-        }
+    for (int i = 0; i < 15; ++i) {
         float x, y;
-        unpack2(add2(s0, s1), x, y);
-        t[i] = (i == col ? 1.0f : 0.0f) - (x + y);
-        pair[i / 2] = (i & 1) ? pack2(t[i - 1], t[i]) : pack2(t[i], 0.0f);
+        unpack2(pair[i / 2], x, y);
+        const uint64_t f = (i & 1) ? pack2(y, y) : pack2(x, x);
+#pragma unroll
+        for (int r = i / 4; r < 4; ++r) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(A + i * kDiagRow + 4 * r);
+            if (4 * r + 1 > i) pair[2 * r] = fma2(f, a.x, pair[2 * r]);
+            pair[2 * r + 1] = fma2(f, a.y, pair[2 * r + 1]);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack2(pair[i], t[2 * i], t[2 * i + 1]);
+}
+// Where 8 columns of a row of A below its diagonal blocks stand: 32 columns a row; those of
+// the second half's own block in the rows of the first 16, which have none.
+__device__ __forceinline__ uint32_t a_at(uint32_t tile, int row, int unit) {
+    return tile + (uint32_t)(row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
 }
 // Rows R.., columns C.. of T below its diagonal blocks, 8 columns `n8` of it a warp:
 //   -T22 (A21 T11),  T11 and T22 the 16 B rows from C and R on, every product of two
 // parts each without the smallest (lo lo).
 template <int B>
 __device__ __forceinline__ void join_blocks(uint32_t A, uint32_t T, int R, int C, int n8, int lane) {
-    constexpr uint32_t kPart = kTok * 128;
+    const int a_row = C == 0 ? R : 0;
     float m[B][4];
 #pragma unroll
     for (int i = 0; i < B; ++i) m[i][0] = m[i][1] = m[i][2] = m[i][3] = 0.0f;
@@ -156,13 +204,13 @@ __device__ __forceinline__ void join_blocks(uint32_t A, uint32_t T, int R, int C
         uint32_t bh[2], bl[2];
         const uint32_t at = tile_at(T, C + 16 * kb + (lane & 15), C / 8 + n8);
         ldsm2_t(bh[0], bh[1], at);
-        ldsm2_t(bl[0], bl[1], at + kPart);
+        ldsm2_t(bl[0], bl[1], at + kTile);
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             uint32_t ah[4], al[4];
-            const uint32_t from = tile_at(A, R + 16 * i + (lane & 15), C / 8 + 2 * kb + (lane >> 4));
+            const uint32_t from = a_at(A, a_row + 16 * i + (lane & 15), 2 * kb + (lane >> 4));
             ldsm4(ah, from);
-            ldsm4(al, from + kPart);
+            ldsm4(al, from + kATile);
             mma_bf16(m[i], ah, bh[0], bh[1]);
             mma_bf16(m[i], ah, bl[0], bl[1]);
             mma_bf16(m[i], al, bh[0], bh[1]);
@@ -186,7 +234,7 @@ __device__ __forceinline__ void join_blocks(uint32_t A, uint32_t T, int R, int C
             uint32_t ah[4], al[4];
             const uint32_t from = tile_at(T, R + 16 * i + (lane & 15), R / 8 + 2 * kb + (lane >> 4));
             ldsm4(ah, from);
-            ldsm4(al, from + kPart);
+            ldsm4(al, from + kTile);
             mma_bf16(t, ah, mh[kb][0], mh[kb][1]);
             mma_bf16(t, ah, ml[kb][0], ml[kb][1]);
             mma_bf16(t, al, mh[kb][0], mh[kb][1]);
@@ -197,7 +245,7 @@ __device__ __forceinline__ void join_blocks(uint32_t A, uint32_t T, int R, int C
             split2(t[2 * x], t[2 * x + 1], hi, lo);
             const uint32_t to = tile_at(T, R + 16 * i + 8 * x + lane / 4, C / 8 + n8) + 4u * (lane & 3);
             sts32(to, hi);
-            sts32(to + kPart, lo);
+            sts32(to + kTile, lo);
         }
     }
 }
@@ -225,20 +273,18 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_out,
                    const DeltaArgs a) {
     using C = Cfg<DK>;
-    constexpr int NC = C::NC, HALF = C::HALF;
+    constexpr int NC = C::NC, COLS = C::COLS;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + (uint32_t)C::kBar + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     Coef* const coefs = reinterpret_cast<Coef*>(smem + C::kCoef);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < BARS; ++i) mbar_init(bar(i), (uint32_t)bar_count(i));
-        *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmap_q);
         tma_prefetch_desc(&tmap_k);
@@ -249,46 +295,43 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     for (int i = threadIdx.x; i < kTpStages * C::kTpBytes / 16; i += kThreads)
         reinterpret_cast<uint4*>(smem + C::kTp)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;   // (all of it is this CTA's: it begins at 0)
     pdl_launch_dependents();
     pdl_wait();
 
     const int h = blockIdx.x % a.v_heads, row0 = blockIdx.x / a.v_heads * kRows, hk = h / a.group;
     const StateSeq s = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
     const int chunks = (s.n + kTok - 1) / kTok;
-    auto fail = [&] {
-        if (!*abort_flag) {
-            *abort_flag = 1;
-            report_device_error(&g_delta_chunk_error, TERN_DEVERR_DELTA_WAIT);
-        }
-    };
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait_bounded(bar(b), parity, abort_flag, kDeltaWaitNs); };
-    auto wait_warp = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+    auto fail = [&] { report_device_error(&g_delta_chunk_error, TERN_DEVERR_DELTA_WAIT); };
+    auto wait_warp = [&](int b, uint32_t parity) { return tern::wait_warp(bar(b), parity); };
+    // the n-th use of a ring's stage: full, and free for it
+    auto full = [](int n, int stages) { return (uint32_t)(n / stages) & 1u; };
+    auto free = [](int n, int stages) { return ((uint32_t)(n / stages) & 1u) ^ 1u; };
     auto arrive = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
     };
 
-    if (warp < 8) {
+    if (warp < kOutWarp) {
         // ------------------------------ the chain ------------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane;   // of S's columns and of a chunk's tokens
         const bool live = row0 + row < a.dv;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = mine + T_S + (uint32_t)(HALF * half);
-        float S[HALF];
+        const uint32_t ts = mine + T_S + (uint32_t)(COLS * half), tk = mine + T_KS + 32u * half;
+        float S[COLS];
         {
             const float4* from = reinterpret_cast<const float4*>(
-                a.state + (((long long)s.src * a.v_heads + h) * a.dv + row0 + row) * DK + HALF * half);
+                a.state + (((long long)s.src * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * half);
 #pragma unroll
-            for (int i = 0; i < HALF / 4; ++i) {
+            for (int i = 0; i < COLS / 4; ++i) {
                 const float4 x = s.src >= 0 && live ? from[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 S[4 * i] = x.x;
                 S[4 * i + 1] = x.y;
@@ -296,21 +339,19 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 S[4 * i + 3] = x.w;
             }
         }
-        auto v_tile = [&](int c) {   // this warp's 32 rows of S: [token][32 values]
-            return reinterpret_cast<__nv_bfloat16*>(smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) +
-                                                    half * (32 * 64)) + lane;
-        };
-        // S = e^G_last S + D of a chunk, and its parts to where D was: 16 columns each of 32 values
+        // S = e^G_last S + D of a chunk; its parts, 16 columns each of 32 values, in place of D
+        bool ok = true;
+        auto need = [&](int b, uint32_t parity) { ok = ok && wait_warp(b, parity); };
         auto next_state = [&](int c, bool more) {
             float last = 1.0f;
             if (c >= 0) {
-                if (!wait_warp(D_FULL, (uint32_t)c & 1u)) return false;
+                need(D_FULL, (uint32_t)c & 1u);
                 tc_fence_after();
                 last = coefs[c % kCoefStages].last;
             }
             const uint64_t last2 = pack2(last, last);
 #pragma unroll
-            for (int i = 0; i < HALF; i += 32) {
+            for (int i = 0; i < COLS; i += 32) {
                 if (c >= 0) {
                     uint32_t d[32];
                     tmem_ld_x32(ts + (uint32_t)i, d);
@@ -327,220 +368,293 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 tmem_st_x16(ts + (uint32_t)i, hi);
                 tmem_st_x16(ts + (uint32_t)i + 16u, lo);
             }
-            return true;
-        };
-        // the output of a chunk: this thread's row, 32 of its tokens
-        auto output = [&](int c) {
-            if (!wait_warp(O_FULL, (uint32_t)c & 1u)) return false;
-            tc_fence_after();
-            const Coef& k = coefs[c % kCoefStages];
-            uint32_t x[32], y[32];
-            tmem_ld_x32(mine + T_QS + 32u * half, x);
-            tmem_ld_x32(mine + T_O + 32u * half, y);
-            tmem_ld_wait();
-            tc_fence_before();
-            arrive(O_EMPTY);
-            // over the values that this thread read there, and out of shared memory in one piece
-            __nv_bfloat16* const o = v_tile(c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                o[32 * i] = __float2bfloat16(fmaf(k.near_q[32 * half + i], __uint_as_float(x[i]), __uint_as_float(y[i])));
-            const int first = c * kTok + 32 * half, n = s.n - first;
-            if (n >= 32) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && row0 + row < a.dv) {
-                    tma_store_3d(&tmap_out, smem_u32(o), row0 + row, h, s.t0 + first);
-                    bulk_commit();
-                }
-            } else if (live) {   // the sequence ends among these tokens
-                const long long step = (long long)a.v_heads * a.dv;
-                __nv_bfloat16* to = a.out + (s.t0 + first) * step + (long long)h * a.dv + row0 + row;
-                for (int i = 0; i < n; ++i) to[i * step] = o[32 * i];
+            if (more) {
+                tmem_st_wait();
+                tc_fence_before();
+                chain_arrive(S_READY);
             }
-            arrive(COEF_EMPTY + c % kCoefStages);
-            return true;
+            if (c >= 0) arrive(COEF_EMPTY + c % kCoefStages);
         };
-        auto stored = [&](int c) {   // the stores of a chunk's output have left its place in shared memory
-            if (lane == 0) {
-                bulk_wait_read();
-                mbar_arrive(bar(V_EMPTY + c % kVStages));
-            }
-        };
-        bool ok = true;
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const uint32_t ph = (uint32_t)c & 1u;
-            if (!next_state(c - 1, true)) { ok = false; break; }
-            tmem_st_wait();
-            tc_fence_before();
-            arrive(S_FULL);
-            if (c > 1) stored(c - 2);
-            if (c > 0 && !output(c - 1)) { ok = false; break; }
-
             const Coef& k = coefs[c % kCoefStages];
-            if (!wait_warp(COEF_FULL + c % kCoefStages, (uint32_t)(c / kCoefStages) & 1u) ||
-                !wait_warp(V_FULL + c % kVStages, (uint32_t)(c / kVStages) & 1u) || !wait_warp(KS_FULL, ph)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t x[32], hi[16], lo[16];
-            tmem_ld_x32(mine + T_KS + 32u * half, x);
-            const __nv_bfloat16* v = v_tile(c);
-            float vx[32];   // then what the parts of X leave of it: T's diagonal is 1
+            next_state(c - 1, true);
+            need(TP_FULL + (c & 1), full(c, kTpStages));
+            need(V_FULL + c % kVStages, full(c, kVStages));
+            const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
+                smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) + half * (32 * 64)) + lane;
+            float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) vx[i] = __bfloat162float(v[32 * i]) * k.beta[32 * half + i];
+            for (int i = 0; i < 32; i += 4) {
+                const float4 beta = *reinterpret_cast<const float4*>(&k.beta[32 * half + i]);
+                x[i] = __bfloat162float(v[32 * i]) * beta.x;
+                x[i + 1] = __bfloat162float(v[32 * i + 32]) * beta.y;
+                x[i + 2] = __bfloat162float(v[32 * i + 64]) * beta.z;
+                x[i + 3] = __bfloat162float(v[32 * i + 96]) * beta.w;
+            }
+            need(KS_FULL, ph);
+            tc_fence_after();
+            uint32_t z[32], hi[16], lo[16];
+            tmem_ld_x32(tk, z);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float2 near = *reinterpret_cast<const float2*>(&k.minus_near[32 * half + 2 * e]);
-                float p, q;
-                unpack2(fma2(pack2(near.x, near.y), pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                             pack2(vx[2 * e], vx[2 * e + 1])), p, q);
-                split2(p, q, hi[e], lo[e]);
-                unpack2(add2(pack2(p, q), pack2(-__uint_as_float(hi[e] << 16), -__uint_as_float(hi[e] & 0xFFFF0000u))), p, q);
-                unpack2(add2(pack2(p, q), pack2(-__uint_as_float(lo[e] << 16), -__uint_as_float(lo[e] & 0xFFFF0000u))),
-                        vx[2 * e], vx[2 * e + 1]);
+                unpack2(fma2(pack2(near.x, near.y), pack2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                             pack2(x[2 * e], x[2 * e + 1])), x[2 * e], x[2 * e + 1]);
+                split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
             }
             tmem_st_x16(mine + T_X + 16u * half, hi);
             tmem_st_x16(mine + T_X + 32u + 16u * half, lo);
             tmem_st_wait();
             tc_fence_before();
-            arrive(X_FULL);
-
-            if (!wait_warp(U_FULL, ph)) { ok = false; break; }
-            tc_fence_after();
-            tmem_ld_x32(mine + T_KS + 32u * half, x);
-            tmem_ld_wait();
+            chain_arrive(X_READY);
+            // what the parts leave of X
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + vx[i]);
+            for (int e = 0; e < 16; ++e)
+                unpack2(less_bf16(less_bf16(pack2(x[2 * e], x[2 * e + 1]), hi[e]), lo[e]), x[2 * e], x[2 * e + 1]);
+
+            need(U_FULL, ph);
+            tc_fence_after();
+            tmem_ld_x32(tk, z);
+            tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float2 left = *reinterpret_cast<const float2*>(&k.left[32 * half + 2 * e]);
+                const uint64_t u = add2(pack2(x[2 * e], x[2 * e + 1]), pack2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])));
                 float p, q;
-                unpack2(mul2(pack2(left.x, left.y), pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]))), p, q);
+                unpack2(u, x[2 * e], x[2 * e + 1]);
+                unpack2(mul2(pack2(left.x, left.y), u), p, q);
                 split2(p, q, hi[e], lo[e]);
             }
             tmem_st_x16(mine + T_UP + 16u * half, hi);
             tmem_st_x16(mine + T_UP + 32u + 16u * half, lo);
             tmem_st_wait();
             tc_fence_before();
-            arrive(UP_FULL);
+            chain_arrive(UP_READY);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) split2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), hi[e], lo[e]);
-            tmem_st_x16(mine + T_X + 16u * half, hi);
-            tmem_st_x16(mine + T_X + 32u + 16u * half, lo);
+            for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+            tmem_st_x16(tk, hi);
+            tmem_st_x16(tk + 16u, lo);
             tmem_st_wait();
             tc_fence_before();
-            arrive(U2_FULL);
+            chain_arrive(U2_READY);
         }
-        if (ok && chunks > 0) ok = next_state(chunks - 1, false) && output(chunks - 1);
-        if (lane == 0) bulk_wait();
+        if (chunks > 0) next_state(chunks - 1, false);
         if (!ok) {
             if (lane == 0) fail();
         } else if (s.dst >= 0 && live && (s.n > 0 || s.dst != s.src)) {
             float4* to = reinterpret_cast<float4*>(
-                a.state + (((long long)s.dst * a.v_heads + h) * a.dv + row0 + row) * DK + HALF * half);
+                a.state + (((long long)s.dst * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * half);
 #pragma unroll
-            for (int i = 0; i < HALF / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            for (int i = 0; i < COLS / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
         }
         __syncwarp();
-    } else if (warp < 12) {
-        // ------------------------------ T and P from the Gram matrices ------------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        // warps 8 and 9: K K^T, rows 0-31 and 32-63; 10 and 11: Q K^T
-        const int part = (warp - 8) & 1, i = 32 * part + lane, me = warp - 8;
-        const bool is_k = warp < 10, low = lane < 16;
-        const uint32_t gram = tmem + ((uint32_t)((warp - 8) * 32) << 16) + T_GRAM;
-        const uint32_t A = sbase + (uint32_t)C::kA;
-        float* const diag = reinterpret_cast<float*>(smem + C::kDiag);
-        uint32_t syncs = 0;
-        auto sync_warps = [&] {   // the four of them
-            arrive(PREP);
-            return wait_warp(PREP, syncs++ & 1u);
-        };
-        // 16 values as bf16 to two units of a row of a tile (and what that leaves of them to the next tile)
-        auto put16 = [&](uint32_t tile, int unit, const float (&z)[16], bool both) {
+    } else if (warp < kGramWarp) {
+        // ------------------------------ the output ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int quad = warp - kOutWarp, row = quad * 32 + lane;
+        const bool live = row0 + row < a.dv;
+        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16);
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            if (!wait_warp(O_FULL, (uint32_t)c & 1u)) { ok = false; break; }
+            tc_fence_after();
+            const Coef& k = coefs[c % kCoefStages];
+            // over the values of V, which have been used, and out of shared memory in one piece
+            __nv_bfloat16* const o = reinterpret_cast<__nv_bfloat16*>(smem + C::kV + (c % kVStages) * C::kVBytes + quad * (kTok * 64)) + lane;
+            const uint32_t qs = mine + ((c & 1) ? T_QS_ODD : T_QS_EVEN);
+#pragma unroll 1
+            for (int t = 0; t < kTok; t += 16) {
+                uint32_t x[16], y[16];
+                tmem_ld_x16(qs + (uint32_t)t, x);
+                tmem_ld_x16(mine + T_O + (uint32_t)t, y);
+                tmem_ld_wait();
+                if (t == kTok - 16) {
+                    tc_fence_before();
+                    arrive(O_EMPTY);
+                }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t hi[4], lo[4];
+                for (int i = 0; i < 16; i += 4) {   // (all read before anything is stored)
+                    const float4 f = *reinterpret_cast<const float4*>(&k.near_q[t + i]);
+                    float p, q;
+                    unpack2(fma2(pack2(f.x, f.y), pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                 pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]))), p, q);
+                    x[i] = pack_bf16(p, q);
+                    unpack2(fma2(pack2(f.z, f.w), pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                 pack2(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]))), p, q);
+                    x[i + 2] = pack_bf16(p, q);
+                }
+                const uint32_t to = smem_u32(o + 32 * t);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) split2(z[8 * u + 2 * e], z[8 * u + 2 * e + 1], hi[e], lo[e]);
-                const uint32_t at = tile_at(tile, i, unit + u);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-                if (both)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kTok * 128), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+                for (int i = 0; i < 16; i += 2) {
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + 64u * i), "h"((unsigned short)x[i]) : "memory");
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + 64u * i + 64u), "h"((unsigned short)(x[i] >> 16)) : "memory");
+                }
             }
+            const int first = c * kTok, n = s.n - first;
+            if (n >= kTok) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (live) {
+                        tma_store_3d(&tmap_out, smem_u32(o), row0 + row, h, s.t0 + first);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                    mbar_arrive(bar(V_EMPTY + c % kVStages));
+                }
+            } else if (live) {   // the sequence ends in this chunk
+                const long long step = (long long)a.v_heads * a.dv;
+                __nv_bfloat16* to = a.out + (s.t0 + first) * step + (long long)h * a.dv + row0 + row;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) to[i * step] = o[32 * i];
+            }
+            arrive(COEF_EMPTY + c % kCoefStages);
+        }
+        if (lane == 0) {
+            bulk_wait();
+            if (!ok) fail();
+        }
+        __syncwarp();
+    } else if (warp < kInvWarp) {
+        // ------------------------------ A and P from the Gram matrices ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // a thread a row: two warps have K K^T, two Q K^T, in turn
+        const int me = warp - kGramWarp, part = me & 1, i = 32 * part + lane;
+        const bool low = lane < 16;
+        const uint32_t gram = tmem + ((uint32_t)(me * 32) << 16) + T_GRAM;
+        // 8 values as bf16, and what that leaves of them another place on
+        auto put8 = [&](uint32_t at, const float* z, bool parts) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split2(z[2 * e], z[2 * e + 1], hi[e], lo[e]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+            if (parts)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kATile), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
         };
         bool ok = true;
-        for (int c = 0; c < chunks && ok; ++c) {
-            const Coef& k = coefs[c % kCoefStages];
-            const uint32_t T = sbase + (uint32_t)(C::kTp + (c % kTpStages) * C::kTpBytes);
-            if (!wait_warp(COEF_FULL + c % kCoefStages, (uint32_t)(c / kCoefStages) & 1u) ||
-                !wait_warp(GRAM_FULL, (uint32_t)c & 1u) ||
-                !wait_warp(TP_EMPTY + c % kTpStages, ((uint32_t)(c / kTpStages) & 1u) ^ 1u) ||
-                (c > 0 && !wait_warp(TP_FULL + (c - 1) % kTpStages, (uint32_t)((c - 1) / kTpStages) & 1u))) {
-                ok = false;   // (the last: all four are done with the last chunk's A)
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            Coef& k = coefs[c % kCoefStages];
+            const uint32_t P = sbase + (uint32_t)(C::kTp + (c & 1) * C::kTpBytes) + 2 * kTile;
+            const uint32_t A = sbase + (uint32_t)(C::kA + (c & 1) * C::kABytes);
+            const bool is_k = (me < 2) == ((c & 1) == 0);
+            if (!wait_warp(COEF_FULL + c % kCoefStages, full(c, kCoefStages)) || !wait_warp(GRAM_FULL, (uint32_t)c & 1u)) {
+                ok = false;
                 break;
             }
             tc_fence_after();
-            const float mul = is_k ? k.beta_k[i] : k.scale_q[i];
+            uint32_t x[32];
+            tmem_ld_x32(gram + 32u * part, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = low ? x[e] : x[16 + e];   // this row's own 16 columns
+            float mul = k.scale_q[i];
+            if (is_k) {   // K's lengths stand on the diagonal
+                float kk = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) kk = e == (lane & 15) ? __uint_as_float(x[e]) : kk;
+                const float ik = a.norm ? rsqrtf(kk + kDeltaNormEps) : 1.0f, beta = k.beta[i];
+                k.Gk[i] = make_float2(k.G[i].x, k.G[i].y - log2f(ik));
+                k.left[i] *= ik;
+                k.to_end[i] *= ik;
+                k.minus_near[i] = -beta * k.near[i] * ik;
+                mul = beta * ik;
+            } else {
+                k.near_q[i] = mul * k.near[i];
+            }
+            arrive(LENGTHS);
+            if (!wait_warp(LENGTHS, (uint32_t)c & 1u) || !wait_warp(A_EMPTY + (c & 1), free(c, kAStages)) ||
+                !wait_warp(TP_EMPTY + (c & 1), free(c, kTpStages))) {
+                ok = false;
+                break;
+            }
             const uint64_t G = pack2(k.G[i].x, k.G[i].y);
             auto decay_to = [&](float2 g) {   // e^(G_i - g)
-                float x, y;
-                unpack2(add2(G, pack2(-g.x, -g.y)), x, y);
-                return exp2_fast(x + y);
+                float p, q;
+                unpack2(add2(G, pack2(-g.x, -g.y)), p, q);
+                return exp2_fast(p + q);
             };
-            const uint32_t to = is_k ? A : T + 2 * kTok * 128;
-            // tokens of the 16s before this row's: through the last token of their 16, so that no factor is above 1
-            auto before = [&](int b, const uint32_t* x) {
+            // tokens of the 16s before this row's own: through the last token of their 16, so that no factor is above 1
+#pragma unroll 1
+            for (int b = 0; b <= 2 * part; ++b) {
+                uint32_t y[16];
+                __syncwarp();
+                tmem_ld_x16(gram + 16u * b, y);
+                tmem_ld_wait();
+                if (b == 2 * part && low) continue;
                 const float f = decay_to(k.end[b]) * mul;
                 float z[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) z[e] = f * k.to_end[16 * b + e] * __uint_as_float(x[e]);
-                put16(to, 2 * b, z, is_k);
-            };
-            uint32_t x[32];
-            if (part) {
-                tmem_ld_x32(gram, x);
-                tmem_ld_wait();
-                before(0, x);
-                before(1, x + 16);
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 t = *reinterpret_cast<const float2*>(&k.to_end[16 * b + e]);
+                    unpack2(mul2(mul2(pack2(f, f), pack2(t.x, t.y)), pack2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))),
+                            z[e], z[e + 1]);
+                }
+                const int r = b == 2 ? i - 48 : i, unit = b == 2 ? 0 : 2 * b;
+                put8(is_k ? a_at(A, r, unit) : tile_at(P, i, 2 * b), z, is_k);
+                put8(is_k ? a_at(A, r, unit + 1) : tile_at(P, i, 2 * b + 1), z + 8, is_k);
             }
             __syncwarp();
-            tmem_ld_x32(gram + 32u * part, x);
-            tmem_ld_wait();
             tc_fence_before();
             arrive(GRAM_EMPTY);
-            if (!low) before(2 * part, x);
-            {   // this row's own 16: the difference itself, 0 right of the diagonal
+            {   // its own: the difference itself, 0 right of the diagonal
                 const int j0 = 32 * part + (lane & 16);
                 float z[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float f = decay_to(k.G[j0 + e]) * k.k[j0 + e] * mul;
-                    const int over = e - (lane & 15);
-                    z[e] = over < (is_k ? 0 : 1) ? f * __uint_as_float(low ? x[e] : x[16 + e]) : 0.0f;
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 g = *reinterpret_cast<const float4*>(&k.Gk[j0 + e]);
+                    unpack2(mul2(mul2(pack2(decay_to(make_float2(g.x, g.y)), decay_to(make_float2(g.z, g.w))),
+                                      pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))), pack2(mul, mul)), z[e], z[e + 1]);
                 }
-                if (is_k) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<float4*>(diag + i * kDiagRow + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+                for (int e = 0; e < 16; ++e) z[e] = e - (lane & 15) < (is_k ? 0 : 1) ? z[e] : 0.0f;
+                if (is_k) {
+                    float* at = reinterpret_cast<float*>(smem + C::kA + (c & 1) * C::kABytes + 2 * kATile) + (i / 16) * kDiagBlock + (lane & 15);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) at[e * kDiagRow] = -z[e];
                 } else {
-                    put16(to, j0 / 8, z, false);
+                    put8(tile_at(P, i, j0 / 8), z, false);
+                    put8(tile_at(P, i, j0 / 8 + 1), z + 8, false);
                 }
             }
-            if (!sync_warps()) { ok = false; break; }
-            {   // the diagonal blocks of T, one a warp, a column a lane; the upper lanes keep the lower parts
+            fence_proxy_async_smem();
+            arrive(A_FULL + (c & 1));
+        }
+        if (!ok && lane == 0) fail();
+        __syncwarp();
+    } else if (warp < kMmaWarp) {
+        // ------------------------------ T, the inverse of I + A ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int me = warp - kInvWarp;
+        const bool low = lane < 16;
+        uint32_t syncs = 0;
+        auto sync_warps = [&] {   // the four of them
+            arrive(INVERSE);
+            return wait_warp(INVERSE, syncs++ & 1u);
+        };
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t T = sbase + (uint32_t)(C::kTp + (c & 1) * C::kTpBytes);
+            const uint32_t A = sbase + (uint32_t)(C::kA + (c & 1) * C::kABytes);
+            // (A comes with the P beside T: T's place is free)
+            if (!wait_warp(A_FULL + (c & 1), full(c, kAStages))) { ok = false; break; }
+            {   // the diagonal blocks, one a warp, a column a lane; the upper lanes keep the lower parts
                 float t[16];
-                solve16(diag + 16 * me * kDiagRow, lane & 15, t);
+                solve16(reinterpret_cast<const float*>(smem + C::kA + (c & 1) * C::kABytes + 2 * kATile) + me * kDiagBlock, lane & 15, t);
                 const int col = 16 * me + (lane & 15);
+                const uint32_t to = T + (uint32_t)(16 * me * 128) + 2u * (col & 7) + (low ? 0u : kTile);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const __nv_bfloat16 hi = __float2bfloat16(t[r]), lo = __float2bfloat16(t[r] - __bfloat162float(hi));
-                    const uint32_t at = tile_at(T, 16 * me + r, col / 8) + 2u * (col & 7) + (low ? 0u : (uint32_t)(kTok * 128));
-                    const __nv_bfloat16 w = low ? hi : lo;
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const unsigned short*>(&w)) : "memory");
+                for (int r = 0; r < 16; r += 2) {
+                    uint32_t hi, lo;
+                    split2(t[r], t[r + 1], hi, lo);
+                    const uint32_t w = low ? hi : lo;
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(tile_at(to, r, col / 8)), "h"((unsigned short)w) : "memory");
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(tile_at(to, r + 1, col / 8)), "h"((unsigned short)(w >> 16)) : "memory");
                 }
             }
             if (!sync_warps()) { ok = false; break; }
@@ -548,151 +662,161 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (!sync_warps()) { ok = false; break; }
             join_blocks<2>(A, T, 32, 0, me, lane);
             fence_proxy_async_smem();
-            arrive(TP_FULL + c % kTpStages);
+            arrive(TP_FULL + (c & 1));
+            if (lane == 0) mbar_arrive(bar(A_EMPTY + (c & 1)));
         }
         if (!ok && lane == 0) fail();
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 12) {
-            // ------------------------------ MMA ------------------------------
-            if (lane == 0) {
-                constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTok);
-                constexpr uint32_t kIdescD = idesc_bf16_f32(kRows, DK) | kIdescBMnMajor;
-                bool ok = true, issued = false;
-                auto need = [&](int b, uint32_t parity) {
-                    if (ok && !wait(b, parity)) ok = false;
-                    return ok;
-                };
-                auto kq = [&](int c) { return sbase + (uint32_t)(C::kKq + (c % kKqStages) * C::kKqBytes); };
-                auto gram = [&](int c) {
-                    if (!need(KQ_FULL + c % kKqStages, (uint32_t)(c / kKqStages) & 1u) ||
-                        !need(GRAM_EMPTY, ((uint32_t)c & 1u) ^ 1u))
-                        return;
-                    tc_fence_after();
-                    const uint64_t d = smem_desc_k_sw128(kq(c));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == kMmaWarp) {
+            // ------------------------------ products ------------------------------
+            constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTok), kIdescKq = idesc_bf16_f32(kRows, 2 * kTok);
+            constexpr uint32_t kIdescD = idesc_bf16_f32(kRows, DK) | kIdescBMnMajor;
+            bool ok = true;
+            auto need = [&](int b, uint32_t parity) { ok = ok && wait_warp(b, parity); };
+            auto kq = [&](int c) { return sbase + (uint32_t)(C::kKq + (c % kKqStages) * C::kKqBytes); };
+            auto step = [](int kk) { return (uint64_t)((kk / 4) * (2 * kTile >> 4) + 2 * (kk % 4)); };
+            // (+)= 64 tokens in tensor memory times a [64][64] tile
+            auto with_tile = [&](uint32_t to, uint32_t left, uint32_t half, uint32_t tile, bool more) {
+                const uint64_t d = smem_desc_k_sw128(tile);
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) {
-                        const uint64_t at = d + (uint64_t)((kk / 4) * ((2 * kTok * 128) >> 4) + 2 * (kk % 4));
-                        mma_f16_ss(tmem + T_GRAM, at, at, kIdesc, kk > 0);
+                for (int kk = 0; kk < kTok / 16; ++kk)
+                    mma_f16_ts(to, left + half * (kk / 2) + 8u * (kk % 2), d + 2 * kk, kIdesc, (more || kk) ? 1u : 0u);
+            };
+            // the first two Gram matrices, then in chunk c that of c + 2
+#pragma unroll 1
+            for (int c = -2; c < chunks; ++c) {
+                const uint32_t ph = (uint32_t)c & 1u;
+                const uint32_t tp = sbase + (uint32_t)(C::kTp + (c & 1) * C::kTpBytes);
+                if (c >= 0) {
+                    // (Q S^T goes to where the chunk before the last had its own, whose output had been read
+                    // before the last chunk's P U; that has to be done with U's parts)
+                    need(KQ_FULL + c % kKqStages, full(c, kKqStages));
+                    if (c > 0) need(O_FULL, ph ^ 1u);
+                    chain_wait(S_READY);
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        const uint64_t d = smem_desc_k_sw128(kq(c));
+                        const uint32_t to = (c & 1) ? T_QS_ODD : T_KS;
+#pragma unroll
+                        for (int kk = 0; kk < DK / 16; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                mma_f16_ts(to, T_S + 32u * (kk / 2) + 8u * (kk % 2) + 16u * x, d + step(kk), kIdescKq, (kk | x) ? 1u : 0u);
+                        mma_commit(bar(KS_FULL));
                     }
-                    issued = true;
-                    mma_commit(bar(GRAM_FULL));
-                };
-                // (+)= parts of S times K (first = 0) or Q (1) rows
-                auto with_state = [&](int c, uint32_t to, int first) {
-                    const uint64_t d = smem_desc_k_sw128(kq(c) + (uint32_t)(first * kTok * 128));
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-#pragma unroll
-                        for (int kk = 0; kk < DK / 16; ++kk) {
-                            const uint32_t left = tmem + T_S + (uint32_t)(32 * (kk / 2) + 16 * p + 8 * (kk % 2));
-                            mma_f16_ts(tmem + to, left, d + (uint64_t)((kk / 4) * ((2 * kTok * 128) >> 4) + 2 * (kk % 4)),
-                                       kIdesc, (p | kk) ? 1u : 0u);
-                        }
-                };
-                // (+)= 64 tokens in tensor memory times a [64][64] tile
-                auto with_tile = [&](uint32_t to, uint32_t left, uint32_t tile, bool more) {
-                    const uint64_t d = smem_desc_k_sw128(tile);
-#pragma unroll
-                    for (int kk = 0; kk < kTok / 16; ++kk)
-                        mma_f16_ts(tmem + to, tmem + left + 8u * kk, d + 2 * kk, kIdesc, (more || kk) ? 1u : 0u);
-                };
-                if (chunks > 0) gram(0);
-                if (chunks > 1) gram(1);
-                for (int c = 0; c < chunks && ok; ++c) {
-                    const uint32_t ph = (uint32_t)c & 1u;
-                    const uint32_t tp = sbase + (uint32_t)(C::kTp + (c % kTpStages) * C::kTpBytes);
-                    if (!need(S_FULL, ph)) break;
+                    __syncwarp();
+                    need(TP_FULL + (c & 1), full(c, kTpStages));
+                    chain_wait(X_READY);
                     tc_fence_after();
-                    with_state(c, T_KS, 0);
-                    mma_commit(bar(KS_FULL));
-                    if (c > 0 && !need(O_EMPTY, ph ^ 1u)) break;
-                    tc_fence_after();
-                    with_state(c, T_QS, 1);
-                    if (!need(TP_FULL + c % kTpStages, (uint32_t)(c / kTpStages) & 1u) || !need(X_FULL, ph)) break;
-                    tc_fence_after();
-                    with_tile(T_KS, T_X, tp, false);
-                    with_tile(T_KS, T_X + 32, tp, true);
-                    with_tile(T_KS, T_X, tp + kTok * 128, true);
-                    mma_commit(bar(U_FULL));
-                    if (c + 2 < chunks) gram(c + 2);
-                    if (!need(UP_FULL, ph)) break;
-                    tc_fence_after();
-                    {
-                        const uint64_t d = smem_desc_mn_sw128(kq(c), 2 * kTok * 128);
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-#pragma unroll
-                            for (int kk = 0; kk < kTok / 16; ++kk)
-                                mma_f16_ts(tmem + T_S, tmem + T_UP + 32u * p + 8u * kk, d + (uint64_t)(kk * (2048 >> 4)),
-                                           kIdescD, (p | kk) ? 1u : 0u);
+                    if (ok && elect_one()) {
+                        with_tile(T_KS, T_X, 16, tp, false);
+                        with_tile(T_KS, T_X + 32, 16, tp, true);
+                        with_tile(T_KS, T_X, 16, tp + kTile, true);
+                        mma_commit(bar(U_FULL));
                     }
-                    mma_commit(bar(D_FULL));
-                    mma_commit(bar(KQ_EMPTY + c % kKqStages));
-                    if (!need(U2_FULL, ph)) break;
-                    tc_fence_after();
-                    with_tile(T_O, T_X, tp + 2 * kTok * 128, false);
-                    with_tile(T_O, T_X + 32, tp + 2 * kTok * 128, true);
-                    mma_commit(bar(TP_EMPTY + c % kTpStages));
-                    mma_commit(bar(O_FULL));   // (the last: the CTA ends after it)
+                    __syncwarp();
                 }
-                if (!ok) {
-                    fail();
-                    if (issued) {
-                        mma_commit(bar(DRAIN));
-                        (void)mbar_wait_drain(bar(DRAIN), 0u, 100000000ull);
+                const int next = c + 2;
+                if (next < chunks) {
+                    need(KQ_FULL + next % kKqStages, full(next, kKqStages));
+                    need(GRAM_EMPTY, ph ^ 1u);
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        const uint64_t d = smem_desc_k_sw128(kq(next)), k = d + (uint64_t)(k_row(next) * 128 >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < DK / 16; ++kk) mma_f16_ss(T_GRAM, d + step(kk), k + step(kk), kIdesc, kk > 0);
+                        mma_commit(bar(GRAM_FULL));
                     }
+                    __syncwarp();
+                }
+                if (c >= 0) {
+                    chain_wait(UP_READY);
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        const uint64_t d = smem_desc_mn_sw128(kq(c) + (uint32_t)(k_row(c) * 128), 2 * kTile);
+#pragma unroll
+                        for (int kk = 0; kk < kTok / 16; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                mma_f16_ts(T_S, T_UP + 8u * kk + 32u * x, d + (uint64_t)(kk * (2048 >> 4)), kIdescD, (kk | x) ? 1u : 0u);
+                        mma_commit(bar(D_FULL));
+                        mma_commit(bar(KQ_EMPTY + c % kKqStages));
+                    }
+                    __syncwarp();
+                    if (c > 0) need(O_EMPTY, ph ^ 1u);
+                    chain_wait(U2_READY);
+                    tc_fence_after();
+                    if (ok && elect_one()) {
+                        with_tile(T_O, T_KS, 32, tp + 2 * kTile, false);
+                        with_tile(T_O, T_KS + 16, 32, tp + 2 * kTile, true);
+                        mma_commit(bar(TP_EMPTY + (c & 1)));
+                        mma_commit(bar(O_FULL));   // (of the last chunk the last: the CTA ends after it)
+                    }
+                    __syncwarp();
                 }
             }
-            __syncwarp();
-        } else if (warp == 13) {
-            // ------------------------------ TMA ------------------------------
+            if (!ok) {
+                if (lane == 0) fail();
+                if (elect_one()) {   // what has been issued ends before the CTA does
+                    mma_commit(bar(DRAIN));
+                    (void)mbar_wait_drain(bar(DRAIN), 0u, 100000000ull);
+                }
+                __syncwarp();
+            }
+        } else if (warp == kTmaWarp) {
+            // ------------------------------ copies ------------------------------
             // V comes a chunk behind K and Q, which are wanted two chunks ahead
-            const int v_chunks = min(4, (a.dv - row0 + 31) / 32);
-            const uint32_t kq_bytes = (uint32_t)C::kKqBytes, v_bytes = (uint32_t)(v_chunks * kTok * 64);
+            const int v_tiles = min(4, (a.dv - row0 + 31) / 32);
+            const uint32_t kq_bytes = (uint32_t)C::kKqBytes, v_bytes = (uint32_t)(v_tiles * kTok * 64);
             // rows past the sequence's end count as 0
             auto zero = [&](unsigned char* rows, int from, int row_bytes) {
+#pragma unroll 1
                 for (int i = from * (row_bytes / 16) + lane; i < kTok * (row_bytes / 16); i += 32)
                     *reinterpret_cast<uint4*>(rows + i * 16) = make_uint4(0, 0, 0, 0);
             };
             bool ok = true;
             int kqs = 0, vs = 0;   // copies begun
+#pragma unroll 1
             for (int c = 0; c <= chunks && ok; ++c) {
                 if (c < chunks) {
-                    const int st = c % kKqStages, left = s.n - c * kTok;
-                    if (!wait_warp(KQ_EMPTY + st, ((uint32_t)(c / kKqStages) & 1u) ^ 1u)) { ok = false; break; }
+                    const int st = c % kKqStages, left = s.n - c * kTok, kr = k_row(c) * 128, qr = q_row(c) * 128;
+                    if (!wait_warp(KQ_EMPTY + st, free(c, kKqStages))) { ok = false; break; }
                     const uint32_t at = sbase + (uint32_t)(C::kKq + st * C::kKqBytes), to = left < kTok ? bar(TAIL) : bar(KQ_FULL + st);
                     if (lane == 0) {
                         mbar_arrive_expect_tx(to, kq_bytes);
                         for (int x = 0; x < NC; ++x) {
-                            tma_load_2d(at + (uint32_t)(2 * x * kTok * 128), &tmap_k, hk * DK + 64 * x, s.t0 + c * kTok, to);
-                            tma_load_2d(at + (uint32_t)((2 * x + 1) * kTok * 128), &tmap_q, hk * DK + 64 * x, s.t0 + c * kTok, to);
+                            tma_load_2d(at + 2 * x * kTile + (uint32_t)kr, &tmap_k, hk * DK + 64 * x, s.t0 + c * kTok, to);
+                            tma_load_2d(at + 2 * x * kTile + (uint32_t)qr, &tmap_q, hk * DK + 64 * x, s.t0 + c * kTok, to);
                         }
                     }
                     ++kqs;
                     __syncwarp();
                     if (left < kTok) {
                         if (!wait_warp(TAIL, 0u)) { ok = false; break; }
-                        for (int x = 0; x < NC; ++x) zero(smem + C::kKq + st * C::kKqBytes + 2 * x * kTok * 128, left, 128);
+#pragma unroll 1
+                        for (int x = 0; x < NC; ++x) zero(smem + C::kKq + st * C::kKqBytes + 2 * x * kTile + kr, left, 128);
                         fence_proxy_async_smem();
                         arrive(KQ_FULL + st);
                     }
                 }
                 if (c > 0) {
                     const int b = c - 1, st = b % kVStages, left = s.n - b * kTok;
-                    if (!wait_warp(V_EMPTY + st, ((uint32_t)(b / kVStages) & 1u) ^ 1u)) { ok = false; break; }
+                    if (!wait_warp(V_EMPTY + st, free(b, kVStages))) { ok = false; break; }
                     const uint32_t at = sbase + (uint32_t)(C::kV + st * C::kVBytes), to = left < kTok ? bar(TAIL) : bar(V_FULL + st);
                     if (lane == 0) {
                         mbar_arrive_expect_tx(to, v_bytes);
-                        for (int x = 0; x < v_chunks; ++x)
+#pragma unroll 1
+                        for (int x = 0; x < v_tiles; ++x)
                             tma_load_2d(at + (uint32_t)(x * kTok * 64), &tmap_v, h * a.dv + row0 + 32 * x, s.t0 + b * kTok, to);
                     }
                     ++vs;
                     __syncwarp();
                     if (left < kTok) {
                         if (!wait_warp(TAIL, 1u)) { ok = false; break; }
-                        for (int x = 0; x < v_chunks; ++x) zero(smem + C::kV + st * C::kVBytes + x * kTok * 64, left, 64);
+#pragma unroll 1
+                        for (int x = 0; x < v_tiles; ++x) zero(smem + C::kV + st * C::kVBytes + x * kTok * 64, left, 64);
                         fence_proxy_async_smem();
                         arrive(V_FULL + st);
                     }
@@ -704,93 +828,94 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const bool tail = s.n % kTok != 0;
                 for (int i = max(0, kqs - kKqStages); i < kqs; ++i)
                     (void)mbar_wait_drain(tail && i == chunks - 1 ? bar(TAIL) : bar(KQ_FULL + i % kKqStages),
-                                          tail && i == chunks - 1 ? 0u : (uint32_t)(i / kKqStages) & 1u, 20000000ull);
+                                          tail && i == chunks - 1 ? 0u : full(i, kKqStages), 20000000ull);
                 for (int i = max(0, vs - kVStages); i < vs; ++i)
                     (void)mbar_wait_drain(tail && i == chunks - 1 ? bar(TAIL) : bar(V_FULL + i % kVStages),
-                                          tail && i == chunks - 1 ? 1u : (uint32_t)(i / kVStages) & 1u, 20000000ull);
+                                          tail && i == chunks - 1 ? 1u : full(i, kVStages), 20000000ull);
             }
             __syncwarp();
         } else {
-            // ------------------------------ decays, steps and lengths ------------------------------
-            const int part = warp - 14, i = 32 * part + lane;
-            auto gates = [&](int c, int token) {
-                const int t = c * kTok + token;
-                return t < s.n ? delta_gates(a, s.t0 + t, h) : make_float2(0.0f, 0.0f);
+            // ------------------------------ decays, steps, lengths of q ------------------------------
+            // one warp has the decays and steps of all 64 tokens, lane's and lane + 32's, their loads a chunk ahead,
+            // the other the lengths of q
+            const bool decays = warp == kCoefWarp;
+            const DeltaHead head = delta_head(a, h);
+            float2 raw[2] = {};
+            auto load = [&](int c) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int t = c * kTok + 32 * x + lane;
+                    if (t < s.n) raw[x] = delta_raw_gates(a, s.t0 + t, h);
+                }
             };
-            float2 now = make_float2(0.0f, 0.0f);
-            float beside = 0.0f;   // the other half's token's
-            if (chunks > 0) {
-                now = gates(0, i);
-                beside = gates(0, i ^ 32).x;
-            }
+            if (decays && chunks > 0) load(0);
             bool ok = true;
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
-                const float2 gate = now;
-                long long other = fixed_log2(beside);
-                if (c + 1 < chunks) {
-                    now = gates(c + 1, i);
-                    beside = gates(c + 1, i ^ 32).x;
-                }
                 const int ks = c % kKqStages, cs = c % kCoefStages;
-                if (!wait_warp(COEF_EMPTY + cs, ((uint32_t)(c / kCoefStages) & 1u) ^ 1u) ||
-                    !wait_warp(KQ_FULL + ks, (uint32_t)(c / kKqStages) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                float ik = 1.0f, iq = 1.0f;
-                if (a.norm) {
-                    float kk = 0.0f, qq = 0.0f;
-                    const unsigned char* at = smem + C::kKq + ks * C::kKqBytes + i * 128;
-                    uint64_t k2 = 0, q2 = 0;
-                    for (int x = 0; x < NC; ++x, at += 2 * kTok * 128)
-#pragma unroll 2
-                        for (int u = 0; u < 8; ++u) {
-                            const uint4 kv = *reinterpret_cast<const uint4*>(at + ((u ^ (i & 7)) << 4));
-                            const uint4 qv = *reinterpret_cast<const uint4*>(at + kTok * 128 + ((u ^ (i & 7)) << 4));
-                            const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint64_t kp = pack2(__uint_as_float(kw[e] << 16), __uint_as_float(kw[e] & 0xFFFF0000u));
-                                const uint64_t qp = pack2(__uint_as_float(qw[e] << 16), __uint_as_float(qw[e] & 0xFFFF0000u));
-                                k2 = fma2(kp, kp, k2);
-                                q2 = fma2(qp, qp, q2);
-                            }
-                        }
-                    float x, y;
-                    unpack2(k2, x, y);
-                    kk = x + y;
-                    unpack2(q2, x, y);
-                    qq = x + y;
-                    ik = 1.0f / sqrtf(kk + kDeltaNormEps);
-                    iq = 1.0f / sqrtf(qq + kDeltaNormEps);
-                }
-                // the running sum, in 64 bits of which 40 stand behind the point
-                long long G = fixed_log2(gate.x);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long x = __shfl_up_sync(0xffffffffu, G, o);
-                    if (lane >= o) G += x;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
-                if (part) G += other;
-                const long long end = __shfl_sync(0xffffffffu, G, lane | 15);
-                const long long all = __shfl_sync(0xffffffffu, G, 31) + (part ? 0 : other);
                 Coef& k = coefs[cs];
-                const float hi = unfixed(G), near = exp2f(hi);
-                const float2 both = make_float2(hi, unfixed(G - __float2ll_rn(hi * 1099511627776.0f)));
-                const float beta = fmaf(gate.x, 0.0f, gate.y);   // (a decay that is no number makes the step none)
-                k.beta[i] = beta;
-                k.minus_near[i] = -beta * near * ik;
-                k.left[i] = exp2f(unfixed(all - G)) * ik;
-                k.near_q[i] = a.scale * iq * near;
-                k.beta_k[i] = beta * ik;
-                k.scale_q[i] = a.scale * iq;
-                k.k[i] = ik;
-                k.to_end[i] = exp2f(unfixed(end - G)) * ik;
-                k.G[i] = both;
-                if ((lane & 15) == 15) k.end[i / 16] = both;
-                if (part && lane == 31) k.last = exp2f(unfixed(all));
+                if (!wait_warp(COEF_EMPTY + cs, free(c, kCoefStages))) { ok = false; break; }
+                if (decays) {
+                    // the running sums, in 64 bits of which 40 stand behind the point
+                    long long G[2], all = 0;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        const int i = 32 * x + lane;
+                        const float2 in = x ? raw[1] : raw[0];
+                        const float2 gate = c * kTok + i < s.n ? delta_gates(head, in) : make_float2(0.0f, 0.0f);
+                        k.beta[i] = fmaf(gate.x, 0.0f, gate.y);   // (a decay that is no number makes the step none)
+                        long long sum = fixed_log2(gate.x);
+#pragma unroll 1
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                            if (lane >= o) sum += y;
+                        }
+                        sum += all;
+                        all = __shfl_sync(0xffffffffu, sum, 31);
+                        if (x) G[1] = sum;
+                        else G[0] = sum;
+                    }
+                    if (c + 1 < chunks) load(c + 1);
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        const int i = 32 * x + lane;
+                        const long long sum = x ? G[1] : G[0], end = __shfl_sync(0xffffffffu, sum, lane | 15);
+                        const float hi = unfixed(sum);
+                        const float2 both = make_float2(hi, unfixed(sum - __float2ll_rn(hi * 1099511627776.0f)));
+                        k.near[i] = exp2_fast(hi);
+                        k.left[i] = exp2_fast(unfixed(all - sum));
+                        k.to_end[i] = exp2_fast(unfixed(end - sum));
+                        k.G[i] = both;
+                        if ((lane & 15) == 15) k.end[i / 16] = both;
+                    }
+                    if (lane == 0) k.last = exp2_fast(unfixed(all));
+                } else {
+                    if (!wait_warp(KQ_FULL + ks, full(c, kKqStages))) { ok = false; break; }
+#pragma unroll 1
+                    for (int i = lane; i < kTok; i += 32) {
+                        float iq = 1.0f;
+                        if (a.norm) {
+                            const unsigned char* at = smem + C::kKq + ks * C::kKqBytes + (q_row(c) + i) * 128;
+                            uint64_t q2 = 0, r2 = 0;
+#pragma unroll 1
+                            for (int x = 0; x < NC; ++x, at += 2 * kTile)
+#pragma unroll 2
+                                for (int u = 0; u < 8; ++u) {
+                                    const uint4 w = *reinterpret_cast<const uint4*>(at + ((u ^ (i & 7)) << 4));
+                                    auto two = [](uint32_t v) { return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)); };
+                                    const uint64_t w0 = two(w.x), w1 = two(w.y), w2 = two(w.z), w3 = two(w.w);
+                                    q2 = fma2(w0, w0, q2);
+                                    r2 = fma2(w1, w1, r2);
+                                    q2 = fma2(w2, w2, q2);
+                                    r2 = fma2(w3, w3, r2);
+                                }
+                            float x, y;
+                            unpack2(add2(q2, r2), x, y);
+                            iq = rsqrtf(x + y + kDeltaNormEps);
+                        }
+                        k.scale_q[i] = a.scale * iq;
+                    }
+                }
                 arrive(COEF_FULL + cs);
             }
             if (!ok && lane == 0) fail();
@@ -800,7 +925,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -818,14 +943,14 @@ bool make_token_map(CUtensorMap* m, const __nv_bfloat16* base, long long stride,
                CU_TENSOR_MAP_INTERLEAVE_NONE, box_width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The output, [T][heads][dv]: a box of 32 values of one head and 32 tokens; what
+// The output, [T][heads][dv]: a box of 32 values of one head and 64 tokens; what
 // lies past a head's last value is not written.
 bool make_out_map(CUtensorMap* m, __nv_bfloat16* base, int heads, int dv, int T) {
     auto enc = get_encode();
     if (!enc) return false;
     const cuuint64_t dim[3] = {(cuuint64_t)dv, (cuuint64_t)heads, (cuuint64_t)T};
     const cuuint64_t step[2] = {(cuuint64_t)dv * 2, (cuuint64_t)dv * heads * 2};
-    const cuuint32_t box[3] = {32, 1, 32};
+    const cuuint32_t box[3] = {32, 1, kTok};
     const cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dim, step, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
