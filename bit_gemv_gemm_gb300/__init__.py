@@ -455,7 +455,8 @@ def device_error() -> int:
 SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER = 0, 1
 DEVERR_GEMM_MMA_WAIT, DEVERR_GEMV_RANGE_FLAG_WAIT, DEVERR_GEMV_ACTIVATION_RANGE = 0x103, 0x202, 0x203
 DEVERR_CACHE_PAGE, DEVERR_CACHE_SEQUENCE, DEVERR_CACHE_SLOT = 0x301, 0x302, 0x303
-DEVERR_ATTN_WAIT, DEVERR_STATE_SLOT, DEVERR_DELTA_WAIT = 0x311, 0x321, 0x322
+DEVERR_ATTN_WAIT = 0x311
+DEVERR_STATE_SLOT, DEVERR_DELTA_WAIT, DEVERR_NORM_WAIT = 0x321, 0x322, 0x323
 
 
 def wait_selftest(which: int, limit_us: int, stream=None) -> None:
@@ -780,10 +781,42 @@ def _row_strides(name: str, shape, stride, like=None) -> tuple[int, int]:
     return stride[0], stride[1] if len(shape) == 3 else 0
 
 
-def _f32_or_bf16(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor")
-    return 1 if t.dtype is torch.float32 else 0
+# (A call of one token takes the host longer than the GPU: each tensor's type, device and
+# layout are asked for once, and what is wrong is found out only when something is.)
+
+def _now(x: torch.Tensor) -> int:
+    """The current device; that of no tensor, where the first argument lies on none."""
+    return torch.cuda.current_device() if x.is_cuda else -2
+
+
+def _refuse(t, name: str, now: int) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != now:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{now}")
+
+
+def _ptr(t: torch.Tensor, dtype, name: str, now: int) -> int:
+    """The address of a contiguous tensor of the current device."""
+    if t.dtype is dtype and t.get_device() == now and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, now)
+    return _dev(t, dtype, name)
+
+
+def _opt(t, dtype, name: str, now: int):
+    return None if t is None else _ptr(t, dtype, name, now)
+
+
+def _f32_or_bf16(t: torch.Tensor, name: str, now: int) -> int:
+    kind = t.dtype
+    if t.get_device() == now:
+        if kind is torch.bfloat16:
+            return 0
+        if kind is torch.float32:
+            return 1
+    _refuse(t, name, now)
+    raise TypeError(f"{name} must be float32 or bfloat16, got {kind}")
 
 
 _GATES = {"silu": 0, "sigmoid": 1}
@@ -809,13 +842,14 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     T, dim = shape[0], shape[-1]
     heads = shape[1] if len(shape) == 3 else 1
     rt = rh = gt = gh = 0
-    kinds = [_f32_or_bf16(x, "x"), 0, 0]
+    now = _now(x)
+    kinds = [_f32_or_bf16(x, "x", now), 0, 0]
     if residual is not None:
         rt, rh = _row_strides("residual", residual.shape, residual.stride(), shape)
-        kinds[1] = _f32_or_bf16(residual, "residual")
+        kinds[1] = _f32_or_bf16(residual, "residual", now)
     if gate is not None:
         gt, gh = _row_strides("gate", gate.shape, gate.stride(), shape)
-        kinds[2] = _f32_or_bf16(gate, "gate")
+        kinds[2] = _f32_or_bf16(gate, "gate", now)
     if residual_out is not None and residual is None:
         raise ValueError("residual_out needs a residual")
     if residual_out is not None and after:
@@ -825,26 +859,23 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
                    stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    of32 = _f32_or_bf16(out, "out")
+    of32 = _f32_or_bf16(out, "out", now)
     _covers(weight=(weight, dim), out=(out, T * heads * dim), residual_out=(residual_out, T * heads * dim))
-    _here("x weight residual gate residual_out out", x, weight, residual, gate, residual_out, out)
     _check("tern_rms_norm", lib().tern_rms_norm(
         x.data_ptr(), kinds[0], xt, xh, None if residual is None else residual.data_ptr(), kinds[1], rt, rh,
         None if gate is None else gate.data_ptr(), kinds[2], gt, gh, _GATES[gate_act],
-        _dev(weight, torch.float32, "weight"), weight_offset, scale, eps, 1 if after else 0, T, heads, dim,
-        _dev(out, out.dtype, "out"), of32,
-        None if residual_out is None else _dev(residual_out, residual.dtype, "residual_out"), _stream(stream)))
+        _ptr(weight, torch.float32, "weight", now), weight_offset, scale, eps, 1 if after else 0, T, heads, dim,
+        _ptr(out, out.dtype, "out", now), of32,
+        None if residual_out is None else _ptr(residual_out, residual.dtype, "residual_out", now), _stream(stream)))
     return out
 
 
-def _states(T: int, slots, dst_slots, past, q_start, max_new):
+def _states(T: int, slots, dst_slots, past, q_start, max_new, now: int):
     """(slots, dst_slots, past, q_start pointers, B, max_new) of the sequences of a call."""
-    B = slots.numel()
+    B, i32 = slots.numel(), torch.int32
     _covers(dst_slots=(dst_slots, B), past=(past, B), q_start=(q_start, B + 1))
-    i32 = torch.int32
-    return (_dev(slots, i32, "slots"), None if dst_slots is None else _dev(dst_slots, i32, "dst_slots"),
-            None if past is None else _dev(past, i32, "past"),
-            None if q_start is None else _dev(q_start, i32, "q_start"), B, T if max_new is None else max_new)
+    return (_ptr(slots, i32, "slots", now), _opt(dst_slots, i32, "dst_slots", now), _opt(past, i32, "past", now),
+            _opt(q_start, i32, "q_start", now), B, T if max_new is None else max_new)
 
 
 def short_conv(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, slots: torch.Tensor,
@@ -868,18 +899,17 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, slots
     W = weight.shape[1]
     if state.dim() != 3 or state.shape[1:] != (W - 1, C):
         raise ValueError(f"state must be [pool, {W - 1}, {C}], got {tuple(state.shape)}")
-    kind = _f32_or_bf16(x, "x")
+    now = _now(x)
+    kind = _f32_or_bf16(x, "x", now)
     if out is None:
         out = _new((T, C), torch.bfloat16, x.device, stream)
     _covers(out=(out, T * C), bias=(bias, C))
-    _here("x weight state slots q_start bias past dst_slots out", x, weight, state, slots, q_start, bias, past,
-          dst_slots, out)
-    sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new)
+    sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new, now)
     _check("tern_short_conv", lib().tern_short_conv(
-        x.data_ptr(), kind, x.stride(0) if T > 1 else C, _dev(weight, torch.float32, "weight"), W,
-        None if bias is None else _dev(bias, torch.float32, "bias"), 1 if silu else 0,
-        _dev(state, torch.float32, "state"), state.shape[0], sl, dl, pp, qp, B, T, max_new, C,
-        _dev(out, torch.bfloat16, "out"), _stream(stream)))
+        x.data_ptr(), kind, x.stride(0) if T > 1 else C, _ptr(weight, torch.float32, "weight", now), W,
+        _opt(bias, torch.float32, "bias", now), 1 if silu else 0,
+        _ptr(state, torch.float32, "state", now), state.shape[0], sl, dl, pp, qp, B, T, max_new, C,
+        _ptr(out, torch.bfloat16, "out", now), _stream(stream)))
     return out
 
 
@@ -888,6 +918,17 @@ def _gate_stride(name: str, shape, stride, tokens: int, heads: int) -> int:
     if tuple(shape) != (tokens, heads) or (stride[1] != 1 and heads > 1):
         raise ValueError(f"{name} must be [{tokens}, {heads}] with contiguous tokens, got {tuple(shape)}")
     return stride[0] if tokens > 1 else heads
+
+
+@functools.lru_cache(maxsize=4096)
+def _delta_strides(qs, qt, ks, kt, vs, vt, gs, gt, bs, bt, Hv: int, Dv: int, Dk: int):
+    """(T, key heads, token strides of q, k, v, g and beta), from their shapes and strides."""
+    strides = (_token_stride("q", qs, qt, None, Dk), _token_stride("k", ks, kt, qs[1], Dk),
+               _token_stride("v", vs, vt, Hv, Dv))
+    T = qs[0]
+    if ks[0] != T or vs[0] != T:
+        raise ValueError("q, k and v must hold the same number of tokens")
+    return (T, qs[1], *strides, _gate_stride("g", gs, gt, T, Hv), _gate_stride("beta", bs, bt, T, Hv))
 
 
 def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -910,28 +951,22 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     if state.dim() != 4:
         raise ValueError("state must be [pool, v_heads, Dv, Dk]")
     pool, Hv, Dv, Dk = state.shape
-    bf16 = torch.bfloat16
-    qs, ks, vs = _tokens(q, bf16, "q", None, Dk), _tokens(k, bf16, "k", q.shape[1], Dk), _tokens(v, bf16, "v", Hv, Dv)
-    T, Hk = q.shape[:2]
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v must hold the same number of tokens")
-    gs = _gate_stride("g", g.shape, g.stride(), T, Hv)
-    bs = _gate_stride("beta", beta.shape, beta.stride(), T, Hv)
-    for name, t in (("g", g), ("beta", beta)):
-        if not t.is_cuda or t.dtype is not torch.float32:
-            raise TypeError(f"{name} must be a float32 CUDA tensor")
+    bf16, f32, now = torch.bfloat16, torch.float32, _now(q)
+    T, Hk, qs, ks, vs, gs, bs = _delta_strides(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), g.shape,
+                                               g.stride(), beta.shape, beta.stride(), Hv, Dv, Dk)
+    for name, t, kind in (("q", q, bf16), ("k", k, bf16), ("v", v, bf16), ("g", g, f32), ("beta", beta, f32)):
+        if t.dtype is not kind or t.get_device() != now:
+            _refuse(t, name, now)
+            raise TypeError(f"{name} must be {kind}, got {t.dtype}")
     if (a_log is None) != (dt_bias is None):
         raise ValueError("a_log and dt_bias come together")
     if out is None:
         out = _new((T, Hv, Dv), bf16, q.device, stream)
     _covers(out=(out, T * Hv * Dv), a_log=(a_log, Hv), dt_bias=(dt_bias, Hv))
-    _here("q k v g beta state slots q_start a_log dt_bias past dst_slots out", q, k, v, g, beta, state, slots, q_start,
-          a_log, dt_bias, past, dst_slots, out)
-    sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new)
+    sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new, now)
     _check("tern_gated_delta", lib().tern_gated_delta(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, g.data_ptr(), gs, beta.data_ptr(), bs,
-        None if a_log is None else _dev(a_log, torch.float32, "a_log"),
-        None if dt_bias is None else _dev(dt_bias, torch.float32, "dt_bias"), Dk ** -0.5 if scale is None else scale,
-        1 if qk_norm else 0, _dev(state, torch.float32, "state"), pool, sl, dl, pp, qp, B, T, max_new, Hk, Hv, Dk, Dv,
-        _dev(out, bf16, "out"), _stream(stream)))
+        _opt(a_log, f32, "a_log", now), _opt(dt_bias, f32, "dt_bias", now), Dk ** -0.5 if scale is None else scale,
+        1 if qk_norm else 0, _ptr(state, f32, "state", now), pool, sl, dl, pp, qp, B, T, max_new, Hk, Hv, Dk, Dv,
+        _ptr(out, bf16, "out", now), _stream(stream)))
     return out

@@ -91,7 +91,8 @@ tern_status tern_device_error(int* code) {
                                             read_mass_tiles_device_error, read_attn_rows_device_error,
                                             read_attn_tiles_device_error,
                                             read_attn_chunk_device_error, read_evict_device_error,
-                                            read_conv_device_error, read_delta_device_error,
+                                            read_norm_device_error, read_conv_device_error,
+                                            read_delta_device_error,
                                             read_delta_chunk_device_error};
     for (auto* read : readers) {
         int c = 0;

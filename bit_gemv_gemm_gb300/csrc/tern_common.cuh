@@ -42,6 +42,7 @@ cudaError_t read_attn_rows_device_error(int* code);
 cudaError_t read_attn_tiles_device_error(int* code);
 cudaError_t read_attn_chunk_device_error(int* code);
 cudaError_t read_evict_device_error(int* code);
+cudaError_t read_norm_device_error(int* code);
 cudaError_t read_conv_device_error(int* code);
 cudaError_t read_delta_device_error(int* code);
 cudaError_t read_delta_chunk_device_error(int* code);

@@ -7,7 +7,7 @@
 //
 // A thread owns 4 channels and walks a stretch of one sequence's tokens with the
 // last W - 1 inputs in registers, so each input is read once (but for W - 1 at
-// the start of a stretch).  Bound by the bytes read and written.
+// the start of a stretch), a batch of tokens ahead.  Bound by the bytes read and written.
 #include "tern_state.cuh"
 
 namespace tern {
@@ -15,7 +15,8 @@ namespace {
 
 __device__ int g_conv_error;
 
-constexpr int kConvThreads = 128, kConvBatch = 8, kConvStretch = 32;
+constexpr int kConvThreads = 128, kConvStretch = 64;
+constexpr int kPairs = 2, kBatch = 8;   // of channels a thread; tokens in flight
 
 struct ConvArgs {
     StateSeqView s;
@@ -24,26 +25,47 @@ struct ConvArgs {
     const float *weight, *bias;
     float* state;
     __nv_bfloat16* out;
-    int channels, in_f32, silu;
+    int channels, silu;
 };
 
-__device__ __forceinline__ uint4 load4(const ConvArgs& a, long long at) {
-    if (a.in_f32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + at);
-    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.x) + at);
-    return make_uint4(v.x, v.y, 0, 0);
+// A thread's channels of one token as they lie in memory, and as pairs.
+template <bool F32>
+struct Raw {
+    uint32_t u[kPairs * (F32 ? 2 : 1)];
+};
+template <bool F32>
+__device__ __forceinline__ void load_raw(const void* base, long long at, Raw<F32>& r) {
+    constexpr int kWords = kPairs * (F32 ? 2 : 1);
+    const void* p = F32 ? static_cast<const void*>(static_cast<const float*>(base) + at)
+                        : static_cast<const void*>(static_cast<const __nv_bfloat16*>(base) + at);
+    if constexpr (kWords == 2) {
+        const uint2 v = *static_cast<const uint2*>(p);
+        r.u[0] = v.x;
+        r.u[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 v = static_cast<const uint4*>(p)[i];
+            r.u[4 * i] = v.x;
+            r.u[4 * i + 1] = v.y;
+            r.u[4 * i + 2] = v.z;
+            r.u[4 * i + 3] = v.w;
+        }
+    }
 }
-__device__ __forceinline__ float4 widen4(const ConvArgs& a, uint4 r) {
-    if (a.in_f32)
-        return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
-                       __uint_as_float(r.y & 0xFFFF0000u));
+template <bool F32>
+__device__ __forceinline__ void widen(const Raw<F32>& r, uint64_t (&x)[kPairs]) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+        x[i] = F32 ? pack2(__uint_as_float(r.u[2 * i]), __uint_as_float(r.u[2 * i + (F32 ? 1 : 0)]))
+                   : pack2(__uint_as_float(r.u[i] << 16), __uint_as_float(r.u[i] & 0xFFFF0000u));
 }
 
-template <int W>
+template <int W, bool F32>
 __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs a) {
     pdl_launch_dependents();
     pdl_wait();
-    const int c = 4 * (blockIdx.x * kConvThreads + threadIdx.x);
+    const int c = 2 * kPairs * (blockIdx.x * kConvThreads + threadIdx.x);
     const StateSeq q = load_state_seq(a.s, blockIdx.y, &g_conv_error);
     const long long stretch = (long long)blockIdx.z * kConvStretch;
     // (the first stretch's CTA is there for a sequence without tokens too: its state moves)
@@ -51,79 +73,89 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
     const int first = (int)stretch, last = min(first + kConvStretch, q.n);
     const long long base = (long long)q.t0 * a.x_token + c;
 
-    uint4 in[kConvBatch];
-    auto load = [&](int t) {
+    Raw<F32> in[kBatch];
 #pragma unroll
-        for (int i = 0; i < kConvBatch; ++i)
-            if (t + i < last) in[i] = load4(a, base + (t + i) * a.x_token);
+    for (int i = 0; i < kBatch; ++i)
+        if (first + i < last) load_raw<F32>(a.x, base + (first + i) * a.x_token, in[i]);
+    auto input = [&](int t, uint64_t (&x)[kPairs]) {
+        Raw<F32> r;
+        load_raw<F32>(a.x, base + t * a.x_token, r);
+        widen<F32>(r, x);
     };
-    load(first);
+    auto state_of = [&](int slot, int w) {
+        return reinterpret_cast<uint64_t*>(a.state + ((long long)slot * (W - 1) + w) * a.channels + c);
+    };
     // the inputs before the stretch: back[0] the oldest
-    float4 back[W - 1];
-    float4* const old = reinterpret_cast<float4*>(a.state + (long long)q.src * (W - 1) * a.channels + c);
+    uint64_t back[W - 1][kPairs];
 #pragma unroll
     for (int w = 0; w < W - 1; ++w) {
         const int t = first - (W - 1) + w;
-        back[w] = t >= 0 ? widen4(a, load4(a, base + t * a.x_token))
-                  : q.src >= 0 ? old[(long long)w * (a.channels / 4)]
-                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-    float4 weight[W], bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (a.bias) bias = make_float4(a.bias[c], a.bias[c + 1], a.bias[c + 2], a.bias[c + 3]);
-    {
-        // [C][W]: the 4 channels' weights lie in a row
-        const float* p = a.weight + (long long)c * W;
+        if (t >= 0) {
+            input(t, back[w]);
+        } else {
 #pragma unroll
-        for (int w = 0; w < W; ++w) weight[w] = make_float4(p[w], p[W + w], p[2 * W + w], p[3 * W + w]);
+            for (int i = 0; i < kPairs; ++i) back[w][i] = q.src >= 0 ? state_of(q.src, w)[i] : 0;
+        }
+    }
+    uint64_t weight[W][kPairs], bias[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const float* p = a.weight + (long long)(c + 2 * i) * W;   // [C][W]
+        bias[i] = a.bias ? pack2(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) weight[w][i] = pack2(p[w], p[W + w]);
     }
     // the new state, by the thread that has read the old one: its first tokens may be what is left of that
     if (blockIdx.z == 0 && q.dst >= 0 && (q.n > 0 || q.dst != q.src)) {
-        float4* const to = reinterpret_cast<float4*>(a.state + (long long)q.dst * (W - 1) * a.channels + c);
-        float4 keep[W - 1];
+        uint64_t keep[W - 1][kPairs];
 #pragma unroll
         for (int w = 0; w < W - 1; ++w) {
             const int t = q.n - (W - 1) + w;
-            keep[w] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (t >= 0) {
-                keep[w] = widen4(a, load4(a, base + t * a.x_token));
+                input(t, keep[w]);
             } else {
 #pragma unroll
-                for (int o = 0; o < W - 1; ++o)
-                    if (o == q.n + w) keep[w] = back[o];
+                for (int i = 0; i < kPairs; ++i) {
+                    keep[w][i] = 0;
+#pragma unroll
+                    for (int o = 0; o < W - 1; ++o) keep[w][i] = o == q.n + w ? back[o][i] : keep[w][i];
+                }
             }
         }
 #pragma unroll
-        for (int w = 0; w < W - 1; ++w) to[(long long)w * (a.channels / 4)] = keep[w];
+        for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) state_of(q.dst, w)[i] = keep[w][i];
     }
-    for (int t = first; t < last; t += kConvBatch) {
-        float4 x[kConvBatch];
+    __nv_bfloat16* out = a.out + (long long)(q.t0 + first) * a.channels + c;
+    for (int t = first; t < last; t += kBatch) {
 #pragma unroll
-        for (int i = 0; i < kConvBatch; ++i) x[i] = widen4(a, in[i]);
-        load(t + kConvBatch);
+        for (int i = 0; i < kBatch; ++i) {
+            if (t + i >= last) return;
+            uint64_t x[kPairs];
+            uint32_t y[kPairs];
+            widen<F32>(in[i], x);
+            if (t + i + kBatch < last) load_raw<F32>(a.x, base + (t + i + kBatch) * a.x_token, in[i]);
 #pragma unroll
-        for (int i = 0; i < kConvBatch; ++i) {
-            if (t + i >= last) break;
-            float4 y = bias;
+            for (int p = 0; p < kPairs; ++p) {
+                uint64_t s = bias[p];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const int j = i - (W - 1) + w;
-                const float4 v = j >= 0 ? x[j < 0 ? 0 : j] : back[j < 0 ? j + W - 1 : 0];
-                y.x = fmaf(weight[w].x, v.x, y.x);
-                y.y = fmaf(weight[w].y, v.y, y.y);
-                y.z = fmaf(weight[w].z, v.z, y.z);
-                y.w = fmaf(weight[w].w, v.w, y.w);
+                for (int w = 0; w < W - 1; ++w) s = fma2(weight[w][p], back[w][p], s);
+                float u, v;
+                unpack2(fma2(weight[W - 1][p], x[p], s), u, v);
+#pragma unroll
+                for (int w = 0; w < W - 2; ++w) back[w][p] = back[w + 1][p];
+                back[W - 2][p] = x[p];
+                if (a.silu) {
+                    u *= sigmoid(u);
+                    v *= sigmoid(v);
+                }
+                y[p] = pack_bf16(u, v);
             }
-            if (a.silu) {
-                y.x *= sigmoid(y.x);
-                y.y *= sigmoid(y.y);
-                y.z *= sigmoid(y.z);
-                y.w *= sigmoid(y.w);
-            }
-            *reinterpret_cast<uint2*>(a.out + (long long)(q.t0 + t + i) * a.channels + c) =
-                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+            if constexpr (kPairs == 2) *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
+            else *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2 % kPairs], y[3 % kPairs]);
+            out += a.channels;
         }
-#pragma unroll
-        for (int w = 0; w < W - 1; ++w) back[w] = x[kConvBatch - (W - 1) + w];
     }
 }
 
@@ -163,11 +195,12 @@ extern "C" tern_status tern_short_conv(const void* x, int x_is_f32, long long x_
     a.state = state;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.channels = channels;
-    a.in_f32 = x_is_f32;
     a.silu = silu;
-    auto kernel = width == 2 ? short_conv_kernel<2> : width == 3 ? short_conv_kernel<3> : short_conv_kernel<4>;
+    auto kernel = width == 2   ? (x_is_f32 ? short_conv_kernel<2, true> : short_conv_kernel<2, false>)
+                  : width == 3 ? (x_is_f32 ? short_conv_kernel<3, true> : short_conv_kernel<3, false>)
+                               : (x_is_f32 ? short_conv_kernel<4, true> : short_conv_kernel<4, false>);
     const int most = a.s.max_new > 1 ? a.s.max_new : 1;
-    const dim3 grid((channels / 4 + kConvThreads - 1) / kConvThreads, B, (most + kConvStretch - 1) / kConvStretch);
+    const dim3 grid((channels / (2 * kPairs) + kConvThreads - 1) / kConvThreads, B, (most + kConvStretch - 1) / kConvStretch);
     if (launch_pdl(kernel, grid, dim3(kConvThreads), 0, (cudaStream_t)stream, true, a) != cudaSuccess)
         return TERN_ERR_CUDA;
     set_launch_count(1);

@@ -10,10 +10,15 @@
 // bytes; a call of a few rows by its latency.
 #include <math.h>
 
+#include <algorithm>
+
+#include "tern_sm100.cuh"
 #include "tern_state.cuh"
 
 namespace tern {
 namespace {
+
+__device__ int g_norm_error;
 
 constexpr int kMaxDim = 32768;
 
@@ -24,6 +29,7 @@ struct NormArgs {
     long long x_token, x_head, r_token, r_head, g_token, g_head;   // strides in elements
     int x_f32, r_f32, g_f32, out_f32;
     int heads, dim, rows, after, sigmoid_gate;
+    unsigned div, shift;   // row / heads = umulhi(row, div) >> shift
     float scale, eps, offset, part, whole;   // part: 2^-k >= 1 / (2 dim); whole: 2^k / dim
 };
 
@@ -36,8 +42,14 @@ struct NormRow {
     long long x, r, g;
 };
 __device__ __forceinline__ NormRow norm_row(const NormArgs& a, int row) {
-    const int t = a.heads == 1 ? row : (int)((unsigned)row / (unsigned)a.heads), h = row - t * a.heads;
+    const int t = a.heads == 1 ? row : (int)(__umulhi((unsigned)row, a.div) >> a.shift), h = row - t * a.heads;
     return NormRow{t * a.x_token + h * a.x_head, t * a.r_token + h * a.r_head, t * a.g_token + h * a.g_head};
+}
+
+// 16-byte pieces to shared memory, counted on `bar` in bytes.
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+                 "r"(bytes), "r"(bar) : "memory");
 }
 
 // One piece of 8 values of one row.
@@ -60,14 +72,22 @@ __device__ __forceinline__ void open_piece(const NormArgs& a, const NormPiece& p
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = fmaf(a.scale, h[e], r[e]);
     }
+    uint64_t s = pack2(sum, 0.0f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(h[e] * a.part, h[e], sum);
+    for (int e = 0; e < 8; e += 2) {
+        const uint64_t v = pack2(h[e], h[e + 1]);
+        s = fma2(mul2(v, pack2(a.part, a.part)), v, s);
+    }
+    float odd;
+    unpack2(s, sum, odd);
+    sum += odd;
 }
 __device__ __forceinline__ void close_piece(const NormArgs& a, const NormPiece& p, long long out, float inv,
                                             const float (&w)[8], float (&h)[8]) {
     if (a.residual_out) store_raw8(a.residual_out, out, a.r_f32, h);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = h[e] * inv * w[e];
+    for (int e = 0; e < 8; e += 2)
+        unpack2(mul2(mul2(pack2(h[e], h[e + 1]), pack2(inv, inv)), pack2(w[e], w[e + 1])), h[e], h[e + 1]);
     if (a.gate) {
         float z[8];
         widen8(p.g, a.g_f32, z);
@@ -126,50 +146,142 @@ __global__ void __launch_bounds__(256) norm_warp_kernel(const NormArgs a) {
     }
 }
 
-// Longer rows: a CTA a row, the next row's values on their way while this one's
-// sum is formed.
-template <int PIECES>
-__global__ void __launch_bounds__(1024) norm_cta_kernel(const NormArgs a) {
-    __shared__ float part[2][32];
+// Longer rows: CTAs that stay, with their rows' values some rows ahead on the way to a
+// ring in shared memory, a bulk copy an input and row.  (With the next row's values in
+// registers instead, 4096 rows of 5120 took 67 us; a CTA a row 43.)
+constexpr int kStreamBytes = 200 * 1024;   // of an SM's shared memory
+constexpr uint32_t kStreamTries = 1u << 20;
+
+struct NormRing {
+    int stages, row_bytes, r_at, g_at;   // a stage: x, then the residual, then the gate
+};
+
+__device__ __forceinline__ Raw8 shared_raw8(const unsigned char* row, int d, int is_f32) {
+    Raw8 r;
+    if (is_f32) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + 4 * d);
+        r.a = p[0];
+        r.b = p[1];
+    } else {
+        r.a = *reinterpret_cast<const uint4*>(row + 2 * d);
+        r.b = make_uint4(0, 0, 0, 0);
+    }
+    return r;
+}
+
+template <int THREADS, int PIECES, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) norm_stream_kernel(const NormArgs a, const NormRing ring) {
+    extern __shared__ __align__(128) unsigned char rows[];
+    __shared__ __align__(8) uint64_t full[16];
+    __shared__ float part[2][THREADS / 32];
+    constexpr int n = THREADS;
+    const int pieces = a.dim / 8;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ring.stages; ++i) sm100::mbar_init(sm100::smem_u32(&full[i]), 1);
+        sm100::fence_barrier_init();
+    }
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
-    const int n = blockDim.x, pieces = a.dim / 8, warps = n / 32;
+    auto fetch = [&](int row, int stage) {   // one thread
+        const NormRow at = norm_row(a, row);
+        const uint32_t to = sm100::smem_u32(rows + stage * ring.row_bytes), bar = sm100::smem_u32(&full[stage]);
+        const uint32_t xb = a.dim * (a.x_f32 ? 4 : 2), rb = a.residual ? a.dim * (a.r_f32 ? 4 : 2) : 0, gb = a.gate ? a.dim * (a.g_f32 ? 4 : 2) : 0;
+        sm100::mbar_arrive_expect_tx(bar, xb + rb + gb);
+        bulk_load(to, static_cast<const unsigned char*>(a.x) + at.x * (a.x_f32 ? 4 : 2), xb, bar);
+        if (rb) bulk_load(to + ring.r_at, static_cast<const unsigned char*>(a.residual) + at.r * (a.r_f32 ? 4 : 2), rb, bar);
+        if (gb) bulk_load(to + ring.g_at, static_cast<const unsigned char*>(a.gate) + at.g * (a.g_f32 ? 4 : 2), gb, bar);
+    };
+    const int step = gridDim.x, count = (a.rows - 1 - (int)blockIdx.x) / step + 1;   // rows of this CTA
+    if (threadIdx.x == 0)
+        for (int i = 0; i < ring.stages && i < count; ++i) fetch(blockIdx.x + i * step, i);
     float w[PIECES][8];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
         if (threadIdx.x + i * n < pieces) load_weight(a, 8 * (threadIdx.x + i * n), w[i]);
-    NormPiece next[PIECES];
-    int row = blockIdx.x;
-    auto load = [&](int r) {
-        const NormRow at = norm_row(a, r);
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-            if (threadIdx.x + i * n < pieces) load_piece(a, at, 8 * (threadIdx.x + i * n), next[i]);
-    };
-    if (row < a.rows) load(row);
-    for (int turn = 0; row < a.rows; turn ^= 1) {
+    int stage = 0;
+    uint32_t phase = 0, tries = kStreamTries;
+    for (int k = 0; k < count; ++k) {
+        const int row = blockIdx.x + k * step;
+        bool landed = false;
+        for (uint32_t left = tries; !landed && left > 0; --left) landed = sm100::mbar_try_wait(sm100::smem_u32(&full[stage]), phase);
+        if (!landed && tries > 1) {   // (and the rows after it are not waited for again)
+            report_device_error(&g_norm_error, TERN_DEVERR_NORM_WAIT);
+            tries = 1;
+        }
+        const unsigned char* src = rows + stage * ring.row_bytes;
         NormPiece p[PIECES];
         float h[PIECES][8], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            p[i] = next[i];
-            if (threadIdx.x + i * n < pieces) open_piece(a, p[i], h[i], sum);
+            const int d = 8 * (threadIdx.x + i * n);
+            if (d < a.dim) {
+                p[i].x = shared_raw8(src, d, a.x_f32);
+                if (a.residual) p[i].r = shared_raw8(src + ring.r_at, d, a.r_f32);
+                if (a.gate) p[i].g = shared_raw8(src + ring.g_at, d, a.g_f32);
+                open_piece(a, p[i], h[i], sum);
+            }
         }
-        const int after = row > a.rows - 1 - (int)gridDim.x ? a.rows : row + gridDim.x;
-        if (after < a.rows) load(after);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = sum;
+        if (threadIdx.x % 32 == 0) part[k & 1][threadIdx.x / 32] = sum;
         __syncthreads();   // (two sets of parts: a warp may be a row ahead, never two)
-        sum = threadIdx.x % 32 < warps ? part[turn][threadIdx.x % 32] : 0.0f;
+        if (threadIdx.x == 0 && k + ring.stages < count) fetch(row + ring.stages * step, stage);
+        sum = threadIdx.x % 32 < n / 32 ? part[k & 1][threadIdx.x % 32] : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = rsqrtf(fmaf(sum, a.whole, a.eps));
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-            if (threadIdx.x + i * n < pieces)
-                close_piece(a, p[i], (long long)row * a.dim + 8 * (threadIdx.x + i * n), inv, w[i], h[i]);
-        row = after;
+        for (int i = 0; i < PIECES; ++i) {
+            const int d = 8 * (threadIdx.x + i * n);
+            if (d < a.dim) close_piece(a, p[i], (long long)row * a.dim + d, inv, w[i], h[i]);
+        }
+        if (++stage == ring.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+// Calls of a few rows, where the ring would only be in the way, and rows past 10240 values:
+// a CTA a row, the first 5120 values in registers, those past them read again.
+constexpr int kRowThreads = 640;
+__global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a) {
+    __shared__ float part[kRowThreads / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const NormRow at = norm_row(a, blockIdx.x);
+    const int first = 8 * threadIdx.x;
+    const long long out = (long long)blockIdx.x * a.dim;
+    float sum = 0.0f, h[8], w[8];
+    NormPiece p;
+    if (first < a.dim) {
+        load_piece(a, at, first, p);
+        load_weight(a, first, w);
+        open_piece(a, p, h, sum);
+    }
+    for (int d = first + 8 * kRowThreads; d < a.dim; d += 8 * kRowThreads) {
+        NormPiece q;
+        float g[8];
+        load_piece(a, at, d, q);
+        open_piece(a, q, g, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = threadIdx.x % 32 < blockDim.x / 32 ? part[threadIdx.x % 32] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = rsqrtf(fmaf(sum, a.whole, a.eps));
+    if (first < a.dim) close_piece(a, p, out + first, inv, w, h);
+    for (int d = first + 8 * kRowThreads; d < a.dim; d += 8 * kRowThreads) {
+        NormPiece q;
+        float g[8], unused = 0.0f;
+        load_piece(a, at, d, q);
+        load_weight(a, d, w);
+        open_piece(a, q, g, unused);
+        close_piece(a, q, out + d, inv, w, g);
     }
 }
 
@@ -179,17 +291,35 @@ cudaError_t launch_warp(const NormArgs& a, cudaStream_t stream) {
     return launch_pdl(norm_warp_kernel<TEAM, PIECES, ROWS>, dim3((a.rows + per - 1) / per), dim3(256), 0, stream, true,
                       a);
 }
-template <int PIECES>
-cudaError_t launch_cta(const NormArgs& a, int sms, cudaStream_t stream) {
-    const int threads = (a.dim / 8 + 32 * PIECES - 1) / (32 * PIECES) * 32;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_cta_kernel<PIECES>, threads, 0) != cudaSuccess)
-        return cudaErrorUnknown;
-    const int most = sms * (per_sm > 0 ? per_sm : 1);
-    return launch_pdl(norm_cta_kernel<PIECES>, dim3(a.rows < most ? a.rows : most), dim3(threads), 0, stream, true, a);
+template <int THREADS, int PIECES, int CTAS>
+cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t stream) {
+    NormRing r;
+    auto bytes = [&](const void* p, int f32) { return p ? (a.dim * (f32 ? 4 : 2) + 127) / 128 * 128 : 0; };
+    r.r_at = bytes(a.x, a.x_f32);
+    r.g_at = r.r_at + bytes(a.residual, a.r_f32);
+    r.row_bytes = r.g_at + bytes(a.gate, a.g_f32);
+    r.stages = std::min(kStreamBytes / CTAS / r.row_bytes, 16);
+    auto kernel = norm_stream_kernel<THREADS, PIECES, CTAS>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes / CTAS);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    return launch_pdl(kernel, dim3(std::min(a.rows, CTAS * sms)), dim3(THREADS), (size_t)r.stages * r.row_bytes, stream, true, a, r);
 }
 
 }  // namespace
+
+cudaError_t read_norm_device_error(int* code) {
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_norm_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_norm_error, &zero, sizeof(int));
+}
+
 }  // namespace tern
 
 using namespace tern;
@@ -217,20 +347,24 @@ extern "C" tern_status tern_rms_norm(const void* x, int x_is_f32, long long x_to
     const tern_status st = check_device(&sms);
     if (st != TERN_OK) return st;
     if (T == 0) return TERN_OK;
-    int k = 0;
+    int k = 0, b = 0;
     while (1 << k < dim) ++k;
+    while (1 << b < heads) ++b;
+    // (exact for rows below 2^31: 2^b < 2 heads)
+    const unsigned div = (unsigned)(((1ull << (31 + b)) + heads - 1) / heads);
     const NormArgs a{x, residual, gate, weight, out, residual_out, x_token, x_head, residual_token, residual_head,
                      gate_token, gate_head, x_is_f32, residual_is_f32, gate_is_f32, out_is_f32, heads, dim, T * heads,
-                     after, gate_act == TERN_GATE_SIGMOID, scale, eps, weight_offset,
+                     after, gate_act == TERN_GATE_SIGMOID, div, b > 0 ? (unsigned)b - 1 : 0u, scale, eps, weight_offset,
                      ldexpf(1.0f, -k), (float)(1 << k) / (float)dim};
     auto* s = (cudaStream_t)stream;
     const cudaError_t e = dim <= 64     ? launch_warp<8, 1, 2>(a, s)
                           : dim <= 128  ? launch_warp<16, 1, 2>(a, s)
                           : dim <= 256  ? launch_warp<32, 1, 2>(a, s)
                           : dim <= 512  ? launch_warp<32, 2, 1>(a, s)
-                          : dim <= 8192 ? launch_cta<1>(a, sms, s)
-                          : dim <= 16384 ? launch_cta<2>(a, sms, s)
-                                         : launch_cta<4>(a, sms, s);
+                          : dim > 10240 || a.rows <= 2 * sms ? launch_pdl(norm_row_kernel, dim3(a.rows), dim3(std::min((dim / 8 + 31) / 32 * 32, kRowThreads)), 0, s, true, a)
+                          : dim <= 2560 ? launch_stream<320, 1, 2>(a, sms, s)
+                          : dim <= 5120 ? launch_stream<320, 2, 2>(a, sms, s)
+                                        : launch_stream<640, 2, 1>(a, sms, s);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;

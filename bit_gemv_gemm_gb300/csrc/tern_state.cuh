@@ -99,6 +99,12 @@ __device__ __forceinline__ void store_raw8(void* base, long long at, int is_f32,
             make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
     }
 }
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + __expf(-x)); }
+// 1 / (1 + e^-x) by the approximate exponential and reciprocal: some units in the last
+// place, far below a bf16's step.  (The exact quotient took a third of a convolution's time.)
+__device__ __forceinline__ float sigmoid(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp2_fast(-1.44269504088896341f * x)));
+    return y;
+}
 
 }  // namespace tern

@@ -611,7 +611,8 @@ enum {
     TERN_DEVERR_ATTN_WAIT = 0x311,           /* attention: a wait for a copy or a product gave up */
     TERN_DEVERR_CACHE_SLOT = 0x303,          /* cache: a slot past the pool's last */
     TERN_DEVERR_STATE_SLOT = 0x321,          /* short_conv, gated_delta: a state slot past the pool's last */
-    TERN_DEVERR_DELTA_WAIT = 0x322           /* gated_delta: a wait for a copy or a product gave up */
+    TERN_DEVERR_DELTA_WAIT = 0x322,          /* gated_delta: a wait for a copy or a product gave up */
+    TERN_DEVERR_NORM_WAIT = 0x323            /* rms_norm: a wait for a copy gave up */
 };
 
 /* Reads and clears the sticky device-side error words of the current device
