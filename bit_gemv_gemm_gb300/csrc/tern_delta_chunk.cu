@@ -11,8 +11,8 @@
 // products have M = 128 and their left operand in tensor memory, and what passes
 // from one product to the next never leaves its lane.
 //
-// What bounds a sequence is the chain from chunk to chunk, three phases of eight
-// warps (two threads a row) between three products:
+// What bounds a sequence is the chain from chunk to chunk, three phases of sixteen
+// warps (four threads a row) between three products:
 //   S = e^G_last S + D, its parts to tensor memory  ->  [K; Q] S^T
 //   X                                               ->  U = T X
 //   e^(G_last - G) U                                ->  D = U^T K
@@ -61,7 +61,7 @@ struct alignas(16) Coef {
 template <int DK>
 struct Cfg {
     static constexpr int NC = DK / 64;                          // chunks of 64 values of a K or Q row
-    static constexpr int COLS = DK / 2;                         // columns of S that a thread holds
+    static constexpr int COLS = DK / 4;                         // columns of S that a thread holds
     static constexpr int kKqBytes = NC * 2 * (int)kTile;        // 64 values of K's and Q's rows, the next 64
     static constexpr int kVBytes = 4 * kTok * 64;               // 32 rows of S a tile: [token][32]
     static constexpr int kTpBytes = 3 * (int)kTile;             // T's two parts, P
@@ -71,35 +71,30 @@ struct Cfg {
                             kMisc = kBar + 48 * 8, kSmem = kMisc + 64 + 1024;
 };
 // warps: the chain, the output, A and P, T, then one each for products and copies and two for decays
-constexpr int kOutWarp = 8, kGramWarp = 12, kInvWarp = 16, kMmaWarp = 20, kTmaWarp = 21, kCoefWarp = 22, kThreads = 24 * 32;
-// registers a thread: 256 x 144 + 128 x (48 + 56 + 48 + 40) = 768 x 80, what the CTA is launched with
+constexpr int kOutWarp = 16, kGramWarp = 20, kInvWarp = 24, kMmaWarp = 28, kTmaWarp = 29, kCoefWarp = 30, kThreads = 32 * 32;
+// registers a thread: 512 x 72 + 128 x (56 + 64 + 56 + 48) = 1024 x 64, what the CTA is launched with
 // tensor memory columns: D over the parts of S, then those of X; Q S^T of odd chunks; K S^T, then U,
 // then U's parts; Q S^T of even chunks; parts of the scaled U; P U; Gram matrices
 enum { T_S = 0, T_X = T_S, T_QS_ODD = 128, T_KS = 192, T_QS_EVEN = 256, T_UP = 320, T_O = 384, T_GRAM = 448 };
-// An odd chunk's rows of Q stand before those of K, an even one's behind: [K; Q] S^T is
-// one product either way, and its Q half does not wait for the last chunk's output.
-__host__ __device__ constexpr int k_row(int chunk) { return (chunk & 1) * kTok; }
-__host__ __device__ constexpr int q_row(int chunk) { return kTok - k_row(chunk); }
-
 enum {
     KQ_FULL = 0, KQ_EMPTY = KQ_FULL + kKqStages, V_FULL = KQ_EMPTY + kKqStages, V_EMPTY = V_FULL + kVStages,
     COEF_FULL = V_EMPTY + kVStages, COEF_EMPTY = COEF_FULL + kCoefStages, TP_FULL = COEF_EMPTY + kCoefStages,
     TP_EMPTY = TP_FULL + kTpStages, GRAM_FULL = TP_EMPTY + kTpStages, GRAM_EMPTY, KS_FULL, U_FULL, D_FULL, O_FULL, O_EMPTY, A_FULL, A_EMPTY = A_FULL + kAStages, LENGTHS = A_EMPTY + kAStages,
-    INVERSE, TAIL, DRAIN, BARS
+    INVERSE, DIAG_FULL, TAIL = DIAG_FULL + kAStages, DRAIN, BARS
 };
 static_assert(BARS <= 48, "barriers");
-// From the chain's 8 warps to the one that issues products: the SM's own barriers, whose
+// From the chain's 16 warps to the one that issues products: the SM's own barriers, whose
 // last arrival wakes it sooner than an mbarrier's.  Nothing bounds a wait at one, so both
 // sides go through all their turns whatever has failed: a failed wait only ends the others.
 enum { S_READY = 1, X_READY, UP_READY, U2_READY };
-constexpr int kChainThreads = 256 + 32;
+constexpr int kChainThreads = 512 + 32;
 __device__ __forceinline__ void chain_arrive(int b) { asm volatile("bar.arrive %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
 __device__ __forceinline__ void chain_wait(int b) { asm volatile("bar.sync %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
 
 __device__ __forceinline__ int bar_count(int i) {
     if (i >= V_EMPTY && i < V_EMPTY + kVStages) return 4;
-    if (i >= COEF_FULL && i < COEF_EMPTY) return 2;
-    if (i >= COEF_EMPTY && i < TP_FULL) return 12;
+    if ((i >= COEF_FULL && i < COEF_EMPTY) || (i >= DIAG_FULL && i < TAIL)) return 2;
+    if (i >= COEF_EMPTY && i < TP_FULL) return 20;
     if ((i >= TP_FULL && i < TP_EMPTY) || i == GRAM_EMPTY || i == O_EMPTY || (i >= A_FULL && i <= INVERSE)) return 4;
     return 1;
 }
@@ -159,6 +154,10 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -321,15 +320,15 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
     if (warp < kOutWarp) {
         // ------------------------------ the chain ------------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane;   // of S's columns and of a chunk's tokens
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
+        const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;   // of S's columns and of a chunk's tokens
         const bool live = row0 + row < a.dv;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = mine + T_S + (uint32_t)(COLS * half), tk = mine + T_KS + 32u * half;
+        const uint32_t ts = mine + T_S + (uint32_t)(COLS * quarter), tk = mine + T_KS + 16u * quarter;
         float S[COLS];
         {
             const float4* from = reinterpret_cast<const float4*>(
-                a.state + (((long long)s.src * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * half);
+                a.state + (((long long)s.src * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * quarter);
 #pragma unroll
             for (int i = 0; i < COLS / 4; ++i) {
                 const float4 x = s.src >= 0 && live ? from[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -339,36 +338,35 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 S[4 * i + 3] = x.w;
             }
         }
-        // S = e^G_last S + D of a chunk; its parts, 16 columns each of 32 values, in place of D
+        // S = e^G_last S + D of a chunk; its parts in place of D
         bool ok = true;
         auto need = [&](int b, uint32_t parity) { ok = ok && wait_warp(b, parity); };
         auto next_state = [&](int c, bool more) {
-            float last = 1.0f;
             if (c >= 0) {
                 need(D_FULL, (uint32_t)c & 1u);
                 tc_fence_after();
-                last = coefs[c % kCoefStages].last;
-            }
-            const uint64_t last2 = pack2(last, last);
+                const float last = coefs[c % kCoefStages].last;
+                const uint64_t last2 = pack2(last, last);
+                uint32_t d[COLS];
+                if constexpr (COLS == 32) tmem_ld_x32(ts, d);
+                else tmem_ld_x16(ts, d);
+                tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < COLS; i += 32) {
-                if (c >= 0) {
-                    uint32_t d[32];
-                    tmem_ld_x32(ts + (uint32_t)i, d);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        unpack2(fma2(last2, pack2(S[i + e], S[i + e + 1]),
-                                     pack2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]))), S[i + e], S[i + e + 1]);
-                }
-                if (!more) continue;
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) split2(S[i + 2 * e], S[i + 2 * e + 1], hi[e], lo[e]);
-                tmem_st_x16(ts + (uint32_t)i, hi);
-                tmem_st_x16(ts + (uint32_t)i + 16u, lo);
+                for (int e = 0; e < COLS; e += 2)
+                    unpack2(fma2(last2, pack2(S[e], S[e + 1]), pack2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]))), S[e],
+                            S[e + 1]);
             }
             if (more) {
+                uint32_t hi[COLS / 2], lo[COLS / 2];
+#pragma unroll
+                for (int e = 0; e < COLS / 2; ++e) split2(S[2 * e], S[2 * e + 1], hi[e], lo[e]);
+                if constexpr (COLS == 32) {
+                    tmem_st_x16(ts, hi);
+                    tmem_st_x16(ts + COLS / 2, lo);
+                } else {
+                    tmem_st_x8(ts, hi);
+                    tmem_st_x8(ts + COLS / 2, lo);
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 chain_arrive(S_READY);
@@ -383,11 +381,11 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             need(TP_FULL + (c & 1), full(c, kTpStages));
             need(V_FULL + c % kVStages, full(c, kVStages));
             const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
-                smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) + half * (32 * 64)) + lane;
-            float x[32];
+                smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) + quarter * (16 * 64)) + lane;
+            float x[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 beta = *reinterpret_cast<const float4*>(&k.beta[32 * half + i]);
+            for (int i = 0; i < 16; i += 4) {
+                const float4 beta = *reinterpret_cast<const float4*>(&k.beta[16 * quarter + i]);
                 x[i] = __bfloat162float(v[32 * i]) * beta.x;
                 x[i + 1] = __bfloat162float(v[32 * i + 32]) * beta.y;
                 x[i + 2] = __bfloat162float(v[32 * i + 64]) * beta.z;
@@ -395,48 +393,48 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
             need(KS_FULL, ph);
             tc_fence_after();
-            uint32_t z[32], hi[16], lo[16];
-            tmem_ld_x32(tk, z);
+            uint32_t z[16], hi[8], lo[8];
+            tmem_ld_x16(tk, z);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 near = *reinterpret_cast<const float2*>(&k.minus_near[32 * half + 2 * e]);
+            for (int e = 0; e < 8; ++e) {
+                const float2 near = *reinterpret_cast<const float2*>(&k.minus_near[16 * quarter + 2 * e]);
                 unpack2(fma2(pack2(near.x, near.y), pack2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
                              pack2(x[2 * e], x[2 * e + 1])), x[2 * e], x[2 * e + 1]);
                 split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
             }
-            tmem_st_x16(mine + T_X + 16u * half, hi);
-            tmem_st_x16(mine + T_X + 32u + 16u * half, lo);
+            tmem_st_x8(mine + T_X + 8u * quarter, hi);
+            tmem_st_x8(mine + T_X + 32u + 8u * quarter, lo);
             tmem_st_wait();
             tc_fence_before();
             chain_arrive(X_READY);
             // what the parts leave of X
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
                 unpack2(less_bf16(less_bf16(pack2(x[2 * e], x[2 * e + 1]), hi[e]), lo[e]), x[2 * e], x[2 * e + 1]);
 
             need(U_FULL, ph);
             tc_fence_after();
-            tmem_ld_x32(tk, z);
+            tmem_ld_x16(tk, z);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 left = *reinterpret_cast<const float2*>(&k.left[32 * half + 2 * e]);
+            for (int e = 0; e < 8; ++e) {
+                const float2 left = *reinterpret_cast<const float2*>(&k.left[16 * quarter + 2 * e]);
                 const uint64_t u = add2(pack2(x[2 * e], x[2 * e + 1]), pack2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])));
                 float p, q;
                 unpack2(u, x[2 * e], x[2 * e + 1]);
                 unpack2(mul2(pack2(left.x, left.y), u), p, q);
                 split2(p, q, hi[e], lo[e]);
             }
-            tmem_st_x16(mine + T_UP + 16u * half, hi);
-            tmem_st_x16(mine + T_UP + 32u + 16u * half, lo);
+            tmem_st_x8(mine + T_UP + 8u * quarter, hi);
+            tmem_st_x8(mine + T_UP + 32u + 8u * quarter, lo);
             tmem_st_wait();
             tc_fence_before();
             chain_arrive(UP_READY);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-            tmem_st_x16(tk, hi);
-            tmem_st_x16(tk + 16u, lo);
+            for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+            tmem_st_x8(tk, hi);
+            tmem_st_x8(tk + 8u, lo);
             tmem_st_wait();
             tc_fence_before();
             chain_arrive(U2_READY);
@@ -446,14 +444,14 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (lane == 0) fail();
         } else if (s.dst >= 0 && live && (s.n > 0 || s.dst != s.src)) {
             float4* to = reinterpret_cast<float4*>(
-                a.state + (((long long)s.dst * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * half);
+                a.state + (((long long)s.dst * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * quarter);
 #pragma unroll
             for (int i = 0; i < COLS / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
         }
         __syncwarp();
     } else if (warp < kGramWarp) {
         // ------------------------------ the output ------------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int quad = warp - kOutWarp, row = quad * 32 + lane;
         const bool live = row0 + row < a.dv;
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16);
@@ -521,10 +519,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         __syncwarp();
     } else if (warp < kInvWarp) {
         // ------------------------------ A and P from the Gram matrices ------------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // a thread a row: two warps have K K^T, two Q K^T, in turn
+        // a thread a row: two warps have K K^T, two Q K^T
         const int me = warp - kGramWarp, part = me & 1, i = 32 * part + lane;
-        const bool low = lane < 16;
+        const bool low = lane < 16, is_k = me < 2;
         const uint32_t gram = tmem + ((uint32_t)(me * 32) << 16) + T_GRAM;
         // 8 values as bf16, and what that leaves of them another place on
         auto put8 = [&](uint32_t at, const float* z, bool parts) {
@@ -541,7 +538,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             Coef& k = coefs[c % kCoefStages];
             const uint32_t P = sbase + (uint32_t)(C::kTp + (c & 1) * C::kTpBytes) + 2 * kTile;
             const uint32_t A = sbase + (uint32_t)(C::kA + (c & 1) * C::kABytes);
-            const bool is_k = (me < 2) == ((c & 1) == 0);
             if (!wait_warp(COEF_FULL + c % kCoefStages, full(c, kCoefStages)) || !wait_warp(GRAM_FULL, (uint32_t)c & 1u)) {
                 ok = false;
                 break;
@@ -558,7 +554,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 16; ++e) kk = e == (lane & 15) ? __uint_as_float(x[e]) : kk;
                 const float ik = a.norm ? rsqrtf(kk + kDeltaNormEps) : 1.0f, beta = k.beta[i];
-                k.Gk[i] = make_float2(k.G[i].x, k.G[i].y - log2f(ik));
+                k.Gk[i] = make_float2(k.G[i].x, k.G[i].y - __log2f(ik));
                 k.left[i] *= ik;
                 k.to_end[i] *= ik;
                 k.minus_near[i] = -beta * k.near[i] * ik;
@@ -578,7 +574,28 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 unpack2(add2(G, pack2(-g.x, -g.y)), p, q);
                 return exp2_fast(p + q);
             };
-            // tokens of the 16s before this row's own: through the last token of their 16, so that no factor is above 1
+            {   // this row's own 16: the difference itself, 0 right of the diagonal
+                const int j0 = 32 * part + (lane & 16);
+                float z[16];
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 g = *reinterpret_cast<const float4*>(&k.Gk[j0 + e]);
+                    unpack2(mul2(mul2(pack2(decay_to(make_float2(g.x, g.y)), decay_to(make_float2(g.z, g.w))),
+                                      pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))), pack2(mul, mul)), z[e], z[e + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e] = e - (lane & 15) < (is_k ? 0 : 1) ? z[e] : 0.0f;
+                if (is_k) {
+                    float* at = reinterpret_cast<float*>(smem + C::kA + (c & 1) * C::kABytes + 2 * kATile) + (i / 16) * kDiagBlock + (lane & 15);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) at[e * kDiagRow] = -z[e];
+                } else {
+                    put8(tile_at(P, i, j0 / 8), z, false);
+                    put8(tile_at(P, i, j0 / 8 + 1), z + 8, false);
+                }
+            }
+            if (is_k) arrive(DIAG_FULL + (c & 1));   // (T's diagonal blocks can be begun)
+            // tokens of the 16s before: through the last token of their 16, so that no factor is above 1
 #pragma unroll 1
             for (int b = 0; b <= 2 * part; ++b) {
                 uint32_t y[16];
@@ -601,26 +618,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             __syncwarp();
             tc_fence_before();
             arrive(GRAM_EMPTY);
-            {   // its own: the difference itself, 0 right of the diagonal
-                const int j0 = 32 * part + (lane & 16);
-                float z[16];
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 g = *reinterpret_cast<const float4*>(&k.Gk[j0 + e]);
-                    unpack2(mul2(mul2(pack2(decay_to(make_float2(g.x, g.y)), decay_to(make_float2(g.z, g.w))),
-                                      pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))), pack2(mul, mul)), z[e], z[e + 1]);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) z[e] = e - (lane & 15) < (is_k ? 0 : 1) ? z[e] : 0.0f;
-                if (is_k) {
-                    float* at = reinterpret_cast<float*>(smem + C::kA + (c & 1) * C::kABytes + 2 * kATile) + (i / 16) * kDiagBlock + (lane & 15);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) at[e * kDiagRow] = -z[e];
-                } else {
-                    put8(tile_at(P, i, j0 / 8), z, false);
-                    put8(tile_at(P, i, j0 / 8 + 1), z + 8, false);
-                }
-            }
             fence_proxy_async_smem();
             arrive(A_FULL + (c & 1));
         }
@@ -628,7 +625,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         __syncwarp();
     } else if (warp < kMmaWarp) {
         // ------------------------------ T, the inverse of I + A ------------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int me = warp - kInvWarp;
         const bool low = lane < 16;
         uint32_t syncs = 0;
@@ -641,8 +638,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         for (int c = 0; c < chunks; ++c) {
             const uint32_t T = sbase + (uint32_t)(C::kTp + (c & 1) * C::kTpBytes);
             const uint32_t A = sbase + (uint32_t)(C::kA + (c & 1) * C::kABytes);
-            // (A comes with the P beside T: T's place is free)
-            if (!wait_warp(A_FULL + (c & 1), full(c, kAStages))) { ok = false; break; }
+            if (!wait_warp(DIAG_FULL + (c & 1), full(c, kAStages)) || !wait_warp(TP_EMPTY + (c & 1), free(c, kTpStages))) {
+                ok = false;
+                break;
+            }
             {   // the diagonal blocks, one a warp, a column a lane; the upper lanes keep the lower parts
                 float t[16];
                 solve16(reinterpret_cast<const float*>(smem + C::kA + (c & 1) * C::kABytes + 2 * kATile) + me * kDiagBlock, lane & 15, t);
@@ -657,7 +656,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     asm volatile("st.shared.b16 [%0], %1;" ::"r"(tile_at(to, r + 1, col / 8)), "h"((unsigned short)(w >> 16)) : "memory");
                 }
             }
-            if (!sync_warps()) { ok = false; break; }
+            if (!sync_warps() || !wait_warp(A_FULL + (c & 1), full(c, kAStages))) { ok = false; break; }
             join_blocks<1>(A, T, 32 * (me >> 1) + 16, 32 * (me >> 1), me & 1, lane);
             if (!sync_warps()) { ok = false; break; }
             join_blocks<2>(A, T, 32, 0, me, lane);
@@ -668,21 +667,31 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (!ok && lane == 0) fail();
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == kMmaWarp) {
             // ------------------------------ products ------------------------------
-            constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTok), kIdescKq = idesc_bf16_f32(kRows, 2 * kTok);
+            constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTok);
             constexpr uint32_t kIdescD = idesc_bf16_f32(kRows, DK) | kIdescBMnMajor;
             bool ok = true;
             auto need = [&](int b, uint32_t parity) { ok = ok && wait_warp(b, parity); };
             auto kq = [&](int c) { return sbase + (uint32_t)(C::kKq + (c % kKqStages) * C::kKqBytes); };
             auto step = [](int kk) { return (uint64_t)((kk / 4) * (2 * kTile >> 4) + 2 * (kk % 4)); };
+            // parts of S times the rows of K or Q
+            auto with_state = [&](uint32_t to, uint64_t rows) {
+                constexpr int kSteps = COLS / 16;   // of a thread's columns
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        mma_f16_ts(to, T_S + (uint32_t)(COLS * (kk / kSteps) + 8 * (kk % kSteps) + COLS / 2 * x), rows + step(kk), kIdesc,
+                                   (kk | x) ? 1u : 0u);
+            };
             // (+)= 64 tokens in tensor memory times a [64][64] tile
-            auto with_tile = [&](uint32_t to, uint32_t left, uint32_t half, uint32_t tile, bool more) {
+            auto with_tile = [&](uint32_t to, uint32_t left, uint32_t stride, uint32_t tile, bool more) {
                 const uint64_t d = smem_desc_k_sw128(tile);
 #pragma unroll
                 for (int kk = 0; kk < kTok / 16; ++kk)
-                    mma_f16_ts(to, left + half * (kk / 2) + 8u * (kk % 2), d + 2 * kk, kIdesc, (more || kk) ? 1u : 0u);
+                    mma_f16_ts(to, left + stride * kk, d + 2 * kk, kIdesc, (more || kk) ? 1u : 0u);
             };
             // the first two Gram matrices, then in chunk c that of c + 2
 #pragma unroll 1
@@ -697,23 +706,20 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     chain_wait(S_READY);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        const uint64_t d = smem_desc_k_sw128(kq(c));
-                        const uint32_t to = (c & 1) ? T_QS_ODD : T_KS;
-#pragma unroll
-                        for (int kk = 0; kk < DK / 16; ++kk)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                mma_f16_ts(to, T_S + 32u * (kk / 2) + 8u * (kk % 2) + 16u * x, d + step(kk), kIdescKq, (kk | x) ? 1u : 0u);
+                        // (K first, for which the chain waits; both as one product of N = 128 take less of the
+                        // tensor pipe, which is not what bounds this, but hold the chain for 600 clocks more)
+                        with_state(T_KS, smem_desc_k_sw128(kq(c)));
                         mma_commit(bar(KS_FULL));
+                        with_state((c & 1) ? T_QS_ODD : T_QS_EVEN, smem_desc_k_sw128(kq(c) + kTile));
                     }
                     __syncwarp();
                     need(TP_FULL + (c & 1), full(c, kTpStages));
                     chain_wait(X_READY);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        with_tile(T_KS, T_X, 16, tp, false);
-                        with_tile(T_KS, T_X + 32, 16, tp, true);
-                        with_tile(T_KS, T_X, 16, tp + kTile, true);
+                        with_tile(T_KS, T_X, 8, tp, false);
+                        with_tile(T_KS, T_X + 32, 8, tp, true);
+                        with_tile(T_KS, T_X, 8, tp + kTile, true);
                         mma_commit(bar(U_FULL));
                     }
                     __syncwarp();
@@ -724,9 +730,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     need(GRAM_EMPTY, ph ^ 1u);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        const uint64_t d = smem_desc_k_sw128(kq(next)), k = d + (uint64_t)(k_row(next) * 128 >> 4);
+                        const uint64_t d = smem_desc_k_sw128(kq(next));
 #pragma unroll
-                        for (int kk = 0; kk < DK / 16; ++kk) mma_f16_ss(T_GRAM, d + step(kk), k + step(kk), kIdesc, kk > 0);
+                        for (int kk = 0; kk < DK / 16; ++kk) mma_f16_ss(T_GRAM, d + step(kk), d + step(kk), kIdesc, kk > 0);
                         mma_commit(bar(GRAM_FULL));
                     }
                     __syncwarp();
@@ -735,7 +741,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     chain_wait(UP_READY);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        const uint64_t d = smem_desc_mn_sw128(kq(c) + (uint32_t)(k_row(c) * 128), 2 * kTile);
+                        const uint64_t d = smem_desc_mn_sw128(kq(c), 2 * kTile);
 #pragma unroll
                         for (int kk = 0; kk < kTok / 16; ++kk)
 #pragma unroll
@@ -749,8 +755,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     chain_wait(U2_READY);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        with_tile(T_O, T_KS, 32, tp + 2 * kTile, false);
-                        with_tile(T_O, T_KS + 16, 32, tp + 2 * kTile, true);
+                        with_tile(T_O, T_KS, 16, tp + 2 * kTile, false);
+                        with_tile(T_O, T_KS + 8, 16, tp + 2 * kTile, true);
                         mma_commit(bar(TP_EMPTY + (c & 1)));
                         mma_commit(bar(O_FULL));   // (of the last chunk the last: the CTA ends after it)
                     }
@@ -781,14 +787,14 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll 1
             for (int c = 0; c <= chunks && ok; ++c) {
                 if (c < chunks) {
-                    const int st = c % kKqStages, left = s.n - c * kTok, kr = k_row(c) * 128, qr = q_row(c) * 128;
+                    const int st = c % kKqStages, left = s.n - c * kTok;
                     if (!wait_warp(KQ_EMPTY + st, free(c, kKqStages))) { ok = false; break; }
                     const uint32_t at = sbase + (uint32_t)(C::kKq + st * C::kKqBytes), to = left < kTok ? bar(TAIL) : bar(KQ_FULL + st);
                     if (lane == 0) {
                         mbar_arrive_expect_tx(to, kq_bytes);
                         for (int x = 0; x < NC; ++x) {
-                            tma_load_2d(at + 2 * x * kTile + (uint32_t)kr, &tmap_k, hk * DK + 64 * x, s.t0 + c * kTok, to);
-                            tma_load_2d(at + 2 * x * kTile + (uint32_t)qr, &tmap_q, hk * DK + 64 * x, s.t0 + c * kTok, to);
+                            tma_load_2d(at + 2 * x * kTile, &tmap_k, hk * DK + 64 * x, s.t0 + c * kTok, to);
+                            tma_load_2d(at + (2 * x + 1) * kTile, &tmap_q, hk * DK + 64 * x, s.t0 + c * kTok, to);
                         }
                     }
                     ++kqs;
@@ -796,7 +802,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     if (left < kTok) {
                         if (!wait_warp(TAIL, 0u)) { ok = false; break; }
 #pragma unroll 1
-                        for (int x = 0; x < NC; ++x) zero(smem + C::kKq + st * C::kKqBytes + 2 * x * kTile + kr, left, 128);
+                        for (int x = 0; x < NC; ++x) zero(smem + C::kKq + st * C::kKqBytes + 2 * x * kTile, left, 128);
                         fence_proxy_async_smem();
                         arrive(KQ_FULL + st);
                     }
@@ -895,7 +901,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     for (int i = lane; i < kTok; i += 32) {
                         float iq = 1.0f;
                         if (a.norm) {
-                            const unsigned char* at = smem + C::kKq + ks * C::kKqBytes + (q_row(c) + i) * 128;
+                            const unsigned char* at = smem + C::kKq + ks * C::kKqBytes + (kTok + i) * 128;
                             uint64_t q2 = 0, r2 = 0;
 #pragma unroll 1
                             for (int x = 0; x < NC; ++x, at += 2 * kTile)
