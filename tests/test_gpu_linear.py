@@ -272,8 +272,8 @@ def check_delta(inputs, scale, norm, before, after, out, sl, start, past=None, d
 
 
 @pytest.mark.parametrize("heads", HEADS)
-@pytest.mark.parametrize("lens", [[1], [1, 1, 1], [0, 3, 1], [5, 8, 0, 9], [16, 2], [17], [33, 64, 1, 0, 31], [200, 47],
-                                  [500]])
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1], [0, 3, 1], [5, 8, 0, 9], [16, 2], [17], [24, 1], [25], [33, 64, 1, 0, 31],
+                                  [128, 65, 63], [200, 47], [500]])
 @pytest.mark.parametrize("raw", [False, True])
 def test_delta(tern, heads, lens, raw):
     Hk, Hv, Dk, Dv = heads
@@ -315,7 +315,7 @@ def test_delta_extreme_gates(tern, n):
 def test_delta_negative_slots_shared_reads_and_no_tokens(tern):
     Hk, Hv, Dk, Dv = 1, 2, 64, 32
     g = gen(11)
-    for n in (1, 20):
+    for n in (1, 20, 40):
         inputs = delta_inputs(3 * n, Hk, Hv, Dk, Dv, g)
         pool = rand((5, Hv, Dv, Dk), g)
         state = pool.clone()
@@ -368,7 +368,7 @@ def test_states_past_2_to_the_31(tern):
     slots = [4200, 4150]
     state = torch.empty((4201, Hv, Dv, Dk), device="cuda")
     g = gen(14)
-    for n in (1, 20):
+    for n in (1, 70):
         inputs = delta_inputs(n, Hk, Hv, Dk, Dv, g)
         state[slots] = 0.1 * rand((2, Hv, Dv, Dk), g)
         before = f64(state[slots])
@@ -402,7 +402,7 @@ def test_another_stream_and_replays(tern):
     B, Hk, Hv, D = 3, 1, 2, 64
     C = (2 * Hk + Hv) * D
     side = torch.cuda.Stream()
-    for n in (1, 21):
+    for n in (1, 21, 75):
         T = B * n
         x, w = rand((T, C), g, torch.bfloat16), rand((C, 4), g)
         gates, nw = rand((T, 2, Hv), g), 1 + 0.1 * rand(D, g)
