@@ -75,7 +75,8 @@ EXPORTS = {
                            _I, _P, _P]),
     "tern_short_conv": (_I, [_P, _I, _LL, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "tern_gated_delta": (_I, [_P, _P, _P, _LL, _LL, _LL, _P, _LL, _P, _LL, _P, _P, _F, _I, _P, _I, _P, _P, _P, _P, _I,
-                              _I, _I, _I, _I, _I, _I, _P, _P]),
+                              _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "tern_gated_delta_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "tern_cache_evict": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P]),
 }
 
@@ -964,9 +965,13 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
         out = _new((T, Hv, Dv), bf16, q.device, stream)
     _covers(out=(out, T * Hv * Dv), a_log=(a_log, Hv), dt_bias=(dt_bias, Hv))
     sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new, now)
+    # (a few tokens take none: not asked for)
+    need = int(lib().tern_gated_delta_workspace_bytes(B, T, max_new if q_start is not None else T // B, Hv, Dk, Dv)) \
+        if T > 64 else 0
+    ws = _new((need,), torch.uint8, q.device, stream) if need else None
     _check("tern_gated_delta", lib().tern_gated_delta(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, g.data_ptr(), gs, beta.data_ptr(), bs,
         _opt(a_log, f32, "a_log", now), _opt(dt_bias, f32, "dt_bias", now), Dk ** -0.5 if scale is None else scale,
         1 if qk_norm else 0, _ptr(state, f32, "state", now), pool, sl, dl, pp, qp, B, T, max_new, Hk, Hv, Dk, Dv,
-        _ptr(out, bf16, "out", now), _stream(stream)))
+        _ptr(out, bf16, "out", now), None if ws is None else ws.data_ptr(), need, _stream(stream)))
     return out

@@ -93,7 +93,7 @@ tern_status tern_device_error(int* code) {
                                             read_attn_chunk_device_error, read_evict_device_error,
                                             read_norm_device_error, read_conv_device_error,
                                             read_delta_device_error,
-                                            read_delta_chunk_device_error};
+                                            read_delta_chunk_device_error, read_delta_join_device_error};
     for (auto* read : readers) {
         int c = 0;
         if (read(&c) != cudaSuccess) return TERN_ERR_CUDA;

@@ -46,6 +46,7 @@ cudaError_t read_norm_device_error(int* code);
 cudaError_t read_conv_device_error(int* code);
 cudaError_t read_delta_device_error(int* code);
 cudaError_t read_delta_chunk_device_error(int* code);
+cudaError_t read_delta_join_device_error(int* code);
 // One-CTA kernels that run a bounded wait nothing completes (tern_wait_selftest).
 cudaError_t launch_flag_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_mbar_wait_selftest(uint64_t limit_ns, cudaStream_t stream);

@@ -8,6 +8,8 @@
 // every state once and is bound by that.
 #include "tern_delta.cuh"
 
+#include <algorithm>
+
 namespace tern {
 namespace {
 
@@ -165,13 +167,56 @@ cudaError_t read_delta_device_error(int* code) {
 
 using namespace tern;
 
+namespace {
+// How many pieces the sequences go in: no more than let every CTA of them have an SM of its own
+// (a piece behind the first takes two, one for what it does to any state), and no more than
+// the root of the longest one's chunks, past which the steps from piece to piece take longer
+// than they save (8192 tokens of 2 heads: 11 pieces 111 us, 16 119; 4096: 8 pieces 81 us, 16 101).
+// From kPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 37.0
+// against 40.7 us, 2048 76 and 132, of 32 heads 38.4 and 40.8, 94 and 132, of 48 heads 38.9
+// and 41.1, 103 and 134; with 7 chunks the join takes what the pieces save.  The outputs of all
+// pieces but the first go through the workspace: calls that would need more than a gigabyte
+// of it go whole.
+constexpr int kPieceChunks = 8;
+constexpr size_t kMostWorkspace = (size_t)1 << 30;
+int delta_pieces(int B, int max_new, int v_heads, int dv, int sms) {
+    const int chunks = (max_new + kDeltaChunk - 1) / kDeltaChunk;
+    if (chunks < kPieceChunks) return 1;
+    const long long moves = (long long)B * v_heads, ctas = moves * ((dv + kDeltaRows - 1) / kDeltaRows);
+    const long long most = (sms + moves) / (ctas + moves);
+    int count = 1;
+    while (count < most && (long long)(count + 1) * (count + 1) <= chunks) ++count;
+    return count;
+}
+struct PieceSizes {
+    size_t state, move, parts, out, out_move;   // bytes
+    size_t all() const { return state + move + parts + out + out_move; }
+};
+PieceSizes piece_sizes(int count, int B, int T, int v_heads, int dk, int dv) {
+    const size_t heads = (size_t)B * v_heads, chunks = (size_t)delta_piece_chunk(count, T, B) * v_heads;
+    return {heads * count * dv * dk * 4, heads * (count - 1) * delta_parts_bytes(dk, dk),
+            heads * ((dv + kDeltaRows - 1) / kDeltaRows) * (count - 1) * delta_parts_bytes(kDeltaRows, dk), chunks * dv * kDeltaChunk * 4,
+            chunks * delta_parts_bytes(kDeltaChunk, dk)};
+}
+}  // namespace
+
+extern "C" size_t tern_gated_delta_workspace_bytes(int B, int T, int max_new, int v_heads, int dk, int dv) {
+    int sms = 0;
+    if (B < 1 || B > 65535 || T < 1 || max_new < 0 || v_heads < 1 || v_heads > 65535 || (dk != 64 && dk != 128) || dv < 16 ||
+        dv % 16 != 0 || dv > 256 || check_device(&sms) != TERN_OK)
+        return 0;
+    const int count = delta_pieces(B, std::min(max_new, T), v_heads, dv, sms);
+    const size_t bytes = count > 1 ? piece_sizes(count, B, T, v_heads, dk, dv).all() : 0;
+    return bytes <= kMostWorkspace ? bytes : 0;
+}
+
 extern "C" tern_status tern_gated_delta(const void* q, const void* k, const void* v, long long q_token,
                                         long long k_token, long long v_token, const float* g, long long g_token,
                                         const float* beta, long long beta_token, const float* a_log,
                                         const float* dt_bias, float scale, int qk_norm, float* state, int pool,
                                         const int* slots, const int* dst_slots, const int* past, const int* q_start,
                                         int B, int T, int max_new, int k_heads, int v_heads, int dk, int dv, void* out,
-                                        tern_stream_t stream) {
+                                        void* workspace, size_t workspace_bytes, tern_stream_t stream) {
     set_launch_count(0);
     DeltaArgs a;
     tern_status st = make_state_seq_view(q_start, slots, dst_slots, past, B, T, max_new, pool, &a.s);
@@ -186,11 +231,24 @@ extern "C" tern_status tern_gated_delta(const void* q, const void* k, const void
             return TERN_ERR_SHAPE;
     if (!state || (!a_log) != (!dt_bias) || (T > 0 && (!q || !k || !v || !g || !beta || !out))) return TERN_ERR_NULL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(out) || !aligned_to(g, 4) ||
-        !aligned_to(beta, 4) || !aligned_to(a_log, 4) || !aligned_to(dt_bias, 4))
+        !aligned_to(beta, 4) || !aligned_to(a_log, 4) || !aligned_to(dt_bias, 4) || !aligned_to(workspace, 256))
         return TERN_ERR_ALIGN;
     int sms = 0;
     st = check_device(&sms);
     if (st != TERN_OK) return st;
+    a.p = DeltaPieces{1, nullptr, nullptr, nullptr, nullptr, nullptr};
+    const size_t need = workspace ? tern_gated_delta_workspace_bytes(B, T, a.s.max_new, v_heads, dk, dv) : 0;
+    if (workspace_bytes < need) return TERN_ERR_WORKSPACE;
+    if (need > 0) {
+        a.p.count = delta_pieces(B, a.s.max_new, v_heads, dv, sms);
+        const PieceSizes sizes = piece_sizes(a.p.count, B, T, v_heads, dk, dv);
+        unsigned char* at = static_cast<unsigned char*>(workspace);
+        a.p.state = reinterpret_cast<float*>(at);
+        a.p.move = at += sizes.state;
+        a.p.parts = at += sizes.move;
+        a.p.out = reinterpret_cast<float*>(at += sizes.parts);
+        a.p.out_move = at + sizes.out;
+    }
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.k = static_cast<const __nv_bfloat16*>(k);
     a.v = static_cast<const __nv_bfloat16*>(v);
@@ -212,9 +270,10 @@ extern "C" tern_status tern_gated_delta(const void* q, const void* k, const void
     a.group = v_heads / k_heads;
     a.norm = qk_norm;
     a.scale = scale;
-    const cudaError_t e = a.s.max_new > kStepTokens ? launch_delta_chunk(a, (cudaStream_t)stream)
-                                                    : launch_delta_step(a, (cudaStream_t)stream);
+    cudaError_t e = a.s.max_new > kStepTokens ? launch_delta_chunk(a, (cudaStream_t)stream)
+                                              : launch_delta_step(a, (cudaStream_t)stream);
+    if (e == cudaSuccess && a.p.count > 1) e = launch_delta_join(a, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return TERN_ERR_CUDA;
-    set_launch_count(1);
+    set_launch_count(a.p.count == 1 ? 1 : a.p.count == 2 ? 2 : 3);
     return TERN_OK;
 }

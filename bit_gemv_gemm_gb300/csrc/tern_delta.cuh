@@ -5,6 +5,23 @@
 
 namespace tern {
 
+// A sequence's chunks in `count` pieces of equal length, each run at once with the others
+// from S = 0 (the first from the sequence's own): what it makes of S = 0 and, rows of the
+// unit matrix in place of S's and no v, what it does to any S.  By linearity
+//   S after it = S M + B,  out = S out_move + out,
+// which the join kernels make of the arrays here.
+struct DeltaPieces {
+    int count;
+    float* state;            // [B][v_heads][count][dv][dk] fp32: B of each piece (the first: S after it)
+    unsigned char* move;     // [B][v_heads][count - 1]: parts of M of each but the first, dk rows
+    unsigned char* parts;    // [B][v_heads][128 rows][count - 1]: parts of S after each but the last, 128 rows
+    float* out;              // [chunks behind first pieces][v_heads][128 rows][64 tokens][rows] fp32
+    unsigned char* out_move; // [chunks][v_heads]: parts of it, 64 rows
+};
+// Two parts of a matrix of dk columns, each in tiles of 64 columns with 128-byte swizzled rows.
+__host__ __device__ constexpr uint32_t delta_parts_bytes(int rows, int dk) { return 4u * (uint32_t)rows * (uint32_t)dk; }
+constexpr int kDeltaChunk = 64, kDeltaRows = 128;
+
 struct DeltaArgs {
     StateSeqView s;
     const __nv_bfloat16 *q, *k, *v;
@@ -16,9 +33,47 @@ struct DeltaArgs {
     __nv_bfloat16* out;                     // [T][v_heads][dv]
     int k_heads, v_heads, dk, dv, group, norm;
     float scale;
+    DeltaPieces p;
 };
 
 constexpr float kDeltaNormEps = 1e-6f;
+
+// The chunks of a piece of a sequence of n tokens; a sequence of one chunk has one piece.
+__device__ __forceinline__ int delta_piece_chunks(const DeltaPieces& p, int n) {
+    const int chunks = (n + kDeltaChunk - 1) / kDeltaChunk;
+    return (chunks + p.count - 1) / p.count;
+}
+// Where in out and out_move sequence b's chunks behind its first piece begin.  Of its n tokens
+// they are fewer than n (count - 1) / (64 count) + 1: sequences in a row stay apart, the last
+// ends at (T - T / count) / 64 + 2 B at most.
+__host__ __device__ inline long long delta_piece_chunk(int count, int t0, int b) {
+    return (t0 - t0 / count) / kDeltaChunk + 2LL * b;
+}
+// a - a bf16 pair
+__device__ __forceinline__ uint64_t less_bf16(uint64_t a, uint32_t b) {
+    return fma2(pack2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), pack2(-1.0f, -1.0f), a);
+}
+// Two neighbours as a bf16 pair and what it leaves of them as another.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(a, b);
+    float x, y;
+    unpack2(less_bf16(pack2(a, b), hi), x, y);
+    lo = pack_bf16(x, y);
+}
+
+// Where the parts of S after a piece lie, of rows 128 `tile` on of `tiles` such.
+__device__ __forceinline__ unsigned char* delta_parts(const DeltaPieces& p, int b, int v_heads, int h, int dk, int tiles, int tile, int piece) {
+    return p.parts + ((((long long)b * v_heads + h) * tiles + tile) * (p.count - 1) + piece) * (long long)delta_parts_bytes(kDeltaRows, dk);
+}
+// Stores 8 neighbours of a row from column `col` on as parts.
+__device__ __forceinline__ void put_parts8(unsigned char* parts, int rows, int dk, int row, int col, const float* v) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(v[2 * e], v[2 * e + 1], hi[e], lo[e]);
+    unsigned char* at = parts + col / 64 * (rows * 128) + row * 128 + ((col % 64 / 8 ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + rows * dk * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
 
 // The gates of one token and value head as they lie in memory...
 __device__ __forceinline__ float2 delta_raw_gates(const DeltaArgs& a, long long token, int h) {
@@ -44,7 +99,35 @@ __device__ __forceinline__ float2 delta_gates(const DeltaHead& head, float2 raw)
     return make_float2(g < -200.0f ? -200.0f : g, b);
 }
 
+constexpr uint32_t kDeltaTries = 1u << 19, kDeltaNap = 2000;   // of a wait, and ns of each: a second, far beyond any real one
+// A thread's and a warp's wait, which give up after a number of tries.  (Short: some forty
+// of them stand in loops whose code has to stay in the instruction cache, and asking the
+// time takes longer than most of them.  Every lane asks; one for all made the others wait
+// longer.)
+__device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity) {
+    uint32_t ok = 0;
+#pragma unroll 1
+    for (uint32_t n = kDeltaTries; !ok && n > 0; --n)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kDeltaNap)
+            : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_tries(bar, parity));
+}
+// One lane of a warp whose lanes all come here: what it alone then does is known to be
+// done by one, and its operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e != 0;
+}
+
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_chunk(const DeltaArgs& a, cudaStream_t stream);
+cudaError_t launch_delta_join(const DeltaArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace tern

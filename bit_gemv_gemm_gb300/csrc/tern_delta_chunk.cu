@@ -37,12 +37,11 @@ using namespace sm100;
 
 __device__ int g_delta_chunk_error;
 
-constexpr int kTok = 64, kRows = 128;                 // tokens of a chunk, rows of S
+constexpr int kTok = kDeltaChunk, kRows = kDeltaRows;                 // tokens of a chunk, rows of S
 constexpr int kKqStages = 3, kVStages = 2, kCoefStages = 4, kTpStages = 2, kAStages = 2;
 constexpr uint32_t kTile = kTok * 128;                // bytes of a [64][64] bf16 tile, 128-byte swizzled rows
 constexpr uint32_t kATile = kTok * 64;                // of a part of A below its diagonal blocks: a_at()
 constexpr int kDiagRow = 20, kDiagBlock = 16 * kDiagRow + 16;   // floats of a column and of a block of -A's diagonal blocks
-constexpr uint32_t kDeltaTries = 1u << 19, kDeltaNap = 2000;   // of a wait, and ns of each: a second, far beyond any real one
 
 // What one chunk's tokens are scaled by.
 struct alignas(16) Coef {
@@ -99,46 +98,19 @@ __device__ __forceinline__ int bar_count(int i) {
     return 1;
 }
 
-// A warp's wait, which gives up after a number of tries.  (Short: some forty of them
-// stand in loops whose code has to stay in the instruction cache.  Every lane asks; one
-// for all made the others wait longer.)
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-    uint32_t ok = 0;
-#pragma unroll 1
-    for (uint32_t n = kDeltaTries; !ok && n > 0; --n)
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(kDeltaNap)
-            : "memory");
-    return __all_sync(0xffffffffu, ok);
-}
-// One lane of a warp whose lanes all come here: what it alone then does is known to be
-// done by one, and its operands stay in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
-    return e != 0;
-}
-// a - a bf16 pair
-__device__ __forceinline__ uint64_t less_bf16(uint64_t a, uint32_t b) {
-    return fma2(pack2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), pack2(-1.0f, -1.0f), a);
-}
-// Two neighbours as a bf16 pair and what it leaves of them as another.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(a, b);
-    float x, y;
-    unpack2(less_bf16(pack2(a, b), hi), x, y);
-    lo = pack_bf16(x, y);
-}
-
-// A 16-byte unit of a row of a [64][64] bf16 tile with 128-byte swizzled rows.
+// A 16-byte unit of a row of a tile of 64 bf16 a row with 128-byte swizzled rows.
 __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int row, int unit) {
     return tile + (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldsm2_t(uint32_t& a, uint32_t& b, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
@@ -148,12 +120,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -266,7 +232,7 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-template <int DK>
+template <int DK, bool PIECES>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_out,
@@ -306,7 +272,19 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     pdl_wait();
 
     const int h = blockIdx.x % a.v_heads, row0 = blockIdx.x / a.v_heads * kRows, hk = h / a.group;
-    const StateSeq s = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
+    StateSeq s = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
+    // this CTA's piece, whether it has the unit matrix in place of S, its rows
+    int piece = 0, rows = a.dv;
+    bool moves = false;
+    if constexpr (PIECES) {
+        const int z = blockIdx.z, per = delta_piece_chunks(a.p, s.n) * kTok;
+        moves = z >= a.p.count;
+        piece = moves ? z - a.p.count + 1 : z;
+        if (moves) rows = DK;
+        const int n = row0 < rows ? min(s.n - piece * per, per) : 0;
+        s.t0 += piece * per;
+        s.n = max(n, 0);
+    }
     const int chunks = (s.n + kTok - 1) / kTok;
     auto fail = [&] { report_device_error(&g_delta_chunk_error, TERN_DEVERR_DELTA_WAIT); };
     auto wait_warp = [&](int b, uint32_t parity) { return tern::wait_warp(bar(b), parity); };
@@ -322,11 +300,14 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // ------------------------------ the chain ------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
         const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;   // of S's columns and of a chunk's tokens
-        const bool live = row0 + row < a.dv;
+        const bool live = row0 + row < rows;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = mine + T_S + (uint32_t)(COLS * quarter), tk = mine + T_KS + 16u * quarter;
         float S[COLS];
-        {
+        if (piece > 0) {
+#pragma unroll
+            for (int i = 0; i < COLS; ++i) S[i] = moves && COLS * quarter + i == row ? 1.0f : 0.0f;
+        } else {
             const float4* from = reinterpret_cast<const float4*>(
                 a.state + (((long long)s.src * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * quarter);
 #pragma unroll
@@ -379,10 +360,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const Coef& k = coefs[c % kCoefStages];
             next_state(c - 1, true);
             need(TP_FULL + (c & 1), full(c, kTpStages));
+            float x[16];
             need(V_FULL + c % kVStages, full(c, kVStages));
             const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
                 smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) + quarter * (16 * 64)) + lane;
-            float x[16];
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const ulonglong2 beta = *reinterpret_cast<const ulonglong2*>(&k.beta[16 * quarter + i]);
@@ -446,19 +427,46 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (chunks > 0) next_state(chunks - 1, false);
         if (!ok) {
             if (lane == 0) fail();
-        } else if (s.dst >= 0 && live && (s.n > 0 || s.dst != s.src)) {
-            float4* to = reinterpret_cast<float4*>(
-                a.state + (((long long)s.dst * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * quarter);
+        }
+        // S goes to the pool, or to where the join finds it: a sequence of more than one piece
+        float* to_head = s.dst >= 0 && (s.n > 0 || s.dst != s.src) ? a.state + ((long long)s.dst * a.v_heads + h) * a.dv * DK : nullptr;
+        unsigned char* parts = nullptr;
+        if constexpr (PIECES) {
+            const int all = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error).n;
+            if (all > delta_piece_chunks(a.p, all) * kTok) {
+                const long long at = (long long)blockIdx.y * a.v_heads + h;
+                to_head = a.p.state + (at * a.p.count + piece) * ((long long)a.dv * DK);
+                if (piece == 0) parts = delta_parts(a.p, blockIdx.y, a.v_heads, h, DK, (a.dv + kRows - 1) / kRows, row0 / kRows, 0);
+                if (moves) parts = a.p.move + (at * (a.p.count - 1) + piece - 1) * delta_parts_bytes(DK, DK);
+            }
+            if (piece > 0 && s.n == 0) to_head = nullptr;
+        }
+        if (ok && live && to_head) {
+            float4* to = reinterpret_cast<float4*>(to_head + (row0 + row) * DK + COLS * quarter);
+            if (!moves) {
 #pragma unroll
-            for (int i = 0; i < COLS / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+                for (int i = 0; i < COLS / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            }
+            if (PIECES && parts) {
+#pragma unroll
+                for (int i = 0; i < COLS; i += 8) put_parts8(parts, moves ? DK : kRows, DK, row, COLS * quarter + i, S + i);
+            }
         }
         __syncwarp();
     } else if (warp < kGramWarp) {
         // ------------------------------ the output ------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int quad = warp - kOutWarp, row = quad * 32 + lane;
-        const bool live = row0 + row < a.dv;
+        const bool live = row0 + row < rows;
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16);
+        unsigned char* piece_out = nullptr;   // this thread's place in the piece's outputs
+        if (PIECES && piece > 0) {
+            const StateSeq whole = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
+            const long long first = delta_piece_chunk(a.p.count, whole.t0, blockIdx.y) + (piece - 1) * delta_piece_chunks(a.p, whole.n);
+            piece_out = moves ? a.p.out_move + row / 64 * (kTok * 128) + 2 * (row & 7)
+                              : reinterpret_cast<unsigned char*>(a.p.out + row);
+            piece_out += ((first * a.v_heads + h) * rows + row0) * (long long)(kTok * 4);
+        }
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
@@ -477,6 +485,38 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (t == kTok - 16) {
                     tc_fence_before();
                     arrive(O_EMPTY);
+                }
+                if (PIECES && piece > 0) {
+                    // (a row over the lanes a store: 16 bytes of a row of tokens a lane took 14 us more of 82)
+                    unsigned char* const tile = piece_out + (long long)c * a.v_heads * rows * (kTok * 4);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&k.near_q[t + i]);
+                        const float m[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[i + e] = __float_as_uint(fmaf(m[e], __uint_as_float(x[i + e]), __uint_as_float(y[i + e])));
+                    }
+                    if (!live) continue;
+                    if (moves) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            uint32_t hi, lo;
+                            split2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), hi, lo);
+                            unsigned char* to = tile + (t + i) * 128;
+                            const int u0 = (row % 64 / 8 ^ (i & 7)) << 4, u1 = ((row % 64 / 8 ^ (i & 7) ^ 1) << 4) + 128;
+                            *reinterpret_cast<unsigned short*>(to + u0) = (unsigned short)hi;
+                            *reinterpret_cast<unsigned short*>(to + u1) = (unsigned short)(hi >> 16);
+                            *reinterpret_cast<unsigned short*>(to + u0 + DK * 128) = (unsigned short)lo;
+                            *reinterpret_cast<unsigned short*>(to + u1 + DK * 128) = (unsigned short)(lo >> 16);
+                        }
+                    } else {
+                        const int width = min(kRows, rows - row0);
+                        float* to = reinterpret_cast<float*>(tile) + t * width;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) to[i * width] = __uint_as_float(x[i]);
+                    }
+                    continue;
                 }
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {   // (all read before anything is stored)
@@ -497,7 +537,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 }
             }
             const int first = c * kTok, n = s.n - first;
-            if (n >= kTok) {
+            if (PIECES && piece > 0) {
+                arrive(V_EMPTY + c % kVStages);
+            } else if (n >= kTok) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -816,6 +858,14 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (c > 0) {
                     const int b = c - 1, st = b % kVStages, left = s.n - b * kTok;
                     if (!wait_warp(V_EMPTY + st, free(b, kVStages))) { ok = false; break; }
+                    if (moves) {   // no v (and nothing else is put in its place)
+                        if (b < kVStages) {
+#pragma unroll 1
+                            for (int x = 0; x < 4; ++x) zero(smem + C::kV + st * C::kVBytes + x * kTok * 64, 0, 64);
+                        }
+                        arrive(V_FULL + st);
+                        continue;
+                    }
                     const uint32_t at = sbase + (uint32_t)(C::kV + st * C::kVBytes), to = left < kTok ? bar(TAIL) : bar(V_FULL + st);
                     if (lane == 0) {
                         mbar_arrive_expect_tx(to, v_bytes);
@@ -977,16 +1027,16 @@ cudaError_t launch(const DeltaArgs& a, cudaStream_t stream) {
         !make_token_map(&mk, a.k, a.k_token, a.k_heads * DK, a.s.T, 64) ||
         !make_token_map(&mv, a.v, a.v_token, a.v_heads * a.dv, a.s.T, 32) || !make_out_map(&mo, a.out, a.v_heads, a.dv, a.s.T))
         return cudaErrorInvalidValue;
-    static bool attr_set[64] = {};
+    auto kernel = a.p.count > 1 ? delta_chunk_kernel<DK, true> : delta_chunk_kernel<DK, false>;
+    static bool attr_set[64][2] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(delta_chunk_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (!attr_set[dev][a.p.count > 1]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
         if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
+        attr_set[dev][a.p.count > 1] = true;
     }
-    return launch_pdl(delta_chunk_kernel<DK>, dim3((unsigned)((a.dv + kRows - 1) / kRows * a.v_heads), (unsigned)a.s.B),
+    return launch_pdl(kernel, dim3((unsigned)((a.dv + kRows - 1) / kRows * a.v_heads), (unsigned)a.s.B, (unsigned)(2 * a.p.count - 1)),
                       dim3(kThreads), C::kSmem, stream, true, mq, mk, mv, mo, a);
 }
 

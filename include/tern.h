@@ -534,8 +534,9 @@ tern_status tern_cache_evict(const void *k_cache, const void *v_cache, const ter
 /* not fit are reported through tern_device_error (CACHE_SEQUENCE,         */
 /* STATE_SLOT), never followed out of bounds; a bad slot is neither read   */
 /* nor written.  Every array is memory of the current device; nothing is   */
-/* read before the previous kernel on the stream has finished.  One kernel */
-/* launch, no workspace, no atomics: a result does not vary from run to run. */
+/* read before the previous kernel on the stream has finished.  Outputs    */
+/* overlap no input (but as tern_rms_norm says), nor the state.  No        */
+/* atomics: a result does not vary from run to run.                        */
 /* ---------------------------------------------------------------------- */
 
 /* Norms of T x heads rows of dim values, fused with the residual stream and a gate:
@@ -582,13 +583,22 @@ tern_status tern_short_conv(const void *x, int x_is_f32, long long x_token, cons
  *   g <- -exp(a_log) * softplus(g + dt_bias),  beta <- 1 / (1 + exp(-beta)).
  * qk_norm != 0: q and k are divided by sqrt(sum of squares + 1e-6).  out bf16
  * [T][v_heads][dv].  The state and all sums are fp32; out is rounded once.
- * dk 64 or 128, dv a multiple of 16, at most 256; |scale| finite (TERN_ERR_SHAPE). */
+ * dk 64 or 128, dv a multiple of 16, at most 256; |scale| finite (TERN_ERR_SHAPE).
+ * Sequences of more than 24 tokens (max_new) go 64 tokens at a time, where the state and
+ * what is taken to it are two bf16 values each in the products (2^-17 of a value) and the
+ * weights of a chunk's own tokens one (2^-8 of their part of out); there a value that is
+ * not finite may also reach the tokens up to 63 before it in its sequence.
+ * workspace: NULL, or tern_gated_delta_workspace_bytes(B, T, max_new, v_heads, dk, dv)
+ * bytes (max_new T / B without q_start; TERN_ERR_WORKSPACE if it is smaller), 256-byte
+ * aligned, any contents: with it, few heads of long sequences go in pieces at once (one
+ * of 2048 tokens and 32 heads of 128 x 128: 94 us, not 132).  0 bytes: none of use. */
+size_t tern_gated_delta_workspace_bytes(int B, int T, int max_new, int v_heads, int dk, int dv);
 tern_status tern_gated_delta(const void *q, const void *k, const void *v, long long q_token, long long k_token,
                              long long v_token, const float *g, long long g_token, const float *beta,
                              long long beta_token, const float *a_log, const float *dt_bias, float scale, int qk_norm,
                              float *state, int pool, const int *slots, const int *dst_slots, const int *past,
                              const int *q_start, int B, int T, int max_new, int k_heads, int v_heads, int dk, int dv,
-                             void *out, tern_stream_t stream);
+                             void *out, void *workspace, size_t workspace_bytes, tern_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */

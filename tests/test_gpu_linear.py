@@ -273,7 +273,7 @@ def check_delta(inputs, scale, norm, before, after, out, sl, start, past=None, d
 
 @pytest.mark.parametrize("heads", HEADS)
 @pytest.mark.parametrize("lens", [[1], [1, 1, 1], [0, 3, 1], [5, 8, 0, 9], [16, 2], [17], [24, 1], [25], [33, 64, 1, 0, 31],
-                                  [128, 65, 63], [200, 47], [500]])
+                                  [128, 65, 63], [200, 47], [500], [64, 1100, 0, 513, 300], [1800]])
 @pytest.mark.parametrize("raw", [False, True])
 def test_delta(tern, heads, lens, raw):
     Hk, Hv, Dk, Dv = heads
@@ -296,7 +296,46 @@ def test_delta(tern, heads, lens, raw):
                     np.full(out.shape, 7.0))
 
 
-@pytest.mark.parametrize("n", [1, 6, 70])
+def delta_call(tern, inputs, scale, state, sl, start, max_new, ws_bytes):
+    """The C entry point with a workspace of `ws_bytes` bytes (0: none); its status and output."""
+    q, k, v, g, b, al, dt = inputs
+    B, T, (pool, Hv, Dv, Dk), at, first = len(sl), q.shape[0], state.shape, i32(sl), i32(start)
+    out = torch.full((T, Hv, Dv), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((max(ws_bytes, 1),), 0xFF, dtype=torch.uint8, device="cuda")     # (not a number, wherever it is read)
+    status = tern.lib().tern_gated_delta(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0), v.stride(0), g.data_ptr(), g.stride(0),
+        b.data_ptr(), b.stride(0), None if al is None else al.data_ptr(), None if dt is None else dt.data_ptr(), scale, 1,
+        state.data_ptr(), pool, at.data_ptr(), None, None, first.data_ptr(), B, T, max_new, q.shape[1], Hv, Dk, Dv,
+        out.data_ptr(), ws.data_ptr() if ws_bytes else None, ws_bytes, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    return status, out
+
+
+# the most pieces of each: 11, 2 (the root), 2 and 3 (the SMs), as many rows of S as two tiles have, one head alone
+@pytest.mark.parametrize("heads,lens", [((1, 1, 64, 16), [8192]), ((1, 2, 128, 128), [512, 3, 0, 511]),
+                                        ((5, 15, 64, 96), [700, 65, 640]), ((4, 24, 128, 128), [64 * 17 + 1]),
+                                        ((1, 7, 128, 256), [1300, 64]), ((2, 6, 128, 176), [1024, 1025]),
+                                        ((1, 40, 64, 64), [577])])
+def test_delta_in_pieces_and_whole(tern, heads, lens):
+    Hk, Hv, Dk, Dv = heads
+    g = gen(21)
+    T, B = sum(lens), len(lens)
+    start, sl = sequences(lens)[0], list(range(B, 0, -1))
+    inputs = delta_inputs(T, Hk, Hv, Dk, Dv, g)
+    pool = rand((B + 1, Hv, Dv, Dk), g)
+    need = tern.lib().tern_gated_delta_workspace_bytes(B, T, max(lens), Hv, Dk, Dv)
+    assert need > 0 and need % 256 == 0
+    assert tern.lib().tern_gated_delta_workspace_bytes(B, T, 448, Hv, Dk, Dv) == 0      # too short
+    for ws in (need, 0):
+        state = pool.clone()
+        status, out = delta_call(tern, inputs, Dk ** -0.5, state, sl, start, max(lens), ws)
+        assert status == 0 and tern.lib().tern_last_launch_count() in ((2, 3) if ws else (1,))
+        assert tern.device_error() == 0
+        check_delta(inputs, Dk ** -0.5, True, f64(pool), state, out, sl, start)
+    assert delta_call(tern, inputs, Dk ** -0.5, pool.clone(), sl, start, max(lens), need - 256)[0] == 4
+
+
+@pytest.mark.parametrize("n", [1, 6, 70, 640])
 def test_delta_extreme_gates(tern, n):
     """Decays of 0 (-inf, far below fp32's least), of 1, steps of 0 and 1, in one sequence."""
     Hk, Hv, Dk, Dv = 1, 2, 128, 32
@@ -315,7 +354,7 @@ def test_delta_extreme_gates(tern, n):
 def test_delta_negative_slots_shared_reads_and_no_tokens(tern):
     Hk, Hv, Dk, Dv = 1, 2, 64, 32
     g = gen(11)
-    for n in (1, 20, 40):
+    for n in (1, 20, 40, 600):
         inputs = delta_inputs(3 * n, Hk, Hv, Dk, Dv, g)
         pool = rand((5, Hv, Dv, Dk), g)
         state = pool.clone()
@@ -342,7 +381,7 @@ def test_delta_in_one_piece_and_in_several(tern):
         check_delta(inputs, 128 ** -0.5, True, f64(pool), state, torch.cat(outs), [0], [0, 150])
 
 
-@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("n", [1, 40, 600])
 def test_delta_reports_bad_values(tern, n):
     Hk, Hv, Dk, Dv = 1, 2, 64, 32
     g = gen(13)
@@ -368,7 +407,7 @@ def test_states_past_2_to_the_31(tern):
     slots = [4200, 4150]
     state = torch.empty((4201, Hv, Dv, Dk), device="cuda")
     g = gen(14)
-    for n in (1, 70):
+    for n in (1, 70, 600):
         inputs = delta_inputs(n, Hk, Hv, Dk, Dv, g)
         state[slots] = 0.1 * rand((2, Hv, Dv, Dk), g)
         before = f64(state[slots])
@@ -380,7 +419,7 @@ def test_states_past_2_to_the_31(tern):
 def test_one_head_alone(tern):
     """NaN in one sequence's values, state and gates: the other sequences and heads stay as they were."""
     heads = (1, 2, 64, 32)
-    for n in (1, 45):
+    for n in (1, 45, 600):
         g = gen(15)
         inputs = [t if t is None else t.clone() for t in delta_inputs(3 * n, *heads, g)]
         pool = rand((3, 2, 32, 64), g)
@@ -402,7 +441,7 @@ def test_another_stream_and_replays(tern):
     B, Hk, Hv, D = 3, 1, 2, 64
     C = (2 * Hk + Hv) * D
     side = torch.cuda.Stream()
-    for n in (1, 21, 75):
+    for n in (1, 21, 75, 600):
         T = B * n
         x, w = rand((T, C), g, torch.bfloat16), rand((C, 4), g)
         gates, nw = rand((T, 2, Hv), g), 1 + 0.1 * rand(D, g)

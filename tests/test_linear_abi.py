@@ -55,7 +55,8 @@ def test_conv_refuses(tern, bad, code):
 
 def delta(tern, **k):
     a = dict(q=P, k=P, v=P, qt=256, kt=256, vt=512, g=P, gt=4, beta=P, bt=4, al=P, dt=P, scale=0.1, norm=1, state=P,
-             pool=5, slots=P, dst=P, past=P, start=P, B=2, T=4, max_new=3, hk=2, hv=4, dk=128, dv=128, out=P, stream=None)
+             pool=5, slots=P, dst=P, past=P, start=P, B=2, T=4, max_new=3, hk=2, hv=4, dk=128, dv=128, out=P, ws=None, ws_bytes=0,
+             stream=None)
     assert set(k) <= set(a)
     return tern.lib().tern_gated_delta(*{**a, **k}.values())
 
@@ -70,9 +71,16 @@ def delta(tern, **k):
     (dict(state=None), NULL), (dict(q=None), NULL), (dict(v=None), NULL), (dict(g=None), NULL), (dict(out=None), NULL),
     (dict(slots=None), NULL), (dict(q=P + 8), ALIGN), (dict(k=P + 2), ALIGN), (dict(v=P + 8), ALIGN),
     (dict(state=P + 8), ALIGN), (dict(out=P + 2), ALIGN), (dict(g=P + 2), ALIGN), (dict(al=P + 1), ALIGN),
-    (dict(start=P + 1), ALIGN)])
+    (dict(start=P + 1), ALIGN), (dict(ws=P + 128, ws_bytes=1 << 20), ALIGN)])
 def test_delta_refuses(tern, bad, code):
     assert delta(tern, **bad) == code
+
+
+@pytest.mark.parametrize("bad", [(0, 4096, 4096, 8, 128, 128), (1, -1, 4096, 8, 128, 128), (1, 4096, -1, 8, 128, 128),
+                                 (1, 4096, 4096, 0, 128, 128), (1, 4096, 4096, 8, 96, 128), (1, 4096, 4096, 8, 128, 272),
+                                 (1, 4096, 4096, 8, 128, 24), (1, 4096, 24, 8, 128, 128), (1, 64, 4096, 8, 128, 128)])
+def test_delta_workspace_of_nothing(tern, bad):
+    assert tern.lib().tern_gated_delta_workspace_bytes(*bad) == 0
 
 
 # --- the binding (CPU tensors: shapes first, then the device) ---
