@@ -5,7 +5,11 @@
 // per value head, S [dv][dk] in 32 bits.  A CTA owns some rows of one head's S,
 // which depend on one another's only through q and k: they stay in registers
 // from the first token to the last, so a call of a few tokens reads and writes
-// every state once and is bound by that.
+// every state once and is bound by that: one token of 64 sequences of 48 heads of 128 x 128
+// 61.2 us, 97 % of the copy bandwidth.  Each token more costs a CTA some 0.8 us of products
+// and of sums over the 8 lanes that share a row: five of 8 sequences of 32 heads 10.0 us, of
+// which 6.2 are the states'.  (Products by pairs, fewer sums and 16 rows a warp in place of
+// 8 each change that by 5 % at most, and lose as much where few CTAs run.)
 #include "tern_delta.cuh"
 
 #include <algorithm>

@@ -9,7 +9,8 @@ does to y passes through an activation whose slope is at most 1.1, and whose own
 relative error is 2^-16 from the exponential.  The delta rule: with R the
 largest row of S plus the largest |v|, a token adds errors of at most 2^-17 R to
 a row (two dot products of Dk <= 128 terms, an update; in the chunk form the
-same products with their operands in parts that carry 2^-24), decays shrink them and the
+same products, and those from piece to piece, with operands in parts that carry 2^-17
+of each factor), decays shrink them and the
 correction does not grow them (|k| <= 1, beta <= 1), so a row of the final state is
 off by at most `memory` 2^-17 R, `memory` the largest sum of what the decays
 leave.  out reads that with |q| <= 1, and in the chunk form adds products of
@@ -106,6 +107,25 @@ def test_norm_sizes(tern, T, heads, D, kinds):
     out = tern.rms_norm(x, w, residual=r, scale=-0.5, gate=z, gate_act="sigmoid", weight_offset=1.0, after=True)
     assert out.dtype == kind
     check_norm(tern, x, w, out, r, -0.5, z, "sigmoid", 1.0, True)
+
+
+@pytest.mark.parametrize("T,heads,D", [(41, 3, 128), (23, 2, 48), (11, 1, 400), (330, 1, 1288), (310, 1, 2568), (307, 1, 8200)])
+@pytest.mark.parametrize("residual", [None, "f32", "bf16"])
+@pytest.mark.parametrize("gate", [None, "f32", "bf16"])
+def test_norm_types(tern, T, heads, D, residual, gate):
+    """Every mix of types, before and after a block, the new residual over the old."""
+    g = gen(T + D)
+    w, z = 1 + 0.3 * rand(D, g), None if gate is None else rand((T, heads, D), g, KINDS[gate])
+    for xk in KINDS.values():
+        for ok in KINDS.values():
+            x, r = rand((T, heads, D), g, xk), None if residual is None else 3 * rand((T, heads, D), g, KINDS[residual])
+            was = None if r is None else f64(r)
+            out = tern.rms_norm(x, w, residual=r, scale=0.5, gate=z, after=True, out_dtype=ok)
+            assert out.dtype == ok
+            check_norm(tern, x, w, out, r, 0.5, z, after=True)
+            out = tern.rms_norm(x, w, residual=r, scale=1.0 if r is None else 0.5, gate=z, residual_out=r, out_dtype=ok)
+            check_norm(tern, x, w, out, None, 1.0 if r is None else 0.5, z, res_out=r, residual_was=was)
+    assert tern.device_error() == 0
 
 
 def test_norm_in_place_strided_and_mixed(tern):
