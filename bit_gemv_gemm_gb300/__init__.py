@@ -966,7 +966,7 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     _covers(out=(out, T * Hv * Dv), a_log=(a_log, Hv), dt_bias=(dt_bias, Hv))
     sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new, now)
     # (a few tokens take none: not asked for)
-    need = int(lib().tern_gated_delta_workspace_bytes(B, T, max_new if q_start is not None else T // B, Hv, Dk, Dv)) \
+    need = int(lib().tern_gated_delta_workspace_bytes(B, T, max_new if q_start is not None else T // max(B, 1), Hv, Dk, Dv)) \
         if T > 64 else 0
     ws = _new((need,), torch.uint8, q.device, stream) if need else None
     _check("tern_gated_delta", lib().tern_gated_delta(

@@ -176,16 +176,15 @@ namespace {
 // (a piece behind the first takes two, one for what it does to any state), and no more than
 // the root of the longest one's chunks, past which the steps from piece to piece take longer
 // than they save (8192 tokens of 2 heads: 11 pieces 111 us, 16 119; 4096: 8 pieces 81 us, 16 101).
-// From kPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 37.0
+// From kDeltaPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 37.0
 // against 40.7 us, 2048 76 and 132, of 32 heads 38.4 and 40.8, 94 and 132, of 48 heads 38.9
 // and 41.1, 103 and 134; with 7 chunks the join takes what the pieces save.  The outputs of all
 // pieces but the first go through the workspace: calls that would need more than a gigabyte
 // of it go whole.
-constexpr int kPieceChunks = 8;
 constexpr size_t kMostWorkspace = (size_t)1 << 30;
 int delta_pieces(int B, int max_new, int v_heads, int dv, int sms) {
     const int chunks = (max_new + kDeltaChunk - 1) / kDeltaChunk;
-    if (chunks < kPieceChunks) return 1;
+    if (chunks < kDeltaPieceChunks) return 1;
     const long long moves = (long long)B * v_heads, ctas = moves * ((dv + kDeltaRows - 1) / kDeltaRows);
     const long long most = (sms + moves) / (ctas + moves);
     int count = 1;

@@ -20,7 +20,7 @@ struct DeltaPieces {
 };
 // Two parts of a matrix of dk columns, each in tiles of 64 columns with 128-byte swizzled rows.
 __host__ __device__ constexpr uint32_t delta_parts_bytes(int rows, int dk) { return 4u * (uint32_t)rows * (uint32_t)dk; }
-constexpr int kDeltaChunk = 64, kDeltaRows = 128;
+constexpr int kDeltaChunk = 64, kDeltaRows = 128, kDeltaPieceChunks = 8;   // (the fewest chunks that go in pieces)
 
 struct DeltaArgs {
     StateSeqView s;
@@ -38,10 +38,10 @@ struct DeltaArgs {
 
 constexpr float kDeltaNormEps = 1e-6f;
 
-// The chunks of a piece of a sequence of n tokens; a sequence of one chunk has one piece.
+// The chunks of a piece of a sequence of n tokens; short ones are one piece.
 __device__ __forceinline__ int delta_piece_chunks(const DeltaPieces& p, int n) {
     const int chunks = (n + kDeltaChunk - 1) / kDeltaChunk;
-    return (chunks + p.count - 1) / p.count;
+    return chunks < kDeltaPieceChunks ? chunks : (chunks + p.count - 1) / p.count;
 }
 // Where in out and out_move sequence b's chunks behind its first piece begin.  Of its n tokens
 // they are fewer than n (count - 1) / (64 count) + 1: sequences in a row stay apart, the last

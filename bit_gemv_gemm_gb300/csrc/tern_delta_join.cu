@@ -80,6 +80,7 @@ struct Join {
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
+        pdl_launch_dependents();   // (the next kernel may want tensor memory: not before this one has its own)
         return *reinterpret_cast<volatile uint32_t*>(smem + L::kBar + 48);
     }
     __device__ __forceinline__ void close(uint32_t tmem) {
@@ -249,7 +250,6 @@ delta_join_kernel(const DeltaArgs a, int states, int ctas, int count) {
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-    pdl_launch_dependents();
     pdl_wait();
     const StateSeq s = load_state_seq(a.s, blockIdx.z, &g_delta_join_error);
     const int per = delta_piece_chunks(a.p, s.n) * kTok, x = (int)blockIdx.x - states;

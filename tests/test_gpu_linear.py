@@ -505,3 +505,51 @@ def test_another_stream_and_replays(tern):
         graph.replay()
         assert torch.equal(out, second) and torch.equal(conv, last[0]) and torch.equal(delta, last[1])
     assert tern.device_error() == 0
+
+
+def test_streams_at_once(tern):
+    """Sequences in pieces on two streams and products on a third, all at once: each as if alone."""
+    g = gen(23)
+    heads, n = (2, 8, 64, 64), 640
+    C = 2 * 2 * 64 + 8 * 64
+    inputs = [delta_inputs(n, *heads, g) for _ in range(2)]
+    pools = [rand((1, 8, 64, 64), g) for _ in range(2)]
+    t = torch.randint(-1, 2, (1024, C - C % 128), dtype=torch.int8, device="cuda", generator=g)
+    codes, scales = tern.pack(t), torch.full((1024, t.shape[1] // 128), 0.01, dtype=torch.half, device="cuda")
+    x = rand((512, t.shape[1]), g, torch.bfloat16)
+
+    def run(i, state, stream=None):
+        return tern.gated_delta(*inputs[i][:5], state, i32([0]), qk_norm=True, stream=stream)
+
+    alone = [pools[i].clone() for i in range(2)]
+    want = [[run(i, alone[i]) for _ in range(4)] for i in range(2)]
+    product = tern.gemm(x, codes, scales)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    state = [p.clone() for p in pools]
+    torch.cuda.synchronize()
+    got, products = [[], []], []
+    for _ in range(4):
+        for i in range(2):
+            got[i].append(run(i, state[i], streams[i]))
+        products.append(tern.gemm(x, codes, scales, stream=streams[2]))
+    torch.cuda.synchronize()
+    assert tern.device_error() == 0
+    for i in range(2):
+        assert torch.equal(state[i], alone[i]) and all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+    assert all(torch.allclose(p, product, rtol=1e-4, atol=1e-4) for p in products)
+
+
+def test_short_sequences_of_a_long_call(tern):
+    """max_new as large as all tokens together: sequences too short for pieces stay whole, beside one that is not."""
+    Hk, Hv, Dk, Dv = 1, 2, 64, 64
+    g = gen(24)
+    lens = [300, 1, 448, 449, 0, 700, 65]
+    start, T = sequences(lens)
+    inputs = delta_inputs(T, Hk, Hv, Dk, Dv, g)
+    state = rand((8, Hv, Dv, Dk), g)
+    before, sl = f64(state), [6, 5, 4, 3, 2, 1, 0]
+    out = tern.gated_delta(*inputs[:5], state, i32(sl), q_start=i32(start), qk_norm=True)
+    assert tern.device_error() == 0
+    check_delta(inputs, Dk ** -0.5, True, before, state, out, sl, start)
+    with pytest.raises(tern.TernError):
+        tern.gated_delta(*inputs[:5], state, i32([]), qk_norm=True)
