@@ -78,9 +78,10 @@ struct Cfg {
 // warps: the chain, the output, A and P, T, then one each for products and copies and two for decays
 constexpr int kOutWarp = 16, kGramWarp = 20, kInvWarp = 24, kMmaWarp = 28, kTmaWarp = 29, kCoefWarp = 30, kThreads = 32 * 32;
 // registers a thread: 512 x 72 + 128 x (56 + 64 + 56 + 48) = 1024 x 64, what the CTA is launched with
-// tensor memory columns: D over the parts of S, then those of X; Q S^T of odd chunks; K S^T, then U,
-// then U's parts; Q S^T of even chunks; parts of the scaled U; P U; Gram matrices
-enum { T_S = 0, T_X = T_S, T_QS_ODD = 128, T_KS = 192, T_QS_EVEN = 256, T_UP = 320, T_O = 384, T_GRAM = 448 };
+// tensor memory columns: D over the parts of S; Q S^T of odd chunks; K S^T, then U, then U's parts; Q S^T
+// of even chunks; the parts of X, then of the scaled U (X cannot take the place of S, which Q S^T may
+// still be read from when K S^T is there); P U; Gram matrices
+enum { T_S = 0, T_QS_ODD = 128, T_KS = 192, T_QS_EVEN = 256, T_X = 320, T_UP = T_X, T_O = 384, T_GRAM = 448 };
 enum {
     KQ_FULL = 0, KQ_EMPTY = KQ_FULL + kKqStages, V_FULL = KQ_EMPTY + kKqStages, V_EMPTY = V_FULL + kVStages,
     COEF_FULL = V_EMPTY + kVStages, COEF_EMPTY = COEF_FULL + kCoefStages, TP_FULL = COEF_EMPTY + kCoefStages,
@@ -503,8 +504,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         for (int e = 0; e < 4; ++e)
                             x[i + e] = __float_as_uint(fmaf(m[e], __uint_as_float(x[i + e]), __uint_as_float(y[i + e])));
                     }
-                    if (!live) continue;
-                    if (moves) {
+                    if (!live) {
+                    } else if (moves) {
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             uint32_t hi, lo;
@@ -522,6 +523,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                         for (int i = 0; i < 16; ++i) to[i * width] = __uint_as_float(x[i]);
                     }
+                    __syncwarp();
                     continue;
                 }
 #pragma unroll

@@ -539,6 +539,26 @@ def test_streams_at_once(tern):
     assert all(torch.allclose(p, product, rtol=1e-4, atol=1e-4) for p in products)
 
 
+@pytest.mark.parametrize("heads,lens", [((5, 15, 64, 96), [700, 65, 640]), ((1, 40, 64, 64), [577]), ((4, 24, 128, 128), [1089])])
+@pytest.mark.parametrize("whole", [False, True])
+def test_delta_repeats_bit_for_bit(tern, heads, lens, whole):
+    """Every run of a call gives the same bits (what products read may not be written before they have: when X took
+    S's place beside Q S^T, one run in forty of the first case differed)."""
+    Hk, Hv, Dk, Dv = heads
+    g = gen(21)
+    start, T = sequences(lens)
+    inputs, sl = delta_inputs(T, Hk, Hv, Dk, Dv, g), list(range(len(lens)))
+    pool = rand((len(lens), Hv, Dv, Dk), g)
+    ws = 0 if whole else tern.lib().tern_gated_delta_workspace_bytes(len(lens), T, max(lens), Hv, Dk, Dv)
+    first = None
+    for _ in range(150):
+        state = pool.clone()
+        status, out = delta_call(tern, inputs, Dk ** -0.5, state, sl, start, max(lens), ws)
+        assert status == 0
+        first = first or (out, state)
+        assert torch.equal(out, first[0]) and torch.equal(state, first[1])
+
+
 def test_short_sequences_of_a_long_call(tern):
     """max_new as large as all tokens together: sequences too short for pieces stay whole, beside one that is not."""
     Hk, Hv, Dk, Dv = 1, 2, 64, 64
