@@ -273,6 +273,7 @@ extern "C" tern_status tern_gated_delta(const void* q, const void* k, const void
     a.group = v_heads / k_heads;
     a.norm = qk_norm;
     a.scale = scale;
+    a.by_length = q_start && (long long)((dv + kDeltaRows - 1) / kDeltaRows) * v_heads * B > sms;
     cudaError_t e = a.s.max_new > kStepTokens ? launch_delta_chunk(a, (cudaStream_t)stream)
                                               : launch_delta_step(a, (cudaStream_t)stream);
     if (e == cudaSuccess && a.p.count > 1) e = launch_delta_join(a, sms, (cudaStream_t)stream);

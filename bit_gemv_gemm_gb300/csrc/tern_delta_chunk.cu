@@ -239,6 +239,22 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// The sequence that comes `y`-th by length among its 32 neighbours: CTAs begin in their grid's
+// order, and a long one that begins late is alone at the end.  Twelve prompts of 128 to 4096 tokens
+// in no order, 48 heads, 461 -> 364 us; 32 short ones among which two are long 583 -> 439.
+__device__ __forceinline__ int by_length(const StateSeqView& s, int y) {
+    const int lane = threadIdx.x & 31, i = (y & ~31) + lane;
+    const int mine = i < s.B ? max(s.q_start[i + 1] - s.q_start[i], 0) : -1;
+    if (__all_sync(0xffffffffu, mine == __shfl_sync(0xffffffffu, mine, 0))) return y;
+    int before = 0;   // (every lane another number)
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+        const int other = __shfl_sync(0xffffffffu, mine, j);
+        before += other > mine || (other == mine && j < lane);
+    }
+    return (y & ~31) + __ffs(__ballot_sync(0xffffffffu, before == (y & 31))) - 1;
+}
+
 template <int DK, bool PIECES>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -279,7 +295,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     pdl_wait();
 
     const int h = blockIdx.x % a.v_heads, row0 = blockIdx.x / a.v_heads * kRows, hk = h / a.group;
-    StateSeq s = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
+    // (every warp for itself: handed on through shared memory, the number costs the roles their uniform registers)
+    const int b = !PIECES && a.by_length ? by_length(a.s, blockIdx.y) : (int)blockIdx.y;
+    StateSeq s = load_state_seq(a.s, b, &g_delta_chunk_error);
     // this CTA's piece, whether it has the unit matrix in place of S, its rows
     int piece = 0, rows = a.dv;
     bool moves = false;

@@ -559,6 +559,29 @@ def test_delta_repeats_bit_for_bit(tern, heads, lens, whole):
         assert torch.equal(out, first[0]) and torch.equal(state, first[1])
 
 
+@pytest.mark.parametrize("lens", [[70] * 33 + [1, 0, 200] + [65] * 30, [64, 320, 0, 130, 64, 500, 30]])
+def test_more_sequences_than_sms(tern, lens):
+    """Sequences by length, past 32 of them, equal and unequal, with a bad range among them."""
+    Hk, Hv, Dk, Dv = 2, 24, 64, 16
+    g = gen(25)
+    start, T = sequences(lens, behind=3)
+    inputs = delta_inputs(T, Hk, Hv, Dk, Dv, g)
+    B = len(lens)
+    state = rand((B, Hv, Dv, Dk), g)
+    before, sl = f64(state), list(range(B))[::-1]
+    out = torch.full((T, Hv, Dv), 7.0, dtype=torch.bfloat16, device="cuda")
+    tern.gated_delta(*inputs[:5], state, i32(sl), q_start=i32(start), max_new=max(lens), qk_norm=True, out=out)
+    assert tern.device_error() == 0
+    check_delta(inputs, Dk ** -0.5, True, before, state, out, sl, start, out_was=np.full(out.shape, 7.0))
+    good, kept = out.clone(), state.clone()
+    state.copy_(torch.from_numpy(before))
+    start[2] = -5                              # its own range and the one before it
+    tern.gated_delta(*inputs[:5], state, i32(sl), q_start=i32(start), max_new=max(lens), qk_norm=True, out=out)
+    assert tern.device_error() == tern.DEVERR_CACHE_SEQUENCE
+    last = start[4]
+    assert torch.equal(out[last:], good[last:]) and torch.equal(state[:B - 4], kept[:B - 4])
+
+
 def test_short_sequences_of_a_long_call(tern):
     """max_new as large as all tokens together: sequences too short for pieces stay whole, beside one that is not."""
     Hk, Hv, Dk, Dv = 1, 2, 64, 64
