@@ -21,8 +21,8 @@ __device__ int g_delta_error;
 
 constexpr int kStepThreads = 128, kStepBatch = 8;
 // The most tokens of a sequence that go one by one.  24 (32) tokens so and by chunks, 32 heads of
-// 128 x 128: one sequence 13.4 against 16.7 us (17.3, 16.9), eight 34.0 against 33.0 (44.1,
-// 33.6), sixty-four 230 against 239 (302, 244).
+// 128 x 128: one sequence 13.5 against 16.8 us (17.3, 17.2), eight 33.9 against 35.6 (44.1,
+// 36.4), sixty-four 230 against 245 (302, 251).
 constexpr int kStepTokens = 24;
 
 // 8 lanes share a row: lane l has the values 32 i + 4 l + {0..3}, so that a row's
@@ -175,10 +175,10 @@ namespace {
 // How many pieces the sequences go in: no more than let every CTA of them have an SM of its own
 // (a piece behind the first takes two, one for what it does to any state), and no more than
 // the root of the longest one's chunks, past which the steps from piece to piece take longer
-// than they save (8192 tokens of 2 heads: 11 pieces 111 us, 16 119; 4096: 8 pieces 81 us, 16 101).
-// From kDeltaPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 37.0
-// against 40.7 us, 2048 76 and 132, of 32 heads 38.4 and 40.8, 94 and 132, of 48 heads 38.9
-// and 41.1, 103 and 134; with 7 chunks the join takes what the pieces save.  The outputs of all
+// than they save (8192 tokens of 2 heads: 11 pieces 113 us, 16 119; 4096: 8 pieces 82 us, 16 101).
+// From kDeltaPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 36.1
+// against 41.0 us, 2048 77 and 133, of 32 heads 38.9 and 41.3, 97 and 134, of 48 heads 39.9
+// and 41.5, 106 and 135; with 7 chunks the join takes what the pieces save.  The outputs of all
 // pieces but the first go through the workspace: calls that would need more than a gigabyte
 // of it go whole.
 constexpr size_t kMostWorkspace = (size_t)1 << 30;

@@ -22,9 +22,9 @@
 //
 // A chunk takes 3.9 us where few SMs run, 4.6 where all do (latency of that chain, the
 // issue of some 17 thousand instructions by 32 warps, and, with all SMs at work, the
-// fetching of code): six prompts, 16381 tokens of 48 heads of 128 x 128, 398 us, and one
-// of 2048 tokens of 32 heads 132 us whole.  Where that leaves SMs idle, sequences go in
-// pieces at once (DeltaPieces): 94 us.
+// fetching of code): six prompts, 16381 tokens of 48 heads of 128 x 128, 389 us, and one
+// of 2048 tokens of 32 heads 134 us whole.  Where that leaves SMs idle, sequences go in
+// pieces at once (DeltaPieces): 97 us.
 //
 // Rounding.  q, k, v are exact as bf16.  S, X, U and T are fp32 cut into two bf16
 // values, which carry 2^-17 of each (one would lose 2^-8 of the state a chunk); what

@@ -591,7 +591,7 @@ tern_status tern_short_conv(const void *x, int x_is_f32, long long x_token, cons
  * workspace: NULL, or tern_gated_delta_workspace_bytes(B, T, max_new, v_heads, dk, dv)
  * bytes (max_new T / B without q_start; TERN_ERR_WORKSPACE if it is smaller), 256-byte
  * aligned, any contents: with it, few heads of long sequences go in pieces at once (one
- * of 2048 tokens and 32 heads of 128 x 128: 94 us, not 132).  0 bytes: none of use. */
+ * of 2048 tokens and 32 heads of 128 x 128: 97 us, not 134).  0 bytes: none of use. */
 size_t tern_gated_delta_workspace_bytes(int B, int T, int max_new, int v_heads, int dk, int dv);
 tern_status tern_gated_delta(const void *q, const void *k, const void *v, long long q_token, long long k_token,
                              long long v_token, const float *g, long long g_token, const float *beta,
