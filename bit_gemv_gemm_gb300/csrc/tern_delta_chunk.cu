@@ -26,11 +26,10 @@
 // of 2048 tokens of 32 heads 134 us whole.  Where that leaves SMs idle, sequences go in
 // pieces at once (DeltaPieces): 97 us.
 //
-// Rounding.  q, k, v are exact as bf16.  S, X, U and T are fp32 cut into two bf16
+// Rounding.  q, k, v are exact as bf16.  S, X, U, T and P are fp32 cut into two bf16
 // values, which carry 2^-17 of each (one would lose 2^-8 of the state a chunk); what
 // that leaves of X is added to U in fp32, T's diagonal being 1.  Lengths and decays
-// are applied in fp32, to rows and columns of results.  P is one bf16: it only
-// reaches the output, which is rounded to that.  Exponents are differences of G, at
+// are applied in fp32, to rows and columns of results.  Exponents are differences of G, at
 // most 0, and G is a sum in 64 bits kept as two fp32: a long or strong decay before
 // a pair of tokens does not blur theirs.
 #include "tern_delta.cuh"
@@ -47,6 +46,9 @@ constexpr int kTok = kDeltaChunk, kRows = kDeltaRows;                 // tokens 
 constexpr int kKqStages = 3, kVStages = 2, kCoefStages = 4, kTpStages = 2, kAStages = 2;
 constexpr uint32_t kTile = kTok * 128;                // bytes of a [64][64] bf16 tile, 128-byte swizzled rows
 constexpr uint32_t kATile = kTok * 64;                // of a part of A below its diagonal blocks: a_at()
+// P's two parts, side by side in rows of 64 values: columns 0 .. 31 of all 64 tokens, then 32 .. 63
+// of the later 32 (the earlier have none)
+constexpr uint32_t kPRight = kTile, kPBytes = kTile + kTile / 2;
 constexpr int kDiagRow = 20, kDiagBlock = 16 * kDiagRow + 16;   // floats of a column and of a block of -A's diagonal blocks
 
 // What one chunk's tokens are scaled by.
@@ -69,7 +71,7 @@ struct Cfg {
     static constexpr int COLS = DK / 4;                         // columns of S that a thread holds
     static constexpr int kKqBytes = NC * 2 * (int)kTile;        // 64 values of K's and Q's rows, the next 64
     static constexpr int kVBytes = 4 * kTok * 64;               // 32 rows of S a tile: [token][32]
-    static constexpr int kTpBytes = 3 * (int)kTile;             // T's two parts, P
+    static constexpr int kTpBytes = 2 * (int)kTile + (int)kPBytes;   // T's two parts, P's
     static constexpr int kABytes = 2 * (int)kATile + 4 * kDiagBlock * 4;   // A's two parts, its diagonal blocks
     static constexpr size_t kKq = 0, kV = kKq + (size_t)kKqStages * kKqBytes, kTp = kV + (size_t)kVStages * kVBytes,
                             kA = kTp + (size_t)kTpStages * kTpBytes, kCoef = kA + (size_t)kAStages * kABytes, kBar = kCoef + kCoefStages * sizeof(Coef),
@@ -595,14 +597,20 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int me = warp - kGramWarp, part = me & 1, i = 32 * part + lane;
         const bool low = lane < 16, is_k = me < 2;
         const uint32_t gram = tmem + ((uint32_t)(me * 32) << 16) + T_GRAM;
-        // 8 values as bf16, and what that leaves of them another place on
-        auto put8 = [&](uint32_t at, const float* z, bool parts) {
-            uint32_t hi[4], lo[4];
+        // 16 values as bf16 and what that leaves of them: two units of a row each, the second at ^ 16
+        auto put16 = [&](uint32_t at, uint32_t rest, const float* z) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split2(z[2 * e], z[2 * e + 1], hi[e], lo[e]);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-            if (parts)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kATile), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+            for (int u = 0; u < 2; ++u) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2(z[8 * u + 2 * e], z[8 * u + 2 * e + 1], hi[e], lo[e]);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u * u), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rest ^ 16u * u), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+            }
+        };
+        // columns 8 `unit` on of this row of P; the rest of them at ^ 64
+        auto p_at = [&](uint32_t P, int unit) {
+            return unit < 4 ? tile_at(P, i, unit) : tile_at(P + kPRight, i - 32, unit - 4);
         };
         bool ok = true;
 #pragma unroll 1
@@ -662,8 +670,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                     for (int e = 0; e < 16; ++e) at[e * kDiagRow] = -z[e];
                 } else {
-                    put8(tile_at(P, i, j0 / 8), z, false);
-                    put8(tile_at(P, i, j0 / 8 + 1), z + 8, false);
+                    const uint32_t at = p_at(P, j0 / 8);
+                    put16(at, at ^ 64u, z);
                 }
             }
             if (is_k) arrive(DIAG_FULL + (c & 1));   // (T's diagonal blocks can be begun)
@@ -683,9 +691,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     unpack2(mul2(mul2(pack2(f, f), pack2(t.x, t.y)), pack2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))),
                             z[e], z[e + 1]);
                 }
-                const int r = b == 2 ? i - 48 : i, unit = b == 2 ? 0 : 2 * b;
-                put8(is_k ? a_at(A, r, unit) : tile_at(P, i, 2 * b), z, is_k);
-                put8(is_k ? a_at(A, r, unit + 1) : tile_at(P, i, 2 * b + 1), z + 8, is_k);
+                const uint32_t at = !is_k ? p_at(P, 2 * b) : b == 2 ? a_at(A, i - 48, 0) : a_at(A, i, 2 * b);
+                put16(at, is_k ? at + kATile : at ^ 64u, z);
             }
             __syncwarp();
             tc_fence_before();
@@ -742,7 +749,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == kMmaWarp) {
             // ------------------------------ products ------------------------------
-            constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTok);
+            constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTok), kIdescHalf = idesc_bf16_f32(kRows, kTok / 2);
             constexpr uint32_t kIdescD = idesc_bf16_f32(kRows, DK) | kIdescBMnMajor;
             bool ok = true;
             auto need = [&](int b, uint32_t parity) { ok = ok && wait_warp(b, parity); };
@@ -761,11 +768,26 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                    (kk | x) ? 1u : 0u);
             };
             // (+)= 64 tokens in tensor memory times a [64][64] tile
-            auto with_tile = [&](uint32_t to, uint32_t left, uint32_t stride, uint32_t tile, bool more) {
+            auto with_tile = [&](uint32_t to, uint32_t left, uint32_t tile, bool more) {
                 const uint64_t d = smem_desc_k_sw128(tile);
 #pragma unroll
                 for (int kk = 0; kk < kTok / 16; ++kk)
-                    mma_f16_ts(to, left + stride * kk, d + 2 * kk, kIdesc, (more || kk) ? 1u : 0u);
+                    mma_f16_ts(to, left + 8 * kk, d + 2 * kk, kIdesc, (more || kk) ? 1u : 0u);
+            };
+            // U times P, three products of parts: outputs of 32 tokens each (the earlier need no later U)
+            auto with_p = [&](uint32_t P) {
+#pragma unroll 1
+                for (int part = 0; part < 3; ++part) {   // hi hi, lo hi, hi lo
+                    const uint32_t left = part == 1 ? T_KS + 8u : (uint32_t)T_KS;
+                    const uint64_t d = smem_desc_k_sw128(P) + (part == 2 ? 4 : 0), later = d + (32 * 128 >> 4), right = d + (kPRight >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        mma_f16_ts(T_O, left + 16 * kk, d + 2 * kk, kIdescHalf, (part | kk) ? 1u : 0u);
+                        mma_f16_ts(T_O + 32, left + 16 * kk, later + 2 * kk, kIdescHalf, (part | kk) ? 1u : 0u);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) mma_f16_ts(T_O + 32, left + 32 + 16 * kk, right + 2 * kk, kIdescHalf, 1u);
+                }
             };
             // the first two Gram matrices, then in chunk c that of c + 2
 #pragma unroll 1
@@ -791,9 +813,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     chain_wait(X_READY);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        with_tile(T_KS, T_X, 8, tp, false);
-                        with_tile(T_KS, T_X + 32, 8, tp, true);
-                        with_tile(T_KS, T_X, 8, tp + kTile, true);
+                        with_tile(T_KS, T_X, tp, false);
+                        with_tile(T_KS, T_X + 32, tp, true);
+                        with_tile(T_KS, T_X, tp + kTile, true);
                         mma_commit(bar(U_FULL));
                     }
                     __syncwarp();
@@ -829,8 +851,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     chain_wait(U2_READY);
                     tc_fence_after();
                     if (ok && elect_one()) {
-                        with_tile(T_O, T_KS, 16, tp + 2 * kTile, false);
-                        with_tile(T_O, T_KS + 8, 16, tp + 2 * kTile, true);
+                        with_p(tp + 2 * kTile);
                         mma_commit(bar(TP_EMPTY + (c & 1)));
                         mma_commit(bar(O_FULL));   // (of the last chunk the last: the CTA ends after it)
                     }

@@ -316,6 +316,30 @@ def test_delta(tern, heads, lens, raw):
                     np.full(out.shape, 7.0))
 
 
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("lens", [[25], [64], [33, 64, 1, 0, 31], [200, 47], [700, 65]])
+def test_delta_outputs_are_rounded_once(tern, heads, lens):
+    """A chunk's products leave less of an output than its own rounding does: it is the rounded value, but
+    where that lies next to a border.
+
+    Every factor of Q S^T and P U is two bf16 values (2^-17 of it) and their smallest product is left out
+    (2^-18); with what U and S are off by, a few times 2^-17 of what goes into an output, e <= 2^-13 of it here
+    (it is the norm of a sum of at least as many parts).  A rounding changes to the neighbour, a step of at
+    most 2^-7 of the value away, for a share e / step of the values: the mean square of what changes is at
+    most e 2^-7, its root 2^-10.  One bf16 for P (e = 2^-9.5) would change half of them, 2^-8.3."""
+    Hk, Hv, Dk, Dv = heads
+    g, B = gen(sum(lens) + Dk), len(lens)
+    start, T = sequences(lens)
+    q, k, v, a, b, _, _ = delta_inputs(T, *heads, g)
+    pool = 0.1 * rand((B, Hv, Dv, Dk), g)
+    state, sl = pool.clone(), list(range(B))
+    out = tern.gated_delta(q, k, v, a, b, state, i32(sl), q_start=i32(start), max_new=max(lens), qk_norm=True)
+    assert tern.device_error() == 0
+    want = ref.gated_delta(f64(q), f64(k), f64(v), f64(a), f64(b), f64(pool), sl, start, Dk ** -0.5, True)[0]
+    rounded = f64(torch.from_numpy(want).to(torch.bfloat16))
+    assert np.linalg.norm(f64(out) - rounded) <= 2.0 ** -10 * np.linalg.norm(want)
+
+
 def delta_call(tern, inputs, scale, state, sl, start, max_new, ws_bytes):
     """The C entry point with a workspace of `ws_bytes` bytes (0: none); its status and output."""
     q, k, v, g, b, al, dt = inputs
