@@ -68,15 +68,14 @@ int tern_last_launch_count(void) { return g_last_launches.load(std::memory_order
 
 tern_status tern_wait_selftest(int which, int limit_us, tern_stream_t stream) {
     set_launch_count(0);
-    if ((which != TERN_SELFTEST_RANGE_FLAG && which != TERN_SELFTEST_MBARRIER) || limit_us < 1 ||
-        limit_us > 1000000)
-        return TERN_ERR_SHAPE;
+    auto* const launch = which == TERN_SELFTEST_RANGE_FLAG ? launch_flag_wait_selftest
+                         : which == TERN_SELFTEST_MBARRIER ? launch_mbar_wait_selftest
+                         : which == TERN_SELFTEST_DELTA    ? launch_delta_wait_selftest
+                                                           : nullptr;
+    if (!launch || limit_us < 1 || limit_us > 1000000) return TERN_ERR_SHAPE;
     const tern_status d = check_device(nullptr);
     if (d != TERN_OK) return d;
-    const uint64_t ns = 1000ull * (uint64_t)limit_us;
-    const cudaError_t e = which == TERN_SELFTEST_RANGE_FLAG ? launch_flag_wait_selftest(ns, stream)
-                                                            : launch_mbar_wait_selftest(ns, stream);
-    if (e != cudaSuccess) return TERN_ERR_CUDA;
+    if (launch(1000ull * (uint64_t)limit_us, stream) != cudaSuccess) return TERN_ERR_CUDA;
     set_launch_count(1);
     return TERN_OK;
 }

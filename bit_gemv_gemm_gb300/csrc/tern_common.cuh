@@ -50,6 +50,7 @@ cudaError_t read_delta_join_device_error(int* code);
 // One-CTA kernels that run a bounded wait nothing completes (tern_wait_selftest).
 cudaError_t launch_flag_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_mbar_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_delta_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------
 // Bounded waits.  No kernel of the library spins without a time limit: a wait

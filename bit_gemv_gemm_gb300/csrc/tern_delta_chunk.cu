@@ -93,11 +93,18 @@ enum {
 static_assert(BARS <= 48, "barriers");
 // From the chain's 16 warps to the one that issues products: the SM's own barriers, whose
 // last arrival wakes it sooner than an mbarrier's.  Nothing bounds a wait at one, so both
-// sides go through all their turns whatever has failed: a failed wait only ends the others.
-enum { S_READY = 1, X_READY, UP_READY, U2_READY };
+// sides go through all their turns whatever has failed, and no warp may be a turn ahead: it
+// would be counted in another's place, and the last turn would miss one.  A warp of the chain
+// is held by its waits (each turn's product is issued after the turn); one of which a wait has
+// given up waits for nothing more, and goes through what is left at the barriers themselves.
+enum { S_READY = 1, X_READY, UP_READY, U2_READY, TURNS = 4 };
 constexpr int kChainThreads = 512 + 32;
 __device__ __forceinline__ void chain_arrive(int b) { asm volatile("bar.arrive %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
 __device__ __forceinline__ void chain_wait(int b) { asm volatile("bar.sync %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
+__device__ __forceinline__ void chain_rest(int turn, int chunks) {   // the turns from `turn` on
+#pragma unroll 1
+    for (; turn < TURNS * chunks; ++turn) chain_wait(S_READY + turn % TURNS);
+}
 
 __device__ __forceinline__ int bar_count(int i) {
     if (i >= V_EMPTY && i < V_EMPTY + kVStages) return 4;
@@ -347,11 +354,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
         }
         // S = e^G_last S + D of a chunk; its parts in place of D
-        bool ok = true;
-        auto need = [&](int b, uint32_t parity) { ok = ok && wait_warp(b, parity); };
         auto next_state = [&](int c, bool more) {
             if (c >= 0) {
-                need(D_FULL, (uint32_t)c & 1u);
+                if (!wait_warp(D_FULL, (uint32_t)c & 1u)) return false;
                 tc_fence_after();
                 const float last = coefs[c % kCoefStages].last;
                 const uint64_t last2 = pack2(last, last);
@@ -380,80 +385,87 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 chain_arrive(S_READY);
             }
             if (c >= 0) arrive(COEF_EMPTY + c % kCoefStages);
+            return true;
         };
+        // -1, or the turns that have been gone through when a wait gave up
+        auto walk = [&] {
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = (uint32_t)c & 1u;
-            const Coef& k = coefs[c % kCoefStages];
-            next_state(c - 1, true);
-            need(TP_FULL + (c & 1), full(c, kTpStages));
-            float x[16];
-            need(V_FULL + c % kVStages, full(c, kVStages));
-            const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
-                smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) + quarter * (16 * 64)) + lane;
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t ph = (uint32_t)c & 1u;
+                const Coef& k = coefs[c % kCoefStages];
+                if (!next_state(c - 1, true)) return TURNS * c;
+                if (!wait_warp(TP_FULL + (c & 1), full(c, kTpStages))) return TURNS * c + 1;
+                float x[16];
+                if (!wait_warp(V_FULL + c % kVStages, full(c, kVStages))) return TURNS * c + 1;
+                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
+                    smem + C::kV + (c % kVStages) * C::kVBytes + (warp & 3) * (kTok * 64) + quarter * (16 * 64)) + lane;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const ulonglong2 beta = *reinterpret_cast<const ulonglong2*>(&k.beta[16 * quarter + i]);
-                unpack2(mul2(pack2(__bfloat162float(v[32 * i]), __bfloat162float(v[32 * i + 32])), beta.x), x[i], x[i + 1]);
-                unpack2(mul2(pack2(__bfloat162float(v[32 * i + 64]), __bfloat162float(v[32 * i + 96])), beta.y), x[i + 2], x[i + 3]);
-            }
-            need(KS_FULL, ph);
-            tc_fence_after();
-            uint32_t z[16], hi[8], lo[8];
-            tmem_ld_x16(tk, z);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const ulonglong2 near = *reinterpret_cast<const ulonglong2*>(&k.minus_near[16 * quarter + 2 * e]);
-#pragma unroll
-                for (int f = e; f < e + 2; ++f) {
-                    unpack2(fma2(f == e ? near.x : near.y, pack2(__uint_as_float(z[2 * f]), __uint_as_float(z[2 * f + 1])),
-                                 pack2(x[2 * f], x[2 * f + 1])), x[2 * f], x[2 * f + 1]);
-                    split2(x[2 * f], x[2 * f + 1], hi[f], lo[f]);
+                for (int i = 0; i < 16; i += 4) {
+                    const ulonglong2 beta = *reinterpret_cast<const ulonglong2*>(&k.beta[16 * quarter + i]);
+                    unpack2(mul2(pack2(__bfloat162float(v[32 * i]), __bfloat162float(v[32 * i + 32])), beta.x), x[i], x[i + 1]);
+                    unpack2(mul2(pack2(__bfloat162float(v[32 * i + 64]), __bfloat162float(v[32 * i + 96])), beta.y), x[i + 2], x[i + 3]);
                 }
-            }
-            tmem_st_x8(mine + T_X + 8u * quarter, hi);
-            tmem_st_x8(mine + T_X + 32u + 8u * quarter, lo);
-            tmem_st_wait();
-            tc_fence_before();
-            chain_arrive(X_READY);
-            // what the parts leave of X
+                if (!wait_warp(KS_FULL, ph)) return TURNS * c + 1;
+                tc_fence_after();
+                uint32_t z[16], hi[8], lo[8];
+                tmem_ld_x16(tk, z);
+                tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                unpack2(less_bf16(less_bf16(pack2(x[2 * e], x[2 * e + 1]), hi[e]), lo[e]), x[2 * e], x[2 * e + 1]);
+                for (int e = 0; e < 8; e += 2) {
+                    const ulonglong2 near = *reinterpret_cast<const ulonglong2*>(&k.minus_near[16 * quarter + 2 * e]);
+#pragma unroll
+                    for (int f = e; f < e + 2; ++f) {
+                        unpack2(fma2(f == e ? near.x : near.y, pack2(__uint_as_float(z[2 * f]), __uint_as_float(z[2 * f + 1])),
+                                     pack2(x[2 * f], x[2 * f + 1])), x[2 * f], x[2 * f + 1]);
+                        split2(x[2 * f], x[2 * f + 1], hi[f], lo[f]);
+                    }
+                }
+                tmem_st_x8(mine + T_X + 8u * quarter, hi);
+                tmem_st_x8(mine + T_X + 32u + 8u * quarter, lo);
+                tmem_st_wait();
+                tc_fence_before();
+                chain_arrive(X_READY);
+                // what the parts leave of X
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    unpack2(less_bf16(less_bf16(pack2(x[2 * e], x[2 * e + 1]), hi[e]), lo[e]), x[2 * e], x[2 * e + 1]);
 
-            need(U_FULL, ph);
-            tc_fence_after();
-            tmem_ld_x16(tk, z);
-            tmem_ld_wait();
+                if (!wait_warp(U_FULL, ph)) return TURNS * c + 2;
+                tc_fence_after();
+                tmem_ld_x16(tk, z);
+                tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const ulonglong2 left = *reinterpret_cast<const ulonglong2*>(&k.left[16 * quarter + 2 * e]);
+                for (int e = 0; e < 8; e += 2) {
+                    const ulonglong2 left = *reinterpret_cast<const ulonglong2*>(&k.left[16 * quarter + 2 * e]);
 #pragma unroll
-                for (int f = e; f < e + 2; ++f) {
-                    const uint64_t u = add2(pack2(x[2 * f], x[2 * f + 1]), pack2(__uint_as_float(z[2 * f]), __uint_as_float(z[2 * f + 1])));
-                    float p, q;
-                    unpack2(u, x[2 * f], x[2 * f + 1]);
-                    unpack2(mul2(f == e ? left.x : left.y, u), p, q);
-                    split2(p, q, hi[f], lo[f]);
+                    for (int f = e; f < e + 2; ++f) {
+                        const uint64_t u = add2(pack2(x[2 * f], x[2 * f + 1]), pack2(__uint_as_float(z[2 * f]), __uint_as_float(z[2 * f + 1])));
+                        float p, q;
+                        unpack2(u, x[2 * f], x[2 * f + 1]);
+                        unpack2(mul2(f == e ? left.x : left.y, u), p, q);
+                        split2(p, q, hi[f], lo[f]);
+                    }
                 }
-            }
-            tmem_st_x8(mine + T_UP + 8u * quarter, hi);
-            tmem_st_x8(mine + T_UP + 32u + 8u * quarter, lo);
-            tmem_st_wait();
-            tc_fence_before();
-            chain_arrive(UP_READY);
+                tmem_st_x8(mine + T_UP + 8u * quarter, hi);
+                tmem_st_x8(mine + T_UP + 32u + 8u * quarter, lo);
+                tmem_st_wait();
+                tc_fence_before();
+                chain_arrive(UP_READY);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-            tmem_st_x8(tk, hi);
-            tmem_st_x8(tk + 8u, lo);
-            tmem_st_wait();
-            tc_fence_before();
-            chain_arrive(U2_READY);
-        }
-        if (chunks > 0) next_state(chunks - 1, false);
+                for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+                tmem_st_x8(tk, hi);
+                tmem_st_x8(tk + 8u, lo);
+                tmem_st_wait();
+                tc_fence_before();
+                chain_arrive(U2_READY);
+            }
+            return chunks > 0 && !next_state(chunks - 1, false) ? TURNS * chunks : -1;
+        };
+        const int lost = walk();
+        const bool ok = lost < 0;
         if (!ok) {
             if (lane == 0) fail();
+            chain_rest(lost, chunks);
         }
         // S goes to the pool, or to where the join finds it: a sequence of more than one piece
         float* to_head = s.dst >= 0 && (s.n > 0 || s.dst != s.src) ? a.state + ((long long)s.dst * a.v_heads + h) * a.dv * DK : nullptr;
@@ -1087,7 +1099,64 @@ cudaError_t launch(const DeltaArgs& a, cudaStream_t stream) {
                       dim3(kThreads), C::kSmem, stream, true, mq, mk, mv, mo, a);
 }
 
+// The chain and the issuing warp over six chunks, from the third of which on nothing comes after a
+// turn: the chain's waits run out while the issuing warp still is in a longer one of its own.
+__global__ void __launch_bounds__(kChainThreads) delta_wait_selftest_kernel(uint32_t tries) {
+    __shared__ __align__(8) uint64_t bars[4];
+    enum { KS, U, D, NEVER };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(bar(i), 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    constexpr int kChunks = 6;
+    bool ok = true;
+    if (warp < kOutWarp) {
+        auto walk = [&] {
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+                const uint32_t ph = (uint32_t)c & 1u;
+                if (c > 0 && !wait_warp(bar(D), ph ^ 1u, tries)) return TURNS * c;
+                chain_arrive(S_READY);
+                if (!wait_warp(bar(KS), ph, tries)) return TURNS * c + 1;
+                chain_arrive(X_READY);
+                if (!wait_warp(bar(U), ph, tries)) return TURNS * c + 2;
+                chain_arrive(UP_READY);
+                chain_arrive(U2_READY);
+            }
+            return -1;
+        };
+        const int lost = walk();
+        ok = lost < 0;
+        if (!ok) chain_rest(lost, kChunks);
+    } else {
+        auto done = [&](int b) {
+            if (ok && lane == 0) mbar_arrive(bar(b));
+        };
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+            if (c == 2) ok = wait_warp(bar(NEVER), 0u, 4 * tries);
+            chain_wait(S_READY);
+            done(KS);
+            chain_wait(X_READY);
+            done(U);
+            chain_wait(UP_READY);
+            done(D);
+            chain_wait(U2_READY);
+        }
+    }
+    if (!ok && lane == 0) report_device_error(&g_delta_chunk_error, TERN_DEVERR_DELTA_WAIT);
+}
+
 }  // namespace
+
+cudaError_t launch_delta_wait_selftest(uint64_t limit_ns, cudaStream_t stream) {
+    const uint64_t tries = limit_ns / kDeltaNap;
+    delta_wait_selftest_kernel<<<1, kChainThreads, 0, stream>>>(tries > 0 ? (uint32_t)tries : 1u);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_delta_chunk(const DeltaArgs& a, cudaStream_t stream) {
     return a.dk == 128 ? launch<128>(a, stream) : launch<64>(a, stream);

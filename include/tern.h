@@ -641,11 +641,16 @@ tern_status tern_device_error(int *code);
  *     runs out, raises the CTA's abort flag and reports
  *     TERN_DEVERR_GEMM_MMA_WAIT; a second role in a 1 s wait sees the flag and
  *     returns early, so the kernel ends about limit_us after it starts.
+ *   TERN_SELFTEST_DELTA -- the waits of gated_delta's roles and the hand-over from
+ *     sixteen warps to the one that issues their products: they run out in the third
+ *     of six turns, the issuing warp's after four times limit_us; all go through their
+ *     turns to the end and report TERN_DEVERR_DELTA_WAIT.
  * The code is then read with tern_device_error, and the context stays usable.
  * Returns TERN_ERR_SHAPE for an unknown `which` or a limit out of range
  * (nothing launched), TERN_ERR_ARCH / TERN_ERR_CUDA as the products do. */
 #define TERN_SELFTEST_RANGE_FLAG 0
 #define TERN_SELFTEST_MBARRIER 1
+#define TERN_SELFTEST_DELTA 3
 tern_status tern_wait_selftest(int which, int limit_us, tern_stream_t stream);
 
 /* The number of kernels the last entry point call launched (for launch

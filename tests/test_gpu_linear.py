@@ -620,3 +620,22 @@ def test_short_sequences_of_a_long_call(tern):
     check_delta(inputs, Dk ** -0.5, True, before, state, out, sl, start)
     with pytest.raises(tern.TernError):
         tern.gated_delta(*inputs[:5], state, i32([]), qk_norm=True)
+
+
+def test_waits_that_run_out(tern):
+    """A wait that nothing ends: every role goes on to the kernel's end, the error is read, calls after it work."""
+    assert tern.device_error() == 0
+    tern.wait_selftest(tern.SELFTEST_DELTA, 1000)
+    assert tern.device_error() == tern.DEVERR_DELTA_WAIT
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    tern.wait_selftest(tern.SELFTEST_DELTA, 2000)
+    end.record()
+    assert tern.device_error() == tern.DEVERR_DELTA_WAIT and tern.device_error() == 0
+    # four times the limit (a try may end a little before or after its 2 us), far from a second
+    assert 1.0 < begin.elapsed_time(end) < 100.0, begin.elapsed_time(end)
+    inputs = delta_inputs(70, 1, 2, 64, 32, gen(1))
+    state = torch.zeros((1, 2, 32, 64), device="cuda")
+    out = tern.gated_delta(*inputs[:5], state, i32([0]), qk_norm=True)
+    assert tern.device_error() == 0
+    check_delta(inputs, 64 ** -0.5, True, np.zeros((1, 2, 32, 64)), state, out, [0], [0, 70])

@@ -126,3 +126,8 @@ def test_delta_binding(tern):
     with pytest.raises(ValueError, match="beta must be"):
         tern._gate_stride("beta", (3, 4), (1, 3), 3, 4)
     assert tern._gate_stride("g", (3, 4), (16, 1), 3, 4) == 16 and tern._gate_stride("g", (1, 4), (0, 1), 1, 4) == 4
+
+
+def test_wait_selftest_refuses(tern):
+    for which, limit in ((2, 1000), (tern.SELFTEST_DELTA, 0), (tern.SELFTEST_DELTA, 1000001)):
+        assert tern.lib().tern_wait_selftest(which, limit, None) == SHAPE
