@@ -453,7 +453,7 @@ def device_error() -> int:
     return int(code.value)
 
 
-SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER, SELFTEST_DELTA = 0, 1, 3
+SELFTEST_RANGE_FLAG, SELFTEST_MBARRIER, SELFTEST_DELTA, SELFTEST_NORM = 0, 1, 3, 4
 DEVERR_GEMM_MMA_WAIT, DEVERR_GEMV_RANGE_FLAG_WAIT, DEVERR_GEMV_ACTIVATION_RANGE = 0x103, 0x202, 0x203
 DEVERR_CACHE_PAGE, DEVERR_CACHE_SEQUENCE, DEVERR_CACHE_SLOT = 0x301, 0x302, 0x303
 DEVERR_ATTN_WAIT = 0x311

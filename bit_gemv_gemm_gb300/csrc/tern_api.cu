@@ -71,6 +71,7 @@ tern_status tern_wait_selftest(int which, int limit_us, tern_stream_t stream) {
     auto* const launch = which == TERN_SELFTEST_RANGE_FLAG ? launch_flag_wait_selftest
                          : which == TERN_SELFTEST_MBARRIER ? launch_mbar_wait_selftest
                          : which == TERN_SELFTEST_DELTA    ? launch_delta_wait_selftest
+                         : which == TERN_SELFTEST_NORM     ? launch_norm_wait_selftest
                                                            : nullptr;
     if (!launch || limit_us < 1 || limit_us > 1000000) return TERN_ERR_SHAPE;
     const tern_status d = check_device(nullptr);

@@ -51,6 +51,7 @@ cudaError_t read_delta_join_device_error(int* code);
 cudaError_t launch_flag_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_mbar_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_delta_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_norm_wait_selftest(uint64_t limit_ns, cudaStream_t stream);
 
 // ----------------------------------------------------------------------------
 // Bounded waits.  No kernel of the library spins without a time limit: a wait

@@ -100,23 +100,8 @@ __device__ __forceinline__ float2 delta_gates(const DeltaHead& head, float2 raw)
     return make_float2(g < -200.0f ? -200.0f : g, b);
 }
 
-constexpr uint32_t kDeltaTries = 1u << 19, kDeltaNap = 2000;   // of a wait, and ns of each: a second, far beyond any real one
-// A thread's and a warp's wait, which give up after a number of tries.  (Short: some forty
-// of them stand in loops whose code has to stay in the instruction cache, and asking the
-// time takes longer than most of them.  Every lane asks; one for all made the others wait
-// longer.)
-__device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity, uint32_t tries) {
-    uint32_t ok = 0;
-#pragma unroll 1
-    for (uint32_t n = tries; !ok && n > 0; --n)
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(kDeltaNap)
-            : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t tries = kDeltaTries) {
+// A warp's wait.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t tries = kWaitTries) {
     return __all_sync(0xffffffffu, wait_tries(bar, parity, tries));
 }
 // One lane of a warp whose lanes all come here: what it alone then does is known to be

@@ -1153,7 +1153,7 @@ __global__ void __launch_bounds__(kChainThreads) delta_wait_selftest_kernel(uint
 }  // namespace
 
 cudaError_t launch_delta_wait_selftest(uint64_t limit_ns, cudaStream_t stream) {
-    const uint64_t tries = limit_ns / kDeltaNap;
+    const uint64_t tries = limit_ns / kWaitNap;
     delta_wait_selftest_kernel<<<1, kChainThreads, 0, stream>>>(tries > 0 ? (uint32_t)tries : 1u);
     return cudaGetLastError();
 }

@@ -186,7 +186,19 @@ __global__ void __launch_bounds__(256) norm_warp_kernel(const NormArgs args) {
 // ring in shared memory, a bulk copy an input and row.  (With the next row's values in
 // registers instead, 4096 rows of 5120 took 67 us; a CTA a row 43.)
 constexpr int kStreamBytes = 200 * 1024;   // of an SM's shared memory
-constexpr uint32_t kStreamTries = 1u << 20;
+
+// After a wait that gave up, where nothing more is fetched: waits for the copies still on their way
+// to the `left` stages from `stage` on, so that none lands in shared memory that is another CTA's by then.
+__device__ __noinline__ void ring_drain(const uint64_t* full, int stages, int stage, uint32_t phase, int left, uint64_t limit_ns) {
+    for (; left > 0; --left) {
+        (void)sm100::mbar_wait_drain(sm100::smem_u32(&full[stage]), phase, limit_ns);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+}
+constexpr uint64_t kStreamDrainNs = 20000000;
 
 struct NormRing {
     int stages, row_bytes, r_at, g_at;   // a stage: x, then the residual, then the gate
@@ -237,15 +249,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_stream_kernel(const NormAr
     for (int i = 0; i < PIECES; ++i)
         if (threadIdx.x + i * n < pieces) load_weight(a, 8 * (threadIdx.x + i * n), w[i]);
     int stage = 0;
-    uint32_t phase = 0, tries = kStreamTries;
+    uint32_t phase = 0;
     for (int k = 0; k < count; ++k) {
         const int row = blockIdx.x + k * step;
-        bool landed = false;
-        for (uint32_t left = tries; !landed && left > 0; --left) landed = sm100::mbar_try_wait(sm100::smem_u32(&full[stage]), phase);
-        if (!landed && tries > 1) {   // (and the rows after it are not waited for again)
-            report_device_error(&g_norm_error, TERN_DEVERR_NORM_WAIT);
-            tries = 1;
-        }
+        const bool landed = wait_tries(sm100::smem_u32(&full[stage]), phase, kWaitTries);
         const unsigned char* src = rows + stage * ring.row_bytes;
         NormPiece p[PIECES];
         float h[PIECES][8], sum = 0.0f;
@@ -262,7 +269,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_stream_kernel(const NormAr
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (threadIdx.x % 32 == 0) part[k & 1][threadIdx.x / 32] = sum;
-        __syncthreads();   // (two sets of parts: a warp may be a row ahead, never two)
+        // (two sets of parts: a warp may be a row ahead, never two)
+        if (!__syncthreads_and(landed)) {   // one thread's wait gave up: the CTA ends here
+            if (threadIdx.x == 0) {
+                report_device_error(&g_norm_error, TERN_DEVERR_NORM_WAIT);
+                ring_drain(full, ring.stages, stage, phase, min(ring.stages, count - k), kStreamDrainNs);
+            }
+            return;
+        }
         if (threadIdx.x == 0 && k + ring.stages < count) fetch(row + ring.stages * step, stage);
         sum = threadIdx.x % 32 < n / 32 ? part[k & 1][threadIdx.x % 32] : 0.0f;
 #pragma unroll
@@ -322,6 +336,39 @@ __global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a)
     }
 }
 
+// The ring's wait, of a CTA of two warps: of four rows through two stages the third never comes
+// (one copy of 16 bytes lands, 16 bytes more are waited for).
+__global__ void __launch_bounds__(64) norm_wait_selftest_kernel(uint32_t tries, uint64_t limit_ns, const int* from) {
+    __shared__ __align__(16) unsigned char rows[2][16];
+    __shared__ __align__(8) uint64_t full[2];
+    constexpr int kRows = 4;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) sm100::mbar_init(sm100::smem_u32(&full[i]), 1);
+        sm100::fence_barrier_init();
+    }
+    __syncthreads();
+    auto fetch = [&](int k) {
+        const uint32_t bar = sm100::smem_u32(&full[k & 1]);
+        sm100::mbar_arrive_expect_tx(bar, k == 2 ? 32 : 16);
+        bulk_load(sm100::smem_u32(rows[k & 1]), from, 16, bar);
+    };
+    if (threadIdx.x == 0) {
+        fetch(0);
+        fetch(1);
+    }
+    for (int k = 0; k < kRows; ++k) {
+        const bool landed = wait_tries(sm100::smem_u32(&full[k & 1]), k / 2, tries);
+        if (!__syncthreads_and(landed)) {
+            if (threadIdx.x == 0) {
+                report_device_error(&g_norm_error, TERN_DEVERR_NORM_WAIT);
+                ring_drain(full, 2, k & 1, k / 2, min(2, kRows - k), limit_ns);
+            }
+            return;
+        }
+        if (threadIdx.x == 0 && k + 2 < kRows) fetch(k + 2);
+    }
+}
+
 template <int TEAM, int PIECES, int ROWS>
 cudaError_t launch_warp(const NormArgs& a, cudaStream_t stream) {
     const int per = 256 / TEAM * ROWS;
@@ -356,7 +403,18 @@ cudaError_t launch_stream(const NormArgs& a, int sms, cudaStream_t stream) {
     return launch_pdl(kernel, dim3(std::min(a.rows, CTAS * sms)), dim3(THREADS), (size_t)r.stages * r.row_bytes, stream, true, a, r);
 }
 
+__device__ __align__(16) int g_norm_selftest[4];
+
 }  // namespace
+
+cudaError_t launch_norm_wait_selftest(uint64_t limit_ns, cudaStream_t stream) {
+    void* from = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&from, g_norm_selftest);
+    if (e != cudaSuccess) return e;
+    const uint64_t tries = limit_ns / kWaitNap;
+    norm_wait_selftest_kernel<<<1, 64, 0, stream>>>(tries > 0 ? (uint32_t)tries : 1u, limit_ns, static_cast<const int*>(from));
+    return cudaGetLastError();
+}
 
 cudaError_t read_norm_device_error(int* code) {
     int zero = 0;

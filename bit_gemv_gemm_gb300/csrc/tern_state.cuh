@@ -107,4 +107,21 @@ __device__ __forceinline__ float sigmoid(float x) {
     return y;
 }
 
+constexpr uint32_t kWaitTries = 1u << 19, kWaitNap = 2000;   // of a wait, and ns of each: a second, far beyond any real one
+// A thread's wait for an mbarrier, which gives up after a number of tries.  (Short: some forty
+// of them stand in loops of gated_delta whose code has to stay in the instruction cache, and
+// asking the time takes longer than most of them.  Every lane asks; one for all made the others
+// wait longer.)
+__device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity, uint32_t tries) {
+    uint32_t ok = 0;
+#pragma unroll 1
+    for (uint32_t n = tries; !ok && n > 0; --n)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kWaitNap)
+            : "memory");
+    return ok != 0;
+}
+
 }  // namespace tern

@@ -645,12 +645,16 @@ tern_status tern_device_error(int *code);
  *     sixteen warps to the one that issues their products: they run out in the third
  *     of six turns, the issuing warp's after four times limit_us; all go through their
  *     turns to the end and report TERN_DEVERR_DELTA_WAIT.
+ *   TERN_SELFTEST_NORM -- the wait of rms_norm's ring for a row: it runs out in the
+ *     third of four; nothing more is fetched, what is on its way is waited for (limit_us
+ *     at most), and TERN_DEVERR_NORM_WAIT is reported.
  * The code is then read with tern_device_error, and the context stays usable.
  * Returns TERN_ERR_SHAPE for an unknown `which` or a limit out of range
  * (nothing launched), TERN_ERR_ARCH / TERN_ERR_CUDA as the products do. */
 #define TERN_SELFTEST_RANGE_FLAG 0
 #define TERN_SELFTEST_MBARRIER 1
 #define TERN_SELFTEST_DELTA 3
+#define TERN_SELFTEST_NORM 4
 tern_status tern_wait_selftest(int which, int limit_us, tern_stream_t stream);
 
 /* The number of kernels the last entry point call launched (for launch

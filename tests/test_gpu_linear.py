@@ -622,20 +622,33 @@ def test_short_sequences_of_a_long_call(tern):
         tern.gated_delta(*inputs[:5], state, i32([]), qk_norm=True)
 
 
-def test_waits_that_run_out(tern):
-    """A wait that nothing ends: every role goes on to the kernel's end, the error is read, calls after it work."""
+def run_out(tern, which, code):
+    """Milliseconds of a self-test with a limit of 2 ms, whose code is read once."""
     assert tern.device_error() == 0
-    tern.wait_selftest(tern.SELFTEST_DELTA, 1000)
-    assert tern.device_error() == tern.DEVERR_DELTA_WAIT
+    tern.wait_selftest(which, 1000)
+    assert tern.device_error() == code
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()
-    tern.wait_selftest(tern.SELFTEST_DELTA, 2000)
+    tern.wait_selftest(which, 2000)
     end.record()
-    assert tern.device_error() == tern.DEVERR_DELTA_WAIT and tern.device_error() == 0
+    assert tern.device_error() == code and tern.device_error() == 0
+    return begin.elapsed_time(end)
+
+
+def test_waits_that_run_out(tern):
+    """A wait that nothing ends: every role goes on to the kernel's end, the error is read, calls after it work."""
     # four times the limit (a try may end a little before or after its 2 us), far from a second
-    assert 1.0 < begin.elapsed_time(end) < 100.0, begin.elapsed_time(end)
+    assert 1.0 < run_out(tern, tern.SELFTEST_DELTA, tern.DEVERR_DELTA_WAIT) < 100.0
     inputs = delta_inputs(70, 1, 2, 64, 32, gen(1))
     state = torch.zeros((1, 2, 32, 64), device="cuda")
     out = tern.gated_delta(*inputs[:5], state, i32([0]), qk_norm=True)
     assert tern.device_error() == 0
     check_delta(inputs, 64 ** -0.5, True, np.zeros((1, 2, 32, 64)), state, out, [0], [0, 70])
+
+
+def test_a_row_that_never_comes(tern):
+    """The ring's wait runs out, then the one for what is on its way: twice the limit; rows after it are right."""
+    assert 1.0 < run_out(tern, tern.SELFTEST_NORM, tern.DEVERR_NORM_WAIT) < 100.0
+    x, w = rand((700, 1032), gen(2)), torch.ones(1032, device="cuda")
+    check_norm(tern, x, w, tern.rms_norm(x, w))
+    assert tern.device_error() == 0

@@ -129,5 +129,6 @@ def test_delta_binding(tern):
 
 
 def test_wait_selftest_refuses(tern):
-    for which, limit in ((2, 1000), (tern.SELFTEST_DELTA, 0), (tern.SELFTEST_DELTA, 1000001)):
+    for which, limit in ((2, 1000), (5, 1000), (tern.SELFTEST_DELTA, 0), (tern.SELFTEST_DELTA, 1000001),
+                         (tern.SELFTEST_NORM, 0), (tern.SELFTEST_NORM, 1000001)):
         assert tern.lib().tern_wait_selftest(which, limit, None) == SHAPE
