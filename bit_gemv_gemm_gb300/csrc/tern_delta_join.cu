@@ -47,12 +47,15 @@ struct Join {
     uint32_t base;
     int b, h, tile, warp, lane, per, used;   // per: tokens of a piece, used: pieces of this sequence
     bool ok = true;
+    int begun = 0;   // copies to the stages, one after the other (in the warp that waits for them)
 
     __device__ __forceinline__ uint32_t copied(int stage) const { return base + L::kBar + 8 * stage; }
     __device__ __forceinline__ uint32_t done(int stage) const { return base + L::kBar + 16 + 8 * stage; }
     __device__ __forceinline__ uint32_t read(int stage) const { return base + L::kBar + 32 + 8 * stage; }
     __device__ __forceinline__ uint32_t stage(int i) const { return base + L::kS + (i & 1) * L::kStage; }
-    __device__ __forceinline__ void need(uint32_t bar, int i) { ok = wait_warp(bar, (uint32_t)(i >> 1) & 1u) && ok; }
+    __device__ __forceinline__ uint32_t drained() const { return base + L::kBar + 56; }
+    // A role that gives up goes to close(): nothing is copied or issued after it.
+    __device__ __forceinline__ bool need(uint32_t bar, int i) { return ok = wait_warp(bar, (uint32_t)(i >> 1) & 1u); }
     __device__ __forceinline__ void arrive(uint32_t bar) const {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -69,6 +72,7 @@ struct Join {
                 mbar_init(done(i), 1);
                 mbar_init(read(i), 16);
             }
+            mbar_init(drained(), 1);
             fence_barrier_init();
             first();
         }
@@ -86,7 +90,15 @@ struct Join {
     __device__ __forceinline__ void close(uint32_t tmem) {
         if (!ok && lane == 0) report_device_error(&g_delta_join_error, TERN_DEVERR_DELTA_WAIT);
         tc_fence_before();
-        __syncthreads();
+        if (!__syncthreads_and(ok)) {   // a wait gave up: what is on its way ends before the CTA does
+            if (warp == 16 && elect_one()) {
+                for (int i = max(0, begun - 2); i < begun; ++i)
+                    (void)mbar_wait_drain(copied(i & 1), (uint32_t)(i >> 1) & 1u, 20000000ull);
+                mma_commit(drained());
+                (void)mbar_wait_drain(drained(), 0u, 100000000ull);
+            }
+            __syncthreads();
+        }
         if (warp == 0) {
             tc_fence_after();
             tmem_dealloc(tmem, 128);
@@ -118,16 +130,22 @@ struct Join {
             bulk_load(stage(0), move, kM, copied(0));
         });
         if (warp == 16) {
+            begun = 1;
 #pragma unroll 1
             for (int i = 0; i + 1 < used; ++i) {
-                if (i > 0) need(read(i - 1 & 1), i - 1);   // S is there, the columns are free, and M before the last is done with
-                if (i + 2 < used && lane == 0) {
-                    mbar_arrive_expect_tx(copied(i + 1 & 1), kM);
-                    bulk_load(stage(i + 1), move + (i + 1) * (long long)kM, kM, copied(i + 1 & 1));
+                // S is there, the columns are free, and M before the last is done with
+                if (i > 0 && !need(read(i - 1 & 1), i - 1)) break;
+                if (i + 2 < used) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(copied(i + 1 & 1), kM);
+                        bulk_load(stage(i + 1), move + (i + 1) * (long long)kM, kM, copied(i + 1 & 1));
+                    }
+                    ++begun;
+                    __syncwarp();
                 }
-                need(copied(i & 1), i);
+                if (!need(copied(i & 1), i)) break;
                 tc_fence_after();
-                if (ok && elect_one()) {
+                if (elect_one()) {
                     product<DK, true>(tmem, stage(i));
                     mma_commit(done(i & 1));
                 }
@@ -148,7 +166,7 @@ struct Join {
                     const float4 x = live ? *reinterpret_cast<const float4*>(from + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
                 }
-                need(done(i & 1), i);
+                if (!need(done(i & 1), i)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kCols; c += kAt) {
@@ -197,18 +215,20 @@ struct Join {
             if (chunks > 1) copy(1);
         });
         if (warp == 16) {
+            begun = min(2, chunks);
 #pragma unroll 1
             for (int i = 0; i < chunks; ++i) {
-                need(copied(i & 1), i);
+                if (!need(copied(i & 1), i)) break;
                 tc_fence_after();
-                if (ok && elect_one()) {
+                if (elect_one()) {
                     product<kTok, false>(tmem + kTok * (i & 1), stage(i));
                     mma_commit(done(i & 1));
                 }
                 __syncwarp();
                 if (i > 0 && i + 1 < chunks) {   // the chunk before has left its stage and its columns
-                    need(read(i - 1 & 1), i - 1);
+                    if (!need(read(i - 1 & 1), i - 1)) break;
                     if (lane == 0) copy(i + 1);
+                    ++begun;
                     __syncwarp();
                 }
             }
@@ -218,12 +238,12 @@ struct Join {
             const long long step = (long long)a.v_heads * a.dv;
 #pragma unroll 1
             for (int i = 0; i < chunks; ++i) {
-                need(copied(i & 1), i);   // (for out_B)
+                if (!need(copied(i & 1), i)) break;   // (for out_B)
                 const float* local = reinterpret_cast<const float*>(smem + (stage(i) - base) + L::kO) + quarter * width + min(row, width - 1);
                 float v[16];
 #pragma unroll
                 for (int t = 0; t < 16; ++t) v[t] = local[t * width];
-                need(done(i & 1), i);
+                if (!need(done(i & 1), i)) break;
                 tc_fence_after();
                 uint32_t d[16];
                 tmem_ld_x16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(kTok * (i & 1) + quarter), d);
