@@ -870,14 +870,12 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     __syncwarp();
                 }
             }
-            if (!ok) {
-                if (lane == 0) fail();
-                if (elect_one()) {   // what has been issued ends before the CTA does
-                    mma_commit(bar(DRAIN));
-                    (void)mbar_wait_drain(bar(DRAIN), 0u, 100000000ull);
-                }
-                __syncwarp();
+            if (!ok && lane == 0) fail();
+            if (elect_one()) {   // what has been issued ends before the CTA does, whichever role gave up
+                mma_commit(bar(DRAIN));
+                (void)mbar_wait_drain(bar(DRAIN), 0u, 100000000ull);
             }
+            __syncwarp();
         } else if (warp == kTmaWarp) {
             // ------------------------------ copies ------------------------------
             // V comes a chunk behind K and Q, which are wanted two chunks ahead
@@ -943,16 +941,20 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     }
                 }
             }
-            if (!ok && lane == 0) {
-                fail();
-                // copies in flight land before the CTA goes away
+            if (lane == 0) {
+                // copies in flight land before the CTA goes away, whichever role gave up (those of the
+                // sequence's end have been waited for here)
+                if (!ok) fail();
                 const bool tail = s.n % kTok != 0;
-                for (int i = max(0, kqs - kKqStages); i < kqs; ++i)
-                    (void)mbar_wait_drain(tail && i == chunks - 1 ? bar(TAIL) : bar(KQ_FULL + i % kKqStages),
-                                          tail && i == chunks - 1 ? 0u : full(i, kKqStages), 20000000ull);
-                for (int i = max(0, vs - kVStages); i < vs; ++i)
-                    (void)mbar_wait_drain(tail && i == chunks - 1 ? bar(TAIL) : bar(V_FULL + i % kVStages),
-                                          tail && i == chunks - 1 ? 1u : full(i, kVStages), 20000000ull);
+                auto drain = [&](int begun, int stages, int first, uint32_t parity) {
+#pragma unroll 1
+                    for (int i = max(0, begun - stages); i < begun; ++i) {
+                        if (!tail || i < chunks - 1) (void)mbar_wait_drain(bar(first + i % stages), full(i, stages), 20000000ull);
+                        else if (!ok) (void)mbar_wait_drain(bar(TAIL), parity, 20000000ull);
+                    }
+                };
+                drain(kqs, kKqStages, KQ_FULL, 0u);
+                drain(vs, kVStages, V_FULL, 1u);
             }
             __syncwarp();
         } else {
