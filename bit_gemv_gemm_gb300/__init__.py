@@ -820,6 +820,15 @@ def _f32_or_bf16(t: torch.Tensor, name: str, now: int) -> int:
     raise TypeError(f"{name} must be float32 or bfloat16, got {kind}")
 
 
+def _shaped(**need) -> None:
+    """name=(tensor, shapes): each tensor must have one of the shapes; one of as many elements
+    or more would be read or written as if it had (a [heads, dim] weight as its first row).
+    (Called where a call has found some other shape than the usual.)"""
+    for name, (t, *shapes) in need.items():
+        if t is not None and t.shape not in shapes:
+            raise ValueError(f"{name} must be {' or '.join(str(list(s)) for s in shapes)}, got {list(t.shape)}")
+
+
 _GATES = {"silu": 0, "sigmoid": 1}
 
 
@@ -834,8 +843,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     after=True: out = residual + scale * (x / rms(x) * (weight + weight_offset) [* act(gate)]).
 
     x, residual and gate [T, dim] or [T, heads, dim], fp32 or bf16 each, any token
-    and head strides; weight fp32 [dim].  Returns out, contiguous, of out_dtype:
-    bf16 if not given, the residual's type after a block."""
+    and head strides; weight fp32 [dim].  Returns out, contiguous, of x's shape (one
+    that is given may be [T, heads * dim], residual_out too) and of out_dtype: bf16 if
+    not given, the residual's type after a block."""
     if gate_act not in _GATES:
         raise ValueError(f"gate_act must be one of {sorted(_GATES)}")
     shape = x.shape
@@ -843,6 +853,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     T, dim = shape[0], shape[-1]
     heads = shape[1] if len(shape) == 3 else 1
     rt = rh = gt = gh = 0
+    if weight.shape != (dim,) or (out is not None and out.shape != shape) or (
+            residual_out is not None and residual_out.shape != shape):
+        flat = (T, heads * dim)
+        _shaped(weight=(weight, (dim,)), out=(out, shape, flat), residual_out=(residual_out, shape, flat))
     now = _now(x)
     kinds = [_f32_or_bf16(x, "x", now), 0, 0]
     if residual is not None:
@@ -861,7 +875,6 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
     of32 = _f32_or_bf16(out, "out", now)
-    _covers(weight=(weight, dim), out=(out, T * heads * dim), residual_out=(residual_out, T * heads * dim))
     _check("tern_rms_norm", lib().tern_rms_norm(
         x.data_ptr(), kinds[0], xt, xh, None if residual is None else residual.data_ptr(), kinds[1], rt, rh,
         None if gate is None else gate.data_ptr(), kinds[2], gt, gh, _GATES[gate_act],
@@ -873,8 +886,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
 
 def _states(T: int, slots, dst_slots, past, q_start, max_new, now: int):
     """(slots, dst_slots, past, q_start pointers, B, max_new) of the sequences of a call."""
-    B, i32 = slots.numel(), torch.int32
-    _covers(dst_slots=(dst_slots, B), past=(past, B), q_start=(q_start, B + 1))
+    B, i32, one = slots.numel(), torch.int32, slots.shape
+    if len(one) != 1 or (dst_slots is not None and dst_slots.shape != one) or (past is not None and past.shape != one) or (
+            q_start is not None and q_start.shape != (B + 1,)):
+        _shaped(slots=(slots, (B,)), dst_slots=(dst_slots, (B,)), past=(past, (B,)), q_start=(q_start, (B + 1,)))
     return (_ptr(slots, i32, "slots", now), _opt(dst_slots, i32, "dst_slots", now), _opt(past, i32, "past", now),
             _opt(q_start, i32, "q_start", now), B, T if max_new is None else max_new)
 
@@ -900,11 +915,12 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, slots
     W = weight.shape[1]
     if state.dim() != 3 or state.shape[1:] != (W - 1, C):
         raise ValueError(f"state must be [pool, {W - 1}, {C}], got {tuple(state.shape)}")
+    if (bias is not None and bias.shape != (C,)) or (out is not None and out.shape != x.shape):
+        _shaped(bias=(bias, (C,)), out=(out, (T, C)))
     now = _now(x)
     kind = _f32_or_bf16(x, "x", now)
     if out is None:
         out = _new((T, C), torch.bfloat16, x.device, stream)
-    _covers(out=(out, T * C), bias=(bias, C))
     sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new, now)
     _check("tern_short_conv", lib().tern_short_conv(
         x.data_ptr(), kind, x.stride(0) if T > 1 else C, _ptr(weight, torch.float32, "weight", now), W,
@@ -948,22 +964,24 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     dst_slots as short_conv's.  scale 1/sqrt(Dk) if not given.  qk_norm divides
     queries and keys by their lengths.  With a_log and dt_bias (fp32 [v_heads])
     the gates come raw: g <- -exp(a_log) softplus(g + dt_bias), beta <-
-    sigmoid(beta).  Returns bf16 [T, v_heads, Dv]."""
+    sigmoid(beta).  Returns bf16 [T, v_heads, Dv] (out may be [T, v_heads * Dv])."""
     if state.dim() != 4:
         raise ValueError("state must be [pool, v_heads, Dv, Dk]")
     pool, Hv, Dv, Dk = state.shape
     bf16, f32, now = torch.bfloat16, torch.float32, _now(q)
     T, Hk, qs, ks, vs, gs, bs = _delta_strides(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), g.shape,
                                                g.stride(), beta.shape, beta.stride(), Hv, Dv, Dk)
+    if (a_log is None) != (dt_bias is None):
+        raise ValueError("a_log and dt_bias come together")
+    if (a_log is not None and (a_log.shape != (Hv,) or dt_bias.shape != (Hv,))) or (
+            out is not None and out.shape != (T, Hv, Dv)):
+        _shaped(a_log=(a_log, (Hv,)), dt_bias=(dt_bias, (Hv,)), out=(out, (T, Hv, Dv), (T, Hv * Dv)))
     for name, t, kind in (("q", q, bf16), ("k", k, bf16), ("v", v, bf16), ("g", g, f32), ("beta", beta, f32)):
         if t.dtype is not kind or t.get_device() != now:
             _refuse(t, name, now)
             raise TypeError(f"{name} must be {kind}, got {t.dtype}")
-    if (a_log is None) != (dt_bias is None):
-        raise ValueError("a_log and dt_bias come together")
     if out is None:
         out = _new((T, Hv, Dv), bf16, q.device, stream)
-    _covers(out=(out, T * Hv * Dv), a_log=(a_log, Hv), dt_bias=(dt_bias, Hv))
     sl, dl, pp, qp, B, max_new = _states(T, slots, dst_slots, past, q_start, max_new, now)
     # (a few tokens take none: not asked for)
     need = int(lib().tern_gated_delta_workspace_bytes(B, T, max_new if q_start is not None else T // max(B, 1), Hv, Dk, Dv)) \

@@ -128,6 +128,40 @@ def test_delta_binding(tern):
     assert tern._gate_stride("g", (3, 4), (16, 1), 3, 4) == 16 and tern._gate_stride("g", (1, 4), (0, 1), 1, 4) == 4
 
 
+def test_binding_takes_no_other_shapes(tern):
+    """A tensor of another shape with elements enough would give numbers, not an error."""
+    bf, i32 = torch.bfloat16, torch.int32
+    x, w = torch.zeros(3, 4, 64), torch.ones(64)
+    for name, kw in (("weight", dict(weight=torch.ones(4, 64))), ("weight", dict(weight=torch.ones(65))),
+                     ("weight", dict(weight=torch.ones(63))), ("out", dict(out=torch.zeros(4, 4, 64))),
+                     ("out", dict(out=torch.zeros(3, 64, 4))), ("out", dict(out=torch.zeros(12, 64))),
+                     ("residual_out", dict(residual=x, residual_out=torch.zeros(64, 4, 3))),
+                     ("residual_out", dict(residual=x, residual_out=torch.zeros(4, 4, 64)))):
+        with pytest.raises(ValueError, match=f"^{name} must be"):
+            tern.rms_norm(**{**dict(x=x, weight=w), **kw})
+    for kw in (dict(out=torch.zeros(3, 4, 64)), dict(out=torch.zeros(3, 256)),
+               dict(residual=x, residual_out=torch.zeros(3, 256))):   # (these get as far as the device)
+        with pytest.raises(TypeError, match="x must be"):
+            tern.rms_norm(x, w, **kw)
+    x, slots = torch.zeros(3, 64), torch.zeros(1, dtype=i32)
+    for name, kw in (("bias", dict(bias=torch.zeros(65))), ("bias", dict(bias=torch.zeros(64, 1))),
+                     ("out", dict(out=torch.zeros(4, 64))), ("out", dict(out=torch.zeros(64, 3)))):
+        with pytest.raises(ValueError, match=f"^{name} must be"):
+            tern.short_conv(x, torch.zeros(64, 4), torch.zeros(2, 3, 64), slots, **kw)
+    q, v, g = torch.zeros(3, 2, 64, dtype=bf), torch.zeros(3, 4, 32, dtype=bf), torch.zeros(3, 4)
+    h = torch.zeros(4)
+    for name, kw in (("a_log", dict(a_log=torch.zeros(5), dt_bias=h)), ("dt_bias", dict(a_log=h, dt_bias=torch.zeros(1, 4))),
+                     ("out", dict(out=torch.zeros(4, 4, 32))), ("out", dict(out=torch.zeros(3, 32, 4)))):
+        with pytest.raises(ValueError, match=f"^{name} must be"):
+            tern.gated_delta(q, q, v, g, g, torch.zeros(2, 4, 32, 64), slots, **kw)
+    two = torch.zeros(2, dtype=i32)
+    for name, (sl, dst, past, start) in (("slots", (torch.zeros(2, 1, dtype=i32), None, None, None)), ("dst_slots", (slots, two, None, None)),
+                                         ("past", (slots, None, two, None)), ("q_start", (slots, None, None, slots)),
+                                         ("q_start", (two, None, None, torch.zeros(4, dtype=i32)))):
+        with pytest.raises(ValueError, match=f"^{name} must be"):
+            tern._states(4, sl, dst, past, start, None, -2)
+
+
 def test_wait_selftest_refuses(tern):
     for which, limit in ((2, 1000), (5, 1000), (tern.SELFTEST_DELTA, 0), (tern.SELFTEST_DELTA, 1000001),
                          (tern.SELFTEST_NORM, 0), (tern.SELFTEST_NORM, 1000001)):
