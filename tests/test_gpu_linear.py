@@ -379,6 +379,48 @@ def test_delta_in_pieces_and_whole(tern, heads, lens):
     assert delta_call(tern, inputs, Dk ** -0.5, pool.clone(), sl, start, max(lens), need - 256)[0] == 4
 
 
+@pytest.mark.parametrize("heads", [(1, 2, 64, 48), (2, 2, 128, 128)])
+@pytest.mark.parametrize("n", [64, 130, 640])
+@pytest.mark.parametrize("kind", ["one key", "two signs", "nearly one", "some zero", "one key, a little decay"])
+def test_delta_of_like_keys(tern, heads, n, kind):
+    """Keys that depend on one another as far as keys can, full steps and (but in one) no decay: every entry of A
+    is 1, -1 or 0 and all of T counts; whole and, of 640 tokens, in pieces.
+
+    Bounds.  A token adds roundings of at most 2^-17 R to a row of S (R its length plus the largest |v|): those
+    of its u, of what is taken of the u before it, of its key's share.  The products with I - k k^T do not make
+    them grow.  Their sum over n tokens is at most n 2^-17 R; as roundings of no one sign its length is at most
+    sqrt(3 n) 2^-17 times that of R.  out reads it with |q| <= 1 and is rounded: 2^-8 at most, in length
+    2^-7 / sqrt(12)."""
+    Hk, Hv, Dk, Dv = heads
+    g = gen(n + Dk)
+    q, k, v, a, b, _, _ = delta_inputs(n, *heads, g)
+    k = k.clone()
+    one = rand((1, Hk, Dk), g)
+    if kind in ("one key", "one key, a little decay"):
+        k.copy_(one.expand_as(k))
+    elif kind == "two signs":
+        k.copy_(one * (1 - 2 * (torch.arange(n, device="cuda") % 2)).view(-1, 1, 1))
+    elif kind == "nearly one":
+        k.copy_(one + 1e-2 * rand(k.shape, g))
+    else:
+        k[torch.rand(n, generator=g, device="cuda") < 0.4] = 0.0
+    a.fill_(-1e-3 if "decay" in kind else 0.0)
+    b.fill_(1.0)
+    inputs, pool = (q, k, v, a, b, None, None), rand((1, Hv, Dv, Dk), g)
+    want, new, reach, _ = ref.gated_delta(f64(q), f64(k), f64(v), f64(a), f64(b), f64(pool), [0], [0, n], Dk ** -0.5, True)
+    need = tern.lib().tern_gated_delta_workspace_bytes(1, n, n, Hv, Dk, Dv)
+    assert (need > 0) == (n == 640)
+    for ws in {0, need}:
+        state = pool.clone()
+        status, out = delta_call(tern, inputs, Dk ** -0.5, state, [0], [0, n], n, ws)
+        assert status == 0 and tern.device_error() == 0
+        worst, length = n * 2.0 ** -17 * reach, (3 * n) ** 0.5 * 2.0 ** -17 * np.linalg.norm(reach) * Dv ** 0.5
+        within(state, new, worst[None, :, None, None], "state")
+        assert np.linalg.norm(f64(state) - new) <= length
+        within(out, want, 2.0 ** -8 * np.abs(want) + Dk ** -0.5 * worst[None, :, None], "delta")
+        assert np.linalg.norm(f64(out) - want) <= 2.0 ** -7 / 12 ** 0.5 * np.linalg.norm(want) + Dk ** -0.5 * length * n ** 0.5
+
+
 @pytest.mark.parametrize("n", [1, 6, 70, 640])
 def test_delta_extreme_gates(tern, n):
     """Decays of 0 (-inf, far below fp32's least), of 1, steps of 0 and 1, in one sequence."""
