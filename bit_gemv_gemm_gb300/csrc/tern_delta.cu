@@ -29,7 +29,7 @@ constexpr int kStepTokens = 24;
 // loads are 128 bytes in a piece.  A warp holds 4 x ROWS rows.
 template <int DK>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArgs a) {
-    constexpr int V4 = DK / 32, ROWS = 256 / DK, PER_WARP = 4 * ROWS, PER_CTA = 4 * PER_WARP, MY = DK / 32;
+    constexpr int V4 = DK / 32, ROWS = 256 / DK, PER_WARP = 4 * ROWS, PER_CTA = 4 * PER_WARP;
     __shared__ __align__(16) float ks[kStepBatch][DK], qs[kStepBatch][DK];
     __shared__ float4 gates[kStepBatch];          // decay, beta, k.q, unused
     __shared__ float vs[kStepBatch][PER_CTA];
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane % 8;
-    const int h = blockIdx.y, row0 = blockIdx.x * PER_CTA, hk = h / a.group;
+    const int h = blockIdx.y, row0 = blockIdx.x * PER_CTA;
     const StateSeq s = load_state_seq(a.s, blockIdx.z, &g_delta_error);
     const int live = min(PER_CTA, a.dv - row0);
 
@@ -59,43 +59,9 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
         // a warp a token: its query and key (divided by their lengths), its gates and values
         for (int i = warp; i < n; i += 4) {
             const long long t = s.t0 + t0 + i;
-            const __nv_bfloat16* kp = a.k + t * a.k_token + hk * DK + MY * lane;
-            const __nv_bfloat16* qp = a.q + t * a.q_token + hk * DK + MY * lane;
-            float k[MY], q[MY], kk = 0.0f, qq = 0.0f, kq = 0.0f;
-#pragma unroll
-            for (int e = 0; e < MY; e += 2) {
-                const float2 k2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kp + e));
-                const float2 q2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qp + e));
-                k[e] = k2.x;
-                k[e + 1] = k2.y;
-                q[e] = q2.x;
-                q[e + 1] = q2.y;
-            }
             for (int r = lane; r < live; r += 32)
                 vs[i][r] = __bfloat162float(a.v[t * a.v_token + (long long)h * a.dv + row0 + r]);
-#pragma unroll
-            for (int e = 0; e < MY; ++e) {
-                kk = fmaf(k[e], k[e], kk);
-                qq = fmaf(q[e], q[e], qq);
-                kq = fmaf(k[e], q[e], kq);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                kk += __shfl_xor_sync(0xffffffffu, kk, o);
-                qq += __shfl_xor_sync(0xffffffffu, qq, o);
-                kq += __shfl_xor_sync(0xffffffffu, kq, o);
-            }
-            const float ik = a.norm ? 1.0f / sqrtf(kk + kDeltaNormEps) : 1.0f;
-            const float iq = (a.norm ? 1.0f / sqrtf(qq + kDeltaNormEps) : 1.0f) * a.scale;
-#pragma unroll
-            for (int e = 0; e < MY; ++e) {
-                ks[i][MY * lane + e] = k[e] * ik;
-                qs[i][MY * lane + e] = q[e] * iq;
-            }
-            if (lane == 0) {
-                const float2 gb = delta_gates(delta_head(a, h), delta_raw_gates(a, t, h));
-                gates[i] = make_float4(expf(gb.x), gb.y, kq * ik * iq, 0.0f);
-            }
+            delta_stage<DK>(a, t, h, lane, ks[i], qs[i], &gates[i]);
         }
         __syncthreads();
         for (int i = 0; i < n; ++i) {

@@ -100,6 +100,48 @@ __device__ __forceinline__ float2 delta_gates(const DeltaHead& head, float2 raw)
     return make_float2(g < -200.0f ? -200.0f : g, b);
 }
 
+// What a token is to the rows of S: its key and query, divided by their lengths and times the
+// scale where they are to be, and its decay, step and k.q.  A warp each.
+template <int DK>
+__device__ __forceinline__ void delta_stage(const DeltaArgs& a, long long t, int h, int lane, float* k_to, float* q_to, float4* gate_to) {
+    constexpr int MY = DK / 32;
+    const __nv_bfloat16* kp = a.k + t * a.k_token + h / a.group * DK + MY * lane;
+    const __nv_bfloat16* qp = a.q + t * a.q_token + h / a.group * DK + MY * lane;
+    float k[MY], q[MY], kk = 0.0f, qq = 0.0f, kq = 0.0f;
+#pragma unroll
+    for (int e = 0; e < MY; e += 2) {
+        const float2 k2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kp + e));
+        const float2 q2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(qp + e));
+        k[e] = k2.x;
+        k[e + 1] = k2.y;
+        q[e] = q2.x;
+        q[e + 1] = q2.y;
+    }
+#pragma unroll
+    for (int e = 0; e < MY; ++e) {
+        kk = fmaf(k[e], k[e], kk);
+        qq = fmaf(q[e], q[e], qq);
+        kq = fmaf(k[e], q[e], kq);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        kk += __shfl_xor_sync(0xffffffffu, kk, o);
+        qq += __shfl_xor_sync(0xffffffffu, qq, o);
+        kq += __shfl_xor_sync(0xffffffffu, kq, o);
+    }
+    const float ik = a.norm ? 1.0f / sqrtf(kk + kDeltaNormEps) : 1.0f;
+    const float iq = (a.norm ? 1.0f / sqrtf(qq + kDeltaNormEps) : 1.0f) * a.scale;
+#pragma unroll
+    for (int e = 0; e < MY; ++e) {
+        k_to[MY * lane + e] = k[e] * ik;
+        q_to[MY * lane + e] = q[e] * iq;
+    }
+    if (lane == 0) {
+        const float2 gb = delta_gates(delta_head(a, h), delta_raw_gates(a, t, h));
+        *gate_to = make_float4(expf(gb.x), gb.y, kq * ik * iq, 0.0f);
+    }
+}
+
 // A warp's wait.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t tries = kWaitTries) {
     return __all_sync(0xffffffffu, wait_tries(bar, parity, tries));

@@ -32,6 +32,11 @@
 // are applied in fp32, to rows and columns of results.  Exponents are differences of G, at
 // most 0, and G is a sum in 64 bits kept as two fp32: a long or strong decay before
 // a pair of tokens does not blur theirs.
+//
+// A value that is not finite would reach back: T and P are 0 above their diagonals, and
+// 0 x NaN is NaN.  It also stays in its rows of S for good, so those that are not finite
+// at the end go once more, token by token, up to where they are not (redo): no code in the
+// loops above (masks in X and A took 8 % of the time where sequences go in pieces).
 #include "tern_delta.cuh"
 #include "tern_sm100.cuh"
 
@@ -75,7 +80,7 @@ struct Cfg {
     static constexpr int kABytes = 2 * (int)kATile + 4 * kDiagBlock * 4;   // A's two parts, its diagonal blocks
     static constexpr size_t kKq = 0, kV = kKq + (size_t)kKqStages * kKqBytes, kTp = kV + (size_t)kVStages * kVBytes,
                             kA = kTp + (size_t)kTpStages * kTpBytes, kCoef = kA + (size_t)kAStages * kABytes, kBar = kCoef + kCoefStages * sizeof(Coef),
-                            kMisc = kBar + 48 * 8, kSmem = kMisc + 64 + 1024;
+                            kMisc = kBar + 48 * 8, kSmem = kMisc + 128 + 1024;
 };
 // warps: the chain, the output, A and P, T, then one each for products and copies and two for decays
 constexpr int kOutWarp = 16, kGramWarp = 20, kInvWarp = 24, kMmaWarp = 28, kTmaWarp = 29, kCoefWarp = 30, kThreads = 32 * 32;
@@ -101,6 +106,13 @@ enum { S_READY = 1, X_READY, UP_READY, U2_READY, TURNS = 4 };
 constexpr int kChainThreads = 512 + 32;
 __device__ __forceinline__ void chain_arrive(int b) { asm volatile("bar.arrive %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
 __device__ __forceinline__ void chain_wait(int b) { asm volatile("bar.sync %0, %1;" ::"r"(b), "n"(kChainThreads) : "memory"); }
+// The chain's warps alone; true if `x` is, of any thread.
+__device__ __forceinline__ void chain_sync() { asm volatile("bar.sync 5, 512;" ::: "memory"); }
+__device__ __forceinline__ bool chain_any(bool x) {
+    uint32_t any;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 5, 512, p;\nselp.u32 %0, 1, 0, q;\n}" : "=r"(any) : "r"((uint32_t)x) : "memory");
+    return any != 0;
+}
 __device__ __forceinline__ void chain_rest(int turn, int chunks) {   // the turns from `turn` on
 #pragma unroll 1
     for (; turn < TURNS * chunks; ++turn) chain_wait(S_READY + turn % TURNS);
@@ -264,11 +276,155 @@ __device__ __forceinline__ int by_length(const StateSeqView& s, int y) {
     return (y & ~31) + __ffs(__ballot_sync(0xffffffffu, before == (y & 31))) - 1;
 }
 
+// What of a head a CTA has: the rows from row0 on of `rows`, the piece, whether it has the unit
+// matrix in place of S.
+struct Part {
+    int h, row0, rows, piece;
+    bool moves;
+};
+// S before the first token, of a thread's columns and row: the pool's, or a piece's
+template <int DK>
+__device__ __forceinline__ void first_state(const DeltaArgs& a, const StateSeq& s, const Part& p, float (&S)[DK / 4], int quarter, int row) {
+    constexpr int COLS = DK / 4;
+    if (p.piece > 0) {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) S[i] = p.moves && COLS * quarter + i == row ? 1.0f : 0.0f;
+    } else {
+        const float4* from = reinterpret_cast<const float4*>(
+            a.state + (((long long)s.src * a.v_heads + p.h) * a.dv + p.row0 + row) * DK + COLS * quarter);
+#pragma unroll
+        for (int i = 0; i < COLS / 4; ++i) {
+            const float4 x = s.src >= 0 && p.row0 + row < p.rows ? from[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            S[4 * i] = x.x;
+            S[4 * i + 1] = x.y;
+            S[4 * i + 2] = x.z;
+            S[4 * i + 3] = x.w;
+        }
+    }
+}
+// S after the last goes to the pool, or to where the join finds it: a sequence of more than one piece
+template <int DK, bool PIECES>
+__device__ __forceinline__ void last_state(const DeltaArgs& a, const StateSeq& s, const Part& p, const float (&S)[DK / 4], int quarter, int row) {
+    constexpr int COLS = DK / 4;
+    float* to_head = s.dst >= 0 && (s.n > 0 || s.dst != s.src) ? a.state + ((long long)s.dst * a.v_heads + p.h) * a.dv * DK : nullptr;
+    unsigned char* parts = nullptr;
+    if constexpr (PIECES) {
+        const int all = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error).n;
+        if (all > delta_piece_chunks(a.p, all) * kTok) {
+            const long long at = (long long)blockIdx.y * a.v_heads + p.h;
+            to_head = a.p.state + (at * a.p.count + p.piece) * ((long long)a.dv * DK);
+            if (p.piece == 0) parts = delta_parts(a.p, blockIdx.y, a.v_heads, p.h, DK, (a.dv + kRows - 1) / kRows, p.row0 / kRows, 0);
+            if (p.moves) parts = a.p.move + (at * (a.p.count - 1) + p.piece - 1) * delta_parts_bytes(DK, DK);
+        }
+        if (p.piece > 0 && s.n == 0) to_head = nullptr;
+    }
+    if (to_head) {
+        float4* to = reinterpret_cast<float4*>(to_head + (p.row0 + row) * DK + COLS * quarter);
+        if (!p.moves) {
+#pragma unroll
+            for (int i = 0; i < COLS / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
+        if (PIECES && parts) {
+#pragma unroll
+            for (int i = 0; i < COLS; i += 8) put_parts8(parts, p.moves ? DK : kRows, DK, row, COLS * quarter + i, S + i);
+        }
+    }
+}
+__device__ __forceinline__ bool row_is_odd(const uint32_t* odd_rows, int w, int l) {
+    return ((odd_rows[w & 3] | odd_rows[4 + (w & 3)] | odd_rows[8 + (w & 3)] | odd_rows[12 + (w & 3)]) >> l & 1u) != 0;
+}
+// Rows that are not finite at the end, token by token, by the chain's warps once the roles have met: a
+// thread has its columns of its row again; a token's key, query and gates are in shared memory, where
+// the keys were, with four partial sums a row.  Outputs are written over up to where a row is not finite.
+template <int DK, bool PIECES>
+__device__ __noinline__ void redo(const DeltaArgs& a, const StateSeq s, const Part p, const uint32_t* odd_rows, unsigned char* smem) {
+    constexpr int COLS = DK / 4;
+    constexpr int kBatch = 16;
+    struct Staged {
+        float k[kBatch][DK], q[kBatch][DK];
+        float4 gate[kBatch];
+        float2 part[2][4][kRows];
+    };
+    static_assert(sizeof(Staged) <= (size_t)kKqStages * Cfg<DK>::kKqBytes, "in the keys' place");
+    Staged& st = *reinterpret_cast<Staged*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp >> 2, row = (warp & 3) * 32 + lane;
+    const bool mine = p.row0 + row < p.rows && row_is_odd(odd_rows, warp, lane);
+    bool left = mine;   // still finite
+    float S[COLS];
+    first_state<DK>(a, s, p, S, quarter, row);
+    {
+        float nothing = 0.0f;
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) nothing = fmaf(S[e], 0.0f, nothing);
+        st.part[0][quarter][row] = make_float2(nothing, 0.0f);
+        chain_sync();
+        for (int i = 0; i < 4; ++i) left = left && st.part[0][i][row].x == 0.0f;
+    }
+#pragma unroll 1
+    for (int t0 = 0; t0 < s.n; t0 += kBatch) {
+        if (!chain_any(left)) break;
+        const int n = min(kBatch, s.n - t0);
+        if (warp < n) delta_stage<DK>(a, s.t0 + t0 + warp, p.h, lane, st.k[warp], st.q[warp], &st.gate[warp]);
+        chain_sync();
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const float* k = st.k[i] + COLS * quarter;
+            const float* q = st.q[i] + COLS * quarter;
+            float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) {
+                sk = fmaf(S[e], k[e], sk);
+                sq = fmaf(S[e], q[e], sq);
+            }
+            st.part[i & 1][quarter][row] = make_float2(sk, sq);
+            chain_sync();   // (the other half of part is not written again before all have come to the next)
+            sk = sq = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 two = st.part[i & 1][x][row];
+                sk += two.x;
+                sq += two.y;
+            }
+            const float4 gate = st.gate[i];
+            const int token = t0 + i;
+            const float v = mine && !p.moves ? __bfloat162float(a.v[(s.t0 + token) * a.v_token + (long long)p.h * a.dv + p.row0 + row]) : 0.0f;
+            const float u = gate.y * (v - gate.x * sk), out = fmaf(u, gate.z, gate.x * sq);
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) S[e] = fmaf(u, k[e], gate.x * S[e]);
+            if (left && quarter == 0) {
+                if (!PIECES || p.piece == 0) {
+                    a.out[((s.t0 + token) * (long long)a.v_heads + p.h) * a.dv + p.row0 + row] = __float2bfloat16(out);
+                } else {
+                    const StateSeq whole = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
+                    const long long chunk = delta_piece_chunk(a.p.count, whole.t0, blockIdx.y) + (p.piece - 1) * delta_piece_chunks(a.p, whole.n) + token / kTok;
+                    const long long tile = ((chunk * a.v_heads + p.h) * p.rows + p.row0) * (kTok * 4);   // as the output warps have it
+                    const int t = token % kTok;
+                    if (p.moves) {
+                        uint32_t hi, lo;
+                        split2(out, 0.0f, hi, lo);
+                        unsigned char* to = a.p.out_move + tile + row / 64 * (kTok * 128) + t * 128 + ((row % 64 / 8 ^ (t & 7)) << 4) + 2 * (row & 7);
+                        *reinterpret_cast<unsigned short*>(to) = (unsigned short)hi;
+                        *reinterpret_cast<unsigned short*>(to + DK * 128) = (unsigned short)lo;
+                    } else {
+                        reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(a.p.out) + tile)[t * min(kRows, p.rows - p.row0) + row] = out;
+                    }
+                }
+            }
+            left = left && fabsf(u) < INFINITY;
+        }
+    }
+    if (mine) {
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) S[e] = left ? S[e] : NAN;
+        last_state<DK, PIECES>(a, s, p, S, quarter, row);
+    }
+}
+
 template <int DK, bool PIECES>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_out,
-                   const DeltaArgs a) {
+                   const __grid_constant__ DeltaArgs a) {
     using C = Cfg<DK>;
     constexpr int NC = C::NC, COLS = C::COLS;
     extern __shared__ __align__(1024) unsigned char smem_dyn[];
@@ -277,6 +433,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + (uint32_t)C::kBar + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
+    uint32_t* const odd_rows = tmem_slot + 16;   // [chain's warps] rows of S that are not finite at the end, of its quarter
     Coef* const coefs = reinterpret_cast<Coef*>(smem + C::kCoef);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -319,6 +476,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         s.t0 += piece * per;
         s.n = max(n, 0);
     }
+    const Part part{h, row0, rows, piece, moves};
     const int chunks = (s.n + kTok - 1) / kTok;
     auto fail = [&] { report_device_error(&g_delta_chunk_error, TERN_DEVERR_DELTA_WAIT); };
     auto wait_warp = [&](int b, uint32_t parity) { return tern::wait_warp(bar(b), parity); };
@@ -338,21 +496,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = mine + T_S + (uint32_t)(COLS * quarter), tk = mine + T_KS + 16u * quarter;
         float S[COLS];
-        if (piece > 0) {
-#pragma unroll
-            for (int i = 0; i < COLS; ++i) S[i] = moves && COLS * quarter + i == row ? 1.0f : 0.0f;
-        } else {
-            const float4* from = reinterpret_cast<const float4*>(
-                a.state + (((long long)s.src * a.v_heads + h) * a.dv + row0 + row) * DK + COLS * quarter);
-#pragma unroll
-            for (int i = 0; i < COLS / 4; ++i) {
-                const float4 x = s.src >= 0 && live ? from[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                S[4 * i] = x.x;
-                S[4 * i + 1] = x.y;
-                S[4 * i + 2] = x.z;
-                S[4 * i + 3] = x.w;
-            }
-        }
+        first_state<DK>(a, s, part, S, quarter, row);
         // S = e^G_last S + D of a chunk; its parts in place of D
         auto next_state = [&](int c, bool more) {
             if (c >= 0) {
@@ -467,30 +611,13 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (lane == 0) fail();
             chain_rest(lost, chunks);
         }
-        // S goes to the pool, or to where the join finds it: a sequence of more than one piece
-        float* to_head = s.dst >= 0 && (s.n > 0 || s.dst != s.src) ? a.state + ((long long)s.dst * a.v_heads + h) * a.dv * DK : nullptr;
-        unsigned char* parts = nullptr;
-        if constexpr (PIECES) {
-            const int all = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error).n;
-            if (all > delta_piece_chunks(a.p, all) * kTok) {
-                const long long at = (long long)blockIdx.y * a.v_heads + h;
-                to_head = a.p.state + (at * a.p.count + piece) * ((long long)a.dv * DK);
-                if (piece == 0) parts = delta_parts(a.p, blockIdx.y, a.v_heads, h, DK, (a.dv + kRows - 1) / kRows, row0 / kRows, 0);
-                if (moves) parts = a.p.move + (at * (a.p.count - 1) + piece - 1) * delta_parts_bytes(DK, DK);
-            }
-            if (piece > 0 && s.n == 0) to_head = nullptr;
-        }
-        if (ok && live && to_head) {
-            float4* to = reinterpret_cast<float4*>(to_head + (row0 + row) * DK + COLS * quarter);
-            if (!moves) {
+        float nothing = 0.0f;   // 0, or NaN
 #pragma unroll
-                for (int i = 0; i < COLS / 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-            }
-            if (PIECES && parts) {
-#pragma unroll
-                for (int i = 0; i < COLS; i += 8) put_parts8(parts, moves ? DK : kRows, DK, row, COLS * quarter + i, S + i);
-            }
-        }
+        for (int e = 0; e < COLS; ++e) nothing = fmaf(S[e], 0.0f, nothing);
+        const uint32_t odd = __ballot_sync(0xffffffffu, ok && live && !(nothing == 0.0f));
+        if (lane == 0) odd_rows[warp] = odd;
+        chain_sync();
+        if (ok && live && !row_is_odd(odd_rows, warp, lane)) last_state<DK, PIECES>(a, s, part, S, quarter, row);
         __syncwarp();
     } else if (warp < kGramWarp) {
         // ------------------------------ the output ------------------------------
@@ -1052,6 +1179,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    uint32_t any_odd = 0;
+#pragma unroll 1
+    for (int i = 0; i < kOutWarp; ++i) any_odd |= odd_rows[i];
+    if (any_odd && warp < kOutWarp) redo<DK, PIECES>(a, s, part, odd_rows, smem + C::kKq);
 }
 
 // [T][heads * dim] as the TMA sees it, a box of `box` values of 64 tokens.

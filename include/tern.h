@@ -586,8 +586,7 @@ tern_status tern_short_conv(const void *x, int x_is_f32, long long x_token, cons
  * dk 64 or 128, dv a multiple of 16, at most 256; |scale| finite (TERN_ERR_SHAPE).
  * Sequences of more than 24 tokens (max_new) go 64 tokens at a time, where the state,
  * what is taken to it and the weights of a chunk's own tokens are two bf16 values each in
- * the products (2^-17 of a value); there a value that is not finite may also reach the
- * tokens up to 63 before it in its sequence.
+ * the products (2^-17 of a value).
  * workspace: NULL, or tern_gated_delta_workspace_bytes(B, T, max_new, v_heads, dk, dv)
  * bytes (max_new T / B without q_start; TERN_ERR_WORKSPACE if it is smaller), 256-byte
  * aligned, any contents: with it, few heads of long sequences go in pieces at once (one

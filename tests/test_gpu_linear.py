@@ -521,6 +521,52 @@ def test_one_head_alone(tern):
         assert torch.isnan(got[2 * n - 1, 1]).any()
 
 
+@pytest.mark.parametrize("heads", [(1, 2, 64, 48), (2, 2, 128, 144)])
+@pytest.mark.parametrize("n", [20, 64, 100, 640])
+@pytest.mark.parametrize("what", ["q", "k", "v", "g", "beta", "v inf", "k inf", "beta inf"])
+def test_not_finite_goes_forward_only(tern, heads, n, what):
+    """One value that is not finite: the rows and heads that it does not concern are bit for bit as with a finite
+    one, and so is what comes before it but for roundings (its rows of S go token by token then: two results of
+    half a step, 2^-8, and of at most 2^-15 of scale memory R each); the rest is not finite where it is not in the
+    definition."""
+    Hk, Hv, Dk, Dv = heads
+    g = gen(n + Dv)
+    clean = [t.clone() for t in delta_inputs(n, *heads, g)[:5]]
+    pool = rand((1, Hv, Dv, Dk), g)
+    need = tern.lib().tern_gated_delta_workspace_bytes(1, n, n, Hv, Dk, Dv)
+    assert (need > 0) == (n == 640)
+    bad = float("inf" if "inf" in what else "nan")
+    _, _, reach, memory = ref.gated_delta(*(f64(t) for t in clean), f64(pool), [0], [0, n], Dk ** -0.5, True)
+    for ws in {0, need}:
+        state = pool.clone()
+        assert delta_call(tern, (*clean, None, None), Dk ** -0.5, state, [0], [0, n], n, ws)[0] == 0
+        state, fine = pool.clone(), state
+        want = delta_call(tern, (*clean, None, None), Dk ** -0.5, state, [0], [0, n], n, ws)[1]
+        assert torch.equal(state, fine)
+        for at in sorted({0, 3, 14, 17 % n, 35 % n, 47 % n, 63 % n, n // 2 + 7, n - 1}):
+            inputs = [t.clone() for t in clean]
+            i = {"q": 0, "k": 1, "v": 2, "g": 3, "beta": 4}[what.split()[0]]
+            inputs[i][(at, 0, 5)[:inputs[i].dim()]] = bad
+            state = pool.clone()
+            status, out = delta_call(tern, (*inputs, None, None), Dk ** -0.5, state, [0], [0, n], n, ws)
+            assert status == 0 and tern.device_error() == 0
+            hit = torch.zeros((n, Hv, Dv), dtype=torch.bool, device="cuda")       # what it concerns
+            if what.startswith("v"):
+                hit[at:, 0, 5] = True
+            elif what == "q":
+                hit[at, :Hv // Hk] = True
+            else:
+                hit[at:, :Hv // Hk if what.startswith("k") else 1] = True
+            assert torch.equal(torch.isfinite(out), ~hit), (at, torch.nonzero(torch.isfinite(out) == hit)[:4])
+            before = hit.any(0, keepdim=True).expand_as(hit) & ~hit if what != "q" else torch.zeros_like(hit)
+            assert torch.equal(out[~hit & ~before], want[~hit & ~before]), at
+            near = 2.0 ** -7 * np.abs(f64(want)) + (Dk ** -0.5 * 2.0 ** -14 * memory * reach)[None, :, None]
+            within(out[before], f64(want)[f64(before) > 0], near[f64(before) > 0], f"before {at}")
+            rows = hit[-1] if what != "q" else torch.zeros_like(hit[0])
+            assert torch.equal(state[0][~rows], fine[0][~rows]), at
+            assert not torch.isfinite(state[0][rows]).any(), at
+
+
 def test_another_stream_and_replays(tern):
     """The three calls captured once and replayed on new inputs, on a stream of their own."""
     g = gen(16)
