@@ -32,11 +32,6 @@ struct Shared {
     static_assert(delta_parts_bytes(DK, DK) <= kStage, "M in a stage");
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
-                 "r"(bytes), "r"(bar) : "memory");
-}
-
 // What both kinds of CTA have.
 template <int DK>
 struct Join {

@@ -81,12 +81,6 @@ __device__ __forceinline__ NormRow norm_row(const NormArgs& a, int row) {
     return NormRow{t * a.x_token + h * a.x_head, t * a.r_token + h * a.r_head, t * a.g_token + h * a.g_head};
 }
 
-// 16-byte pieces to shared memory, counted on `bar` in bytes.
-__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
-                 "r"(bytes), "r"(bar) : "memory");
-}
-
 // One piece of 8 values of one row.
 struct NormPiece {
     Raw8 x, r, g;
@@ -237,9 +231,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_stream_kernel(const NormAr
         const uint32_t to = sm100::smem_u32(rows + stage * ring.row_bytes), bar = sm100::smem_u32(&full[stage]);
         const uint32_t xb = a.dim * (a.x_f32 ? 4 : 2), rb = a.residual ? a.dim * (a.r_f32 ? 4 : 2) : 0, gb = a.gate ? a.dim * (a.g_f32 ? 4 : 2) : 0;
         sm100::mbar_arrive_expect_tx(bar, xb + rb + gb);
-        bulk_load(to, static_cast<const unsigned char*>(a.x) + at.x * (a.x_f32 ? 4 : 2), xb, bar);
-        if (rb) bulk_load(to + ring.r_at, static_cast<const unsigned char*>(a.residual) + at.r * (a.r_f32 ? 4 : 2), rb, bar);
-        if (gb) bulk_load(to + ring.g_at, static_cast<const unsigned char*>(a.gate) + at.g * (a.g_f32 ? 4 : 2), gb, bar);
+        sm100::bulk_load(to, static_cast<const unsigned char*>(a.x) + at.x * (a.x_f32 ? 4 : 2), xb, bar);
+        if (rb) sm100::bulk_load(to + ring.r_at, static_cast<const unsigned char*>(a.residual) + at.r * (a.r_f32 ? 4 : 2), rb, bar);
+        if (gb) sm100::bulk_load(to + ring.g_at, static_cast<const unsigned char*>(a.gate) + at.g * (a.g_f32 ? 4 : 2), gb, bar);
     };
     const int step = gridDim.x, count = (a.rows - 1 - (int)blockIdx.x) / step + 1;   // rows of this CTA
     if (threadIdx.x == 0)
@@ -350,7 +344,7 @@ __global__ void __launch_bounds__(64) norm_wait_selftest_kernel(uint32_t tries, 
     auto fetch = [&](int k) {
         const uint32_t bar = sm100::smem_u32(&full[k & 1]);
         sm100::mbar_arrive_expect_tx(bar, k == 2 ? 32 : 16);
-        bulk_load(sm100::smem_u32(rows[k & 1]), from, 16, bar);
+        sm100::bulk_load(sm100::smem_u32(rows[k & 1]), from, 16, bar);
     };
     if (threadIdx.x == 0) {
         fetch(0);
