@@ -32,7 +32,7 @@ struct DeltaArgs {
     float* state;                           // [pool][v_heads][dv][dk]
     __nv_bfloat16* out;                     // [T][v_heads][dv]
     int k_heads, v_heads, dk, dv, group, norm;
-    int by_length;                          // more CTAs than SMs: the longest sequences first
+    int by_length;                          // more CTAs than SMs: the longest of each 32 neighbours first
     float scale;
     DeltaPieces p;
 };
