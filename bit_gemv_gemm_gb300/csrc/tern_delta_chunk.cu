@@ -324,28 +324,38 @@ __device__ __forceinline__ bool row_is_odd(const uint32_t* odd_rows, int w, int 
     return ((odd_rows[w & 3] | odd_rows[4 + (w & 3)] | odd_rows[8 + (w & 3)] | odd_rows[12 + (w & 3)]) >> l & 1u) != 0;
 }
 // Rows that are not finite at the end, token by token, by the chain's warps once the roles have met: a
-// thread has its columns of its row again; a token's key, query and gates are in shared memory, where
-// the keys were, with four partial sums a row.  Outputs are written over up to where a row is not finite.
+// thread has its columns of its row again.  All is in shared memory, where the rings were: S by columns
+// (a function has too few registers for it: 4.8 us a token, 2.4 so), a token's key, query, values and gates,
+// and four partial sums a row.  Outputs are written over up to where a row is not finite.
 template <int DK, bool PIECES>
 __device__ __noinline__ void redo(const DeltaArgs& a, const StateSeq s, const Part p, const uint32_t* odd_rows, unsigned char* smem) {
     constexpr int COLS = DK / 4;
     constexpr int kBatch = 16;
     struct Staged {
-        float k[kBatch][DK], q[kBatch][DK];
+        float S[DK][kRows];
+        float k[kBatch][DK], q[kBatch][DK], v[kBatch][kRows];
         float4 gate[kBatch];
         float2 part[2][4][kRows];
     };
-    static_assert(sizeof(Staged) <= (size_t)kKqStages * Cfg<DK>::kKqBytes, "in the keys' place");
+    static_assert(sizeof(Staged) <= Cfg<DK>::kBar, "in the place of the roles' rings");
     Staged& st = *reinterpret_cast<Staged*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp >> 2, row = (warp & 3) * 32 + lane;
     const bool mine = p.row0 + row < p.rows && row_is_odd(odd_rows, warp, lane);
     bool left = mine;   // still finite
-    float S[COLS];
-    first_state<DK>(a, s, p, S, quarter, row);
+    long long first_chunk = 0;   // of the piece's, in the outputs
+    if (PIECES && p.piece > 0) {
+        const StateSeq whole = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
+        first_chunk = delta_piece_chunk(a.p.count, whole.t0, blockIdx.y) + (p.piece - 1) * delta_piece_chunks(a.p, whole.n);
+    }
+    float (*const S)[kRows] = reinterpret_cast<float (*)[kRows]>(&st.S[COLS * quarter][row]);   // this thread's: S[e][0]
     {
-        float nothing = 0.0f;
+        float first[COLS], nothing = 0.0f;
+        first_state<DK>(a, s, p, first, quarter, row);
 #pragma unroll
-        for (int e = 0; e < COLS; ++e) nothing = fmaf(S[e], 0.0f, nothing);
+        for (int e = 0; e < COLS; ++e) {
+            S[e][0] = first[e];
+            nothing = fmaf(first[e], 0.0f, nothing);
+        }
         st.part[0][quarter][row] = make_float2(nothing, 0.0f);
         chain_sync();
         for (int i = 0; i < 4; ++i) left = left && st.part[0][i][row].x == 0.0f;
@@ -354,17 +364,24 @@ __device__ __noinline__ void redo(const DeltaArgs& a, const StateSeq s, const Pa
     for (int t0 = 0; t0 < s.n; t0 += kBatch) {
         if (!chain_any(left)) break;
         const int n = min(kBatch, s.n - t0);
-        if (warp < n) delta_stage<DK>(a, s.t0 + t0 + warp, p.h, lane, st.k[warp], st.q[warp], &st.gate[warp]);
+        if (warp < n) {
+            const long long t = s.t0 + t0 + warp;
+            delta_stage<DK>(a, t, p.h, lane, st.k[warp], st.q[warp], &st.gate[warp]);
+            for (int i = lane; i < kRows; i += 32)
+                st.v[warp][i] = !p.moves && p.row0 + i < p.rows ? __bfloat162float(a.v[t * a.v_token + (long long)p.h * a.dv + p.row0 + i]) : 0.0f;
+        }
         chain_sync();
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const float* k = st.k[i] + COLS * quarter;
-            const float* q = st.q[i] + COLS * quarter;
+            const float4* k = reinterpret_cast<const float4*>(st.k[i] + COLS * quarter);
+            const float4* q = reinterpret_cast<const float4*>(st.q[i] + COLS * quarter);
             float sk = 0.0f, sq = 0.0f;
-#pragma unroll
-            for (int e = 0; e < COLS; ++e) {
-                sk = fmaf(S[e], k[e], sk);
-                sq = fmaf(S[e], q[e], sq);
+#pragma unroll 4
+            for (int e = 0; e < COLS / 4; ++e) {
+                const float4 k4 = k[e], q4 = q[e];
+                const float x = S[4 * e][0], y = S[4 * e + 1][0], z = S[4 * e + 2][0], w = S[4 * e + 3][0];
+                sk = fmaf(x, k4.x, fmaf(y, k4.y, fmaf(z, k4.z, fmaf(w, k4.w, sk))));
+                sq = fmaf(x, q4.x, fmaf(y, q4.y, fmaf(z, q4.z, fmaf(w, q4.w, sq))));
             }
             st.part[i & 1][quarter][row] = make_float2(sk, sq);
             chain_sync();   // (the other half of part is not written again before all have come to the next)
@@ -377,17 +394,21 @@ __device__ __noinline__ void redo(const DeltaArgs& a, const StateSeq s, const Pa
             }
             const float4 gate = st.gate[i];
             const int token = t0 + i;
-            const float v = mine && !p.moves ? __bfloat162float(a.v[(s.t0 + token) * a.v_token + (long long)p.h * a.dv + p.row0 + row]) : 0.0f;
-            const float u = gate.y * (v - gate.x * sk), out = fmaf(u, gate.z, gate.x * sq);
-#pragma unroll
-            for (int e = 0; e < COLS; ++e) S[e] = fmaf(u, k[e], gate.x * S[e]);
+            const float u = gate.y * (st.v[i][row] - gate.x * sk), out = fmaf(u, gate.z, gate.x * sq);
+#pragma unroll 4
+            for (int e = 0; e < COLS / 4; ++e) {
+                const float4 k4 = k[e];
+                S[4 * e][0] = fmaf(u, k4.x, gate.x * S[4 * e][0]);
+                S[4 * e + 1][0] = fmaf(u, k4.y, gate.x * S[4 * e + 1][0]);
+                S[4 * e + 2][0] = fmaf(u, k4.z, gate.x * S[4 * e + 2][0]);
+                S[4 * e + 3][0] = fmaf(u, k4.w, gate.x * S[4 * e + 3][0]);
+            }
             if (left && quarter == 0) {
                 if (!PIECES || p.piece == 0) {
                     a.out[((s.t0 + token) * (long long)a.v_heads + p.h) * a.dv + p.row0 + row] = __float2bfloat16(out);
                 } else {
-                    const StateSeq whole = load_state_seq(a.s, blockIdx.y, &g_delta_chunk_error);
-                    const long long chunk = delta_piece_chunk(a.p.count, whole.t0, blockIdx.y) + (p.piece - 1) * delta_piece_chunks(a.p, whole.n) + token / kTok;
-                    const long long tile = ((chunk * a.v_heads + p.h) * p.rows + p.row0) * (kTok * 4);   // as the output warps have it
+                    // as the output warps have it
+                    const long long tile = (((first_chunk + token / kTok) * a.v_heads + p.h) * p.rows + p.row0) * (kTok * 4);
                     const int t = token % kTok;
                     if (p.moves) {
                         uint32_t hi, lo;
@@ -404,9 +425,10 @@ __device__ __noinline__ void redo(const DeltaArgs& a, const StateSeq s, const Pa
         }
     }
     if (mine) {
+        float last[COLS];
 #pragma unroll
-        for (int e = 0; e < COLS; ++e) S[e] = left ? S[e] : NAN;
-        last_state<DK, PIECES>(a, s, p, S, quarter, row);
+        for (int e = 0; e < COLS; ++e) last[e] = left ? S[e][0] : NAN;
+        last_state<DK, PIECES>(a, s, p, last, quarter, row);
     }
 }
 
@@ -1172,7 +1194,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     uint32_t any_odd = 0;
 #pragma unroll 1
     for (int i = 0; i < kOutWarp; ++i) any_odd |= odd_rows[i];
-    if (any_odd && warp < kOutWarp) redo<DK, PIECES>(a, s, part, odd_rows, smem + C::kKq);
+    if (any_odd && warp < kOutWarp) redo<DK, PIECES>(a, s, part, odd_rows, smem);
 }
 
 // [T][heads * dim] as the TMA sees it, a box of `box` values of 64 tokens.
