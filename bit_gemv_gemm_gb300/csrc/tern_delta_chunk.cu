@@ -626,7 +626,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         float nothing = 0.0f;   // 0, or NaN
 #pragma unroll
         for (int e = 0; e < COLS; ++e) nothing = fmaf(S[e], 0.0f, nothing);
-        const uint32_t odd = __ballot_sync(0xffffffffu, ok && live && !(nothing == 0.0f));
+        const uint32_t odd = __ballot_sync(0xffffffffu, ok && live && chunks > 0 && !(nothing == 0.0f));   // (without tokens S moves as it is)
         if (lane == 0) odd_rows[warp] = odd;
         chain_sync();
         if (ok && live && !row_is_odd(odd_rows, warp, lane)) last_state<DK, PIECES>(a, s, part, S, quarter, row);

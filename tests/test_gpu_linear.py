@@ -567,6 +567,47 @@ def test_not_finite_goes_forward_only(tern, heads, n, what):
             assert not torch.isfinite(state[0][rows]).any(), at
 
 
+@pytest.mark.parametrize("lens", [[0, 40, 70], [0, 40, 900, 3], [0, 40, 130] + [70] * 40])
+def test_states_that_are_not_finite(tern, lens):
+    """A value of a state that is not finite takes its row with it, in its own sequence; a state that only moves
+    keeps it where it is; a value among the tokens of a sequence that is not stored, of one among many."""
+    Hk, Hv, Dk, Dv = 2, 8, 64, 48
+    B, g = len(lens), gen(31)
+    start, T = sequences(lens)
+    inputs = delta_inputs(T, Hk, Hv, Dk, Dv, g)
+    pool = rand((2 * B, Hv, Dv, Dk), g)
+    sl, dst = list(range(B)), [B + b if b != 2 else -1 for b in range(B)]
+
+    def run(inputs, pool):
+        state = pool.clone()
+        out = tern.gated_delta(*inputs[:5], state, i32(sl), q_start=i32(start), max_new=max(lens), qk_norm=True, dst_slots=i32(dst))
+        assert tern.device_error() == 0
+        return out, state
+
+    want, fine = run(inputs, pool)
+    pool[0, 1, 7, 3] = float("inf")
+    pool[1, 2, 9, 5] = float("nan")
+    v = inputs[2].clone()
+    v[start[2] + 33, 0, 4] = float("nan")
+    out, state = run((inputs[0], inputs[1], v, *inputs[3:]), pool)
+    same = lambda a, b: torch.equal(a.view(torch.int32), b.view(torch.int32))    # noqa: E731
+    assert same(state[:B], pool[:B]) and same(state[dst[0]], pool[0])
+    hit = torch.zeros((T, Hv, Dv), dtype=torch.bool, device="cuda")
+    hit[start[1]:start[2], 2, 9] = True
+    hit[start[2] + 33:start[3], 0, 4] = True
+    assert torch.equal(torch.isfinite(out), ~hit)
+    before = torch.zeros_like(hit)
+    before[start[2]:start[2] + 33, 0, 4] = True
+    assert torch.equal(out[~hit & ~before], want[~hit & ~before])
+    # (two results of half a step each, and of 2^-13 of what goes into them)
+    a, b = f64(out[before]), f64(want[before])
+    assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max() + 2.0 ** -12 * np.abs(f64(want)).max()
+    row = torch.zeros((Hv, Dv), dtype=torch.bool, device="cuda")
+    row[2, 9] = True
+    assert not torch.isfinite(state[dst[1]][row]).any() and torch.equal(state[dst[1]][~row], fine[dst[1]][~row])
+    assert torch.equal(state[B + 3:], fine[B + 3:])
+
+
 def test_another_stream_and_replays(tern):
     """The three calls captured once and replayed on new inputs, on a stream of their own."""
     g = gen(16)
