@@ -962,7 +962,10 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     convolution's output included; g, beta fp32 [T, v_heads]; state fp32 [pool,
     v_heads, Dv, Dk], read and written by slot; slots, q_start, max_new, past and
     dst_slots as short_conv's.  scale 1/sqrt(Dk) if not given.  qk_norm divides
-    queries and keys by their lengths.  With a_log and dt_bias (fp32 [v_heads])
+    queries and keys by their lengths.  max_new also chooses the kernel: above 24
+    every sequence goes in chunks of 64 tokens, so that a step of single tokens
+    called without it takes several times as long, and so does one in the call of
+    a prompt.  With a_log and dt_bias (fp32 [v_heads])
     the gates come raw: g <- -exp(a_log) softplus(g + dt_bias), beta <-
     sigmoid(beta).  Returns bf16 [T, v_heads, Dv] (out may be [T, v_heads * Dv])."""
     if state.dim() != 4:

@@ -6,8 +6,8 @@
 // which depend on one another's only through q and k: they stay in registers
 // from the first token to the last, so a call of a few tokens reads and writes
 // every state once and is bound by that: one token of 64 sequences of 48 heads of 128 x 128
-// 61.2 us, 97 % of the copy bandwidth.  Each token more costs a CTA some 0.8 us of products
-// and of sums over the 8 lanes that share a row: five of 8 sequences of 32 heads 10.0 us, of
+// 61.4 us, 97 % of the copy bandwidth.  Each token more costs a CTA some 0.8 us of products
+// and of sums over the 8 lanes that share a row: five of 8 sequences of 32 heads 9.9 us, of
 // which 6.2 are the states'.  (Products by pairs, fewer sums and 16 rows a warp in place of
 // 8 each change that by 5 % at most, and lose as much where few CTAs run.)
 #include "tern_delta.cuh"
@@ -21,8 +21,8 @@ __device__ int g_delta_error;
 
 constexpr int kStepThreads = 128, kStepBatch = 8;
 // The most tokens of a sequence that go one by one.  24 (32) tokens so and by chunks, 32 heads of
-// 128 x 128: one sequence 13.5 against 16.8 us (17.3, 17.2), eight 33.9 against 35.6 (44.1,
-// 36.4), sixty-four 230 against 245 (302, 251).
+// 128 x 128: one sequence 13.1 against 16.7 us (16.8, 16.9), eight 32.7 against 35.7 (42.6,
+// 36.1), sixty-four 223 against 246 (293, 249).
 constexpr int kStepTokens = 24;
 
 // 8 lanes share a row: lane l has the values 32 i + 4 l + {0..3}, so that a row's
@@ -142,9 +142,9 @@ namespace {
 // (a piece behind the first takes two, one for what it does to any state), and no more than
 // the root of the longest one's chunks, past which the steps from piece to piece take longer
 // than they save (8192 tokens of 2 heads: 11 pieces 113 us, 16 119; 4096: 8 pieces 82 us, 16 101).
-// From kDeltaPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 36.1
-// against 41.0 us, 2048 77 and 133, of 32 heads 38.9 and 41.3, 97 and 134, of 48 heads 39.9
-// and 41.5, 106 and 135; with 7 chunks the join takes what the pieces save.  The outputs of all
+// From kDeltaPieceChunks on; one sequence in pieces and whole, 128 x 128: 512 tokens of 16 heads 36.7
+// against 42.8 us, 2048 77 and 138, of 32 heads 39.3 and 42.7, 99 and 138, of 48 heads 40.3
+// and 43.0, 107 and 139; with 7 chunks the join takes what the pieces save.  The outputs of all
 // pieces but the first go through the workspace: calls that would need more than a gigabyte
 // of it go whole.
 constexpr size_t kMostWorkspace = (size_t)1 << 30;

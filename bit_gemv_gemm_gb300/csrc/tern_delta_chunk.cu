@@ -20,11 +20,11 @@
 // chunk after the next, from which four warps make P and T (16 x 16 blocks by
 // substitution, a column a lane, joined by mma.sync); two for decays and lengths.
 //
-// A chunk takes 3.9 us where few SMs run, 4.6 where all do (latency of that chain, the
+// A chunk takes 4.0 us where few SMs run, 4.6 where all do (latency of that chain, the
 // issue of some 17 thousand instructions by 32 warps, and, with all SMs at work, the
-// fetching of code): six prompts, 16381 tokens of 48 heads of 128 x 128, 389 us, and one
-// of 2048 tokens of 32 heads 134 us whole.  Where that leaves SMs idle, sequences go in
-// pieces at once (DeltaPieces): 97 us.
+// fetching of code): six prompts, 16381 tokens of 48 heads of 128 x 128, 386 us, and one
+// of 2048 tokens of 32 heads 138 us whole.  Where that leaves SMs idle, sequences go in
+// pieces at once (DeltaPieces): 99 us.
 //
 // Rounding.  q, k, v are exact as bf16.  S, X, U, T and P are fp32 cut into two bf16
 // values, which carry 2^-17 of each (one would lose 2^-8 of the state a chunk); what
@@ -325,7 +325,7 @@ __device__ __forceinline__ bool row_is_odd(const uint32_t* odd_rows, int w, int 
 }
 // Rows that are not finite at the end, token by token, by the chain's warps once the roles have met: a
 // thread has its columns of its row again.  All is in shared memory, where the rings were: S by columns
-// (a function has too few registers for it: 4.8 us a token, 2.4 so), a token's key, query, values and gates,
+// (a function has too few registers for it: 4.8 us a token, 2.2 so), a token's key, query, values and gates,
 // and four partial sums a row.  Outputs are written over up to where a row is not finite.
 template <int DK, bool PIECES>
 __device__ __noinline__ void redo(const DeltaArgs& a, const StateSeq s, const Part p, const uint32_t* odd_rows, unsigned char* smem) {

@@ -7,8 +7,8 @@
 // A row's values stay in the registers of a team of threads between the sum of
 // squares and the output: every input is read once, every output written once,
 // and the weight stays in registers over all rows of a team.  Bound by those
-// bytes: 4096 rows of 5120 with a residual, all in bf16, 27.4 us, 6.1 TB/s, 90 % of the
-// copy bandwidth; 777 rows of 4104, fp32 after a block, 7.2 us.  A call of a few rows is
+// bytes: 4096 rows of 5120 with a residual, all in bf16, 27.7 us, 6.1 TB/s, 89 % of the
+// copy bandwidth; 777 rows of 4104, fp32 after a block, 7.4 us.  A call of a few rows is
 // bound by its latency, 2.9 us.
 #include <math.h>
 

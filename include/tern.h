@@ -584,13 +584,17 @@ tern_status tern_short_conv(const void *x, int x_is_f32, long long x_token, cons
  * qk_norm != 0: q and k are divided by sqrt(sum of squares + 1e-6).  out bf16
  * [T][v_heads][dv].  The state and all sums are fp32; out is rounded once.
  * dk 64 or 128, dv a multiple of 16, at most 256; |scale| finite (TERN_ERR_SHAPE).
- * Sequences of more than 24 tokens (max_new) go 64 tokens at a time, where the state,
- * what is taken to it and the weights of a chunk's own tokens are two bf16 values each in
- * the products (2^-17 of a value).
+ * Where max_new is more than 24, all sequences of the call go 64 tokens at a time, short
+ * ones as a whole chunk: a step of single tokens says so in max_new (64 sequences, 48 heads:
+ * 61 us, 342 with max_new 64) and goes in another call than a prompt (63 beside one of 2048
+ * tokens 393 us, 173 in two calls).  In chunks the state, what is taken to it and the weights
+ * of a chunk's own tokens are two bf16 values each in the products (2^-17 of a value); rows
+ * of a state that a value that is not finite has reached go token by token up to it (some
+ * 2.2 us each).
  * workspace: NULL, or tern_gated_delta_workspace_bytes(B, T, max_new, v_heads, dk, dv)
  * bytes (max_new T / B without q_start; TERN_ERR_WORKSPACE if it is smaller), 256-byte
  * aligned, any contents: with it, few heads of long sequences go in pieces at once (one
- * of 2048 tokens and 32 heads of 128 x 128: 97 us, not 134).  0 bytes: none of use. */
+ * of 2048 tokens and 32 heads of 128 x 128: 99 us, not 138).  0 bytes: none of use. */
 size_t tern_gated_delta_workspace_bytes(int B, int T, int max_new, int v_heads, int dk, int dv);
 tern_status tern_gated_delta(const void *q, const void *k, const void *v, long long q_token, long long k_token,
                              long long v_token, const float *g, long long g_token, const float *beta,
